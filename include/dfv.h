@@ -69,7 +69,7 @@ enum {
 };
 
 /* DFV_Q8: 8-bit expert weights (see dfv_moe_layer).  DFV_F16 (IEEE binary16)
- * appears only in dfv_selftest_mma. */
+ * is a cache dtype (dfv_kv_cache) and appears in dfv_selftest_mma. */
 typedef enum { DFV_F32 = 0, DFV_BF16 = 1, DFV_MXFP4 = 2, DFV_Q8 = 3, DFV_F16 = 4 } dfv_dtype;
 
 /* Device-side error bits a kernel may set in the workspace (see
@@ -419,6 +419,266 @@ int dfv_selftest_mma(int dtype, const void *A, const void *B, float *D, void *st
  *   for the MMAs gave up (D is then not written).
  */
 int dfv_selftest_tcgen05(const void *A, const void *B, int N, int K, float *D, int32_t *status, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Tree verify: what the target's verify step needs around the MoE layers when
+ * the draft is a TREE of tokens (a chain is the tree whose mask is NULL):
+ * rotary positions and the paged cache, attention of the drafted nodes over
+ * that cache, rules on the logits, the greedy walk and the cache's pages.
+ * ("Speculating on a Strix Halo", section "Speculative decoding": the target
+ * checks the whole draft in one pass, and rejected positions are cropped from
+ * its cache.)
+ * ---------------------------------------------------------------------- */
+
+#define DFV_MAX_TREE 64        /* nodes of one drafted tree                   */
+#define DFV_MAX_TREE_SEQS 1024 /* sequences of one call                       */
+
+/* Bits that a call may set in dfv_kv_cache.err (sticky; the caller clears the
+ * word).  They flag device-side data that host checks cannot see; no call
+ * reads or writes outside the caller's buffers whatever that data holds. */
+#define DFV_KVERR_PAGE 0x1u    /* a page that is needed is missing or out of range */
+#define DFV_KVERR_LEN 0x2u     /* a length or row offset out of range, or no room left in a page-table row */
+#define DFV_KVERR_NO_PAGE 0x4u /* not enough free pages */
+#define DFV_KVERR_PATH 0x8u    /* an accepted path that is not increasing or leaves its tree */
+#define DFV_KVERR_SEQ 0x10u    /* a sequence index out of range or given twice, a fork into a sequence in use */
+
+/*
+ * A paged key/value cache of all layers.  Token `pos` of sequence s lives in
+ * page page_table[s][pos / page_size], row pos % page_size; its key of layer l
+ * and head h starts at element
+ *   l * stride_layer + page * stride_page + h * stride_head + row * stride_token
+ * of k (the same of v for values), head_dim consecutive elements.  The strides
+ * are in elements, non-negative multiples of 8 and the same for k and v, so
+ * head-major pages, token-major pages and k and v in one allocation all fit;
+ * k and v are 16-byte aligned.  Offsets are 64-bit.
+ *   dtype      DFV_BF16 or DFV_F16
+ *   page_size  a power of two, 8..256
+ *   head_dim   a multiple of 16 up to 256 (dfv_tree_attention: 64 or 128)
+ *   page_table [max_seqs, max_pages] int32, -1 where there is no page
+ *   lens       [max_seqs] int32 committed tokens of each sequence
+ *   refs       [n_pages] int32 how many sequences hold each page, 0 = free;
+ *              only the page calls use it (NULL otherwise)
+ *   err        [1] uint32 error bits (DFV_KVERR_*), or NULL
+ */
+typedef struct dfv_kv_cache {
+  int n_layers, n_pages, page_size, n_kv_heads, head_dim, dtype;
+  int max_seqs, max_pages;
+  void *k, *v;
+  int64_t stride_layer, stride_page, stride_head, stride_token;
+  int32_t *page_table, *lens, *refs;
+  uint32_t *err;
+} dfv_kv_cache;
+
+/*
+ * The drafted trees of one call: sequence b of the call owns rows row_off[b]
+ * .. row_off[b+1] of every [n_rows, ...] argument, one row per node, at most
+ * max_nodes (<= 64) and possibly none.  Node 0 is the root (the known token),
+ * and a node's number is larger than its parent's.
+ *   seq      [n_seqs] int32 cache sequence of each, or NULL: b itself
+ *   row_off  [n_seqs + 1] int32
+ *   mask     [n_rows] bit j of row i: node i sees node j of its own tree; its
+ *            ancestors and itself for a tree.  NULL: a chain (bits 0..i)
+ * A tree's node i is stored in the cache at token lens[s] + i, whatever its
+ * depth.
+ */
+typedef struct dfv_tree_batch {
+  int n_seqs, n_rows, max_nodes;
+  const int32_t *seq, *row_off;
+  const uint64_t *mask;
+} dfv_tree_batch;
+
+/* How rotary frequencies are scaled for contexts longer than the trained one
+ * (f_i = theta^(-2i/rot_dim) is the unscaled angle per position of pair i):
+ *   NONE    f_i
+ *   LINEAR  f_i / factor (positions interpolated)
+ *   NTK     theta * factor^(rot_dim / (rot_dim - 2)) in place of theta
+ *   BANDS   by how often a pair turns over the original context, n_i =
+ *           original * f_i / (2 pi):  g = clamp((n_i - low) / (high - low), 0, 1),
+ *           (1 - g) f_i / factor + g f_i  (slow pairs interpolated, fast kept) */
+typedef enum { DFV_ROPE_NONE = 0, DFV_ROPE_LINEAR = 1, DFV_ROPE_NTK = 2, DFV_ROPE_BANDS = 3 } dfv_rope_scaling;
+
+/*
+ * Rotary plan, filled by the caller on the HOST:
+ *   turns [rot_dim / 2] HOST array that receives the plan's table: the turn per
+ *   position of each pair as a 64-bit fraction of a whole turn,
+ *   round(f_i / (2 pi) * 2^64).  position * turns mod 2^64 is then the exact
+ *   fraction of a turn, so far positions lose nothing.
+ * The caller copies the table to the device and passes it to dfv_rope_append.
+ * rot_dim: a multiple of 16; theta > 1; factor >= 1; 0 <= low < high (BANDS),
+ * original >= 1 (BANDS).
+ */
+int dfv_rope_table(int rot_dim, double theta, int scaling, double factor, double original, double low, double high,
+                   uint64_t *turns);
+
+/*
+ * Rotary positions of the drafted rows, and their keys and values stored into
+ * the cache, in one launch.  With angle a = positions[t] * f_i and a pair
+ * (x1, x2) of a head's first rot_dim elements,
+ *   y1 = scale * (x1 cos a - x2 sin a),   y2 = scale * (x2 cos a + x1 sin a)
+ * in fp32, rounded once; pair i is elements (i, i + rot_dim/2), or (2i, 2i+1)
+ * when interleaved.  The head's other elements are copied.
+ *   q        [n_rows, n_heads, head_dim], row stride q_row, head stride q_head
+ *   k, v     [n_rows, n_kv_heads, head_dim], row strides k_row, v_row, head
+ *            strides k_head, v_head
+ *   q_out    [n_rows, n_heads, head_dim], strides o_row, o_head; may be q itself
+ *            (same strides)
+ *   positions [n_rows] int32, the rotary position of each row (a node's depth
+ *            counts, not its number: lens[s] + depth); negative ones turn back
+ *   turns    [rot_dim / 2] DEVICE copy of the dfv_rope_table
+ *   scale    factor on cos and sin (1 without attention scaling)
+ * All in the cache's dtype; strides in elements, multiples of 8; pointers
+ * 16-byte aligned.  rot_dim <= head_dim, a multiple of 16.
+ * The rotated k and v of node i go to token lens[s] + i of layer `layer`; a row
+ * whose page is missing is not stored (DFV_KVERR_PAGE) while its q is still
+ * turned.  Rows that row_off gives to no sequence are not touched.
+ */
+int dfv_rope_append(const dfv_kv_cache *cache, int layer, const dfv_tree_batch *tree, int n_heads, int rot_dim,
+                    int interleaved, float scale, const uint64_t *turns, const void *q, int64_t q_row, int64_t q_head,
+                    const void *k, int64_t k_row, int64_t k_head, const void *v, int64_t v_row, int64_t v_head,
+                    const int32_t *positions, void *q_out, int64_t o_row, int64_t o_head, void *stream);
+
+/* Bytes of workspace dfv_tree_attention needs for trees of up to max_nodes
+ * nodes with n_heads query heads (0 on invalid arguments). */
+size_t dfv_tree_attention_workspace_size(const dfv_kv_cache *cache, const dfv_tree_batch *tree, int n_heads);
+
+/*
+ * Attention of the drafted nodes over the paged cache.  Row t = (sequence s,
+ * node i) attends to every committed token of s (pos < lens[s]) and to the
+ * nodes of its own tree in its mask (pos = lens[s] + j, bit j):
+ *   o[t,h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q[t,h] . k_j - max)
+ * with key/value head h / (n_heads / n_kv_heads).  A row that attends to
+ * nothing (lens[s] = 0 and an empty mask) gives o = 0 and lse = -inf.  What a
+ * row's mask leaves out, and what lies past the last node in its page, does
+ * not change the row whatever it holds (infinities and NaN included).
+ *   q    [n_rows, n_heads, head_dim], strides q_row, q_head
+ *   out  [n_rows, n_heads, head_dim], strides o_row, o_head
+ *   opt_lse [n_rows, n_heads] fp32: max + ln(sum), or NULL
+ * q and out in the cache's dtype, strides in elements and multiples of 8,
+ * pointers 16-byte aligned; out may not overlap q.  head_dim 64 or 128; n_heads
+ * a multiple of n_kv_heads, at most 16 query heads per kv head.
+ * Scores, maxima, sums and the output accumulator are fp32; p is rounded to
+ * the cache's dtype for the second product, and the output once.
+ * A page-table entry out of range is read as page 0 (DFV_KVERR_PAGE; that
+ * sequence's outputs are invalid), a sequence with a length out of range is
+ * taken as empty (DFV_KVERR_LEN).  Lengths, tables, masks and row offsets are
+ * read on the device: a captured graph may be replayed after they change.
+ */
+int dfv_tree_attention(const dfv_kv_cache *cache, int layer, const dfv_tree_batch *tree, int n_heads, float scale,
+                       const void *q, int64_t q_row, int64_t q_head, void *out, int64_t o_row, int64_t o_head,
+                       float *opt_lse, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Rules on the target's logits before acceptance or sampling.  Any pointer may
+ * be NULL: that rule is then off.
+ *   hist       [n_seqs, hist_row] int32: what each sequence of the call said
+ *              before its tree's root; hist_len [n_seqs] entries of it count,
+ *              of which the first prompt_len [n_seqs] are the prompt (NULL: 0)
+ *   repetition, frequency, presence  [n_seqs] fp32
+ *   bias       fp32, row b * bias_row for sequence b (bias_row = 0: shared)
+ *   allowed    bit v % 32 of word v / 32: token v is allowed; row t * allowed_row
+ *              words for row t (allowed_row = 0: shared)
+ * Token ids outside 0..V-1 in hist are ignored.
+ */
+typedef struct dfv_logit_rules {
+  const int32_t *hist, *hist_len, *prompt_len;
+  int64_t hist_row;
+  const float *repetition, *frequency, *presence;
+  const float *bias;
+  int64_t bias_row;
+  const uint32_t *allowed;
+  int64_t allowed_row;
+} dfv_logit_rules;
+
+/* Bytes of workspace dfv_logits_process needs for up to n_rows_max rows (0 on
+ * invalid arguments). */
+size_t dfv_logits_workspace_size(int n_rows_max);
+
+/*
+ * Logits of every drafted node under the rules, and their argmax, in one pass.
+ * Row t's own context is its sequence's history followed by the drafted tokens
+ * of the nodes in its mask (ancestors and itself).  With c_v how often token v
+ * was generated there (history past the prompt, and drafted tokens) and seen_v
+ * whether it is there at all (prompt included), step by step in fp32:
+ *   1. repetition: if seen_v, x = x > 0 ? x / r : x * r
+ *   2. x = x - f * c_v (product rounded, then difference)
+ *   3. if c_v > 0, x = x - p
+ *   4. x = x + bias_v
+ *   5. x = -inf where v is not allowed
+ * rounded once to the logits' dtype.
+ *   logits [n_rows, V] BF16 or F32, row stride `row` elements
+ *   tokens [n_rows] int32 drafted token of each node (NULL without penalties)
+ *   out    [n_rows, V], row stride `out_row`; may be logits itself (same stride),
+ *          or NULL: argmax only
+ *   argmax [n_rows] int32 or NULL: of the rounded values, equal ones to the
+ *          lowest index (0 when nothing is allowed); logits must not be NaN
+ * Bases are 4-byte (BF16: 2-byte) aligned; rows may start anywhere.
+ */
+int dfv_logits_process(const void *logits, int64_t row, int dtype, int V, const dfv_tree_batch *tree,
+                       const int32_t *tokens, const dfv_logit_rules *rules, void *out, int64_t out_row,
+                       int32_t *argmax, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Greedy acceptance of drafted trees: from the root, go to the child whose
+ * drafted token is the target's token at the current node (the lowest such
+ * child), until there is none.  A node's parent is the highest node below it
+ * in its mask.
+ *   tokens, target [n_rows] int32: drafted token of each node, and the target's
+ *          own (argmax) token at it
+ *   path   [n_seqs, path_row] int32: accepted nodes from the root on, then -1
+ *          up to max_nodes entries (path_row >= max_nodes)
+ *   tau    [n_seqs] int32: accepted nodes, the root included (0 for a sequence
+ *          without rows).  The committed tokens are target[path[0..tau-1]].
+ * A chain gives dfv_accept_greedy's tau.
+ */
+int dfv_accept_tree(const dfv_tree_batch *tree, const int32_t *tokens, const int32_t *target, int32_t *path,
+                    int64_t path_row, int32_t *tau, void *stream);
+
+/* Bytes of workspace dfv_cache_commit and the dfv_pages_* calls need. */
+size_t dfv_cache_workspace_size(const dfv_kv_cache *cache);
+
+/*
+ * Keep the accepted path of each tree and drop its other nodes: in every layer,
+ * token lens[s] + path[j] moves to lens[s] + j for j < tau, and then
+ * new_lens[s] = lens[s] + tau.
+ *   path [n_seqs, path_row], tau [n_seqs]: as dfv_accept_tree leaves them;
+ *        increasing node numbers
+ *   new_lens [max_seqs] int32; cache->lens itself updates it in place.  Only the
+ *        call's sequences are written.
+ * A sequence whose path is not increasing or leaves its tree keeps its rows and
+ * its length (DFV_KVERR_PATH).
+ */
+int dfv_cache_commit(const dfv_kv_cache *cache, const dfv_tree_batch *tree, const int32_t *path, int64_t path_row,
+                     const int32_t *tau, int32_t *new_lens, void *ws, size_t ws_bytes, void *stream);
+
+/* Copy whole pages dst[i] <- src[i] (device int32 [n]) in every layer.  A page
+ * is the destination of at most one pair and then the source of none. */
+int dfv_cache_copy_pages(const dfv_kv_cache *cache, const int32_t *src, const int32_t *dst, int n, void *stream);
+
+/*
+ * Pages for the next tokens: sequence seqs[i] gets a page wherever it has none
+ * for tokens up to lens + n_new[i].  Free pages (refs 0) are given out lowest
+ * index first, in the order of the list and of the tokens; refs becomes 1.
+ * When the pool runs short, the first sequence that cannot be served in full
+ * and all after it get nothing (DFV_KVERR_NO_PAGE).
+ *   seqs, n_new [n] int32 device; n <= DFV_MAX_TREE_SEQS; seqs distinct
+ */
+int dfv_pages_reserve(const dfv_kv_cache *cache, const int32_t *seqs, const int32_t *n_new, int n, void *ws,
+                      size_t ws_bytes, void *stream);
+
+/*
+ * Fork: sequence dst[i], which holds nothing, becomes a copy of src[i].  Whole
+ * pages are shared (refs + 1); a last page in part used is copied, its used rows
+ * in every layer, to the lowest free pages in the order of the list.  Pages
+ * that the source reserved beyond its tokens are not shared.  Several forks may
+ * have one source.  A fork that finds no page leaves dst empty
+ * (DFV_KVERR_NO_PAGE), as does one into a sequence in use (DFV_KVERR_SEQ).
+ */
+int dfv_pages_fork(const dfv_kv_cache *cache, const int32_t *src, const int32_t *dst, int n, void *ws,
+                   size_t ws_bytes, void *stream);
+
+/* Drop sequences seqs[i] (device int32 [n]): every page's refs - 1, their table
+ * rows become -1 and their lens 0.  Dropping an empty sequence does nothing. */
+int dfv_pages_free(const dfv_kv_cache *cache, const int32_t *seqs, int n, void *stream);
 
 const char *dfv_status_string(int status);
 const char *dfv_last_error_detail(void);

@@ -492,6 +492,18 @@ int run_layer(const dfv_moe_layer *L, const void *x, int act, int k, void *out, 
 
 }  // namespace
 
+namespace dfv {
+// Status and detail text for the entry points of the other files.
+int api_fail(int status, const char *fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return fail(status, "%s", buf);
+}
+}  // namespace dfv
+
 extern "C" {
 
 int dfv_version(void) { return DFV_VERSION; }

@@ -1,0 +1,185 @@
+// tree_common.cuh -- parameter blocks and device helpers shared by the
+// tree-verify kernels: the paged cache, the drafted trees of a call, and the
+// checks on device-side data (lengths, row offsets, page ids) that the host
+// cannot see.  Every one of those checks turns bad data into an error bit and a
+// skipped access.
+#pragma once
+
+#include "dfv_internal.cuh"
+
+namespace dfv {
+
+struct CacheParams {
+  char *k, *v;
+  long long sl, sp, sh, st;  // strides in elements: layer, page, head, token
+  int n_layers, n_pages, page_shift, Hkv, D, f16;
+  int max_seqs, max_pages;
+  int32_t *table, *lens, *refs;
+  uint32_t *err;
+};
+
+struct TreeParams {
+  int n_seqs, n_rows, max_nodes;
+  const int32_t *seq, *row_off;
+  const uint64_t *mask;  // null: chain
+};
+
+struct RopeParams {
+  CacheParams c;
+  TreeParams t;
+  int layer, H, rot, inter;
+  float scale;
+  const uint64_t *turns;
+  const char *q, *k, *v;
+  char *o;
+  long long q_row, q_head, k_row, k_head, v_row, v_head, o_row, o_head;
+  const int32_t *positions;
+};
+
+struct TreeAttnParams {
+  CacheParams c;
+  TreeParams t;
+  int layer, H, G;   // query heads, query heads per kv head
+  float scale_log2;  // scale * log2(e)
+  const char *q;
+  char *o;
+  long long q_row, q_head, o_row, o_head;
+  float *lse;
+  unsigned *err;  // workspace error word (bounded waits)
+};
+
+struct LogitsParams {
+  TreeParams t;
+  dfv_logit_rules r;
+  const char *x;
+  char *out;
+  long long row, out_row;
+  int V, f32, slice;
+  const int32_t *tokens;
+  int32_t *argmax;
+  unsigned long long *key;  // [n_rows] running maximum of each row, zero between calls
+  unsigned *ticket;         // [n_rows] slices done, zero between calls
+};
+
+struct AcceptTreeParams {
+  TreeParams t;
+  const int32_t *tokens, *target;
+  int32_t *path, *tau;
+  long long path_row;
+};
+
+struct CommitParams {
+  CacheParams c;
+  TreeParams t;
+  const int32_t *path, *tau;
+  long long path_row;
+  int32_t *new_lens;
+  unsigned *ticket;
+};
+
+struct PagesParams {
+  CacheParams c;
+  const int32_t *a, *b;  // reserve: seqs, n_new; fork: src, dst; copy: src, dst; free: seqs
+  int n;
+  int32_t *got;     // [n_pages] pages handed out
+  int32_t *plan;    // fork: [n][4] source length, last source page, its copy, state
+};
+
+__device__ __forceinline__ void flag_err(uint32_t *err, uint32_t bit) {
+  if (err) atomicOr(err, bit);
+}
+
+// Sequence b of a call: its rows [row0, row0 + n) and its cache sequence s with
+// len committed tokens; s = -1 when the cache side is unusable (flagged).
+struct SeqView {
+  int row0, n, s, len;
+};
+__device__ __forceinline__ SeqView seq_view(const CacheParams &c, const TreeParams &t, int b) {
+  SeqView v;
+  v.row0 = t.row_off[b];
+  const int r1 = t.row_off[b + 1];
+  v.s = t.seq ? t.seq[b] : b;
+  v.len = 0;
+  v.n = r1 - v.row0;
+  if (v.row0 < 0 || r1 > t.n_rows || v.n < 0 || v.n > t.max_nodes) {
+    flag_err(c.err, DFV_KVERR_LEN);
+    v.n = 0;
+    v.row0 = 0;
+  }
+  if (v.s < 0 || v.s >= c.max_seqs) {
+    flag_err(c.err, DFV_KVERR_SEQ);
+    v.s = -1;
+    return v;
+  }
+  v.len = c.lens[v.s];
+  if (v.len < 0 || (long long)v.len + v.n > ((long long)c.max_pages << c.page_shift)) {
+    flag_err(c.err, DFV_KVERR_LEN);
+    v.s = -1;
+    v.len = 0;
+  }
+  return v;
+}
+
+// Page of token `pos` of cache sequence s, or -1 (flagged) when there is none.
+__device__ __forceinline__ int page_of(const CacheParams &c, int s, int pos) {
+  const int pg = c.table[(size_t)s * c.max_pages + (pos >> c.page_shift)];
+  if ((unsigned)pg >= (unsigned)c.n_pages) {
+    flag_err(c.err, DFV_KVERR_PAGE);
+    return -1;
+  }
+  return pg;
+}
+
+// Element offset of row `row` of page pg, head h, layer l.
+__device__ __forceinline__ long long kv_off(const CacheParams &c, int l, int pg, int h, int row) {
+  return l * c.sl + pg * c.sp + h * c.sh + row * c.st;
+}
+
+__device__ __forceinline__ uint64_t row_mask(const TreeParams &t, int row0, int i) {
+  return t.mask ? t.mask[row0 + i] : (i >= 63 ? ~0ull : (2ull << i) - 1ull);
+}
+
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  if (F16) return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+  return make_float2(bf16_lo(v), bf16_hi(v));
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if (F16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+cudaError_t launch_rope_append(const RopeParams &p, cudaStream_t s);
+cudaError_t launch_tree_attn(const TreeAttnParams &p, cudaStream_t s);
+cudaError_t launch_logits(const LogitsParams &p, cudaStream_t s);
+cudaError_t launch_accept_tree(const AcceptTreeParams &p, cudaStream_t s);
+cudaError_t launch_commit(const CommitParams &p, cudaStream_t s);
+cudaError_t launch_copy_pages(const PagesParams &p, cudaStream_t s);
+cudaError_t launch_reserve(const PagesParams &p, cudaStream_t s);
+cudaError_t launch_fork(const PagesParams &p, cudaStream_t s);
+cudaError_t launch_free(const PagesParams &p, cudaStream_t s);
+
+// status reporting of api.cu (thread-local detail text)
+int api_fail(int status, const char *fmt, ...);
+
+template <class Kern, class Par>
+cudaError_t launch_chained(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream_t s, const Par &p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace dfv

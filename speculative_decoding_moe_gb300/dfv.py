@@ -4,6 +4,7 @@ CUDA tensors; calls enqueue work on torch's current CUDA stream."""
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Sequence
 
@@ -18,6 +19,9 @@ F32, BF16, MXFP4, Q8, F16 = 0, 1, 2, 3, 4
 # device error bits (DFV_DEVERR_* in include/dfv.h)
 DEVERR_STAGE_WAIT, DEVERR_SLOT_WAIT, DEVERR_DRAIN_WAIT, DEVERR_GRID_WAIT = 0x1, 0x2, 0x4, 0x8
 DEVERR_SCALE_RANGE, DEVERR_REDUCE_WAIT, DEVERR_ROUTING = 0x10, 0x20, 0x40
+# cache error bits (DFV_KVERR_* in include/dfv.h)
+KVERR_PAGE, KVERR_LEN, KVERR_NO_PAGE, KVERR_PATH, KVERR_SEQ = 0x1, 0x2, 0x4, 0x8, 0x10
+MAX_TREE, MAX_TREE_SEQS = 64, 1024
 _NAMES = {"f32": F32, "bf16": BF16, "mxfp4": MXFP4, "q8": Q8}
 EXPORTS = ("dfv_version", "dfv_status_string", "dfv_last_error_detail", "dfv_profile_set_events",
            "dfv_read_device_error", "dfv_set_path", "dfv_last_layer_path", "dfv_fused_unavailable_reason",
@@ -26,7 +30,10 @@ EXPORTS = ("dfv_version", "dfv_status_string", "dfv_last_error_detail", "dfv_pro
            "dfv_route_topk", "dfv_moe_block_forward", "dfv_moe_block_forward_host", "dfv_moe_stack_forward",
            "dfv_accept_workspace_size", "dfv_accept_greedy", "dfv_selftest_bounded_waits", "dfv_selftest_mma",
            "dfv_selftest_tcgen05", "dfv_moe_batch_workspace_size", "dfv_moe_batch_forward",
-           "dfv_set_stack_launch")
+           "dfv_set_stack_launch",
+           "dfv_rope_table", "dfv_rope_append", "dfv_tree_attention_workspace_size", "dfv_tree_attention",
+           "dfv_logits_workspace_size", "dfv_logits_process", "dfv_accept_tree", "dfv_cache_workspace_size",
+           "dfv_cache_commit", "dfv_cache_copy_pages", "dfv_pages_reserve", "dfv_pages_fork", "dfv_pages_free")
 
 
 class DfvError(RuntimeError):
@@ -46,6 +53,26 @@ class CLayer(ctypes.Structure):
         ("w_down", ctypes.c_void_p), ("s_gate", ctypes.c_void_p), ("s_up", ctypes.c_void_p),
         ("s_down", ctypes.c_void_p), ("n_shared", ctypes.c_int),
     ]
+
+
+class CCache(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("n_layers", "n_pages", "page_size", "n_kv_heads", "head_dim", "dtype",
+                                             "max_seqs", "max_pages")]
+                + [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+                + [(n, ctypes.c_int64) for n in ("stride_layer", "stride_page", "stride_head", "stride_token")]
+                + [(n, ctypes.c_void_p) for n in ("page_table", "lens", "refs", "err")])
+
+
+class CTree(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int), ("n_rows", ctypes.c_int), ("max_nodes", ctypes.c_int),
+                ("seq", ctypes.c_void_p), ("row_off", ctypes.c_void_p), ("mask", ctypes.c_void_p)]
+
+
+class CRules(ctypes.Structure):
+    _fields_ = [("hist", ctypes.c_void_p), ("hist_len", ctypes.c_void_p), ("prompt_len", ctypes.c_void_p),
+                ("hist_row", ctypes.c_int64), ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("bias_row", ctypes.c_int64),
+                ("allowed", ctypes.c_void_p), ("allowed_row", ctypes.c_int64)]
 
 
 _lib = None
@@ -88,6 +115,23 @@ def _load():
         L.dfv_last_staging.argtypes = []
         L.dfv_last_layer_path.restype = I
         L.dfv_fused_unavailable_reason.restype = ctypes.c_char_p
+        F, F64, L64 = ctypes.c_float, ctypes.c_double, ctypes.c_int64
+        L.dfv_rope_table.argtypes = [I, F64, I, F64, F64, F64, F64, P]
+        L.dfv_rope_append.argtypes = [P, I, P, I, I, I, F, P, P, L64, L64, P, L64, L64, P, L64, L64, P, P, L64, L64, P]
+        L.dfv_tree_attention_workspace_size.restype = S
+        L.dfv_tree_attention_workspace_size.argtypes = [P, P, I]
+        L.dfv_tree_attention.argtypes = [P, I, P, I, F, P, L64, L64, P, L64, L64, P, P, S, P]
+        L.dfv_logits_workspace_size.restype = S
+        L.dfv_logits_workspace_size.argtypes = [I]
+        L.dfv_logits_process.argtypes = [P, L64, I, I, P, P, P, P, L64, P, P, S, P]
+        L.dfv_accept_tree.argtypes = [P, P, P, P, L64, P, P]
+        L.dfv_cache_workspace_size.restype = S
+        L.dfv_cache_workspace_size.argtypes = [P]
+        L.dfv_cache_commit.argtypes = [P, P, P, L64, P, P, P, S, P]
+        L.dfv_cache_copy_pages.argtypes = [P, P, P, I, P]
+        L.dfv_pages_reserve.argtypes = [P, P, P, I, P, S, P]
+        L.dfv_pages_fork.argtypes = [P, P, P, I, P, S, P]
+        L.dfv_pages_free.argtypes = [P, P, I, P]
         _lib = L
     return _lib
 
@@ -340,3 +384,301 @@ def accept_greedy_noalloc(logits: torch.Tensor, draft: torch.Tensor, tau: Option
                                            _stream(stream))
     _check(st, "dfv_accept_greedy_noalloc")
     return tau, committed
+
+
+# ---------------------------------------------------------------- tree verify
+def _need(t: Optional[torch.Tensor], what: str, dtype, shape=None, optional=False, like: Optional[torch.Tensor] = None):
+    """Type, shape (None entries free), contiguity and device of one argument."""
+    if t is None:
+        if optional:
+            return
+        raise ValueError("%s is missing" % what)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise ValueError("%s must have shape %s, got %s" % (what, shape, tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    if like is not None and t.device != like.device:
+        raise ValueError("%s is on %s, not on %s" % (what, t.device, like.device))
+
+
+def _rows3(t: torch.Tensor, what: str, rows: int, heads: int, dim: int, dtype, like: torch.Tensor):
+    """(pointer, row stride, head stride) of a [rows, heads, dim] tensor whose last dimension is contiguous."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s like the cache, got %s" % (what, dtype, t.dtype))
+    if tuple(t.shape) != (rows, heads, dim):
+        raise ValueError("%s must have shape %s, got %s" % (what, (rows, heads, dim), tuple(t.shape)))
+    if t.stride(2) != 1:
+        raise ValueError("%s: the head dimension must be contiguous" % what)
+    if t.device != like.device:
+        raise ValueError("%s is on %s, not on %s" % (what, t.device, like.device))
+    # a dimension of size 1 has no stride of its own
+    return t.data_ptr(), t.stride(0) if rows > 1 else 0, t.stride(1) if heads > 1 else 0
+
+
+class KVCache:
+    """A paged key/value cache of all layers (include/dfv.h, dfv_kv_cache).
+
+    k, v        [n_layers, n_pages, n_kv_heads, page_size, head_dim] bf16 or fp16, any strides that both share with
+                the last dimension contiguous (permuted views of token-major pages, halves of one allocation)
+    page_table  [max_seqs, max_pages] int32, -1 where there is no page
+    lens        [max_seqs] int32 committed tokens
+    refs        [n_pages] int32 holders of each page, 0 = free (for the page calls)
+    err         [1] int32 error bits (KVERR_*), sticky; made here when not given
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                 refs: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None):
+        if k.dim() != 5 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must be alike: [layers, pages, kv heads, page size, head dim]")
+        if k.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("the cache must be bf16 or fp16, got %s" % k.dtype)
+        if k.stride(4) != 1 or v.stride(4) != 1 or any(a != b for a, b, n in zip(k.stride(), v.stride(), k.shape) if n > 1):
+            raise ValueError("k and v must have the same strides and a contiguous head dimension")
+        _need(page_table, "page_table", torch.int32, (None, None), like=k)
+        _need(lens, "lens", torch.int32, (page_table.shape[0],), like=k)
+        _need(refs, "refs", torch.int32, (k.shape[1],), optional=True, like=k)
+        if err is None:
+            err = torch.zeros(1, dtype=torch.int32, device=k.device)
+        _need(err, "err", torch.int32, (1,), like=k)
+        self.k, self.v, self.page_table, self.lens, self.refs, self.err = k, v, page_table, lens, refs, err
+        self.n_layers, self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+        self.dtype = k.dtype
+        st = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(4)]
+        self.c = CCache(self.n_layers, self.n_pages, self.page_size, self.n_kv_heads, self.head_dim,
+                        BF16 if k.dtype == torch.bfloat16 else F16, page_table.shape[0], page_table.shape[1],
+                        k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], k.stride(3) if self.page_size > 1 else self.head_dim,
+                        page_table.data_ptr(), lens.data_ptr(), None if refs is None else refs.data_ptr(),
+                        err.data_ptr())
+        self.ref = ctypes.byref(self.c)
+
+    @classmethod
+    def empty(cls, n_layers: int, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, max_seqs: int,
+              max_pages: int, dtype=torch.bfloat16, device="cuda") -> "KVCache":
+        """An empty cache: every page free, every sequence without tokens."""
+        kv = torch.zeros(2, n_layers, n_pages, n_kv_heads, page_size, head_dim, dtype=dtype, device=device)
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(kv[0], kv[1], torch.full((max_seqs, max_pages), -1, **i32), torch.zeros(max_seqs, **i32),
+                   refs=torch.zeros(n_pages, **i32))
+
+    def errors(self) -> int:
+        """Error bits so far (waits for the device)."""
+        return int(self.err.item()) & 0xffffffff
+
+
+class TreeBatch:
+    """The drafted trees of one call (include/dfv.h, dfv_tree_batch): n_rows nodes, sequence b's in rows
+    row_off[b] .. row_off[b + 1], at most max_nodes each; mask [n_rows] int64 bit patterns (None: chains); seq
+    [n_seqs] int32 cache sequences (None: 0, 1, ...)."""
+
+    def __init__(self, row_off: torch.Tensor, n_rows: int, max_nodes: int, mask: Optional[torch.Tensor] = None,
+                 seq: Optional[torch.Tensor] = None):
+        _need(row_off, "row_off", torch.int32, (None,))
+        if row_off.numel() < 2:
+            raise ValueError("row_off needs one entry per sequence and one more")
+        self.n_seqs, self.n_rows, self.max_nodes = row_off.numel() - 1, int(n_rows), int(max_nodes)
+        _need(mask, "mask", torch.int64, (self.n_rows,), optional=True, like=row_off)
+        _need(seq, "seq", torch.int32, (self.n_seqs,), optional=True, like=row_off)
+        self.row_off, self.mask, self.seq = row_off, mask, seq
+        self.c = CTree(self.n_seqs, self.n_rows, self.max_nodes, None if seq is None else seq.data_ptr(),
+                       row_off.data_ptr(), None if mask is None else mask.data_ptr())
+        self.ref = ctypes.byref(self.c)
+
+
+class Rope:
+    """Rotary plan: the device table of dfv_rope_table and the factor on cos and sin.
+
+    scaling: "none", "linear", "ntk" or "bands" (frequency bands between `low` and `high` turns over the `original`
+    context; attention is then scaled by 0.1 ln(factor) + 1 unless `scale` says otherwise)."""
+
+    KINDS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3}
+
+    def __init__(self, head_dim: int, rot_dim: Optional[int] = None, theta: float = 1e4, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0, original: int = 4096, low: float = 1.0, high: float = 32.0,
+                 scale: Optional[float] = None, device="cuda"):
+        if scaling not in self.KINDS:
+            raise ValueError("scaling must be one of %s, got %r" % (sorted(self.KINDS), scaling))
+        self.head_dim, self.rot_dim, self.interleaved = int(head_dim), int(rot_dim or head_dim), bool(interleaved)
+        turns = (ctypes.c_uint64 * max(1, self.rot_dim // 2))()
+        _check(_load().dfv_rope_table(self.rot_dim, float(theta), self.KINDS[scaling], float(factor), float(original),
+                                      float(low), float(high), turns), "dfv_rope_table")
+        if scale is None:
+            scale = 0.1 * math.log(factor) + 1.0 if scaling == "bands" else 1.0
+        self.scale = float(scale)
+        signed = [t - (1 << 64) if t >> 63 else t for t in turns]
+        self.turns = torch.tensor(signed, dtype=torch.int64, device=device)
+
+
+def rope_append(cache: KVCache, layer: int, tree: TreeBatch, rope: Rope, q: torch.Tensor, k: torch.Tensor,
+                v: torch.Tensor, positions: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rotated q (out, a new tensor or q itself), and the rows' rotated k and their v stored into the cache.
+    q [rows, heads, dim], k and v [rows, kv heads, dim] may be slices of one projection."""
+    rows, H, D = tree.n_rows, q.shape[1] if q.dim() == 3 else 0, cache.head_dim
+    qp, qr, qh = _rows3(q, "q", rows, H, D, cache.dtype, cache.k)
+    kp, kr, kh = _rows3(k, "k", rows, cache.n_kv_heads, D, cache.dtype, cache.k)
+    vp, vr, vh = _rows3(v, "v", rows, cache.n_kv_heads, D, cache.dtype, cache.k)
+    _need(positions, "positions", torch.int32, (rows,), like=cache.k)
+    if rope.head_dim != D:
+        raise ValueError("the rotary plan is for head_dim %d, the cache has %d" % (rope.head_dim, D))
+    if out is None:
+        out = torch.empty(rows, H, D, dtype=q.dtype, device=q.device)
+    op, orow, oh = _rows3(out, "out", rows, H, D, cache.dtype, cache.k)
+    st = _load().dfv_rope_append(cache.ref, int(layer), tree.ref, H, rope.rot_dim, 1 if rope.interleaved else 0,
+                                 rope.scale, rope.turns.data_ptr(), qp, qr, qh, kp, kr, kh, vp, vr, vh,
+                                 positions.data_ptr(), op, orow, oh, _stream(stream))
+    _check(st, "dfv_rope_append")
+    return out
+
+
+def tree_attention_workspace_size(cache: KVCache, tree: TreeBatch, n_heads: int) -> int:
+    return int(_load().dfv_tree_attention_workspace_size(cache.ref, tree.ref, int(n_heads)))
+
+
+def tree_attention(cache: KVCache, layer: int, tree: TreeBatch, q: torch.Tensor, ws: torch.Tensor,
+                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of every drafted node over its sequence's committed tokens and the nodes of its mask.
+    scale: 1/sqrt(head_dim) by default; lse: optional fp32 [rows, heads] that receives ln(sum exp)."""
+    rows, H, D = tree.n_rows, q.shape[1] if q.dim() == 3 else 0, cache.head_dim
+    qp, qr, qh = _rows3(q, "q", rows, H, D, cache.dtype, cache.k)
+    if out is None:
+        out = torch.empty(rows, H, D, dtype=q.dtype, device=q.device)
+    op, orow, oh = _rows3(out, "out", rows, H, D, cache.dtype, cache.k)
+    _need(lse, "lse", torch.float32, (rows, H), optional=True, like=cache.k)
+    st = _load().dfv_tree_attention(cache.ref, int(layer), tree.ref, H, D ** -0.5 if scale is None else float(scale),
+                                    qp, qr, qh, op, orow, oh, None if lse is None else lse.data_ptr(),
+                                    ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(st, "dfv_tree_attention")
+    return out
+
+
+class LogitRules:
+    """Penalties, bias and grammar mask of a call (include/dfv.h, dfv_logit_rules); any of them may be None.
+
+    hist [n_seqs, width] int32 with hist_len, prompt_len [n_seqs] int32; repetition, frequency, presence [n_seqs]
+    fp32; bias [n_seqs or 1, V] fp32; allowed [rows or 1, ceil(V / 32)] int32 bit words."""
+
+    def __init__(self, hist=None, hist_len=None, prompt_len=None, repetition=None, frequency=None, presence=None,
+                 bias=None, allowed=None):
+        _need(hist, "hist", torch.int32, (None, None), optional=True)
+        if hist is not None and hist_len is None:
+            raise ValueError("hist needs hist_len")
+        n = None if hist is None else hist.shape[0]
+        for name, t, dt in (("hist_len", hist_len, torch.int32), ("prompt_len", prompt_len, torch.int32),
+                            ("repetition", repetition, torch.float32), ("frequency", frequency, torch.float32),
+                            ("presence", presence, torch.float32)):
+            _need(t, name, dt, (n,), optional=True)
+            n = t.shape[0] if t is not None else n
+        _need(bias, "bias", torch.float32, (None, None), optional=True)
+        _need(allowed, "allowed", torch.int32, (None, None), optional=True)
+        self.n_seqs, self.bias, self.allowed = n, bias, allowed
+        self.keep = (hist, hist_len, prompt_len, repetition, frequency, presence)
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self.c = CRules(ptr(hist), ptr(hist_len), ptr(prompt_len), 0 if hist is None else hist.shape[1], ptr(repetition),
+                        ptr(frequency), ptr(presence), ptr(bias), 0 if bias is None or bias.shape[0] == 1 else bias.shape[1],
+                        ptr(allowed), 0 if allowed is None or allowed.shape[0] == 1 else allowed.shape[1])
+        self.ref = ctypes.byref(self.c)
+
+
+def logits_workspace_size(n_rows_max: int) -> int:
+    return int(_load().dfv_logits_workspace_size(int(n_rows_max)))
+
+
+def logits_process(logits: torch.Tensor, tree: TreeBatch, tokens: Optional[torch.Tensor], rules: LogitRules,
+                   ws: torch.Tensor, out: Optional[torch.Tensor] = None, argmax: Optional[torch.Tensor] = None,
+                   store: bool = True, stream=None):
+    """(logits under the rules, argmax of each row).  logits [rows, V] bf16 or fp32 with contiguous rows; out may be
+    logits itself; store=False computes the argmax only (out is then None)."""
+    if logits.dim() != 2 or logits.shape[0] != tree.n_rows or logits.stride(1) != 1:
+        raise ValueError("logits must be [%d, V] with contiguous rows" % tree.n_rows)
+    rows, V = logits.shape
+    if rules.n_seqs is not None and rules.n_seqs != tree.n_seqs:
+        raise ValueError("the rules are for %d sequences, the call has %d" % (rules.n_seqs, tree.n_seqs))
+    if rules.bias is not None and (rules.bias.shape[1] != V or rules.bias.shape[0] not in (1, tree.n_seqs)):
+        raise ValueError("bias must be [1 or %d, %d]" % (tree.n_seqs, V))
+    if rules.allowed is not None and (rules.allowed.shape[1] != (V + 31) // 32 or rules.allowed.shape[0] not in (1, rows)):
+        raise ValueError("allowed must be [1 or %d, %d]" % (rows, (V + 31) // 32))
+    _need(tokens, "tokens", torch.int32, (rows,), optional=True, like=logits)
+    if not store:
+        if out is not None:
+            raise ValueError("store=False takes no out")
+    elif out is None:
+        out = torch.empty(rows, V, dtype=logits.dtype, device=logits.device)
+    elif out.shape != logits.shape or out.dtype != logits.dtype or out.stride(1) != 1:
+        raise ValueError("out must be like logits")
+    if argmax is None:
+        argmax = torch.empty(rows, dtype=torch.int32, device=logits.device)
+    _need(argmax, "argmax", torch.int32, (rows,), like=logits)
+    st = _load().dfv_logits_process(logits.data_ptr(), logits.stride(0) if rows > 1 else V, _act(logits), V, tree.ref,
+                                    None if tokens is None else tokens.data_ptr(), rules.ref,
+                                    None if out is None else out.data_ptr(),
+                                    0 if out is None else out.stride(0) if rows > 1 else V, argmax.data_ptr(),
+                                    ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(st, "dfv_logits_process")
+    return out, argmax
+
+
+def accept_tree(tree: TreeBatch, tokens: torch.Tensor, target: torch.Tensor, path: Optional[torch.Tensor] = None,
+                tau: Optional[torch.Tensor] = None, stream=None):
+    """(path [n_seqs, max_nodes], tau [n_seqs]): the accepted nodes of each tree, root first, then -1."""
+    _need(tokens, "tokens", torch.int32, (tree.n_rows,), like=tree.row_off)
+    _need(target, "target", torch.int32, (tree.n_rows,), like=tree.row_off)
+    if path is None:
+        path = torch.empty(tree.n_seqs, tree.max_nodes, dtype=torch.int32, device=tokens.device)
+    if tau is None:
+        tau = torch.empty(tree.n_seqs, dtype=torch.int32, device=tokens.device)
+    _need(path, "path", torch.int32, (tree.n_seqs, None), like=tokens)
+    _need(tau, "tau", torch.int32, (tree.n_seqs,), like=tokens)
+    st = _load().dfv_accept_tree(tree.ref, tokens.data_ptr(), target.data_ptr(), path.data_ptr(), path.shape[1],
+                                 tau.data_ptr(), _stream(stream))
+    _check(st, "dfv_accept_tree")
+    return path, tau
+
+
+def cache_workspace_size(cache: KVCache) -> int:
+    return int(_load().dfv_cache_workspace_size(cache.ref))
+
+
+def cache_commit(cache: KVCache, tree: TreeBatch, path: torch.Tensor, tau: torch.Tensor, ws: torch.Tensor,
+                 new_lens: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Moves the accepted rows together in every layer and adds tau to the lengths (cache.lens unless new_lens is
+    given); returns the lengths."""
+    _need(path, "path", torch.int32, (tree.n_seqs, None), like=cache.k)
+    _need(tau, "tau", torch.int32, (tree.n_seqs,), like=cache.k)
+    if new_lens is None:
+        new_lens = cache.lens
+    _need(new_lens, "new_lens", torch.int32, tuple(cache.lens.shape), like=cache.k)
+    st = _load().dfv_cache_commit(cache.ref, tree.ref, path.data_ptr(), path.shape[1], tau.data_ptr(),
+                                  new_lens.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(st, "dfv_cache_commit")
+    return new_lens
+
+
+def _index(t: torch.Tensor, what: str, cache: KVCache, n: Optional[int] = None):
+    _need(t, what, torch.int32, (n,), like=cache.k)
+    return t.data_ptr()
+
+
+def cache_copy_pages(cache: KVCache, src: torch.Tensor, dst: torch.Tensor, stream=None):
+    """Page dst[i] <- page src[i] in every layer."""
+    _check(_load().dfv_cache_copy_pages(cache.ref, _index(src, "src", cache), _index(dst, "dst", cache, src.shape[0]),
+                                        src.shape[0], _stream(stream)), "dfv_cache_copy_pages")
+
+
+def pages_reserve(cache: KVCache, seqs: torch.Tensor, n_new: torch.Tensor, ws: torch.Tensor, stream=None):
+    """Pages for n_new[i] tokens after those of sequence seqs[i]."""
+    _check(_load().dfv_pages_reserve(cache.ref, _index(seqs, "seqs", cache), _index(n_new, "n_new", cache, seqs.shape[0]),
+                                     seqs.shape[0], ws.data_ptr(), ws.numel(), _stream(stream)), "dfv_pages_reserve")
+
+
+def pages_fork(cache: KVCache, src: torch.Tensor, dst: torch.Tensor, ws: torch.Tensor, stream=None):
+    """Sequence dst[i], which holds nothing, becomes a copy of src[i]."""
+    _check(_load().dfv_pages_fork(cache.ref, _index(src, "src", cache), _index(dst, "dst", cache, src.shape[0]),
+                                  src.shape[0], ws.data_ptr(), ws.numel(), _stream(stream)), "dfv_pages_fork")
+
+
+def pages_free(cache: KVCache, seqs: torch.Tensor, stream=None):
+    """Drops sequences: their pages lose a holder, their lengths become 0."""
+    _check(_load().dfv_pages_free(cache.ref, _index(seqs, "seqs", cache), seqs.shape[0], _stream(stream)),
+           "dfv_pages_free")
