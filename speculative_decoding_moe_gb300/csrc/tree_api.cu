@@ -222,7 +222,8 @@ static int check_attn_shape(const dfv_kv_cache *cache, const dfv_tree_batch *tre
 
 size_t dfv_tree_attention_workspace_size(const dfv_kv_cache *cache, const dfv_tree_batch *tree, int n_heads) {
   if (check_attn_shape(cache, tree, n_heads)) return 0;
-  return 4096;
+  const dfv::AttnPlan a = dfv::tree_attn_plan(tree->max_nodes, n_heads / cache->n_kv_heads);
+  return dfv::tree_attn_ws(a, tree->n_seqs, cache->head_dim);
 }
 
 int dfv_tree_attention(const dfv_kv_cache *cache, int layer, const dfv_tree_batch *tree, int n_heads, float scale,
@@ -254,7 +255,11 @@ int dfv_tree_attention(const dfv_kv_cache *cache, int layer, const dfv_tree_batc
   p.o_head = o_head;
   p.lse = opt_lse;
   p.err = (unsigned *)((char *)ws + 256);
-  return launched(dfv::launch_tree_attn(p, (cudaStream_t)stream), "tree attention launch");
+  char why[256] = {0};
+  const cudaError_t e = dfv::launch_tree_attn(p, dfv::tree_attn_plan(tree->max_nodes, p.G), ws, (cudaStream_t)stream,
+                                              why, sizeof why);
+  if (e != cudaSuccess && why[0]) return api_fail(DFV_ERR_CUDA, "tree attention: %s", why);
+  return launched(e, "tree attention launch");
 }
 
 size_t dfv_logits_workspace_size(int n_rows_max) {

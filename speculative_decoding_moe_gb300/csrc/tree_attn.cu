@@ -1,93 +1,494 @@
 // tree_attn.cu -- attention of drafted tree nodes over the paged cache.
-#include "tree_common.cuh"
+//
+// Mathematics.  For row (node i, query head of kv head h) and the keys it sees,
+// o = sum_j p_j v_j / sum_j p_j with p_j = 2^(c q.k_j - M), c = scale log2(e),
+// for any M: M is the running maximum of c q.k_j, so one pass over the keys
+// needs only (M, l = sum p, O = sum p v) as state.  Two states over disjoint
+// keys join exactly: with M = max(M1, M2) both l and O are weighted by
+// 2^(Mi - M).  fp16 caches use M - 6 instead (p up to 64), which keeps small p
+// out of fp16's subnormals.
+//
+// Work split.  The nodes x query heads of one kv head are the rows of one tile,
+// so keys and values are read once for all of them.  All (sequence, kv head)
+// pairs' key tiles form one line of units that is cut into equal ranges, one
+// per CTA (or per group of CTAs when the rows need several): short and long
+// sequences, few and many of them, load the SMs alike.  A range that ends
+// inside a pair leaves its state (M, l, O) in the workspace, and a second launch
+// joins the states in range order (no atomics: the same bits every time).
+// The cut depends on the lengths only on the device, so a captured call may be
+// replayed after they change.
+//
+// Kernels, by rows per kv head:
+//   up to 32   mma.sync m16n8k16: bound by reading the cache (the tensor pipe
+//              could take about 64 rows at the HBM rate)
+//   above      tcgen05 on 128-row tiles, scores and outputs in tensor memory
+#include <cstdio>
+#include <cstring>
+
+#include <cudaTypedefs.h>
+
+#include "tc05.cuh"
+#include "tree_attn.cuh"
 
 namespace dfv {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn(char *why, size_t why_len);
+
 namespace {
 
-constexpr int kWarps = 4;
+// ---------------------------------------------------------------- mma.sync kernel
+constexpr int kKt = 64;              // keys per tile: 16 for each of four consumer warps
+constexpr int kMmaThreads = 160;     // producer warp and four consumer warps
+constexpr int kRing = 180 * 1024;    // bytes of the ring of key/value tiles
 
-// One CTA per (sequence, node, query head): each warp takes every fourth key,
-// lanes hold D / 32 elements, with the running maximum and sum of a softmax;
-// the warps' states are joined at the end.
+template <int D>
+constexpr int mma_stages() {
+  return kRing / (2 * kKt * D * 2);
+}
+template <int D, int MT>
+constexpr size_t mma_smem() {
+  return 1024 + (size_t)mma_stages<D>() * 2 * kKt * D * 2 + (size_t)16 * MT * (D + 4) * 4;
+}
+
+// Keys of a tile sit in rows of 128 bytes (64 elements), one block of rows per
+// 64 elements of the head, 16-byte chunks XOR row % 8 (128-byte TMA swizzle).
+__device__ __forceinline__ uint32_t tile_addr(uint32_t base, int half, int row, int chunk) {
+  return base + (uint32_t)(half * kKt * 128 + row * 128) + (uint32_t)((chunk ^ (row & 7)) << 4);
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F16)
+    mma_f16(c, a[0], a[1], a[2], a[3], b0, b1);
+  else
+    mma_bf16(c, a[0], a[1], a[2], a[3], b0, b1);
+}
+
+template <bool F16, int D, int MT>
+__global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __grid_constant__ AttnLaunch L) {
+  constexpr int kStages = mma_stages<D>();
+  constexpr int kHalves = D / 64;
+  constexpr uint32_t kTileBytes = kKt * D * 2;
+  constexpr int kOPitch = D + 4;  // floats; rows of the join buffer 16 bytes apart in banks
+  extern __shared__ __align__(1024) unsigned char sm_raw[];
+  unsigned char *sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
+  __shared__ __align__(8) unsigned long long s_full[kStages], s_empty[kStages];
+  __shared__ volatile int s_abort;
+  __shared__ SchedStart s_start;
+  __shared__ long long s_scan[kMmaThreads / 32];
+  __shared__ float s_m[4][16 * MT], s_l[4][16 * MT];
+  __shared__ int s_bad;
+  const TreeAttnParams &p = L.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring = smem_u32(sm);
+  float *s_o = reinterpret_cast<float *>(sm + (size_t)kStages * 2 * kTileBytes);  // [16 MT][kOPitch]
+  pdl_trigger();
+  if (tid == 0) {
+    s_abort = 0;
+    s_bad = 0;
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&s_full[s]), 1);
+      mbar_init(smem_u32(&s_empty[s]), 4);
+    }
+    mbar_init_fence();
+  }
+  pdl_wait();
+  sched_start<kMmaThreads, kKt>(L, blockIdx.x, s_scan, &s_start);  // syncs the CTA
+  const int row0 = (int)(blockIdx.x % L.n_rt) * 16 * MT;  // first row of this CTA
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    int st = 0, ph = 0, issued = 0;
+    bool ok = true;
+    SegWalk<kKt> wk(L, s_start);
+    const int shift = p.c.page_shift, boxes = shift >= 6 ? 1 : kKt >> shift, rows = kKt / boxes;
+    while (ok && wk.next()) {
+      const int pages = wk.v.s < 0 ? 0 : (wk.total + (1 << shift) - 1) >> shift;
+      const int32_t *table = p.c.table + (size_t)(wk.v.s < 0 ? 0 : wk.v.s) * p.c.max_pages;
+      auto page = [&](int t) {  // this lane's page of tile t, or -1 when there is none
+        const int at = ((t * kKt) >> shift) + lane;
+        return lane < boxes && at < pages ? checked_page(p.c, table[at]) : -1;
+      };
+      int pg = page(wk.t0);
+      for (int t = wk.t0; t < wk.t1; ++t) {
+        const int pgn = t + 1 < wk.t1 ? page(t + 1) : -1;  // the next tile's ids are fetched a tile ahead
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_empty[st]), ph ^ 1, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
+        if (!ok) break;
+        const uint32_t fb = smem_u32(&s_full[st]), dst = ring + (uint32_t)st * 2 * kTileBytes;
+        const unsigned have = __ballot_sync(0xffffffffu, pg >= 0);
+        if (lane == 0) {
+          if (have)
+            mbar_expect_tx(fb, (uint32_t)__popc(have) * 2 * rows * D * 2);
+          else
+            mbar_arrive(fb);
+        }
+        __syncwarp();
+        if (pg >= 0) {
+          const int tok = (t * kKt) & ((1 << shift) - 1);  // 0 unless a page holds several tiles
+#pragma unroll
+          for (int hf = 0; hf < kHalves; ++hf) {
+            const uint32_t off = (uint32_t)(hf * kKt * 128 + lane * rows * 128);
+            tma_kv(dst + off, &L.tm_k, hf * 64, tok, wk.h, pg, L.swap, fb);
+            tma_kv(dst + kTileBytes + off, &L.tm_v, hf * 64, tok, wk.h, pg, L.swap, fb);
+          }
+        }
+        ++issued;
+        if (++st == kStages) { st = 0; ph ^= 1; }
+        pg = pgn;
+      }
+    }
+    // no copy may land after the CTA exits: wait for the last fill of every stage
+    volatile int never = 0;
+    for (int j = issued - kStages < 0 ? 0 : issued - kStages; j < issued; ++j)
+      if (!mbar_wait(smem_u32(&s_full[j % kStages]), (j / kStages) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never)) break;
+    return;
+  }
+
+  // ------------------------------------------------------------------ consumers
+  const int cw = warp - 1, gr = lane >> 2, qc = lane & 3;
+  const float c = p.scale_log2;
+  constexpr float kBias = F16 ? 6.f : 0.f;
+  int st = 0, ph = 0;
+  bool ok = true;
+  SegWalk<kKt> wk(L, s_start);
+  while (wk.next()) {
+    const int R = wk.v.n * p.G;
+    // row r = node * G + head of the group; rows past R are zero and see nothing
+    uint32_t q[MT][D / 16][4];
+    uint64_t mask[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int r = row0 + mt * 16 + hh * 8 + gr;
+        const int i = r / p.G, g = r - i * p.G;
+        mask[mt][hh] = 0;
+        const uint32_t *qp = nullptr;
+        if (r < R) {
+          mask[mt][hh] = row_mask(p.t, wk.v.row0, i) & (wk.v.n >= 64 ? ~0ull : (1ull << wk.v.n) - 1ull);
+          qp = reinterpret_cast<const uint32_t *>(p.q + 2 * ((wk.v.row0 + i) * p.q_row + (wk.h * p.G + g) * p.q_head));
+        }
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          q[mt][ks][hh] = qp ? qp[ks * 8 + qc] : 0u;
+          q[mt][ks][2 + hh] = qp ? qp[ks * 8 + 4 + qc] : 0u;
+        }
+      }
+    float o[MT][D / 8][4], m[MT][2], l[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) { m[mt][hh] = -INFINITY; l[mt][hh] = 0.f; }
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+    }
+    bool bad = false;
+    for (int t = wk.t0; t < wk.t1; ++t) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_full[st]), ph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+      if (!ok) break;
+      const uint32_t kb = ring + (uint32_t)st * 2 * kTileBytes, vb = kb + kTileBytes;
+      const int k0 = t * kKt + cw * 16;  // this warp's 16 keys
+      if (k0 < wk.total) {
+        float s[MT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+        {
+          const int row = cw * 16 + ((lane >> 4) << 3) + (lane & 7), ch = (lane >> 3) & 1;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t b[4];
+            ldsm4(b, tile_addr(kb, ks >> 2, row, (ks & 3) * 2 + ch));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma16<F16>(s[mt][0], q[mt][ks], b[0], b[1]);
+              mma16<F16>(s[mt][1], q[mt][ks], b[2], b[3]);
+            }
+          }
+        }
+        const bool special = k0 + 16 > wk.v.len;  // tree nodes or keys past the end among the 16
+        if (special) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int j = k0 + nt * 8 + 2 * qc + (e & 1) - wk.v.len;  // below 0: committed
+                if (j >= 0 && (j >= wk.v.n || !((mask[mt][e >> 1] >> j) & 1))) s[mt][nt][e] = -INFINITY;
+              }
+        }
+        uint32_t a[MT][4];
+        bool grew = false;
+        float mn[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            float x = fmaxf(fmaxf(s[mt][0][2 * hh], s[mt][0][2 * hh + 1]), fmaxf(s[mt][1][2 * hh], s[mt][1][2 * hh + 1]));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            mn[mt][hh] = fmaxf(m[mt][hh], x);
+            grew |= mn[mt][hh] > m[mt][hh];
+          }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const float f = m[mt][hh] == -INFINITY ? 0.f : ex2((m[mt][hh] - mn[mt][hh]) * c);
+              m[mt][hh] = mn[mt][hh];
+              l[mt][hh] *= f;
+              // nothing is summed yet where f is 0 for want of keys
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n) {
+                o[mt][n][2 * hh] *= f;
+                o[mt][n][2 * hh + 1] *= f;
+              }
+            }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const float z = (m[mt][hh] == -INFINITY ? 0.f : m[mt][hh] * c) - kBias;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const float x = ex2(fmaf(s[mt][nt][2 * hh], c, -z)), y = ex2(fmaf(s[mt][nt][2 * hh + 1], c, -z));
+              l[mt][hh] += x + y;
+              a[mt][nt * 2 + hh] = pack2<F16>(x, y);
+            }
+          }
+        {
+          const int row = cw * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), cc = lane >> 4;
+#pragma unroll
+          for (int d2 = 0; d2 < D / 16; ++d2) {  // 16 elements of the head at a time
+            uint32_t b[4];
+            ldsm4t(b, tile_addr(vb, d2 >> 2, row, (d2 & 3) * 2 + cc));
+            if (special) {
+              // keys past the end count as zero; what is not finite in a node's
+              // value is taken out here and given to the rows that see it at the end
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                b[e] = clean_pair<F16>(b[e], k0 + (e & 1) * 8 + 2 * qc - wk.v.len, wk.v.n, &bad);
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma16<F16>(o[mt][2 * d2], a[mt], b[0], b[1]);
+              mma16<F16>(o[mt][2 * d2 + 1], a[mt], b[2], b[3]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s_empty[st]));
+      if (++st == kStages) { st = 0; ph ^= 1; }
+    }
+    // ---- join the four warps' states
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        float x = l[mt][hh];
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        if (qc == 0) {
+          s_m[cw][mt * 16 + hh * 8 + gr] = m[mt][hh];
+          s_l[cw][mt * 16 + hh * 8 + gr] = x;
+        }
+      }
+    if (bad) s_bad = 1;
+    bar_sync_n(1, 128);
+    for (int w = 0; w < 4; ++w) {
+      if (cw == w) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const int r = mt * 16 + hh * 8 + gr;
+            const float M = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+            const float f = m[mt][hh] == -INFINITY ? 0.f : ex2((m[mt][hh] - M) * c);
+            // a warp without keys for the row adds its zeros (or NaN of a NaN query)
+            const float g = m[mt][hh] == -INFINITY ? 1.f : f;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+              float2 *z = reinterpret_cast<float2 *>(s_o + r * kOPitch + n * 8 + 2 * qc);
+              float2 y = make_float2(o[mt][n][2 * hh] * g, o[mt][n][2 * hh + 1] * g);
+              if (w) {
+                y.x += z->x;
+                y.y += z->y;
+              }
+              *z = y;
+            }
+          }
+      }
+      bar_sync_n(1, 128);
+    }
+    const int isbad = s_bad;
+    const int ct = tid - 32;
+    // ---- the state of the whole segment: output, or partial state
+    for (int u = ct; u < 16 * MT * (D / 8); u += 128) {
+      const int r = u / (D / 8), e = u - r * (D / 8);
+      float M = -INFINITY, lsum = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, s_m[w][r]);
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        lsum += s_m[w][r] == -INFINITY ? s_l[w][r] : s_l[w][r] * ex2((s_m[w][r] - M) * c);
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        const float4 y = *reinterpret_cast<const float4 *>(s_o + r * kOPitch + e * 8 + j);
+        x[j] = y.x; x[j + 1] = y.y; x[j + 2] = y.z; x[j + 3] = y.w;
+      }
+      const float z = (M == -INFINITY ? 0.f : M * c) - kBias;
+      if (wk.whole()) {
+        if (row0 + r < R) store_out<F16>(p, wk.v, row0 + r, wk.h, e, x, z, lsum, isbad);
+      } else {
+        float *to = L.part_o + ((size_t)wk.slot(blockIdx.x) * L.rows + r) * D + e * 8;
+        *reinterpret_cast<float4 *>(to) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4 *>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        if (e == 0) {
+          L.part_ml[(size_t)wk.slot(blockIdx.x) * L.rows + r] = make_float2(M == -INFINITY ? -INFINITY : z, lsum);
+          if (r == 0) L.part_bad[wk.slot(blockIdx.x)] = isbad;
+        }
+      }
+    }
+    bar_sync_n(1, 128);  // the join buffers are free
+    if (ct == 0) s_bad = 0;
+  }
+}
+
+// ---------------------------------------------------------------- join
+// One warp per row of every pair whose units were cut: the states of its ranges
+// in order.  Pairs done by one range were stored by it.
+constexpr int kJoinWarps = 8;
+
 template <bool F16, int D>
-__global__ void __launch_bounds__(32 * kWarps) tree_attn_simple_kernel(const TreeAttnParams p) {
-  constexpr int E = D / 64;  // 32-bit words per lane
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
+__global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join_kernel(const __grid_constant__ AttnLaunch L) {
   pdl_trigger();
   pdl_wait();
-  const int h = blockIdx.x, i = blockIdx.y, b = blockIdx.z;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const TreeAttnParams &p = L.p;
+  const int b = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31;
+  const int r = blockIdx.z * kJoinWarps + (threadIdx.x >> 5);
   const SeqView v = seq_view(p.c, p.t, b);
-  if (i >= v.n) return;
-  const int row = v.row0 + i, hk = h / p.G;
-  const uint64_t mask = row_mask(p.t, v.row0, i);
-  const int total = v.s < 0 ? 0 : v.len + v.n;
-  float2 q[E], o[E];
-  const uint32_t *qp = reinterpret_cast<const uint32_t *>(p.q + 2 * (row * p.q_row + h * p.q_head));
+  if (r >= v.n * p.G) return;
+  const long long s0 = L.starts[b], s1 = L.starts[b + 1], U = L.starts[p.t.n_seqs];
+  const long long T = (s1 - s0) / p.c.Hkv, a = s0 + h * T, e = a + T;
+  const int G = ranges_of(U, L.n_groups), g0 = group_of(a, U, G), g1 = group_of(e - 1, U, G);
+  if (g0 == g1) return;
+  const int rt = r / L.rows, rr = r - rt * L.rows;
+  float M = -INFINITY, l = 0.f, x[D / 32];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = unpack2<F16>(qp[lane + 32 * e]);
-    o[e] = make_float2(0.f, 0.f);
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int pos = warp; pos < total; pos += kWarps) {
-    if (pos >= v.len && !((mask >> (pos - v.len)) & 1)) continue;
-    const int pg = page_of(p.c, v.s, pos);
-    const long long off = kv_off(p.c, p.layer, pg < 0 ? 0 : pg, hk, pos & ((1 << p.c.page_shift) - 1));
-    const uint32_t *kp = reinterpret_cast<const uint32_t *>(p.c.k + 2 * off);
-    const uint32_t *vp = reinterpret_cast<const uint32_t *>(p.c.v + 2 * off);
-    float x = 0.f;
+  for (int j = 0; j < D / 32; ++j) x[j] = 0.f;
+  int bad = 0;
+  for (int g = g0; g <= g1; ++g) {
+    const int second = g == g0 && group_start(g, U, G) != a;
+    const size_t slot = (size_t)(2 * (g * L.n_rt + rt) + second);
+    const float2 ml = __ldcg(&L.part_ml[slot * L.rows + rr]);
+    const float Mn = fmaxf(M, ml.x);
+    const float f0 = M == -INFINITY ? 1.f : ex2(M - Mn), f1 = ml.x == -INFINITY ? 1.f : ex2(ml.x - Mn);
+    M = Mn;
+    l = l * f0 + ml.y * f1;
+    bad |= L.part_bad[slot];
+    const float *src = L.part_o + (slot * L.rows + rr) * D;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float2 kk = unpack2<F16>(kp[lane + 32 * e]);
-      x += q[e].x * kk.x + q[e].y * kk.y;
+    for (int j = 0; j < D / 64; ++j) {
+      const float2 y = __ldcg(reinterpret_cast<const float2 *>(src + j * 64 + lane * 2));
+      x[2 * j] = x[2 * j] * f0 + y.x * f1;
+      x[2 * j + 1] = x[2 * j + 1] * f0 + y.y * f1;
     }
+  }
+  const int i = r / p.G, gg = r - i * p.G, head = h * p.G + gg;
+  const size_t row = v.row0 + i;
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-    x *= p.scale_log2;
-    const float mn = fmaxf(m, x);
-    const float a = m == -INFINITY ? 0.f : exp2f(m - mn), pr = x == -INFINITY ? 0.f : exp2f(x - mn);
-    l = l * a + pr;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float2 vv = unpack2<F16>(vp[lane + 32 * e]);
-      o[e].x = o[e].x * a + pr * vv.x;
-      o[e].y = o[e].y * a + pr * vv.y;
+  for (int j = 0; j < D / 64; ++j) {
+    float2 y = make_float2(x[2 * j] * inv, x[2 * j + 1] * inv);
+    if (bad) {
+      y.x += unseen<F16>(p, v, i, h, j * 64 + lane * 2);
+      y.y += unseen<F16>(p, v, i, h, j * 64 + lane * 2 + 1);
     }
-    m = mn;
+    reinterpret_cast<uint32_t *>(p.o + 2 * (row * p.o_row + head * p.o_head))[j * 32 + lane] = pack2<F16>(y.x, y.y);
   }
-  if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
-#pragma unroll
-  for (int e = 0; e < E; ++e) reinterpret_cast<float2 *>(s_o[warp])[lane + 32 * e] = o[e];
-  __syncthreads();
-  float M = -INFINITY, L = 0.f, f[kWarps];
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
-  for (int w = 0; w < kWarps; ++w) {
-    f[w] = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - M);
-    L += f[w] * s_l[w];
+  if (p.lse && lane == 0)
+    p.lse[row * p.H + head] = l == 0.f ? -INFINITY : (M == -INFINITY ? l : (M + log2f(l)) * 0.69314718055994531f);
+}
+
+bool encode_kv(CUtensorMap *map, const CacheParams &c, const char *base, int layer, int rows, int swap, char *why,
+               size_t why_len) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn(why, why_len);
+  if (!fn) return false;
+  // a dimension of one entry has no stride of its own
+  const cuuint64_t one = 16;
+  const cuuint64_t tok[2] = {(cuuint64_t)1 << c.page_shift, (cuuint64_t)c.st * 2};
+  const cuuint64_t head[2] = {(cuuint64_t)c.Hkv, c.Hkv > 1 ? (cuuint64_t)c.sh * 2 : one};
+  const cuuint64_t page[2] = {(cuuint64_t)c.n_pages, c.n_pages > 1 ? (cuuint64_t)c.sp * 2 : one};
+  const cuuint64_t *a = swap ? head : tok, *b = swap ? tok : head;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.D, a[0], b[0], page[0]};
+  const cuuint64_t strides[3] = {a[1], b[1], page[1]};
+  const cuuint32_t box[4] = {64, swap ? 1u : (cuuint32_t)rows, swap ? (cuuint32_t)rows : 1u, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, c.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                        const_cast<char *>(base + 2 * layer * c.sl), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    snprintf(why, why_len, "tensor map of the cache refused (%d)", (int)r);
+    return false;
   }
-  for (int e = threadIdx.x; e < D / 2; e += 32 * kWarps) {
-    float x = 0.f, y = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      x += f[w] * s_o[w][2 * e];
-      y += f[w] * s_o[w][2 * e + 1];
-    }
-    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // NaN stays NaN
-    reinterpret_cast<uint32_t *>(p.o + 2 * (row * p.o_row + h * p.o_head))[e] = pack2<F16>(x * inv, y * inv);
-  }
-  if (p.lse && threadIdx.x == 0)
-    p.lse[(size_t)row * p.H + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+  return true;
+}
+
+template <bool F16, int D, int MT>
+cudaError_t launch_mma(const AttnLaunch &L, cudaStream_t s) {
+  auto kern = tree_attn_mma_kernel<F16, D, MT>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)mma_smem<D, MT>());
+  if (e != cudaSuccess) return e;
+  return launch_chained(kern, dim3(L.n_groups * L.n_rt), dim3(kMmaThreads), mma_smem<D, MT>(), s, L);
+}
+
+template <bool F16, int D>
+cudaError_t launch_typed(AttnLaunch &L, cudaStream_t s) {
+  const int R = L.p.t.max_nodes * L.p.G;
+  cudaError_t e = L.rows == 16 ? launch_mma<F16, D, 1>(L, s) : launch_mma<F16, D, 2>(L, s);
+  if (e != cudaSuccess) return e;
+  return launch_chained(tree_attn_join_kernel<F16, D>, dim3(L.p.t.n_seqs, L.p.c.Hkv, (R + kJoinWarps - 1) / kJoinWarps),
+                        dim3(32 * kJoinWarps), 0, s, L);
 }
 
 }  // namespace
 
-cudaError_t launch_tree_attn(const TreeAttnParams &p, cudaStream_t s) {
-  const dim3 grid(p.H, p.t.max_nodes, p.t.n_seqs), block(32 * kWarps);
-  if (p.c.D == 128)
-    return p.c.f16 ? launch_chained(tree_attn_simple_kernel<true, 128>, grid, block, 0, s, p)
-                   : launch_chained(tree_attn_simple_kernel<false, 128>, grid, block, 0, s, p);
-  return p.c.f16 ? launch_chained(tree_attn_simple_kernel<true, 64>, grid, block, 0, s, p)
-                 : launch_chained(tree_attn_simple_kernel<false, 64>, grid, block, 0, s, p);
+AttnPlan tree_attn_plan(int max_nodes, int G) {
+  AttnPlan a = {};
+  const int R = max_nodes * G;
+  a.rows = R <= 16 ? 16 : 32;
+  a.n_rt = (R + a.rows - 1) / a.rows;
+  a.n_groups = kAttnCtas / a.n_rt < 1 ? 1 : kAttnCtas / a.n_rt;
+  return a;
+}
+
+size_t tree_attn_ws(const AttnPlan &a, int n_seqs, int D) { return attn_sections(nullptr, a, n_seqs, D, nullptr); }
+
+cudaError_t launch_tree_attn(const TreeAttnParams &p, const AttnPlan &a, void *ws, cudaStream_t s, char *why,
+                             size_t why_len) {
+  static thread_local AttnLaunch L;
+  L.p = p;
+  L.rows = a.rows;
+  L.n_rt = a.n_rt;
+  L.n_groups = a.n_groups;
+  attn_sections(&L, a, p.t.n_seqs, p.c.D, ws);
+  const int tile = kKt, page = 1 << p.c.page_shift, rows = page < tile ? page : tile;
+  L.swap = p.c.Hkv > 1 && p.c.sh < p.c.st;
+  if (!encode_kv(&L.tm_k, p.c, p.c.k, p.layer, rows, L.swap, why, why_len) ||
+      !encode_kv(&L.tm_v, p.c, p.c.v, p.layer, rows, L.swap, why, why_len))
+    return cudaErrorInvalidValue;
+  if (p.c.D == 128) return p.c.f16 ? launch_typed<true, 128>(L, s) : launch_typed<false, 128>(L, s);
+  return p.c.f16 ? launch_typed<true, 64>(L, s) : launch_typed<false, 64>(L, s);
 }
 
 }  // namespace dfv

@@ -1,0 +1,244 @@
+// tree_attn.cuh -- what the attention kernels share: the cut of the work line
+// into ranges, the walk over a range's segments, and how states and outputs
+// are stored.
+#pragma once
+
+#include "tree_common.cuh"
+
+namespace dfv {
+
+struct AttnLaunch {
+  CUtensorMap tm_k, tm_v;  // one layer's pages: {head_dim, token, head, page}, token and head in stride order
+  TreeAttnParams p;
+  int rows;      // rows (nodes x heads of a kv head) per CTA
+  int n_rt;      // CTAs per range, for further rows
+  int n_groups;  // ranges
+  int swap;      // head before token in the tensor maps
+  long long *starts;  // [n_seqs + 1] first unit of each sequence, then the number of units
+  float2 *part_ml;    // [2 CTAs][rows] (M, l) of partial states
+  float *part_o;      // [2 CTAs][rows][D] their sums of p v
+  int *part_bad;      // [2 CTAs] a tree value that is not finite was left out
+};
+
+// Sections of the attention workspace; returns its size.
+inline size_t attn_sections(AttnLaunch *L, const AttnPlan &a, int n_seqs, int D, void *ws) {
+  const size_t slots = 2 * (size_t)a.n_groups * a.n_rt;
+  size_t off = 512;  // the error word is at 256
+  auto take = [&](size_t n) {
+    void *q = ws ? (void *)((char *)ws + off) : nullptr;
+    off += (n + 255) & ~(size_t)255;
+    return q;
+  };
+  long long *starts = (long long *)take((size_t)(n_seqs + 1) * 8);
+  int *bad = (int *)take(slots * 4);
+  float2 *ml = (float2 *)take(slots * a.rows * 8);
+  float *o = (float *)take(slots * a.rows * D * 4);
+  if (L) {
+    L->starts = starts;
+    L->part_bad = bad;
+    L->part_ml = ml;
+    L->part_o = o;
+  }
+  return off;
+}
+
+// ---------------------------------------------------------------- the work line
+// Sequence b's units are its kv heads' key tiles, head after head; a pair
+// without keys is one unit (its outputs have to be written), a sequence
+// without rows none.  Range g of G over U units is [g U / G, (g + 1) U / G);
+// there are no more ranges than units.
+struct SchedStart {
+  long long u0, u1, base;  // the range, and the first unit of sequence b
+  int b;
+};
+
+// Ranges in use: no range is empty.
+__device__ __forceinline__ int ranges_of(long long U, int n_groups) {
+  return U >= n_groups ? n_groups : U > 0 ? (int)U : 1;
+}
+__device__ __forceinline__ long long group_start(int g, long long U, int G) { return g * U / G; }
+__device__ __forceinline__ int group_of(long long u, long long U, int G) { return (int)(((u + 1) * G - 1) / U); }
+
+template <int KT>
+__device__ __forceinline__ long long seq_units(const AttnLaunch &L, int b) {
+  const SeqView v = seq_view(L.p.c, L.p.t, b);
+  if (v.n == 0) return 0;
+  const int total = v.s < 0 ? 0 : v.len + v.n;
+  return (long long)L.p.c.Hkv * (total > 0 ? (total + KT - 1) / KT : 1);
+}
+
+// The range of CTA `block` and the sequence it starts in.  All NT threads of
+// the CTA call it; s_scan holds NT / 32 values.  CTA 0 also writes the first
+// units of all sequences for the join.
+template <int NT, int KT>
+__device__ __forceinline__ void sched_start(const AttnLaunch &L, int block, long long *s_scan, SchedStart *out) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = L.p.t.n_seqs;
+  const int per = (n + NT - 1) / NT, b0 = min(n, tid * per), b1 = min(n, b0 + per);
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) sum += seq_units<KT>(L, b);
+  long long v = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += a;
+  }
+  if (lane == 31) s_scan[warp] = v;
+  if (tid == 0) {
+    out->u0 = out->u1 = out->base = 0;
+    out->b = 0;
+  }
+  __syncthreads();
+  long long U = 0, at = v - sum;
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) at += s_scan[w];
+    U += s_scan[w];
+  }
+  const int g = block / L.n_rt, G = ranges_of(U, L.n_groups);
+  const long long u0 = group_start(g, U, G), u1 = g < G ? group_start(g + 1, U, G) : u0;
+  const bool mine = u0 < u1 && at <= u0 && u0 < at + sum;
+  if (mine || block == 0) {
+    long long base = at;
+    for (int b = b0; b < b1; ++b) {
+      const long long c = seq_units<KT>(L, b);
+      if (block == 0) L.starts[b] = base;
+      if (mine && base <= u0 && u0 < base + c) {
+        out->u0 = u0;
+        out->u1 = u1;
+        out->base = base;
+        out->b = b;
+      }
+      base += c;
+    }
+  }
+  if (block == 0 && tid == 0) L.starts[n] = U;
+  __syncthreads();
+}
+
+// Segments of a range: tiles [t0, t1) of one (sequence, kv head).
+template <int KT>
+struct SegWalk {
+  const AttnLaunch &L;
+  const long long first, end;
+  long long u, base;
+  int b, h, t0, t1, T, total;
+  long long at;  // first unit of the segment
+  SeqView v;
+  __device__ __forceinline__ SegWalk(const AttnLaunch &l, const SchedStart &s)
+      : L(l), first(s.u0), end(s.u1), u(s.u0), base(s.base), b(s.b) {}
+  __device__ __forceinline__ bool next() {
+    while (u < end) {
+      v = seq_view(L.p.c, L.p.t, b);
+      total = v.s < 0 ? 0 : v.len + v.n;
+      T = v.n == 0 ? 0 : total > 0 ? (total + KT - 1) / KT : 1;
+      const long long w = u - base, units = (long long)L.p.c.Hkv * T;
+      if (w < units) {
+        h = (int)(w / T);
+        t0 = (int)(w - (long long)h * T);
+        t1 = (int)min((long long)T, t0 + (end - u));
+        at = u;
+        u += t1 - t0;
+        return true;
+      }
+      base += units;
+      ++b;
+    }
+    return false;
+  }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == T; }
+  // a range cuts at most two pairs: the one it starts in and the one it ends in
+  __device__ __forceinline__ int slot(int block) const { return 2 * block + (at != first); }
+};
+
+// ---------------------------------------------------------------- pieces
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A page id as read from the table; one out of range is read as page 0.
+__device__ __forceinline__ int checked_page(const CacheParams &c, int pg) {
+  if ((unsigned)pg < (unsigned)c.n_pages) return pg;
+  flag_err(c.err, DFV_KVERR_PAGE);
+  return 0;
+}
+
+__device__ __forceinline__ void tma_kv(uint32_t dst, const CUtensorMap *map, int x, int tok, int h, int pg, int swap,
+                                       uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(swap ? h : tok), "r"(swap ? tok : h), "r"(pg), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+// Values of keys j (low half) and j + 1, j counted from the tree's first node:
+// zero past the last node; a node's value that is not finite becomes zero and
+// sets *bad.
+template <bool F16>
+__device__ __forceinline__ uint32_t clean_pair(uint32_t v, int j, int n, bool *bad) {
+  constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
+  if (j >= n) v &= 0xffff0000u;
+  if (j + 1 >= n) v &= 0x0000ffffu;
+  if (j >= 0 && (v & kExp) == kExp) {
+    v &= 0xffff0000u;
+    *bad = true;
+  }
+  if (j + 1 >= 0 && (v & (kExp << 16)) == (kExp << 16)) {
+    v &= 0x0000ffffu;
+    *bad = true;
+  }
+  return v;
+}
+
+// What clean_pair took out of element d of the values that node i sees.
+template <bool F16>
+__device__ __noinline__ float unseen(const TreeAttnParams &p, const SeqView &v, int i, int h, int d) {
+  if (v.s < 0) return 0.f;
+  const uint64_t mask = row_mask(p.t, v.row0, i);
+  float x = 0.f;
+  for (int j = 0; j < v.n; ++j) {
+    if (!((mask >> j) & 1)) continue;
+    const int pos = v.len + j;
+    const int pg = checked_page(p.c, p.c.table[(size_t)v.s * p.c.max_pages + (pos >> p.c.page_shift)]);
+    const long long off = kv_off(p.c, p.layer, pg, h, pos & ((1 << p.c.page_shift) - 1)) + d;
+    const uint32_t w = reinterpret_cast<const uint16_t *>(p.c.v)[off];
+    const float y = unpack2<F16>(w).x;
+    if (!isfinite(y)) x += y;
+  }
+  return x;
+}
+
+// Output piece e (8 elements) of row r: x / l, and lse = (z + log2 l) ln 2.
+template <bool F16>
+__device__ __forceinline__ void store_out(const TreeAttnParams &p, const SeqView &v, int r, int h, int e, const float *x,
+                                          float z, float l, int bad) {
+  const int i = r / p.G, g = r - i * p.G, head = h * p.G + g;
+  const size_t row = v.row0 + i;
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a = x[2 * j] * inv, b = x[2 * j + 1] * inv;
+    if (bad) {
+      a += unseen<F16>(p, v, i, h, e * 8 + 2 * j);
+      b += unseen<F16>(p, v, i, h, e * 8 + 2 * j + 1);
+    }
+    w[j] = pack2<F16>(a, b);
+  }
+  *reinterpret_cast<uint4 *>(p.o + 2 * (row * p.o_row + head * p.o_head + e * 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (e == 0 && p.lse) p.lse[row * p.H + head] = l == 0.f ? -INFINITY : (z + log2f(l)) * 0.69314718055994531f;
+}
+
+}  // namespace dfv

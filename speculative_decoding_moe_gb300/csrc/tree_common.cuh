@@ -155,7 +155,15 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 
 cudaError_t launch_rope_append(const RopeParams &p, cudaStream_t s);
-cudaError_t launch_tree_attn(const TreeAttnParams &p, cudaStream_t s);
+// Rows per CTA, CTAs per range and ranges of an attention call.
+constexpr int kAttnCtas = 152;  // one per SM of GB300
+struct AttnPlan {
+  int rows, n_rt, n_groups;
+};
+AttnPlan tree_attn_plan(int max_nodes, int G);
+size_t tree_attn_ws(const AttnPlan &a, int n_seqs, int D);
+cudaError_t launch_tree_attn(const TreeAttnParams &p, const AttnPlan &a, void *ws, cudaStream_t s, char *why,
+                             size_t why_len);
 cudaError_t launch_logits(const LogitsParams &p, cudaStream_t s);
 cudaError_t launch_accept_tree(const AcceptTreeParams &p, cudaStream_t s);
 cudaError_t launch_commit(const CommitParams &p, cudaStream_t s);
