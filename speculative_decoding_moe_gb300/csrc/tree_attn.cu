@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
         mask[mt][hh] = 0;
         const uint32_t *qp = nullptr;
         if (r < R) {
-          mask[mt][hh] = row_mask(p.t, wk.v.row0, i) & (wk.v.n >= 64 ? ~0ull : (1ull << wk.v.n) - 1ull);
+          mask[mt][hh] = wk.mask_of(r);
           qp = reinterpret_cast<const uint32_t *>(p.q + 2 * ((wk.v.row0 + i) * p.q_row + (wk.h * p.G + g) * p.q_head));
         }
 #pragma unroll
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int j = k0 + nt * 8 + 2 * qc + (e & 1) - wk.v.len;  // below 0: committed
-                if (j >= 0 && (j >= wk.v.n || !((mask[mt][e >> 1] >> j) & 1))) s[mt][nt][e] = -INFINITY;
+                if (j >= 0 && (j >= wk.nodes || !((mask[mt][e >> 1] >> j) & 1))) s[mt][nt][e] = -INFINITY;
               }
         }
         uint32_t a[MT][4];
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
               // value is taken out here and given to the rows that see it at the end
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                b[e] = clean_pair<F16>(b[e], k0 + (e & 1) * 8 + 2 * qc - wk.v.len, wk.v.n, &bad);
+                b[e] = clean_pair<F16>(b[e], k0 + (e & 1) * 8 + 2 * qc - wk.v.len, wk.nodes, &bad);
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -455,7 +455,9 @@ cudaError_t launch_mma(const AttnLaunch &L, cudaStream_t s) {
 template <bool F16, int D>
 cudaError_t launch_typed(AttnLaunch &L, cudaStream_t s) {
   const int R = L.p.t.max_nodes * L.p.G;
-  cudaError_t e = L.rows == 16 ? launch_mma<F16, D, 1>(L, s) : launch_mma<F16, D, 2>(L, s);
+  cudaError_t e = L.rows >= 128  ? launch_attn_tc(L, s)
+                  : L.rows == 16 ? launch_mma<F16, D, 1>(L, s)
+                                 : launch_mma<F16, D, 2>(L, s);
   if (e != cudaSuccess) return e;
   return launch_chained(tree_attn_join_kernel<F16, D>, dim3(L.p.t.n_seqs, L.p.c.Hkv, (R + kJoinWarps - 1) / kJoinWarps),
                         dim3(32 * kJoinWarps), 0, s, L);
@@ -466,7 +468,7 @@ cudaError_t launch_typed(AttnLaunch &L, cudaStream_t s) {
 AttnPlan tree_attn_plan(int max_nodes, int G) {
   AttnPlan a = {};
   const int R = max_nodes * G;
-  a.rows = R <= 16 ? 16 : 32;
+  a.rows = R <= 16 ? 16 : R <= 32 ? 32 : R <= 128 ? 128 : 256;
   a.n_rt = (R + a.rows - 1) / a.rows;
   a.n_groups = kAttnCtas / a.n_rt < 1 ? 1 : kAttnCtas / a.n_rt;
   return a;
@@ -482,7 +484,7 @@ cudaError_t launch_tree_attn(const TreeAttnParams &p, const AttnPlan &a, void *w
   L.n_rt = a.n_rt;
   L.n_groups = a.n_groups;
   attn_sections(&L, a, p.t.n_seqs, p.c.D, ws);
-  const int tile = kKt, page = 1 << p.c.page_shift, rows = page < tile ? page : tile;
+  const int tile = L.rows >= 128 ? 128 : kKt, page = 1 << p.c.page_shift, rows = page < tile ? page : tile;
   L.swap = p.c.Hkv > 1 && p.c.sh < p.c.st;
   if (!encode_kv(&L.tm_k, p.c, p.c.k, p.layer, rows, L.swap, why, why_len) ||
       !encode_kv(&L.tm_v, p.c, p.c.v, p.layer, rows, L.swap, why, why_len))

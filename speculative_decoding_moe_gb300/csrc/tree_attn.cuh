@@ -20,6 +20,8 @@ struct AttnLaunch {
   int *part_bad;      // [2 CTAs] a tree value that is not finite was left out
 };
 
+cudaError_t launch_attn_tc(const AttnLaunch &L, cudaStream_t s);  // tree_attn_tc.cu: rows 128 or 256
+
 // Sections of the attention workspace; returns its size.
 inline size_t attn_sections(AttnLaunch *L, const AttnPlan &a, int n_seqs, int D, void *ws) {
   const size_t slots = 2 * (size_t)a.n_groups * a.n_rt;
@@ -121,6 +123,7 @@ struct SegWalk {
   const long long first, end;
   long long u, base;
   int b, h, t0, t1, T, total;
+  int nodes;  // of the sequence in the cache: none where the cache side is unusable
   long long at;  // first unit of the segment
   SeqView v;
   __device__ __forceinline__ SegWalk(const AttnLaunch &l, const SchedStart &s)
@@ -128,7 +131,8 @@ struct SegWalk {
   __device__ __forceinline__ bool next() {
     while (u < end) {
       v = seq_view(L.p.c, L.p.t, b);
-      total = v.s < 0 ? 0 : v.len + v.n;
+      nodes = v.s < 0 ? 0 : v.n;
+      total = v.len + nodes;
       T = v.n == 0 ? 0 : total > 0 ? (total + KT - 1) / KT : 1;
       const long long w = u - base, units = (long long)L.p.c.Hkv * T;
       if (w < units) {
@@ -143,6 +147,11 @@ struct SegWalk {
       ++b;
     }
     return false;
+  }
+  // The nodes that row r sees.
+  __device__ __forceinline__ uint64_t mask_of(int r) const {
+    if (nodes == 0) return 0;
+    return row_mask(L.p.t, v.row0, r / L.p.G) & (nodes >= 64 ? ~0ull : (1ull << nodes) - 1ull);
   }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == T; }
   // a range cuts at most two pairs: the one it starts in and the one it ends in
