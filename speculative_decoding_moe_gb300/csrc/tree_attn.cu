@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
   constexpr int kHalves = D / 64;
   constexpr uint32_t kTileBytes = kKt * D * 2;
   constexpr int kOPitch = D + 4;  // floats; rows of the join buffer 16 bytes apart in banks
-  extern __shared__ __align__(1024) unsigned char sm_raw[];
+  extern __shared__ __align__(16) unsigned char sm_raw[];
   unsigned char *sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) unsigned long long s_full[kStages], s_empty[kStages];
   __shared__ volatile int s_abort;
@@ -81,7 +81,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = smem_u32(sm);
   float *s_o = reinterpret_cast<float *>(sm + (size_t)kStages * 2 * kTileBytes);  // [16 MT][kOPitch]
-  pdl_trigger();
   if (tid == 0) {
     s_abort = 0;
     s_bad = 0;
@@ -92,6 +91,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
     mbar_init_fence();
   }
   pdl_wait();
+  pdl_trigger();  // the join may now read the call's inputs
   sched_start<kMmaThreads, kKt>(L, blockIdx.x, s_scan, &s_start);  // syncs the CTA
   const int row0 = (int)(blockIdx.x % L.n_rt) * 16 * MT;  // first row of this CTA
 
@@ -365,56 +365,96 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
 
 // ---------------------------------------------------------------- join
 // One warp per row of every pair whose units were cut: the states of its ranges
-// in order.  Pairs done by one range were stored by it.
-constexpr int kJoinWarps = 8;
+// in order.  Pairs done by one range were stored by it.  Lane k takes the (M, l)
+// of every 32nd state, so all of them are in flight at once; the sums of p v
+// follow eight states at a time.
+constexpr int kJoinWarps = 4;
+constexpr int kJoinStates = (kAttnCtas + 31) / 32;
 
 template <bool F16, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join_kernel(const __grid_constant__ AttnLaunch L) {
+  constexpr int E = D / 32;  // elements of a lane
   pdl_trigger();
-  pdl_wait();
   const TreeAttnParams &p = L.p;
   const int b = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31;
   const int r = blockIdx.z * kJoinWarps + (threadIdx.x >> 5);
+  // the first launch releases this one after its own wait: the call's inputs are final
   const SeqView v = seq_view(p.c, p.t, b);
   if (r >= v.n * p.G) return;
+  pdl_wait();
   const long long s0 = L.starts[b], s1 = L.starts[b + 1], U = L.starts[p.t.n_seqs];
   const long long T = (s1 - s0) / p.c.Hkv, a = s0 + h * T, e = a + T;
   const int G = ranges_of(U, L.n_groups), g0 = group_of(a, U, G), g1 = group_of(e - 1, U, G);
   if (g0 == g1) return;
-  const int rt = r / L.rows, rr = r - rt * L.rows;
-  float M = -INFINITY, l = 0.f, x[D / 32];
-#pragma unroll
-  for (int j = 0; j < D / 32; ++j) x[j] = 0.f;
+  const int rt = r / L.rows, rr = r - rt * L.rows, n = g1 - g0 + 1;
+  // state k is range g0 + k's; only the first range can hold the pair as its second cut
+  const int second = group_start(g0, U, G) != a;
+  auto slot = [&](int k) { return (size_t)(2 * ((g0 + k) * L.n_rt + rt) + (k == 0 ? second : 0)); };
+  float2 ml[kJoinStates];
   int bad = 0;
-  for (int g = g0; g <= g1; ++g) {
-    const int second = g == g0 && group_start(g, U, G) != a;
-    const size_t slot = (size_t)(2 * (g * L.n_rt + rt) + second);
-    const float2 ml = __ldcg(&L.part_ml[slot * L.rows + rr]);
-    const float Mn = fmaxf(M, ml.x);
-    const float f0 = M == -INFINITY ? 1.f : ex2(M - Mn), f1 = ml.x == -INFINITY ? 1.f : ex2(ml.x - Mn);
-    M = Mn;
-    l = l * f0 + ml.y * f1;
-    bad |= L.part_bad[slot];
-    const float *src = L.part_o + (slot * L.rows + rr) * D;
+  float M = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-      const float2 y = __ldcg(reinterpret_cast<const float2 *>(src + j * 64 + lane * 2));
-      x[2 * j] = x[2 * j] * f0 + y.x * f1;
-      x[2 * j + 1] = x[2 * j + 1] * f0 + y.y * f1;
+  for (int q = 0; q < kJoinStates; ++q) {
+    const int k = lane + 32 * q;
+    ml[q] = make_float2(-INFINITY, 0.f);
+    if (k < n) {
+      ml[q] = __ldcg(&L.part_ml[slot(k) * L.rows + rr]);
+      bad |= __ldcg(&L.part_bad[slot(k)]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kJoinStates; ++q) M = fmaxf(M, ml[q].x);
+  M = warp_max(M);
+  bad = __any_sync(0xffffffffu, bad != 0);
+  float l = 0.f, w[kJoinStates];
+#pragma unroll
+  for (int q = 0; q < kJoinStates; ++q) {
+    w[q] = ml[q].x == -INFINITY ? 1.f : ex2(ml[q].x - M);  // a state without keys holds zeros (or NaN of a NaN query)
+    l += ml[q].y * w[q];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  float x[E];
+#pragma unroll
+  for (int j = 0; j < E; ++j) x[j] = 0.f;
+  const float *base = L.part_o + rr * D + lane * E;
+  const size_t pitch = (size_t)L.rows * D;
+#pragma unroll
+  for (int q = 0; q < kJoinStates; ++q) {
+#pragma unroll 1
+    for (int k0 = 32 * q; k0 < min(n, 32 * q + 32); k0 += 8) {
+      float y[8][E];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (k0 + i < n) load_floats<E>(base + slot(k0 + i) * pitch, y[i]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float f = __shfl_sync(0xffffffffu, w[q], (k0 + i) & 31);
+        if (k0 + i < n) {
+#pragma unroll
+          for (int j = 0; j < E; ++j) x[j] = fmaf(y[i][j], f, x[j]);
+        }
+      }
     }
   }
   const int i = r / p.G, gg = r - i * p.G, head = h * p.G + gg;
   const size_t row = v.row0 + i;
   const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
+  uint32_t out[E / 2];
 #pragma unroll
-  for (int j = 0; j < D / 64; ++j) {
-    float2 y = make_float2(x[2 * j] * inv, x[2 * j + 1] * inv);
+  for (int j = 0; j < E; j += 2) {
+    float2 y = make_float2(x[j] * inv, x[j + 1] * inv);
     if (bad) {
-      y.x += unseen<F16>(p, v, i, h, j * 64 + lane * 2);
-      y.y += unseen<F16>(p, v, i, h, j * 64 + lane * 2 + 1);
+      y.x += unseen<F16>(p, v, i, h, lane * E + j);
+      y.y += unseen<F16>(p, v, i, h, lane * E + j + 1);
     }
-    reinterpret_cast<uint32_t *>(p.o + 2 * (row * p.o_row + head * p.o_head))[j * 32 + lane] = pack2<F16>(y.x, y.y);
+    out[j / 2] = pack2<F16>(y.x, y.y);
   }
+  uint32_t *to = reinterpret_cast<uint32_t *>(p.o + 2 * (row * p.o_row + head * p.o_head)) + lane * (E / 2);
+  if (E == 4)
+    *reinterpret_cast<uint2 *>(to) = make_uint2(out[0], out[E / 2 - 1]);
+  else
+    *to = out[0];
   if (p.lse && lane == 0)
     p.lse[row * p.H + head] = l == 0.f ? -INFINITY : (M == -INFINITY ? l : (M + log2f(l)) * 0.69314718055994531f);
 }

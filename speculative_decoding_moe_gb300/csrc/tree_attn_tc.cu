@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
   constexpr int LA = DUAL ? 1 : 2;  // K tiles ahead of the V tile in the ring
   constexpr float kBias = F16 ? 6.f : 0.f;
   constexpr int kHalves = D / 64;
-  extern __shared__ __align__(1024) unsigned char sm_raw[];
+  extern __shared__ __align__(16) unsigned char sm_raw[];
   unsigned char *sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) unsigned long long s_full[S::kSlots], s_empty[S::kSlots], s_sfull[2], s_pready[2], s_odone[2],
       s_qready, s_drain;
@@ -156,7 +156,6 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned char *s_q = sm, *s_ring = sm + S::kQ;
   const uint32_t q_addr = smem_u32(s_q), ring = smem_u32(s_ring);
-  pdl_trigger();
   if (tid == 0) {
     s_abort = 0;
     s_bad = 0;
@@ -179,6 +178,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
   }
   tc_fence_before();
   pdl_wait();
+  pdl_trigger();  // the join may now read the call's inputs
   sched_start<kTThreads, kTKeys>(L, blockIdx.x, s_scan, &s_start);  // syncs the CTA
   tc_fence_after();
   const uint32_t tmem = s_tmem;
