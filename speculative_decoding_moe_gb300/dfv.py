@@ -387,34 +387,49 @@ def accept_greedy_noalloc(logits: torch.Tensor, draft: torch.Tensor, tau: Option
 
 
 # ---------------------------------------------------------------- tree verify
-def _need(t: Optional[torch.Tensor], what: str, dtype, shape=None, optional=False, like: Optional[torch.Tensor] = None):
-    """Type, shape (None entries free), contiguity and device of one argument."""
+# The arguments of a small call cost more to check than its kernel to run, so each helper decides with one condition
+# and only a refusal takes the time to say why.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _on(stream, index: int) -> int:
+    """Stream handle of a call: the given stream, or torch's current one on the tensors' device."""
+    return _raw_stream(index) if stream is None else stream.cuda_stream
+
+
+def _refuse(t, what: str, dtype, shape, index: int):
     if t is None:
-        if optional:
-            return
         raise ValueError("%s is missing" % what)
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
-    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
-        raise ValueError("%s must have shape %s, got %s" % (what, shape, tuple(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % what)
-    if like is not None and t.device != like.device:
-        raise ValueError("%s is on %s, not on %s" % (what, t.device, like.device))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, not with the other tensors of the call" % (what, t.device))
+    raise ValueError("%s must be contiguous%s" % (what, " in its last dimension" if len(shape) == 3 else ""))
 
 
-def _rows3(t: torch.Tensor, what: str, rows: int, heads: int, dim: int, dtype, like: torch.Tensor):
-    """(pointer, row stride, head stride) of a [rows, heads, dim] tensor whose last dimension is contiguous."""
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s like the cache, got %s" % (what, dtype, t.dtype))
-    if tuple(t.shape) != (rows, heads, dim):
-        raise ValueError("%s must have shape %s, got %s" % (what, (rows, heads, dim), tuple(t.shape)))
-    if t.stride(2) != 1:
-        raise ValueError("%s: the head dimension must be contiguous" % what)
-    if t.device != like.device:
-        raise ValueError("%s is on %s, not on %s" % (what, t.device, like.device))
+def _need(t: Optional[torch.Tensor], what: str, dtype, shape, index: int) -> int:
+    """Address of a contiguous tensor of this type and shape on this device."""
+    if t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+        _refuse(t, what, dtype, shape, index)
+    return t.data_ptr()
+
+
+def _given(t: Optional[torch.Tensor], what: str, dtype, shape, index: int) -> Optional[int]:
+    """_need for an argument that may be left out."""
+    return None if t is None else _need(t, what, dtype, shape, index)
+
+
+def _rows3(t: torch.Tensor, what: str, rows: int, heads: int, dim: int, dtype, index: int):
+    """(address, row stride, head stride) of a [rows, heads, dim] tensor whose last dimension is contiguous."""
+    if t.dtype is not dtype or t.shape != (rows, heads, dim) or t.get_device() != index:
+        _refuse(t, what, dtype, (rows, heads, dim), index)
+    s = t.stride()
+    if s[2] != 1:
+        _refuse(t, what, dtype, (rows, heads, dim), index)
     # a dimension of size 1 has no stride of its own
-    return t.data_ptr(), t.stride(0) if rows > 1 else 0, t.stride(1) if heads > 1 else 0
+    return t.data_ptr(), s[0] if rows > 1 else 0, s[1] if heads > 1 else 0
 
 
 class KVCache:
@@ -436,12 +451,16 @@ class KVCache:
             raise TypeError("the cache must be bf16 or fp16, got %s" % k.dtype)
         if k.stride(4) != 1 or v.stride(4) != 1 or any(a != b for a, b, n in zip(k.stride(), v.stride(), k.shape) if n > 1):
             raise ValueError("k and v must have the same strides and a contiguous head dimension")
-        _need(page_table, "page_table", torch.int32, (None, None), like=k)
-        _need(lens, "lens", torch.int32, (page_table.shape[0],), like=k)
-        _need(refs, "refs", torch.int32, (k.shape[1],), optional=True, like=k)
+        at = k.get_device()
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [max_seqs, max_pages], got %s" % (tuple(page_table.shape),))
+        _need(page_table, "page_table", torch.int32, page_table.shape, at)
+        _need(lens, "lens", torch.int32, page_table.shape[:1], at)
+        _given(refs, "refs", torch.int32, k.shape[1:2], at)
         if err is None:
             err = torch.zeros(1, dtype=torch.int32, device=k.device)
-        _need(err, "err", torch.int32, (1,), like=k)
+        _need(err, "err", torch.int32, (1,), at)
+        self.index = at
         self.k, self.v, self.page_table, self.lens, self.refs, self.err = k, v, page_table, lens, refs, err
         self.n_layers, self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self.dtype = k.dtype
@@ -474,12 +493,14 @@ class TreeBatch:
 
     def __init__(self, row_off: torch.Tensor, n_rows: int, max_nodes: int, mask: Optional[torch.Tensor] = None,
                  seq: Optional[torch.Tensor] = None):
-        _need(row_off, "row_off", torch.int32, (None,))
-        if row_off.numel() < 2:
+        if row_off.dim() != 1 or row_off.numel() < 2:
             raise ValueError("row_off needs one entry per sequence and one more")
+        at = row_off.get_device()
+        _need(row_off, "row_off", torch.int32, row_off.shape, at)
         self.n_seqs, self.n_rows, self.max_nodes = row_off.numel() - 1, int(n_rows), int(max_nodes)
-        _need(mask, "mask", torch.int64, (self.n_rows,), optional=True, like=row_off)
-        _need(seq, "seq", torch.int32, (self.n_seqs,), optional=True, like=row_off)
+        _given(mask, "mask", torch.int64, (self.n_rows,), at)
+        _given(seq, "seq", torch.int32, (self.n_seqs,), at)
+        self.index = at
         self.row_off, self.mask, self.seq = row_off, mask, seq
         self.c = CTree(self.n_seqs, self.n_rows, self.max_nodes, None if seq is None else seq.data_ptr(),
                        row_off.data_ptr(), None if mask is None else mask.data_ptr())
@@ -499,7 +520,7 @@ class Rope:
                  scale: Optional[float] = None, device="cuda"):
         if scaling not in self.KINDS:
             raise ValueError("scaling must be one of %s, got %r" % (sorted(self.KINDS), scaling))
-        self.head_dim, self.rot_dim, self.interleaved = int(head_dim), int(rot_dim or head_dim), bool(interleaved)
+        self.head_dim, self.rot_dim, self.interleaved = int(head_dim), int(rot_dim or head_dim), int(bool(interleaved))
         turns = (ctypes.c_uint64 * max(1, self.rot_dim // 2))()
         _check(_load().dfv_rope_table(self.rot_dim, float(theta), self.KINDS[scaling], float(factor), float(original),
                                       float(low), float(high), turns), "dfv_rope_table")
@@ -514,20 +535,21 @@ def rope_append(cache: KVCache, layer: int, tree: TreeBatch, rope: Rope, q: torc
                 v: torch.Tensor, positions: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rotated q (out, a new tensor or q itself), and the rows' rotated k and their v stored into the cache.
     q [rows, heads, dim], k and v [rows, kv heads, dim] may be slices of one projection."""
-    rows, H, D = tree.n_rows, q.shape[1] if q.dim() == 3 else 0, cache.head_dim
-    qp, qr, qh = _rows3(q, "q", rows, H, D, cache.dtype, cache.k)
-    kp, kr, kh = _rows3(k, "k", rows, cache.n_kv_heads, D, cache.dtype, cache.k)
-    vp, vr, vh = _rows3(v, "v", rows, cache.n_kv_heads, D, cache.dtype, cache.k)
-    _need(positions, "positions", torch.int32, (rows,), like=cache.k)
+    rows, H, K, D, dt, at = tree.n_rows, q.shape[1] if q.dim() == 3 else 0, cache.n_kv_heads, cache.head_dim, cache.dtype, cache.index
+    qp, qr, qh = _rows3(q, "q", rows, H, D, dt, at)
+    kp, kr, kh = _rows3(k, "k", rows, K, D, dt, at)
+    vp, vr, vh = _rows3(v, "v", rows, K, D, dt, at)
+    pp = _need(positions, "positions", torch.int32, (rows,), at)
     if rope.head_dim != D:
         raise ValueError("the rotary plan is for head_dim %d, the cache has %d" % (rope.head_dim, D))
     if out is None:
-        out = torch.empty(rows, H, D, dtype=q.dtype, device=q.device)
-    op, orow, oh = _rows3(out, "out", rows, H, D, cache.dtype, cache.k)
-    st = _load().dfv_rope_append(cache.ref, int(layer), tree.ref, H, rope.rot_dim, 1 if rope.interleaved else 0,
-                                 rope.scale, rope.turns.data_ptr(), qp, qr, qh, kp, kr, kh, vp, vr, vh,
-                                 positions.data_ptr(), op, orow, oh, _stream(stream))
-    _check(st, "dfv_rope_append")
+        out = torch.empty((rows, H, D), dtype=dt, device=q.device)
+    op, orow, oh = _rows3(out, "out", rows, H, D, dt, at)
+    st = _load().dfv_rope_append(cache.ref, layer, tree.ref, H, rope.rot_dim, rope.interleaved, rope.scale,
+                                 rope.turns.data_ptr(), qp, qr, qh, kp, kr, kh, vp, vr, vh, pp, op, orow, oh,
+                                 _on(stream, at))
+    if st:
+        raise DfvError(st, "dfv_rope_append")
     return out
 
 
@@ -540,16 +562,16 @@ def tree_attention(cache: KVCache, layer: int, tree: TreeBatch, q: torch.Tensor,
                    lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention of every drafted node over its sequence's committed tokens and the nodes of its mask.
     scale: 1/sqrt(head_dim) by default; lse: optional fp32 [rows, heads] that receives ln(sum exp)."""
-    rows, H, D = tree.n_rows, q.shape[1] if q.dim() == 3 else 0, cache.head_dim
-    qp, qr, qh = _rows3(q, "q", rows, H, D, cache.dtype, cache.k)
+    rows, H, D, dt, at = tree.n_rows, q.shape[1] if q.dim() == 3 else 0, cache.head_dim, cache.dtype, cache.index
+    qp, qr, qh = _rows3(q, "q", rows, H, D, dt, at)
     if out is None:
-        out = torch.empty(rows, H, D, dtype=q.dtype, device=q.device)
-    op, orow, oh = _rows3(out, "out", rows, H, D, cache.dtype, cache.k)
-    _need(lse, "lse", torch.float32, (rows, H), optional=True, like=cache.k)
-    st = _load().dfv_tree_attention(cache.ref, int(layer), tree.ref, H, D ** -0.5 if scale is None else float(scale),
-                                    qp, qr, qh, op, orow, oh, None if lse is None else lse.data_ptr(),
-                                    ws.data_ptr(), ws.numel(), _stream(stream))
-    _check(st, "dfv_tree_attention")
+        out = torch.empty((rows, H, D), dtype=dt, device=q.device)
+    op, orow, oh = _rows3(out, "out", rows, H, D, dt, at)
+    lp = _given(lse, "lse", torch.float32, (rows, H), at)
+    st = _load().dfv_tree_attention(cache.ref, layer, tree.ref, H, D ** -0.5 if scale is None else scale, qp, qr, qh,
+                                    op, orow, oh, lp, ws.data_ptr(), ws.numel(), _on(stream, at))
+    if st:
+        raise DfvError(st, "dfv_tree_attention")
     return out
 
 
@@ -561,17 +583,22 @@ class LogitRules:
 
     def __init__(self, hist=None, hist_len=None, prompt_len=None, repetition=None, frequency=None, presence=None,
                  bias=None, allowed=None):
-        _need(hist, "hist", torch.int32, (None, None), optional=True)
+        given = [t for t in (hist, hist_len, prompt_len, repetition, frequency, presence, bias, allowed) if t is not None]
+        at = given[0].get_device() if given else None
+        for name, t, dt in (("hist", hist, torch.int32), ("bias", bias, torch.float32), ("allowed", allowed, torch.int32)):
+            if t is not None and t.dim() != 2:
+                raise ValueError("%s must have two dimensions, got %s" % (name, tuple(t.shape)))
+            _given(t, name, dt, None if t is None else t.shape, at)
         if hist is not None and hist_len is None:
             raise ValueError("hist needs hist_len")
         n = None if hist is None else hist.shape[0]
         for name, t, dt in (("hist_len", hist_len, torch.int32), ("prompt_len", prompt_len, torch.int32),
                             ("repetition", repetition, torch.float32), ("frequency", frequency, torch.float32),
                             ("presence", presence, torch.float32)):
-            _need(t, name, dt, (n,), optional=True)
-            n = t.shape[0] if t is not None else n
-        _need(bias, "bias", torch.float32, (None, None), optional=True)
-        _need(allowed, "allowed", torch.int32, (None, None), optional=True)
+            if t is not None:
+                n = t.numel() if n is None else n
+                _need(t, name, dt, (n,), at)
+        self.index = at
         self.n_seqs, self.bias, self.allowed = n, bias, allowed
         self.keep = (hist, hist_len, prompt_len, repetition, frequency, presence)
         ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
@@ -593,46 +620,51 @@ def logits_process(logits: torch.Tensor, tree: TreeBatch, tokens: Optional[torch
     if logits.dim() != 2 or logits.shape[0] != tree.n_rows or logits.stride(1) != 1:
         raise ValueError("logits must be [%d, V] with contiguous rows" % tree.n_rows)
     rows, V = logits.shape
+    at, dt = tree.index, logits.dtype
+    if logits.get_device() != at or (rules.index is not None and rules.index != at):
+        raise ValueError("logits, tree and rules are not on one device")
     if rules.n_seqs is not None and rules.n_seqs != tree.n_seqs:
         raise ValueError("the rules are for %d sequences, the call has %d" % (rules.n_seqs, tree.n_seqs))
     if rules.bias is not None and (rules.bias.shape[1] != V or rules.bias.shape[0] not in (1, tree.n_seqs)):
         raise ValueError("bias must be [1 or %d, %d]" % (tree.n_seqs, V))
     if rules.allowed is not None and (rules.allowed.shape[1] != (V + 31) // 32 or rules.allowed.shape[0] not in (1, rows)):
         raise ValueError("allowed must be [1 or %d, %d]" % (rows, (V + 31) // 32))
-    _need(tokens, "tokens", torch.int32, (rows,), optional=True, like=logits)
+    tp = _given(tokens, "tokens", torch.int32, (rows,), at)
+    op = orow = 0
     if not store:
         if out is not None:
             raise ValueError("store=False takes no out")
-    elif out is None:
-        out = torch.empty(rows, V, dtype=logits.dtype, device=logits.device)
-    elif out.shape != logits.shape or out.dtype != logits.dtype or out.stride(1) != 1:
-        raise ValueError("out must be like logits")
+    else:
+        if out is None:
+            out = torch.empty((rows, V), dtype=dt, device=logits.device)
+        elif out.shape != logits.shape or out.dtype is not dt or out.stride(1) != 1 or out.get_device() != at:
+            raise ValueError("out must be like logits")
+        op, orow = out.data_ptr(), out.stride(0) if rows > 1 else V
     if argmax is None:
-        argmax = torch.empty(rows, dtype=torch.int32, device=logits.device)
-    _need(argmax, "argmax", torch.int32, (rows,), like=logits)
+        argmax = torch.empty((rows,), dtype=torch.int32, device=logits.device)
+    ap = _need(argmax, "argmax", torch.int32, (rows,), at)
     st = _load().dfv_logits_process(logits.data_ptr(), logits.stride(0) if rows > 1 else V, _act(logits), V, tree.ref,
-                                    None if tokens is None else tokens.data_ptr(), rules.ref,
-                                    None if out is None else out.data_ptr(),
-                                    0 if out is None else out.stride(0) if rows > 1 else V, argmax.data_ptr(),
-                                    ws.data_ptr(), ws.numel(), _stream(stream))
-    _check(st, "dfv_logits_process")
+                                    tp, rules.ref, op or None, orow, ap, ws.data_ptr(), ws.numel(), _on(stream, at))
+    if st:
+        raise DfvError(st, "dfv_logits_process")
     return out, argmax
 
 
 def accept_tree(tree: TreeBatch, tokens: torch.Tensor, target: torch.Tensor, path: Optional[torch.Tensor] = None,
                 tau: Optional[torch.Tensor] = None, stream=None):
     """(path [n_seqs, max_nodes], tau [n_seqs]): the accepted nodes of each tree, root first, then -1."""
-    _need(tokens, "tokens", torch.int32, (tree.n_rows,), like=tree.row_off)
-    _need(target, "target", torch.int32, (tree.n_rows,), like=tree.row_off)
+    at = tree.index
+    tp = _need(tokens, "tokens", torch.int32, (tree.n_rows,), at)
+    gp = _need(target, "target", torch.int32, (tree.n_rows,), at)
     if path is None:
-        path = torch.empty(tree.n_seqs, tree.max_nodes, dtype=torch.int32, device=tokens.device)
+        path = torch.empty((tree.n_seqs, tree.max_nodes), dtype=torch.int32, device=tokens.device)
     if tau is None:
-        tau = torch.empty(tree.n_seqs, dtype=torch.int32, device=tokens.device)
-    _need(path, "path", torch.int32, (tree.n_seqs, None), like=tokens)
-    _need(tau, "tau", torch.int32, (tree.n_seqs,), like=tokens)
-    st = _load().dfv_accept_tree(tree.ref, tokens.data_ptr(), target.data_ptr(), path.data_ptr(), path.shape[1],
-                                 tau.data_ptr(), _stream(stream))
-    _check(st, "dfv_accept_tree")
+        tau = torch.empty((tree.n_seqs,), dtype=torch.int32, device=tokens.device)
+    width = path.shape[-1]
+    st = _load().dfv_accept_tree(tree.ref, tp, gp, _need(path, "path", torch.int32, (tree.n_seqs, width), at), width,
+                                 _need(tau, "tau", torch.int32, (tree.n_seqs,), at), _on(stream, at))
+    if st:
+        raise DfvError(st, "dfv_accept_tree")
     return path, tau
 
 
@@ -644,41 +676,43 @@ def cache_commit(cache: KVCache, tree: TreeBatch, path: torch.Tensor, tau: torch
                  new_lens: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Moves the accepted rows together in every layer and adds tau to the lengths (cache.lens unless new_lens is
     given); returns the lengths."""
-    _need(path, "path", torch.int32, (tree.n_seqs, None), like=cache.k)
-    _need(tau, "tau", torch.int32, (tree.n_seqs,), like=cache.k)
+    at = cache.index
+    width = path.shape[-1]
+    pp = _need(path, "path", torch.int32, (tree.n_seqs, width), at)
+    tp = _need(tau, "tau", torch.int32, (tree.n_seqs,), at)
     if new_lens is None:
         new_lens = cache.lens
-    _need(new_lens, "new_lens", torch.int32, tuple(cache.lens.shape), like=cache.k)
-    st = _load().dfv_cache_commit(cache.ref, tree.ref, path.data_ptr(), path.shape[1], tau.data_ptr(),
-                                  new_lens.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
-    _check(st, "dfv_cache_commit")
+    st = _load().dfv_cache_commit(cache.ref, tree.ref, pp, width, tp,
+                                  _need(new_lens, "new_lens", torch.int32, cache.lens.shape, at), ws.data_ptr(),
+                                  ws.numel(), _on(stream, at))
+    if st:
+        raise DfvError(st, "dfv_cache_commit")
     return new_lens
 
 
 def _index(t: torch.Tensor, what: str, cache: KVCache, n: Optional[int] = None):
-    _need(t, what, torch.int32, (n,), like=cache.k)
-    return t.data_ptr()
+    return _need(t, what, torch.int32, (t.numel() if n is None else n,), cache.index)
 
 
 def cache_copy_pages(cache: KVCache, src: torch.Tensor, dst: torch.Tensor, stream=None):
     """Page dst[i] <- page src[i] in every layer."""
     _check(_load().dfv_cache_copy_pages(cache.ref, _index(src, "src", cache), _index(dst, "dst", cache, src.shape[0]),
-                                        src.shape[0], _stream(stream)), "dfv_cache_copy_pages")
+                                        src.shape[0], _on(stream, cache.index)), "dfv_cache_copy_pages")
 
 
 def pages_reserve(cache: KVCache, seqs: torch.Tensor, n_new: torch.Tensor, ws: torch.Tensor, stream=None):
     """Pages for n_new[i] tokens after those of sequence seqs[i]."""
     _check(_load().dfv_pages_reserve(cache.ref, _index(seqs, "seqs", cache), _index(n_new, "n_new", cache, seqs.shape[0]),
-                                     seqs.shape[0], ws.data_ptr(), ws.numel(), _stream(stream)), "dfv_pages_reserve")
+                                     seqs.shape[0], ws.data_ptr(), ws.numel(), _on(stream, cache.index)), "dfv_pages_reserve")
 
 
 def pages_fork(cache: KVCache, src: torch.Tensor, dst: torch.Tensor, ws: torch.Tensor, stream=None):
     """Sequence dst[i], which holds nothing, becomes a copy of src[i]."""
     _check(_load().dfv_pages_fork(cache.ref, _index(src, "src", cache), _index(dst, "dst", cache, src.shape[0]),
-                                  src.shape[0], ws.data_ptr(), ws.numel(), _stream(stream)), "dfv_pages_fork")
+                                  src.shape[0], ws.data_ptr(), ws.numel(), _on(stream, cache.index)), "dfv_pages_fork")
 
 
 def pages_free(cache: KVCache, seqs: torch.Tensor, stream=None):
     """Drops sequences: their pages lose a holder, their lengths become 0."""
-    _check(_load().dfv_pages_free(cache.ref, _index(seqs, "seqs", cache), seqs.shape[0], _stream(stream)),
+    _check(_load().dfv_pages_free(cache.ref, _index(seqs, "seqs", cache), seqs.shape[0], _on(stream, cache.index)),
            "dfv_pages_free")
