@@ -1,137 +1,376 @@
 // logits.cu -- penalties for repeated tokens, biases and grammar masks on the
 // logits of drafted nodes, with the argmax of each row in the same pass.
 //
-// A row's counts are those of its sequence's history plus the drafted tokens on
-// the row's own path.  A CTA owns one vocabulary slice of one sequence: it
-// counts the history's tokens of that slice in shared memory once (integer
-// atomics: the order does not matter), and then takes rows of the sequence one
-// after the other, adding the row's path tokens before and removing them after.
+// Bound by memory: every logit is read and written once.  A CTA owns a slice of
+// kSlice vocabulary columns of one sequence, eight columns per thread, and
+// walks rows of the sequence: the thread's bias and its knowledge of which
+// columns repeat stay in registers over the rows, several rows' loads are in
+// flight at once, and no barrier separates rows.
+//
+// The columns that penalties can touch are few (the history and the tree's
+// tokens).  The CTA counts the history's tokens of its slice in shared memory
+// (integer atomics: their order does not matter) and lists the columns met.  The
+// dense walk leaves those columns' logits as they are and out of the argmax;
+// afterwards a warp per row applies all steps to the listed columns, where the
+// row's own path adds to the counts.  (Applying the steps in the dense walk took
+// twice the instructions: some lane of a warp nearly always meets a token.)
 #include "tree_common.cuh"
 
 namespace dfv {
 namespace {
 
 constexpr int kLogitThreads = 512;
-constexpr uint32_t kSeenBit = 0x80000000u;  // the token is in the prompt; low bits count generated ones
+constexpr int kCols = 8;                              // columns of a thread
+constexpr int kSlice = kLogitThreads * kCols;
+constexpr int kAhead = 4;                             // listed columns of a lane in flight
+constexpr uint32_t kPromptBit = 0x80000000u;          // the token is in the prompt
+constexpr uint32_t kTreeBit = 0x40000000u;            // some drafted node holds the token
+constexpr uint32_t kCountMask = kTreeBit - 1u;        // how often it was generated
 
-struct RowRules {
-  float rep, freq, pres;
-  bool pen;
-};
-
-// Steps 1-5 of dfv_logits_process, every product, quotient and difference
-// rounded on its own (no contraction).
-__device__ __forceinline__ float rule(float x, uint32_t cnt, const RowRules &r, const LogitsParams &p, float bias,
-                                      bool allowed) {
-  if (r.pen) {
-    const uint32_t c = cnt & ~kSeenBit;
-    if (p.r.repetition && cnt) x = x > 0.f ? __fdiv_rn(x, r.rep) : __fmul_rn(x, r.rep);
-    if (p.r.frequency) x = __fsub_rn(x, __fmul_rn(r.freq, (float)c));
-    if (p.r.presence && c) x = __fsub_rn(x, r.pres);
-  }
-  if (p.r.bias) x = __fadd_rn(x, bias);
-  return allowed ? x : -INFINITY;
+// Eight columns of a row: consecutive ones of a 16-byte aligned row (VEC), or
+// one in kLogitThreads each, so that a warp's 2- or 4-byte accesses are
+// consecutive whatever the row's alignment.
+template <bool VEC>
+__device__ __forceinline__ int column(int j) {
+  return VEC ? (int)threadIdx.x * kCols + j : (int)threadIdx.x + j * kLogitThreads;
 }
 
+// A row's columns of the thread, as loaded: packed pairs of bf16, or fp32.  Masks
+// over them have all bits of a column set or none.
 template <bool F32>
-__global__ void __launch_bounds__(kLogitThreads) logits_kernel(const LogitsParams p) {
-  extern __shared__ uint32_t s_cnt[];
-  __shared__ unsigned long long s_w[kLogitThreads / 32];
+struct Raw {
+  static constexpr int kWords = F32 ? kCols : kCols / 2;
+  static constexpr uint32_t kNegInf = F32 ? 0xff800000u : 0xff80ff80u;
+  uint32_t w[kWords];
+  __device__ __forceinline__ float at(int j) const {
+    if (F32) return __uint_as_float(w[j % kWords]);
+    return j & 1 ? bf16_hi(w[j / 2 % kWords]) : bf16_lo(w[j / 2 % kWords]);
+  }
+  __device__ __forceinline__ float largest() const {
+    if (F32) {
+      float m = at(0);
+#pragma unroll
+      for (int j = 1; j < kCols; ++j) m = fmaxf(m, at(j));
+      return m;
+    }
+    __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162 *>(&w[0]);
+#pragma unroll
+    for (int q = 1; q < kWords; ++q) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162 *>(&w[q]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+};
+
+// Bit j of `bits` as a mask over column j.
+template <bool F32>
+__device__ __forceinline__ void spread(uint32_t bits, uint32_t (&m)[Raw<F32>::kWords]) {
+  if (F32) {
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) m[j % Raw<F32>::kWords] = (uint32_t)((int)(bits << (31 - j)) >> 31);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // four bits to the top bits of four bytes, then each byte's sign twice
+      const uint32_t t = ((bits >> (4 * h) & 0xfu) * 0x10204080u) & 0x80808080u;
+      asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(m[2 * h % Raw<F32>::kWords]) : "r"(t));
+      asm("prmt.b32 %0, %1, 0, 0xbbaa;" : "=r"(m[(2 * h + 1) % Raw<F32>::kWords]) : "r"(t));
+    }
+  }
+}
+
+template <bool F32, bool VEC>
+__device__ __forceinline__ void load_row(const char *row, int left, Raw<F32> &x) {
+  constexpr int kBytes = F32 ? 4 : 2;
+  if (VEC) {
+    if (column<VEC>(0) < left) {  // left is a multiple of kCols
+#pragma unroll
+      for (int q = 0; q < Raw<F32>::kWords; q += 4) {
+        const uint4 a = ldg_stream(row + kBytes * column<VEC>(0) + 4 * q);
+        x.w[q] = a.x; x.w[q + 1] = a.y; x.w[q + 2] = a.z; x.w[q + 3] = a.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      const int c = column<VEC>(j);
+      if (c < left) {
+        if (F32)
+          x.w[j % Raw<F32>::kWords] = reinterpret_cast<const uint32_t *>(row)[c];
+        else {
+          const uint32_t v = reinterpret_cast<const uint16_t *>(row)[c];
+          x.w[j / 2 % Raw<F32>::kWords] = j & 1 ? (x.w[j / 2 % Raw<F32>::kWords] & 0xffffu) | v << 16 : v;
+        }
+      }
+    }
+  }
+}
+
+template <bool F32, bool VEC>
+__device__ __forceinline__ void store_row(char *row, int left, const Raw<F32> &x) {
+  constexpr int kBytes = F32 ? 4 : 2;
+  if (VEC) {
+    if (column<VEC>(0) < left) {
+#pragma unroll
+      for (int q = 0; q < Raw<F32>::kWords; q += 4)
+        *reinterpret_cast<uint4 *>(row + kBytes * column<VEC>(0) + 4 * q) =
+            make_uint4(x.w[q], x.w[q + 1], x.w[q + 2], x.w[q + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      const int c = column<VEC>(j);
+      if (c < left) {
+        if (F32)
+          reinterpret_cast<uint32_t *>(row)[c] = x.w[j % Raw<F32>::kWords];
+        else
+          reinterpret_cast<uint16_t *>(row)[c] = (uint16_t)(x.w[j / 2 % Raw<F32>::kWords] >> (j & 1 ? 16 : 0));
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float round_bf16(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+
+// The largest of a warp's values (the lowest column among equals) into *key;
+// col() is only asked of lanes that hold it.  A lane without a value above -inf
+// passes best = -inf.
+template <class Col>
+__device__ __forceinline__ void warp_argmax(unsigned long long *key, float best, Col col) {
+  const uint32_t k = best == -INFINITY ? 0u : float_key(best);
+  const uint32_t m = __reduce_max_sync(0xffffffffu, k);
+  if (m == 0u) return;
+  uint32_t c = 0xffffffffu;
+  if (k == m) c = (uint32_t)col();
+  c = __reduce_min_sync(0xffffffffu, c);
+  if ((threadIdx.x & 31) == 0) atomicMax(key, ((unsigned long long)m << 32) | (0xffffffffu - c));
+}
+
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsParams p) {
+  __shared__ __align__(16) uint32_t s_cnt[kSlice];
+  __shared__ uint16_t s_list[kSlice];
+  __shared__ unsigned long long s_key[DFV_MAX_TREE];
+  __shared__ int s_tok[DFV_MAX_TREE];
+  __shared__ int s_n;
   pdl_trigger();
   pdl_wait();
-  const int tid = threadIdx.x, b = blockIdx.y;
-  const int v0 = blockIdx.x * p.slice, v1 = min(p.V, v0 + p.slice);
-  int r0 = p.t.row_off[b], r1 = p.t.row_off[b + 1];
-  if (r0 < 0 || r1 > p.t.n_rows || r1 - r0 > p.t.max_nodes) return;
-  const int n = r1 - r0;
-  if (n <= 0) return;
-  RowRules rr = {};
-  rr.pen = p.r.repetition || p.r.frequency || p.r.presence;
-  if (rr.pen) {
-    if (p.r.repetition) rr.rep = p.r.repetition[b];
-    if (p.r.frequency) rr.freq = p.r.frequency[b];
-    if (p.r.presence) rr.pres = p.r.presence[b];
-    for (int i = tid; i < v1 - v0; i += kLogitThreads) s_cnt[i] = 0u;
+  const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.y;
+  const int v0 = blockIdx.x * kSlice, left = min(kSlice, p.V - v0);  // columns of the slice
+  const int r0 = p.t.row_off[b], r1 = p.t.row_off[b + 1], n = r1 - r0;
+  if (r0 < 0 || r1 > p.t.n_rows || n > p.t.max_nodes || n <= (int)blockIdx.z) return;
+  const bool pen = p.r.repetition || p.r.frequency || p.r.presence;
+  const float *bias = p.r.bias ? p.r.bias + b * p.r.bias_row + v0 : nullptr;
+  constexpr int kBytes = F32 ? 4 : 2;
+  constexpr int kRowsAhead = F32 ? 2 : 4;  // rows whose logits are in flight
+  if (tid < DFV_MAX_TREE) s_key[tid] = 0ull;
+
+  // ---- the thread's columns
+  float bv[kCols];
+  uint32_t listed = 0u;  // bit j: penalties may touch column j
+#pragma unroll
+  for (int j = 0; j < kCols; ++j) bv[j] = bias && column<VEC>(j) < left ? bias[column<VEC>(j)] : 0.f;
+  if (pen) {
+    for (int i = tid; i < kSlice / 4; i += kLogitThreads) reinterpret_cast<uint4 *>(s_cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0) s_n = 0;
+    if (tid < n) s_tok[tid] = p.tokens[r0 + tid] - v0;
     __syncthreads();
     if (p.r.hist) {
       const int32_t *h = p.r.hist + b * p.r.hist_row;
-      const int L = (int)min((long long)p.r.hist_len[b], (long long)p.r.hist_row), P = p.r.prompt_len ? p.r.prompt_len[b] : 0;
-      for (int i = tid; i < L; i += kLogitThreads) {
+      const int len = (int)min((long long)p.r.hist_len[b], (long long)p.r.hist_row);
+      const int prompt = p.r.prompt_len ? p.r.prompt_len[b] : 0;
+#pragma unroll 4
+      for (int i = tid; i < len; i += kLogitThreads) {
         const unsigned c = (unsigned)h[i] - (unsigned)v0;
-        if (c < (unsigned)(v1 - v0)) {
-          if (i < P)
-            atomicOr(&s_cnt[c], kSeenBit);
+        if (c < (unsigned)left) {
+          if (i < prompt)
+            atomicOr(&s_cnt[c], kPromptBit);
           else
             atomicAdd(&s_cnt[c], 1u);
         }
       }
     }
+    if (tid < n && (unsigned)s_tok[tid] < (unsigned)left) atomicOr(&s_cnt[s_tok[tid]], kTreeBit);
     __syncthreads();
-  }
-  for (int i = blockIdx.z; i < n; i += gridDim.z) {
-    const int row = r0 + i;
-    unsigned mine = 0xffffffffu;  // slice column of the path token this thread adds
-    if (rr.pen && p.tokens) {
-      if (tid < n && ((row_mask(p.t, r0, i) >> tid) & 1)) mine = (unsigned)p.tokens[r0 + tid] - (unsigned)v0;
-      if (mine < (unsigned)(v1 - v0))
-        atomicAdd(&s_cnt[mine], 1u);
-      else
-        mine = 0xffffffffu;
-      __syncthreads();
-    }
-    const float *bias = p.r.bias ? p.r.bias + b * p.r.bias_row : nullptr;
-    const uint32_t *ok = p.r.allowed ? p.r.allowed + row * p.r.allowed_row : nullptr;
-    unsigned long long best = 0ull;
-    for (int v = v0 + tid; v < v1; v += kLogitThreads) {
-      float x = F32 ? reinterpret_cast<const float *>(p.x)[row * p.row + v]
-                    : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(p.x)[row * p.row + v] << 16);
-      x = rule(x, rr.pen ? s_cnt[v - v0] : 0u, rr, p, bias ? bias[v] : 0.f,
-               !ok || ((ok[v >> 5] >> (v & 31)) & 1u));
-      if (!F32) {
-        const uint16_t y = f32_to_bf16_bits(x);
-        x = __uint_as_float((uint32_t)y << 16);
-        if (p.out) reinterpret_cast<uint16_t *>(p.out)[row * p.out_row + v] = y;
-      } else if (p.out) {
-        reinterpret_cast<float *>(p.out)[row * p.out_row + v] = x;
-      }
-      const unsigned long long key =
-          ((unsigned long long)float_key(x) << 32) | (unsigned long long)(0xffffffffu - (unsigned)v);
-      best = key > best ? key : best;
-    }
-    if (p.argmax) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const unsigned long long w = __shfl_xor_sync(0xffffffffu, best, o);
-        best = w > best ? w : best;
-      }
-      if ((tid & 31) == 0) s_w[tid >> 5] = best;
-      __syncthreads();
-      if (tid == 0) {
-        for (int w = 1; w < kLogitThreads / 32; ++w) best = s_w[w] > best ? s_w[w] : best;
-        atomicMax(&p.key[row], best);
-        __threadfence();
-        if (atomicAdd(&p.ticket[row], 1u) == gridDim.x - 1) {
-          __threadfence();
-          const unsigned long long k = atomicExch(&p.key[row], 0ull);
-          p.argmax[row] = (int32_t)(0xffffffffu - (unsigned)(k & 0xffffffffull));
-          p.ticket[row] = 0u;
+    for (int j = 0; j < kCols; ++j)
+      if (s_cnt[column<VEC>(j)]) listed |= 1u << j;
+    int at = 0;
+    const int mine = __popc(listed);
+    int run = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += a;
+    }
+    if (lane == 31) at = atomicAdd(&s_n, run);
+    at = __shfl_sync(0xffffffffu, at, 31) + run - mine;
+#pragma unroll
+    for (int j = 0; j < kCols; ++j)
+      if (listed >> j & 1u) s_list[at++] = (uint16_t)column<VEC>(j);
+  }
+  __syncthreads();
+
+  // ---- all rows, dense: bias and mask
+  uint32_t keep[Raw<F32>::kWords], inside = 0u;
+  spread<F32>(listed, keep);
+#pragma unroll
+  for (int j = 0; j < kCols; ++j) inside |= (column<VEC>(j) < left ? 1u : 0u) << j;
+  for (int i0 = blockIdx.z; i0 < n; i0 += kRowsAhead * gridDim.z) {
+    Raw<F32> x[kRowsAhead];
+    uint32_t ok[kRowsAhead];
+#pragma unroll
+    for (int q = 0; q < kRowsAhead; ++q) {
+      const int i = i0 + q * gridDim.z;
+      ok[q] = inside;  // past the slice's end nothing is loaded and nothing may win
+      if (i >= n) continue;
+      load_row<F32, VEC>(p.x + kBytes * ((r0 + i) * p.row + v0), left, x[q]);
+      if (p.r.allowed) {
+        const uint32_t *words = p.r.allowed + (r0 + i) * p.r.allowed_row + v0 / 32;
+        if (VEC) {
+          if (inside) ok[q] &= __ldg(reinterpret_cast<const uint8_t *>(words) + tid);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j)
+            if (column<VEC>(j) < left && !(__ldg(words + (column<VEC>(j) >> 5)) >> (column<VEC>(j) & 31) & 1u))
+              ok[q] &= ~(1u << j);
         }
       }
     }
-    __syncthreads();  // the counts and s_w are read
-    if (mine != 0xffffffffu) atomicSub(&s_cnt[mine], 1u);
+#pragma unroll
+    for (int q = 0; q < kRowsAhead; ++q) {
+      const int i = i0 + q * gridDim.z;
+      if (i >= n) break;
+      if (bias) {
+        Raw<F32> y;
+#pragma unroll
+        for (int j = 0; j < Raw<F32>::kWords; ++j) {
+          if (F32)
+            y.w[j] = __float_as_uint(__fadd_rn(x[q].at(j), bv[j]));
+          else
+            y.w[j] = pack2<false>(__fadd_rn(x[q].at(2 * j), bv[2 * j % kCols]),
+                                  __fadd_rn(x[q].at(2 * j + 1), bv[(2 * j + 1) % kCols]));
+          x[q].w[j] = (x[q].w[j] & keep[j]) | (y.w[j] & ~keep[j]);
+        }
+      }
+      // not allowed: -inf; listed: stored as they came, out of the argmax
+      uint32_t okm[Raw<F32>::kWords];
+      spread<F32>(ok[q], okm);
+      Raw<F32> y;
+#pragma unroll
+      for (int j = 0; j < Raw<F32>::kWords; ++j) {
+        const uint32_t may = okm[j] & ~keep[j];
+        y.w[j] = (x[q].w[j] & may) | (Raw<F32>::kNegInf & ~may);
+        x[q].w[j] = (y.w[j] & ~keep[j]) | (x[q].w[j] & keep[j]);
+      }
+      if (p.out) store_row<F32, VEC>(p.out + kBytes * ((r0 + i) * p.out_row + v0), left, x[q]);
+      if (p.argmax) {
+        const float best = y.largest();
+        warp_argmax(&s_key[i], best, [&]() {
+          int bj = 0;
+#pragma unroll
+          for (int j = kCols - 1; j >= 0; --j)
+            if (y.at(j) == best) bj = j;
+          return v0 + column<VEC>(bj);
+        });
+      }
+    }
+  }
+
+  // ---- the listed columns, a warp per row: every step
+  if (pen) {
+    __syncthreads();  // the dense walk's stores come first
+    const int m = s_n;
+    const float rep = p.r.repetition ? p.r.repetition[b] : 1.f, freq = p.r.frequency ? p.r.frequency[b] : 0.f,
+                pres = p.r.presence ? p.r.presence[b] : 0.f;
+    for (int i = blockIdx.z + (tid >> 5) * gridDim.z; i < n; i += (kLogitThreads / 32) * gridDim.z) {
+      const uint64_t mask = row_mask(p.t, r0, i);
+      const char *from = p.x + kBytes * ((r0 + i) * p.row + v0);
+      char *to = p.out + kBytes * ((r0 + i) * p.out_row + v0);
+      const uint32_t *words = p.r.allowed ? p.r.allowed + (r0 + i) * p.r.allowed_row : nullptr;
+      float best = -INFINITY;
+      int bc = 0x7fffffff;
+      for (int k0 = 0; k0 < m; k0 += 32 * kAhead) {
+        int c[kAhead];
+        float x[kAhead], add[kAhead];
+        uint32_t ok[kAhead];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+          const int k = k0 + 32 * q + lane;
+          c[q] = k < m ? (int)s_list[k] : -1;
+          if (c[q] >= 0) {
+            x[q] = F32 ? *reinterpret_cast<const float *>(from + 4 * c[q])
+                       : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(from + 2 * c[q]) << 16);
+            add[q] = bias ? bias[c[q]] : 0.f;
+            ok[q] = words ? words[(v0 + c[q]) >> 5] >> ((v0 + c[q]) & 31) & 1u : 1u;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+          if (c[q] < 0) continue;
+          const uint32_t w = s_cnt[c[q]];
+          uint32_t cnt = w & kCountMask;
+          if (w & kTreeBit)
+            for (int j = 0; j < n; ++j) cnt += s_tok[j] == c[q] && (mask >> j & 1);
+          // steps 1-5 of dfv_logits_process, every product, quotient and
+          // difference rounded on its own (no contraction)
+          float y = x[q];
+          if (p.r.repetition && (cnt || (w & kPromptBit))) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
+          if (p.r.frequency) y = __fsub_rn(y, __fmul_rn(freq, (float)cnt));
+          if (p.r.presence && cnt) y = __fsub_rn(y, pres);
+          if (bias) y = __fadd_rn(y, add[q]);
+          if (!ok[q]) y = -INFINITY;
+          if (!F32) y = round_bf16(y);
+          if (p.out) {
+            if (F32)
+              *reinterpret_cast<float *>(to + 4 * c[q]) = y;
+            else
+              *reinterpret_cast<uint16_t *>(to + 2 * c[q]) = f32_to_bf16_bits(y);
+          }
+          if (y > best || (y == best && c[q] < bc)) {  // the list is in no order
+            best = y;
+            bc = c[q];
+          }
+        }
+      }
+      if (p.argmax) warp_argmax(&s_key[i], best, [&]() { return v0 + bc; });
+    }
+  }
+
+  // ---- join the slices of each row: the last one to arrive writes the token
+  if (!p.argmax) return;
+  __syncthreads();
+  const int i = blockIdx.z + tid * gridDim.z;
+  if (tid < DFV_MAX_TREE && i < n) {
+    const int row = r0 + i;
+    unsigned long long k = s_key[i];
+    if (gridDim.x > 1) {
+      if (k) atomicMax(&p.key[row], k);
+      __threadfence();
+      if (atomicAdd(&p.ticket[row], 1u) != gridDim.x - 1) return;
+      __threadfence();
+      k = atomicExch(&p.key[row], 0ull);
+      p.ticket[row] = 0u;
+    }
+    p.argmax[row] = k ? (int32_t)(0xffffffffu - (unsigned)(k & 0xffffffffull)) : 0;  // nothing above -inf: column 0
   }
 }
 
 }  // namespace
 
-cudaError_t launch_logits(const LogitsParams &p0, cudaStream_t s) {
-  LogitsParams p = p0;
-  p.slice = 4096;
-  const dim3 grid((p.V + p.slice - 1) / p.slice, p.t.n_seqs, 1);
-  const size_t smem = (size_t)p.slice * 4;
-  return p.f32 ? launch_chained(logits_kernel<true>, grid, dim3(kLogitThreads), smem, s, p)
-               : launch_chained(logits_kernel<false>, grid, dim3(kLogitThreads), smem, s, p);
+cudaError_t launch_logits(const LogitsParams &p, cudaStream_t s) {
+  const int slices = (p.V + kSlice - 1) / kSlice;
+  // rows of a sequence share a CTA's counts; they are spread over more CTAs only
+  // while those would not give every SM three
+  int z = (456 + slices * p.t.n_seqs - 1) / (slices * p.t.n_seqs);
+  z = z < 1 ? 1 : z > p.t.max_nodes ? p.t.max_nodes : z;
+  const dim3 grid(slices, p.t.n_seqs, z);
+  const int esz = p.f32 ? 4 : 2;
+  const bool vec = p.V % kCols == 0 && ((uintptr_t)p.x | (uintptr_t)p.out) % 16 == 0 && p.row * esz % 16 == 0 &&
+                   (!p.out || p.out_row * esz % 16 == 0);
+  if (p.f32)
+    return vec ? launch_chained(logits_kernel<true, true>, grid, dim3(kLogitThreads), 0, s, p)
+               : launch_chained(logits_kernel<true, false>, grid, dim3(kLogitThreads), 0, s, p);
+  return vec ? launch_chained(logits_kernel<false, true>, grid, dim3(kLogitThreads), 0, s, p)
+             : launch_chained(logits_kernel<false, false>, grid, dim3(kLogitThreads), 0, s, p);
 }
 
 }  // namespace dfv

@@ -54,7 +54,7 @@ struct LogitsParams {
   const char *x;
   char *out;
   long long row, out_row;
-  int V, f32, slice;
+  int V, f32;
   const int32_t *tokens;
   int32_t *argmax;
   unsigned long long *key;  // [n_rows] running maximum of each row, zero between calls
