@@ -11,8 +11,8 @@
 // tokens).  The CTA counts the history's tokens of its slice in shared memory
 // (integer atomics: their order does not matter) and lists the columns met.  The
 // dense walk leaves those columns' logits as they are and out of the argmax;
-// afterwards a warp per row applies all steps to the listed columns, where the
-// row's own path adds to the counts.  (Applying the steps in the dense walk took
+// afterwards warps apply all steps to the listed columns, where the row's own
+// path adds to the counts.  (Applying the steps in the dense walk took
 // twice the instructions: some lane of a warp nearly always meets a token.)
 #include "tree_common.cuh"
 
@@ -163,6 +163,32 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   constexpr int kRowsAhead = F32 ? 2 : 4;  // rows whose logits are in flight
   if (tid < DFV_MAX_TREE) s_key[tid] = 0ull;
 
+  // rows i0, i0 + gridDim.z, ... of the sequence, and their masks: the first ones
+  // are on their way while the history is counted
+  uint32_t inside = 0u;
+#pragma unroll
+  for (int j = 0; j < kCols; ++j) inside |= (column<VEC>(j) < left ? 1u : 0u) << j;
+  Raw<F32> x[kRowsAhead];
+  uint32_t ok[kRowsAhead];
+  auto fetch = [&](int q, int i) {
+    ok[q] = inside;  // past the slice's end nothing is loaded and nothing may win
+    if (i >= n) return;
+    load_row<F32, VEC>(p.x + kBytes * ((r0 + i) * p.row + v0), left, x[q]);
+    if (p.r.allowed) {
+      const uint32_t *words = p.r.allowed + (r0 + i) * p.r.allowed_row + v0 / 32;
+      if (VEC) {
+        if (inside) ok[q] &= __ldg(reinterpret_cast<const uint8_t *>(words) + tid);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+          if (column<VEC>(j) < left && !(__ldg(words + (column<VEC>(j) >> 5)) >> (column<VEC>(j) & 31) & 1u))
+            ok[q] &= ~(1u << j);
+      }
+    }
+  };
+#pragma unroll
+  for (int q = 0; q < kRowsAhead; ++q) fetch(q, blockIdx.z + q * gridDim.z);
+
   // ---- the thread's columns
   float bv[kCols];
   uint32_t listed = 0u;  // bit j: penalties may touch column j
@@ -177,16 +203,29 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
       const int32_t *h = p.r.hist + b * p.r.hist_row;
       const int len = (int)min((long long)p.r.hist_len[b], (long long)p.r.hist_row);
       const int prompt = p.r.prompt_len ? p.r.prompt_len[b] : 0;
-#pragma unroll 4
-      for (int i = tid; i < len; i += kLogitThreads) {
-        const unsigned c = (unsigned)h[i] - (unsigned)v0;
+      auto count = [&](int token, int i) {
+        const unsigned c = (unsigned)token - (unsigned)v0;
         if (c < (unsigned)left) {
           if (i < prompt)
             atomicOr(&s_cnt[c], kPromptBit);
           else
             atomicAdd(&s_cnt[c], 1u);
         }
+      };
+      // four tokens a load from the first 16-byte boundary on
+      const int head = min(max(len, 0), (int)((16u - ((uint32_t)(uintptr_t)h & 15u)) & 15u) / 4), quads = max(len - head, 0) / 4;
+      const int4 *h4 = reinterpret_cast<const int4 *>(h + head);
+#pragma unroll 2
+      for (int i = tid; i < quads; i += kLogitThreads) {
+        const int4 t = __ldg(h4 + i);
+        count(t.x, head + 4 * i);
+        count(t.y, head + 4 * i + 1);
+        count(t.z, head + 4 * i + 2);
+        count(t.w, head + 4 * i + 3);
       }
+      const int rest = head + 4 * quads;
+      if (tid < head) count(h[tid], tid);
+      if (tid >= 32 && tid - 32 < len - rest) count(h[rest + tid - 32], rest + tid - 32);
     }
     if (tid < n && (unsigned)s_tok[tid] < (unsigned)left) atomicOr(&s_cnt[s_tok[tid]], kTreeBit);
     __syncthreads();
@@ -210,31 +249,9 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   __syncthreads();
 
   // ---- all rows, dense: bias and mask
-  uint32_t keep[Raw<F32>::kWords], inside = 0u;
+  uint32_t keep[Raw<F32>::kWords];
   spread<F32>(listed, keep);
-#pragma unroll
-  for (int j = 0; j < kCols; ++j) inside |= (column<VEC>(j) < left ? 1u : 0u) << j;
   for (int i0 = blockIdx.z; i0 < n; i0 += kRowsAhead * gridDim.z) {
-    Raw<F32> x[kRowsAhead];
-    uint32_t ok[kRowsAhead];
-#pragma unroll
-    for (int q = 0; q < kRowsAhead; ++q) {
-      const int i = i0 + q * gridDim.z;
-      ok[q] = inside;  // past the slice's end nothing is loaded and nothing may win
-      if (i >= n) continue;
-      load_row<F32, VEC>(p.x + kBytes * ((r0 + i) * p.row + v0), left, x[q]);
-      if (p.r.allowed) {
-        const uint32_t *words = p.r.allowed + (r0 + i) * p.r.allowed_row + v0 / 32;
-        if (VEC) {
-          if (inside) ok[q] &= __ldg(reinterpret_cast<const uint8_t *>(words) + tid);
-        } else {
-#pragma unroll
-          for (int j = 0; j < kCols; ++j)
-            if (column<VEC>(j) < left && !(__ldg(words + (column<VEC>(j) >> 5)) >> (column<VEC>(j) & 31) & 1u))
-              ok[q] &= ~(1u << j);
-        }
-      }
-    }
 #pragma unroll
     for (int q = 0; q < kRowsAhead; ++q) {
       const int i = i0 + q * gridDim.z;
@@ -262,6 +279,7 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
         x[q].w[j] = (y.w[j] & ~keep[j]) | (x[q].w[j] & keep[j]);
       }
       if (p.out) store_row<F32, VEC>(p.out + kBytes * ((r0 + i) * p.out_row + v0), left, x[q]);
+      fetch(q, i + kRowsAhead * gridDim.z);
       if (p.argmax) {
         const float best = y.largest();
         warp_argmax(&s_key[i], best, [&]() {
@@ -275,63 +293,64 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
     }
   }
 
-  // ---- the listed columns, a warp per row: every step
+  // ---- the listed columns: every step
   if (pen) {
     __syncthreads();  // the dense walk's stores come first
     const int m = s_n;
     const float rep = p.r.repetition ? p.r.repetition[b] : 1.f, freq = p.r.frequency ? p.r.frequency[b] : 0.f,
                 pres = p.r.presence ? p.r.presence[b] : 0.f;
-    for (int i = blockIdx.z + (tid >> 5) * gridDim.z; i < n; i += (kLogitThreads / 32) * gridDim.z) {
-      const uint64_t mask = row_mask(p.t, r0, i);
-      const char *from = p.x + kBytes * ((r0 + i) * p.row + v0);
-      char *to = p.out + kBytes * ((r0 + i) * p.out_row + v0);
-      const uint32_t *words = p.r.allowed ? p.r.allowed + (r0 + i) * p.r.allowed_row : nullptr;
-      float best = -INFINITY;
-      int bc = 0x7fffffff;
-      for (int k0 = 0; k0 < m; k0 += 32 * kAhead) {
-        int c[kAhead];
-        float x[kAhead], add[kAhead];
-        uint32_t ok[kAhead];
+    // an item is 32 listed columns of one row; a warp has kAhead of them in flight
+    constexpr int kW = kLogitThreads / 32;
+    const int chunks = (m + 31) / 32, rows = (n - (int)blockIdx.z + (int)gridDim.z - 1) / (int)gridDim.z;
+    for (int u0 = tid >> 5; u0 < rows * chunks; u0 += kW * kAhead) {
+      int c[kAhead], row[kAhead];
+      float z[kAhead], add[kAhead];
+      uint32_t may[kAhead];
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
-          const int k = k0 + 32 * q + lane;
-          c[q] = k < m ? (int)s_list[k] : -1;
-          if (c[q] >= 0) {
-            x[q] = F32 ? *reinterpret_cast<const float *>(from + 4 * c[q])
-                       : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(from + 2 * c[q]) << 16);
-            add[q] = bias ? bias[c[q]] : 0.f;
-            ok[q] = words ? words[(v0 + c[q]) >> 5] >> ((v0 + c[q]) & 31) & 1u : 1u;
-          }
+      for (int q = 0; q < kAhead; ++q) {
+        const int u = u0 + q * kW, k = (u % chunks) * 32 + lane;
+        row[q] = blockIdx.z + (u / chunks) * gridDim.z;
+        c[q] = u < rows * chunks && k < m ? (int)s_list[k] : -1;
+        if (c[q] >= 0) {
+          const char *from = p.x + kBytes * ((r0 + row[q]) * p.row + v0 + c[q]);
+          z[q] = F32 ? *reinterpret_cast<const float *>(from)
+                     : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(from) << 16);
+          add[q] = bias ? bias[c[q]] : 0.f;
+          may[q] = 1u;
+          if (p.r.allowed)
+            may[q] = p.r.allowed[(r0 + row[q]) * p.r.allowed_row + ((v0 + c[q]) >> 5)] >> ((v0 + c[q]) & 31) & 1u;
         }
+      }
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
-          if (c[q] < 0) continue;
+      for (int q = 0; q < kAhead; ++q) {
+        if (u0 + q * kW >= rows * chunks) break;
+        float y = -INFINITY;
+        if (c[q] >= 0) {
           const uint32_t w = s_cnt[c[q]];
           uint32_t cnt = w & kCountMask;
-          if (w & kTreeBit)
+          if (w & kTreeBit) {
+            const uint64_t mask = row_mask(p.t, r0, row[q]);
             for (int j = 0; j < n; ++j) cnt += s_tok[j] == c[q] && (mask >> j & 1);
+          }
           // steps 1-5 of dfv_logits_process, every product, quotient and
           // difference rounded on its own (no contraction)
-          float y = x[q];
+          y = z[q];
           if (p.r.repetition && (cnt || (w & kPromptBit))) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
           if (p.r.frequency) y = __fsub_rn(y, __fmul_rn(freq, (float)cnt));
           if (p.r.presence && cnt) y = __fsub_rn(y, pres);
           if (bias) y = __fadd_rn(y, add[q]);
-          if (!ok[q]) y = -INFINITY;
+          if (!may[q]) y = -INFINITY;
           if (!F32) y = round_bf16(y);
           if (p.out) {
+            char *to = p.out + kBytes * ((r0 + row[q]) * p.out_row + v0 + c[q]);
             if (F32)
-              *reinterpret_cast<float *>(to + 4 * c[q]) = y;
+              *reinterpret_cast<float *>(to) = y;
             else
-              *reinterpret_cast<uint16_t *>(to + 2 * c[q]) = f32_to_bf16_bits(y);
-          }
-          if (y > best || (y == best && c[q] < bc)) {  // the list is in no order
-            best = y;
-            bc = c[q];
+              *reinterpret_cast<uint16_t *>(to) = f32_to_bf16_bits(y);
           }
         }
+        if (p.argmax) warp_argmax(&s_key[row[q]], y, [&]() { return v0 + c[q]; });
       }
-      if (p.argmax) warp_argmax(&s_key[i], best, [&]() { return v0 + bc; });
     }
   }
 
