@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const int r = row0 + mt * 16 + hh * 8 + gr;
-        const int i = r / p.G, g = r - i * p.G;
+        const int i = node_of(L, r), g = r - i * p.G;
         mask[mt][hh] = 0;
         const uint32_t *qp = nullptr;
         if (r < R) {
@@ -523,6 +523,7 @@ cudaError_t launch_tree_attn(const TreeAttnParams &p, const AttnPlan &a, void *w
   L.rows = a.rows;
   L.n_rt = a.n_rt;
   L.n_groups = a.n_groups;
+  L.inv_g = (65536u + p.G - 1) / p.G;
   attn_sections(&L, a, p.t.n_seqs, p.c.D, ws);
   const int tile = L.rows >= 128 ? 128 : kKt, page = 1 << p.c.page_shift, rows = page < tile ? page : tile;
   L.swap = p.c.Hkv > 1 && p.c.sh < p.c.st;

@@ -14,6 +14,7 @@ struct AttnLaunch {
   int n_rt;      // CTAs per range, for further rows
   int n_groups;  // ranges
   int swap;      // head before token in the tensor maps
+  uint32_t inv_g;  // ceil(2^16 / G)
   long long *starts;  // [n_seqs + 1] first unit of each sequence, then the number of units
   float2 *part_ml;    // [2 CTAs][rows] (M, l) of partial states
   float *part_o;      // [2 CTAs][rows][D] their sums of p v
@@ -43,6 +44,10 @@ inline size_t attn_sections(AttnLaunch *L, const AttnPlan &a, int n_seqs, int D,
   }
   return off;
 }
+
+// Node of row r: r / G for r < 1024 + 256 and G <= 16 (the product's error stays
+// below one part in 2^16 / G).
+__device__ __forceinline__ int node_of(const AttnLaunch &L, int r) { return (int)(((uint32_t)r * L.inv_g) >> 16); }
 
 // ---------------------------------------------------------------- the work line
 // Sequence b's units are its kv heads' key tiles, head after head; a pair
@@ -136,7 +141,7 @@ struct SegWalk {
       T = v.n == 0 ? 0 : total > 0 ? (total + KT - 1) / KT : 1;
       const long long w = u - base, units = (long long)L.p.c.Hkv * T;
       if (w < units) {
-        h = (int)(w / T);
+        h = (units >> 31) ? (int)(w / T) : (int)((uint32_t)w / (uint32_t)T);
         t0 = (int)(w - (long long)h * T);
         t1 = (int)min((long long)T, t0 + (end - u));
         at = u;
@@ -151,7 +156,7 @@ struct SegWalk {
   // The nodes that row r sees.
   __device__ __forceinline__ uint64_t mask_of(int r) const {
     if (nodes == 0) return 0;
-    return row_mask(L.p.t, v.row0, r / L.p.G) & (nodes >= 64 ? ~0ull : (1ull << nodes) - 1ull);
+    return row_mask(L.p.t, v.row0, node_of(L, r)) & (nodes >= 64 ? ~0ull : (1ull << nodes) - 1ull);
   }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == T; }
   // a range cuts at most two pairs: the one it starts in and the one it ends in
@@ -243,6 +248,21 @@ __device__ __noinline__ float unseen(const TreeAttnParams &p, const SeqView &v, 
     if (!isfinite(y)) x += y;
   }
   return x;
+}
+
+// unseen() added to elements c0 .. c1 of a stored output (rare: a value in the
+// tree is not finite).
+template <bool F16>
+__device__ __noinline__ void add_unseen(const TreeAttnParams &p, const SeqView &v, int i, int h, char *out, int c0,
+                                        int c1) {
+  uint32_t *w = reinterpret_cast<uint32_t *>(out);
+#pragma unroll 1
+  for (int d = c0; d < c1; d += 2) {
+    float2 x = unpack2<F16>(w[d / 2]);
+    x.x += unseen<F16>(p, v, i, h, d);
+    x.y += unseen<F16>(p, v, i, h, d + 1);
+    w[d / 2] = pack2<F16>(x.x, x.y);
+  }
 }
 
 // Output piece e (8 elements) of row r: x / l, and lse = (z + log2 l) ln 2.

@@ -59,12 +59,30 @@ __device__ __forceinline__ uint32_t idesc_16(int N, bool b_mn) {
          ((uint32_t)(128 >> 4) << 24);
 }
 
+// The MMA warp runs in step and one elected lane issues: descriptors stay in
+// uniform registers (issued under `if (lane == 0)` every operand was moved there
+// first, about as long as the MMA itself takes).
+// D[tmem] (+)= A[smem] * B[smem]^T
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_elect(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
+      : "memory");
+}
 // D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -97,13 +115,28 @@ __device__ __forceinline__ void load_scores(uint32_t addr, float *s) {
   tmem_ld32(addr + 32, s + 32);
   tmem_wait_ld();
 }
-// Scores of 64 keys, the first of them node j0: what the row does not see is -inf.
-__device__ __forceinline__ void mask_scores(float *s, int j0, uint64_t mask) {
+// Scores of a tile whose first key is node j0 (below 0: committed): what the row
+// does not see becomes -inf, in place.  A short loop, as is clean_row: they run
+// once per sequence, and unrolled their instructions took longer to fetch than
+// to execute.
+__device__ __forceinline__ void mask_tile(uint32_t t_s, int j0, uint64_t mask) {
+#pragma unroll 1
+  for (int q = 0; q < kTKeys; q += 16) {
+    const int j = j0 + q;  // node of the first of 16 keys
+    if (j + 16 <= 0) continue;
+    uint32_t sees;
+    if (j >= 0)
+      sees = j < 64 ? (uint32_t)(mask >> j) : 0u;
+    else
+      sees = (uint32_t)(mask << -j) | ((1u << -j) - 1u);
+    float s[16];
+    tmem_ld16(t_s + q, s);
+    uint32_t x[16];
 #pragma unroll
-  for (int q = 0; q < 64; ++q) {
-    const int node = j0 + q;
-    if (node >= 0 && (node >= 64 || !((mask >> (node & 63)) & 1))) s[q] = -INFINITY;
+    for (int e = 0; e < 16; ++e) x[e] = sees >> e & 1u ? __float_as_uint(s[e]) : 0xff800000u;
+    tmem_st16(t_s + q, x);
   }
+  tmem_wait_st();
 }
 
 // Key row `row` of a V tile in shared memory: zeroed past the last node (j >= n);
@@ -112,28 +145,22 @@ template <bool F16, int D>
 __device__ __forceinline__ void clean_row(unsigned char *tile, int row, int j, int n, int *bad) {
   if (j < 0) return;
   constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
+#pragma unroll 1
+  for (int c = 0; c < D / 8; ++c) {  // chunk order turned by the row: no bank conflicts, and any order will do
+    uint4 *at = reinterpret_cast<uint4 *>(tile + (c >> 3) * 16384 + row * 128 + (((c ^ row) & 7) << 4));
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    bool hit = j >= n;
+    if (!hit) {
+      v = *at;
+      uint32_t *w = &v.x;
 #pragma unroll
-  for (int hf = 0; hf < D / 64; ++hf) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {  // chunk order turned by the row: no bank conflicts, and any order will do
-      uint4 *at = reinterpret_cast<uint4 *>(tile + hf * 16384 + row * 128 + ((c ^ (row & 7)) << 4));
-      if (j >= n) {
-        *at = make_uint4(0u, 0u, 0u, 0u);
-      } else {
-        uint4 v = *at;
-        uint32_t *w = &v.x;
-        bool hit = false;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if ((w[e] & kExp) == kExp) { w[e] &= 0xffff0000u; hit = true; }
-          if ((w[e] & (kExp << 16)) == (kExp << 16)) { w[e] &= 0x0000ffffu; hit = true; }
-        }
-        if (hit) {
-          *at = v;
-          *bad = 1;
-        }
+      for (int e = 0; e < 4; ++e) {
+        if ((w[e] & kExp) == kExp) { w[e] &= 0xffff0000u; hit = true; }
+        if ((w[e] & (kExp << 16)) == (kExp << 16)) { w[e] &= 0x0000ffffu; hit = true; }
       }
+      if (hit) *bad = 1;
     }
+    if (hit) *at = v;
   }
 }
 
@@ -241,29 +268,29 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
       if (!mbar_wait(smem_u32(&s_full[j % S::kSlots]), (j / S::kSlots) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never)) break;
   } else if (warp == 9) {
     // ---------------------------------------------------------------- MMA issue
-    if (lane == 0) {
+    {
       int st = 0, ph = 0, seg = 0;
       unsigned np[2] = {0u, 0u};  // tiles of each warpgroup whose P was awaited
       bool ok = true;
       const uint32_t iq = idesc_16<F16>(kTKeys, false), iv = idesc_16<F16>(D, true);
       auto full = [&]() {
-        ok = ok && mbar_wait_fast(smem_u32(&s_full[st]), ph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort);
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_full[st]), ph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
         tc_fence_after();
       };
       auto done = [&]() {  // the slot is free once the MMAs issued so far have read it
-        tc_commit(smem_u32(&s_empty[st]));
+        tc_commit_elect(smem_u32(&s_empty[st]));
         if (++st == S::kSlots) { st = 0; ph ^= 1; }
       };
       auto qk = [&](int w) {
         const uint32_t kb = ring + (uint32_t)st * S::kTile, qb = q_addr + (DUAL ? (uint32_t)w * 128u * D * 2u : 0u);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-          tc_mma(tmem + (uint32_t)w * 128u, sdesc_k128(qb + (ks >> 2) * 16384) + (uint64_t)(2 * (ks & 3)),
+          tc_mma_ss(tmem + (uint32_t)w * 128u, sdesc_k128(qb + (ks >> 2) * 16384) + (uint64_t)(2 * (ks & 3)),
                  sdesc_k128(kb + (ks >> 2) * 16384) + (uint64_t)(2 * (ks & 3)), iq, ks > 0 ? 1u : 0u);
-        tc_commit(smem_u32(&s_sfull[w]));
+        tc_commit_elect(smem_u32(&s_sfull[w]));
       };
       auto pv = [&](int w, bool first) {
-        ok = ok && mbar_wait_fast(smem_u32(&s_pready[w]), np[w] & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort);
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_pready[w]), np[w] & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
         if (!ok) return;
         ++np[w];
         tc_fence_after();
@@ -272,12 +299,12 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
         for (int ks = 0; ks < kTKeys / 16; ++ks)
           tc_mma_ts(tmem + 256u + (uint32_t)w * 128u, tmem + (uint32_t)w * 128u + (uint32_t)ks * 8u,
                     sdesc_mn128(vb + (uint32_t)ks * 2048u), iv, (first && ks == 0) ? 0u : 1u);
-        tc_commit(smem_u32(&s_odone[w]));
+        tc_commit_elect(smem_u32(&s_odone[w]));
       };
       while (ok && wk.next()) {
         if (row0 >= wk.v.n * p.G) continue;
         const int n = wk.t1 - wk.t0;
-        ok = mbar_wait_fast(smem_u32(&s_qready), seg & 1, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort);
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_qready), seg & 1, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
         ++seg;
         tc_fence_after();
         if (DUAL) {
@@ -333,7 +360,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
         }
       }
       // every MMA issued has completed before tensor memory is released
-      tc_commit(smem_u32(&s_drain));
+      tc_commit_elect(smem_u32(&s_drain));
       volatile int never = 0;
       mbar_wait(smem_u32(&s_drain), 0u, p.err, DFV_DEVERR_DRAIN_WAIT, &never);
     }
@@ -353,15 +380,27 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
       if (row0 >= R) continue;
       const int n = wk.t1 - wk.t0;
       // rows into the swizzled layout; past R zero
-      for (int u = tid; u < (DUAL ? 256 : 128) * (D / 8); u += 256) {
-        const int rr = u / (D / 8), ch = u - rr * (D / 8), r = row0 + rr;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (r < R) {
-          const int i = r / p.G, g = r - i * p.G;
-          x = *reinterpret_cast<const uint4 *>(p.q + 2 * ((wk.v.row0 + i) * p.q_row + (wk.h * p.G + g) * p.q_head + ch * 8));
+      {
+        constexpr int kCh = D / 8, kStep = 256 / kCh;  // 16-byte chunks of a row; rows apart
+        constexpr int kIter = (DUAL ? 256 : 128) / kStep, kBatch = kIter < 8 ? kIter : 8;
+        const int ch = tid % kCh;
+        const char *qh = p.q + 2 * (wk.v.row0 * p.q_row + (long long)wk.h * p.G * p.q_head + ch * 8);
+        uint4 x[kBatch];
+#pragma unroll
+        for (int k0 = 0; k0 < kIter; k0 += kBatch) {
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int r = row0 + tid / kCh + (k0 + k) * kStep, i = node_of(L, r);
+            x[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < R) x[k] = *reinterpret_cast<const uint4 *>(qh + 2 * (i * p.q_row + (r - i * p.G) * p.q_head));
+          }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int rr = tid / kCh + (k0 + k) * kStep;
+            *reinterpret_cast<uint4 *>(s_q + (rr >> 7) * (128 * D * 2) + (ch >> 3) * 16384 + (rr & 127) * 128 +
+                                       (((ch & 7) ^ (rr & 7)) << 4)) = x[k];
+          }
         }
-        *reinterpret_cast<uint4 *>(s_q + (rr >> 7) * (128 * D * 2) + (ch >> 3) * 16384 + (rr & 127) * 128 +
-                                   (((ch & 7) ^ (rr & 7)) << 4)) = x;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(smem_u32(&s_qready));
@@ -380,12 +419,12 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
         // which stays in registers; the upper half is read again below
         const int k0 = (wk.t0 + j) * kTKeys, j0 = k0 - wk.v.len;  // node number of the tile's first key
         const bool special = j0 + kTKeys > 0;  // tree nodes or keys past the end in the tile
+        if (special) mask_tile(t_s, j0, mask);
         float s[64];
         float mx = -INFINITY;
 #pragma unroll
         for (int hf = 1; hf >= 0; --hf) {
           load_scores(t_s + 64 * hf, s);
-          if (special) mask_scores(s, j0 + 64 * hf, mask);
 #pragma unroll
           for (int q = 0; q < 64; q += 2) mx = fmaxf(mx, fmaxf(s[q], s[q + 1]));
         }
@@ -416,10 +455,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
         float l0 = 0.f, l1 = 0.f;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          if (hf) {
-            load_scores(t_s + 64, s);
-            if (special) mask_scores(s, j0 + 64, mask);
-          }
+          if (hf) load_scores(t_s + 64, s);
 #pragma unroll
           for (int q = 0; q < 64; q += 32) {
             uint32_t x[16];
@@ -473,29 +509,48 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
       const int bad = s_bad;
       const float z = (M == -INFINITY ? 0.f : M * c) - kBias;
       const int c0 = DUAL ? 0 : w * (D / 2), c1 = DUAL ? D : c0 + D / 2;
+      const bool whole = wk.whole();
+      const int slot = wk.slot(blockIdx.x), i = node_of(L, r), head = wk.h * p.G + r - i * p.G;
+      const size_t row = wk.v.row0 + i;
+      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // NaN stays NaN
+      char *out = p.o + 2 * (row * p.o_row + head * p.o_head);
+      float *part = L.part_o + ((size_t)slot * L.rows + rr) * D;
 #pragma unroll 1
-      for (int q = c0; q < c1 && ok; q += 16) {
-        float o[16];
-        tmem_ld16(lane_base + 256u + (DUAL ? (uint32_t)w * 128u : 0u) + q, o);
+      for (int q = c0; q < c1 && ok; q += 32) {
+        float o[32];
+        tmem_ld32(lane_base + 256u + (DUAL ? (uint32_t)w * 128u : 0u) + q, o);
         if (!DUAL && n > 1) {
-          float o1[16];
-          tmem_ld16(lane_base + 384u + q, o1);
+          float o1[32];
+          tmem_ld32(lane_base + 384u + q, o1);
+          tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = o[e] * f0 + o1[e] * f1;
+          for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
+        } else {
+          tmem_wait_ld();
         }
-        if (wk.whole()) {
-          if (r < R) {
+        if (r >= R) continue;
+        if (whole) {
+          uint32_t x[16];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) store_out<F16>(p, wk.v, r, wk.h, q / 8 + e, o + 8 * e, z, lsum, bad);
-          }
-        } else if (r < R) {
-          float *to = L.part_o + ((size_t)wk.slot(blockIdx.x) * L.rows + rr) * D + q;
+          for (int e = 0; e < 16; ++e) x[e] = pack2<F16>(o[2 * e] * inv, o[2 * e + 1] * inv);
+          uint4 *to = reinterpret_cast<uint4 *>(out + 2 * q);
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4 *>(to + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          if (q == 0) L.part_ml[(size_t)wk.slot(blockIdx.x) * L.rows + rr] = make_float2(M == -INFINITY ? -INFINITY : z, lsum);
+          for (int e = 0; e < 4; ++e) to[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        } else {
+          float4 *to = reinterpret_cast<float4 *>(part + q);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) to[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
-      if (!wk.whole() && tid == 0) L.part_bad[wk.slot(blockIdx.x)] = bad;
+      if (r < R && ok && c0 == 0) {
+        if (whole) {
+          if (p.lse) p.lse[row * p.H + head] = lsum == 0.f ? -INFINITY : (z + log2f(lsum)) * 0.69314718055994531f;
+        } else {
+          L.part_ml[(size_t)slot * L.rows + rr] = make_float2(M == -INFINITY ? -INFINITY : z, lsum);
+        }
+      }
+      if (whole && bad && r < R && ok) add_unseen<F16>(p, wk.v, i, wk.h, out, c0, c1);
+      if (!whole && tid == 0) L.part_bad[slot] = bad;
       tc_fence_before();
       bar_sync_n(1, 256);  // O, Q's place and s_bad are read
       if (tid == 0) s_bad = 0;
