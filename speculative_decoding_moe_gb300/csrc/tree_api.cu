@@ -223,7 +223,7 @@ static int check_attn_shape(const dfv_kv_cache *cache, const dfv_tree_batch *tre
 size_t dfv_tree_attention_workspace_size(const dfv_kv_cache *cache, const dfv_tree_batch *tree, int n_heads) {
   if (check_attn_shape(cache, tree, n_heads)) return 0;
   const dfv::AttnPlan a = dfv::tree_attn_plan(tree->max_nodes, n_heads / cache->n_kv_heads);
-  return dfv::tree_attn_ws(a, tree->n_seqs, cache->head_dim);
+  return dfv::tree_attn_ws(a, tree->n_seqs, cache->n_kv_heads, cache->head_dim);
 }
 
 int dfv_tree_attention(const dfv_kv_cache *cache, int layer, const dfv_tree_batch *tree, int n_heads, float scale,

@@ -358,38 +358,40 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
         }
       }
     }
+    if (ct == 0) wk.tell(s_start, blockIdx.x);
     bar_sync_n(1, 128);  // the join buffers are free
     if (ct == 0) s_bad = 0;
   }
 }
 
 // ---------------------------------------------------------------- join
-// One warp per row of every pair whose units were cut: the states of its ranges
-// in order.  Pairs done by one range were stored by it.  Lane k takes the (M, l)
-// of every 32nd state, so all of them are in flight at once; the sums of p v
-// follow eight states at a time.
-constexpr int kJoinWarps = 4;
+// Rows of pairs whose units were cut: the states of their ranges, in order.
+// Pairs done by one range were stored by it.  WPR warps share a row: one where
+// there are many rows of few states each, eight where few rows have many states
+// (the latency of reading them one after the other is what counts then).  Lane k
+// takes the (M, l) of every 32nd state, so all of them are in flight at once; a
+// warp reads the sums of p v of its states eight at a time.
+constexpr int kJoinWarps = 8;
 constexpr int kJoinStates = (kAttnCtas + 31) / 32;
 
-template <bool F16, int D>
+template <bool F16, int D, int WPR>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join_kernel(const __grid_constant__ AttnLaunch L) {
   constexpr int E = D / 32;  // elements of a lane
+  __shared__ float s_x[WPR > 1 ? kJoinWarps : 1][D];
   pdl_trigger();
   const TreeAttnParams &p = L.p;
-  const int b = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31;
-  const int r = blockIdx.z * kJoinWarps + (threadIdx.x >> 5);
+  const int b = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = blockIdx.z * (kJoinWarps / WPR) + warp / WPR, part = warp % WPR;
   // the first launch releases this one after its own wait: the call's inputs are final
   const SeqView v = seq_view(p.c, p.t, b);
   if (r >= v.n * p.G) return;
   pdl_wait();
-  const long long s0 = L.starts[b], s1 = L.starts[b + 1], U = L.starts[p.t.n_seqs];
-  const long long T = (s1 - s0) / p.c.Hkv, a = s0 + h * T, e = a + T;
-  const int G = ranges_of(U, L.n_groups), g0 = group_of(a, U, G), g1 = group_of(e - 1, U, G);
-  if (g0 == g1) return;
-  const int rt = r / L.rows, rr = r - rt * L.rows, n = g1 - g0 + 1;
-  // state k is range g0 + k's; only the first range can hold the pair as its second cut
-  const int second = group_start(g0, U, G) != a;
-  auto slot = [&](int k) { return (size_t)(2 * ((g0 + k) * L.n_rt + rt) + (k == 0 ? second : 0)); };
+  const int4 pair = __ldcg(&L.pairs[b * p.c.Hkv + h]);
+  const int g0 = pair.x, n = pair.y;
+  if (n < 2) return;
+  const int rt = r / L.rows, rr = r - rt * L.rows;
+  // state k is range g0 + k's; only in the first range can the pair be the second cut
+  auto slot = [&](int k) { return (size_t)(2 * ((g0 + k) * L.n_rt + rt) + (k == 0 ? pair.z : 0)); };
   float2 ml[kJoinStates];
   int bad = 0;
   float M = -INFINITY;
@@ -417,27 +419,37 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join_kernel(const _
   float x[E];
 #pragma unroll
   for (int j = 0; j < E; ++j) x[j] = 0.f;
-  const float *base = L.part_o + rr * D + lane * E;
+  const float *base = L.part_o + (size_t)rr * D + lane * E;
   const size_t pitch = (size_t)L.rows * D;
 #pragma unroll
   for (int q = 0; q < kJoinStates; ++q) {
 #pragma unroll 1
-    for (int k0 = 32 * q; k0 < min(n, 32 * q + 32); k0 += 8) {
+    for (int k0 = 32 * q + part; k0 < min(n, 32 * q + 32); k0 += 8 * WPR) {
       float y[8][E];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (k0 + i < n) load_floats<E>(base + slot(k0 + i) * pitch, y[i]);
+        if (k0 + i * WPR < min(n, 32 * q + 32)) load_floats<E>(base + slot(k0 + i * WPR) * pitch, y[i]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float f = __shfl_sync(0xffffffffu, w[q], (k0 + i) & 31);
-        if (k0 + i < n) {
+        const float f = __shfl_sync(0xffffffffu, w[q], (k0 + i * WPR) & 31);
+        if (k0 + i * WPR < min(n, 32 * q + 32)) {
 #pragma unroll
           for (int j = 0; j < E; ++j) x[j] = fmaf(y[i][j], f, x[j]);
         }
       }
     }
   }
-  const int i = r / p.G, gg = r - i * p.G, head = h * p.G + gg;
+  if (WPR > 1) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) s_x[warp % kJoinWarps][lane * E + j] = x[j];
+    __syncthreads();  // one row per CTA: all of its warps are here
+    if (part) return;
+#pragma unroll
+    for (int k = 1; k < WPR; ++k)
+#pragma unroll
+      for (int j = 0; j < E; ++j) x[j] += s_x[k][lane * E + j];
+  }
+  const int i = node_of(L, r), head = h * p.G + r - i * p.G;
   const size_t row = v.row0 + i;
   const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
   uint32_t out[E / 2];
@@ -499,7 +511,11 @@ cudaError_t launch_typed(AttnLaunch &L, cudaStream_t s) {
                   : L.rows == 16 ? launch_mma<F16, D, 1>(L, s)
                                  : launch_mma<F16, D, 2>(L, s);
   if (e != cudaSuccess) return e;
-  return launch_chained(tree_attn_join_kernel<F16, D>, dim3(L.p.t.n_seqs, L.p.c.Hkv, (R + kJoinWarps - 1) / kJoinWarps),
+  // a warp per row fills the SMs from about 4000 rows on; with fewer, eight share one
+  if ((long long)L.p.t.n_seqs * L.p.c.Hkv * R < 4096)
+    return launch_chained(tree_attn_join_kernel<F16, D, kJoinWarps>, dim3(L.p.t.n_seqs, L.p.c.Hkv, R),
+                          dim3(32 * kJoinWarps), 0, s, L);
+  return launch_chained(tree_attn_join_kernel<F16, D, 1>, dim3(L.p.t.n_seqs, L.p.c.Hkv, (R + kJoinWarps - 1) / kJoinWarps),
                         dim3(32 * kJoinWarps), 0, s, L);
 }
 
@@ -514,7 +530,9 @@ AttnPlan tree_attn_plan(int max_nodes, int G) {
   return a;
 }
 
-size_t tree_attn_ws(const AttnPlan &a, int n_seqs, int D) { return attn_sections(nullptr, a, n_seqs, D, nullptr); }
+size_t tree_attn_ws(const AttnPlan &a, int n_seqs, int Hkv, int D) {
+  return attn_sections(nullptr, a, n_seqs, Hkv, D, nullptr);
+}
 
 cudaError_t launch_tree_attn(const TreeAttnParams &p, const AttnPlan &a, void *ws, cudaStream_t s, char *why,
                              size_t why_len) {
@@ -524,7 +542,7 @@ cudaError_t launch_tree_attn(const TreeAttnParams &p, const AttnPlan &a, void *w
   L.n_rt = a.n_rt;
   L.n_groups = a.n_groups;
   L.inv_g = (65536u + p.G - 1) / p.G;
-  attn_sections(&L, a, p.t.n_seqs, p.c.D, ws);
+  attn_sections(&L, a, p.t.n_seqs, p.c.Hkv, p.c.D, ws);
   const int tile = L.rows >= 128 ? 128 : kKt, page = 1 << p.c.page_shift, rows = page < tile ? page : tile;
   L.swap = p.c.Hkv > 1 && p.c.sh < p.c.st;
   if (!encode_kv(&L.tm_k, p.c, p.c.k, p.layer, rows, L.swap, why, why_len) ||

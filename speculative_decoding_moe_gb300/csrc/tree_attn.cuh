@@ -15,7 +15,7 @@ struct AttnLaunch {
   int n_groups;  // ranges
   int swap;      // head before token in the tensor maps
   uint32_t inv_g;  // ceil(2^16 / G)
-  long long *starts;  // [n_seqs + 1] first unit of each sequence, then the number of units
+  int4 *pairs;        // [n_seqs][kv heads] of each pair: first range, ranges, whether it starts inside that range
   float2 *part_ml;    // [2 CTAs][rows] (M, l) of partial states
   float *part_o;      // [2 CTAs][rows][D] their sums of p v
   int *part_bad;      // [2 CTAs] a tree value that is not finite was left out
@@ -24,7 +24,7 @@ struct AttnLaunch {
 cudaError_t launch_attn_tc(const AttnLaunch &L, cudaStream_t s);  // tree_attn_tc.cu: rows 128 or 256
 
 // Sections of the attention workspace; returns its size.
-inline size_t attn_sections(AttnLaunch *L, const AttnPlan &a, int n_seqs, int D, void *ws) {
+inline size_t attn_sections(AttnLaunch *L, const AttnPlan &a, int n_seqs, int Hkv, int D, void *ws) {
   const size_t slots = 2 * (size_t)a.n_groups * a.n_rt;
   size_t off = 512;  // the error word is at 256
   auto take = [&](size_t n) {
@@ -32,12 +32,12 @@ inline size_t attn_sections(AttnLaunch *L, const AttnPlan &a, int n_seqs, int D,
     off += (n + 255) & ~(size_t)255;
     return q;
   };
-  long long *starts = (long long *)take((size_t)(n_seqs + 1) * 8);
+  int4 *pairs = (int4 *)take((size_t)n_seqs * Hkv * 16);
   int *bad = (int *)take(slots * 4);
   float2 *ml = (float2 *)take(slots * a.rows * 8);
   float *o = (float *)take(slots * a.rows * D * 4);
   if (L) {
-    L->starts = starts;
+    L->pairs = pairs;
     L->part_bad = bad;
     L->part_ml = ml;
     L->part_o = o;
@@ -56,7 +56,8 @@ __device__ __forceinline__ int node_of(const AttnLaunch &L, int r) { return (int
 // there are no more ranges than units.
 struct SchedStart {
   long long u0, u1, base;  // the range, and the first unit of sequence b
-  int b;
+  long long U;             // units, and ranges in use
+  int b, G;
 };
 
 // Ranges in use: no range is empty.
@@ -75,8 +76,7 @@ __device__ __forceinline__ long long seq_units(const AttnLaunch &L, int b) {
 }
 
 // The range of CTA `block` and the sequence it starts in.  All NT threads of
-// the CTA call it; s_scan holds NT / 32 values.  CTA 0 also writes the first
-// units of all sequences for the join.
+// the CTA call it; s_scan holds NT / 32 values.
 template <int NT, int KT>
 __device__ __forceinline__ void sched_start(const AttnLaunch &L, int block, long long *s_scan, SchedStart *out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = L.p.t.n_seqs;
@@ -102,13 +102,11 @@ __device__ __forceinline__ void sched_start(const AttnLaunch &L, int block, long
   }
   const int g = block / L.n_rt, G = ranges_of(U, L.n_groups);
   const long long u0 = group_start(g, U, G), u1 = g < G ? group_start(g + 1, U, G) : u0;
-  const bool mine = u0 < u1 && at <= u0 && u0 < at + sum;
-  if (mine || block == 0) {
+  if (u0 < u1 && at <= u0 && u0 < at + sum) {
     long long base = at;
     for (int b = b0; b < b1; ++b) {
       const long long c = seq_units<KT>(L, b);
-      if (block == 0) L.starts[b] = base;
-      if (mine && base <= u0 && u0 < base + c) {
+      if (base <= u0 && u0 < base + c) {
         out->u0 = u0;
         out->u1 = u1;
         out->base = base;
@@ -117,7 +115,10 @@ __device__ __forceinline__ void sched_start(const AttnLaunch &L, int block, long
       base += c;
     }
   }
-  if (block == 0 && tid == 0) L.starts[n] = U;
+  if (tid == 0) {
+    out->U = U;
+    out->G = G;
+  }
   __syncthreads();
 }
 
@@ -159,6 +160,13 @@ struct SegWalk {
     return row_mask(L.p.t, v.row0, node_of(L, r)) & (nodes >= 64 ? ~0ull : (1ull << nodes) - 1ull);
   }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == T; }
+  // For the join: one thread of the range that holds the pair's first unit tells
+  // which ranges share it.
+  __device__ __forceinline__ void tell(const SchedStart &s, int block) const {
+    if (t0 || block % L.n_rt) return;
+    const int g = block / L.n_rt, last = whole() ? g : group_of(at + T - 1, s.U, s.G);
+    L.pairs[b * L.p.c.Hkv + h] = make_int4(g, last - g + 1, at != first, 0);
+  }
   // a range cuts at most two pairs: the one it starts in and the one it ends in
   __device__ __forceinline__ int slot(int block) const { return 2 * block + (at != first); }
 };

@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
     // tensor memory, so the warpgroups meet at every barrier
     while (wk.next()) {
       const int R = wk.v.n * p.G;
-      if (row0 >= R) continue;
+      if (row0 >= R) continue;  // never the CTA that tells of the pair: its rows are the first
       const int n = wk.t1 - wk.t0;
       // rows into the swizzled layout; past R zero
       {
@@ -550,7 +550,10 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
         }
       }
       if (whole && bad && r < R && ok) add_unseen<F16>(p, wk.v, i, wk.h, out, c0, c1);
-      if (!whole && tid == 0) L.part_bad[slot] = bad;
+      if (tid == 0) {
+        if (!whole) L.part_bad[slot] = bad;
+        wk.tell(s_start, blockIdx.x);
+      }
       tc_fence_before();
       bar_sync_n(1, 256);  // O, Q's place and s_bad are read
       if (tid == 0) s_bad = 0;

@@ -161,7 +161,7 @@ struct AttnPlan {
   int rows, n_rt, n_groups;
 };
 AttnPlan tree_attn_plan(int max_nodes, int G);
-size_t tree_attn_ws(const AttnPlan &a, int n_seqs, int D);
+size_t tree_attn_ws(const AttnPlan &a, int n_seqs, int Hkv, int D);
 cudaError_t launch_tree_attn(const TreeAttnParams &p, const AttnPlan &a, void *ws, cudaStream_t s, char *why,
                              size_t why_len);
 cudaError_t launch_logits(const LogitsParams &p, cudaStream_t s);
