@@ -36,18 +36,25 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn(char *why, size_t why_len);
 namespace {
 
 // ---------------------------------------------------------------- mma.sync kernel
-constexpr int kKt = 64;              // keys per tile: 16 for each of four consumer warps
-constexpr int kMmaThreads = 160;     // producer warp and four consumer warps
-constexpr int kRing = 180 * 1024;    // bytes of the ring of key/value tiles
-
-template <int D>
-constexpr int mma_stages() {
-  return kRing / (2 * kKt * D * 2);
-}
+// A CTA is a producer warp and four or eight consumer warps.  A tile is 64 keys,
+// 16 for each of four warps; with eight, two groups of four take every other
+// tile, which hides the chain from one tile's scores to its product (16-row
+// tiles; the registers of 32 rows leave room for four warps).  Each group has
+// stages of its own: a parity wait is only sound for a warp that sees every
+// phase of a barrier.
+constexpr int kKt = 64;
 template <int D, int MT>
-constexpr size_t mma_smem() {
-  return 1024 + (size_t)mma_stages<D>() * 2 * kKt * D * 2 + (size_t)16 * MT * (D + 4) * 4;
-}
+struct MmaShape {
+  static constexpr int kGroups = MT == 1 ? 2 : 1;
+  static constexpr int kWarps = 4 * kGroups;
+  static constexpr int kThreads = 32 * (1 + kWarps);
+  static constexpr uint32_t kTile = kKt * D * 2;           // one K or V tile
+  static constexpr int kStages = D == 64 ? 10 : 4;         // of K and V: 160 and 128 KB in flight
+  static constexpr int kPer = kStages / kGroups;           // stages of a group
+  static constexpr int kPitch = D + 4;                     // floats of a row of a warp's state
+  static constexpr size_t kState = (size_t)16 * MT * kPitch * 4;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * kTile + kWarps * kState;
+};
 
 // Keys of a tile sit in rows of 128 bytes (64 elements), one block of rows per
 // 64 elements of the head, 16-byte chunks XOR row % 8 (128-byte TMA swizzle).
@@ -64,23 +71,22 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
 }
 
 template <bool F16, int D, int MT>
-__global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __grid_constant__ AttnLaunch L) {
-  constexpr int kStages = mma_stages<D>();
-  constexpr int kHalves = D / 64;
-  constexpr uint32_t kTileBytes = kKt * D * 2;
-  constexpr int kOPitch = D + 4;  // floats; rows of the join buffer 16 bytes apart in banks
+__global__ void __launch_bounds__(MmaShape<D, MT>::kThreads, 1) tree_attn_mma_kernel(const __grid_constant__ AttnLaunch L) {
+  using S = MmaShape<D, MT>;
+  constexpr int kStages = S::kStages, kHalves = D / 64;
+  constexpr uint32_t kTileBytes = S::kTile;
   extern __shared__ __align__(16) unsigned char sm_raw[];
   unsigned char *sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) unsigned long long s_full[kStages], s_empty[kStages];
   __shared__ volatile int s_abort;
   __shared__ SchedStart s_start;
-  __shared__ long long s_scan[kMmaThreads / 32];
-  __shared__ float s_m[4][16 * MT], s_l[4][16 * MT];
+  __shared__ long long s_scan[S::kThreads / 32];
+  __shared__ float2 s_ml[S::kWarps][16 * MT];
   __shared__ int s_bad;
   const TreeAttnParams &p = L.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = smem_u32(sm);
-  float *s_o = reinterpret_cast<float *>(sm + (size_t)kStages * 2 * kTileBytes);  // [16 MT][kOPitch]
+  unsigned char *s_state = sm + (size_t)kStages * 2 * kTileBytes;  // [warp][16 MT][kPitch] fp32
   if (tid == 0) {
     s_abort = 0;
     s_bad = 0;
@@ -92,12 +98,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
   }
   pdl_wait();
   pdl_trigger();  // the join may now read the call's inputs
-  sched_start<kMmaThreads, kKt>(L, blockIdx.x, s_scan, &s_start);  // syncs the CTA
+  sched_start<S::kThreads, kKt>(L, blockIdx.x, s_scan, &s_start);  // syncs the CTA
   const int row0 = (int)(blockIdx.x % L.n_rt) * 16 * MT;  // first row of this CTA
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
-    int st = 0, ph = 0, issued = 0;
+    int issued[S::kGroups] = {};  // tiles of each group
     bool ok = true;
     SegWalk<kKt> wk(L, s_start);
     const int shift = p.c.page_shift, boxes = shift >= 6 ? 1 : kKt >> shift, rows = kKt / boxes;
@@ -111,8 +117,14 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
       int pg = page(wk.t0);
       for (int t = wk.t0; t < wk.t1; ++t) {
         const int pgn = t + 1 < wk.t1 ? page(t + 1) : -1;  // the next tile's ids are fetched a tile ahead
+        const int g = S::kGroups > 1 ? (t - wk.t0) & 1 : 0;
+        const int turn = g ? issued[S::kGroups - 1]++ : issued[0]++;
+        const int st = g * S::kPer + turn % S::kPer, ph = (turn / S::kPer) & 1;
         ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_empty[st]), ph ^ 1, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
-        if (!ok) break;
+        if (!ok) {  // this tile is not issued
+          issued[g ? S::kGroups - 1 : 0] = turn;
+          break;
+        }
         const uint32_t fb = smem_u32(&s_full[st]), dst = ring + (uint32_t)st * 2 * kTileBytes;
         const unsigned have = __ballot_sync(0xffffffffu, pg >= 0);
         if (lane == 0) {
@@ -131,23 +143,24 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
             tma_kv(dst + kTileBytes + off, &L.tm_v, hf * 64, tok, wk.h, pg, L.swap, fb);
           }
         }
-        ++issued;
-        if (++st == kStages) { st = 0; ph ^= 1; }
         pg = pgn;
       }
     }
     // no copy may land after the CTA exits: wait for the last fill of every stage
     volatile int never = 0;
-    for (int j = issued - kStages < 0 ? 0 : issued - kStages; j < issued; ++j)
-      if (!mbar_wait(smem_u32(&s_full[j % kStages]), (j / kStages) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never)) break;
+#pragma unroll
+    for (int g = 0; g < S::kGroups; ++g)
+      for (int j = issued[g] - S::kPer < 0 ? 0 : issued[g] - S::kPer; j < issued[g]; ++j)
+        if (!mbar_wait(smem_u32(&s_full[g * S::kPer + j % S::kPer]), (j / S::kPer) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never))
+          break;
     return;
   }
 
   // ------------------------------------------------------------------ consumers
-  const int cw = warp - 1, gr = lane >> 2, qc = lane & 3;
+  const int cw = (warp - 1) & 3, group = (warp - 1) >> 2, gr = lane >> 2, qc = lane & 3;
   const float c = p.scale_log2;
   constexpr float kBias = F16 ? 6.f : 0.f;
-  int st = 0, ph = 0;
+  int st = group * S::kPer, ph = 0;
   bool ok = true;
   SegWalk<kKt> wk(L, s_start);
   while (wk.next()) {
@@ -184,7 +197,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
         for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
     }
     bool bad = false;
-    for (int t = wk.t0; t < wk.t1; ++t) {
+    for (int t = wk.t0 + group; t < wk.t1; t += S::kGroups) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_full[st]), ph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
       if (!ok) break;
       const uint32_t kb = ring + (uint32_t)st * 2 * kTileBytes, vb = kb + kTileBytes;
@@ -286,80 +299,67 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&s_empty[st]));
-      if (++st == kStages) { st = 0; ph ^= 1; }
+      if (++st == (group + 1) * S::kPer) { st = group * S::kPer; ph ^= 1; }
     }
-    // ---- join the four warps' states
+    // ---- the warps' states, side by side
+    {
+      const int w = warp - 1;
+      float *mine = reinterpret_cast<float *>(s_state + w * S::kState);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        float x = l[mt][hh];
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        if (qc == 0) {
-          s_m[cw][mt * 16 + hh * 8 + gr] = m[mt][hh];
-          s_l[cw][mt * 16 + hh * 8 + gr] = x;
+        for (int hh = 0; hh < 2; ++hh) {
+          const int r = mt * 16 + hh * 8 + gr;
+          float x = l[mt][hh];
+          x += __shfl_xor_sync(0xffffffffu, x, 1);
+          x += __shfl_xor_sync(0xffffffffu, x, 2);
+          if (qc == 0) s_ml[w][r] = make_float2(m[mt][hh], x);
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<float2 *>(mine + r * S::kPitch + n * 8 + 2 * qc) =
+                make_float2(o[mt][n][2 * hh], o[mt][n][2 * hh + 1]);
         }
-      }
-    if (bad) s_bad = 1;
-    bar_sync_n(1, 128);
-    for (int w = 0; w < 4; ++w) {
-      if (cw == w) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const int r = mt * 16 + hh * 8 + gr;
-            const float M = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
-            const float f = m[mt][hh] == -INFINITY ? 0.f : ex2((m[mt][hh] - M) * c);
-            // a warp without keys for the row adds its zeros (or NaN of a NaN query)
-            const float g = m[mt][hh] == -INFINITY ? 1.f : f;
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-              float2 *z = reinterpret_cast<float2 *>(s_o + r * kOPitch + n * 8 + 2 * qc);
-              float2 y = make_float2(o[mt][n][2 * hh] * g, o[mt][n][2 * hh + 1] * g);
-              if (w) {
-                y.x += z->x;
-                y.y += z->y;
-              }
-              *z = y;
-            }
-          }
-      }
-      bar_sync_n(1, 128);
     }
-    const int isbad = s_bad;
-    const int ct = tid - 32;
+    if (bad) s_bad = 1;
+    bar_sync_n(1, 32 * S::kWarps);
+    const int isbad = s_bad, ct = tid - 32;
+    const bool whole = wk.whole();
+    const int slot = wk.slot(blockIdx.x);
     // ---- the state of the whole segment: output, or partial state
-    for (int u = ct; u < 16 * MT * (D / 8); u += 128) {
+#pragma unroll 1
+    for (int u = ct; u < 16 * MT * (D / 8); u += 32 * S::kWarps) {
       const int r = u / (D / 8), e = u - r * (D / 8);
-      float M = -INFINITY, lsum = 0.f;
+      float M = -INFINITY, lsum = 0.f, x[8];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) M = fmaxf(M, s_m[w][r]);
+      for (int w = 0; w < S::kWarps; ++w) M = fmaxf(M, s_ml[w][r].x);
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
-        lsum += s_m[w][r] == -INFINITY ? s_l[w][r] : s_l[w][r] * ex2((s_m[w][r] - M) * c);
-      float x[8];
+      for (int j = 0; j < 8; ++j) x[j] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; j += 4) {
-        const float4 y = *reinterpret_cast<const float4 *>(s_o + r * kOPitch + e * 8 + j);
-        x[j] = y.x; x[j + 1] = y.y; x[j + 2] = y.z; x[j + 3] = y.w;
+      for (int w = 0; w < S::kWarps; ++w) {
+        const float2 ml = s_ml[w][r];
+        // a warp without keys for the row adds its zeros (or NaN of a NaN query)
+        const float f = ml.x == -INFINITY ? 1.f : ex2((ml.x - M) * c);
+        lsum = fmaf(ml.y, f, lsum);
+        const float4 *from = reinterpret_cast<const float4 *>(s_state + w * S::kState) + (r * S::kPitch + e * 8) / 4;
+        const float4 a = from[0], b = from[1];
+        x[0] = fmaf(a.x, f, x[0]); x[1] = fmaf(a.y, f, x[1]); x[2] = fmaf(a.z, f, x[2]); x[3] = fmaf(a.w, f, x[3]);
+        x[4] = fmaf(b.x, f, x[4]); x[5] = fmaf(b.y, f, x[5]); x[6] = fmaf(b.z, f, x[6]); x[7] = fmaf(b.w, f, x[7]);
       }
       const float z = (M == -INFINITY ? 0.f : M * c) - kBias;
-      if (wk.whole()) {
-        if (row0 + r < R) store_out<F16>(p, wk.v, row0 + r, wk.h, e, x, z, lsum, isbad);
+      if (whole) {
+        if (row0 + r < R) store_out<F16>(L, wk.v, row0 + r, wk.h, e, x, z, lsum, isbad);
       } else {
-        float *to = L.part_o + ((size_t)wk.slot(blockIdx.x) * L.rows + r) * D + e * 8;
+        float *to = L.part_o + ((size_t)slot * L.rows + r) * D + e * 8;
         *reinterpret_cast<float4 *>(to) = make_float4(x[0], x[1], x[2], x[3]);
         *reinterpret_cast<float4 *>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
         if (e == 0) {
-          L.part_ml[(size_t)wk.slot(blockIdx.x) * L.rows + r] = make_float2(M == -INFINITY ? -INFINITY : z, lsum);
-          if (r == 0) L.part_bad[wk.slot(blockIdx.x)] = isbad;
+          L.part_ml[(size_t)slot * L.rows + r] = make_float2(M == -INFINITY ? -INFINITY : z, lsum);
+          if (r == 0) L.part_bad[slot] = isbad;
         }
       }
     }
     if (ct == 0) wk.tell(s_start, blockIdx.x);
-    bar_sync_n(1, 128);  // the join buffers are free
+    bar_sync_n(1, 32 * S::kWarps);  // the states' places are free
     if (ct == 0) s_bad = 0;
   }
 }
@@ -498,10 +498,11 @@ bool encode_kv(CUtensorMap *map, const CacheParams &c, const char *base, int lay
 
 template <bool F16, int D, int MT>
 cudaError_t launch_mma(const AttnLaunch &L, cudaStream_t s) {
+  using S = MmaShape<D, MT>;
   auto kern = tree_attn_mma_kernel<F16, D, MT>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)mma_smem<D, MT>());
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_chained(kern, dim3(L.n_groups * L.n_rt), dim3(kMmaThreads), mma_smem<D, MT>(), s, L);
+  return launch_chained(kern, dim3(L.n_groups * L.n_rt), dim3(S::kThreads), S::kSmem, s, L);
 }
 
 template <bool F16, int D>

@@ -275,22 +275,17 @@ __device__ __noinline__ void add_unseen(const TreeAttnParams &p, const SeqView &
 
 // Output piece e (8 elements) of row r: x / l, and lse = (z + log2 l) ln 2.
 template <bool F16>
-__device__ __forceinline__ void store_out(const TreeAttnParams &p, const SeqView &v, int r, int h, int e, const float *x,
+__device__ __forceinline__ void store_out(const AttnLaunch &L, const SeqView &v, int r, int h, int e, const float *x,
                                           float z, float l, int bad) {
-  const int i = r / p.G, g = r - i * p.G, head = h * p.G + g;
+  const TreeAttnParams &p = L.p;
+  const int i = node_of(L, r), head = h * p.G + r - i * p.G;
   const size_t row = v.row0 + i;
   const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
-  uint32_t w[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float a = x[2 * j] * inv, b = x[2 * j + 1] * inv;
-    if (bad) {
-      a += unseen<F16>(p, v, i, h, e * 8 + 2 * j);
-      b += unseen<F16>(p, v, i, h, e * 8 + 2 * j + 1);
-    }
-    w[j] = pack2<F16>(a, b);
-  }
-  *reinterpret_cast<uint4 *>(p.o + 2 * (row * p.o_row + head * p.o_head + e * 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+  char *out = p.o + 2 * (row * p.o_row + head * p.o_head);
+  *reinterpret_cast<uint4 *>(out + 16 * e) =
+      make_uint4(pack2<F16>(x[0] * inv, x[1] * inv), pack2<F16>(x[2] * inv, x[3] * inv),
+                 pack2<F16>(x[4] * inv, x[5] * inv), pack2<F16>(x[6] * inv, x[7] * inv));
+  if (bad) add_unseen<F16>(p, v, i, h, out, 8 * e, 8 * e + 8);
   if (e == 0 && p.lse) p.lse[row * p.H + head] = l == 0.f ? -INFINITY : (z + log2f(l)) * 0.69314718055994531f;
 }
 

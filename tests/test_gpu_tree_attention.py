@@ -341,3 +341,10 @@ def test_mask_bits_past_the_tree_are_ignored(dfv):
         assert all(signed(m) < 0 for m in c.masks)
         out, _, _ = run(dfv, c)
         assert bool(((out - want[0]).abs() <= c.tolerances(*want)[0]).all())
+
+
+@pytest.mark.parametrize("dim,heads,kv", [(64, 4, 1), (64, 16, 2), (128, 8, 1), (64, 16, 1), (128, 12, 1)])
+def test_many_tiles_per_range(dfv, dim, heads, kv):
+    """Long enough that every range goes round its ring of tiles several times."""
+    c = Case([90001, 70003], [2, 1], heads, kv, dim, 64, FP, seed=dim + heads)
+    check(c, *run(dfv, c)[:2])
