@@ -107,14 +107,50 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
       DFV_I8(r, 0), DFV_I8(r, 8)
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for every load of the thread; r passes through, so that no use of it can
+// move above the wait.
+#define DFV_P8(r, b) "+f"(r[b]), "+f"(r[b + 1]), "+f"(r[b + 2]), "+f"(r[b + 3]), "+f"(r[b + 4]), "+f"(r[b + 5]), \
+                     "+f"(r[b + 6]), "+f"(r[b + 7])
+__device__ __forceinline__ void tmem_wait_ld32(float *r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : DFV_P8(r, 0), DFV_P8(r, 8), DFV_P8(r, 16), DFV_P8(r, 24)::"memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void load_scores(uint32_t addr, float *s) {
-  tmem_ld32(addr, s);
-  tmem_ld32(addr + 32, s + 32);
-  tmem_wait_ld();
+// (a, b) * (c, c) + (d, d) and sums, two at a time
+__device__ __forceinline__ float2 fma2(float2 a, float c, float d) {
+  float2 r;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mov.b64 z, {%5, %5};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(c), "f"(d));
+  return r;
 }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float max32(const float *s, float m) {
+#pragma unroll
+  for (int q = 0; q < 32; q += 2) m = fmaxf(m, fmaxf(s[q], s[q + 1]));
+  return m;
+}
+// p of 32 scores as 16-bit pairs, and their sum
+template <bool F16>
+__device__ __forceinline__ void exp32(const float *s, float c, float z, uint32_t *x, float2 &l) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float2 y = fma2(make_float2(s[2 * e], s[2 * e + 1]), c, -z);
+    y.x = ex2(y.x);
+    y.y = ex2(y.y);
+    l = add2(l, y);
+    x[e] = pack2<F16>(y.x, y.y);
+  }
+}
+
 // Scores of a tile whose first key is node j0 (below 0: committed): what the row
 // does not see becomes -inf, in place.  A short loop, as is clean_row: they run
 // once per sequence, and unrolled their instructions took longer to fetch than
@@ -172,7 +208,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
   constexpr int kHalves = D / 64;
   extern __shared__ __align__(16) unsigned char sm_raw[];
   unsigned char *sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) unsigned long long s_full[S::kSlots], s_empty[S::kSlots], s_sfull[2], s_pready[2], s_odone[2],
+  __shared__ __align__(8) unsigned long long s_full[S::kSlots], s_empty[S::kSlots], s_sfull[2], s_pready[2][2], s_odone[2],
       s_qready, s_drain;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
@@ -192,7 +228,8 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(smem_u32(&s_sfull[w]), 1);
-      mbar_init(smem_u32(&s_pready[w]), 128);
+      mbar_init(smem_u32(&s_pready[w][0]), 128);
+      mbar_init(smem_u32(&s_pready[w][1]), 128);
       mbar_init(smem_u32(&s_odone[w]), 1);
     }
     mbar_init(smem_u32(&s_qready), 256);
@@ -290,15 +327,18 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
         tc_commit_elect(smem_u32(&s_sfull[w]));
       };
       auto pv = [&](int w, bool first) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_pready[w]), np[w] & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-        if (!ok) return;
-        ++np[w];
-        tc_fence_after();
         const uint32_t vb = ring + (uint32_t)st * S::kTile;
 #pragma unroll
-        for (int ks = 0; ks < kTKeys / 16; ++ks)
-          tc_mma_ts(tmem + 256u + (uint32_t)w * 128u, tmem + (uint32_t)w * 128u + (uint32_t)ks * 8u,
-                    sdesc_mn128(vb + (uint32_t)ks * 2048u), iv, (first && ks == 0) ? 0u : 1u);
+        for (int hf = 0; hf < 2; ++hf) {  // each half of P as it is ready
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_pready[w][hf]), np[w] & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = hf * 4; ks < hf * 4 + 4; ++ks)
+            tc_mma_ts(tmem + 256u + (uint32_t)w * 128u, tmem + (uint32_t)w * 128u + (uint32_t)ks * 8u,
+                      sdesc_mn128(vb + (uint32_t)ks * 2048u), iv, (first && ks == 0) ? 0u : 1u);
+        }
+        ++np[w];
         tc_commit_elect(smem_u32(&s_odone[w]));
       };
       while (ok && wk.next()) {
@@ -415,19 +455,26 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
         ++nt;
         if (!ok) continue;
         tc_fence_after();
-        // the upper half of the scores for their maximum, then the lower half,
-        // which stays in registers; the upper half is read again below
         const int k0 = (wk.t0 + j) * kTKeys, j0 = k0 - wk.v.len;  // node number of the tile's first key
         const bool special = j0 + kTKeys > 0;  // tree nodes or keys past the end in the tile
         if (special) mask_tile(t_s, j0, mask);
-        float s[64];
+        // quarters of the scores in two buffers, each read while the other is
+        // used: last to first for the maximum, which leaves the first two in
+        // registers, then first to last for p
+        float s0[32], s1[32];
         float mx = -INFINITY;
-#pragma unroll
-        for (int hf = 1; hf >= 0; --hf) {
-          load_scores(t_s + 64 * hf, s);
-#pragma unroll
-          for (int q = 0; q < 64; q += 2) mx = fmaxf(mx, fmaxf(s[q], s[q + 1]));
-        }
+        tmem_ld32(t_s + 96, s1);
+        tmem_wait_ld32(s1);
+        tmem_ld32(t_s + 64, s0);
+        mx = max32(s1, mx);
+        tmem_wait_ld32(s0);
+        tmem_ld32(t_s + 32, s1);
+        mx = max32(s0, mx);
+        tmem_wait_ld32(s1);
+        tmem_ld32(t_s, s0);
+        mx = max32(s1, mx);
+        tmem_wait_ld32(s0);
+        mx = max32(s0, mx);
         mx = fmaxf(mx, m);
         if (!started) {
           m = mx;
@@ -452,24 +499,6 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
         }
         started = true;
         const float z = (m == -INFINITY ? 0.f : m * c) - kBias;
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          if (hf) load_scores(t_s + 64, s);
-#pragma unroll
-          for (int q = 0; q < 64; q += 32) {
-            uint32_t x[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float a = ex2(fmaf(s[q + 2 * e], c, -z)), b = ex2(fmaf(s[q + 2 * e + 1], c, -z));
-              l0 += a;
-              l1 += b;
-              x[e] = pack2<F16>(a, b);
-            }
-            tmem_st16(t_s + 32 * hf + q / 2, x);
-          }
-        }
-        l += l0 + l1;
         if (special && (!DUAL || w == 0)) {
           // this tile's V before it is multiplied
           const unsigned it = items + (unsigned)(j + (j + LA < n ? j + LA : n));
@@ -479,9 +508,28 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
           clean_row<F16, D>(s_ring + (size_t)(it % S::kSlots) * S::kTile, wt, j0 + wt, wk.nodes, &s_bad);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
+        float2 l2 = make_float2(0.f, 0.f);
+        uint32_t x[16];
+        exp32<F16>(s0, c, z, x, l2);
+        tmem_st16(t_s, x);
+        tmem_ld32(t_s + 64, s0);
+        exp32<F16>(s1, c, z, x, l2);
+        tmem_st16(t_s + 16, x);
+        // the first half of P may be multiplied
+        tmem_wait_st();
+        tmem_wait_ld32(s0);
+        tc_fence_before();
+        mbar_arrive(smem_u32(&s_pready[w][0]));
+        tmem_ld32(t_s + 96, s1);
+        exp32<F16>(s0, c, z, x, l2);
+        tmem_st16(t_s + 32, x);
+        tmem_wait_ld32(s1);
+        exp32<F16>(s1, c, z, x, l2);
+        tmem_st16(t_s + 48, x);
+        l += l2.x + l2.y;
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(smem_u32(&s_pready[w]));
+        mbar_arrive(smem_u32(&s_pready[w][1]));
       }
       items += 2u * (unsigned)n;
       // ---- output: the last product of this warpgroup, then (SINGLE) both states
@@ -522,11 +570,12 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
         if (!DUAL && n > 1) {
           float o1[32];
           tmem_ld32(lane_base + 384u + q, o1);
-          tmem_wait_ld();
+          tmem_wait_ld32(o);
+          tmem_wait_ld32(o1);
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
         } else {
-          tmem_wait_ld();
+          tmem_wait_ld32(o);
         }
         if (r >= R) continue;
         if (whole) {
