@@ -59,9 +59,10 @@ __device__ __forceinline__ uint32_t idesc_16(int N, bool b_mn) {
          ((uint32_t)(128 >> 4) << 24);
 }
 
-// The MMA warp runs in step and one elected lane issues: descriptors stay in
-// uniform registers (issued under `if (lane == 0)` every operand was moved there
-// first, about as long as the MMA itself takes).
+// The MMA warp runs in step and an elected lane issues: descriptors are computed
+// in uniform registers.  (Issued under `if (lane == 0)`, or under a predicate that
+// does not come from elect.sync, every operand was moved there first, about as
+// long as the MMA itself takes.)
 // D[tmem] (+)= A[smem] * B[smem]^T
 __device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                           uint32_t accumulate) {
@@ -71,12 +72,6 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t adesc, uint6
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tc_commit_elect(uint32_t bar) {
-  asm volatile(
-      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
-      : "memory");
-}
 // D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                           uint32_t accumulate) {
@@ -84,6 +79,12 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_elect(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
       : "memory");
 }
 
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
                  sdesc_k128(kb + (ks >> 2) * 16384) + (uint64_t)(2 * (ks & 3)), iq, ks > 0 ? 1u : 0u);
         tc_commit_elect(smem_u32(&s_sfull[w]));
       };
-      auto pv = [&](int w, bool first) {
+      auto pv = [&](int w, bool first, bool last) {
         const uint32_t vb = ring + (uint32_t)st * S::kTile;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {  // each half of P as it is ready
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
                       sdesc_mn128(vb + (uint32_t)ks * 2048u), iv, (first && ks == 0) ? 0u : 1u);
         }
         ++np[w];
-        tc_commit_elect(smem_u32(&s_odone[w]));
+        if (last) tc_commit_elect(smem_u32(&s_odone[w]));
       };
       while (ok && wk.next()) {
         if (row0 >= wk.v.n * p.G) continue;
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
             // V_j, then K_j+1; each warpgroup's next scores right after its own product
             full();
             if (!ok) break;
-            pv(0, j == 0);
+            pv(0, j == 0, j == n - 1);
             if (!ok) break;
             if (j + 1 < n) {
               int kst = st + 1, kph = ph;
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
               qk(0);
               st = sv; ph = pv_;
             }
-            pv(1, j == 0);
+            pv(1, j == 0, j == n - 1);
             if (!ok) break;
             done();  // V_j
             if (j + 1 < n) {
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
           for (int j = 0; j < n && ok; ++j) {
             full();
             if (!ok) break;
-            pv(j & 1, j < 2);
+            pv(j & 1, j < 2, j + 2 >= n);
             if (!ok) break;
             done();
             if (j + LA < n) {
@@ -411,6 +412,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
     const uint32_t t_s = lane_base + (uint32_t)w * 128u, t_o = lane_base + 256u + (uint32_t)w * 128u;
     const float c = p.scale_log2;
     unsigned nt = 0;     // tiles this warpgroup has taken
+    unsigned outs = 0;   // segments it has put out
     unsigned items = 0;  // ring items of the segments before
     bool ok = true;
     // after a wait gives up the loops still run to the end without touching
@@ -479,10 +481,8 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
         if (!started) {
           m = mx;
         } else if (__any_sync(0xffffffffu, (mx - m) * c > 8.f)) {
-          // the last product into O has to be complete
-          ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_odone[w]), nt & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-          if (!ok) continue;
-          tc_fence_after();
+          // the last product into O is complete: it was issued before these
+          // scores, and their barrier follows all that was issued before it
           const float f = m == -INFINITY ? 0.f : ex2((m - mx) * c);
           m = mx;
           l *= f;
@@ -533,8 +533,10 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
       }
       items += 2u * (unsigned)n;
       // ---- output: the last product of this warpgroup, then (SINGLE) both states
-      if (started)
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_odone[w]), (nt - 1) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+      if (DUAL || w < n) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_odone[w]), outs & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+        ++outs;
+      }
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       const int rr = DUAL ? w * 128 + wt : wt;
