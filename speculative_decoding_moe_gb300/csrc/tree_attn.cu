@@ -134,13 +134,15 @@ __global__ void __launch_bounds__(MmaShape<D, MT>::kThreads, 1) tree_attn_mma_ke
             mbar_arrive(fb);
         }
         __syncwarp();
-        if (pg >= 0) {
-          const int tok = (t * kKt) & ((1 << shift) - 1);  // 0 unless a page holds several tiles
+        const int tok = (t * kKt) & ((1 << shift) - 1), nb = __popc(have);  // tok: 0 unless a page holds several tiles
+#pragma unroll 2
+        for (int b = 0; b < nb; ++b) {
+          const int pb = __shfl_sync(0xffffffffu, pg, b);
 #pragma unroll
           for (int hf = 0; hf < kHalves; ++hf) {
-            const uint32_t off = (uint32_t)(hf * kKt * 128 + lane * rows * 128);
-            tma_kv(dst + off, &L.tm_k, hf * 64, tok, wk.h, pg, L.swap, fb);
-            tma_kv(dst + kTileBytes + off, &L.tm_v, hf * 64, tok, wk.h, pg, L.swap, fb);
+            const uint32_t off = (uint32_t)(hf * kKt * 128 + b * rows * 128);
+            tma_kv(dst + off, &L.tm_k, hf * 64, tok, wk.h, pb, L.swap, fb);
+            tma_kv(dst + kTileBytes + off, &L.tm_v, hf * 64, tok, wk.h, pb, L.swap, fb);
           }
         }
         pg = pgn;

@@ -201,11 +201,16 @@ __device__ __forceinline__ int checked_page(const CacheParams &c, int pg) {
   return 0;
 }
 
+// One page's box of a tile, issued by an elected lane of a warp in step.  (With a
+// lane per page the compiler issued the lanes' copies one after the other, each
+// after moving its operands to uniform registers: 16-token pages were bound by
+// that.)
 __device__ __forceinline__ void tma_kv(uint32_t dst, const CUtensorMap *map, int x, int tok, int h, int pg, int swap,
                                        uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(dst),
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];\n}" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(swap ? h : tok), "r"(swap ? tok : h), "r"(pg), "r"(bar)
       : "memory");
 }

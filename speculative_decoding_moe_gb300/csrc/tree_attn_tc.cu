@@ -15,8 +15,9 @@
 // 2^8: p then stays below 2^8 (fp16: 2^14 with its offset), the sums are exact
 // in the same M, and almost every tile skips the read and write of O.
 //
-// Warps 0-3 and 4-7 are the two warpgroups, warp 8 streams K and V tiles with TMA
-// into one ring in the order the MMAs use them, warp 9 issues the MMAs.
+// Warps 0-3 and 4-7 are the two warpgroups, warps 8 and 10 stream K and V tiles
+// with TMA into one ring in the order the MMAs use them (half of each tile's boxes
+// each), warp 9 issues the MMAs.
 // Tensor memory: S0 S1 O0 O1 of 128 columns each; P (16-bit pairs) over S.
 #include <cstdio>
 
@@ -27,7 +28,8 @@ namespace dfv {
 namespace {
 
 constexpr int kTKeys = 128;
-constexpr int kTThreads = 320;
+constexpr int kTThreads = 352;
+constexpr int kProducers = 2;
 
 template <int D, bool DUAL>
 struct TcShape {
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
     s_abort = 0;
     s_bad = 0;
     for (int s = 0; s < S::kSlots; ++s) {
-      mbar_init(smem_u32(&s_full[s]), 1);
+      mbar_init(smem_u32(&s_full[s]), kProducers);
       mbar_init(smem_u32(&s_empty[s]), 1);
     }
     for (int w = 0; w < 2; ++w) {
@@ -250,8 +252,9 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
   const int row0 = (int)(blockIdx.x % L.n_rt) * L.rows;  // first row of this CTA
   SegWalk<kTKeys> wk(L, s_start);
 
-  if (warp == 8) {
+  if (warp == 8 || warp == 10) {
     // ---------------------------------------------------------------- producer
+    const int me = (warp - 8) / 2;
     int st = 0, ph = 0, issued = 0;
     bool ok = true;
     const int shift = p.c.page_shift, boxes = shift >= 7 ? 1 : kTKeys >> shift, rows = kTKeys / boxes;
@@ -268,20 +271,22 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
                               mbar_wait_fast(smem_u32(&s_empty[st]), ph ^ 1, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
         if (!ok) return;
         const uint32_t fb = smem_u32(&s_full[st]), dst = ring + (uint32_t)st * S::kTile;
-        const unsigned have = __ballot_sync(0xffffffffu, pg >= 0);
+        const int nb = __popc(__ballot_sync(0xffffffffu, pg >= 0));
+        // this warp's boxes: one half of the head (D = 128), or every other page
+        const int b0 = kHalves > 1 ? 0 : me, step = kHalves > 1 ? 1 : kProducers, hf = kHalves > 1 ? me : 0;
+        const int mine = (nb - b0 + step - 1) / step;
         if (lane == 0) {
-          if (have)
-            mbar_expect_tx(fb, (uint32_t)__popc(have) * rows * D * 2);
+          if (mine > 0)
+            mbar_expect_tx(fb, (uint32_t)mine * rows * 128);
           else
             mbar_arrive(fb);
         }
         __syncwarp();
-        if (pg >= 0) {
-          const int tok = ((wk.t0 + j) * kTKeys) & ((1 << shift) - 1);  // 0 unless a page holds several tiles
-#pragma unroll
-          for (int hf = 0; hf < kHalves; ++hf)
-            tma_kv(dst + (uint32_t)(hf * 16384 + lane * rows * 128), map, hf * 64, tok, wk.h, pg, L.swap, fb);
-        }
+        const int tok = ((wk.t0 + j) * kTKeys) & ((1 << shift) - 1);  // 0 unless a page holds several tiles
+#pragma unroll 2
+        for (int b = b0; b < nb; b += step)
+          tma_kv(dst + (uint32_t)(hf * 16384 + b * rows * 128), map, hf * 64, tok, wk.h, __shfl_sync(0xffffffffu, pg, b),
+                 L.swap, fb);
         ++issued;
         if (++st == S::kSlots) { st = 0; ph ^= 1; }
       };
