@@ -19,9 +19,10 @@
 // replayed after they change.
 //
 // Kernels, by rows per kv head:
-//   up to 32   mma.sync m16n8k16: bound by reading the cache (the tensor pipe
-//              could take about 64 rows at the HBM rate)
+//   up to 16   mma.sync m16n8k16: bound by reading the cache
 //   above      tcgen05 on 128-row tiles, scores and outputs in tensor memory
+//              (two 16-row tiles of mma.sync took 110 us where it takes 86:
+//              32 x 4 nodes of 8 heads over 8191 keys)
 #include <cstdio>
 #include <cstring>
 
@@ -36,24 +37,22 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn(char *why, size_t why_len);
 namespace {
 
 // ---------------------------------------------------------------- mma.sync kernel
-// A CTA is a producer warp and four or eight consumer warps.  A tile is 64 keys,
-// 16 for each of four warps; with eight, two groups of four take every other
-// tile, which hides the chain from one tile's scores to its product (16-row
-// tiles; the registers of 32 rows leave room for four warps).  Each group has
-// stages of its own: a parity wait is only sound for a warp that sees every
+// A CTA is two producer warps (keys and values) and eight consumer warps.  A tile
+// is 64 keys, 16 for each of four warps; two groups of four warps take every other
+// tile, which hides the chain from one tile's scores to its product.  Each group
+// has stages of its own: a parity wait is only sound for a warp that sees every
 // phase of a barrier.
 constexpr int kKt = 64;
-template <int D, int MT>
+constexpr int kRows = 16;
+constexpr int kProd = 2, kCons = 8, kGroups = 2, kMmaThreads = 32 * (kProd + kCons);
+template <int D>
 struct MmaShape {
-  static constexpr int kGroups = MT == 1 ? 2 : 1;
-  static constexpr int kWarps = 4 * kGroups;
-  static constexpr int kThreads = 32 * (1 + kWarps);
   static constexpr uint32_t kTile = kKt * D * 2;           // one K or V tile
   static constexpr int kStages = D == 64 ? 10 : 4;         // of K and V: 160 and 128 KB in flight
   static constexpr int kPer = kStages / kGroups;           // stages of a group
   static constexpr int kPitch = D + 4;                     // floats of a row of a warp's state
-  static constexpr size_t kState = (size_t)16 * MT * kPitch * 4;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * kTile + kWarps * kState;
+  static constexpr size_t kState = (size_t)kRows * kPitch * 4;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * kTile + kCons * kState;
 };
 
 // Keys of a tile sit in rows of 128 bytes (64 elements), one block of rows per
@@ -70,9 +69,9 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
     mma_bf16(c, a[0], a[1], a[2], a[3], b0, b1);
 }
 
-template <bool F16, int D, int MT>
-__global__ void __launch_bounds__(MmaShape<D, MT>::kThreads, 1) tree_attn_mma_kernel(const __grid_constant__ AttnLaunch L) {
-  using S = MmaShape<D, MT>;
+template <bool F16, int D>
+__global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __grid_constant__ AttnLaunch L) {
+  using S = MmaShape<D>;
   constexpr int kStages = S::kStages, kHalves = D / 64;
   constexpr uint32_t kTileBytes = S::kTile;
   extern __shared__ __align__(16) unsigned char sm_raw[];
@@ -80,30 +79,31 @@ __global__ void __launch_bounds__(MmaShape<D, MT>::kThreads, 1) tree_attn_mma_ke
   __shared__ __align__(8) unsigned long long s_full[kStages], s_empty[kStages];
   __shared__ volatile int s_abort;
   __shared__ SchedStart s_start;
-  __shared__ long long s_scan[S::kThreads / 32];
-  __shared__ float2 s_ml[S::kWarps][16 * MT];
+  __shared__ long long s_scan[kMmaThreads / 32];
+  __shared__ float2 s_ml[kCons][kRows];
   __shared__ int s_bad;
   const TreeAttnParams &p = L.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = smem_u32(sm);
-  unsigned char *s_state = sm + (size_t)kStages * 2 * kTileBytes;  // [warp][16 MT][kPitch] fp32
+  unsigned char *s_state = sm + (size_t)kStages * 2 * kTileBytes;  // [warp][row][kPitch] fp32
   if (tid == 0) {
     s_abort = 0;
     s_bad = 0;
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_u32(&s_full[s]), 1);
+      mbar_init(smem_u32(&s_full[s]), kProd);
       mbar_init(smem_u32(&s_empty[s]), 4);
     }
     mbar_init_fence();
   }
   pdl_wait();
   pdl_trigger();  // the join may now read the call's inputs
-  sched_start<S::kThreads, kKt>(L, blockIdx.x, s_scan, &s_start);  // syncs the CTA
-  const int row0 = (int)(blockIdx.x % L.n_rt) * 16 * MT;  // first row of this CTA
+  sched_start<kMmaThreads, kKt>(L, blockIdx.x, s_scan, &s_start);  // syncs the CTA
+  const int row0 = (int)(blockIdx.x % L.n_rt) * kRows;  // first row of this CTA
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- producer
-    int issued[S::kGroups] = {};  // tiles of each group
+  if (warp < kProd) {
+    // ---------------------------------------------------------------- producers: warp 0 keys, warp 1 values
+    const CUtensorMap *map = warp == 0 ? &L.tm_k : &L.tm_v;
+    int issued[kGroups] = {};  // tiles of each group
     bool ok = true;
     SegWalk<kKt> wk(L, s_start);
     const int shift = p.c.page_shift, boxes = shift >= 6 ? 1 : kKt >> shift, rows = kKt / boxes;
@@ -117,41 +117,35 @@ __global__ void __launch_bounds__(MmaShape<D, MT>::kThreads, 1) tree_attn_mma_ke
       int pg = page(wk.t0);
       for (int t = wk.t0; t < wk.t1; ++t) {
         const int pgn = t + 1 < wk.t1 ? page(t + 1) : -1;  // the next tile's ids are fetched a tile ahead
-        const int g = S::kGroups > 1 ? (t - wk.t0) & 1 : 0;
-        const int turn = g ? issued[S::kGroups - 1]++ : issued[0]++;
+        const int g = (t - wk.t0) & 1, turn = issued[g];
         const int st = g * S::kPer + turn % S::kPer, ph = (turn / S::kPer) & 1;
         ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_empty[st]), ph ^ 1, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
-        if (!ok) {  // this tile is not issued
-          issued[g ? S::kGroups - 1 : 0] = turn;
-          break;
-        }
-        const uint32_t fb = smem_u32(&s_full[st]), dst = ring + (uint32_t)st * 2 * kTileBytes;
-        const unsigned have = __ballot_sync(0xffffffffu, pg >= 0);
+        if (!ok) break;
+        const uint32_t fb = smem_u32(&s_full[st]), dst = ring + (uint32_t)(2 * st + warp) * kTileBytes;
+        const int nb = __popc(__ballot_sync(0xffffffffu, pg >= 0));
         if (lane == 0) {
-          if (have)
-            mbar_expect_tx(fb, (uint32_t)__popc(have) * 2 * rows * D * 2);
+          if (nb)
+            mbar_expect_tx(fb, (uint32_t)nb * rows * D * 2);
           else
             mbar_arrive(fb);
         }
         __syncwarp();
-        const int tok = (t * kKt) & ((1 << shift) - 1), nb = __popc(have);  // tok: 0 unless a page holds several tiles
+        const int tok = (t * kKt) & ((1 << shift) - 1);  // 0 unless a page holds several tiles
 #pragma unroll 2
         for (int b = 0; b < nb; ++b) {
           const int pb = __shfl_sync(0xffffffffu, pg, b);
 #pragma unroll
-          for (int hf = 0; hf < kHalves; ++hf) {
-            const uint32_t off = (uint32_t)(hf * kKt * 128 + b * rows * 128);
-            tma_kv(dst + off, &L.tm_k, hf * 64, tok, wk.h, pb, L.swap, fb);
-            tma_kv(dst + kTileBytes + off, &L.tm_v, hf * 64, tok, wk.h, pb, L.swap, fb);
-          }
+          for (int hf = 0; hf < kHalves; ++hf)
+            tma_kv(dst + (uint32_t)(hf * kKt * 128 + b * rows * 128), map, hf * 64, tok, wk.h, pb, L.swap, fb);
         }
+        ++issued[g];
         pg = pgn;
       }
     }
     // no copy may land after the CTA exits: wait for the last fill of every stage
     volatile int never = 0;
 #pragma unroll
-    for (int g = 0; g < S::kGroups; ++g)
+    for (int g = 0; g < kGroups; ++g)
       for (int j = issued[g] - S::kPer < 0 ? 0 : issued[g] - S::kPer; j < issued[g]; ++j)
         if (!mbar_wait(smem_u32(&s_full[g * S::kPer + j % S::kPer]), (j / S::kPer) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never))
           break;
@@ -159,7 +153,7 @@ __global__ void __launch_bounds__(MmaShape<D, MT>::kThreads, 1) tree_attn_mma_ke
   }
 
   // ------------------------------------------------------------------ consumers
-  const int cw = (warp - 1) & 3, group = (warp - 1) >> 2, gr = lane >> 2, qc = lane & 3;
+  const int cw = (warp - kProd) & 3, group = (warp - kProd) >> 2, gr = lane >> 2, qc = lane & 3;
   const float c = p.scale_log2;
   constexpr float kBias = F16 ? 6.f : 0.f;
   int st = group * S::kPer, ph = 0;
@@ -168,116 +162,93 @@ __global__ void __launch_bounds__(MmaShape<D, MT>::kThreads, 1) tree_attn_mma_ke
   while (wk.next()) {
     const int R = wk.v.n * p.G;
     // row r = node * G + head of the group; rows past R are zero and see nothing
-    uint32_t q[MT][D / 16][4];
-    uint64_t mask[MT][2];
+    uint32_t q[D / 16][4];
+    uint64_t mask[2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int r = row0 + mt * 16 + hh * 8 + gr;
-        const int i = node_of(L, r), g = r - i * p.G;
-        mask[mt][hh] = 0;
-        const uint32_t *qp = nullptr;
-        if (r < R) {
-          mask[mt][hh] = wk.mask_of(r);
-          qp = reinterpret_cast<const uint32_t *>(p.q + 2 * ((wk.v.row0 + i) * p.q_row + (wk.h * p.G + g) * p.q_head));
-        }
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          q[mt][ks][hh] = qp ? qp[ks * 8 + qc] : 0u;
-          q[mt][ks][2 + hh] = qp ? qp[ks * 8 + 4 + qc] : 0u;
-        }
+    for (int hh = 0; hh < 2; ++hh) {
+      const int r = row0 + hh * 8 + gr, i = node_of(L, r), g = r - i * p.G;
+      mask[hh] = 0;
+      const uint32_t *qp = nullptr;
+      if (r < R) {
+        mask[hh] = wk.mask_of(r);
+        qp = reinterpret_cast<const uint32_t *>(p.q + 2 * ((wk.v.row0 + i) * p.q_row + (wk.h * p.G + g) * p.q_head));
       }
-    float o[MT][D / 8][4], m[MT][2], l[MT][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) { m[mt][hh] = -INFINITY; l[mt][hh] = 0.f; }
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+      for (int ks = 0; ks < D / 16; ++ks) {
+        q[ks][hh] = qp ? qp[ks * 8 + qc] : 0u;
+        q[ks][2 + hh] = qp ? qp[ks * 8 + 4 + qc] : 0u;
+      }
     }
+    float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
     bool bad = false;
-    for (int t = wk.t0 + group; t < wk.t1; t += S::kGroups) {
+    for (int t = wk.t0 + group; t < wk.t1; t += kGroups) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_full[st]), ph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
       if (!ok) break;
       const uint32_t kb = ring + (uint32_t)st * 2 * kTileBytes, vb = kb + kTileBytes;
       const int k0 = t * kKt + cw * 16;  // this warp's 16 keys
       if (k0 < wk.total) {
-        float s[MT][2][4];
+        float s[2][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+          for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
         {
           const int row = cw * 16 + ((lane >> 4) << 3) + (lane & 7), ch = (lane >> 3) & 1;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             uint32_t b[4];
             ldsm4(b, tile_addr(kb, ks >> 2, row, (ks & 3) * 2 + ch));
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma16<F16>(s[mt][0], q[mt][ks], b[0], b[1]);
-              mma16<F16>(s[mt][1], q[mt][ks], b[2], b[3]);
-            }
+            mma16<F16>(s[0], q[ks], b[0], b[1]);
+            mma16<F16>(s[1], q[ks], b[2], b[3]);
           }
         }
         const bool special = k0 + 16 > wk.v.len;  // tree nodes or keys past the end among the 16
         if (special) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int j = k0 + nt * 8 + 2 * qc + (e & 1) - wk.v.len;  // below 0: committed
-                if (j >= 0 && (j >= wk.nodes || !((mask[mt][e >> 1] >> j) & 1))) s[mt][nt][e] = -INFINITY;
-              }
-        }
-        uint32_t a[MT][4];
-        bool grew = false;
-        float mn[MT][2];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            float x = fmaxf(fmaxf(s[mt][0][2 * hh], s[mt][0][2 * hh + 1]), fmaxf(s[mt][1][2 * hh], s[mt][1][2 * hh + 1]));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-            mn[mt][hh] = fmaxf(m[mt][hh], x);
-            grew |= mn[mt][hh] > m[mt][hh];
-          }
-        if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const float f = m[mt][hh] == -INFINITY ? 0.f : ex2((m[mt][hh] - mn[mt][hh]) * c);
-              m[mt][hh] = mn[mt][hh];
-              l[mt][hh] *= f;
-              // nothing is summed yet where f is 0 for want of keys
-#pragma unroll
-              for (int n = 0; n < D / 8; ++n) {
-                o[mt][n][2 * hh] *= f;
-                o[mt][n][2 * hh + 1] *= f;
-              }
+            for (int e = 0; e < 4; ++e) {
+              const int j = k0 + nt * 8 + 2 * qc + (e & 1) - wk.v.len;  // below 0: committed
+              if (j >= 0 && (j >= wk.nodes || !((mask[e >> 1] >> j) & 1))) s[nt][e] = -INFINITY;
             }
         }
+        float mn[2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int hh = 0; hh < 2; ++hh) {
+          float x = fmaxf(fmaxf(s[0][2 * hh], s[0][2 * hh + 1]), fmaxf(s[1][2 * hh], s[1][2 * hh + 1]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          mn[hh] = fmaxf(m[hh], x);
+        }
+        if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
-            const float z = (m[mt][hh] == -INFINITY ? 0.f : m[mt][hh] * c) - kBias;
+            // f = 0 without keys so far: nothing is summed yet
+            const float f = m[hh] == -INFINITY ? 0.f : ex2((m[hh] - mn[hh]) * c);
+            m[hh] = mn[hh];
+            l[hh] *= f;
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              const float x = ex2(fmaf(s[mt][nt][2 * hh], c, -z)), y = ex2(fmaf(s[mt][nt][2 * hh + 1], c, -z));
-              l[mt][hh] += x + y;
-              a[mt][nt * 2 + hh] = pack2<F16>(x, y);
+            for (int n = 0; n < D / 8; ++n) {
+              o[n][2 * hh] *= f;
+              o[n][2 * hh + 1] *= f;
             }
           }
+        }
+        uint32_t a[4];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const float z = (m[hh] == -INFINITY ? 0.f : m[hh] * c) - kBias;
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            const float x = ex2(fmaf(s[nt][2 * hh], c, -z)), y = ex2(fmaf(s[nt][2 * hh + 1], c, -z));
+            l[hh] += x + y;
+            a[nt * 2 + hh] = pack2<F16>(x, y);
+          }
+        }
         {
           const int row = cw * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), cc = lane >> 4;
 #pragma unroll
@@ -291,11 +262,8 @@ __global__ void __launch_bounds__(MmaShape<D, MT>::kThreads, 1) tree_attn_mma_ke
               for (int e = 0; e < 4; ++e)
                 b[e] = clean_pair<F16>(b[e], k0 + (e & 1) * 8 + 2 * qc - wk.v.len, wk.nodes, &bad);
             }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma16<F16>(o[mt][2 * d2], a[mt], b[0], b[1]);
-              mma16<F16>(o[mt][2 * d2 + 1], a[mt], b[2], b[3]);
-            }
+            mma16<F16>(o[2 * d2], a, b[0], b[1]);
+            mma16<F16>(o[2 * d2 + 1], a, b[2], b[3]);
           }
         }
       }
@@ -305,39 +273,36 @@ __global__ void __launch_bounds__(MmaShape<D, MT>::kThreads, 1) tree_attn_mma_ke
     }
     // ---- the warps' states, side by side
     {
-      const int w = warp - 1;
+      const int w = warp - kProd;
       float *mine = reinterpret_cast<float *>(s_state + w * S::kState);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int hh = 0; hh < 2; ++hh) {
+        const int r = hh * 8 + gr;
+        float x = l[hh];
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        if (qc == 0) s_ml[w][r] = make_float2(m[hh], x);
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int r = mt * 16 + hh * 8 + gr;
-          float x = l[mt][hh];
-          x += __shfl_xor_sync(0xffffffffu, x, 1);
-          x += __shfl_xor_sync(0xffffffffu, x, 2);
-          if (qc == 0) s_ml[w][r] = make_float2(m[mt][hh], x);
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n)
-            *reinterpret_cast<float2 *>(mine + r * S::kPitch + n * 8 + 2 * qc) =
-                make_float2(o[mt][n][2 * hh], o[mt][n][2 * hh + 1]);
-        }
+        for (int n = 0; n < D / 8; ++n)
+          *reinterpret_cast<float2 *>(mine + r * S::kPitch + n * 8 + 2 * qc) = make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
+      }
     }
     if (bad) s_bad = 1;
-    bar_sync_n(1, 32 * S::kWarps);
-    const int isbad = s_bad, ct = tid - 32;
+    bar_sync_n(1, 32 * kCons);
+    const int isbad = s_bad, ct = tid - 32 * kProd;
     const bool whole = wk.whole();
     const int slot = wk.slot(blockIdx.x);
     // ---- the state of the whole segment: output, or partial state
 #pragma unroll 1
-    for (int u = ct; u < 16 * MT * (D / 8); u += 32 * S::kWarps) {
-      const int r = u / (D / 8), e = u - r * (D / 8);
+    for (int u = ct; u < kRows * (D / 8); u += 32 * kCons) {
+      const int r = u % kRows, e = u / kRows;
       float M = -INFINITY, lsum = 0.f, x[8];
 #pragma unroll
-      for (int w = 0; w < S::kWarps; ++w) M = fmaxf(M, s_ml[w][r].x);
+      for (int w = 0; w < kCons; ++w) M = fmaxf(M, s_ml[w][r].x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = 0.f;
 #pragma unroll
-      for (int w = 0; w < S::kWarps; ++w) {
+      for (int w = 0; w < kCons; ++w) {
         const float2 ml = s_ml[w][r];
         // a warp without keys for the row adds its zeros (or NaN of a NaN query)
         const float f = ml.x == -INFINITY ? 1.f : ex2((ml.x - M) * c);
@@ -351,9 +316,9 @@ __global__ void __launch_bounds__(MmaShape<D, MT>::kThreads, 1) tree_attn_mma_ke
       if (whole) {
         if (row0 + r < R) store_out<F16>(L, wk.v, row0 + r, wk.h, e, x, z, lsum, isbad);
       } else {
-        float *to = L.part_o + ((size_t)slot * L.rows + r) * D + e * 8;
-        *reinterpret_cast<float4 *>(to) = make_float4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<float4 *>(to + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        float4 *to = reinterpret_cast<float4 *>(L.part_o) + ((size_t)slot * (D / 4) + 2 * e) * L.rows + r;
+        to[0] = make_float4(x[0], x[1], x[2], x[3]);
+        to[L.rows] = make_float4(x[4], x[5], x[6], x[7]);
         if (e == 0) {
           L.part_ml[(size_t)slot * L.rows + r] = make_float2(M == -INFINITY ? -INFINITY : z, lsum);
           if (r == 0) L.part_bad[slot] = isbad;
@@ -361,115 +326,118 @@ __global__ void __launch_bounds__(MmaShape<D, MT>::kThreads, 1) tree_attn_mma_ke
       }
     }
     if (ct == 0) wk.tell(s_start, blockIdx.x);
-    bar_sync_n(1, 32 * S::kWarps);  // the states' places are free
+    bar_sync_n(1, 32 * kCons);  // the states' places are free
     if (ct == 0) s_bad = 0;
   }
 }
 
 // ---------------------------------------------------------------- join
 // Rows of pairs whose units were cut: the states of their ranges, in order.
-// Pairs done by one range were stored by it.  WPR warps share a row: one where
-// there are many rows of few states each, eight where few rows have many states
-// (the latency of reading them one after the other is what counts then).  Lane k
-// takes the (M, l) of every 32nd state, so all of them are in flight at once; a
-// warp reads the sums of p v of its states eight at a time.
+// Pairs done by one range were stored by it.  A CTA takes eight rows and CH
+// blocks of 16 head elements; its eight warps are those blocks times a split of
+// the states.  Many rows of few states: all blocks, no split; few rows of many
+// states: one block and eight parts, because then the latency of reading the
+// states one after the other is what counts.  A lane holds four elements of a
+// row, so that a warp's 16-byte reads cover eight rows side by side (the order
+// the states are stored in: the kernels' threads hold a row each).
 constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 8;
 constexpr int kJoinStates = (kAttnCtas + 31) / 32;
 
-template <bool F16, int D, int WPR>
+template <bool F16, int D, int CH>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join_kernel(const __grid_constant__ AttnLaunch L) {
-  constexpr int E = D / 32;  // elements of a lane
-  __shared__ float s_x[WPR > 1 ? kJoinWarps : 1][D];
+  constexpr int kBlocks = D / 16, kSplit = kJoinWarps / CH;
+  __shared__ float s_w[kAttnCtas][kJoinRows], s_max[kJoinWarps][kJoinRows], s_l[kJoinWarps][kJoinRows];
+  __shared__ float4 s_x[kSplit > 1 ? kJoinWarps : 1][32];
   pdl_trigger();
   const TreeAttnParams &p = L.p;
   const int b = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = blockIdx.z * (kJoinWarps / WPR) + warp / WPR, part = warp % WPR;
+  const int r0 = (int)blockIdx.z / (kBlocks / CH) * kJoinRows, r8 = lane & 7, cg = lane >> 3, r = r0 + r8;
   // the first launch releases this one after its own wait: the call's inputs are final
   const SeqView v = seq_view(p.c, p.t, b);
-  if (r >= v.n * p.G) return;
+  const int R = v.n * p.G;
+  if (r0 >= R) return;
   pdl_wait();
   const int4 pair = __ldcg(&L.pairs[b * p.c.Hkv + h]);
   const int g0 = pair.x, n = pair.y;
   if (n < 2) return;
-  const int rt = r / L.rows, rr = r - rt * L.rows;
+  const int rt = r0 / L.rows, rr = r - rt * L.rows;
   // state k is range g0 + k's; only in the first range can the pair be the second cut
   auto slot = [&](int k) { return (size_t)(2 * ((g0 + k) * L.n_rt + rt) + (k == 0 ? pair.z : 0)); };
+  // ---- weights of the states, and the sum
   float2 ml[kJoinStates];
   int bad = 0;
-  float M = -INFINITY;
+  float M = -INFINITY, l = 0.f;
 #pragma unroll
   for (int q = 0; q < kJoinStates; ++q) {
-    const int k = lane + 32 * q;
+    const int k = warp * 4 + cg + 32 * q;
     ml[q] = make_float2(-INFINITY, 0.f);
-    if (k < n) {
+    if (k < n && r < R) {
       ml[q] = __ldcg(&L.part_ml[slot(k) * L.rows + rr]);
       bad |= __ldcg(&L.part_bad[slot(k)]);
     }
+    M = fmaxf(M, ml[q].x);
   }
+  M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
+  M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+  if (cg == 0) s_max[warp][r8] = M;
+  bad = __syncthreads_or(bad);
 #pragma unroll
-  for (int q = 0; q < kJoinStates; ++q) M = fmaxf(M, ml[q].x);
-  M = warp_max(M);
-  bad = __any_sync(0xffffffffu, bad != 0);
-  float l = 0.f, w[kJoinStates];
+  for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_max[w][r8]);
 #pragma unroll
   for (int q = 0; q < kJoinStates; ++q) {
-    w[q] = ml[q].x == -INFINITY ? 1.f : ex2(ml[q].x - M);  // a state without keys holds zeros (or NaN of a NaN query)
-    l += ml[q].y * w[q];
+    const int k = warp * 4 + cg + 32 * q;
+    const float w = ml[q].x == -INFINITY ? 1.f : ex2(ml[q].x - M);  // a state without keys holds zeros (or NaN of a NaN query)
+    l += ml[q].y * w;
+    if (k < n) s_w[k][r8] = w;
   }
+  l += __shfl_xor_sync(0xffffffffu, l, 8);
+  l += __shfl_xor_sync(0xffffffffu, l, 16);
+  if (cg == 0) s_l[warp][r8] = l;
+  __syncthreads();
+  l = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  float x[E];
-#pragma unroll
-  for (int j = 0; j < E; ++j) x[j] = 0.f;
-  const float *base = L.part_o + (size_t)rr * D + lane * E;
-  const size_t pitch = (size_t)L.rows * D;
-#pragma unroll
-  for (int q = 0; q < kJoinStates; ++q) {
-#pragma unroll 1
-    for (int k0 = 32 * q + part; k0 < min(n, 32 * q + 32); k0 += 8 * WPR) {
-      float y[8][E];
+  for (int w = 0; w < kJoinWarps; ++w) l += s_l[w][r8];
+  // ---- sums of p v
+  const int part = warp % kSplit, c4 = ((int)blockIdx.z % (kBlocks / CH) * CH + warp / kSplit) * 4 + cg;
+  const float4 *base = reinterpret_cast<const float4 *>(L.part_o) + (size_t)c4 * L.rows + rr;
+  const size_t pitch = (size_t)(D / 4) * L.rows;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (r < R) {
+    for (int k0 = part; k0 < n; k0 += 8 * kSplit) {
+      float4 y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (k0 + i * WPR < min(n, 32 * q + 32)) load_floats<E>(base + slot(k0 + i * WPR) * pitch, y[i]);
+        if (k0 + i * kSplit < n) y[i] = __ldcg(base + slot(k0 + i * kSplit) * pitch);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float f = __shfl_sync(0xffffffffu, w[q], (k0 + i * WPR) & 31);
-        if (k0 + i * WPR < min(n, 32 * q + 32)) {
-#pragma unroll
-          for (int j = 0; j < E; ++j) x[j] = fmaf(y[i][j], f, x[j]);
+      for (int i = 0; i < 8; ++i)
+        if (k0 + i * kSplit < n) {
+          const float f = s_w[k0 + i * kSplit][r8];
+          x.x = fmaf(y[i].x, f, x.x);
+          x.y = fmaf(y[i].y, f, x.y);
+          x.z = fmaf(y[i].z, f, x.z);
+          x.w = fmaf(y[i].w, f, x.w);
         }
-      }
     }
   }
-  if (WPR > 1) {
-#pragma unroll
-    for (int j = 0; j < E; ++j) s_x[warp % kJoinWarps][lane * E + j] = x[j];
-    __syncthreads();  // one row per CTA: all of its warps are here
+  if (kSplit > 1) {
+    s_x[warp % kJoinWarps][lane] = x;
+    __syncthreads();
     if (part) return;
 #pragma unroll
-    for (int k = 1; k < WPR; ++k)
-#pragma unroll
-      for (int j = 0; j < E; ++j) x[j] += s_x[k][lane * E + j];
+    for (int k = 1; k < kSplit; ++k) {
+      const float4 y = s_x[(warp + k) % kJoinWarps][lane];
+      x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+    }
   }
+  if (r >= R) return;
   const int i = node_of(L, r), head = h * p.G + r - i * p.G;
   const size_t row = v.row0 + i;
   const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
-  uint32_t out[E / 2];
-#pragma unroll
-  for (int j = 0; j < E; j += 2) {
-    float2 y = make_float2(x[j] * inv, x[j + 1] * inv);
-    if (bad) {
-      y.x += unseen<F16>(p, v, i, h, lane * E + j);
-      y.y += unseen<F16>(p, v, i, h, lane * E + j + 1);
-    }
-    out[j / 2] = pack2<F16>(y.x, y.y);
-  }
-  uint32_t *to = reinterpret_cast<uint32_t *>(p.o + 2 * (row * p.o_row + head * p.o_head)) + lane * (E / 2);
-  if (E == 4)
-    *reinterpret_cast<uint2 *>(to) = make_uint2(out[0], out[E / 2 - 1]);
-  else
-    *to = out[0];
-  if (p.lse && lane == 0)
+  char *out = p.o + 2 * (row * p.o_row + head * p.o_head);
+  *reinterpret_cast<uint2 *>(out + 8 * c4) = make_uint2(pack2<F16>(x.x * inv, x.y * inv), pack2<F16>(x.z * inv, x.w * inv));
+  if (bad) add_unseen<F16>(p, v, i, h, out, 4 * c4, 4 * c4 + 4);
+  if (p.lse && c4 == 0)
     p.lse[row * p.H + head] = l == 0.f ? -INFINITY : (M == -INFINITY ? l : (M + log2f(l)) * 0.69314718055994531f);
 }
 
@@ -498,27 +466,26 @@ bool encode_kv(CUtensorMap *map, const CacheParams &c, const char *base, int lay
   return true;
 }
 
-template <bool F16, int D, int MT>
+template <bool F16, int D>
 cudaError_t launch_mma(const AttnLaunch &L, cudaStream_t s) {
-  using S = MmaShape<D, MT>;
-  auto kern = tree_attn_mma_kernel<F16, D, MT>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+  auto kern = tree_attn_mma_kernel<F16, D>;
+  const size_t smem = MmaShape<D>::kSmem;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_chained(kern, dim3(L.n_groups * L.n_rt), dim3(S::kThreads), S::kSmem, s, L);
+  return launch_chained(kern, dim3(L.n_groups * L.n_rt), dim3(kMmaThreads), smem, s, L);
 }
 
 template <bool F16, int D>
 cudaError_t launch_typed(AttnLaunch &L, cudaStream_t s) {
   const int R = L.p.t.max_nodes * L.p.G;
-  cudaError_t e = L.rows >= 128  ? launch_attn_tc(L, s)
-                  : L.rows == 16 ? launch_mma<F16, D, 1>(L, s)
-                                 : launch_mma<F16, D, 2>(L, s);
+  cudaError_t e = L.rows >= 128 ? launch_attn_tc(L, s) : launch_mma<F16, D>(L, s);
   if (e != cudaSuccess) return e;
-  // a warp per row fills the SMs from about 4000 rows on; with fewer, eight share one
+  const int blocks = (R + kJoinRows - 1) / kJoinRows;
+  // CTAs of eight rows fill the SMs from about 4000 rows on
   if ((long long)L.p.t.n_seqs * L.p.c.Hkv * R < 4096)
-    return launch_chained(tree_attn_join_kernel<F16, D, kJoinWarps>, dim3(L.p.t.n_seqs, L.p.c.Hkv, R),
+    return launch_chained(tree_attn_join_kernel<F16, D, 1>, dim3(L.p.t.n_seqs, L.p.c.Hkv, blocks * (D / 16)),
                           dim3(32 * kJoinWarps), 0, s, L);
-  return launch_chained(tree_attn_join_kernel<F16, D, 1>, dim3(L.p.t.n_seqs, L.p.c.Hkv, (R + kJoinWarps - 1) / kJoinWarps),
+  return launch_chained(tree_attn_join_kernel<F16, D, D / 16>, dim3(L.p.t.n_seqs, L.p.c.Hkv, blocks),
                         dim3(32 * kJoinWarps), 0, s, L);
 }
 
@@ -527,7 +494,7 @@ cudaError_t launch_typed(AttnLaunch &L, cudaStream_t s) {
 AttnPlan tree_attn_plan(int max_nodes, int G) {
   AttnPlan a = {};
   const int R = max_nodes * G;
-  a.rows = R <= 16 ? 16 : R <= 32 ? 32 : R <= 128 ? 128 : 256;
+  a.rows = R <= kRows ? kRows : R <= 128 ? 128 : 256;
   a.n_rt = (R + a.rows - 1) / a.rows;
   a.n_groups = kAttnCtas / a.n_rt < 1 ? 1 : kAttnCtas / a.n_rt;
   return a;

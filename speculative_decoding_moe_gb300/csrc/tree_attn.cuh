@@ -17,7 +17,7 @@ struct AttnLaunch {
   uint32_t inv_g;  // ceil(2^16 / G)
   int4 *pairs;        // [n_seqs][kv heads] of each pair: first range, ranges, whether it starts inside that range
   float2 *part_ml;    // [2 CTAs][rows] (M, l) of partial states
-  float *part_o;      // [2 CTAs][rows][D] their sums of p v
+  float *part_o;      // [2 CTAs][D / 4][rows][4] their sums of p v
   int *part_bad;      // [2 CTAs] a tree value that is not finite was left out
 };
 

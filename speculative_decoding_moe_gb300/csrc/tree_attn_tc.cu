@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
       const size_t row = wk.v.row0 + i;
       const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // NaN stays NaN
       char *out = p.o + 2 * (row * p.o_row + head * p.o_head);
-      float *part = L.part_o + ((size_t)slot * L.rows + rr) * D;
+      float4 *part = reinterpret_cast<float4 *>(L.part_o) + (size_t)slot * (D / 4) * L.rows + rr;
 #pragma unroll 1
       for (int q = c0; q < c1 && ok; q += 32) {
         float o[32];
@@ -593,9 +593,9 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
 #pragma unroll
           for (int e = 0; e < 4; ++e) to[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         } else {
-          float4 *to = reinterpret_cast<float4 *>(part + q);
+          float4 *to = part + (size_t)(q / 4) * L.rows;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) to[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int e = 0; e < 8; ++e) to[(size_t)e * L.rows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
       if (r < R && ok && c0 == 0) {
