@@ -24,8 +24,9 @@ constexpr int kCols = 8;                              // columns of a thread
 constexpr int kSlice = kLogitThreads * kCols;
 constexpr int kAhead = 4;                             // listed columns of a lane in flight
 constexpr uint32_t kPromptBit = 0x80000000u;          // the token is in the prompt
-constexpr uint32_t kTreeBit = 0x40000000u;            // some drafted node holds the token
-constexpr uint32_t kCountMask = kTreeBit - 1u;        // how often it was generated
+constexpr uint32_t kTreeBit = 0x40000000u;            // some drafted node holds the token:
+constexpr int kNodeShift = 24;                        // the first such node, in 6 bits
+constexpr uint32_t kCountMask = (1u << kNodeShift) - 1u;  // how often the history generated it
 
 // Eight columns of a row: consecutive ones of a 16-byte aligned row (VEC), or
 // one in kLogitThreads each, so that a warp's 2- or 4-byte accesses are
@@ -132,7 +133,8 @@ __device__ __forceinline__ float round_bf16(float x) { return __bfloat162float(_
 
 // The largest of a warp's values (the lowest column among equals) into *key;
 // col() is only asked of lanes that hold it.  A lane without a value above -inf
-// passes best = -inf.
+// passes best = -inf.  (Leaving every thread's best in shared memory and asking
+// the row's winner alone took more for its barriers than it saved.)
 template <class Col>
 __device__ __forceinline__ void warp_argmax(unsigned long long *key, float best, Col col) {
   const uint32_t k = best == -INFINITY ? 0u : float_key(best);
@@ -149,12 +151,13 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   __shared__ __align__(16) uint32_t s_cnt[kSlice];
   __shared__ uint16_t s_list[kSlice];
   __shared__ unsigned long long s_key[DFV_MAX_TREE];
-  __shared__ int s_tok[DFV_MAX_TREE];
+  __shared__ int s_tok[DFV_MAX_TREE];                  // drafted tokens, from the slice's start
+  __shared__ uint64_t s_same[DFV_MAX_TREE];            // nodes with the token of this (first) one
   __shared__ int s_n;
   pdl_trigger();
   pdl_wait();
-  const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.y;
-  const int v0 = blockIdx.x * kSlice, left = min(kSlice, p.V - v0);  // columns of the slice
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
+  const int v0 = blockIdx.y * kSlice, left = min(kSlice, p.V - v0);  // columns of the slice
   const int r0 = p.t.row_off[b], r1 = p.t.row_off[b + 1], n = r1 - r0;
   if (r0 < 0 || r1 > p.t.n_rows || n > p.t.max_nodes || n <= (int)blockIdx.z) return;
   const bool pen = p.r.repetition || p.r.frequency || p.r.presence;
@@ -170,21 +173,23 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   for (int j = 0; j < kCols; ++j) inside |= (column<VEC>(j) < left ? 1u : 0u) << j;
   Raw<F32> x[kRowsAhead];
   uint32_t ok[kRowsAhead];
-  auto fetch = [&](int q, int i) {
-    ok[q] = inside;  // past the slice's end nothing is loaded and nothing may win
-    if (i >= n) return;
-    load_row<F32, VEC>(p.x + kBytes * ((r0 + i) * p.row + v0), left, x[q]);
+  auto load = [&](int i, Raw<F32> &x, uint32_t &ok) {
+    ok = inside;  // past the slice's end nothing is loaded and nothing may win
+    load_row<F32, VEC>(p.x + kBytes * ((r0 + i) * p.row + v0), left, x);
     if (p.r.allowed) {
       const uint32_t *words = p.r.allowed + (r0 + i) * p.r.allowed_row + v0 / 32;
       if (VEC) {
-        if (inside) ok[q] &= __ldg(reinterpret_cast<const uint8_t *>(words) + tid);
+        if (inside) ok &= __ldg(reinterpret_cast<const uint8_t *>(words) + tid);
       } else {
 #pragma unroll
         for (int j = 0; j < kCols; ++j)
           if (column<VEC>(j) < left && !(__ldg(words + (column<VEC>(j) >> 5)) >> (column<VEC>(j) & 31) & 1u))
-            ok[q] &= ~(1u << j);
+            ok &= ~(1u << j);
       }
     }
+  };
+  auto fetch = [&](int q, int i) {
+    if (i < n) load(i, x[q], ok[q]);
   };
 #pragma unroll
   for (int q = 0; q < kRowsAhead; ++q) fetch(q, blockIdx.z + q * gridDim.z);
@@ -227,7 +232,12 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
       if (tid < head) count(h[tid], tid);
       if (tid >= 32 && tid - 32 < len - rest) count(h[rest + tid - 32], rest + tid - 32);
     }
-    if (tid < n && (unsigned)s_tok[tid] < (unsigned)left) atomicOr(&s_cnt[s_tok[tid]], kTreeBit);
+    if (tid < n && (unsigned)s_tok[tid] < (unsigned)left) {
+      uint64_t same = 0ull;
+      for (int j = 0; j < n; ++j) same |= (uint64_t)(s_tok[j] == s_tok[tid]) << j;
+      s_same[tid] = same;
+      if (__ffsll((long long)same) - 1 == tid) atomicOr(&s_cnt[s_tok[tid]], kTreeBit | (uint32_t)tid << kNodeShift);
+    }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kCols; ++j)
@@ -251,33 +261,36 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   // ---- all rows, dense: bias and mask
   uint32_t keep[Raw<F32>::kWords];
   spread<F32>(listed, keep);
+  // bias and mask of a row; afterwards x is what is stored, y what may win
+  auto apply = [&](Raw<F32> &x, uint32_t ok, Raw<F32> &y) {
+    if (bias) {
+#pragma unroll
+      for (int j = 0; j < Raw<F32>::kWords; ++j) {
+        if (F32)
+          y.w[j] = __float_as_uint(__fadd_rn(x.at(j), bv[j]));
+        else
+          y.w[j] = pack2<false>(__fadd_rn(x.at(2 * j), bv[2 * j % kCols]),
+                                __fadd_rn(x.at(2 * j + 1), bv[(2 * j + 1) % kCols]));
+        x.w[j] = (x.w[j] & keep[j]) | (y.w[j] & ~keep[j]);
+      }
+    }
+    // not allowed: -inf; listed: stored as they came, out of the argmax
+    uint32_t okm[Raw<F32>::kWords];
+    spread<F32>(ok, okm);
+#pragma unroll
+    for (int j = 0; j < Raw<F32>::kWords; ++j) {
+      const uint32_t may = okm[j] & ~keep[j];
+      y.w[j] = (x.w[j] & may) | (Raw<F32>::kNegInf & ~may);
+      x.w[j] = (y.w[j] & ~keep[j]) | (x.w[j] & keep[j]);
+    }
+  };
   for (int i0 = blockIdx.z; i0 < n; i0 += kRowsAhead * gridDim.z) {
 #pragma unroll
     for (int q = 0; q < kRowsAhead; ++q) {
       const int i = i0 + q * gridDim.z;
       if (i >= n) break;
-      if (bias) {
-        Raw<F32> y;
-#pragma unroll
-        for (int j = 0; j < Raw<F32>::kWords; ++j) {
-          if (F32)
-            y.w[j] = __float_as_uint(__fadd_rn(x[q].at(j), bv[j]));
-          else
-            y.w[j] = pack2<false>(__fadd_rn(x[q].at(2 * j), bv[2 * j % kCols]),
-                                  __fadd_rn(x[q].at(2 * j + 1), bv[(2 * j + 1) % kCols]));
-          x[q].w[j] = (x[q].w[j] & keep[j]) | (y.w[j] & ~keep[j]);
-        }
-      }
-      // not allowed: -inf; listed: stored as they came, out of the argmax
-      uint32_t okm[Raw<F32>::kWords];
-      spread<F32>(ok[q], okm);
       Raw<F32> y;
-#pragma unroll
-      for (int j = 0; j < Raw<F32>::kWords; ++j) {
-        const uint32_t may = okm[j] & ~keep[j];
-        y.w[j] = (x[q].w[j] & may) | (Raw<F32>::kNegInf & ~may);
-        x[q].w[j] = (y.w[j] & ~keep[j]) | (x[q].w[j] & keep[j]);
-      }
+      apply(x[q], ok[q], y);
       if (p.out) store_row<F32, VEC>(p.out + kBytes * ((r0 + i) * p.out_row + v0), left, x[q]);
       fetch(q, i + kRowsAhead * gridDim.z);
       if (p.argmax) {
@@ -299,42 +312,41 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
     const int m = s_n;
     const float rep = p.r.repetition ? p.r.repetition[b] : 1.f, freq = p.r.frequency ? p.r.frequency[b] : 0.f,
                 pres = p.r.presence ? p.r.presence[b] : 0.f;
-    // an item is 32 listed columns of one row; a warp has kAhead of them in flight
+    // a warp takes a row, or several a row with fewer rows than warps; kAhead
+    // columns of a lane are in flight
     constexpr int kW = kLogitThreads / 32;
-    const int chunks = (m + 31) / 32, rows = (n - (int)blockIdx.z + (int)gridDim.z - 1) / (int)gridDim.z;
-    for (int u0 = tid >> 5; u0 < rows * chunks; u0 += kW * kAhead) {
-      int c[kAhead], row[kAhead];
-      float z[kAhead], add[kAhead];
-      uint32_t may[kAhead];
+    const int rows = (n - (int)blockIdx.z + (int)gridDim.z - 1) / (int)gridDim.z;  // of this CTA
+    const int share = rows >= kW ? 1 : kW / rows;
+    for (int u = warp; u < rows * share; u += kW) {
+      const int i = blockIdx.z + (u / share) * gridDim.z, part = u % share;
+      const char *from = p.x + kBytes * ((r0 + i) * p.row + v0);
+      char *to = p.out + kBytes * ((r0 + i) * p.out_row + v0);
+      const uint32_t *words = p.r.allowed ? p.r.allowed + (r0 + i) * p.r.allowed_row + v0 / 32 : nullptr;
+      const uint64_t mask = row_mask(p.t, r0, i);
+      float best = -INFINITY;
+      int bc = 0x7fffffff;
+      for (int k0 = part * 32 * kAhead + lane; k0 < m; k0 += share * 32 * kAhead) {
+        int c[kAhead];
+        float z[kAhead], add[kAhead];
+        uint32_t may[kAhead];
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q) {
-        const int u = u0 + q * kW, k = (u % chunks) * 32 + lane;
-        row[q] = blockIdx.z + (u / chunks) * gridDim.z;
-        c[q] = u < rows * chunks && k < m ? (int)s_list[k] : -1;
-        if (c[q] >= 0) {
-          const char *from = p.x + kBytes * ((r0 + row[q]) * p.row + v0 + c[q]);
-          z[q] = F32 ? *reinterpret_cast<const float *>(from)
-                     : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(from) << 16);
+        for (int q = 0; q < kAhead; ++q) {
+          c[q] = k0 + 32 * q < m ? (int)s_list[k0 + 32 * q] : -1;
+          if (c[q] < 0) continue;
+          z[q] = F32 ? *reinterpret_cast<const float *>(from + 4 * c[q])
+                     : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(from + 2 * c[q]) << 16);
           add[q] = bias ? bias[c[q]] : 0.f;
-          may[q] = 1u;
-          if (p.r.allowed)
-            may[q] = p.r.allowed[(r0 + row[q]) * p.r.allowed_row + ((v0 + c[q]) >> 5)] >> ((v0 + c[q]) & 31) & 1u;
+          may[q] = words ? words[c[q] >> 5] >> (c[q] & 31) & 1u : 1u;
         }
-      }
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q) {
-        if (u0 + q * kW >= rows * chunks) break;
-        float y = -INFINITY;
-        if (c[q] >= 0) {
+        for (int q = 0; q < kAhead; ++q) {
+          if (c[q] < 0) continue;
           const uint32_t w = s_cnt[c[q]];
           uint32_t cnt = w & kCountMask;
-          if (w & kTreeBit) {
-            const uint64_t mask = row_mask(p.t, r0, row[q]);
-            for (int j = 0; j < n; ++j) cnt += s_tok[j] == c[q] && (mask >> j & 1);
-          }
+          if (w & kTreeBit) cnt += __popcll(s_same[w >> kNodeShift & 63u] & mask);
           // steps 1-5 of dfv_logits_process, every product, quotient and
           // difference rounded on its own (no contraction)
-          y = z[q];
+          float y = z[q];
           if (p.r.repetition && (cnt || (w & kPromptBit))) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
           if (p.r.frequency) y = __fsub_rn(y, __fmul_rn(freq, (float)cnt));
           if (p.r.presence && cnt) y = __fsub_rn(y, pres);
@@ -342,15 +354,18 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
           if (!may[q]) y = -INFINITY;
           if (!F32) y = round_bf16(y);
           if (p.out) {
-            char *to = p.out + kBytes * ((r0 + row[q]) * p.out_row + v0 + c[q]);
             if (F32)
-              *reinterpret_cast<float *>(to) = y;
+              *reinterpret_cast<float *>(to + 4 * c[q]) = y;
             else
-              *reinterpret_cast<uint16_t *>(to) = f32_to_bf16_bits(y);
+              *reinterpret_cast<uint16_t *>(to + 2 * c[q]) = f32_to_bf16_bits(y);
+          }
+          if (y > best || (y == best && c[q] < bc)) {  // the list is in no order
+            best = y;
+            bc = c[q];
           }
         }
-        if (p.argmax) warp_argmax(&s_key[row[q]], y, [&]() { return v0 + c[q]; });
       }
+      if (p.argmax) warp_argmax(&s_key[i], best, [&]() { return v0 + bc; });
     }
   }
 
@@ -361,10 +376,10 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   if (tid < DFV_MAX_TREE && i < n) {
     const int row = r0 + i;
     unsigned long long k = s_key[i];
-    if (gridDim.x > 1) {
+    if (gridDim.y > 1) {
       if (k) atomicMax(&p.key[row], k);
       __threadfence();
-      if (atomicAdd(&p.ticket[row], 1u) != gridDim.x - 1) return;
+      if (atomicAdd(&p.ticket[row], 1u) != gridDim.y - 1) return;
       __threadfence();
       k = atomicExch(&p.key[row], 0ull);
       p.ticket[row] = 0u;
@@ -381,7 +396,9 @@ cudaError_t launch_logits(const LogitsParams &p, cudaStream_t s) {
   // while those would not give every SM three
   int z = (456 + slices * p.t.n_seqs - 1) / (slices * p.t.n_seqs);
   z = z < 1 ? 1 : z > p.t.max_nodes ? p.t.max_nodes : z;
-  const dim3 grid(slices, p.t.n_seqs, z);
+  // the first slices first: in most vocabularies the low ids are the frequent
+  // tokens, so those CTAs have the longest lists
+  const dim3 grid(p.t.n_seqs, slices, z);
   const int esz = p.f32 ? 4 : 2;
   const bool vec = p.V % kCols == 0 && ((uintptr_t)p.x | (uintptr_t)p.out) % 16 == 0 && p.row * esz % 16 == 0 &&
                    (!p.out || p.out_row * esz % 16 == 0);

@@ -285,6 +285,8 @@ int dfv_logits_process(const void *logits, int64_t row, int dtype, int V, const 
   if (pen && !tokens) return api_fail(DFV_ERR_INVALID_ARG, "penalties need the drafted tokens");
   if (pen && rules->hist && (!rules->hist_len || rules->hist_row < 0))
     return api_fail(DFV_ERR_INVALID_ARG, "hist needs hist_len and a non-negative hist_row");
+  if (pen && rules->hist && rules->hist_row >= (1 << 24))
+    return api_fail(DFV_ERR_UNSUPPORTED, "hist_row %lld: at most 2^24 - 1 tokens of history", (long long)rules->hist_row);
   if (rules->bias && rules->bias_row != 0 && rules->bias_row < V)
     return api_fail(DFV_ERR_INVALID_ARG, "bias_row must be 0 or at least V");
   if (rules->allowed && rules->allowed_row != 0 && rules->allowed_row < (V + 31) / 32)

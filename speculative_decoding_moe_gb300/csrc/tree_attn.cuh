@@ -178,22 +178,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
-template <int E>
-__device__ __forceinline__ void load_floats(const float *p, float (&x)[E]) {
-  if (E == 4) {
-    const float4 v = __ldcg(reinterpret_cast<const float4 *>(p));
-    x[0] = v.x; x[1] = v.y; x[E - 2] = v.z; x[E - 1] = v.w;
-  } else {
-    const float2 v = __ldcg(reinterpret_cast<const float2 *>(p));
-    x[0] = v.x; x[E - 1] = v.y;
-  }
-}
-
 // A page id as read from the table; one out of range is read as page 0.
 __device__ __forceinline__ int checked_page(const CacheParams &c, int pg) {
   if ((unsigned)pg < (unsigned)c.n_pages) return pg;

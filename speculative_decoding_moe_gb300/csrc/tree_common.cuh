@@ -139,6 +139,12 @@ __device__ __forceinline__ uint64_t row_mask(const TreeParams &t, int row0, int 
   return t.mask ? t.mask[row0 + i] : (i >= 63 ? ~0ull : (2ull << i) - 1ull);
 }
 
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
 template <bool F16>
 __device__ __forceinline__ float2 unpack2(uint32_t v) {
   if (F16) return __half22float2(*reinterpret_cast<const __half2 *>(&v));

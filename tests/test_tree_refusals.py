@@ -156,7 +156,7 @@ def test_attention_head_sizes(dfv, dim):
     (dict(x=0), INVALID), (dict(x=0x2001), INVALID), (dict(out=0x4001), INVALID), (dict(dtype=0, x=0x2002), INVALID),
     (dict(out=None, best=None), INVALID), (dict(row=999), INVALID), (dict(out_row=10), INVALID),
     (dict(out=0x2000, out_row=1200), INVALID), (dict(tokens=None), INVALID), (dict(rules=dict(hist_len=None)), INVALID),
-    (dict(rules=dict(hist_row=-1)), INVALID), (dict(rules=dict(bias=0x100, bias_row=999)), INVALID),
+    (dict(rules=dict(hist_row=-1)), INVALID), (dict(rules=dict(hist_row=1 << 24)), UNSUPPORTED), (dict(rules=dict(bias=0x100, bias_row=999)), INVALID),
     (dict(rules=dict(allowed=0x100, allowed_row=31)), INVALID), (dict(ws=None), WORKSPACE), (dict(ws=0x9080), WORKSPACE),
     (dict(n=600), WORKSPACE)])
 def test_logits(dfv, kw, status):
