@@ -13,7 +13,8 @@
 //           for 256 rows
 // M is only raised, and O only rescaled, when a row's maximum grew by more than
 // 2^8: p then stays below 2^8 (fp16: 2^14 with its offset), the sums are exact
-// in the same M, and almost every tile skips the read and write of O.
+// in the same M, and almost every tile needs one pass over its scores and no read
+// or write of O.
 //
 // Warps 0-3 and 4-7 are the two warpgroups, warps 8 and 10 stream K and V tiles
 // with TMA into one ring in the order the MMAs use them (half of each tile's boxes
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
   constexpr int kHalves = D / 64;
   extern __shared__ __align__(16) unsigned char sm_raw[];
   unsigned char *sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) unsigned long long s_full[S::kSlots], s_empty[S::kSlots], s_sfull[2], s_pready[2][2], s_odone[2],
+  __shared__ __align__(8) unsigned long long s_full[S::kSlots], s_empty[S::kSlots], s_sfull[2], s_pready[2], s_odone[2],
       s_qready, s_drain;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
@@ -231,8 +232,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(smem_u32(&s_sfull[w]), 1);
-      mbar_init(smem_u32(&s_pready[w][0]), 128);
-      mbar_init(smem_u32(&s_pready[w][1]), 128);
+      mbar_init(smem_u32(&s_pready[w]), 128);
       mbar_init(smem_u32(&s_odone[w]), 1);
     }
     mbar_init(smem_u32(&s_qready), 256);
@@ -334,16 +334,13 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
       };
       auto pv = [&](int w, bool first, bool last) {
         const uint32_t vb = ring + (uint32_t)st * S::kTile;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_pready[w]), np[w] & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+        if (!ok) return;
+        tc_fence_after();
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {  // each half of P as it is ready
-          ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_pready[w][hf]), np[w] & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-          if (!ok) return;
-          tc_fence_after();
-#pragma unroll
-          for (int ks = hf * 4; ks < hf * 4 + 4; ++ks)
-            tc_mma_ts(tmem + 256u + (uint32_t)w * 128u, tmem + (uint32_t)w * 128u + (uint32_t)ks * 8u,
-                      sdesc_mn128(vb + (uint32_t)ks * 2048u), iv, (first && ks == 0) ? 0u : 1u);
-        }
+        for (int ks = 0; ks < kTKeys / 16; ++ks)
+          tc_mma_ts(tmem + 256u + (uint32_t)w * 128u, tmem + (uint32_t)w * 128u + (uint32_t)ks * 8u,
+                    sdesc_mn128(vb + (uint32_t)ks * 2048u), iv, (first && ks == 0) ? 0u : 1u);
         ++np[w];
         if (last) tc_commit_elect(smem_u32(&s_odone[w]));
       };
@@ -465,45 +462,6 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
         const int k0 = (wk.t0 + j) * kTKeys, j0 = k0 - wk.v.len;  // node number of the tile's first key
         const bool special = j0 + kTKeys > 0;  // tree nodes or keys past the end in the tile
         if (special) mask_tile(t_s, j0, mask);
-        // quarters of the scores in two buffers, each read while the other is
-        // used: last to first for the maximum, which leaves the first two in
-        // registers, then first to last for p
-        float s0[32], s1[32];
-        float mx = -INFINITY;
-        tmem_ld32(t_s + 96, s1);
-        tmem_wait_ld32(s1);
-        tmem_ld32(t_s + 64, s0);
-        mx = max32(s1, mx);
-        tmem_wait_ld32(s0);
-        tmem_ld32(t_s + 32, s1);
-        mx = max32(s0, mx);
-        tmem_wait_ld32(s1);
-        tmem_ld32(t_s, s0);
-        mx = max32(s1, mx);
-        tmem_wait_ld32(s0);
-        mx = max32(s0, mx);
-        mx = fmaxf(mx, m);
-        if (!started) {
-          m = mx;
-        } else if (__any_sync(0xffffffffu, (mx - m) * c > 8.f)) {
-          // the last product into O is complete: it was issued before these
-          // scores, and their barrier follows all that was issued before it
-          const float f = m == -INFINITY ? 0.f : ex2((m - mx) * c);
-          m = mx;
-          l *= f;
-#pragma unroll 1
-          for (int q = 0; q < D; q += 16) {
-            float o[16];
-            tmem_ld16(t_o + q, o);
-            uint32_t x[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(o[e] * f);
-            tmem_st16(t_o + q, x);
-          }
-          tmem_wait_st();
-        }
-        started = true;
-        const float z = (m == -INFINITY ? 0.f : m * c) - kBias;
         if (special && (!DUAL || w == 0)) {
           // this tile's V before it is multiplied
           const unsigned it = items + (unsigned)(j + (j + LA < n ? j + LA : n));
@@ -513,28 +471,57 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
           clean_row<F16, D>(s_ring + (size_t)(it % S::kSlots) * S::kTile, wt, j0 + wt, wk.nodes, &s_bad);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        float2 l2 = make_float2(0.f, 0.f);
-        uint32_t x[16];
-        exp32<F16>(s0, c, z, x, l2);
-        tmem_st16(t_s, x);
-        tmem_ld32(t_s + 64, s0);
-        exp32<F16>(s1, c, z, x, l2);
-        tmem_st16(t_s + 16, x);
-        // the first half of P may be multiplied
-        tmem_wait_st();
-        tmem_wait_ld32(s0);
-        tc_fence_before();
-        mbar_arrive(smem_u32(&s_pready[w][0]));
-        tmem_ld32(t_s + 96, s1);
-        exp32<F16>(s0, c, z, x, l2);
-        tmem_st16(t_s + 32, x);
-        tmem_wait_ld32(s1);
-        exp32<F16>(s1, c, z, x, l2);
-        tmem_st16(t_s + 48, x);
+        // One pass with the M so far: p and the new maximum together, a quarter
+        // of the scores read while the one before is used.  Only when some row's
+        // maximum grew too far is O rescaled and the pass made again (the first
+        // tile's always is).
+        uint32_t x[64];
+        float2 l2;
+        for (;;) {
+          const float z = (m == -INFINITY ? 0.f : m * c) - kBias;
+          float s0[32], s1[32], mx = m;
+          l2 = make_float2(0.f, 0.f);
+          tmem_ld32(t_s, s0);
+          tmem_wait_ld32(s0);
+          tmem_ld32(t_s + 32, s1);
+          mx = max32(s0, mx);
+          exp32<F16>(s0, c, z, x, l2);
+          tmem_wait_ld32(s1);
+          tmem_ld32(t_s + 64, s0);
+          mx = max32(s1, mx);
+          exp32<F16>(s1, c, z, x + 16, l2);
+          tmem_wait_ld32(s0);
+          tmem_ld32(t_s + 96, s1);
+          mx = max32(s0, mx);
+          exp32<F16>(s0, c, z, x + 32, l2);
+          tmem_wait_ld32(s1);
+          mx = max32(s1, mx);
+          exp32<F16>(s1, c, z, x + 48, l2);
+          if (!__any_sync(0xffffffffu, (mx - m) * c > 8.f)) break;
+          if (started) {
+            // the last product into O is complete: it was issued before these
+            // scores, and their barrier follows all that was issued before it
+            const float f = m == -INFINITY ? 0.f : ex2((m - mx) * c);
+            l *= f;
+#pragma unroll 1
+            for (int q = 0; q < D; q += 16) {
+              float o[16];
+              tmem_ld16(t_o + q, o);
+              uint32_t y[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(o[e] * f);
+              tmem_st16(t_o + q, y);
+            }
+          }
+          m = mx;
+        }
+        started = true;
         l += l2.x + l2.y;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_st16(t_s + 16 * q, x + 16 * q);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(smem_u32(&s_pready[w][1]));
+        mbar_arrive(smem_u32(&s_pready[w]));
       }
       items += 2u * (unsigned)n;
       // ---- output: the last product of this warpgroup, then (SINGLE) both states
