@@ -64,8 +64,13 @@ struct SchedStart {
 __device__ __forceinline__ int ranges_of(long long U, int n_groups) {
   return U >= n_groups ? n_groups : U > 0 ? (int)U : 1;
 }
-__device__ __forceinline__ long long group_start(int g, long long U, int G) { return g * U / G; }
-__device__ __forceinline__ int group_of(long long u, long long U, int G) { return (int)(((u + 1) * G - 1) / U); }
+// (32-bit divisions while the products fit: a 64-bit one takes a few hundred cycles)
+__device__ __forceinline__ long long group_start(int g, long long U, int G) {
+  return U < (1 << 24) ? (long long)((uint32_t)g * (uint32_t)U / (uint32_t)G) : g * U / G;
+}
+__device__ __forceinline__ int group_of(long long u, long long U, int G) {
+  return U < (1 << 24) ? (int)((((uint32_t)u + 1u) * (uint32_t)G - 1u) / (uint32_t)U) : (int)(((u + 1) * G - 1) / U);
+}
 
 template <int KT>
 __device__ __forceinline__ long long seq_units(const AttnLaunch &L, int b) {
@@ -105,7 +110,7 @@ __device__ __forceinline__ void sched_start(const AttnLaunch &L, int block, long
   if (u0 < u1 && at <= u0 && u0 < at + sum) {
     long long base = at;
     for (int b = b0; b < b1; ++b) {
-      const long long c = seq_units<KT>(L, b);
+      const long long c = per == 1 ? sum : seq_units<KT>(L, b);
       if (base <= u0 && u0 < base + c) {
         out->u0 = u0;
         out->u1 = u1;

@@ -95,24 +95,24 @@ struct SeqView {
   int row0, n, s, len;
 };
 __device__ __forceinline__ SeqView seq_view(const CacheParams &c, const TreeParams &t, int b) {
+  // the loads first: one round trip when the sequences are not given by index
+  const int s = t.seq ? t.seq[b] : b;
+  const bool known = (unsigned)s < (unsigned)c.max_seqs;
+  const int len = known ? c.lens[s] : 0, r0 = t.row_off[b], r1 = t.row_off[b + 1];
   SeqView v;
-  v.row0 = t.row_off[b];
-  const int r1 = t.row_off[b + 1];
-  v.s = t.seq ? t.seq[b] : b;
-  v.len = 0;
-  v.n = r1 - v.row0;
-  if (v.row0 < 0 || r1 > t.n_rows || v.n < 0 || v.n > t.max_nodes) {
+  v.row0 = r0;
+  v.n = r1 - r0;
+  v.s = s;
+  v.len = len;
+  if (r0 < 0 || r1 > t.n_rows || r1 < r0 || v.n > t.max_nodes) {
     flag_err(c.err, DFV_KVERR_LEN);
     v.n = 0;
     v.row0 = 0;
   }
-  if (v.s < 0 || v.s >= c.max_seqs) {
+  if (!known) {
     flag_err(c.err, DFV_KVERR_SEQ);
     v.s = -1;
-    return v;
-  }
-  v.len = c.lens[v.s];
-  if (v.len < 0 || (long long)v.len + v.n > ((long long)c.max_pages << c.page_shift)) {
+  } else if (len < 0 || (long long)len + v.n > ((long long)c.max_pages << c.page_shift)) {
     flag_err(c.err, DFV_KVERR_LEN);
     v.s = -1;
     v.len = 0;
