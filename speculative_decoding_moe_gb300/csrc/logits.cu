@@ -173,13 +173,16 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   for (int j = 0; j < kCols; ++j) inside |= (column<VEC>(j) < left ? 1u : 0u) << j;
   Raw<F32> x[kRowsAhead];
   uint32_t ok[kRowsAhead];
+  // nothing here waits for what it loads: ok is only combined with `inside` (past
+  // the slice's end nothing is loaded and nothing may win) when the row is used
+  const int byte = min(tid, max(left - 1, 0) / kCols);
   auto load = [&](int i, Raw<F32> &x, uint32_t &ok) {
-    ok = inside;  // past the slice's end nothing is loaded and nothing may win
     load_row<F32, VEC>(p.x + kBytes * ((r0 + i) * p.row + v0), left, x);
+    ok = 0xffu;
     if (p.r.allowed) {
       const uint32_t *words = p.r.allowed + (r0 + i) * p.r.allowed_row + v0 / 32;
       if (VEC) {
-        if (inside) ok &= __ldg(reinterpret_cast<const uint8_t *>(words) + tid);
+        ok = __ldg(reinterpret_cast<const uint8_t *>(words) + byte);
       } else {
 #pragma unroll
         for (int j = 0; j < kCols; ++j)
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
       const int i = i0 + q * gridDim.z;
       if (i >= n) break;
       Raw<F32> y;
-      apply(x[q], ok[q], y);
+      apply(x[q], ok[q] & inside, y);
       if (p.out) store_row<F32, VEC>(p.out + kBytes * ((r0 + i) * p.out_row + v0), left, x[q]);
       fetch(q, i + kRowsAhead * gridDim.z);
       if (p.argmax) {
