@@ -329,32 +329,33 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
       float best = -INFINITY;
       int bc = 0x7fffffff;
       for (int k0 = part * 32 * kAhead + lane; k0 < m; k0 += share * 32 * kAhead) {
+        // past the list's end the last column again: loads without a branch, none
+        // of them used before all are issued
         int c[kAhead];
-        float z[kAhead], add[kAhead];
-        uint32_t may[kAhead];
+        uint32_t raw[kAhead], word[kAhead];
+        float add[kAhead];
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
-          c[q] = k0 + 32 * q < m ? (int)s_list[k0 + 32 * q] : -1;
-          if (c[q] < 0) continue;
-          z[q] = F32 ? *reinterpret_cast<const float *>(from + 4 * c[q])
-                     : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(from + 2 * c[q]) << 16);
+          c[q] = s_list[min(k0 + 32 * q, m - 1)];
+          raw[q] = F32 ? *reinterpret_cast<const uint32_t *>(from + 4 * c[q])
+                       : (uint32_t)*reinterpret_cast<const uint16_t *>(from + 2 * c[q]);
           add[q] = bias ? bias[c[q]] : 0.f;
-          may[q] = words ? words[c[q] >> 5] >> (c[q] & 31) & 1u : 1u;
+          word[q] = words ? words[c[q] >> 5] : 0xffffffffu;
         }
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
-          if (c[q] < 0) continue;
+          if (k0 + 32 * q >= m) continue;
           const uint32_t w = s_cnt[c[q]];
           uint32_t cnt = w & kCountMask;
           if (w & kTreeBit) cnt += __popcll(s_same[w >> kNodeShift & 63u] & mask);
           // steps 1-5 of dfv_logits_process, every product, quotient and
           // difference rounded on its own (no contraction)
-          float y = z[q];
+          float y = __uint_as_float(F32 ? raw[q] : raw[q] << 16);
           if (p.r.repetition && (cnt || (w & kPromptBit))) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
           if (p.r.frequency) y = __fsub_rn(y, __fmul_rn(freq, (float)cnt));
           if (p.r.presence && cnt) y = __fsub_rn(y, pres);
           if (bias) y = __fadd_rn(y, add[q]);
-          if (!may[q]) y = -INFINITY;
+          if (!(word[q] >> (c[q] & 31) & 1u)) y = -INFINITY;
           if (!F32) y = round_bf16(y);
           if (p.out) {
             if (F32)
