@@ -78,32 +78,52 @@ __device__ __forceinline__ void spread(uint32_t bits, uint32_t (&m)[Raw<F32>::kW
   }
 }
 
+// What is in flight of a row: its columns, one 16-bit column a register where
+// they are loaded one by one, and the mask bits.  Loading waits for nothing that
+// it loads and has no branch on a column; ready() puts the pieces together when
+// the row's turn comes.
 template <bool F32, bool VEC>
-__device__ __forceinline__ void load_row(const char *row, int left, Raw<F32> &x) {
-  constexpr int kBytes = F32 ? 4 : 2;
-  if (VEC) {
-    if (column<VEC>(0) < left) {  // left is a multiple of kCols
+struct Fetched {
+  static constexpr int kWords = VEC || F32 ? Raw<F32>::kWords : kCols;
+  uint32_t w[kWords], bits;
+
+  __device__ __forceinline__ void load(const char *row, const uint32_t *allowed, int left) {
+    constexpr int kBytes = F32 ? 4 : 2;
+    const int tid = threadIdx.x;
+    if (VEC) {
+      if (column<VEC>(0) < left) {  // left is a multiple of kCols
 #pragma unroll
-      for (int q = 0; q < Raw<F32>::kWords; q += 4) {
-        const uint4 a = ldg_stream(row + kBytes * column<VEC>(0) + 4 * q);
-        x.w[q] = a.x; x.w[q + 1] = a.y; x.w[q + 2] = a.z; x.w[q + 3] = a.w;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-      const int c = column<VEC>(j);
-      if (c < left) {
-        if (F32)
-          x.w[j % Raw<F32>::kWords] = reinterpret_cast<const uint32_t *>(row)[c];
-        else {
-          const uint32_t v = reinterpret_cast<const uint16_t *>(row)[c];
-          x.w[j / 2 % Raw<F32>::kWords] = j & 1 ? (x.w[j / 2 % Raw<F32>::kWords] & 0xffffu) | v << 16 : v;
+        for (int q = 0; q < kWords; q += 4) {
+          const uint4 a = ldg_stream(row + kBytes * column<VEC>(0) + 4 * q);
+          w[q] = a.x; w[q + 1] = a.y; w[q + 2] = a.z; w[q + 3] = a.w;
         }
       }
+      bits = allowed ? (uint32_t)__ldg(reinterpret_cast<const uint8_t *>(allowed) + min(tid, (left - 1) / kCols)) : 0xffu;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) {
+        const int c = min(column<VEC>(j), left - 1);
+        w[j % kWords] = F32 ? reinterpret_cast<const uint32_t *>(row)[c] : (uint32_t)reinterpret_cast<const uint16_t *>(row)[c];
+      }
+      // a warp's columns j are one word: lane j holds it
+      bits = allowed ? __ldg(allowed + min((column<VEC>(0) >> 5) + kLogitThreads / 32 * (tid & 7), (left - 1) >> 5)) : 0xffffffffu;
     }
   }
-}
+  __device__ __forceinline__ uint32_t ready(Raw<F32> &x) const {
+    if (VEC || F32) {
+#pragma unroll
+      for (int j = 0; j < Raw<F32>::kWords; ++j) x.w[j] = w[j % kWords];
+    } else {
+#pragma unroll
+      for (int j = 0; j < Raw<F32>::kWords; ++j) x.w[j] = w[2 * j % kWords] | w[(2 * j + 1) % kWords] << 16;
+    }
+    if (VEC) return bits;
+    uint32_t ok = 0u;
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) ok |= (__shfl_sync(0xffffffffu, bits, j) >> (threadIdx.x & 31) & 1u) << j;
+    return ok;
+  }
+};
 
 template <bool F32, bool VEC>
 __device__ __forceinline__ void store_row(char *row, int left, const Raw<F32> &x) {
@@ -163,7 +183,7 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   const bool pen = p.r.repetition || p.r.frequency || p.r.presence;
   const float *bias = p.r.bias ? p.r.bias + b * p.r.bias_row + v0 : nullptr;
   constexpr int kBytes = F32 ? 4 : 2;
-  constexpr int kRowsAhead = F32 ? 2 : 4;  // rows whose logits are in flight
+  constexpr int kRowsAhead = F32 || !VEC ? 2 : 4;  // rows whose logits are in flight: 8 or 16 registers
   if (tid < DFV_MAX_TREE) s_key[tid] = 0ull;
 
   // rows i0, i0 + gridDim.z, ... of the sequence, and their masks: the first ones
@@ -171,28 +191,11 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   uint32_t inside = 0u;
 #pragma unroll
   for (int j = 0; j < kCols; ++j) inside |= (column<VEC>(j) < left ? 1u : 0u) << j;
-  Raw<F32> x[kRowsAhead];
-  uint32_t ok[kRowsAhead];
-  // nothing here waits for what it loads: ok is only combined with `inside` (past
-  // the slice's end nothing is loaded and nothing may win) when the row is used
-  const int byte = min(tid, max(left - 1, 0) / kCols);
-  auto load = [&](int i, Raw<F32> &x, uint32_t &ok) {
-    load_row<F32, VEC>(p.x + kBytes * ((r0 + i) * p.row + v0), left, x);
-    ok = 0xffu;
-    if (p.r.allowed) {
-      const uint32_t *words = p.r.allowed + (r0 + i) * p.r.allowed_row + v0 / 32;
-      if (VEC) {
-        ok = __ldg(reinterpret_cast<const uint8_t *>(words) + byte);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kCols; ++j)
-          if (column<VEC>(j) < left && !(__ldg(words + (column<VEC>(j) >> 5)) >> (column<VEC>(j) & 31) & 1u))
-            ok &= ~(1u << j);
-      }
-    }
-  };
+  Fetched<F32, VEC> ahead[kRowsAhead];
   auto fetch = [&](int q, int i) {
-    if (i < n) load(i, x[q], ok[q]);
+    if (i < n)
+      ahead[q].load(p.x + kBytes * ((r0 + i) * p.row + v0),
+                    p.r.allowed ? p.r.allowed + (r0 + i) * p.r.allowed_row + v0 / 32 : nullptr, left);
   };
 #pragma unroll
   for (int q = 0; q < kRowsAhead; ++q) fetch(q, blockIdx.z + q * gridDim.z);
@@ -292,9 +295,10 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
     for (int q = 0; q < kRowsAhead; ++q) {
       const int i = i0 + q * gridDim.z;
       if (i >= n) break;
-      Raw<F32> y;
-      apply(x[q], ok[q] & inside, y);
-      if (p.out) store_row<F32, VEC>(p.out + kBytes * ((r0 + i) * p.out_row + v0), left, x[q]);
+      Raw<F32> x, y;
+      const uint32_t ok = ahead[q].ready(x) & inside;  // past the slice's end nothing may win
+      apply(x, ok, y);
+      if (p.out) store_row<F32, VEC>(p.out + kBytes * ((r0 + i) * p.out_row + v0), left, x);
       fetch(q, i + kRowsAhead * gridDim.z);
       if (p.argmax) {
         const float best = y.largest();
