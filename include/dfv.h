@@ -421,7 +421,8 @@ int dfv_selftest_mma(int dtype, const void *A, const void *B, float *D, void *st
 int dfv_selftest_tcgen05(const void *A, const void *B, int N, int K, float *D, int32_t *status, void *stream);
 
 /* ------------------------------------------------------------------------
- * Tree verify: what the target's verify step needs around the MoE layers when
+ * Tree verify (arrays of 4-byte elements are 4-byte aligned where no more is
+ * said): what the target's verify step needs around the MoE layers when
  * the draft is a TREE of tokens (a chain is the tree whose mask is NULL):
  * rotary positions and the paged cache, attention of the drafted nodes over
  * that cache, rules on the logits, the greedy walk and the cache's pages.
@@ -474,7 +475,7 @@ typedef struct dfv_kv_cache {
  * .. row_off[b+1] of every [n_rows, ...] argument, one row per node, at most
  * max_nodes (<= 64) and possibly none.  Node 0 is the root (the known token),
  * and a node's number is larger than its parent's.
- *   seq      [n_seqs] int32 cache sequence of each, or NULL: b itself
+ *   seq      [n_seqs] int32 cache sequence of each, all different, or NULL: b itself
  *   row_off  [n_seqs + 1] int32
  *   mask     [n_rows] bit j of row i: node i sees node j of its own tree; its
  *            ancestors and itself for a tree.  NULL: a chain (bits 0..i)

@@ -17,6 +17,7 @@ int launched(cudaError_t e, const char *where) {
   return api_fail(DFV_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
+bool words(const void *p) { return aligned(p, 4); }  // NULL too
 bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s <= ((int64_t)1 << 40); }
 
 int check_cache(const dfv_kv_cache *c) {
@@ -30,8 +31,8 @@ int check_cache(const dfv_kv_cache *c) {
     return api_fail(DFV_ERR_UNSUPPORTED, "head_dim %d: a multiple of 16 up to 256 is needed", c->head_dim);
   if (c->n_kv_heads > 1024 || c->n_layers > 65535)
     return api_fail(DFV_ERR_UNSUPPORTED, "%d kv heads, %d layers (at most 1024 and 65535)", c->n_kv_heads, c->n_layers);
-  if ((int64_t)c->max_pages * c->page_size > 0x7fffffff - DFV_MAX_TREE)
-    return api_fail(DFV_ERR_UNSUPPORTED, "max_pages * page_size exceeds 31 bits");
+  if ((int64_t)c->max_pages * c->page_size > 0x7fff0000)
+    return api_fail(DFV_ERR_UNSUPPORTED, "max_pages * page_size exceeds 2^31 - 2^16 tokens");
   if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16))
     return api_fail(DFV_ERR_INVALID_ARG, "cache k/v NULL or not 16-byte aligned");
   if (!stride_ok(c->stride_layer) || !stride_ok(c->stride_page) || !stride_ok(c->stride_head) ||
@@ -39,7 +40,8 @@ int check_cache(const dfv_kv_cache *c) {
     return api_fail(DFV_ERR_INVALID_ARG, "cache strides must be non-negative multiples of 8 elements");
   if (c->stride_token < c->head_dim)
     return api_fail(DFV_ERR_INVALID_ARG, "stride_token %lld below head_dim", (long long)c->stride_token);
-  if (!c->page_table || !c->lens) return api_fail(DFV_ERR_INVALID_ARG, "page_table/lens NULL");
+  if (!c->page_table || !c->lens || !words(c->page_table) || !words(c->lens) || !words(c->refs) || !words(c->err))
+    return api_fail(DFV_ERR_INVALID_ARG, "page_table/lens NULL, or page_table/lens/refs/err not 4-byte aligned");
   return DFV_OK;
 }
 
@@ -51,7 +53,8 @@ int check_tree(const dfv_tree_batch *t) {
     return api_fail(DFV_ERR_INVALID_ARG, "max_nodes %d outside 1..%d", t->max_nodes, DFV_MAX_TREE);
   if (t->n_rows < 1 || t->n_rows > DFV_MAX_TREE * DFV_MAX_TREE_SEQS)
     return api_fail(DFV_ERR_INVALID_ARG, "n_rows %d outside 1..%d", t->n_rows, DFV_MAX_TREE * DFV_MAX_TREE_SEQS);
-  if (!t->row_off) return api_fail(DFV_ERR_INVALID_ARG, "row_off NULL");
+  if (!t->row_off || !words(t->row_off) || !words(t->seq))
+    return api_fail(DFV_ERR_INVALID_ARG, "row_off NULL, or row_off/seq not 4-byte aligned");
   if (t->mask && !aligned(t->mask, 8)) return api_fail(DFV_ERR_INVALID_ARG, "mask not 8-byte aligned");
   return DFV_OK;
 }
@@ -122,7 +125,7 @@ int check_list(const dfv_kv_cache *c, const int32_t *a, const int32_t *b, int n,
   int st = check_cache(c);
   if (st) return st;
   if (n < 1 || n > DFV_MAX_TREE_SEQS) return api_fail(DFV_ERR_INVALID_ARG, "n %d outside 1..%d", n, DFV_MAX_TREE_SEQS);
-  if (!a || !b) return api_fail(DFV_ERR_INVALID_ARG, "index list NULL");
+  if (!a || !b || !words(a) || !words(b)) return api_fail(DFV_ERR_INVALID_ARG, "index list NULL or not 4-byte aligned");
   if (refs && !c->refs) return api_fail(DFV_ERR_INVALID_ARG, "the cache has no refs");
   return DFV_OK;
 }
@@ -174,7 +177,8 @@ int dfv_rope_append(const dfv_kv_cache *cache, int layer, const dfv_tree_batch *
                     cache->head_dim);
   if (interleaved != 0 && interleaved != 1) return api_fail(DFV_ERR_INVALID_ARG, "interleaved must be 0 or 1");
   if (!std::isfinite(scale)) return api_fail(DFV_ERR_INVALID_ARG, "scale must be finite");
-  if (!turns || !aligned(turns, 8) || !positions) return api_fail(DFV_ERR_INVALID_ARG, "turns/positions NULL");
+  if (!turns || !aligned(turns, 8) || !positions || !words(positions))
+    return api_fail(DFV_ERR_INVALID_ARG, "turns/positions NULL, or not 8- and 4-byte aligned");
   if (!q || !k || !v || !q_out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16))
     return api_fail(DFV_ERR_INVALID_ARG, "q/k/v/q_out NULL or not 16-byte aligned");
   if (!stride_ok(q_row) || !stride_ok(q_head) || !stride_ok(k_row) || !stride_ok(k_head) || !stride_ok(v_row) ||
@@ -237,6 +241,7 @@ int dfv_tree_attention(const dfv_kv_cache *cache, int layer, const dfv_tree_batc
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16))
     return api_fail(DFV_ERR_INVALID_ARG, "q/out NULL or not 16-byte aligned");
   if (q == out) return api_fail(DFV_ERR_INVALID_ARG, "out must not be q");
+  if (!words(opt_lse)) return api_fail(DFV_ERR_INVALID_ARG, "lse not 4-byte aligned");
   if (!stride_ok(q_row) || !stride_ok(q_head) || !stride_ok(o_row) || !stride_ok(o_head))
     return api_fail(DFV_ERR_INVALID_ARG, "row and head strides must be non-negative multiples of 8 elements");
   if ((st = check_ws(ws, ws_bytes, dfv_tree_attention_workspace_size(cache, tree, n_heads)))) return st;
@@ -281,6 +286,10 @@ int dfv_logits_process(const void *logits, int64_t row, int dtype, int V, const 
   if (row < V || (out && out_row < V)) return api_fail(DFV_ERR_INVALID_ARG, "row stride below V");
   if (out == logits && out_row != row) return api_fail(DFV_ERR_INVALID_ARG, "out is logits: the strides must be the same");
   if (!rules) return api_fail(DFV_ERR_INVALID_ARG, "rules is NULL");
+  if (!words(tokens) || !words(argmax) || !words(rules->hist) || !words(rules->hist_len) || !words(rules->prompt_len) ||
+      !words(rules->repetition) || !words(rules->frequency) || !words(rules->presence) || !words(rules->bias) ||
+      !words(rules->allowed))
+    return api_fail(DFV_ERR_INVALID_ARG, "tokens, argmax and the rules' arrays must be 4-byte aligned");
   const bool pen = rules->repetition || rules->frequency || rules->presence;
   if (pen && !tokens) return api_fail(DFV_ERR_INVALID_ARG, "penalties need the drafted tokens");
   if (pen && rules->hist && (!rules->hist_len || rules->hist_row < 0))
@@ -313,7 +322,8 @@ int dfv_accept_tree(const dfv_tree_batch *tree, const int32_t *tokens, const int
                     int64_t path_row, int32_t *tau, void *stream) {
   int st = check_tree(tree);
   if (st) return st;
-  if (!tokens || !target || !path || !tau) return api_fail(DFV_ERR_INVALID_ARG, "tokens/target/path/tau NULL");
+  if (!tokens || !target || !path || !tau || !words(tokens) || !words(target) || !words(path) || !words(tau))
+    return api_fail(DFV_ERR_INVALID_ARG, "tokens/target/path/tau NULL or not 4-byte aligned");
   if (path_row < tree->max_nodes) return api_fail(DFV_ERR_INVALID_ARG, "path_row below max_nodes");
   dfv::AcceptTreeParams p = {};
   p.t = tree_params(tree);
@@ -335,7 +345,8 @@ int dfv_cache_commit(const dfv_kv_cache *cache, const dfv_tree_batch *tree, cons
   int st = check_cache(cache);
   if (st) return st;
   if ((st = check_tree(tree))) return st;
-  if (!path || !tau || !new_lens) return api_fail(DFV_ERR_INVALID_ARG, "path/tau/new_lens NULL");
+  if (!path || !tau || !new_lens || !words(path) || !words(tau) || !words(new_lens))
+    return api_fail(DFV_ERR_INVALID_ARG, "path/tau/new_lens NULL or not 4-byte aligned");
   if (path_row < tree->max_nodes) return api_fail(DFV_ERR_INVALID_ARG, "path_row below max_nodes");
   if ((st = check_ws(ws, ws_bytes, page_ws(cache, nullptr).bytes))) return st;
   dfv::CommitParams p = {};
@@ -353,7 +364,8 @@ int dfv_cache_copy_pages(const dfv_kv_cache *cache, const int32_t *src, const in
   int st = check_cache(cache);
   if (st) return st;
   if (n < 1 || n > (1 << 20)) return api_fail(DFV_ERR_INVALID_ARG, "n %d outside 1..2^20", n);
-  if (!src || !dst) return api_fail(DFV_ERR_INVALID_ARG, "index list NULL");
+  if (!src || !dst || !words(src) || !words(dst))
+    return api_fail(DFV_ERR_INVALID_ARG, "index list NULL or not 4-byte aligned");
   dfv::PagesParams p = {};
   p.c = cache_params(cache);
   p.a = src;

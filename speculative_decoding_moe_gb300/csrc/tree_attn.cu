@@ -356,8 +356,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join_kernel(const _
   // the first launch releases this one after its own wait: the call's inputs are final
   const SeqView v = seq_view(p.c, p.t, b);
   const int R = v.n * p.G;
+  pdl_wait();  // by every CTA: what follows this launch may rely on the first one's end
   if (r0 >= R) return;
-  pdl_wait();
   const int4 pair = __ldcg(&L.pairs[b * p.c.Hkv + h]);
   const int g0 = pair.x, n = pair.y;
   if (n < 2) return;

@@ -38,9 +38,10 @@ BAD_CACHE = [(dict(n_layers=0), INVALID), (dict(n_pages=0), INVALID), (dict(n_kv
              (dict(page_size=512), UNSUPPORTED), (dict(head_dim=72), UNSUPPORTED), (dict(head_dim=272), UNSUPPORTED),
              (dict(k=0), INVALID), (dict(v=0x20008), INVALID), (dict(stride_page=-8), INVALID), (dict(stride_head=4), INVALID),
              (dict(stride_token=64), INVALID), (dict(page_table=0), INVALID), (dict(lens=0), INVALID),
+             (dict(page_table=0x30002), INVALID), (dict(lens=0x40001), INVALID), (dict(refs=0x50002), INVALID), (dict(err=0x60001), INVALID),
              (dict(max_seqs=0), INVALID), (dict(max_pages=1 << 28), UNSUPPORTED), (dict(n_kv_heads=2000), UNSUPPORTED)]
 BAD_TREE = [(dict(n_seqs=0), INVALID), (dict(n_seqs=1025), INVALID), (dict(n_rows=0), INVALID), (dict(max_nodes=0), INVALID),
-            (dict(max_nodes=65), INVALID), (dict(row_off=0), INVALID), (dict(mask=0x80004), INVALID), (dict(n_rows=1 << 20), INVALID)]
+            (dict(max_nodes=65), INVALID), (dict(row_off=0), INVALID), (dict(row_off=0x70002), INVALID), (dict(seq=0x70003), INVALID), (dict(mask=0x80004), INVALID), (dict(n_rows=1 << 20), INVALID)]
 
 
 def rope(dfv, c=None, t=None, **kw):
@@ -99,7 +100,7 @@ def test_trees(dfv, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(layer=-1), INVALID), (dict(layer=4), INVALID), (dict(heads=0), INVALID), (dict(rot=0), UNSUPPORTED),
     (dict(rot=24), UNSUPPORTED), (dict(rot=144), UNSUPPORTED), (dict(inter=2), INVALID), (dict(scale=math.inf), INVALID),
-    (dict(scale=math.nan), INVALID), (dict(turns=0), INVALID), (dict(turns=0x1004), INVALID), (dict(pos=0), INVALID),
+    (dict(scale=math.nan), INVALID), (dict(turns=0), INVALID), (dict(turns=0x1004), INVALID), (dict(pos=0), INVALID), (dict(pos=0x5002), INVALID),
     (dict(q=0), INVALID), (dict(k=0x3002), INVALID), (dict(v=0), INVALID), (dict(o=0), INVALID), (dict(qr=-8), INVALID),
     (dict(kh=12), INVALID), (dict(vr=4), INVALID), (dict(orow=1), INVALID), (dict(o=0x2000, orow=8192), INVALID)])
 def test_rope(dfv, kw, status):
@@ -138,7 +139,7 @@ def test_rope_table_values(dfv):
 @pytest.mark.parametrize("kw,status", [
     (dict(layer=4), INVALID), (dict(heads=30), INVALID), (dict(heads=0), INVALID), (dict(heads=68), UNSUPPORTED),
     (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=math.nan), INVALID), (dict(q=0), INVALID),
-    (dict(q=0x2004), INVALID), (dict(o=0), INVALID), (dict(o=0x2000), INVALID), (dict(qr=3), INVALID), (dict(oh=-8), INVALID),
+    (dict(q=0x2004), INVALID), (dict(o=0), INVALID), (dict(o=0x2000), INVALID), (dict(qr=3), INVALID), (dict(oh=-8), INVALID), (dict(lse=0x7002), INVALID),
     (dict(ws=0), WORKSPACE), (dict(ws=0x9010), WORKSPACE), (dict(n=255), WORKSPACE)])
 def test_attention(dfv, kw, status):
     assert attn(dfv, **kw) == status
@@ -153,6 +154,8 @@ def test_attention_head_sizes(dfv, dim):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=4), UNSUPPORTED), (dict(dtype=2), UNSUPPORTED), (dict(V=0), INVALID), (dict(V=1 << 29), INVALID),
+    (dict(best=0x5002), INVALID), (dict(tokens=0x3001), INVALID), (dict(rules=dict(bias=0x102)), INVALID),
+    (dict(rules=dict(allowed=0x101)), INVALID), (dict(rules=dict(hist=0x1002)), INVALID),
     (dict(x=0), INVALID), (dict(x=0x2001), INVALID), (dict(out=0x4001), INVALID), (dict(dtype=0, x=0x2002), INVALID),
     (dict(out=None, best=None), INVALID), (dict(row=999), INVALID), (dict(out_row=10), INVALID),
     (dict(out=0x2000, out_row=1200), INVALID), (dict(tokens=None), INVALID), (dict(rules=dict(hist_len=None)), INVALID),
@@ -170,7 +173,7 @@ def test_logits_without_rules(dfv):
     assert dfv.lib().dfv_logits_workspace_size((64 << 10) + 1) == 0
 
 
-@pytest.mark.parametrize("kw,status", [(dict(path=0), INVALID), (dict(tau=0), INVALID), (dict(new=0), INVALID), (dict(row=15), INVALID),
+@pytest.mark.parametrize("kw,status", [(dict(path=0), INVALID), (dict(tau=0), INVALID), (dict(new=0), INVALID), (dict(new=0x3002), INVALID), (dict(row=15), INVALID),
                                        (dict(ws=0), WORKSPACE), (dict(ws=0x9001), WORKSPACE), (dict(n=4096), WORKSPACE)])
 def test_commit(dfv, kw, status):
     assert commit(dfv, **kw) == status
@@ -188,6 +191,8 @@ def test_page_lists(dfv):
     assert L.dfv_pages_reserve(c, None, 0x2000, 1, 0x9000, 1 << 20, None) == INVALID
     assert L.dfv_pages_fork(c, 0x1000, None, 1, 0x9000, 1 << 20, None) == INVALID
     assert L.dfv_pages_free(c, None, 1, None) == INVALID
+    assert L.dfv_pages_free(c, 0x1002, 1, None) == INVALID
+    assert L.dfv_cache_copy_pages(c, 0x1000, 0x2001, 1, None) == INVALID
     assert L.dfv_pages_reserve(bare, 0x1000, 0x2000, 1, 0x9000, 1 << 20, None) == INVALID
     assert L.dfv_pages_fork(bare, 0x1000, 0x2000, 1, 0x9000, 1 << 20, None) == INVALID
     assert L.dfv_pages_free(bare, 0x1000, 1, None) == INVALID
