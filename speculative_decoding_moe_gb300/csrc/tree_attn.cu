@@ -51,6 +51,7 @@ struct MmaShape {
   static constexpr int kStages = D == 64 ? 10 : 4;         // of K and V: 160 and 128 KB in flight
   static constexpr int kPer = kStages / kGroups;           // stages of a group
   static constexpr int kPitch = D + 4;                     // floats of a row of a warp's state
+  static constexpr int kOver = D == 64 ? 6 : 3;            // tiles' worth of time that a pair costs at least
   static constexpr size_t kState = (size_t)kRows * kPitch * 4;
   static constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * kTile + kCons * kState;
 };
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
   }
   pdl_wait();
   pdl_trigger();  // the join may now read the call's inputs
-  sched_start<kMmaThreads, kKt>(L, blockIdx.x, s_scan, &s_start);  // syncs the CTA
+  sched_start<kMmaThreads, kKt, S::kOver>(L, blockIdx.x, s_scan, &s_start);  // syncs the CTA
   const int row0 = (int)(blockIdx.x % L.n_rt) * kRows;  // first row of this CTA
 
   if (warp < kProd) {
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
     const CUtensorMap *map = warp == 0 ? &L.tm_k : &L.tm_v;
     int issued[kGroups] = {};  // tiles of each group
     bool ok = true;
-    SegWalk<kKt> wk(L, s_start);
+    SegWalk<kKt, S::kOver> wk(L, s_start);
     const int shift = p.c.page_shift, boxes = shift >= 6 ? 1 : kKt >> shift, rows = kKt / boxes;
     while (ok && wk.next()) {
       const int pages = wk.v.s < 0 ? 0 : (wk.total + (1 << shift) - 1) >> shift;
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
   constexpr float kBias = F16 ? 6.f : 0.f;
   int st = group * S::kPer, ph = 0;
   bool ok = true;
-  SegWalk<kKt> wk(L, s_start);
+  SegWalk<kKt, S::kOver> wk(L, s_start);
   while (wk.next()) {
     const int R = wk.v.n * p.G;
     // row r = node * G + head of the group; rows past R are zero and see nothing
@@ -358,12 +359,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join_kernel(const _
   const int R = v.n * p.G;
   pdl_wait();  // by every CTA: what follows this launch may rely on the first one's end
   if (r0 >= R) return;
-  const int4 pair = __ldcg(&L.pairs[b * p.c.Hkv + h]);
+  const int2 pair = __ldcg(&L.pairs[b * p.c.Hkv + h]);
   const int g0 = pair.x, n = pair.y;
   if (n < 2) return;
   const int rt = r0 / L.rows, rr = r - rt * L.rows;
-  // state k is range g0 + k's; only in the first range can the pair be the second cut
-  auto slot = [&](int k) { return (size_t)(2 * ((g0 + k) * L.n_rt + rt) + (k == 0 ? pair.z : 0)); };
+  // state k is range g0 + k's; the pair goes on after the first and began before the others
+  auto slot = [&](int k) { return (size_t)(2 * ((g0 + k) * L.n_rt + rt) + (k == 0)); };
   // ---- weights of the states, and the sum
   float2 ml[kJoinStates];
   int bad = 0;

@@ -15,7 +15,7 @@ struct AttnLaunch {
   int n_groups;  // ranges
   int swap;      // head before token in the tensor maps
   uint32_t inv_g;  // ceil(2^16 / G)
-  int4 *pairs;        // [n_seqs][kv heads] of each pair: first range, ranges, whether it starts inside that range
+  int2 *pairs;        // [n_seqs][kv heads] of each pair: first range, ranges
   float2 *part_ml;    // [2 CTAs][rows] (M, l) of partial states
   float *part_o;      // [2 CTAs][D / 4][rows][4] their sums of p v
   int *part_bad;      // [2 CTAs] a tree value that is not finite was left out
@@ -32,7 +32,7 @@ inline size_t attn_sections(AttnLaunch *L, const AttnPlan &a, int n_seqs, int Hk
     off += (n + 255) & ~(size_t)255;
     return q;
   };
-  int4 *pairs = (int4 *)take((size_t)n_seqs * Hkv * 16);
+  int2 *pairs = (int2 *)take((size_t)n_seqs * Hkv * 8);
   int *bad = (int *)take(slots * 4);
   float2 *ml = (float2 *)take(slots * a.rows * 8);
   float *o = (float *)take(slots * a.rows * D * 4);
@@ -50,9 +50,11 @@ inline size_t attn_sections(AttnLaunch *L, const AttnPlan &a, int n_seqs, int Hk
 __device__ __forceinline__ int node_of(const AttnLaunch &L, int r) { return (int)(((uint32_t)r * L.inv_g) >> 16); }
 
 // ---------------------------------------------------------------- the work line
-// Sequence b's units are its kv heads' key tiles, head after head; a pair
-// without keys is one unit (its outputs have to be written), a sequence
-// without rows none.  Range g of G over U units is [g U / G, (g + 1) U / G);
+// Sequence b's units are its kv heads' pairs one after the other: V units for
+// what a pair costs however long it is (queries, the first scores, the output;
+// without them the ranges of many short pieces ended last), then its key tiles.
+// A pair without keys has one tile (its outputs have to be written), a sequence
+// without rows no unit.  Range g of G over U units is [g U / G, (g + 1) U / G);
 // there are no more ranges than units.
 struct SchedStart {
   long long u0, u1, base;  // the range, and the first unit of sequence b
@@ -60,7 +62,7 @@ struct SchedStart {
   int b, G;
 };
 
-// Ranges in use: no range is empty.
+// Ranges in use.
 __device__ __forceinline__ int ranges_of(long long U, int n_groups) {
   return U >= n_groups ? n_groups : U > 0 ? (int)U : 1;
 }
@@ -72,35 +74,35 @@ __device__ __forceinline__ int group_of(long long u, long long U, int G) {
   return U < (1 << 24) ? (int)((((uint32_t)u + 1u) * (uint32_t)G - 1u) / (uint32_t)U) : (int)(((u + 1) * G - 1) / U);
 }
 
-template <int KT>
+template <int KT, int V>
 __device__ __forceinline__ long long seq_units(const AttnLaunch &L, int b) {
   const SeqView v = seq_view(L.p.c, L.p.t, b);
   if (v.n == 0) return 0;
   const int total = v.s < 0 ? 0 : v.len + v.n;
-  return (long long)L.p.c.Hkv * (total > 0 ? (total + KT - 1) / KT : 1);
+  return (long long)L.p.c.Hkv * (V + (total > 0 ? (total + KT - 1) / KT : 1));
 }
 
 // The range of CTA `block` and the sequence it starts in.  All NT threads of
 // the CTA call it; s_scan holds NT / 32 values.
-template <int NT, int KT>
+template <int NT, int KT, int V>
 __device__ __forceinline__ void sched_start(const AttnLaunch &L, int block, long long *s_scan, SchedStart *out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = L.p.t.n_seqs;
   const int per = (n + NT - 1) / NT, b0 = min(n, tid * per), b1 = min(n, b0 + per);
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += seq_units<KT>(L, b);
-  long long v = sum;
+  for (int b = b0; b < b1; ++b) sum += seq_units<KT, V>(L, b);
+  long long run = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long a = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += a;
+    const long long a = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += a;
   }
-  if (lane == 31) s_scan[warp] = v;
+  if (lane == 31) s_scan[warp] = run;
   if (tid == 0) {
     out->u0 = out->u1 = out->base = 0;
     out->b = 0;
   }
   __syncthreads();
-  long long U = 0, at = v - sum;
+  long long U = 0, at = run - sum;
   for (int w = 0; w < NT / 32; ++w) {
     if (w < warp) at += s_scan[w];
     U += s_scan[w];
@@ -110,7 +112,7 @@ __device__ __forceinline__ void sched_start(const AttnLaunch &L, int block, long
   if (u0 < u1 && at <= u0 && u0 < at + sum) {
     long long base = at;
     for (int b = b0; b < b1; ++b) {
-      const long long c = per == 1 ? sum : seq_units<KT>(L, b);
+      const long long c = per == 1 ? sum : seq_units<KT, V>(L, b);
       if (base <= u0 && u0 < base + c) {
         out->u0 = u0;
         out->u1 = u1;
@@ -128,31 +130,34 @@ __device__ __forceinline__ void sched_start(const AttnLaunch &L, int block, long
 }
 
 // Segments of a range: tiles [t0, t1) of one (sequence, kv head).
-template <int KT>
+template <int KT, int V>
 struct SegWalk {
   const AttnLaunch &L;
-  const long long first, end;
+  const long long end;
   long long u, base;
   int b, h, t0, t1, T, total;
   int nodes;  // of the sequence in the cache: none where the cache side is unusable
-  long long at;  // first unit of the segment
+  long long last;  // last unit of the pair
   SeqView v;
   __device__ __forceinline__ SegWalk(const AttnLaunch &l, const SchedStart &s)
-      : L(l), first(s.u0), end(s.u1), u(s.u0), base(s.base), b(s.b) {}
+      : L(l), end(s.u1), u(s.u0), base(s.base), b(s.b) {}
   __device__ __forceinline__ bool next() {
     while (u < end) {
       v = seq_view(L.p.c, L.p.t, b);
       nodes = v.s < 0 ? 0 : v.n;
       total = v.len + nodes;
       T = v.n == 0 ? 0 : total > 0 ? (total + KT - 1) / KT : 1;
-      const long long w = u - base, units = (long long)L.p.c.Hkv * T;
+      const int pair = T + V;  // units
+      const long long w = u - base, units = v.n == 0 ? 0 : (long long)L.p.c.Hkv * pair;
       if (w < units) {
-        h = (units >> 31) ? (int)(w / T) : (int)((uint32_t)w / (uint32_t)T);
-        t0 = (int)(w - (long long)h * T);
-        t1 = (int)min((long long)T, t0 + (end - u));
-        at = u;
-        u += t1 - t0;
-        return true;
+        h = (units >> 31) ? (int)(w / pair) : (int)((uint32_t)w / (uint32_t)pair);
+        const int p0 = (int)(w - (long long)h * pair), p1 = (int)min((long long)pair, p0 + (end - u));
+        last = u - p0 + pair - 1;
+        u += p1 - p0;
+        t0 = max(0, p0 - V);
+        t1 = max(0, p1 - V);
+        if (t0 < t1) return true;
+        continue;  // the range ends before the pair's first tile
       }
       base += units;
       ++b;
@@ -165,15 +170,16 @@ struct SegWalk {
     return row_mask(L.p.t, v.row0, node_of(L, r)) & (nodes >= 64 ? ~0ull : (1ull << nodes) - 1ull);
   }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == T; }
-  // For the join: one thread of the range that holds the pair's first unit tells
+  // For the join: one thread of the range that holds the pair's first tile tells
   // which ranges share it.
   __device__ __forceinline__ void tell(const SchedStart &s, int block) const {
     if (t0 || block % L.n_rt) return;
-    const int g = block / L.n_rt, last = whole() ? g : group_of(at + T - 1, s.U, s.G);
-    L.pairs[b * L.p.c.Hkv + h] = make_int4(g, last - g + 1, at != first, 0);
+    const int g = block / L.n_rt;
+    L.pairs[b * L.p.c.Hkv + h] = make_int2(g, whole() ? 1 : group_of(last, s.U, s.G) - g + 1);
   }
-  // a range cuts at most two pairs: the one it starts in and the one it ends in
-  __device__ __forceinline__ int slot(int block) const { return 2 * block + (at != first); }
+  // Partial states of a range: of a pair that began before it, and of one that
+  // goes on after it.
+  __device__ __forceinline__ int slot(int block) const { return 2 * block + (t0 == 0); }
 };
 
 // ---------------------------------------------------------------- pieces

@@ -36,6 +36,7 @@ template <int D, bool DUAL>
 struct TcShape {
   static constexpr uint32_t kTile = kTKeys * D * 2;            // one K or V tile
   static constexpr int kSlots = D == 64 ? 8 : DUAL ? 5 : 6;
+  static constexpr int kOver = 5;                              // tiles' worth of time that a pair costs at least
   static constexpr uint32_t kQ = (DUAL ? 2 : 1) * 128 * D * 2;
   static constexpr size_t kSmem = 1024 + kQ + (size_t)kSlots * kTile;
 };
@@ -246,11 +247,11 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
   tc_fence_before();
   pdl_wait();
   pdl_trigger();  // the join may now read the call's inputs
-  sched_start<kTThreads, kTKeys>(L, blockIdx.x, s_scan, &s_start);  // syncs the CTA
+  sched_start<kTThreads, kTKeys, S::kOver>(L, blockIdx.x, s_scan, &s_start);  // syncs the CTA
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const int row0 = (int)(blockIdx.x % L.n_rt) * L.rows;  // first row of this CTA
-  SegWalk<kTKeys> wk(L, s_start);
+  SegWalk<kTKeys, S::kOver> wk(L, s_start);
 
   if (warp == 8 || warp == 10) {
     // ---------------------------------------------------------------- producer

@@ -24,19 +24,19 @@ def group_of(u, U, G):
     return ((u + 1) * G - 1) // U
 
 
-def units(lens, nodes, heads, tile):
-    return [heads * max(1, -(-(a + n) // tile)) if n else 0 for a, n in zip(lens, nodes)]
+def units(lens, nodes, heads, tile, over):
+    return [heads * (over + max(1, -(-(a + n) // tile))) if n else 0 for a, n in zip(lens, nodes)]
 
 
-@pytest.mark.parametrize("seed", range(12))
-def test_every_unit_in_one_range_and_every_state_read_once(seed):
+@pytest.mark.parametrize("seed", range(24))
+def test_every_tile_in_one_range_and_every_state_read_once(seed):
     rng = random.Random(seed)
-    S, heads, tile = rng.choice([1, 2, 7, 40, 300]), rng.choice([1, 2, 4, 8]), rng.choice([64, 128])
+    S, heads, tile, over = rng.choice([1, 2, 7, 40, 300]), rng.choice([1, 2, 4, 8]), rng.choice([64, 128]), rng.choice([3, 5, 6])
     lens = [rng.choice([0, 1, rng.randint(0, 300), rng.randint(0, 40000)]) for _ in range(S)]
     nodes = [rng.randint(0, 3) for _ in range(S)]
     n_rt = rng.choice([1, 1, 2, 4])
     n_groups = CTAS // n_rt
-    per = units(lens, nodes, heads, tile)
+    per = units(lens, nodes, heads, tile, over)
     U = sum(per)
     if U == 0:
         return
@@ -44,43 +44,44 @@ def test_every_unit_in_one_range_and_every_state_read_once(seed):
     owner, stored, told = {}, {}, {}
     base = [sum(per[:s]) for s in range(S)]
     for g in range(G):
-        u0, u1 = start(g, U, G), start(g + 1, U, G)
-        assert u0 < u1  # no range is empty
-        assert g < n_groups
-        u, first = u0, u0
-        b = max(s for s in range(S) if base[s] <= u0 and per[s] and u0 < base[s] + per[s])
+        u, end = start(g, U, G), start(g + 1, U, G)
+        assert u < end and g < n_groups
+        b = max(s for s in range(S) if base[s] <= u and per[s] and u < base[s] + per[s])
         bb = base[b]
-        while u < u1:
+        while u < end:
             if per[b] == 0 or u >= bb + per[b]:
                 bb += per[b]
                 b += 1
                 continue
-            T = per[b] // heads
-            h, t0 = divmod(u - bb, T)
-            t1 = min(T, t0 + (u1 - u))
+            pair = per[b] // heads
+            h, p0 = divmod(u - bb, pair)
+            p1 = min(pair, p0 + (end - u))
+            last = u - p0 + pair - 1
+            u += p1 - p0
+            t0, t1, T = max(0, p0 - over), max(0, p1 - over), pair - over
+            if t0 >= t1:
+                continue
             for t in range(t0, t1):
                 assert (b, h, t) not in owner
                 owner[b, h, t] = g
-                assert group_of(bb + h * T + t, U, G) == g
             if not (t0 == 0 and t1 == T):  # a partial state
                 for rt in range(n_rt):
-                    slot = 2 * (g * n_rt + rt) + (u != first)
+                    slot = 2 * (g * n_rt + rt) + (t0 == 0)
                     assert slot not in stored and slot < 2 * n_groups * n_rt
                     stored[slot] = (b, h, g, rt)
             if t0 == 0:
-                last = g if t1 == T else group_of(u - t0 + T - 1, U, G)
-                told[b, h] = (g, last - g + 1, int(u != first))
-            u += t1 - t0
-    assert len(owner) == U
+                assert (b, h) not in told
+                told[b, h] = (g, 1 if t1 == T else group_of(last, U, G) - g + 1)
+    assert len(owner) == U - over * heads * sum(n > 0 for n in nodes)
     read = set()
     for s in range(S):
         for h in range(heads if nodes[s] else 0):
-            g0, n, second = told[s, h]
+            g0, n = told[s, h]
             if n < 2:
                 continue
             for rt in range(n_rt):
                 for k in range(n):
-                    slot = 2 * ((g0 + k) * n_rt + rt) + (second if k == 0 else 0)
+                    slot = 2 * ((g0 + k) * n_rt + rt) + (k == 0)
                     assert stored[slot] == (s, h, g0 + k, rt)
                     read.add(slot)
     assert read == set(stored)
