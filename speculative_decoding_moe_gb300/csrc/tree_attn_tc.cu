@@ -36,7 +36,7 @@ template <int D, bool DUAL>
 struct TcShape {
   static constexpr uint32_t kTile = kTKeys * D * 2;            // one K or V tile
   static constexpr int kSlots = D == 64 ? 8 : DUAL ? 5 : 6;
-  static constexpr int kOver = 5;                              // tiles' worth of time that a pair costs at least
+  static constexpr int kOver = DUAL ? 5 : 2;                   // tiles' worth of time that a pair costs at least
   static constexpr uint32_t kQ = (DUAL ? 2 : 1) * 128 * D * 2;
   static constexpr size_t kSmem = 1024 + kQ + (size_t)kSlots * kTile;
 };
