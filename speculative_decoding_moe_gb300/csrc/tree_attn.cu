@@ -346,8 +346,8 @@ constexpr int kJoinRows = 8;
 constexpr int kJoinStates = (kAttnCtas + 31) / 32;
 
 template <bool F16, int D, int CH>
-__global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join_kernel(const __grid_constant__ AttnLaunch L) {
-  constexpr int kBlocks = D / 16, kSplit = kJoinWarps / CH;
+__global__ void __launch_bounds__(32 * kJoinWarps, CH == 1 ? 3 : 6) tree_attn_join_kernel(const __grid_constant__ AttnLaunch L) {
+  constexpr int kBlocks = D / 16, kSplit = kJoinWarps / CH, kAhead = CH == 1 ? 8 : 4;  // states of a warp in flight
   __shared__ float s_w[kAttnCtas][kJoinRows], s_max[kJoinWarps][kJoinRows], s_l[kJoinWarps][kJoinRows];
   __shared__ float4 s_x[kSplit > 1 ? kJoinWarps : 1][32];
   pdl_trigger();
@@ -365,6 +365,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join_kernel(const _
   const int rt = r0 / L.rows, rr = r - rt * L.rows;
   // state k is range g0 + k's; the pair goes on after the first and began before the others
   auto slot = [&](int k) { return (size_t)(2 * ((g0 + k) * L.n_rt + rt) + (k == 0)); };
+  // ---- the first sums of p v, on their way while the weights are found
+  const int part = warp % kSplit, c4 = ((int)blockIdx.z % (kBlocks / CH) * CH + warp / kSplit) * 4 + cg;
+  const float4 *base = reinterpret_cast<const float4 *>(L.part_o) + (size_t)c4 * L.rows + rr;
+  const size_t pitch = (size_t)(D / 4) * L.rows;
+  float4 y[kAhead];
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (k0 + i * kSplit < n && r < R) y[i] = __ldcg(base + slot(k0 + i * kSplit) * pitch);
+  };
+  fetch(part);
   // ---- weights of the states, and the sum
   float2 ml[kJoinStates];
   int bad = 0;
@@ -400,18 +411,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_attn_join_kernel(const _
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) l += s_l[w][r8];
   // ---- sums of p v
-  const int part = warp % kSplit, c4 = ((int)blockIdx.z % (kBlocks / CH) * CH + warp / kSplit) * 4 + cg;
-  const float4 *base = reinterpret_cast<const float4 *>(L.part_o) + (size_t)c4 * L.rows + rr;
-  const size_t pitch = (size_t)(D / 4) * L.rows;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   if (r < R) {
-    for (int k0 = part; k0 < n; k0 += 8 * kSplit) {
-      float4 y[8];
+    for (int k0 = part; k0 < n; k0 += kAhead * kSplit) {
+      if (k0 != part) fetch(k0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (k0 + i * kSplit < n) y[i] = __ldcg(base + slot(k0 + i * kSplit) * pitch);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < kAhead; ++i)
         if (k0 + i * kSplit < n) {
           const float f = s_w[k0 + i * kSplit][r8];
           x.x = fmaf(y[i].x, f, x.x);
