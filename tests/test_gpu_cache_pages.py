@@ -361,3 +361,60 @@ def test_offsets_past_32_bits(dfv):
     assert torch.equal(k[0, 38, 0, 4:7], rows[[4, 7, 9]])
     del buf, k, v, cache
     torch.cuda.empty_cache()
+
+
+def test_a_whole_step_in_a_graph(dfv):
+    """reserve, rotary append, attention, rules, walk, commit, drop and fork captured once and replayed: the same state,
+    step by step, as the calls made eagerly."""
+    def make():
+        g = torch.Generator().manual_seed(11)
+        cache = dfv.KVCache.empty(2, 60, 16, 2, 64, 5, 10)
+        cache.k.copy_(torch.randn(cache.k.shape, generator=g).to(BF))
+        cache.v.copy_(torch.randn(cache.v.shape, generator=g).to(BF))
+        cache.page_table[:3, 0] = i32([7, 3, 9])
+        cache.refs[[7, 3, 9]] = 1
+        cache.lens[:3] = i32([5, 0, 13])
+        rng = random.Random(2)
+        nodes = [6, 1, 17]
+        masks = [m for n in nodes for m in tree_masks(n, rng)]
+        tree = dfv.TreeBatch(i32([0, 6, 7, 24]), 24, 17, mask=torch.tensor([signed(m) for m in masks], dtype=torch.int64).cuda())
+        s = dict(cache=cache, tree=tree, rope=dfv.Rope(64), ws=dfv.alloc_workspace(dfv.cache_workspace_size(cache)),
+                 aws=dfv.alloc_workspace(dfv.tree_attention_workspace_size(cache, tree, 8)),
+                 lws=dfv.alloc_workspace(dfv.logits_workspace_size(24)), all=i32([0, 1, 2]), n=i32([6, 1, 17]),
+                 qkv=torch.randn(24, 12, 64, generator=g).to(BF).cuda(), x=torch.randn(24, 40, generator=g).cuda(),
+                 tokens=torch.randint(0, 40, (24,), generator=g, dtype=torch.int32).cuda(),
+                 rules=dfv.LogitRules(repetition=torch.tensor([1.1, 1.2, 1.3]).cuda()), src=i32([2, 0]), dst=i32([3, 4]))
+        return s
+
+    def step(s):
+        c, t = s["cache"], s["tree"]
+        dfv.pages_reserve(c, s["all"], s["n"], s["ws"])
+        pos = torch.arange(24, dtype=torch.int32, device="cuda") + c.lens[0]
+        out = []
+        for layer in range(2):
+            q = dfv.rope_append(c, layer, t, s["rope"], s["qkv"][:, :8], s["qkv"][:, 8:10], s["qkv"][:, 10:], pos)
+            out.append(dfv.tree_attention(c, layer, t, q, s["aws"]))
+        x, best = dfv.logits_process(s["x"], t, s["tokens"], s["rules"], s["lws"])
+        path, tau = dfv.accept_tree(t, s["tokens"], best)
+        dfv.cache_commit(c, t, path, tau, s["ws"])
+        dfv.pages_free(c, s["dst"])
+        dfv.pages_fork(c, s["src"], s["dst"], s["ws"])
+        return out + [x, best, path, tau]
+
+    def state(s, out):
+        c = s["cache"]
+        return [x.clone() for x in out + [c.k, c.v, c.page_table, c.lens, c.refs, c.err]]
+
+    a, b = make(), make()
+    warm = make()
+    step(warm)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(b)
+    for _ in range(3):
+        want = state(a, step(a))
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(want, state(b, out)):
+            assert torch.equal(x, y)
+    assert a["cache"].errors() == 0
