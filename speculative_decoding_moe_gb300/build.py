@@ -1,5 +1,6 @@
 """Build libdfv.so in-tree: every .cu under csrc/ compiled for sm_103a only,
-in parallel, then linked into one shared library (no cmake)."""
+in parallel, then linked into one shared library (no cmake); and _dfvbind.so,
+the Python binding's extension (host code, torch's headers), beside it."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -7,11 +8,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdfv.so")
+BIND = os.path.join(HERE, "_dfvbind.so")
+BIND_SRC = os.path.join(CSRC, "binding.cpp")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 NVCC = os.environ.get("NVCC", "nvcc")
@@ -24,13 +28,13 @@ def _sources():
 
 
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
+    return [BIND_SRC] + _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     return all(os.path.getmtime(f) <= t for f in _deps() + [__file__])
 
 
@@ -50,14 +54,36 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    bind_obj = os.path.join(BUILD, "binding.o")
+
+    def compile_binding():
+        import torch
+        at = os.path.join(os.path.dirname(torch.__file__), "include")
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", at,
+               "-I", os.path.join(at, "torch", "csrc", "api", "include"), "-c", BIND_SRC, "-o", bind_obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("compiling the binding failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
+
+    with cf.ThreadPoolExecutor(max_workers=min(9, len(srcs) + 1)) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding.result()
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
     os.replace(tmp, LIB)
+    import torch
+    tmp = BIND + ".tmp.%d" % os.getpid()
+    # libdfv.so is found beside the extension; torch's libraries are loaded by then
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, bind_obj, "-L", HERE, "-l:libdfv.so", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("linking the binding failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    os.replace(tmp, BIND)
     return LIB
 
 

@@ -1,9 +1,13 @@
-"""Python binding of libdfv.so (ctypes).  Argument marshalling only: every step
-of the block-verify path runs in the library's CUDA kernels.  Tensors must be
-CUDA tensors; calls enqueue work on torch's current CUDA stream."""
+"""Python binding of libdfv.so.  Argument marshalling only: every step of the
+block-verify path runs in the library's CUDA kernels.  Tensors must be CUDA
+tensors; calls enqueue work on torch's current CUDA stream.  The block-verify
+calls go through ctypes; the tree-verify calls, which a step makes dozens of,
+through the extension built from csrc/binding.cpp."""
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 from typing import Optional, Sequence
@@ -14,6 +18,7 @@ from .inputs import LayerWeights
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdfv.so")
+BIND_PATH = os.path.join(HERE, "_dfvbind.so")
 
 F32, BF16, MXFP4, Q8, F16 = 0, 1, 2, 3, 4
 # device error bits (DFV_DEVERR_* in include/dfv.h)
@@ -75,6 +80,20 @@ class CRules(ctypes.Structure):
                 ("allowed", ctypes.c_void_p), ("allowed_row", ctypes.c_int64)]
 
 
+# the descriptors with what the extension's checks need beside them (csrc/binding.cpp)
+class CCacheHandle(ctypes.Structure):
+    _fields_ = [("c", CCache), ("index", ctypes.c_int)]
+
+
+class CTreeHandle(ctypes.Structure):
+    _fields_ = [("c", CTree), ("index", ctypes.c_int)]
+
+
+class CRulesHandle(ctypes.Structure):
+    _fields_ = [("c", CRules), ("n_seqs", ctypes.c_int), ("index", ctypes.c_int), ("bias_rows", ctypes.c_int),
+                ("allowed_rows", ctypes.c_int), ("bias_cols", ctypes.c_int64), ("allowed_cols", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -134,6 +153,24 @@ def _load():
         L.dfv_pages_free.argtypes = [P, P, I, P]
         _lib = L
     return _lib
+
+
+_ext = None
+
+
+def _bind():
+    """The extension with the tree-verify calls."""
+    global _ext
+    if _ext is None:
+        _load()
+        if not os.path.exists(BIND_PATH):
+            raise ImportError("_dfvbind.so is not built (%s); run speculative_decoding_moe_gb300.build.build()" % BIND_PATH)
+        loader = importlib.machinery.ExtensionFileLoader("_dfvbind", BIND_PATH)
+        spec = importlib.util.spec_from_file_location("_dfvbind", BIND_PATH, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _ext = module
+    return _ext
 
 
 def lib():
@@ -387,14 +424,14 @@ def accept_greedy_noalloc(logits: torch.Tensor, draft: torch.Tensor, tau: Option
 
 
 # ---------------------------------------------------------------- tree verify
-# The arguments of a small call cost more to check than its kernel to run, so each helper decides with one condition
-# and only a refusal takes the time to say why.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _on(stream, index: int) -> int:
     """Stream handle of a call: the given stream, or torch's current one on the tensors' device."""
-    return _raw_stream(index) if stream is None else stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(index) if index >= 0 else 0  # host tensors are refused by the call
 
 
 def _refuse(t, what: str, dtype, shape, index: int):
@@ -406,7 +443,7 @@ def _refuse(t, what: str, dtype, shape, index: int):
         raise ValueError("%s must have shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
     if t.get_device() != index:
         raise ValueError("%s is on %s, not with the other tensors of the call" % (what, t.device))
-    raise ValueError("%s must be contiguous%s" % (what, " in its last dimension" if len(shape) == 3 else ""))
+    raise ValueError("%s must be contiguous" % what)
 
 
 def _need(t: Optional[torch.Tensor], what: str, dtype, shape, index: int) -> int:
@@ -419,17 +456,6 @@ def _need(t: Optional[torch.Tensor], what: str, dtype, shape, index: int) -> int
 def _given(t: Optional[torch.Tensor], what: str, dtype, shape, index: int) -> Optional[int]:
     """_need for an argument that may be left out."""
     return None if t is None else _need(t, what, dtype, shape, index)
-
-
-def _rows3(t: torch.Tensor, what: str, rows: int, heads: int, dim: int, dtype, index: int):
-    """(address, row stride, head stride) of a [rows, heads, dim] tensor whose last dimension is contiguous."""
-    if t.dtype is not dtype or t.shape != (rows, heads, dim) or t.get_device() != index:
-        _refuse(t, what, dtype, (rows, heads, dim), index)
-    s = t.stride()
-    if s[2] != 1:
-        _refuse(t, what, dtype, (rows, heads, dim), index)
-    # a dimension of size 1 has no stride of its own
-    return t.data_ptr(), s[0] if rows > 1 else 0, s[1] if heads > 1 else 0
 
 
 class KVCache:
@@ -470,7 +496,10 @@ class KVCache:
                         k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], k.stride(3) if self.page_size > 1 else self.head_dim,
                         page_table.data_ptr(), lens.data_ptr(), None if refs is None else refs.data_ptr(),
                         err.data_ptr())
+        self._handle = CCacheHandle(self.c, at)
+        self.c = self._handle.c
         self.ref = ctypes.byref(self.c)
+        self.addr = ctypes.addressof(self._handle)
 
     @classmethod
     def empty(cls, n_layers: int, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, max_seqs: int,
@@ -504,7 +533,10 @@ class TreeBatch:
         self.row_off, self.mask, self.seq = row_off, mask, seq
         self.c = CTree(self.n_seqs, self.n_rows, self.max_nodes, None if seq is None else seq.data_ptr(),
                        row_off.data_ptr(), None if mask is None else mask.data_ptr())
+        self._handle = CTreeHandle(self.c, at)
+        self.c = self._handle.c
         self.ref = ctypes.byref(self.c)
+        self.addr = ctypes.addressof(self._handle)
 
 
 class Rope:
@@ -529,28 +561,16 @@ class Rope:
         self.scale = float(scale)
         signed = [t - (1 << 64) if t >> 63 else t for t in turns]
         self.turns = torch.tensor(signed, dtype=torch.int64, device=device)
+        self.turns_addr, self.index = self.turns.data_ptr(), self.turns.get_device()
 
 
 def rope_append(cache: KVCache, layer: int, tree: TreeBatch, rope: Rope, q: torch.Tensor, k: torch.Tensor,
                 v: torch.Tensor, positions: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rotated q (out, a new tensor or q itself), and the rows' rotated k and their v stored into the cache.
     q [rows, heads, dim], k and v [rows, kv heads, dim] may be slices of one projection."""
-    rows, H, K, D, dt, at = tree.n_rows, q.shape[1] if q.dim() == 3 else 0, cache.n_kv_heads, cache.head_dim, cache.dtype, cache.index
-    qp, qr, qh = _rows3(q, "q", rows, H, D, dt, at)
-    kp, kr, kh = _rows3(k, "k", rows, K, D, dt, at)
-    vp, vr, vh = _rows3(v, "v", rows, K, D, dt, at)
-    pp = _need(positions, "positions", torch.int32, (rows,), at)
-    if rope.head_dim != D:
-        raise ValueError("the rotary plan is for head_dim %d, the cache has %d" % (rope.head_dim, D))
-    if out is None:
-        out = torch.empty((rows, H, D), dtype=dt, device=q.device)
-    op, orow, oh = _rows3(out, "out", rows, H, D, dt, at)
-    st = _load().dfv_rope_append(cache.ref, layer, tree.ref, H, rope.rot_dim, rope.interleaved, rope.scale,
-                                 rope.turns.data_ptr(), qp, qr, qh, kp, kr, kh, vp, vr, vh, pp, op, orow, oh,
-                                 _on(stream, at))
-    if st:
-        raise DfvError(st, "dfv_rope_append")
-    return out
+    return (_ext or _bind()).rope_append(cache.addr, layer, tree.addr, rope.head_dim, rope.rot_dim, rope.interleaved,
+                                         rope.scale, rope.turns_addr, q, k, v, positions, out,
+                                         _on(stream, cache.index), rope.index)
 
 
 def tree_attention_workspace_size(cache: KVCache, tree: TreeBatch, n_heads: int) -> int:
@@ -562,17 +582,7 @@ def tree_attention(cache: KVCache, layer: int, tree: TreeBatch, q: torch.Tensor,
                    lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention of every drafted node over its sequence's committed tokens and the nodes of its mask.
     scale: 1/sqrt(head_dim) by default; lse: optional fp32 [rows, heads] that receives ln(sum exp)."""
-    rows, H, D, dt, at = tree.n_rows, q.shape[1] if q.dim() == 3 else 0, cache.head_dim, cache.dtype, cache.index
-    qp, qr, qh = _rows3(q, "q", rows, H, D, dt, at)
-    if out is None:
-        out = torch.empty((rows, H, D), dtype=dt, device=q.device)
-    op, orow, oh = _rows3(out, "out", rows, H, D, dt, at)
-    lp = _given(lse, "lse", torch.float32, (rows, H), at)
-    st = _load().dfv_tree_attention(cache.ref, layer, tree.ref, H, D ** -0.5 if scale is None else scale, qp, qr, qh,
-                                    op, orow, oh, lp, ws.data_ptr(), ws.numel(), _on(stream, at))
-    if st:
-        raise DfvError(st, "dfv_tree_attention")
-    return out
+    return (_ext or _bind()).tree_attention(cache.addr, layer, tree.addr, q, ws, scale, out, lse, _on(stream, cache.index))
 
 
 class LogitRules:
@@ -605,7 +615,12 @@ class LogitRules:
         self.c = CRules(ptr(hist), ptr(hist_len), ptr(prompt_len), 0 if hist is None else hist.shape[1], ptr(repetition),
                         ptr(frequency), ptr(presence), ptr(bias), 0 if bias is None or bias.shape[0] == 1 else bias.shape[1],
                         ptr(allowed), 0 if allowed is None or allowed.shape[0] == 1 else allowed.shape[1])
+        size = lambda t: (0, 0) if t is None else tuple(t.shape)  # noqa: E731
+        (br, bc), (ar, ac) = size(bias), size(allowed)
+        self._handle = CRulesHandle(self.c, -1 if n is None else n, -2 if at is None else at, br, ar, bc, ac)
+        self.c = self._handle.c
         self.ref = ctypes.byref(self.c)
+        self.addr = ctypes.addressof(self._handle)
 
 
 def logits_workspace_size(n_rows_max: int) -> int:
@@ -617,55 +632,14 @@ def logits_process(logits: torch.Tensor, tree: TreeBatch, tokens: Optional[torch
                    store: bool = True, stream=None):
     """(logits under the rules, argmax of each row).  logits [rows, V] bf16 or fp32 with contiguous rows; out may be
     logits itself; store=False computes the argmax only (out is then None)."""
-    if logits.dim() != 2 or logits.shape[0] != tree.n_rows or logits.stride(1) != 1:
-        raise ValueError("logits must be [%d, V] with contiguous rows" % tree.n_rows)
-    rows, V = logits.shape
-    at, dt = tree.index, logits.dtype
-    if logits.get_device() != at or (rules.index is not None and rules.index != at):
-        raise ValueError("logits, tree and rules are not on one device")
-    if rules.n_seqs is not None and rules.n_seqs != tree.n_seqs:
-        raise ValueError("the rules are for %d sequences, the call has %d" % (rules.n_seqs, tree.n_seqs))
-    if rules.bias is not None and (rules.bias.shape[1] != V or rules.bias.shape[0] not in (1, tree.n_seqs)):
-        raise ValueError("bias must be [1 or %d, %d]" % (tree.n_seqs, V))
-    if rules.allowed is not None and (rules.allowed.shape[1] != (V + 31) // 32 or rules.allowed.shape[0] not in (1, rows)):
-        raise ValueError("allowed must be [1 or %d, %d]" % (rows, (V + 31) // 32))
-    tp = _given(tokens, "tokens", torch.int32, (rows,), at)
-    op = orow = 0
-    if not store:
-        if out is not None:
-            raise ValueError("store=False takes no out")
-    else:
-        if out is None:
-            out = torch.empty((rows, V), dtype=dt, device=logits.device)
-        elif out.shape != logits.shape or out.dtype is not dt or out.stride(1) != 1 or out.get_device() != at:
-            raise ValueError("out must be like logits")
-        op, orow = out.data_ptr(), out.stride(0) if rows > 1 else V
-    if argmax is None:
-        argmax = torch.empty((rows,), dtype=torch.int32, device=logits.device)
-    ap = _need(argmax, "argmax", torch.int32, (rows,), at)
-    st = _load().dfv_logits_process(logits.data_ptr(), logits.stride(0) if rows > 1 else V, _act(logits), V, tree.ref,
-                                    tp, rules.ref, op or None, orow, ap, ws.data_ptr(), ws.numel(), _on(stream, at))
-    if st:
-        raise DfvError(st, "dfv_logits_process")
-    return out, argmax
+    return (_ext or _bind()).logits_process(logits, tree.addr, tokens, rules.addr, ws, out, argmax, store,
+                                            _on(stream, tree.index))
 
 
 def accept_tree(tree: TreeBatch, tokens: torch.Tensor, target: torch.Tensor, path: Optional[torch.Tensor] = None,
                 tau: Optional[torch.Tensor] = None, stream=None):
     """(path [n_seqs, max_nodes], tau [n_seqs]): the accepted nodes of each tree, root first, then -1."""
-    at = tree.index
-    tp = _need(tokens, "tokens", torch.int32, (tree.n_rows,), at)
-    gp = _need(target, "target", torch.int32, (tree.n_rows,), at)
-    if path is None:
-        path = torch.empty((tree.n_seqs, tree.max_nodes), dtype=torch.int32, device=tokens.device)
-    if tau is None:
-        tau = torch.empty((tree.n_seqs,), dtype=torch.int32, device=tokens.device)
-    width = path.shape[-1]
-    st = _load().dfv_accept_tree(tree.ref, tp, gp, _need(path, "path", torch.int32, (tree.n_seqs, width), at), width,
-                                 _need(tau, "tau", torch.int32, (tree.n_seqs,), at), _on(stream, at))
-    if st:
-        raise DfvError(st, "dfv_accept_tree")
-    return path, tau
+    return (_ext or _bind()).accept_tree(tree.addr, tokens, target, path, tau, _on(stream, tree.index))
 
 
 def cache_workspace_size(cache: KVCache) -> int:
@@ -676,43 +650,25 @@ def cache_commit(cache: KVCache, tree: TreeBatch, path: torch.Tensor, tau: torch
                  new_lens: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Moves the accepted rows together in every layer and adds tau to the lengths (cache.lens unless new_lens is
     given); returns the lengths."""
-    at = cache.index
-    width = path.shape[-1]
-    pp = _need(path, "path", torch.int32, (tree.n_seqs, width), at)
-    tp = _need(tau, "tau", torch.int32, (tree.n_seqs,), at)
-    if new_lens is None:
-        new_lens = cache.lens
-    st = _load().dfv_cache_commit(cache.ref, tree.ref, pp, width, tp,
-                                  _need(new_lens, "new_lens", torch.int32, cache.lens.shape, at), ws.data_ptr(),
-                                  ws.numel(), _on(stream, at))
-    if st:
-        raise DfvError(st, "dfv_cache_commit")
-    return new_lens
-
-
-def _index(t: torch.Tensor, what: str, cache: KVCache, n: Optional[int] = None):
-    return _need(t, what, torch.int32, (t.numel() if n is None else n,), cache.index)
+    return (_ext or _bind()).cache_commit(cache.addr, tree.addr, path, tau, ws, cache.lens if new_lens is None else new_lens,
+                                          _on(stream, cache.index))
 
 
 def cache_copy_pages(cache: KVCache, src: torch.Tensor, dst: torch.Tensor, stream=None):
     """Page dst[i] <- page src[i] in every layer."""
-    _check(_load().dfv_cache_copy_pages(cache.ref, _index(src, "src", cache), _index(dst, "dst", cache, src.shape[0]),
-                                        src.shape[0], _on(stream, cache.index)), "dfv_cache_copy_pages")
+    (_ext or _bind()).cache_copy_pages(cache.addr, src, dst, _on(stream, cache.index))
 
 
 def pages_reserve(cache: KVCache, seqs: torch.Tensor, n_new: torch.Tensor, ws: torch.Tensor, stream=None):
     """Pages for n_new[i] tokens after those of sequence seqs[i]."""
-    _check(_load().dfv_pages_reserve(cache.ref, _index(seqs, "seqs", cache), _index(n_new, "n_new", cache, seqs.shape[0]),
-                                     seqs.shape[0], ws.data_ptr(), ws.numel(), _on(stream, cache.index)), "dfv_pages_reserve")
+    (_ext or _bind()).pages_reserve(cache.addr, seqs, n_new, ws, _on(stream, cache.index))
 
 
 def pages_fork(cache: KVCache, src: torch.Tensor, dst: torch.Tensor, ws: torch.Tensor, stream=None):
     """Sequence dst[i], which holds nothing, becomes a copy of src[i]."""
-    _check(_load().dfv_pages_fork(cache.ref, _index(src, "src", cache), _index(dst, "dst", cache, src.shape[0]),
-                                  src.shape[0], ws.data_ptr(), ws.numel(), _on(stream, cache.index)), "dfv_pages_fork")
+    (_ext or _bind()).pages_fork(cache.addr, src, dst, ws, _on(stream, cache.index))
 
 
 def pages_free(cache: KVCache, seqs: torch.Tensor, stream=None):
     """Drops sequences: their pages lose a holder, their lengths become 0."""
-    _check(_load().dfv_pages_free(cache.ref, _index(seqs, "seqs", cache), seqs.shape[0], _on(stream, cache.index)),
-           "dfv_pages_free")
+    (_ext or _bind()).pages_free(cache.addr, seqs, _on(stream, cache.index))
