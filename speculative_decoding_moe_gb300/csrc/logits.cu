@@ -25,6 +25,7 @@ namespace {
 constexpr int kLogitThreads = 512;
 constexpr int kCols = 8;                              // columns of a thread
 constexpr int kSlice = kLogitThreads * kCols;
+constexpr int kEarly = 2;                             // quads of history tokens of a thread loaded first
 constexpr int kAhead = 4;                             // listed columns of a lane in flight
 constexpr uint32_t kPromptBit = 0x80000000u;          // the token is in the prompt
 constexpr uint32_t kTreeBit = 0x40000000u;            // some drafted node holds the token:
@@ -50,17 +51,30 @@ struct Raw {
     if (F32) return __uint_as_float(w[j % kWords]);
     return j & 1 ? bf16_hi(w[j / 2 % kWords]) : bf16_lo(w[j / 2 % kWords]);
   }
-  __device__ __forceinline__ float largest() const {
+  // the largest column: fp32, or one of a pair
+  __device__ __forceinline__ uint32_t largest() const {
     if (F32) {
       float m = at(0);
 #pragma unroll
       for (int j = 1; j < kCols; ++j) m = fmaxf(m, at(j));
-      return m;
+      return __float_as_uint(m);
     }
     __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162 *>(&w[0]);
 #pragma unroll
     for (int q = 1; q < kWords; ++q) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162 *>(&w[q]));
-    return fmaxf(__low2float(m), __high2float(m));
+    return *reinterpret_cast<const uint32_t *>(&m);
+  }
+  static __device__ __forceinline__ float value(uint32_t m) {
+    return F32 ? __uint_as_float(m) : fmaxf(bf16_lo(m), bf16_hi(m));
+  }
+  // whether largest() may beat a row's `floor`, held in the same form
+  static __device__ __forceinline__ bool reaches(uint32_t m, uint32_t floor) {
+    if (F32) return !(__uint_as_float(m) < __uint_as_float(floor));
+    return !__hblt2(*reinterpret_cast<const __nv_bfloat162 *>(&m), *reinterpret_cast<const __nv_bfloat162 *>(&floor));
+  }
+  static __device__ __forceinline__ uint32_t floor_of(uint32_t key) {
+    const uint32_t f = key == 0u ? 0xff800000u : key & 0x80000000u ? key ^ 0x80000000u : ~key;
+    return F32 ? f : __byte_perm(f, 0u, 0x3232);
   }
 };
 
@@ -81,6 +95,13 @@ __device__ __forceinline__ void spread(uint32_t bits, uint32_t (&m)[Raw<F32>::kW
   }
 }
 
+// The same for pairs from a table of four bits' masks: few instructions count more
+// here than two shared-memory reads.
+__device__ __forceinline__ void spread_pairs(const uint2 *table, uint32_t bits, uint32_t (&m)[4]) {
+  const uint2 a = table[bits & 15u], b = table[bits >> 4];
+  m[0] = a.x; m[1] = a.y; m[2] = b.x; m[3] = b.y;
+}
+
 // What is in flight of a row: its columns, one 16-bit column a register where
 // they are loaded one by one, and the mask bits.  Loading waits for nothing that
 // it loads and has no branch on a column; ready() puts the pieces together when
@@ -90,18 +111,18 @@ struct Fetched {
   static constexpr int kWords = VEC || F32 ? Raw<F32>::kWords : kCols;
   uint32_t w[kWords], bits;
 
-  __device__ __forceinline__ void load(const char *row, const uint32_t *allowed, int left) {
-    constexpr int kBytes = F32 ? 4 : 2;
+  // row and allowed start at the thread's columns (VEC) or at the slice
+  __device__ __forceinline__ void load(const char *row, const uint8_t *allowed, int left) {
     const int tid = threadIdx.x;
     if (VEC) {
       if (column<VEC>(0) < left) {  // left is a multiple of kCols
 #pragma unroll
         for (int q = 0; q < kWords; q += 4) {
-          const uint4 a = ldg_stream(row + kBytes * column<VEC>(0) + 4 * q);
+          const uint4 a = ldg_stream(row + 4 * q);
           w[q] = a.x; w[q + 1] = a.y; w[q + 2] = a.z; w[q + 3] = a.w;
         }
+        bits = allowed ? (uint32_t)__ldg(allowed) : 0xffu;
       }
-      bits = allowed ? (uint32_t)__ldg(reinterpret_cast<const uint8_t *>(allowed) + min(tid, (left - 1) / kCols)) : 0xffu;
     } else {
 #pragma unroll
       for (int j = 0; j < kCols; ++j) {
@@ -109,7 +130,7 @@ struct Fetched {
         w[j % kWords] = F32 ? reinterpret_cast<const uint32_t *>(row)[c] : (uint32_t)reinterpret_cast<const uint16_t *>(row)[c];
       }
       // a warp's columns j are one word: lane j holds it
-      bits = allowed ? __ldg(allowed + min((column<VEC>(0) >> 5) + kLogitThreads / 32 * (tid & 7), (left - 1) >> 5)) : 0xffffffffu;
+      bits = allowed ? __ldg(reinterpret_cast<const uint32_t *>(allowed) + min((column<VEC>(0) >> 5) + kLogitThreads / 32 * (tid & 7), (left - 1) >> 5)) : 0xffffffffu;
     }
   }
   __device__ __forceinline__ uint32_t ready(Raw<F32> &x) const {
@@ -129,14 +150,12 @@ struct Fetched {
 };
 
 template <bool F32, bool VEC>
-__device__ __forceinline__ void store_row(char *row, int left, const Raw<F32> &x) {
-  constexpr int kBytes = F32 ? 4 : 2;
+__device__ __forceinline__ void store_row(char *row, int left, const Raw<F32> &x) {  // row: as Fetched::load
   if (VEC) {
     if (column<VEC>(0) < left) {
 #pragma unroll
       for (int q = 0; q < Raw<F32>::kWords; q += 4)
-        *reinterpret_cast<uint4 *>(row + kBytes * column<VEC>(0) + 4 * q) =
-            make_uint4(x.w[q], x.w[q + 1], x.w[q + 2], x.w[q + 3]);
+        *reinterpret_cast<uint4 *>(row + 4 * q) = make_uint4(x.w[q], x.w[q + 1], x.w[q + 2], x.w[q + 3]);
     }
   } else {
 #pragma unroll
@@ -162,7 +181,8 @@ template <class Col>
 __device__ __forceinline__ void warp_argmax(unsigned long long *key, float best, Col col) {
   const uint32_t k = best == -INFINITY ? 0u : float_key(best);
   const uint32_t m = __reduce_max_sync(0xffffffffu, k);
-  if (m == 0u) return;
+  // Most warps are below what their row has already: the rest is for the others.
+  if (m == 0u || m < reinterpret_cast<volatile uint32_t *>(key)[1]) return;
   uint32_t c = 0xffffffffu;
   if (k == m) c = (uint32_t)col();
   c = __reduce_min_sync(0xffffffffu, c);
@@ -176,18 +196,48 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   __shared__ unsigned long long s_key[DFV_MAX_TREE];
   __shared__ int s_tok[DFV_MAX_TREE];                  // drafted tokens, from the slice's start
   __shared__ uint64_t s_same[DFV_MAX_TREE];            // nodes with the token of this (first) one
+  __shared__ uint64_t s_mask[DFV_MAX_TREE];            // the rows' own paths
+  __shared__ uint32_t s_floor[DFV_MAX_TREE];           // a row's best so far, or less: skips most of the argmax
+  __shared__ uint2 s_table[16];
+  __shared__ float s_rep, s_freq, s_pres;
   __shared__ int s_n;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
   const int v0 = blockIdx.y * kSlice, left = min(kSlice, p.V - v0);  // columns of the slice
-  const int r0 = p.t.row_off[b], r1 = p.t.row_off[b + 1], n = r1 - r0;
+  // what needs no other load first is on its way together: a chain of loads is
+  // most of a short call's time
+  const int r0 = __ldg(p.t.row_off + b), r1 = __ldg(p.t.row_off + b + 1), n = r1 - r0;
+  const int32_t *h = p.r.hist ? p.r.hist + b * p.r.hist_row : nullptr;
+  // four tokens a load from the first 16-byte boundary on, the first ones before
+  // the history's length is known
+  const int head = h ? (int)((16u - ((uint32_t)(uintptr_t)h & 15u)) & 15u) / 4 : 0;
+  const int4 *h4 = reinterpret_cast<const int4 *>(h + head);
+  int4 early[kEarly];
+  int said = 0, prompt = 0;
+  if (h) {
+    said = __ldg(p.r.hist_len + b);
+    if (p.r.prompt_len) prompt = __ldg(p.r.prompt_len + b);
+#pragma unroll
+    for (int e = 0; e < kEarly; ++e) {
+      early[e] = make_int4(-1, -1, -1, -1);
+      if (head + 4 * (tid + e * kLogitThreads) + 4 <= p.r.hist_row) early[e] = __ldg(h4 + tid + e * kLogitThreads);
+    }
+  }
   if (r0 < 0 || r1 > p.t.n_rows || n > p.t.max_nodes || n <= (int)blockIdx.z) return;
   const bool pen = p.r.repetition || p.r.frequency || p.r.presence;
   const float *bias = p.r.bias ? p.r.bias + b * p.r.bias_row + v0 : nullptr;
   constexpr int kBytes = F32 ? 4 : 2;
   constexpr int kRowsAhead = F32 || !VEC ? 2 : 4;  // rows whose logits are in flight: 8 or 16 registers
-  if (tid < DFV_MAX_TREE) s_key[tid] = 0ull;
+  // a row starts from what the slices that are done have found
+  if (tid < n) {
+    s_key[tid] = p.argmax && gridDim.y > 1 ? __ldcg(p.key + r0 + tid) : 0ull;
+    s_floor[tid] = Raw<F32>::floor_of((uint32_t)(s_key[tid] >> 32));
+  }
+  if (tid >= 64 && tid < 80) {
+    auto pair = [&](int k) { return (tid >> k & 1 ? 0xffffu : 0u) | (tid >> k & 2 ? 0xffff0000u : 0u); };
+    s_table[tid - 64] = make_uint2(pair(0), pair(2));
+  }
 
   // rows i0, i0 + gridDim.z, ... of the sequence, and their masks: the first ones
   // are on their way while the history is counted
@@ -195,10 +245,19 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
 #pragma unroll
   for (int j = 0; j < kCols; ++j) inside |= (column<VEC>(j) < left ? 1u : 0u) << j;
   Fetched<F32, VEC> ahead[kRowsAhead];
-  auto fetch = [&](int q, int i) {
-    if (i < n)
-      ahead[q].load(p.x + kBytes * ((r0 + i) * p.row + v0),
-                    p.r.allowed ? p.r.allowed + (r0 + i) * p.r.allowed_row + v0 / 32 : nullptr, left);
+  // addresses move from row to row: a 64-bit product for each cost a third of the walk
+  const int own = VEC ? column<VEC>(0) : 0;
+  const long long x_step = kBytes * p.row * (int)gridDim.z, out_step = kBytes * p.out_row * (int)gridDim.z,
+                  allowed_step = 4 * p.r.allowed_row * (int)gridDim.z;
+  const char *x_at = p.x + kBytes * ((r0 + (int)blockIdx.z) * p.row + v0 + own);
+  const uint8_t *allowed_at = nullptr;
+  if (p.r.allowed)
+    allowed_at = reinterpret_cast<const uint8_t *>(p.r.allowed + (r0 + (int)blockIdx.z) * p.r.allowed_row + v0 / 32) + own / 8;
+  auto fetch = [&](int q, int i) {  // in the rows' order
+    if (i >= n) return;
+    ahead[q].load(x_at, allowed_at, left);
+    x_at += x_step;
+    if (allowed_at) allowed_at += allowed_step;
   };
 #pragma unroll
   for (int q = 0; q < kRowsAhead; ++q) fetch(q, blockIdx.z + q * gridDim.z);
@@ -211,12 +270,16 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   if (pen) {
     for (int i = tid; i < kSlice / 4; i += kLogitThreads) reinterpret_cast<uint4 *>(s_cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (tid == 0) s_n = 0;
-    if (tid < n) s_tok[tid] = p.tokens[r0 + tid] - v0;
+    if (tid < n) {
+      s_tok[tid] = p.tokens[r0 + tid] - v0;
+      s_mask[tid] = row_mask(p.t, r0, tid);
+    }
+    if (tid == 64) s_rep = p.r.repetition ? p.r.repetition[b] : 1.f;
+    if (tid == 65) s_freq = p.r.frequency ? p.r.frequency[b] : 0.f;
+    if (tid == 66) s_pres = p.r.presence ? p.r.presence[b] : 0.f;
     __syncthreads();
-    if (p.r.hist) {
-      const int32_t *h = p.r.hist + b * p.r.hist_row;
-      const int len = (int)min((long long)p.r.hist_len[b], (long long)p.r.hist_row);
-      const int prompt = p.r.prompt_len ? p.r.prompt_len[b] : 0;
+    if (h) {
+      const int len = (int)min((long long)said, (long long)p.r.hist_row);
       auto count = [&](int token, int i) {
         const unsigned c = (unsigned)token - (unsigned)v0;
         if (c < (unsigned)left) {
@@ -226,19 +289,19 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
             atomicAdd(&s_cnt[c], 1u);
         }
       };
-      // four tokens a load from the first 16-byte boundary on
-      const int head = min(max(len, 0), (int)((16u - ((uint32_t)(uintptr_t)h & 15u)) & 15u) / 4), quads = max(len - head, 0) / 4;
-      const int4 *h4 = reinterpret_cast<const int4 *>(h + head);
-#pragma unroll 2
-      for (int i = tid; i < quads; i += kLogitThreads) {
-        const int4 t = __ldg(h4 + i);
+      const int quads = max(len - head, 0) / 4, rest = head + 4 * quads;
+      auto count4 = [&](const int4 &t, int i) {
         count(t.x, head + 4 * i);
         count(t.y, head + 4 * i + 1);
         count(t.z, head + 4 * i + 2);
         count(t.w, head + 4 * i + 3);
-      }
-      const int rest = head + 4 * quads;
-      if (tid < head) count(h[tid], tid);
+      };
+#pragma unroll
+      for (int e = 0; e < kEarly; ++e)
+        if (tid + e * kLogitThreads < quads) count4(early[e], tid + e * kLogitThreads);
+#pragma unroll 2
+      for (int i = tid + kEarly * kLogitThreads; i < quads; i += kLogitThreads) count4(__ldg(h4 + i), i);
+      if (tid < min(head, len)) count(h[tid], tid);
       if (tid >= 32 && tid - 32 < len - rest) count(h[rest + tid - 32], rest + tid - 32);
     }
     if (tid < n && (unsigned)s_tok[tid] < (unsigned)left) {
@@ -264,35 +327,39 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
 #pragma unroll
     for (int j = 0; j < kCols; ++j)
       if (listed >> j & 1u) s_list[at++] = (uint16_t)column<VEC>(j);
+  } else {
+    __syncthreads();  // s_key
   }
-  __syncthreads();
 
   // ---- all rows, dense: bias and mask
   uint32_t keep[Raw<F32>::kWords];
   spread<F32>(listed, keep);
   // bias and mask of a row; afterwards x is what is stored, y what may win
   auto apply = [&](Raw<F32> &x, uint32_t ok, Raw<F32> &y) {
-    if (bias) {
 #pragma unroll
-      for (int j = 0; j < Raw<F32>::kWords; ++j) {
-        if (F32)
-          y.w[j] = __float_as_uint(__fadd_rn(x.at(j), bv[j]));
-        else
-          y.w[j] = pack2<false>(__fadd_rn(x.at(2 * j), bv[2 * j % kCols]),
-                                __fadd_rn(x.at(2 * j + 1), bv[(2 * j + 1) % kCols]));
-        x.w[j] = (x.w[j] & keep[j]) | (y.w[j] & ~keep[j]);
-      }
+    for (int j = 0; j < Raw<F32>::kWords; ++j) {
+      y.w[j] = x.w[j];
+      if (!bias) continue;
+      if (F32)
+        y.w[j] = __float_as_uint(__fadd_rn(x.at(j), bv[j]));
+      else
+        y.w[j] = pack2<false>(__fadd_rn(x.at(2 * j), bv[2 * j % kCols]),
+                              __fadd_rn(x.at(2 * j + 1), bv[(2 * j + 1) % kCols]));
     }
     // not allowed: -inf; listed: stored as they came, out of the argmax
     uint32_t okm[Raw<F32>::kWords];
-    spread<F32>(ok, okm);
+    if constexpr (F32)
+      spread<F32>(ok, okm);
+    else
+      spread_pairs(s_table, ok, okm);
 #pragma unroll
     for (int j = 0; j < Raw<F32>::kWords; ++j) {
       const uint32_t may = okm[j] & ~keep[j];
-      y.w[j] = (x.w[j] & may) | (Raw<F32>::kNegInf & ~may);
+      y.w[j] = (y.w[j] & may) | (Raw<F32>::kNegInf & ~may);
       x.w[j] = (y.w[j] & ~keep[j]) | (x.w[j] & keep[j]);
     }
   };
+  char *out_at = p.out + kBytes * ((r0 + (int)blockIdx.z) * p.out_row + v0 + own);
   for (int i0 = blockIdx.z; i0 < n; i0 += kRowsAhead * gridDim.z) {
 #pragma unroll
     for (int q = 0; q < kRowsAhead; ++q) {
@@ -301,17 +368,23 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
       Raw<F32> x, y;
       const uint32_t ok = ahead[q].ready(x) & inside;  // past the slice's end nothing may win
       apply(x, ok, y);
-      if (p.out) store_row<F32, VEC>(p.out + kBytes * ((r0 + i) * p.out_row + v0), left, x);
+      if (p.out) store_row<F32, VEC>(out_at, left, x);
+      out_at += out_step;
       fetch(q, i + kRowsAhead * gridDim.z);
       if (p.argmax) {
-        const float best = y.largest();
-        warp_argmax(&s_key[i], best, [&]() {
-          int bj = 0;
+        const uint32_t top = y.largest();
+        if (__any_sync(0xffffffffu, Raw<F32>::reaches(top, *static_cast<volatile uint32_t *>(&s_floor[i])))) {
+          const float best = Raw<F32>::value(top);
+          warp_argmax(&s_key[i], best, [&]() {
+            int bj = 0;
 #pragma unroll
-          for (int j = kCols - 1; j >= 0; --j)
-            if (y.at(j) == best) bj = j;
-          return v0 + column<VEC>(bj);
-        });
+            for (int j = kCols - 1; j >= 0; --j)
+              if (y.at(j) == best) bj = j;
+            return v0 + column<VEC>(bj);
+          });
+          // never above the row's best: any of the values stored here is one of its logits
+          if (lane == 0) s_floor[i] = Raw<F32>::floor_of(reinterpret_cast<volatile uint32_t *>(&s_key[i])[1]);
+        }
       }
     }
   }
@@ -320,8 +393,7 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   if (pen) {
     __syncthreads();  // the dense walk's stores come first
     const int m = s_n;
-    const float rep = p.r.repetition ? p.r.repetition[b] : 1.f, freq = p.r.frequency ? p.r.frequency[b] : 0.f,
-                pres = p.r.presence ? p.r.presence[b] : 0.f;
+    const float rep = s_rep, freq = s_freq, pres = s_pres;
     // a warp takes a row, or several a row with fewer rows than warps; kAhead
     // columns of a lane are in flight
     constexpr int kW = kLogitThreads / 32;
@@ -332,7 +404,7 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
       const char *from = p.x + kBytes * ((r0 + i) * p.row + v0);
       char *to = p.out + kBytes * ((r0 + i) * p.out_row + v0);
       const uint32_t *words = p.r.allowed ? p.r.allowed + (r0 + i) * p.r.allowed_row + v0 / 32 : nullptr;
-      const uint64_t mask = row_mask(p.t, r0, i);
+      const uint64_t mask = s_mask[i];
       float best = -INFINITY;
       int bc = 0x7fffffff;
       for (int k0 = part * 32 * kAhead + lane; k0 < m; k0 += share * 32 * kAhead) {
