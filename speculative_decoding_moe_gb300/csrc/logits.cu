@@ -1,10 +1,11 @@
 // logits.cu -- penalties for repeated tokens, biases and grammar masks on the
 // logits of drafted nodes, with the argmax of each row in the same pass.
 //
-// Bound by memory, next by issue: every logit is read and written once, with some
-// 15 instructions a column.  Measured on the device: 512 rows of 151936 bf16 with
-// every rule and 4093 tokens of history 89 us (3.0 TB/s), without rules 55 us
-// (5.7 TB/s); one row 6.4 us.  A CTA owns a slice of
+// Bound by issue before memory: every logit is read and written once, with some 20
+// instructions a column with every rule and 15 without, two thirds of the issue
+// slots taken.  Measured on the device: 32 trees of up to 16 nodes (390 rows) of
+// 151936 bf16 with every rule and 4093 tokens of history 75 us (3.5 TB/s), without
+// rules 49 us (4.8 TB/s); one row 6.6 us.  A CTA owns a slice of
 // kSlice vocabulary columns of one sequence, eight columns per thread, and
 // walks rows of the sequence: the thread's bias and its knowledge of which
 // columns repeat stay in registers over the rows, several rows' loads are in
@@ -17,6 +18,8 @@
 // afterwards warps apply all steps to the listed columns, where the row's own
 // path adds to the counts.  (Applying the steps in the dense walk took
 // twice the instructions: some lane of a warp nearly always meets a token.)
+#include <algorithm>
+
 #include "tree_common.cuh"
 
 namespace dfv {
@@ -475,9 +478,14 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
 
 cudaError_t launch_logits(const LogitsParams &p, cudaStream_t s) {
   const int slices = (p.V + kSlice - 1) / kSlice;
-  // rows of a sequence share a CTA's counts; they are spread over more CTAs only
-  // while those would not give every SM three
-  int z = (456 + slices * p.t.n_seqs - 1) / (slices * p.t.n_seqs);
+  // Rows of a sequence share a CTA's counts.  They are spread over as many CTAs as
+  // run at once, which ends soonest with few rows (16 nodes of one sequence: 12 us
+  // so, 17 with half as many CTAs again); over twice as many where that leaves more
+  // than eight rows each, so that one CTA's counting overlaps another's rows (4 x 64
+  // nodes: 56 us so, 61 in one round).
+  const int resident = 2 * kAttnCtas, ctas = (int)std::min((long long)slices * p.t.n_seqs, 4ll * resident);
+  int z = resident / ctas;
+  if (z < 1 || p.t.max_nodes > 8 * z) z = 2 * resident / ctas;
   z = z < 1 ? 1 : z > p.t.max_nodes ? p.t.max_nodes : z;
   // the first slices first: in most vocabularies the low ids are the frequent
   // tokens, so those CTAs have the longest lists
