@@ -1,11 +1,11 @@
 // logits.cu -- penalties for repeated tokens, biases and grammar masks on the
 // logits of drafted nodes, with the argmax of each row in the same pass.
 //
-// Bound by issue before memory: every logit is read and written once, with some 20
-// instructions a column with every rule and 15 without, two thirds of the issue
-// slots taken.  Measured on the device: 32 trees of up to 16 nodes (390 rows) of
-// 151936 bf16 with every rule and 4093 tokens of history 75 us (3.5 TB/s), without
-// rules 49 us (4.8 TB/s); one row 6.6 us.  A CTA owns a slice of
+// Bound by issue before memory: every logit is read and written once, with some 26
+// instructions a column with every rule and 16 without, 60 % of the issue slots
+// taken.  Measured on the device: 32 trees of up to 16 nodes (390 rows) of 151936
+// bf16 with every rule and 4093 tokens of history 73 us (3.6 TB/s), without rules
+// 47 us (5.1 TB/s); one row 6.5 us.  A CTA owns a slice of
 // kSlice vocabulary columns of one sequence, eight columns per thread, and
 // walks rows of the sequence: the thread's bias and its knowledge of which
 // columns repeat stay in registers over the rows, several rows' loads are in
@@ -174,6 +174,16 @@ __device__ __forceinline__ void store_row(char *row, int left, const Raw<F32> &x
   }
 }
 
+// Two sums, each rounded to nearest.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long x, y;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(y));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(x));
+  return a;
+}
+
 __device__ __forceinline__ float round_bf16(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 
 // The largest of a warp's values (the lowest column among equals) into *key;
@@ -245,8 +255,12 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   // rows i0, i0 + gridDim.z, ... of the sequence, and their masks: the first ones
   // are on their way while the history is counted
   uint32_t inside = 0u;
+  if (VEC) {
+    inside = column<VEC>(0) < left ? 0xffu : 0u;
+  } else {
 #pragma unroll
-  for (int j = 0; j < kCols; ++j) inside |= (column<VEC>(j) < left ? 1u : 0u) << j;
+    for (int j = 0; j < kCols; ++j) inside |= (column<VEC>(j) < left ? 1u : 0u) << j;
+  }
   Fetched<F32, VEC> ahead[kRowsAhead];
   // addresses move from row to row: a 64-bit product for each cost a third of the walk
   const int own = VEC ? column<VEC>(0) : 0;
@@ -268,8 +282,15 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   // ---- the thread's columns
   float bv[kCols];
   uint32_t listed = 0u;  // bit j: penalties may touch column j
+  if (VEC && ((uint32_t)(uintptr_t)bias & 15u) == 0u) {
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f), *from = reinterpret_cast<const float4 *>(bias) + 2 * tid;
+    const bool some = bias && inside;
+    const float4 a = some ? from[0] : none, b = some ? from[1] : none;
+    bv[0] = a.x; bv[1] = a.y; bv[2] = a.z; bv[3] = a.w; bv[4] = b.x; bv[5] = b.y; bv[6] = b.z; bv[7] = b.w;
+  } else {
 #pragma unroll
-  for (int j = 0; j < kCols; ++j) bv[j] = bias && column<VEC>(j) < left ? bias[column<VEC>(j)] : 0.f;
+    for (int j = 0; j < kCols; ++j) bv[j] = bias && column<VEC>(j) < left ? bias[column<VEC>(j)] : 0.f;
+  }
   if (pen) {
     for (int i = tid; i < kSlice / 4; i += kLogitThreads) reinterpret_cast<uint4 *>(s_cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (tid == 0) s_n = 0;
@@ -314,9 +335,17 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
       if (__ffsll((long long)same) - 1 == tid) atomicOr(&s_cnt[s_tok[tid]], kTreeBit | (uint32_t)tid << kNodeShift);
     }
     __syncthreads();
+    if (VEC) {
+      const uint4 *from = reinterpret_cast<const uint4 *>(s_cnt) + 2 * tid;
+      const uint4 a = from[0], b = from[1];
+      const uint32_t w[kCols] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int j = 0; j < kCols; ++j)
-      if (s_cnt[column<VEC>(j)]) listed |= 1u << j;
+      for (int j = 0; j < kCols; ++j) listed |= (w[j] ? 1u : 0u) << j;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kCols; ++j)
+        if (s_cnt[column<VEC>(j)]) listed |= 1u << j;
+    }
     int at = 0;
     const int mine = __popc(listed);
     int run = mine;
@@ -339,26 +368,29 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   spread<F32>(listed, keep);
   // bias and mask of a row; afterwards x is what is stored, y what may win
   auto apply = [&](Raw<F32> &x, uint32_t ok, Raw<F32> &y) {
+    if (bias) {
 #pragma unroll
-    for (int j = 0; j < Raw<F32>::kWords; ++j) {
-      y.w[j] = x.w[j];
-      if (!bias) continue;
-      if (F32)
-        y.w[j] = __float_as_uint(__fadd_rn(x.at(j), bv[j]));
-      else
-        y.w[j] = pack2<false>(__fadd_rn(x.at(2 * j), bv[2 * j % kCols]),
-                              __fadd_rn(x.at(2 * j + 1), bv[(2 * j + 1) % kCols]));
+      for (int j = 0; j < kCols; j += 2) {
+        const float2 z = add2(make_float2(x.at(j), x.at(j + 1)), make_float2(bv[j], bv[j + 1]));
+        if (F32) {
+          y.w[j % Raw<F32>::kWords] = __float_as_uint(z.x);
+          y.w[(j + 1) % Raw<F32>::kWords] = __float_as_uint(z.y);
+        } else {
+          y.w[j / 2 % Raw<F32>::kWords] = pack2<false>(z.x, z.y);
+        }
+      }
+    } else {
+      y = x;
     }
     // not allowed: -inf; listed: stored as they came, out of the argmax
-    uint32_t okm[Raw<F32>::kWords];
+    uint32_t may[Raw<F32>::kWords];
     if constexpr (F32)
-      spread<F32>(ok, okm);
+      spread<F32>(ok & ~listed, may);
     else
-      spread_pairs(s_table, ok, okm);
+      spread_pairs(s_table, ok & ~listed, may);
 #pragma unroll
     for (int j = 0; j < Raw<F32>::kWords; ++j) {
-      const uint32_t may = okm[j] & ~keep[j];
-      y.w[j] = (y.w[j] & may) | (Raw<F32>::kNegInf & ~may);
+      y.w[j] = (y.w[j] & may[j]) | (Raw<F32>::kNegInf & ~may[j]);
       x.w[j] = (y.w[j] & ~keep[j]) | (x.w[j] & keep[j]);
     }
   };
