@@ -478,7 +478,8 @@ template <bool F16, int D>
 cudaError_t launch_mma(const AttnLaunch &L, cudaStream_t s) {
   auto kern = tree_attn_mma_kernel<F16, D>;
   const size_t smem = MmaShape<D>::kSmem;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
   return launch_chained(kern, dim3(L.n_groups * L.n_rt), dim3(kMmaThreads), smem, s, L);
 }

@@ -619,7 +619,8 @@ template <bool F16, int D, bool DUAL>
 cudaError_t launch_one(const AttnLaunch &L, cudaStream_t s) {
   auto kern = tree_attn_tc_kernel<F16, D, DUAL>;
   const size_t smem = TcShape<D, DUAL>::kSmem;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
   return launch_chained(kern, dim3(L.n_groups * L.n_rt), dim3(kTThreads), smem, s, L);
 }
