@@ -6,6 +6,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -59,8 +60,9 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     def compile_binding():
         import torch
         at = os.path.join(os.path.dirname(torch.__file__), "include")
+        cuda = os.path.join(os.path.dirname(os.path.dirname(shutil.which(NVCC) or "/usr/local/cuda/bin/nvcc")), "include")
         cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", at,
-               "-I", os.path.join(at, "torch", "csrc", "api", "include"), "-c", BIND_SRC, "-o", bind_obj]
+               "-I", os.path.join(at, "torch", "csrc", "api", "include"), "-I", cuda, "-c", BIND_SRC, "-o", bind_obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("compiling the binding failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
@@ -79,7 +81,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     tmp = BIND + ".tmp.%d" % os.getpid()
     # libdfv.so is found beside the extension; torch's libraries are loaded by then
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, bind_obj, "-L", HERE, "-l:libdfv.so", "-Wl,-rpath,$ORIGIN",
-           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("linking the binding failed:\n%s\n%s" % (" ".join(cmd), r.stderr))

@@ -3,8 +3,8 @@
 //
 // A decode step makes dozens of these calls, and checking and marshalling one in
 // Python took longer than its kernels: 18 us for an attention call whose kernels
-// take 10, and 6.6 here, of which two launches and two tensor maps are 4.4 and the
-// result's allocation 2 (a rotary call 3.6, of which the result's 1.5).  Tensors are read through ATen, results allocated
+// take 10, and 5.5 here, of which two launches and two tensor maps are 4.0 and the
+// result's allocation 1.4 (a rotary call 3.1, of which the result's 1.1).  Tensors are read through ATen, results allocated
 // by torch's allocator; everything else goes through include/dfv.h as for any
 // other caller.  Refusals are the binding's own TypeError and ValueError, a
 // status of the library is its DfvError.
@@ -18,7 +18,7 @@
 #include <string>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/dfv.h"
@@ -101,8 +101,14 @@ Rows3 rows3(const at::Tensor &t, const char *what, int64_t rows, int64_t heads, 
   return {t.data_ptr(), rows > 1 ? t.stride(0) : 0, heads > 1 ? t.stride(1) : 0};
 }
 
+// The last check before a launch: host tensors pass the ones of type and shape.
+void on_gpu(int index) {
+  if (index < 0) value_error("the tensors of the call must be CUDA tensors");
+}
+// A result, from torch's allocator without its dispatcher (1.1 us instead of 1.6).
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType dt, const at::Tensor &like) {
-  return at::empty(shape, at::TensorOptions().dtype(dt).device(like.device()));
+  on_gpu(like.get_device());
+  return at::Tensor(at::detail::empty_cuda(shape, dt, like.device(), std::nullopt));
 }
 
 template <class T>
@@ -148,10 +154,6 @@ Space space(PyObject *o, int index) {
 }
 void together(const Cache &c, const Tree &t) {
   if (c.index != t.index) value_error("cache and tree are not on one device");
-}
-// The last check before a launch: host tensors pass the ones above.
-void on_gpu(int index) {
-  if (index < 0) value_error("the tensors of the call must be CUDA tensors");
 }
 
 // Raises DfvError(status, where) of the Python module unless the status is 0.
@@ -249,7 +251,7 @@ PyObject *logits_process(PyObject *const *a) {
   const int store = PyObject_IsTrue(a[7]);
   if (store < 0) throw Refused();
   at::Tensor made, best;
-  void *out = nullptr;
+  void *arg = given(a[6], "argmax", at::kInt, {rows}, t.index), *out = nullptr;
   int64_t out_row = 0;
   if (!store) {
     if (a[5] != Py_None) value_error("store=False takes no out");
@@ -261,8 +263,10 @@ PyObject *logits_process(PyObject *const *a) {
     out = o.data_ptr();
     out_row = rows > 1 ? o.stride(0) : V;
   }
-  if (a[6] == Py_None) best = empty({rows}, at::kInt, x);
-  void *arg = best.defined() ? best.data_ptr() : need(a[6], "argmax", at::kInt, {rows}, t.index);
+  if (!arg) {
+    best = empty({rows}, at::kInt, x);
+    arg = best.data_ptr();
+  }
   on_gpu(t.index);
   done(dfv_logits_process(x.data_ptr(), rows > 1 ? x.stride(0) : V, dt == at::kFloat ? DFV_F32 : DFV_BF16, (int)V, &t.c,
                           static_cast<const int32_t *>(tok), &r.c, out, out_row, static_cast<int32_t *>(arg),
@@ -282,22 +286,20 @@ PyObject *accept_tree(PyObject *const *a) {
   const int64_t rows = t.c.n_rows, S = t.c.n_seqs;
   const void *tok = need(a[1], "tokens", at::kInt, {rows}, t.index), *target = need(a[2], "target", at::kInt, {rows}, t.index);
   const at::Tensor &like = tensor(a[1], "tokens");
-  at::Tensor path, tau;
   int64_t width = t.c.max_nodes;
-  void *pp, *tp;
-  if (a[3] == Py_None) {
-    path = empty({S, width}, at::kInt, like);
-    pp = path.data_ptr();
-  } else {
+  if (a[3] != Py_None) {
     const at::Tensor &g = tensor(a[3], "path");
     width = g.dim() == 2 ? g.size(1) : -1;
-    pp = need(a[3], "path", at::kInt, {S, width}, t.index);
   }
-  if (a[4] == Py_None) {
+  void *pp = given(a[3], "path", at::kInt, {S, width}, t.index), *tp = given(a[4], "tau", at::kInt, {S}, t.index);
+  at::Tensor path, tau;
+  if (!pp) {
+    path = empty({S, width}, at::kInt, like);
+    pp = path.data_ptr();
+  }
+  if (!tp) {
     tau = empty({S}, at::kInt, like);
     tp = tau.data_ptr();
-  } else {
-    tp = need(a[4], "tau", at::kInt, {S}, t.index);
   }
   on_gpu(t.index);
   done(dfv_accept_tree(&t.c, static_cast<const int32_t *>(tok), static_cast<const int32_t *>(target),
