@@ -4,10 +4,10 @@
 // A decode step makes dozens of these calls, and checking and marshalling one in
 // Python took longer than its kernels: 18 us for an attention call whose kernels
 // take 10, and 5.5 here, of which two launches and two tensor maps are 4.0 and the
-// result's allocation 1.4 (a rotary call 3.1, of which the result's 1.1).  Tensors are read through ATen, results allocated
-// by torch's allocator; everything else goes through include/dfv.h as for any
-// other caller.  Refusals are the binding's own TypeError and ValueError, a
-// status of the library is its DfvError.
+// result's allocation 1.4 (a rotary call 3.1, of which the result's 1.1).  Tensors
+// are read through ATen, results allocated by torch's allocator; everything else
+// goes through include/dfv.h as for any other caller.  Refusals are the binding's
+// own TypeError and ValueError, a status of the library is its DfvError.
 #include <Python.h>
 
 #include <cmath>

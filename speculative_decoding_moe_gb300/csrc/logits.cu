@@ -54,6 +54,19 @@ struct Raw {
     if (F32) return __uint_as_float(w[j % kWords]);
     return j & 1 ? bf16_hi(w[j / 2 % kWords]) : bf16_lo(w[j / 2 % kWords]);
   }
+  // a column whose number is not known when compiling, without local memory
+  __device__ __forceinline__ float pick(int j) const {
+    uint32_t v = 0u;
+#pragma unroll
+    for (int q = 0; q < kWords; ++q)
+      if (q == (F32 ? j : j >> 1)) v = w[q];
+    return __uint_as_float(F32 ? v : j & 1 ? v & 0xffff0000u : v << 16);
+  }
+  __device__ __forceinline__ void put(int j, uint32_t f) {  // f: fp32 bits of a value of the type
+#pragma unroll
+    for (int q = 0; q < kWords; ++q)
+      if (q == (F32 ? j : j >> 1)) w[q] = F32 ? f : __byte_perm(w[q], f, j & 1 ? 0x7610 : 0x3276);
+  }
   // the largest column: fp32, or one of a pair
   __device__ __forceinline__ uint32_t largest() const {
     if (F32) {
@@ -202,7 +215,12 @@ __device__ __forceinline__ void warp_argmax(unsigned long long *key, float best,
   if ((threadIdx.x & 31) == 0) atomicMax(key, ((unsigned long long)m << 32) | (0xffffffffu - c));
 }
 
-template <bool F32, bool VEC>
+// ONE: one row a CTA, and more CTAs than run at once.  The walk takes every step
+// itself where a column is met, which is less work than the list, a barrier and
+// reading the columns again (32 single rows with 4093 tokens of history 29 -> 26 us,
+// with 200 tokens 25 -> 20).  Where all CTAs run at once the lanes that meet many
+// columns, one after the other, decide: one row 8 -> 10 us.
+template <bool F32, bool VEC, bool ONE>
 __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsParams p) {
   __shared__ __align__(16) uint32_t s_cnt[kSlice];
   __shared__ uint16_t s_list[kSlice];
@@ -241,7 +259,7 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   const bool pen = p.r.repetition || p.r.frequency || p.r.presence;
   const float *bias = p.r.bias ? p.r.bias + b * p.r.bias_row + v0 : nullptr;
   constexpr int kBytes = F32 ? 4 : 2;
-  constexpr int kRowsAhead = F32 || !VEC ? 2 : 4;  // rows whose logits are in flight: 8 or 16 registers
+  constexpr int kRowsAhead = F32 || !VEC || ONE ? 2 : 4;  // rows whose logits are in flight: 8 or 16 registers
   // a row starts from what the slices that are done have found
   if (tid < n) {
     s_key[tid] = p.argmax && gridDim.y > 1 ? __ldcg(p.key + r0 + tid) : 0ull;
@@ -279,9 +297,23 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
 #pragma unroll
   for (int q = 0; q < kRowsAhead; ++q) fetch(q, blockIdx.z + q * gridDim.z);
 
+  // steps 1-5 of dfv_logits_process on a column that penalties may touch, every
+  // product, quotient and difference rounded on its own (no contraction)
+  auto steps = [&](float y, uint32_t w, uint64_t mask, float add, bool ok, float rep, float freq, float pres) {
+    uint32_t cnt = w & kCountMask;
+    if (w & kTreeBit) cnt += __popcll(s_same[w >> kNodeShift & 63u] & mask);
+    if (p.r.repetition && (cnt || (w & kPromptBit))) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
+    if (p.r.frequency) y = __fsub_rn(y, __fmul_rn(freq, (float)cnt));
+    if (p.r.presence && cnt) y = __fsub_rn(y, pres);
+    if (bias) y = __fadd_rn(y, add);
+    if (!ok) y = -INFINITY;
+    return F32 ? y : round_bf16(y);
+  };
+  const int rows = (n - (int)blockIdx.z + (int)gridDim.z - 1) / (int)gridDim.z;  // of this CTA
+
   // ---- the thread's columns
   float bv[kCols];
-  uint32_t listed = 0u;  // bit j: penalties may touch column j
+  uint32_t listed = 0u, touched = 0u;  // bit j: penalties may touch column j; listed: their steps come after the walk
   if (VEC && ((uint32_t)(uintptr_t)bias & 15u) == 0u) {
     const float4 none = make_float4(0.f, 0.f, 0.f, 0.f), *from = reinterpret_cast<const float4 *>(bias) + 2 * tid;
     const bool some = bias && inside;
@@ -346,19 +378,24 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
       for (int j = 0; j < kCols; ++j)
         if (s_cnt[column<VEC>(j)]) listed |= 1u << j;
     }
-    int at = 0;
-    const int mine = __popc(listed);
-    int run = mine;
+    if (ONE) {
+      touched = listed;
+      listed = 0u;
+    } else {
+      int at = 0;
+      const int mine = __popc(listed);
+      int run = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, run, o);
-      if (lane >= o) run += a;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += a;
+      }
+      if (lane == 31) at = atomicAdd(&s_n, run);
+      at = __shfl_sync(0xffffffffu, at, 31) + run - mine;
+#pragma unroll
+      for (int j = 0; j < kCols; ++j)
+        if (listed >> j & 1u) s_list[at++] = (uint16_t)column<VEC>(j);
     }
-    if (lane == 31) at = atomicAdd(&s_n, run);
-    at = __shfl_sync(0xffffffffu, at, 31) + run - mine;
-#pragma unroll
-    for (int j = 0; j < kCols; ++j)
-      if (listed >> j & 1u) s_list[at++] = (uint16_t)column<VEC>(j);
   } else {
     __syncthreads();  // s_key
   }
@@ -367,6 +404,13 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   uint32_t keep[Raw<F32>::kWords];
   spread<F32>(listed, keep);
   // bias and mask of a row; afterwards x is what is stored, y what may win
+  auto bias_of = [&](int j) {
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < kCols; ++q)
+      if (q == j) v = bv[q];
+    return v;
+  };
   auto apply = [&](Raw<F32> &x, uint32_t ok, Raw<F32> &y) {
     if (bias) {
 #pragma unroll
@@ -402,7 +446,18 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
       if (i >= n) break;
       Raw<F32> x, y;
       const uint32_t ok = ahead[q].ready(x) & inside;  // past the slice's end nothing may win
-      apply(x, ok, y);
+      if (ONE) {
+        const Raw<F32> from = x;
+        apply(x, ok, y);
+        for (uint32_t c = touched; c; c &= c - 1u) {
+          const int j = __ffs((int)c) - 1;
+          y.put(j, __float_as_uint(steps(from.pick(j), s_cnt[column<VEC>(j)], s_mask[i], bias_of(j), ok >> j & 1u, s_rep,
+                                         s_freq, s_pres)));
+        }
+        x = y;  // nothing is listed
+      } else {
+        apply(x, ok, y);
+      }
       if (p.out) store_row<F32, VEC>(out_at, left, x);
       out_at += out_step;
       fetch(q, i + kRowsAhead * gridDim.z);
@@ -425,14 +480,13 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   }
 
   // ---- the listed columns: every step
-  if (pen) {
+  if (pen && !ONE) {
     __syncthreads();  // the dense walk's stores come first
     const int m = s_n;
     const float rep = s_rep, freq = s_freq, pres = s_pres;
     // a warp takes a row, or several a row with fewer rows than warps; kAhead
     // columns of a lane are in flight
     constexpr int kW = kLogitThreads / 32;
-    const int rows = (n - (int)blockIdx.z + (int)gridDim.z - 1) / (int)gridDim.z;  // of this CTA
     const int share = rows >= kW ? 1 : kW / rows;
     for (int u = warp; u < rows * share; u += kW) {
       const int i = blockIdx.z + (u / share) * gridDim.z, part = u % share;
@@ -459,18 +513,8 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
           if (k0 + 32 * q >= m) continue;
-          const uint32_t w = s_cnt[c[q]];
-          uint32_t cnt = w & kCountMask;
-          if (w & kTreeBit) cnt += __popcll(s_same[w >> kNodeShift & 63u] & mask);
-          // steps 1-5 of dfv_logits_process, every product, quotient and
-          // difference rounded on its own (no contraction)
-          float y = __uint_as_float(F32 ? raw[q] : raw[q] << 16);
-          if (p.r.repetition && (cnt || (w & kPromptBit))) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
-          if (p.r.frequency) y = __fsub_rn(y, __fmul_rn(freq, (float)cnt));
-          if (p.r.presence && cnt) y = __fsub_rn(y, pres);
-          if (bias) y = __fadd_rn(y, add[q]);
-          if (!(word[q] >> (c[q] & 31) & 1u)) y = -INFINITY;
-          if (!F32) y = round_bf16(y);
+          const float y = steps(__uint_as_float(F32 ? raw[q] : raw[q] << 16), s_cnt[c[q]], mask, add[q],
+                                word[q] >> (c[q] & 31) & 1u, rep, freq, pres);
           if (p.out) {
             if (F32)
               *reinterpret_cast<float *>(to + 4 * c[q]) = y;
@@ -506,6 +550,12 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   }
 }
 
+template <bool F32, bool VEC>
+cudaError_t launch_rows(const LogitsParams &p, bool one, dim3 grid, cudaStream_t s) {
+  return one ? launch_chained(logits_kernel<F32, VEC, true>, grid, dim3(kLogitThreads), 0, s, p)
+             : launch_chained(logits_kernel<F32, VEC, false>, grid, dim3(kLogitThreads), 0, s, p);
+}
+
 }  // namespace
 
 cudaError_t launch_logits(const LogitsParams &p, cudaStream_t s) {
@@ -525,11 +575,9 @@ cudaError_t launch_logits(const LogitsParams &p, cudaStream_t s) {
   const int esz = p.f32 ? 4 : 2;
   const bool vec = p.V % kCols == 0 && ((uintptr_t)p.x | (uintptr_t)p.out) % 16 == 0 && p.row * esz % 16 == 0 &&
                    (!p.out || p.out_row * esz % 16 == 0);
-  if (p.f32)
-    return vec ? launch_chained(logits_kernel<true, true>, grid, dim3(kLogitThreads), 0, s, p)
-               : launch_chained(logits_kernel<true, false>, grid, dim3(kLogitThreads), 0, s, p);
-  return vec ? launch_chained(logits_kernel<false, true>, grid, dim3(kLogitThreads), 0, s, p)
-             : launch_chained(logits_kernel<false, false>, grid, dim3(kLogitThreads), 0, s, p);
+  const bool one = p.t.max_nodes <= z && (long long)slices * p.t.n_seqs * z > resident;
+  if (p.f32) return vec ? launch_rows<true, true>(p, one, grid, s) : launch_rows<true, false>(p, one, grid, s);
+  return vec ? launch_rows<false, true>(p, one, grid, s) : launch_rows<false, false>(p, one, grid, s);
 }
 
 }  // namespace dfv

@@ -81,3 +81,12 @@ def test_bias_at_any_word(dfv, dtype, V, shift):  # noqa: F811
     ws = dfv.alloc_workspace(dfv.logits_workspace_size(job.rows))
     out, best = dfv.logits_process(x, tree, tokens, rules, ws)
     check(job, out, best)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [32008, 32003])
+@pytest.mark.parametrize("hist", [None, 30, 6000])
+def test_many_single_rows(dfv, dtype, V, hist):  # noqa: F811
+    """One row a sequence, more slices of them than CTAs run at once."""
+    job = Job(V, [1] * 45, dtype, seed=V + (hist or 0), hist=hist, bias=45, allowed=45, few=700)
+    check(job, *run(dfv, job))
