@@ -84,14 +84,14 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
   __shared__ SchedStart s_start;
   __shared__ long long s_scan[kMmaThreads / 32];
   __shared__ float2 s_ml[kCons][kRows];
-  __shared__ int s_bad;
+  __shared__ int s_bad[2];  // of a segment, in turn
   const TreeAttnParams &p = L.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = smem_u32(sm);
   unsigned char *s_state = sm + (size_t)kStages * 2 * kTileBytes;  // [warp][row][kPitch] fp32
   if (tid == 0) {
     s_abort = 0;
-    s_bad = 0;
+    s_bad[0] = s_bad[1] = 0;
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&s_full[s]), kProd);
       mbar_init(smem_u32(&s_empty[s]), 4);
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
   const int cw = (warp - kProd) & 3, group = (warp - kProd) >> 2, gr = lane >> 2, qc = lane & 3;
   const float c = p.scale_log2;
   constexpr float kBias = F16 ? 6.f : 0.f;
-  int st = group * S::kPer, ph = 0;
+  int st = group * S::kPer, ph = 0, turn = 0;
   bool ok = true;
   SegWalk<kKt, S::kOver> wk(L, s_start);
   while (wk.next()) {
@@ -290,9 +290,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
           *reinterpret_cast<float2 *>(mine + r * S::kPitch + n * 8 + 2 * qc) = make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
       }
     }
-    if (bad) s_bad = 1;
+    if (bad) s_bad[turn] = 1;
     bar_sync_n(1, 32 * kCons);
-    const int isbad = s_bad, ct = tid - 32 * kProd;
+    const int isbad = s_bad[turn], ct = tid - 32 * kProd;
     const bool whole = wk.whole();
     const int slot = wk.slot(blockIdx.x);
     // ---- the state of the whole segment: output, or partial state
@@ -329,8 +329,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
       }
     }
     if (ct == 0) wk.tell(s_start, blockIdx.x);
+    // the next segment's flag: last read before this segment's first barrier, set
+    // again after its last one.  (Its own flag cleared after the last barrier could
+    // take back what a warp of the other group, a segment ahead, had set.)
+    if (ct == 0) s_bad[turn ^ 1] = 0;
     bar_sync_n(1, 32 * kCons);  // the states' places are free
-    if (ct == 0) s_bad = 0;
+    turn ^= 1;
   }
 }
 
