@@ -541,11 +541,15 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
       tc_fence_after();
       const int rr = DUAL ? w * 128 + wt : wt;
       float M = m, lsum = l, f0 = 1.f, f1 = 1.f;
+      // all scores are done when either warpgroup's last product is: Q's place is free
+      float2 *ml = reinterpret_cast<float2 *>(s_q);
+      if (!DUAL && started) ml[w * 128 + wt] = make_float2(m, l);
+      // SINGLE: each warpgroup waited for its own products and reads both outputs, so
+      // what it learned about tensor memory goes through the barrier
+      tc_fence_before();
+      bar_sync_n(1, 256);  // the states, s_bad, and Q's place
+      tc_fence_after();
       if (!DUAL) {
-        // all scores are done when either warpgroup's last product is: Q's place is free
-        float2 *ml = reinterpret_cast<float2 *>(s_q);
-        if (started) ml[w * 128 + wt] = make_float2(m, l);
-        bar_sync_n(1, 256);
         const float2 a = ml[wt];
         const float2 b = n > 1 ? ml[128 + wt] : make_float2(-INFINITY, 0.f);
         M = fmaxf(a.x, b.x);
@@ -553,8 +557,6 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
         f0 = a.x == -INFINITY ? 1.f : ex2((a.x - M) * c);
         f1 = b.x == -INFINITY ? 1.f : ex2((b.x - M) * c);
         lsum = a.y * f0 + b.y * f1;
-      } else {
-        bar_sync_n(1, 256);  // s_bad, and Q's place
       }
       const int bad = s_bad;
       const float z = (M == -INFINITY ? 0.f : M * c) - kBias;

@@ -74,3 +74,16 @@ def test_the_model_finds_a_flag_cleared_late():
 @pytest.mark.parametrize("bad", [[(), (1,)], [(1,), ()], [(0,), (1,), ()], [(1,), (), (0, 1), ()], [(0, 2), (1,), (2,)]])
 def test_no_segment_loses_the_flag_of_a_value_that_is_not_finite(bad):
     assert lost_flags(protocol(), bad) == set()
+
+
+# ---------------------------------------------------------------- tensor memory read after another warpgroup's wait
+def test_outputs_in_tensor_memory_are_read_behind_fences():
+    """With one row tile each warpgroup waits for its own last product and reads both accumulators: between the barrier
+    through which it learns of the other's and its first load there is a fence after the barrier's, and the other's wait
+    is fenced before it."""
+    out = source("tree_attn_tc.cu", "// ---- output:", "cudaError_t launch_one")
+    names = r"tc_fence_before\(\)|tc_fence_after\(\)|bar_sync_n\(1, 256\)|tmem_ld32\(|mbar_wait_fast\("
+    order = [m.group(0) for m in re.finditer(names, out)]
+    first = order.index("tmem_ld32(")
+    assert order[first - 3:first] == ["tc_fence_before()", "bar_sync_n(1, 256)", "tc_fence_after()"]
+    assert order.index("mbar_wait_fast(") < first - 3 and order.count("bar_sync_n(1, 256)") == 2
