@@ -572,9 +572,9 @@ int dfv_tree_attention(const dfv_kv_cache *cache, int layer, const dfv_tree_batc
  * Rules on the target's logits before acceptance or sampling.  Any pointer may
  * be NULL: that rule is then off.
  *   hist       [n_seqs, hist_row] int32: what each sequence of the call said
- *              before its tree's root; hist_len [n_seqs] entries of it count,
- *              of which the first prompt_len [n_seqs] are the prompt (NULL: 0);
- *              hist_row < 2^24
+ *              before its tree's root; hist_len [n_seqs] entries of it count
+ *              (not NULL with hist), of which the first prompt_len [n_seqs] are
+ *              the prompt (NULL: 0); hist_row < 2^24.  Read by penalties only
  *   repetition, frequency, presence  [n_seqs] fp32
  *   bias       fp32, row b * bias_row for sequence b (bias_row = 0: shared)
  *   allowed    bit v % 32 of word v / 32: token v is allowed; row t * allowed_row

@@ -292,7 +292,7 @@ int dfv_logits_process(const void *logits, int64_t row, int dtype, int V, const 
     return api_fail(DFV_ERR_INVALID_ARG, "tokens, argmax and the rules' arrays must be 4-byte aligned");
   const bool pen = rules->repetition || rules->frequency || rules->presence;
   if (pen && !tokens) return api_fail(DFV_ERR_INVALID_ARG, "penalties need the drafted tokens");
-  if (pen && rules->hist && (!rules->hist_len || rules->hist_row < 0))
+  if (rules->hist && (!rules->hist_len || rules->hist_row < 0))
     return api_fail(DFV_ERR_INVALID_ARG, "hist needs hist_len and a non-negative hist_row");
   if (pen && rules->hist && rules->hist_row >= (1 << 24))
     return api_fail(DFV_ERR_UNSUPPORTED, "hist_row %lld: at most 2^24 - 1 tokens of history", (long long)rules->hist_row);
@@ -304,6 +304,7 @@ int dfv_logits_process(const void *logits, int64_t row, int dtype, int V, const 
   dfv::LogitsParams p = {};
   p.t = tree_params(tree);
   p.r = *rules;
+  if (!pen) p.r.hist = p.r.hist_len = p.r.prompt_len = nullptr;  // only penalties read the history
   p.x = (const char *)logits;
   p.out = (char *)out;
   p.row = row;
