@@ -23,9 +23,11 @@ struct AttnLaunch {
 
 cudaError_t launch_attn_tc(const AttnLaunch &L, cudaStream_t s);  // tree_attn_tc.cu: rows 128 or 256
 
-// Sections of the attention workspace; returns its size.
+// Sections of the attention workspace; returns its size.  Places for the states of
+// kAttnCtas CTAs whatever the plan (n_groups * n_rt of them run, a few less where n_rt
+// does not divide): a workspace for large trees is then enough for smaller ones.
 inline size_t attn_sections(AttnLaunch *L, const AttnPlan &a, int n_seqs, int Hkv, int D, void *ws) {
-  const size_t slots = 2 * (size_t)a.n_groups * a.n_rt;
+  const size_t slots = 2 * (size_t)kAttnCtas;
   size_t off = 512;  // the error word is at 256
   auto take = [&](size_t n) {
     void *q = ws ? (void *)((char *)ws + off) : nullptr;

@@ -44,3 +44,21 @@ def test_values_that_are_not_finite_stay_with_their_sequence(dfv, heads, kv, nod
     rest = [d for d in range(64) if d != 5]
     assert bool(((out - want[0]).abs() <= tol)[:, :, rest].all())
     assert bool(((out - want[0]).abs() <= tol)[~bad].all())
+
+
+def test_three_row_tiles_and_a_workspace_of_the_largest_tree(dfv):
+    """513 to 768 rows per kv head; one workspace, sized for the largest tree, for all smaller ones."""
+    ws = None
+    for heads, kv, nodes, dim in ((12, 1, 64, 128), (12, 1, 43, 128), (12, 1, 42, 128), (12, 1, 5, 128), (12, 1, 64, 64), (9, 1, 64, 128)):
+        c = Case([700, 130], [nodes, max(1, nodes // 3)], heads, kv, dim, 16, torch.bfloat16, seed=nodes + dim)
+        want = c.attention()
+        tol, tol_lse = c.tolerances(*want)
+        cache, tree = c.gpu(dfv)
+        if ws is None:
+            ws = dfv.alloc_workspace(dfv.tree_attention_workspace_size(cache, tree, heads))
+        lse = torch.empty(c.rows, heads, device="cuda")
+        out = dfv.tree_attention(cache, 0, tree, c.q.cuda(), ws, lse=lse)
+        torch.cuda.synchronize()
+        assert dfv.read_device_error(ws) == 0
+        assert bool(((out.double().cpu() - want[0]).abs() <= tol).all())
+        assert bool(((lse.double().cpu() - want[1]).abs() <= tol_lse).all())

@@ -31,3 +31,21 @@ def logits(dfv, rules, V=1000, tokens=0x3000):
 def test_a_history_needs_its_lengths_with_penalties_and_without(dfv, rules):
     assert logits(dfv, rules) == INVALID
     assert b"hist" in dfv.lib().dfv_last_error_detail()
+
+
+def cache(dfv, **kw):
+    a = dict(n_layers=4, n_pages=100, page_size=16, n_kv_heads=4, head_dim=128, dtype=1, max_seqs=8, max_pages=64, k=0x10000,
+             v=0x20000, stride_layer=100 * 8192, stride_page=8192, stride_head=2048, stride_token=128, page_table=0x30000,
+             lens=0x40000, refs=0x50000, err=0x60000)
+    return ctypes.byref(dfv.CCache(**{**a, **kw}))
+
+
+@pytest.mark.parametrize("group", range(1, 17))
+@pytest.mark.parametrize("kv,dim,seqs", [(1, 128, 1), (4, 64, 33)])
+def test_an_attention_workspace_serves_smaller_trees(dfv, group, kv, dim, seqs):
+    """The size for trees of up to max_nodes nodes is enough for any smaller tree, also of fewer sequences."""
+    c = cache(dfv, n_kv_heads=kv, head_dim=dim)
+    size = lambda n, s: dfv.lib().dfv_tree_attention_workspace_size(c, tree(dfv, n_seqs=s, max_nodes=n), kv * group)  # noqa: E731
+    sizes = [size(n, seqs) for n in range(1, 65)]
+    assert sizes[0] > 0 and sizes == sorted(sizes)
+    assert all(size(n, max(1, seqs // 2)) <= sizes[n - 1] for n in range(1, 65))
