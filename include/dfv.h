@@ -40,10 +40,17 @@
  *   - Workspaces are caller-owned device memory of at least the size the
  *     matching *_workspace_size() reports.  A workspace must be ZERO-FILLED
  *     before its first use (e.g. cudaMemset); every call leaves it zero-ready
- *     for the next one (the counters that must start at zero live at fixed
- *     offsets, so one workspace serves any k and, for d <= 13312, any layer).
+ *     for the next one of its family (the counters that must start at zero live
+ *     at fixed offsets, so one workspace serves any k and, for d <= 13312, any
+ *     layer; and any tree-verify call it is large enough for).
  *     Calls that share a workspace must be ordered (same stream, or
  *     synchronised): concurrent use races.
+ *     Which calls may share one: those of a family, namely (1) dfv_route_topk
+ *     and the MoE block and stack calls, (2) dfv_moe_batch_forward, (3)
+ *     dfv_accept_greedy, (4) all tree-verify calls (attention, logits, cache
+ *     commit and pages).  A workspace that a call of one family has used must be
+ *     zero-filled again before a call of another takes it: what one leaves
+ *     behind lies where another keeps its counters, and nothing detects that.
  *   - Returns DFV_OK (0) or a DFV_ERR_* status; dfv_status_string() names it
  *     and dfv_last_error_detail() gives the last failure's detail text
  *     (thread-local).
@@ -635,7 +642,8 @@ int dfv_logits_process(const void *logits, int64_t row, int dtype, int V, const 
 int dfv_accept_tree(const dfv_tree_batch *tree, const int32_t *tokens, const int32_t *target, int32_t *path,
                     int64_t path_row, int32_t *tau, void *stream);
 
-/* Bytes of workspace dfv_cache_commit and the dfv_pages_* calls need. */
+/* Bytes of workspace dfv_cache_commit and the dfv_pages_* calls need (1 MB and
+ * more: the counters of all tree-verify calls come first). */
 size_t dfv_cache_workspace_size(const dfv_kv_cache *cache);
 
 /*

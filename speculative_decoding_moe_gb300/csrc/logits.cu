@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
   constexpr int kRowsAhead = F32 || !VEC || ONE ? 2 : 4;  // rows whose logits are in flight: 8 or 16 registers
   // a row starts from what the slices that are done have found
   if (tid < n) {
-    s_key[tid] = p.argmax && gridDim.y > 1 ? __ldcg(p.key + r0 + tid) : 0ull;
+    s_key[tid] = p.argmax && gridDim.y > 1 ? __ldcg(&p.state[r0 + tid].key) : 0ull;
     s_floor[tid] = Raw<F32>::floor_of((uint32_t)(s_key[tid] >> 32));
   }
   if (tid >= 64 && tid < 80) {
@@ -539,12 +539,13 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(const LogitsPa
     const int row = r0 + i;
     unsigned long long k = s_key[i];
     if (gridDim.y > 1) {
-      if (k) atomicMax(&p.key[row], k);
+      LogitRow &state = p.state[row];
+      if (k) atomicMax(&state.key, k);
       __threadfence();
-      if (atomicAdd(&p.ticket[row], 1u) != gridDim.y - 1) return;
+      if (atomicAdd(&state.ticket, 1u) != gridDim.y - 1) return;
       __threadfence();
-      k = atomicExch(&p.key[row], 0ull);
-      p.ticket[row] = 0u;
+      k = atomicExch(&state.key, 0ull);
+      state.ticket = 0u;
     }
     p.argmax[row] = k ? (int32_t)(0xffffffffu - (unsigned)(k & 0xffffffffull)) : 0;  // nothing above -inf: column 0
   }

@@ -100,7 +100,7 @@ dfv::TreeParams tree_params(const dfv_tree_batch *t) {
   return p;
 }
 
-// the page calls' workspace: tickets, fork plan, pages handed out
+// the page calls' workspace: tickets, then fork plan and pages handed out
 struct PageWs {
   unsigned *ticket;
   int32_t *plan, *got;
@@ -108,13 +108,13 @@ struct PageWs {
 };
 PageWs page_ws(const dfv_kv_cache *c, void *base) {
   PageWs w = {};
-  size_t off = 512;  // ticket-free head: the error word of other workspaces sits here
+  w.ticket = base ? (unsigned *)((char *)base + dfv::kWsTickets) : nullptr;
+  size_t off = dfv::kWsScratch;
   auto take = [&](size_t n) {
     void *p = base ? (void *)((char *)base + off) : nullptr;
     off += align256(n);
     return p;
   };
-  w.ticket = (unsigned *)take(DFV_MAX_TREE_SEQS * 4);
   w.plan = (int32_t *)take(DFV_MAX_TREE_SEQS * 16);
   w.got = (int32_t *)take((size_t)c->n_pages * 4);
   w.bytes = off;
@@ -259,7 +259,7 @@ int dfv_tree_attention(const dfv_kv_cache *cache, int layer, const dfv_tree_batc
   p.o_row = o_row;
   p.o_head = o_head;
   p.lse = opt_lse;
-  p.err = (unsigned *)((char *)ws + 256);
+  p.err = (unsigned *)((char *)ws + dfv::kWsErr);
   char why[256] = {0};
   const cudaError_t e = dfv::launch_tree_attn(p, dfv::tree_attn_plan(tree->max_nodes, p.G), ws, (cudaStream_t)stream,
                                               why, sizeof why);
@@ -269,7 +269,7 @@ int dfv_tree_attention(const dfv_kv_cache *cache, int layer, const dfv_tree_batc
 
 size_t dfv_logits_workspace_size(int n_rows_max) {
   if (n_rows_max < 1 || n_rows_max > DFV_MAX_TREE * DFV_MAX_TREE_SEQS) return 0;
-  return 512 + align256((size_t)n_rows_max * 8) + align256((size_t)n_rows_max * 4);
+  return dfv::kWsRows + align256((size_t)n_rows_max * sizeof(dfv::LogitRow));
 }
 
 int dfv_logits_process(const void *logits, int64_t row, int dtype, int V, const dfv_tree_batch *tree,
@@ -313,9 +313,7 @@ int dfv_logits_process(const void *logits, int64_t row, int dtype, int V, const 
   p.f32 = dtype == DFV_F32;
   p.tokens = tokens;
   p.argmax = argmax;
-  // both arrays are zero between calls, so one workspace serves calls of any size
-  p.key = (unsigned long long *)((char *)ws + 512);
-  p.ticket = (unsigned *)((char *)ws + 512 + align256((size_t)tree->n_rows * 8));
+  p.state = (dfv::LogitRow *)((char *)ws + dfv::kWsRows);
   return launched(dfv::launch_logits(p, (cudaStream_t)stream), "logit rules launch");
 }
 

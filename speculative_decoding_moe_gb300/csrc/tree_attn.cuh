@@ -28,7 +28,7 @@ cudaError_t launch_attn_tc(const AttnLaunch &L, cudaStream_t s);  // tree_attn_t
 // does not divide): a workspace for large trees is then enough for smaller ones.
 inline size_t attn_sections(AttnLaunch *L, const AttnPlan &a, int n_seqs, int Hkv, int D, void *ws) {
   const size_t slots = 2 * (size_t)kAttnCtas;
-  size_t off = 512;  // the error word is at 256
+  size_t off = kWsScratch;
   auto take = [&](size_t n) {
     void *q = ws ? (void *)((char *)ws + off) : nullptr;
     off += (n + 255) & ~(size_t)255;

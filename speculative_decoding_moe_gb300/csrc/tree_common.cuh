@@ -50,6 +50,21 @@ struct TreeAttnParams {
   unsigned *err;  // workspace error word (bounded waits)
 };
 
+// A row's running maximum and how many slices are done, zero between calls.
+struct LogitRow {
+  unsigned long long key;
+  unsigned ticket, unused;
+};
+
+// Every tree-verify call's workspace begins alike: the error word, then all counters
+// that have to be zero between calls, at offsets that depend on no size.  What a call
+// may leave behind lies after them, so one workspace serves calls of every kind.
+constexpr size_t kWsErr = 256;
+constexpr size_t kWsTickets = 512;                                          // commit: [DFV_MAX_TREE_SEQS] unsigned
+constexpr size_t kWsRows = kWsTickets + DFV_MAX_TREE_SEQS * 4;              // logits: [rows] LogitRow
+constexpr size_t kWsScratch = kWsRows + (size_t)DFV_MAX_TREE * DFV_MAX_TREE_SEQS * sizeof(LogitRow);
+static_assert(kWsRows % 256 == 0 && kWsScratch % 256 == 0, "sections are 256-byte aligned");
+
 struct LogitsParams {
   TreeParams t;
   dfv_logit_rules r;
@@ -59,8 +74,7 @@ struct LogitsParams {
   int V, f32;
   const int32_t *tokens;
   int32_t *argmax;
-  unsigned long long *key;  // [n_rows] running maximum of each row, zero between calls
-  unsigned *ticket;         // [n_rows] slices done, zero between calls
+  LogitRow *state;  // [n_rows]
 };
 
 struct AcceptTreeParams {

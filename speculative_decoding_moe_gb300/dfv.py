@@ -230,7 +230,8 @@ def workspace_size(layer: Layer, k_max: int) -> int:
 
 
 def alloc_workspace(nbytes: int, device="cuda") -> torch.Tensor:
-    """Zero-filled workspace (the library requires zeros before first use)."""
+    """Zero-filled workspace (the library requires zeros before first use).  One may serve several calls in stream order
+    if they are of one family: the MoE block and stack calls, the batched ones, accept_greedy, or all tree-verify calls."""
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 

@@ -49,3 +49,13 @@ def test_an_attention_workspace_serves_smaller_trees(dfv, group, kv, dim, seqs):
     sizes = [size(n, seqs) for n in range(1, 65)]
     assert sizes[0] > 0 and sizes == sorted(sizes)
     assert all(size(n, max(1, seqs // 2)) <= sizes[n - 1] for n in range(1, 65))
+
+
+def test_what_calls_leave_in_a_workspace_lies_behind_the_counters_of_all(dfv):
+    """Counters that have to be zero come first, at the same places for every call: the other calls' workspaces hold
+    those of the largest logits call in front."""
+    L = dfv.lib()
+    counters = L.dfv_logits_workspace_size(64 * 1024)
+    assert L.dfv_logits_workspace_size(1) < counters
+    assert L.dfv_cache_workspace_size(cache(dfv, n_pages=1)) > counters
+    assert L.dfv_tree_attention_workspace_size(cache(dfv, n_kv_heads=1, head_dim=64), tree(dfv, n_seqs=1, max_nodes=1), 1) > counters
