@@ -81,7 +81,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     tmp = BIND + ".tmp.%d" % os.getpid()
     # libdfv.so is found beside the extension; torch's libraries are loaded by then
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, bind_obj, "-L", HERE, "-l:libdfv.so", "-Wl,-rpath,$ORIGIN",
-           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10"]
+           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("linking the binding failed:\n%s\n%s" % (" ".join(cmd), r.stderr))

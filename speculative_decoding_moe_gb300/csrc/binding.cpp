@@ -15,10 +15,12 @@
 #include <cstdint>
 #include <cstdio>
 #include <exception>
+#include <optional>
 #include <string>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/dfv.h"
@@ -105,9 +107,15 @@ Rows3 rows3(const at::Tensor &t, const char *what, int64_t rows, int64_t heads, 
 void on_gpu(int index) {
   if (index < 0) value_error("the tensors of the call must be CUDA tensors");
 }
-// A result, from torch's allocator without its dispatcher (1.1 us instead of 1.6).
-at::Tensor empty(at::IntArrayRef shape, at::ScalarType dt, const at::Tensor &like) {
-  on_gpu(like.get_device());
+// A result, from torch's allocator without its dispatcher (1.1 us instead of 1.6), in
+// the memory of the call's stream: a block of another stream's may still be in use
+// there, and would be handed out there again before this call ends.
+at::Tensor empty(at::IntArrayRef shape, at::ScalarType dt, const at::Tensor &like, void *stream) {
+  const int index = (int)like.get_device();
+  on_gpu(index);
+  std::optional<c10::cuda::CUDAStreamGuard> there;
+  if (c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream() != stream)
+    there.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), (c10::DeviceIndex)index));
   return at::Tensor(at::detail::empty_cuda(shape, dt, like.device(), std::nullopt));
 }
 
@@ -190,7 +198,7 @@ PyObject *rope_append(PyObject *const *a) {
   if (number(a[3]) != D) value_error("the rotary plan is for head_dim %d, the cache has %d", number(a[3]), (int)D);
   if (number(a[14]) != c.index) value_error("the rotary plan and the cache are not on one device");
   at::Tensor made;
-  if (a[12] == Py_None) made = empty({rows, H, D}, dt, q);
+  if (a[12] == Py_None) made = empty({rows, H, D}, dt, q, stream(a[13]));
   const Rows3 ro = rows3(made.defined() ? made : tensor(a[12], "out"), "out", rows, H, D, dt, c.index);
   on_gpu(c.index);
   done(dfv_rope_append(&c.c, layer, &t.c, (int)H, number(a[4]), number(a[5]), (float)real(a[6]),
@@ -214,7 +222,7 @@ PyObject *tree_attention(PyObject *const *a) {
   void *lse = given(a[7], "lse", at::kFloat, {rows, H}, c.index);
   const double scale = a[5] == Py_None ? 1.0 / std::sqrt((double)D) : real(a[5]);
   at::Tensor made;
-  if (a[6] == Py_None) made = empty({rows, H, D}, dt, q);
+  if (a[6] == Py_None) made = empty({rows, H, D}, dt, q, stream(a[8]));
   const Rows3 ro = rows3(made.defined() ? made : tensor(a[6], "out"), "out", rows, H, D, dt, c.index);
   on_gpu(c.index);
   done(dfv_tree_attention(&c.c, layer, &t.c, (int)H, (float)scale, rq.p, rq.row, rq.head, ro.p, ro.row, ro.head,
@@ -256,7 +264,7 @@ PyObject *logits_process(PyObject *const *a) {
   if (!store) {
     if (a[5] != Py_None) value_error("store=False takes no out");
   } else {
-    if (a[5] == Py_None) made = empty({rows, V}, dt, x);
+    if (a[5] == Py_None) made = empty({rows, V}, dt, x, stream(a[8]));
     const at::Tensor &o = made.defined() ? made : tensor(a[5], "out");
     if (o.sizes() != x.sizes() || o.scalar_type() != dt || o.stride(1) != 1 || o.get_device() != t.index)
       value_error("out must be like logits");
@@ -264,7 +272,7 @@ PyObject *logits_process(PyObject *const *a) {
     out_row = rows > 1 ? o.stride(0) : V;
   }
   if (!arg) {
-    best = empty({rows}, at::kInt, x);
+    best = empty({rows}, at::kInt, x, stream(a[8]));
     arg = best.data_ptr();
   }
   on_gpu(t.index);
@@ -294,11 +302,11 @@ PyObject *accept_tree(PyObject *const *a) {
   void *pp = given(a[3], "path", at::kInt, {S, width}, t.index), *tp = given(a[4], "tau", at::kInt, {S}, t.index);
   at::Tensor path, tau;
   if (!pp) {
-    path = empty({S, width}, at::kInt, like);
+    path = empty({S, width}, at::kInt, like, stream(a[5]));
     pp = path.data_ptr();
   }
   if (!tp) {
-    tau = empty({S}, at::kInt, like);
+    tau = empty({S}, at::kInt, like, stream(a[5]));
     tp = tau.data_ptr();
   }
   on_gpu(t.index);

@@ -1,6 +1,8 @@
 """Python binding of libdfv.so.  Argument marshalling only: every step of the
 block-verify path runs in the library's CUDA kernels.  Tensors must be CUDA
-tensors; calls enqueue work on torch's current CUDA stream.  The block-verify
+tensors; calls enqueue work on torch's current CUDA stream, or on the one given
+as `stream` (a result that the call makes is then in that stream's memory, as
+under torch.cuda.stream(stream)).  The block-verify
 calls go through ctypes; the tree-verify calls, which a step makes dozens of,
 through the extension built from csrc/binding.cpp."""
 from __future__ import annotations
@@ -188,6 +190,15 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A result, in the memory of the call's stream: a block of the current stream's may still be in use there, and would
+    be handed out there again before the call ends."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _act(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return BF16
@@ -239,12 +250,13 @@ def route_topk(layer: Layer, hidden: torch.Tensor, ws: torch.Tensor, stream=None
     k = hidden.shape[0]
     s = layer.shape
     dev = hidden.device
-    idx = torch.empty(k, s.top_k, dtype=torch.int32, device=dev)
-    w = torch.empty(k, s.top_k, dtype=torch.float32, device=dev)
-    woken = torch.empty(min(s.n_experts, k * s.top_k), dtype=torch.int32, device=dev)
-    nw = torch.empty(1, dtype=torch.int32, device=dev)
-    offs = torch.empty(min(s.n_experts, k * s.top_k) + 1, dtype=torch.int32, device=dev)
-    gat = torch.empty(k * s.top_k, dtype=torch.int32, device=dev)
+    ints = lambda *shape: _empty(shape, torch.int32, dev, stream)  # noqa: E731
+    idx = ints(k, s.top_k)
+    w = _empty((k, s.top_k), torch.float32, dev, stream)
+    woken = ints(min(s.n_experts, k * s.top_k))
+    nw = ints(1)
+    offs = ints(min(s.n_experts, k * s.top_k) + 1)
+    gat = ints(k * s.top_k)
     st = _load().dfv_route_topk(layer.ref, _p(hidden), _act(hidden), k, _p(idx), _p(w), _p(woken), _p(nw), _p(offs),
                                 _p(gat), _p(ws), ws.numel(), _stream(stream))
     _check(st, "dfv_route_topk")
@@ -255,7 +267,7 @@ def moe_block_forward(layer: Layer, hidden: torch.Tensor, ws: torch.Tensor, out:
                       topk_idx: Optional[torch.Tensor] = None, n_woken: Optional[torch.Tensor] = None, stream=None):
     k = hidden.shape[0]
     if out is None:
-        out = torch.empty_like(hidden)
+        out = torch.empty_like(hidden) if stream is None else _empty(hidden.shape, hidden.dtype, hidden.device, stream)
     st = _load().dfv_moe_block_forward(layer.ref, _p(hidden), _act(hidden), k, _p(out), _p(topk_idx), _p(n_woken),
                                        _p(ws), ws.numel(), _stream(stream))
     _check(st, "dfv_moe_block_forward")
@@ -274,7 +286,7 @@ def moe_batch_forward(layer: Layer, hidden: torch.Tensor, n_blocks: int, ws: tor
     if T % n_blocks:
         raise ValueError("rows %d are not n_blocks=%d blocks of equal size" % (T, n_blocks))
     if out is None:
-        out = torch.empty_like(hidden)
+        out = torch.empty_like(hidden) if stream is None else _empty(hidden.shape, hidden.dtype, hidden.device, stream)
     st = _load().dfv_moe_batch_forward(layer.ref, _p(hidden), n_blocks, T // n_blocks, _p(out), _p(topk_idx),
                                        _p(n_woken), _p(ws), ws.numel(), _stream(stream))
     _check(st, "dfv_moe_batch_forward")
@@ -314,9 +326,9 @@ def accept_greedy(logits: torch.Tensor, draft: torch.Tensor, ws: torch.Tensor, t
     k = rows - 1
     dev = logits.device
     if tau is None:
-        tau = torch.empty(1, dtype=torch.int32, device=dev)
+        tau = _empty(1, torch.int32, dev, stream)
     if committed is None:
-        committed = torch.empty(k + 1, dtype=torch.int32, device=dev)
+        committed = _empty(k + 1, torch.int32, dev, stream)
     st = _load().dfv_accept_greedy(_p(logits), _act(logits), k, V, _p(draft), _p(tau), _p(committed), _p(ws),
                                    ws.numel(), _stream(stream))
     _check(st, "dfv_accept_greedy")
@@ -415,9 +427,9 @@ def accept_greedy_noalloc(logits: torch.Tensor, draft: torch.Tensor, tau: Option
     k = rows - 1
     dev = logits.device
     if tau is None:
-        tau = torch.empty(1, dtype=torch.int32, device=dev)
+        tau = _empty(1, torch.int32, dev, stream)
     if committed is None:
-        committed = torch.empty(k + 1, dtype=torch.int32, device=dev)
+        committed = _empty(k + 1, torch.int32, dev, stream)
     st = _load().dfv_accept_greedy_noalloc(_p(logits), _act(logits), k, V, _p(draft), _p(tau), _p(committed),
                                            _stream(stream))
     _check(st, "dfv_accept_greedy_noalloc")
