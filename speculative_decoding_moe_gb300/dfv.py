@@ -437,14 +437,20 @@ def accept_greedy_noalloc(logits: torch.Tensor, draft: torch.Tensor, tau: Option
 
 
 # ---------------------------------------------------------------- tree verify
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _on(stream, index: int) -> int:
-    """Stream handle of a call: the given stream, or torch's current one on the tensors' device."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _raw_stream(index) if index >= 0 else 0  # host tensors are refused by the call
+    """Stream handle of a call: the given stream, or torch's current one.  The library launches on the current device."""
+    if index < 0:
+        return 0  # host tensors are refused by the call
+    if index != _current_device():
+        raise ValueError("the tensors of the call are on device %d, the current device is %d" % (index, _current_device()))
+    if stream is None:
+        return _raw_stream(index)
+    if stream.device_index != index:
+        raise ValueError("the tensors of the call are on device %d, the stream is on device %d" % (index, stream.device_index))
+    return stream.cuda_stream
 
 
 def _refuse(t, what: str, dtype, shape, index: int):

@@ -78,3 +78,19 @@ def test_descriptors_follow(dfv, setup):
     cache, tree, _ = setup
     for x in (cache, tree, dfv.LogitRules()):
         assert ctypes.addressof(x.c) == x.addr
+
+
+class Queue:
+    def __init__(self, index, handle):
+        self.device_index, self.cuda_stream = index, handle
+
+
+def test_calls_are_refused_on_another_device_than_the_tensors(dfv, monkeypatch):
+    """The library launches on the current device: tensors, stream and current device have to be the same one's."""
+    monkeypatch.setattr(dfv, "_raw_stream", lambda index: 100 + index)
+    monkeypatch.setattr(dfv, "_current_device", lambda: 1, raising=False)
+    assert dfv._on(None, 1) == 101 and dfv._on(Queue(1, 7), 1) == 7
+    for stream, index in ((None, 0), (Queue(0, 7), 0), (Queue(1, 7), 0), (Queue(0, 7), 1)):
+        with pytest.raises(ValueError, match="device"):
+            dfv._on(stream, index)
+    assert dfv._on(None, -1) == 0  # host tensors: refused by the call itself
