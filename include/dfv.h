@@ -614,7 +614,8 @@ size_t dfv_logits_workspace_size(int n_rows_max);
  *   4. x = x + bias_v
  *   5. x = -inf where v is not allowed
  * rounded once to the logits' dtype.
- *   logits [n_rows, V] BF16 or F32, row stride `row` elements
+ *   logits [n_rows, V] BF16 or F32, row stride `row` elements; V up to 65535 *
+ *          4096
  *   tokens [n_rows] int32 drafted token of each node (NULL without penalties)
  *   out    [n_rows, V], row stride `out_row`; may be logits itself (same stride),
  *          or NULL: argmax only

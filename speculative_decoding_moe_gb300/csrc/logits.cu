@@ -28,6 +28,7 @@ namespace {
 constexpr int kLogitThreads = 512;
 constexpr int kCols = 8;                              // columns of a thread
 constexpr int kSlice = kLogitThreads * kCols;
+static_assert(kSlice == kLogitSlice, "the host's limit on V counts these slices");
 constexpr int kEarly = 2;                             // quads of history tokens of a thread loaded first
 constexpr int kAhead = 4;                             // listed columns of a lane in flight
 constexpr uint32_t kPromptBit = 0x80000000u;          // the token is in the prompt

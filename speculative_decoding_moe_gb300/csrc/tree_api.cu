@@ -278,7 +278,7 @@ int dfv_logits_process(const void *logits, int64_t row, int dtype, int V, const 
   int st = check_tree(tree);
   if (st) return st;
   if (dtype != DFV_BF16 && dtype != DFV_F32) return api_fail(DFV_ERR_UNSUPPORTED, "logits dtype %d", dtype);
-  if (V < 1 || V > (1 << 28)) return api_fail(DFV_ERR_INVALID_ARG, "V=%d outside 1..2^28", V);
+  if (V < 1 || V > dfv::kMaxVocab) return api_fail(DFV_ERR_INVALID_ARG, "V=%d outside 1..%d", V, dfv::kMaxVocab);
   const size_t esz = dtype == DFV_F32 ? 4 : 2;
   if (!logits || !aligned(logits, esz) || !aligned(out, esz))
     return api_fail(DFV_ERR_INVALID_ARG, "logits NULL, or logits/out not aligned to their type");

@@ -65,6 +65,10 @@ constexpr size_t kWsRows = kWsTickets + DFV_MAX_TREE_SEQS * 4;              // l
 constexpr size_t kWsScratch = kWsRows + (size_t)DFV_MAX_TREE * DFV_MAX_TREE_SEQS * sizeof(LogitRow);
 static_assert(kWsRows % 256 == 0 && kWsScratch % 256 == 0, "sections are 256-byte aligned");
 
+// Columns of a CTA of the logit rules; a launch has at most 65535 such slices.
+constexpr int kLogitSlice = 4096;
+constexpr int kMaxVocab = 65535 * kLogitSlice;
+
 struct LogitsParams {
   TreeParams t;
   dfv_logit_rules r;

@@ -59,3 +59,9 @@ def test_what_calls_leave_in_a_workspace_lies_behind_the_counters_of_all(dfv):
     assert L.dfv_logits_workspace_size(1) < counters
     assert L.dfv_cache_workspace_size(cache(dfv, n_pages=1)) > counters
     assert L.dfv_tree_attention_workspace_size(cache(dfv, n_kv_heads=1, head_dim=64), tree(dfv, n_seqs=1, max_nodes=1), 1) > counters
+
+
+@pytest.mark.parametrize("V", [65535 * 4096 + 1, 1 << 28])
+def test_vocabularies_beyond_the_slices_of_a_launch(dfv, V):
+    assert logits(dfv, {}, V=V) == INVALID
+    assert b"V=" in dfv.lib().dfv_last_error_detail()
