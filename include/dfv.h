@@ -671,7 +671,8 @@ int dfv_cache_copy_pages(const dfv_kv_cache *cache, const int32_t *src, const in
  * index first, in the order of the list and of the tokens; refs becomes 1.
  * When the pool runs short, the first sequence that cannot be served in full
  * and all after it get nothing (DFV_KVERR_NO_PAGE).
- *   seqs, n_new [n] int32 device; n <= DFV_MAX_TREE_SEQS; seqs distinct
+ *   seqs, n_new [n] int32 device; n <= DFV_MAX_TREE_SEQS, n * max_pages < 2^31;
+ *        seqs distinct
  */
 int dfv_pages_reserve(const dfv_kv_cache *cache, const int32_t *seqs, const int32_t *n_new, int n, void *ws,
                       size_t ws_bytes, void *stream);

@@ -377,6 +377,9 @@ int dfv_pages_reserve(const dfv_kv_cache *cache, const int32_t *seqs, const int3
                       size_t ws_bytes, void *stream) {
   int st = check_list(cache, seqs, n_new, n, true);
   if (st) return st;
+  // missing entries are summed in 32 bits, and n_new may ask for all of them
+  if ((int64_t)n * cache->max_pages > INT32_MAX)
+    return api_fail(DFV_ERR_UNSUPPORTED, "%d sequences of %d table entries: at most 2^31 - 1 in all", n, cache->max_pages);
   if ((st = check_ws(ws, ws_bytes, page_ws(cache, nullptr).bytes))) return st;
   const PageWs w = page_ws(cache, ws);
   dfv::PagesParams p = {};

@@ -65,3 +65,11 @@ def test_what_calls_leave_in_a_workspace_lies_behind_the_counters_of_all(dfv):
 def test_vocabularies_beyond_the_slices_of_a_launch(dfv, V):
     assert logits(dfv, {}, V=V) == INVALID
     assert b"V=" in dfv.lib().dfv_last_error_detail()
+
+
+def test_reservations_whose_missing_entries_cannot_be_counted(dfv):
+    """The kernel sums the missing table entries of all sequences in 32 bits; n_new is device data and may ask for all."""
+    L = dfv.lib()
+    c = cache(dfv, page_size=8, stride_page=4096, stride_head=1024, max_pages=1 << 27)
+    assert L.dfv_pages_reserve(c, 0x1000, 0x2000, 16, 0x9000, 1 << 30, None) == UNSUPPORTED
+    assert b"table" in L.dfv_last_error_detail()
