@@ -571,7 +571,8 @@ class Rope:
                  scale: Optional[float] = None, device="cuda"):
         if scaling not in self.KINDS:
             raise ValueError("scaling must be one of %s, got %r" % (sorted(self.KINDS), scaling))
-        self.head_dim, self.rot_dim, self.interleaved = int(head_dim), int(rot_dim or head_dim), int(bool(interleaved))
+        self.head_dim, self.interleaved = int(head_dim), int(bool(interleaved))
+        self.rot_dim = self.head_dim if rot_dim is None else int(rot_dim)
         turns = (ctypes.c_uint64 * max(1, self.rot_dim // 2))()
         _check(_load().dfv_rope_table(self.rot_dim, float(theta), self.KINDS[scaling], float(factor), float(original),
                                       float(low), float(high), turns), "dfv_rope_table")

@@ -73,3 +73,10 @@ def test_reservations_whose_missing_entries_cannot_be_counted(dfv):
     c = cache(dfv, page_size=8, stride_page=4096, stride_head=1024, max_pages=1 << 27)
     assert L.dfv_pages_reserve(c, 0x1000, 0x2000, 16, 0x9000, 1 << 30, None) == UNSUPPORTED
     assert b"table" in L.dfv_last_error_detail()
+
+
+def test_a_rotary_plan_of_no_elements_is_refused(dfv):
+    """rot_dim 0 is not "the whole head": that is None."""
+    assert dfv.Rope(128, device="cpu").rot_dim == 128 and dfv.Rope(128, rot_dim=64, device="cpu").rot_dim == 64
+    with pytest.raises(dfv.DfvError, match="rot_dim 0"):
+        dfv.Rope(128, rot_dim=0, device="cpu")
