@@ -58,7 +58,10 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     bind_obj = os.path.join(BUILD, "binding.o")
 
     def compile_binding():
-        import torch
+        try:
+            import torch
+        except ImportError as e:
+            raise RuntimeError("the binding needs torch's headers: %s" % e)
         at = os.path.join(os.path.dirname(torch.__file__), "include")
         cuda = os.path.join(os.path.dirname(os.path.dirname(shutil.which(NVCC) or "/usr/local/cuda/bin/nvcc")), "include")
         cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", at,
@@ -70,13 +73,14 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(9, len(srcs) + 1)) as ex:
         binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, srcs))
-        binding.result()
+    # the C library needs nothing of torch and is linked whatever becomes of the binding
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
     os.replace(tmp, LIB)
+    binding.result()
     import torch
     tmp = BIND + ".tmp.%d" % os.getpid()
     # libdfv.so is found beside the extension; torch's libraries are loaded by then
