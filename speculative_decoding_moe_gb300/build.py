@@ -32,9 +32,25 @@ def _deps():
     return [BIND_SRC] + _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
+def _torch() -> str:
+    """The torch that a binding built now is tied to."""
+    try:
+        import torch
+    except ImportError:
+        return ""
+    return "%s %s\n" % (torch.__version__, os.path.dirname(torch.__file__))
+
+
+def _stamp() -> str:
+    return os.path.join(BUILD, "binding.torch")
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
+    if not all(os.path.exists(f) for f in (LIB, BIND, _stamp())):
         return False
+    with open(_stamp()) as f:
+        if f.read() != _torch():
+            return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     return all(os.path.getmtime(f) <= t for f in _deps() + [__file__])
 
@@ -90,6 +106,8 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if r.returncode != 0:
         raise RuntimeError("linking the binding failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
     os.replace(tmp, BIND)
+    with open(_stamp(), "w") as f:
+        f.write(_torch())
     return LIB
 
 

@@ -31,3 +31,16 @@ def test_the_library_is_linked_where_the_binding_cannot_be_built(scratch, monkey
         b.build()
     assert os.path.exists(b.LIB) and not os.path.exists(b.BIND)
     assert not b.up_to_date()
+
+
+def test_another_torch_makes_the_binding_stale(scratch, monkeypatch):
+    import torch
+    assert not b.up_to_date()
+    b.build()
+    assert b.up_to_date()
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    assert not b.up_to_date()
+    b.build()
+    assert b.up_to_date()
+    os.remove(b.BIND)
+    assert not b.up_to_date()
