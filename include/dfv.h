@@ -502,7 +502,12 @@ typedef struct dfv_tree_batch {
  *   NTK     theta * factor^(rot_dim / (rot_dim - 2)) in place of theta
  *   BANDS   by how often a pair turns over the original context, n_i =
  *           original * f_i / (2 pi):  g = clamp((n_i - low) / (high - low), 0, 1),
- *           (1 - g) f_i / factor + g f_i  (slow pairs interpolated, fast kept) */
+ *           (1 - g) f_i / factor + g f_i  (slow pairs interpolated, fast kept).
+ *           The ramp is linear in the turns n_i.  A model whose configuration
+ *           means another ramp (linear in the pair's index i between two rounded
+ *           indexes, say) has other frequencies in between; its caller fills
+ *           the turns of dfv_rope_append from them by the formula of
+ *           dfv_rope_table. */
 typedef enum { DFV_ROPE_NONE = 0, DFV_ROPE_LINEAR = 1, DFV_ROPE_NTK = 2, DFV_ROPE_BANDS = 3 } dfv_rope_scaling;
 
 /*

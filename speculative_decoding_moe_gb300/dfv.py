@@ -562,13 +562,16 @@ class Rope:
     """Rotary plan: the device table of dfv_rope_table and the factor on cos and sin.
 
     scaling: "none", "linear", "ntk" or "bands" (frequency bands between `low` and `high` turns over the `original`
-    context; attention is then scaled by 0.1 ln(factor) + 1 unless `scale` says otherwise)."""
+    context; attention is then scaled by 0.1 ln(factor) + 1 unless `scale` says otherwise).  "bands" ramps linearly in the
+    turns; a model whose configuration means another ramp (linear in the pair's index between two rounded indexes, say)
+    has other frequencies in between, by tens of percent: those go in as
+    freqs: the rot_dim / 2 angles per position of the pairs, in place of theta and scaling (scale: 1 unless given)."""
 
     KINDS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3}
 
     def __init__(self, head_dim: int, rot_dim: Optional[int] = None, theta: float = 1e4, interleaved: bool = False,
                  scaling: str = "none", factor: float = 1.0, original: int = 4096, low: float = 1.0, high: float = 32.0,
-                 scale: Optional[float] = None, device="cuda"):
+                 scale: Optional[float] = None, device="cuda", freqs: Optional[Sequence[float]] = None):
         if scaling not in self.KINDS:
             raise ValueError("scaling must be one of %s, got %r" % (sorted(self.KINDS), scaling))
         self.head_dim, self.interleaved = int(head_dim), int(bool(interleaved))
@@ -576,6 +579,13 @@ class Rope:
         turns = (ctypes.c_uint64 * max(1, self.rot_dim // 2))()
         _check(_load().dfv_rope_table(self.rot_dim, float(theta), self.KINDS[scaling], float(factor), float(original),
                                       float(low), float(high), turns), "dfv_rope_table")
+        if freqs is not None:
+            freqs = [float(f) for f in freqs]
+            if len(freqs) != self.rot_dim // 2 or not all(map(math.isfinite, freqs)):
+                raise ValueError("freqs must be rot_dim / 2 = %d finite angles, got %d" % (self.rot_dim // 2, len(freqs)))
+            if scaling != "none":
+                raise ValueError("freqs are taken as they are: scaling must be 'none'")
+            turns = [round(math.ldexp(f / (2 * math.pi), 64)) % (1 << 64) for f in freqs]
         if scale is None:
             scale = 0.1 * math.log(factor) + 1.0 if scaling == "bands" else 1.0
         self.scale = float(scale)

@@ -80,3 +80,25 @@ def test_a_rotary_plan_of_no_elements_is_refused(dfv):
     assert dfv.Rope(128, device="cpu").rot_dim == 128 and dfv.Rope(128, rot_dim=64, device="cpu").rot_dim == 64
     with pytest.raises(dfv.DfvError, match="rot_dim 0"):
         dfv.Rope(128, rot_dim=0, device="cpu")
+
+
+def test_a_rotary_plan_from_frequencies(dfv):
+    """Frequencies of the caller's own, as a whole turn's 64-bit fractions: within half a unit and the roundings of the
+    quotient by 2 pi (2^-52 relatively)."""
+    import math
+    from fractions import Fraction
+    f = [1.0, 0.37, 1e-3, 2.5e-7, 0.0, 3.0, -0.5, 7.0]
+    r = dfv.Rope(64, rot_dim=16, freqs=f, scale=1.1, device="cpu")
+    assert r.rot_dim == 16 and r.scale == 1.1
+    for got, x in zip(r.turns.tolist(), f):
+        d = (Fraction(got, 1 << 64) - Fraction(x) / Fraction(2 * math.pi)) % 1
+        assert min(d, 1 - d) <= Fraction(1, 1 << 65) + abs(Fraction(x)) / (1 << 52)
+    plain = dfv.Rope(64, theta=1e4, device="cpu").turns
+    own = dfv.Rope(64, freqs=[1e4 ** (-2 * i / 64) for i in range(32)], device="cpu")
+    assert own.scale == 1.0 and all(abs(a - b) <= 1 + abs(b) * 2.0 ** -50 for a, b in zip(own.turns.tolist(), plain.tolist()))
+    for bad in (dict(freqs=f), dict(freqs=f[:7], rot_dim=16), dict(freqs=f[:7] + [math.inf], rot_dim=16),
+                dict(freqs=f, rot_dim=16, scaling="linear", factor=2.0)):
+        with pytest.raises(ValueError):
+            dfv.Rope(64, device="cpu", **bad)
+    with pytest.raises(dfv.DfvError):
+        dfv.Rope(64, freqs=[1.0] * 12, rot_dim=24, device="cpu")
