@@ -4,8 +4,8 @@
 // A decode step makes dozens of these calls, and checking and marshalling one in
 // Python took longer than its kernels: 18 us for an attention call whose kernels
 // take 10, and 5.5 here, of which two launches and two tensor maps are 4.0 and the
-// result's allocation 1.4 (a rotary call 3.1, of which the result's 1.1).  Tensors
-// are read through ATen, results allocated by torch's allocator; everything else
+// result's allocation 1.4 (a rotary call 3.6, of which the result's 1.3 and the
+// stream's look-up 0.2).  Tensors are read through ATen, results allocated by torch's allocator; everything else
 // goes through include/dfv.h as for any other caller.  Refusals are the binding's
 // own TypeError and ValueError, a status of the library is its DfvError.
 #include <Python.h>
@@ -107,7 +107,7 @@ Rows3 rows3(const at::Tensor &t, const char *what, int64_t rows, int64_t heads, 
 void on_gpu(int index) {
   if (index < 0) value_error("the tensors of the call must be CUDA tensors");
 }
-// A result, from torch's allocator without its dispatcher (1.1 us instead of 1.6), in
+// A result, from torch's allocator without its dispatcher (1.3 us instead of 1.8), in
 // the memory of the call's stream: a block of another stream's may still be in use
 // there, and would be handed out there again before this call ends.
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType dt, const at::Tensor &like, void *stream) {

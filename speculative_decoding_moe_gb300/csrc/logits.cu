@@ -5,7 +5,7 @@
 // instructions a column with every rule and 16 without, 60 % of the issue slots
 // taken.  Measured on the device: 32 trees of up to 16 nodes (390 rows) of 151936
 // bf16 with every rule and 4093 tokens of history 73 us (3.6 TB/s), without rules
-// 47 us (5.1 TB/s); one row 6.5 us.  A CTA owns a slice of
+// 47 us (5.1 TB/s); one row 6.3 us.  A CTA owns a slice of
 // kSlice vocabulary columns of one sequence, eight columns per thread, and
 // walks rows of the sequence: the thread's bias and its knowledge of which
 // columns repeat stay in registers over the rows, several rows' loads are in

@@ -8,6 +8,15 @@
 // 2^(Mi - M).  fp16 caches use M - 6 instead (p up to 64), which keeps small p
 // out of fp16's subnormals.
 //
+// Precision.  Scores, M, l and O are fp32.  p alone is rounded to the cache's 16-bit
+// type before it multiplies the values: both operands of a product have one type, and
+// p in 32 bits would take the values widened to tf32 (half the rate, twice the bytes
+// of a tile) or a second product of what the rounding left.  l sums p before its
+// rounding.  An output's error is then a half step of the type for its own rounding
+// and, weighted by p |v|, at most another for p: with normal values the outputs'
+// error in the 2-norm is 0.0020 to 0.0023 on bf16 caches, where their own rounding
+// alone makes 0.0017 (fp16: 0.00028 and 0.00021).
+//
 // Work split.  The nodes x query heads of one kv head are the rows of one tile,
 // so keys and values are read once for all of them.  All (sequence, kv head)
 // pairs' key tiles form one line of units that is cut into equal ranges, one

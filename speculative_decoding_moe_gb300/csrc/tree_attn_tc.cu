@@ -20,8 +20,9 @@
 // nodes x 8 heads over up to 8191 keys: 90 us, 4.6 TB/s with 8 us before the first
 // product and ranges that end 10 us apart); with two the tensor core's shared
 // memory, which the first product reads at its full rate for both operands while
-// the copies write it (8 sequences x 64 nodes over up to 32749 keys: 178 us, 1.17
-// PFLOP/s; the products without exponentials alone take 165).
+// the copies write it (8 sequences x 64 nodes over up to 32749 keys: 196 us as a call
+// among others, 1.07 PFLOP/s; 179 to 181 replayed from a graph, of which the products
+// without exponentials alone take 165).
 //
 // Warps 0-3 and 4-7 are the two warpgroups, warps 8 and 10 stream K and V tiles
 // with TMA into one ring in the order the MMAs use them (half of each tile's boxes
