@@ -76,8 +76,9 @@ enum {
 };
 
 /* DFV_Q8: 8-bit expert weights (see dfv_moe_layer).  DFV_F16 (IEEE binary16)
- * is a cache dtype (dfv_kv_cache) and appears in dfv_selftest_mma. */
-typedef enum { DFV_F32 = 0, DFV_BF16 = 1, DFV_MXFP4 = 2, DFV_Q8 = 3, DFV_F16 = 4 } dfv_dtype;
+ * is a cache dtype (dfv_kv_cache) and appears in dfv_selftest_mma.  DFV_E4M3 is
+ * a cache dtype: 8-bit codes with a power of two per token and head. */
+typedef enum { DFV_F32 = 0, DFV_BF16 = 1, DFV_MXFP4 = 2, DFV_Q8 = 3, DFV_F16 = 4, DFV_E4M3 = 5 } dfv_dtype;
 
 /* Device-side error bits a kernel may set in the workspace (see
  * dfv_read_device_error).  Every wait inside a kernel is bounded; a wait that
@@ -459,7 +460,7 @@ int dfv_selftest_tcgen05(const void *A, const void *B, int N, int K, float *D, i
  * are in elements, non-negative multiples of 8 and the same for k and v, so
  * head-major pages, token-major pages and k and v in one allocation all fit;
  * k and v are 16-byte aligned.  Offsets are 64-bit.
- *   dtype      DFV_BF16 or DFV_F16
+ *   dtype      DFV_BF16, DFV_F16 or DFV_E4M3
  *   page_size  a power of two, 8..256
  *   head_dim   a multiple of 16 up to 256 (dfv_tree_attention: 64 or 128)
  *   page_table [max_seqs, max_pages] int32, -1 where there is no page
@@ -467,6 +468,17 @@ int dfv_selftest_tcgen05(const void *A, const void *B, int N, int K, float *D, i
  *   refs       [n_pages] int32 how many sequences hold each page, 0 = free;
  *              only the page calls use it (NULL otherwise)
  *   err        [1] uint32 error bits (DFV_KVERR_*), or NULL
+ *
+ * DFV_E4M3: k and v hold e4m3 codes (a sign, four bits of exponent, three of
+ * mantissa; 0x7f and 0xff are NaN, there is no infinity), and the value of a
+ * code is code * 2^e with one e for each token and head.  The strides are then
+ * multiples of 16 (one element is a byte), and two fields more are read:
+ *   k_exp, v_exp  [n_layers, n_pages, n_kv_heads, page_size] uint8, contiguous,
+ *              4-byte aligned: e + 127.  The calls write e in -100..120: the
+ *              smallest with max |x| <= 448 * 2^e over the head's finite
+ *              elements.  Values that are not finite become NaN.
+ * Rows that go in and out of such a cache (q, k, v, outputs) are bf16.  What a
+ * caller stores by other means keeps to e in -100..120 too.
  */
 typedef struct dfv_kv_cache {
   int n_layers, n_pages, page_size, n_kv_heads, head_dim, dtype;
@@ -475,6 +487,7 @@ typedef struct dfv_kv_cache {
   int64_t stride_layer, stride_page, stride_head, stride_token;
   int32_t *page_table, *lens, *refs;
   uint32_t *err;
+  uint8_t *k_exp, *v_exp; /* read for DFV_E4M3 only */
 } dfv_kv_cache;
 
 /*
@@ -539,8 +552,8 @@ int dfv_rope_table(int rot_dim, double theta, int scaling, double factor, double
  *            counts, not its number: lens[s] + depth); negative ones turn back
  *   turns    [rot_dim / 2] DEVICE copy of the dfv_rope_table
  *   scale    factor on cos and sin (1 without attention scaling)
- * All in the cache's dtype; strides in elements, multiples of 8; pointers
- * 16-byte aligned.  rot_dim <= head_dim, a multiple of 16.
+ * All in the cache's dtype (bf16 for DFV_E4M3); strides in elements, multiples
+ * of 8; pointers 16-byte aligned.  rot_dim <= head_dim, a multiple of 16.
  * The rotated k and v of node i go to token lens[s] + i of layer `layer`; a row
  * whose page is missing is not stored (DFV_KVERR_PAGE) while its q is still
  * turned.  Rows that row_off gives to no sequence are not touched.
@@ -566,11 +579,13 @@ size_t dfv_tree_attention_workspace_size(const dfv_kv_cache *cache, const dfv_tr
  *   q    [n_rows, n_heads, head_dim], strides q_row, q_head
  *   out  [n_rows, n_heads, head_dim], strides o_row, o_head
  *   opt_lse [n_rows, n_heads] fp32: max + ln(sum), or NULL
- * q and out in the cache's dtype, strides in elements and multiples of 8,
- * pointers 16-byte aligned; out may not overlap q.  head_dim 64 or 128; n_heads
+ * q and out in the cache's dtype (bf16 for DFV_E4M3), strides in elements and
+ * multiples of 8, pointers 16-byte aligned; out may not overlap q.  head_dim 64 or 128; n_heads
  * a multiple of n_kv_heads, at most 16 query heads per kv head.
  * Scores, maxima, sums and the output accumulator are fp32; p is rounded to
- * the cache's dtype for the second product, and the output once.
+ * the cache's dtype for the second product, and the output once.  DFV_E4M3: q is
+ * taken as fp16 times a power of two per row, codes as fp16 (exact), and p times
+ * the value's power of two is rounded to fp16.
  * A page-table entry out of range is read as page 0 (DFV_KVERR_PAGE; that
  * sequence's outputs are invalid), a sequence with a length out of range is
  * taken as empty (DFV_KVERR_LEN).  Lengths, tables, masks and row offsets are
@@ -696,6 +711,97 @@ int dfv_pages_fork(const dfv_kv_cache *cache, const int32_t *src, const int32_t 
 /* Drop sequences seqs[i] (device int32 [n]): every page's refs - 1, their table
  * rows become -1 and their lens 0.  Dropping an empty sequence does nothing. */
 int dfv_pages_free(const dfv_kv_cache *cache, const int32_t *seqs, int n, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Prompts: any number of new rows per sequence (dfv_rope_append and
+ * dfv_tree_attention take up to DFV_MAX_TREE).  A prompt, or its next chunk,
+ * goes through a layer as
+ *   dfv_norm_rope_append    its rows normed, turned and stored at lens[s] + i
+ *   dfv_prompt_attention    over its own k and v when nothing was there before;
+ *                           else over what dfv_cache_read brought back
+ * and once all layers are done the caller adds the row counts to lens.
+ * ---------------------------------------------------------------------- */
+
+#define DFV_MAX_ROWS (1 << 24) /* rows of one call */
+
+/*
+ * The rows of one call: sequence b of the call owns rows row_off[b] ..
+ * row_off[b+1] of every [n_rows, ...] argument, at most max_rows and possibly
+ * none.  row_off does not decrease.
+ *   seq      [n_seqs] int32 cache sequence of each, all different, or NULL: b itself
+ *   row_off  [n_seqs + 1] int32
+ * n_seqs <= DFV_MAX_TREE_SEQS, n_rows and max_rows <= DFV_MAX_ROWS.
+ */
+typedef struct dfv_row_batch {
+  int n_seqs, n_rows, max_rows;
+  const int32_t *seq, *row_off;
+} dfv_row_batch;
+
+/*
+ * Norms of queries and keys for each head, rotary positions, and the rows'
+ * keys and values stored into the cache, in one launch:
+ *   n(x) = x / sqrt(mean(x^2) + eps) * gain    over the head's head_dim elements
+ * (x itself where the gain is NULL), then the rotation of dfv_rope_append, all in
+ * fp32 and rounded once.  Arguments as for dfv_rope_append, and
+ *   q_gain, k_gain  [head_dim] in the rows' dtype, 16-byte aligned, or NULL
+ *   eps             >= 0, finite (read where a gain is given)
+ * Row i of a sequence goes to token lens[s] + i of layer `layer`; rows whose page
+ * is missing are not stored (DFV_KVERR_PAGE) while their q is still written.
+ * Rows that row_off gives to no sequence are not touched.  Of a sequence with
+ * more than max_rows rows, or whose rows do not fit its table, nothing is stored
+ * (DFV_KVERR_LEN).
+ */
+int dfv_norm_rope_append(const dfv_kv_cache *cache, int layer, const dfv_row_batch *rows, int n_heads,
+                         const void *q_gain, const void *k_gain, float eps, int rot_dim, int interleaved, float scale,
+                         const uint64_t *turns, const void *q, int64_t q_row, int64_t q_head, const void *k,
+                         int64_t k_row, int64_t k_head, const void *v, int64_t v_row, int64_t v_head,
+                         const int32_t *positions, void *q_out, int64_t o_row, int64_t o_head, void *stream);
+
+/*
+ * Cached tokens as packed rows: row row_off[b] + i receives token i of sequence b
+ * (from its first token on, whatever lens says: rows that were appended but
+ * are not counted yet are read too), of layer `layer`.
+ *   k_out, v_out  [n_rows, n_kv_heads, head_dim] in the cache's dtype (DFV_E4M3:
+ *                 code * 2^e as bf16, which is exact up to its range), strides
+ *                 multiples of 8, 16-byte aligned; either may be NULL
+ * Rows that row_off gives to no sequence are not touched; a token without a page
+ * gives zeros (DFV_KVERR_PAGE), as does one past the page table (DFV_KVERR_LEN).
+ */
+int dfv_cache_read(const dfv_kv_cache *cache, int layer, const dfv_row_batch *rows, void *k_out, int64_t k_row,
+                   int64_t k_head, void *v_out, int64_t v_row, int64_t v_head, void *stream);
+
+/* Bytes of workspace dfv_prompt_attention needs (0 on invalid arguments).  It is
+ * of the tree-verify family: one workspace, large enough, serves all of it. */
+size_t dfv_prompt_attention_workspace_size(const dfv_row_batch *rows, int n_heads, int n_kv_heads, int head_dim);
+
+/*
+ * Causal attention of packed prompts.  Sequence b has nq rows of q (rows) and nk
+ * rows of k and v (keys; NULL: the same offsets as rows), its q rows being the
+ * last ones: row i attends to keys j <= i + nk - nq,
+ *   o[i,h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q[i,h] . k_j - max)
+ * with key/value head h / (n_heads / n_kv_heads).  A row without keys (nk < nq,
+ * i < nq - nk) gives o = 0 and lse = -inf.  Keys that a row does not attend to
+ * do not change it whatever they hold (infinities and NaN included).
+ *   dtype  DFV_BF16 or DFV_F16: of q, k, v and out
+ *   q      [rows->n_rows, n_heads, head_dim], strides q_row, q_head
+ *   k, v   [keys->n_rows, n_kv_heads, head_dim], strides k_row, k_head, v_row, v_head
+ *   out    as q, strides o_row, o_head; may not overlap q, k or v
+ *   opt_lse [rows->n_rows, n_heads] fp32: max + ln(sum), or NULL
+ * Strides in elements, multiples of 8 below 2^36; pointers 16-byte aligned; the
+ * seq fields are not read.  head_dim 64 or 128; n_heads a multiple of n_kv_heads, at
+ * most 16 query heads per kv head; keys->n_seqs = rows->n_seqs.
+ * Scores, maxima, sums and the output accumulator are fp32; p is rounded to
+ * dtype for the second product, and the output once.
+ * Offsets are read on the device: a captured graph may be replayed after they
+ * change.  A sequence whose offsets are out of range (or longer than max_rows) is
+ * left out, and opt_err (uint32, DFV_KVERR_LEN; may be NULL) says so.  Rows
+ * that belong to no sequence are not touched.
+ */
+int dfv_prompt_attention(int dtype, const dfv_row_batch *rows, const dfv_row_batch *keys, int n_heads, int n_kv_heads,
+                         int head_dim, float scale, const void *q, int64_t q_row, int64_t q_head, const void *k,
+                         int64_t k_row, int64_t k_head, const void *v, int64_t v_row, int64_t v_head, void *out,
+                         int64_t o_row, int64_t o_head, float *opt_lse, uint32_t *opt_err, void *ws, size_t ws_bytes,
+                         void *stream);
 
 const char *dfv_status_string(int status);
 const char *dfv_last_error_detail(void);

@@ -36,6 +36,10 @@ struct Tree {
   dfv_tree_batch c;
   int index;
 };
+struct Rows {
+  dfv_row_batch c;
+  int index;
+};
 struct Rules {
   dfv_logit_rules c;
   int n_seqs, index;                               // -1 / -2: none given
@@ -163,6 +167,9 @@ Space space(PyObject *o, int index) {
 void together(const Cache &c, const Tree &t) {
   if (c.index != t.index) value_error("cache and tree are not on one device");
 }
+void together(const Cache &c, const Rows &r) {
+  if (c.index != r.index) value_error("cache and rows are not on one device");
+}
 
 // Raises DfvError(status, where) of the Python module unless the status is 0.
 void done(int status, const char *where) {
@@ -206,6 +213,90 @@ PyObject *rope_append(PyObject *const *a) {
                        rv.row, rv.head, static_cast<const int32_t *>(pos), ro.p, ro.row, ro.head, stream(a[13])),
        "dfv_rope_append");
   return made.defined() ? THPVariable_Wrap(made) : same(a[12]);
+}
+
+// (cache, layer, rows, plan's head_dim, rot_dim, interleaved, scale, turns, q, k, v, positions, q_gain, k_gain, eps, out,
+// stream, plan's device)
+PyObject *norm_rope_append(PyObject *const *a) {
+  const Cache &c = handle<Cache>(a[0]);
+  const int layer = number(a[1]);
+  const Rows &r = handle<Rows>(a[2]);
+  together(c, r);
+  const at::Tensor &q = tensor(a[8], "q"), &k = tensor(a[9], "k"), &v = tensor(a[10], "v");
+  const int64_t rows = r.c.n_rows, H = q.dim() == 3 ? q.size(1) : 0, K = c.c.n_kv_heads, D = c.c.head_dim;
+  const at::ScalarType dt = type_of(c);
+  const Rows3 rq = rows3(q, "q", rows, H, D, dt, c.index), rk = rows3(k, "k", rows, K, D, dt, c.index),
+              rv = rows3(v, "v", rows, K, D, dt, c.index);
+  const void *pos = need(a[11], "positions", at::kInt, {rows}, c.index);
+  const void *qg = given(a[12], "q_gain", dt, {D}, c.index), *kg = given(a[13], "k_gain", dt, {D}, c.index);
+  if (number(a[3]) != D) value_error("the rotary plan is for head_dim %d, the cache has %d", number(a[3]), (int)D);
+  if (number(a[17]) != c.index) value_error("the rotary plan and the cache are not on one device");
+  at::Tensor made;
+  if (a[15] == Py_None) made = empty({rows, H, D}, dt, q, stream(a[16]));
+  const Rows3 ro = rows3(made.defined() ? made : tensor(a[15], "out"), "out", rows, H, D, dt, c.index);
+  on_gpu(c.index);
+  done(dfv_norm_rope_append(&c.c, layer, &r.c, (int)H, qg, kg, (float)real(a[14]), number(a[4]), number(a[5]),
+                            (float)real(a[6]), static_cast<const uint64_t *>(stream(a[7])), rq.p, rq.row, rq.head, rk.p,
+                            rk.row, rk.head, rv.p, rv.row, rv.head, static_cast<const int32_t *>(pos), ro.p, ro.row,
+                            ro.head, stream(a[16])),
+       "dfv_norm_rope_append");
+  return made.defined() ? THPVariable_Wrap(made) : same(a[15]);
+}
+
+// (cache, layer, rows, a tensor of the cache, k or None, v or None, stream)
+PyObject *cache_read(PyObject *const *a) {
+  const Cache &c = handle<Cache>(a[0]);
+  const int layer = number(a[1]);
+  const Rows &r = handle<Rows>(a[2]);
+  together(c, r);
+  const int64_t rows = r.c.n_rows, K = c.c.n_kv_heads, D = c.c.head_dim;
+  const at::ScalarType dt = type_of(c);
+  at::Tensor made[2];
+  Rows3 out[2];
+  for (int i = 0; i < 2; ++i) {
+    const char *what = i ? "v" : "k";
+    if (a[4 + i] == Py_None) made[i] = empty({rows, K, D}, dt, tensor(a[3], "cache"), stream(a[6]));
+    out[i] = rows3(made[i].defined() ? made[i] : tensor(a[4 + i], what), what, rows, K, D, dt, c.index);
+  }
+  on_gpu(c.index);
+  done(dfv_cache_read(&c.c, layer, &r.c, out[0].p, out[0].row, out[0].head, out[1].p, out[1].row, out[1].head, stream(a[6])),
+       "dfv_cache_read");
+  PyObject *k = made[0].defined() ? THPVariable_Wrap(made[0]) : same(a[4]);
+  PyObject *v = made[1].defined() ? THPVariable_Wrap(made[1]) : same(a[5]);
+  PyObject *both = k && v ? PyTuple_Pack(2, k, v) : nullptr;
+  Py_XDECREF(k);
+  Py_XDECREF(v);
+  return both;
+}
+
+// (rows, keys or 0, q, k, v, ws, scale or None, out, lse, err, stream)
+PyObject *prompt_attention(PyObject *const *a) {
+  const Rows &r = handle<Rows>(a[0]);
+  const Rows &keys = PyObject_IsTrue(a[1]) ? handle<Rows>(a[1]) : r;
+  if (keys.index != r.index) value_error("rows and keys are not on one device");
+  const at::Tensor &q = tensor(a[2], "q"), &k = tensor(a[3], "k"), &v = tensor(a[4], "v");
+  const at::ScalarType dt = q.scalar_type();
+  if (dt != at::kBFloat16 && dt != at::kHalf) {
+    PyErr_Format(PyExc_TypeError, "q must be bf16 or fp16, got %s", at::toString(dt));
+    throw Refused();
+  }
+  const int64_t rows = r.c.n_rows, H = q.dim() == 3 ? q.size(1) : 0, D = q.dim() == 3 ? q.size(2) : 0,
+                K = k.dim() == 3 ? k.size(1) : 0;
+  const Rows3 rq = rows3(q, "q", rows, H, D, dt, r.index), rk = rows3(k, "k", keys.c.n_rows, K, D, dt, r.index),
+              rv = rows3(v, "v", keys.c.n_rows, K, D, dt, r.index);
+  const Space ws = space(a[5], r.index);
+  void *lse = given(a[8], "lse", at::kFloat, {rows, H}, r.index), *err = given(a[9], "err", at::kInt, {1}, r.index);
+  if (H > INT32_MAX || K > INT32_MAX || D > INT32_MAX) value_error("sizes do not fit 32 bits");
+  const double scale = a[6] == Py_None ? 1.0 / std::sqrt((double)(D > 0 ? D : 1)) : real(a[6]);
+  at::Tensor made;
+  if (a[7] == Py_None) made = empty({rows, H, D}, dt, q, stream(a[10]));
+  const Rows3 ro = rows3(made.defined() ? made : tensor(a[7], "out"), "out", rows, H, D, dt, r.index);
+  on_gpu(r.index);
+  done(dfv_prompt_attention(dt == at::kHalf ? DFV_F16 : DFV_BF16, &r.c, &keys.c, (int)H, (int)K, (int)D, (float)scale, rq.p,
+                            rq.row, rq.head, rk.p, rk.row, rk.head, rv.p, rv.row, rv.head, ro.p, ro.row, ro.head,
+                            static_cast<float *>(lse), static_cast<uint32_t *>(err), ws.p, ws.n, stream(a[10])),
+       "dfv_prompt_attention");
+  return made.defined() ? THPVariable_Wrap(made) : same(a[7]);
 }
 
 // (cache, layer, tree, q, ws, scale or None, out, lse, stream)
@@ -407,8 +498,9 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyMethodDef kMethods[] = {DFV_ENTRY(rope_append, 15),   DFV_ENTRY(tree_attention, 9), DFV_ENTRY(logits_process, 9),
                           DFV_ENTRY(accept_tree, 6),    DFV_ENTRY(cache_commit, 7),   DFV_ENTRY(cache_copy_pages, 4),
                           DFV_ENTRY(pages_reserve, 5),  DFV_ENTRY(pages_fork, 5),     DFV_ENTRY(pages_free, 3),
+                          DFV_ENTRY(norm_rope_append, 18), DFV_ENTRY(cache_read, 7),   DFV_ENTRY(prompt_attention, 11),
                           {nullptr, nullptr, 0, nullptr}};
-PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_dfvbind", "hot calls of the tree-verify binding", -1, kMethods,
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_dfvbind", "hot calls of the tree-verify and prompt binding", -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

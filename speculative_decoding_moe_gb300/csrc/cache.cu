@@ -69,6 +69,7 @@ constexpr int kCommitThreads = 128;
 __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitParams p) {
   __shared__ int s_path[DFV_MAX_TREE];
   __shared__ long long s_from[DFV_MAX_TREE], s_to[DFV_MAX_TREE];
+  __shared__ size_t s_efrom[DFV_MAX_TREE], s_eto[DFV_MAX_TREE];  // exponent bytes of head 0
   __shared__ int s_bad;
   pdl_trigger();
   pdl_wait();
@@ -97,6 +98,8 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitPara
       else {
         s_from[tid] = kv_off(c, layer, pf, 0, from & pm);
         s_to[tid] = kv_off(c, layer, pt, 0, to & pm);
+        s_efrom[tid] = exp_off(c, layer, pf, 0, from & pm);
+        s_eto[tid] = exp_off(c, layer, pt, 0, to & pm);
       }
     }
   }
@@ -105,21 +108,27 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitPara
     if (tid == 0) flag_err(c.err, (uint32_t)s_bad);
     tau = 0;
   }
-  const int D8 = c.D / 8, pieces = 2 * c.Hkv * D8;
+  const int D8 = (c.D << c.esh) / 16, pieces = 2 * c.Hkv * D8;
   // accepted rows that are already in place
   int first = 0;
   while (first < tau && s_path[first] == first) ++first;
   for (int u = tid; u < pieces; u += kCommitThreads) {
     const int kv = u / (c.Hkv * D8), w = u - kv * c.Hkv * D8, h = w / D8, e = w - h * D8;
-    char *base = (kv ? c.v : c.k) + 2 * (h * c.sh + e * 8);
+    char *base = (kv ? c.v : c.k) + (h * c.sh << c.esh) + 16 * e;
     for (int j0 = first; j0 < tau; j0 += 8) {
       uint4 x[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j0 + j < tau) x[j] = *reinterpret_cast<const uint4 *>(base + 2 * s_from[j0 + j]);
+        if (j0 + j < tau) x[j] = *reinterpret_cast<const uint4 *>(base + (s_from[j0 + j] << c.esh));
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j0 + j < tau) *reinterpret_cast<uint4 *>(base + 2 * s_to[j0 + j]) = x[j];
+        if (j0 + j < tau) *reinterpret_cast<uint4 *>(base + (s_to[j0 + j] << c.esh)) = x[j];
+    }
+  }
+  if (c.esh == 0) {  // the exponents, a thread per (k or v, head): in path order, as above
+    for (int u = tid; u < 2 * c.Hkv; u += kCommitThreads) {
+      uint8_t *base = (u >= c.Hkv ? c.ve + ((size_t)(u - c.Hkv) << c.page_shift) : c.ke + ((size_t)u << c.page_shift));
+      for (int j = first; j < tau; ++j) base[s_eto[j]] = base[s_efrom[j]];
     }
   }
   // the last layer's CTA of the sequence to finish sets the new length: by then
@@ -140,14 +149,21 @@ constexpr int kCopyThreads = 256;
 // rows [0, rows) of page `from` to page `to`, in one layer
 __device__ __forceinline__ void copy_rows(const CacheParams &c, int layer, int from, int to, int rows, int part,
                                           int parts) {
-  const int D8 = c.D / 8, per = c.Hkv * rows * D8;
+  const int D8 = (c.D << c.esh) / 16, per = c.Hkv * rows * D8;
   const long long f = kv_off(c, layer, from, 0, 0), t = kv_off(c, layer, to, 0, 0);
   for (int u = part; u < 2 * per; u += parts) {
     const int kv = u >= per, w = kv ? u - per : u;
     const int e = w % D8, hr = w / D8, r = hr % rows, h = hr / rows;
-    const long long off = h * c.sh + r * c.st + e * 8;
+    const long long off = ((h * c.sh + r * c.st) << c.esh) + 16 * e;
     char *base = kv ? c.v : c.k;
-    *reinterpret_cast<uint4 *>(base + 2 * (t + off)) = *reinterpret_cast<const uint4 *>(base + 2 * (f + off));
+    *reinterpret_cast<uint4 *>(base + (t << c.esh) + off) = *reinterpret_cast<const uint4 *>(base + (f << c.esh) + off);
+  }
+  if (c.esh == 0) {
+    for (int u = part; u < 2 * c.Hkv * rows; u += parts) {
+      const int kv = u >= c.Hkv * rows, w = kv ? u - c.Hkv * rows : u, h = w / rows, r = w % rows;
+      uint8_t *base = kv ? c.ve : c.ke;
+      base[exp_off(c, layer, to, h, r)] = base[exp_off(c, layer, from, h, r)];
+    }
   }
 }
 

@@ -1,0 +1,383 @@
+// rows.cu -- rows into the paged cache and back: norms of queries and keys for
+// each head, rotary positions and the append in one launch, for any number of
+// rows and for caches in 16 bits or in e4m3 codes; and cached tokens as packed
+// rows.
+//
+// Mathematics.  n(x) = x / sqrt(mean(x^2) + eps) * gain over a head, then each pair
+// turned by the angle position * f_i.  The angle is kept as a 64-bit fraction of a
+// turn: position * turns in wrapping integers is exact, and its upper 32 bits,
+// read as signed, go to sincospi.  Codes: e is the smallest integer with
+// max |y| <= 448 * 2^e, found from the bits of the maximum (448 = 1.75 * 2^8), so
+// that y * 2^-e is exact and the code's rounding (to nearest, ties to even) is
+// the only one after fp32.  A power of two loses nothing against a scale of 24 bits
+// but range: e4m3 is a floating format, and its steps are relative.
+//
+// Both kernels are bound by memory: a row is read and written once.  A head is 16
+// elements a lane, in two 16-byte pieces of which one lane holds both sides of
+// its pairs (half layout: pieces half a rotation apart), so that the sums and
+// maxima over a head are shuffles within D / 16 lanes.  A CTA takes a few rows,
+// whose sines and cosines it finds once for all heads, while its first pieces are
+// on their way.
+#include <cfloat>
+
+#include "tree_common.cuh"
+
+namespace dfv {
+namespace {
+
+constexpr int kRowThreads = 256;
+constexpr int kMaxRowsCta = 8;    // append: rows of a CTA
+constexpr int kAppendAhead = 5;   // items of a lane that are loaded at once
+constexpr int kReadRows = 32;     // read: rows of a CTA
+constexpr int kReadAhead = 4;
+
+struct AppendLaunch {
+  RopeParams p;
+  int rows;     // of a CTA
+  int by_seq;   // rows are counted as (sequence, row of it) with max_nodes each
+  int lanes;    // log2 of the lanes of a head
+};
+struct ReadLaunch {
+  CacheReadParams p;
+  int rows, lanes;
+};
+
+// log2 of the lanes that hold a head of D elements, 16 each
+int head_lanes(int D) {
+  int l = 0;
+  while ((16 << l) < D) ++l;
+  return l;
+}
+
+// a's code in the low byte, b's above it; what is not finite must be NaN by now
+__device__ __forceinline__ uint32_t codes_of(float a, float b) {
+  uint32_t r;
+  asm("{\n .reg .b16 x;\n cvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n cvt.u32.u16 %0, x;\n}" : "=r"(r) : "f"(a), "f"(b));
+  return r;
+}
+// e of a maximum that is finite
+__device__ __forceinline__ int exponent_of(float top) {
+  const uint32_t b = __float_as_uint(top);
+  const int e = (int)(b >> 23) - 135 + ((b & 0x7fffffu) > 0x600000u);
+  return e < -100 ? -100 : e;  // 120 at most: the largest finite value
+}
+
+// Pieces of 8 elements that lane `lid` holds of a head of 2 n pieces.
+__device__ __forceinline__ int2 pieces_of(int lid, int n, int r16, bool halves) {
+  if (!halves) return make_int2(lid, lid + n);
+  if (lid < r16) return make_int2(lid, lid + r16);
+  return make_int2(lid + r16, lid + n);  // behind the turned ones: 2 r16 + (lid - r16), and n - r16 further
+}
+
+template <bool F16>
+__device__ __forceinline__ void widen(const uint4 &a, float *x) {
+  const uint32_t *w = &a.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2<F16>(w[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+template <bool F16>
+__device__ __forceinline__ uint4 narrow(const float *x) {
+  return make_uint4(pack2<F16>(x[0], x[1]), pack2<F16>(x[2], x[3]), pack2<F16>(x[4], x[5]), pack2<F16>(x[6], x[7]));
+}
+
+template <bool F16, bool CODES>
+__global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_constant__ AppendLaunch L) {
+  __shared__ __align__(16) float2 s_cs[kMaxRowsCta][128];
+  __shared__ int s_row[kMaxRowsCta], s_page[kMaxRowsCta], s_tok[kMaxRowsCta];
+  const RopeParams &p = L.p;
+  const CacheParams &c = p.c;
+  const int tid = threadIdx.x, first = blockIdx.x * L.rows, NH = p.H + 2 * c.Hkv, items = L.rows * NH;
+  const int lid = tid & ((1 << L.lanes) - 1), group = tid >> L.lanes, groups = kRowThreads >> L.lanes;
+  const int n16 = c.D / 16, r16 = p.rot / 16;
+  const bool on = lid < n16;
+  pdl_trigger();
+  pdl_wait();
+
+  // item it: head it % NH of the CTA's row it / NH, queries first, then keys, then values
+  auto source = [&](int row, int h, bool &turned) {
+    turned = h < p.H + c.Hkv;
+    if (h < p.H) return p.q + 2 * (row * p.q_row + h * p.q_head);
+    if (turned) return p.k + 2 * (row * p.k_row + (h - p.H) * p.k_head);
+    return p.v + 2 * (row * p.v_row + (h - p.H - c.Hkv) * p.v_head);
+  };
+  uint4 x[kAppendAhead][2];
+  auto load = [&](int it0) {
+#pragma unroll
+    for (int u = 0; u < kAppendAhead; ++u) {
+      const int it = it0 + u * groups;
+      x[u][0] = x[u][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (it >= items || !on) continue;
+      const int j = it / NH, row = L.by_seq ? s_row[j] : first + j;
+      if ((unsigned)row >= (unsigned)p.t.n_rows) continue;
+      bool turned;
+      const uint4 *src = reinterpret_cast<const uint4 *>(source(row, it - j * NH, turned));
+      const int2 at = pieces_of(lid, n16, r16, turned && !p.inter);
+      x[u][0] = src[at.x];
+      x[u][1] = src[at.y];
+    }
+  };
+  if (!L.by_seq) load(group);
+
+  // ---- whose rows, and where they go
+  if (tid < L.rows) {
+    const int v = first + tid;
+    int row = -1, pg = -1, tok = 0, b = -1;
+    if (L.by_seq) {
+      b = v / p.t.max_nodes;
+      if (b >= p.t.n_seqs) b = -1;
+    } else if (v < p.t.n_rows) {
+      b = owner_of(p.t, v);
+    }
+    if (b >= 0) {
+      const SeqView s = seq_view(c, p.t, b);
+      const int i = L.by_seq ? v - b * p.t.max_nodes : v - s.row0;
+      if (i >= 0 && i < s.n) {
+        row = s.row0 + i;
+        if (s.s >= 0) {
+          pg = page_of(c, s.s, s.len + i);
+          tok = (s.len + i) & ((1 << c.page_shift) - 1);
+        }
+      }
+    }
+    s_row[tid] = row;
+    s_page[tid] = pg;
+    s_tok[tid] = tok;
+  }
+  if (L.by_seq) {
+    __syncthreads();
+    load(group);
+  }
+  // ---- sines and cosines, once for all heads
+  for (int u = tid; u < L.rows * (p.rot / 2); u += kRowThreads) {
+    const int j = u / (p.rot / 2), i = u - j * (p.rot / 2), row = L.by_seq ? s_row[j] : first + j;
+    if ((unsigned)row >= (unsigned)p.t.n_rows) continue;
+    const uint64_t turn = (uint64_t)(long long)p.positions[row] * p.turns[i];
+    float sn, cs;
+    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn, &cs);
+    s_cs[j][i] = make_float2(cs * p.scale, sn * p.scale);
+  }
+  __syncthreads();
+
+  for (int it0 = group; it0 - group < items; it0 += kAppendAhead * groups) {
+    if (it0 != group) load(it0);
+#pragma unroll
+    for (int u = 0; u < kAppendAhead; ++u) {
+      const int it = it0 + u * groups;
+      if (it - group >= items) break;  // the same for all threads
+      const int j = it < items ? it / NH : 0, h = it < items ? it - j * NH : 0;
+      const int row = s_row[j], pg = s_page[j];
+      const bool isq = h < p.H, turned = h < p.H + c.Hkv;
+      const int2 at = pieces_of(lid, n16, r16, turned && !p.inter);
+      float a[8], b[8];
+      widen<F16>(x[u][0], a);
+      widen<F16>(x[u][1], b);
+      const char *gain = isq ? p.q_gain : p.k_gain;
+      if (p.q_gain || p.k_gain) {  // the same for all threads
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+        for (int o = 1 << L.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (turned && gain && on) {
+          const float inv = rsqrtf(ss / (float)c.D + p.eps);
+          float g[8];
+          widen<F16>(__ldg(reinterpret_cast<const uint4 *>(gain) + at.x), g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) a[e] = a[e] * inv * g[e];
+          widen<F16>(__ldg(reinterpret_cast<const uint4 *>(gain) + at.y), g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) b[e] = b[e] * inv * g[e];
+        }
+      }
+      if (turned && on) {
+        if (p.inter) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int piece = q ? at.y : at.x;
+            float *y = q ? b : a;
+            if (piece < 2 * r16) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 cs = s_cs[j][4 * piece + e];
+                const float y0 = y[2 * e], y1 = y[2 * e + 1];
+                y[2 * e] = y0 * cs.x - y1 * cs.y;
+                y[2 * e + 1] = y1 * cs.x + y0 * cs.y;
+              }
+            }
+          }
+        } else if (lid < r16) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 cs = s_cs[j][8 * lid + e];
+            const float y0 = a[e], y1 = b[e];
+            a[e] = y0 * cs.x - y1 * cs.y;
+            b[e] = y1 * cs.x + y0 * cs.y;
+          }
+        }
+      }
+      float top = 0.f;
+      if (CODES) {  // of the finite elements; the others become NaN
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (!(fabsf(a[e]) <= FLT_MAX)) a[e] = NAN;
+          if (!(fabsf(b[e]) <= FLT_MAX)) b[e] = NAN;
+          top = fmaxf(top, fmaxf(fabsf(a[e]), fabsf(b[e])));  // fmaxf passes NaN over
+        }
+        for (int o = 1 << L.lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
+      if (it >= items || !on || row < 0) continue;
+      if (isq) {
+        uint4 *to = reinterpret_cast<uint4 *>(p.o + 2 * (row * p.o_row + h * p.o_head));
+        to[at.x] = narrow<F16>(a);
+        to[at.y] = narrow<F16>(b);
+        continue;
+      }
+      if (pg < 0) continue;
+      const int kh = turned ? h - p.H : h - p.H - c.Hkv;
+      const long long dst = kv_off(c, p.layer, pg, kh, s_tok[j]);
+      char *base = turned ? c.k : c.v;
+      if (CODES) {
+        const int e = exponent_of(top);
+        const float f = exp_value((uint32_t)(127 - e));
+        uint2 *to = reinterpret_cast<uint2 *>(base + dst);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float *y = q ? b : a;
+          to[q ? at.y : at.x] = make_uint2(codes_of(y[0] * f, y[1] * f) | codes_of(y[2] * f, y[3] * f) << 16,
+                                           codes_of(y[4] * f, y[5] * f) | codes_of(y[6] * f, y[7] * f) << 16);
+        }
+        if (lid == 0) (turned ? c.ke : c.ve)[exp_off(c, p.layer, pg, kh, s_tok[j])] = (uint8_t)(e + 127);
+      } else {
+        uint4 *to = reinterpret_cast<uint4 *>(base + 2 * dst);
+        to[at.x] = narrow<F16>(a);
+        to[at.y] = narrow<F16>(b);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- read
+template <bool CODES>
+__global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant__ ReadLaunch L) {
+  __shared__ int s_page[kReadRows], s_tok[kReadRows];
+  const CacheReadParams &p = L.p;
+  const CacheParams &c = p.c;
+  const int tid = threadIdx.x, first = blockIdx.x * L.rows;
+  const int lid = tid & ((1 << L.lanes) - 1), group = tid >> L.lanes, groups = kRowThreads >> L.lanes, n16 = c.D / 16;
+  pdl_trigger();
+  pdl_wait();
+  if (tid < L.rows) {
+    const int r = first + tid;
+    int pg = -2, tok = 0;  // -2: nobody's row, -1: zeros
+    if (r < p.t.n_rows) {
+      const int b = owner_of(p.t, r);
+      const int r0 = p.t.row_off[b], r1 = p.t.row_off[b + 1], s = p.t.seq ? p.t.seq[b] : b, i = r - r0;
+      if (r0 < 0 || r1 > p.t.n_rows || r1 - r0 > p.t.max_nodes) {
+        flag_err(c.err, DFV_KVERR_LEN);
+      } else if (i >= 0 && r < r1) {
+        pg = -1;
+        tok = i & ((1 << c.page_shift) - 1);
+        if ((unsigned)s >= (unsigned)c.max_seqs)
+          flag_err(c.err, DFV_KVERR_SEQ);
+        else if ((long long)i >= ((long long)c.max_pages << c.page_shift))
+          flag_err(c.err, DFV_KVERR_LEN);
+        else
+          pg = page_of(c, s, i);
+      }
+    }
+    s_page[tid] = pg;
+    s_tok[tid] = tok;
+  }
+  __syncthreads();
+  if (lid >= n16) return;
+  const int sides = (p.k ? 1 : 0) + (p.v ? 1 : 0), per = sides * c.Hkv, items = L.rows * per;
+  for (int it0 = group; it0 < items; it0 += kReadAhead * groups) {
+    uint4 x[kReadAhead][2];
+    uint32_t e[kReadAhead];
+#pragma unroll
+    for (int u = 0; u < kReadAhead; ++u) {
+      const int it = it0 + u * groups;
+      x[u][0] = x[u][1] = make_uint4(0u, 0u, 0u, 0u);
+      e[u] = 127u;
+      if (it >= items) continue;
+      const int j = it / per, w = it - j * per, h = w % c.Hkv, pg = s_page[j];
+      if (pg < 0) continue;
+      const bool isk = p.k && w < c.Hkv;
+      const char *src = (isk ? c.k : c.v) + (kv_off(c, p.layer, pg, h, s_tok[j]) << c.esh);
+      if (CODES) {
+        const uint2 a = reinterpret_cast<const uint2 *>(src)[lid], b = reinterpret_cast<const uint2 *>(src)[lid + n16];
+        x[u][0] = make_uint4(a.x, a.y, b.x, b.y);
+        e[u] = (isk ? c.ke : c.ve)[exp_off(c, p.layer, pg, h, s_tok[j])];
+      } else {
+        x[u][0] = reinterpret_cast<const uint4 *>(src)[lid];
+        x[u][1] = reinterpret_cast<const uint4 *>(src)[lid + n16];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kReadAhead; ++u) {
+      const int it = it0 + u * groups;
+      if (it >= items) continue;
+      const int j = it / per, w = it - j * per, h = w % c.Hkv;
+      if (s_page[j] == -2) continue;
+      const bool isk = p.k && w < c.Hkv;
+      const long long row = first + j;
+      uint4 *to = reinterpret_cast<uint4 *>(isk ? p.k + 2 * (row * p.k_row + h * p.k_head) : p.v + 2 * (row * p.v_row + h * p.v_head));
+      if (CODES) {
+        const float f = exp_value(e[u]);
+        const uint32_t *codes = &x[u][0].x;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float y[8];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 lo = unpack2<true>(codes_f16(codes[2 * q + i])), hi = unpack2<true>(codes_f16_hi(codes[2 * q + i]));
+            y[4 * i] = lo.x * f;
+            y[4 * i + 1] = lo.y * f;
+            y[4 * i + 2] = hi.x * f;
+            y[4 * i + 3] = hi.y * f;
+          }
+          to[lid + q * n16] = narrow<false>(y);
+        }
+      } else {
+        to[lid] = x[u][0];
+        to[lid + n16] = x[u][1];
+      }
+    }
+  }
+}
+
+template <bool F16, bool CODES>
+cudaError_t append_typed(const AppendLaunch &L, cudaStream_t s) {
+  const long long rows = L.by_seq ? (long long)L.p.t.n_seqs * L.p.t.max_nodes : L.p.t.n_rows;
+  return launch_chained(append_kernel<F16, CODES>, dim3((unsigned)((rows + L.rows - 1) / L.rows)), dim3(kRowThreads), 0, s, L);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope_append(const RopeParams &p, cudaStream_t s) {
+  static thread_local AppendLaunch L;
+  L.p = p;
+  L.by_seq = p.by_seq;
+  L.lanes = head_lanes(p.c.D);
+  // as many rows as a CTA's first loads cover, one while there are fewer CTAs than SMs hold
+  const int fit = kAppendAhead * (kRowThreads >> L.lanes) / (p.H + 2 * p.c.Hkv);
+  L.rows = p.t.n_rows <= 4 * kAttnCtas || fit < 1 ? 1 : fit > kMaxRowsCta ? kMaxRowsCta : fit;
+  if (p.c.esh == 0) return append_typed<false, true>(L, s);
+  return p.c.f16 ? append_typed<true, false>(L, s) : append_typed<false, false>(L, s);
+}
+
+cudaError_t launch_cache_read(const CacheReadParams &p, cudaStream_t s) {
+  static thread_local ReadLaunch L;
+  L.p = p;
+  L.lanes = head_lanes(p.c.D);
+  const int sides = (p.k ? 1 : 0) + (p.v ? 1 : 0), fit = kReadAhead * (kRowThreads >> L.lanes) / (sides * p.c.Hkv);
+  L.rows = fit < 1 ? 1 : fit > kReadRows ? kReadRows : fit;
+  const dim3 grid((unsigned)((p.t.n_rows + L.rows - 1) / L.rows));
+  return p.c.esh == 0 ? launch_chained(read_kernel<true>, grid, dim3(kRowThreads), 0, s, L)
+                      : launch_chained(read_kernel<false>, grid, dim3(kRowThreads), 0, s, L);
+}
+
+}  // namespace dfv

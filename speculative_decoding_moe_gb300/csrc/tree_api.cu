@@ -5,26 +5,19 @@
 
 #include "tree_common.cuh"
 
-namespace {
-
-using dfv::api_fail;
-
-inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
-inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+namespace dfv {
 
 int launched(cudaError_t e, const char *where) {
   if (e == cudaSuccess) return DFV_OK;
   return api_fail(DFV_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-bool words(const void *p) { return aligned(p, 4); }  // NULL too
-bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s <= ((int64_t)1 << 40); }
-
 int check_cache(const dfv_kv_cache *c) {
   if (!c) return api_fail(DFV_ERR_INVALID_ARG, "cache is NULL");
   if (c->n_layers < 1 || c->n_pages < 1 || c->n_kv_heads < 1 || c->max_seqs < 1 || c->max_pages < 1 || c->head_dim < 1)
     return api_fail(DFV_ERR_INVALID_ARG, "non-positive cache size");
-  if (c->dtype != DFV_BF16 && c->dtype != DFV_F16) return api_fail(DFV_ERR_UNSUPPORTED, "cache dtype %d", c->dtype);
+  if (c->dtype != DFV_BF16 && c->dtype != DFV_F16 && c->dtype != DFV_E4M3)
+    return api_fail(DFV_ERR_UNSUPPORTED, "cache dtype %d", c->dtype);
   if (c->page_size < 8 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
     return api_fail(DFV_ERR_UNSUPPORTED, "page_size %d: a power of two in 8..256 is needed", c->page_size);
   if (c->head_dim % 16 || c->head_dim > 256)
@@ -38,24 +31,16 @@ int check_cache(const dfv_kv_cache *c) {
   if (!stride_ok(c->stride_layer) || !stride_ok(c->stride_page) || !stride_ok(c->stride_head) ||
       !stride_ok(c->stride_token))
     return api_fail(DFV_ERR_INVALID_ARG, "cache strides must be non-negative multiples of 8 elements");
+  if (c->dtype == DFV_E4M3) {
+    if ((c->stride_layer | c->stride_page | c->stride_head | c->stride_token) & 15)
+      return api_fail(DFV_ERR_INVALID_ARG, "strides of a cache in codes must be multiples of 16 elements");
+    if (!c->k_exp || !c->v_exp || !words(c->k_exp) || !words(c->v_exp))
+      return api_fail(DFV_ERR_INVALID_ARG, "k_exp/v_exp NULL or not 4-byte aligned");
+  }
   if (c->stride_token < c->head_dim)
     return api_fail(DFV_ERR_INVALID_ARG, "stride_token %lld below head_dim", (long long)c->stride_token);
   if (!c->page_table || !c->lens || !words(c->page_table) || !words(c->lens) || !words(c->refs) || !words(c->err))
     return api_fail(DFV_ERR_INVALID_ARG, "page_table/lens NULL, or page_table/lens/refs/err not 4-byte aligned");
-  return DFV_OK;
-}
-
-int check_tree(const dfv_tree_batch *t) {
-  if (!t) return api_fail(DFV_ERR_INVALID_ARG, "tree is NULL");
-  if (t->n_seqs < 1 || t->n_seqs > DFV_MAX_TREE_SEQS)
-    return api_fail(DFV_ERR_INVALID_ARG, "n_seqs %d outside 1..%d", t->n_seqs, DFV_MAX_TREE_SEQS);
-  if (t->max_nodes < 1 || t->max_nodes > DFV_MAX_TREE)
-    return api_fail(DFV_ERR_INVALID_ARG, "max_nodes %d outside 1..%d", t->max_nodes, DFV_MAX_TREE);
-  if (t->n_rows < 1 || t->n_rows > DFV_MAX_TREE * DFV_MAX_TREE_SEQS)
-    return api_fail(DFV_ERR_INVALID_ARG, "n_rows %d outside 1..%d", t->n_rows, DFV_MAX_TREE * DFV_MAX_TREE_SEQS);
-  if (!t->row_off || !words(t->row_off) || !words(t->seq))
-    return api_fail(DFV_ERR_INVALID_ARG, "row_off NULL, or row_off/seq not 4-byte aligned");
-  if (t->mask && !aligned(t->mask, 8)) return api_fail(DFV_ERR_INVALID_ARG, "mask not 8-byte aligned");
   return DFV_OK;
 }
 
@@ -65,8 +50,8 @@ int check_ws(const void *ws, size_t have, size_t need) {
   return DFV_OK;
 }
 
-dfv::CacheParams cache_params(const dfv_kv_cache *c) {
-  dfv::CacheParams p = {};
+CacheParams cache_params(const dfv_kv_cache *c) {
+  CacheParams p = {};
   p.k = (char *)c->k;
   p.v = (char *)c->v;
   p.sl = c->stride_layer;
@@ -86,7 +71,56 @@ dfv::CacheParams cache_params(const dfv_kv_cache *c) {
   p.lens = c->lens;
   p.refs = c->refs;
   p.err = c->err;
+  p.esh = 1;
+  if (c->dtype == DFV_E4M3) {  // the fields behind err are there
+    p.esh = 0;
+    p.ke = c->k_exp;
+    p.ve = c->v_exp;
+  }
   return p;
+}
+
+// What dfv_rope_append and dfv_norm_rope_append take alike, but for the rows.
+int check_rope(const dfv_kv_cache *cache, int layer, int n_heads, int rot_dim, int interleaved, float scale,
+               const RopeParams &p) {
+  if (layer < 0 || layer >= cache->n_layers)
+    return api_fail(DFV_ERR_INVALID_ARG, "layer %d outside 0..%d", layer, cache->n_layers - 1);
+  if (n_heads < 1 || n_heads > 16384) return api_fail(DFV_ERR_INVALID_ARG, "n_heads %d outside 1..16384", n_heads);
+  if (rot_dim < 16 || rot_dim % 16 || rot_dim > cache->head_dim)
+    return api_fail(DFV_ERR_UNSUPPORTED, "rot_dim %d: a multiple of 16 up to head_dim %d is needed", rot_dim,
+                    cache->head_dim);
+  if (interleaved != 0 && interleaved != 1) return api_fail(DFV_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  if (!std::isfinite(scale)) return api_fail(DFV_ERR_INVALID_ARG, "scale must be finite");
+  if (!p.turns || !aligned(p.turns, 8) || !p.positions || !words(p.positions))
+    return api_fail(DFV_ERR_INVALID_ARG, "turns/positions NULL, or not 8- and 4-byte aligned");
+  if (!p.q || !p.k || !p.v || !p.o || !aligned(p.q, 16) || !aligned(p.k, 16) || !aligned(p.v, 16) || !aligned(p.o, 16))
+    return api_fail(DFV_ERR_INVALID_ARG, "q/k/v/q_out NULL or not 16-byte aligned");
+  if (!stride_ok(p.q_row) || !stride_ok(p.q_head) || !stride_ok(p.k_row) || !stride_ok(p.k_head) || !stride_ok(p.v_row) ||
+      !stride_ok(p.v_head) || !stride_ok(p.o_row) || !stride_ok(p.o_head))
+    return api_fail(DFV_ERR_INVALID_ARG, "row and head strides must be non-negative multiples of 8 elements");
+  if (p.q == p.o && (p.q_row != p.o_row || p.q_head != p.o_head))
+    return api_fail(DFV_ERR_INVALID_ARG, "q_out is q: the strides must be the same");
+  return DFV_OK;
+}
+
+}  // namespace dfv
+
+namespace {
+
+using namespace dfv;
+
+int check_tree(const dfv_tree_batch *t) {
+  if (!t) return api_fail(DFV_ERR_INVALID_ARG, "tree is NULL");
+  if (t->n_seqs < 1 || t->n_seqs > DFV_MAX_TREE_SEQS)
+    return api_fail(DFV_ERR_INVALID_ARG, "n_seqs %d outside 1..%d", t->n_seqs, DFV_MAX_TREE_SEQS);
+  if (t->max_nodes < 1 || t->max_nodes > DFV_MAX_TREE)
+    return api_fail(DFV_ERR_INVALID_ARG, "max_nodes %d outside 1..%d", t->max_nodes, DFV_MAX_TREE);
+  if (t->n_rows < 1 || t->n_rows > DFV_MAX_TREE * DFV_MAX_TREE_SEQS)
+    return api_fail(DFV_ERR_INVALID_ARG, "n_rows %d outside 1..%d", t->n_rows, DFV_MAX_TREE * DFV_MAX_TREE_SEQS);
+  if (!t->row_off || !words(t->row_off) || !words(t->seq))
+    return api_fail(DFV_ERR_INVALID_ARG, "row_off NULL, or row_off/seq not 4-byte aligned");
+  if (t->mask && !aligned(t->mask, 8)) return api_fail(DFV_ERR_INVALID_ARG, "mask not 8-byte aligned");
+  return DFV_OK;
 }
 
 dfv::TreeParams tree_params(const dfv_tree_batch *t) {
@@ -169,23 +203,6 @@ int dfv_rope_append(const dfv_kv_cache *cache, int layer, const dfv_tree_batch *
   int st = check_cache(cache);
   if (st) return st;
   if ((st = check_tree(tree))) return st;
-  if (layer < 0 || layer >= cache->n_layers)
-    return api_fail(DFV_ERR_INVALID_ARG, "layer %d outside 0..%d", layer, cache->n_layers - 1);
-  if (n_heads < 1 || n_heads > 16384) return api_fail(DFV_ERR_INVALID_ARG, "n_heads %d outside 1..16384", n_heads);
-  if (rot_dim < 16 || rot_dim % 16 || rot_dim > cache->head_dim)
-    return api_fail(DFV_ERR_UNSUPPORTED, "rot_dim %d: a multiple of 16 up to head_dim %d is needed", rot_dim,
-                    cache->head_dim);
-  if (interleaved != 0 && interleaved != 1) return api_fail(DFV_ERR_INVALID_ARG, "interleaved must be 0 or 1");
-  if (!std::isfinite(scale)) return api_fail(DFV_ERR_INVALID_ARG, "scale must be finite");
-  if (!turns || !aligned(turns, 8) || !positions || !words(positions))
-    return api_fail(DFV_ERR_INVALID_ARG, "turns/positions NULL, or not 8- and 4-byte aligned");
-  if (!q || !k || !v || !q_out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16))
-    return api_fail(DFV_ERR_INVALID_ARG, "q/k/v/q_out NULL or not 16-byte aligned");
-  if (!stride_ok(q_row) || !stride_ok(q_head) || !stride_ok(k_row) || !stride_ok(k_head) || !stride_ok(v_row) ||
-      !stride_ok(v_head) || !stride_ok(o_row) || !stride_ok(o_head))
-    return api_fail(DFV_ERR_INVALID_ARG, "row and head strides must be non-negative multiples of 8 elements");
-  if (q == q_out && (q_row != o_row || q_head != o_head))
-    return api_fail(DFV_ERR_INVALID_ARG, "q_out is q: the strides must be the same");
   dfv::RopeParams p = {};
   p.c = cache_params(cache);
   p.t = tree_params(tree);
@@ -208,6 +225,11 @@ int dfv_rope_append(const dfv_kv_cache *cache, int layer, const dfv_tree_batch *
   p.o_row = o_row;
   p.o_head = o_head;
   p.positions = positions;
+  if ((st = check_rope(cache, layer, n_heads, rot_dim, interleaved, scale, p))) return st;
+  if (cache->dtype == DFV_E4M3) {  // the codes are found where the norms are
+    p.by_seq = 1;
+    return launched(dfv::launch_norm_rope_append(p, (cudaStream_t)stream), "rotary append launch");
+  }
   return launched(dfv::launch_rope_append(p, (cudaStream_t)stream), "rotary append launch");
 }
 
@@ -215,6 +237,7 @@ static int check_attn_shape(const dfv_kv_cache *cache, const dfv_tree_batch *tre
   int st = check_cache(cache);
   if (st) return st;
   if ((st = check_tree(tree))) return st;
+  if (cache->dtype == DFV_E4M3) return api_fail(DFV_ERR_UNSUPPORTED, "tree attention over a cache in codes");
   if (cache->head_dim != 64 && cache->head_dim != 128)
     return api_fail(DFV_ERR_UNSUPPORTED, "attention takes head_dim 64 or 128, not %d", cache->head_dim);
   if (n_heads < 1 || n_heads % cache->n_kv_heads)

@@ -185,12 +185,6 @@ struct SegWalk {
 };
 
 // ---------------------------------------------------------------- pieces
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // A page id as read from the table; one out of range is read as page 0.
 __device__ __forceinline__ int checked_page(const CacheParams &c, int pg) {
   if ((unsigned)pg < (unsigned)c.n_pages) return pg;

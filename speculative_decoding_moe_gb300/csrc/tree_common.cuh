@@ -18,8 +18,11 @@ struct CacheParams {
   int max_seqs, max_pages;
   int32_t *table, *lens, *refs;
   uint32_t *err;
+  int esh;            // log2 of an element's bytes: 1, or 0 for e4m3 codes
+  uint8_t *ke, *ve;   // e4m3: exponent bytes [layer][page][head][token of the page]
 };
 
+// Drafted trees, or (max_nodes = max_rows, no mask) a batch of rows.
 struct TreeParams {
   int n_seqs, n_rows, max_nodes;
   const int32_t *seq, *row_off;
@@ -36,6 +39,33 @@ struct RopeParams {
   char *o;
   long long q_row, q_head, k_row, k_head, v_row, v_head, o_row, o_head;
   const int32_t *positions;
+  // norm_rope_append only
+  const char *q_gain, *k_gain;  // null: no norm
+  float eps;
+  int by_seq;  // row_off may be in any order
+};
+
+struct CacheReadParams {
+  CacheParams c;
+  TreeParams t;
+  int layer;
+  char *k, *v;
+  long long k_row, k_head, v_row, v_head;
+};
+
+struct PromptParams {
+  int n_seqs, n_rows, max_rows, n_keys, max_keys;
+  const int32_t *row_off, *key_off;
+  int H, Hkv, G, D, f16;
+  float scale_log2;  // scale * log2(e)
+  const char *q;
+  char *o;
+  long long q_row, q_head, o_row, o_head;
+  const char *k, *v;
+  long long k_row, k_head, v_row, v_head;
+  float *lse;
+  uint32_t *kverr;  // the caller's error bits, or null
+  unsigned *err;    // workspace error word (bounded waits)
 };
 
 struct TreeAttnParams {
@@ -155,6 +185,39 @@ __device__ __forceinline__ long long kv_off(const CacheParams &c, int l, int pg,
   return l * c.sl + pg * c.sp + h * c.sh + row * c.st;
 }
 
+// Byte of token `row` of page pg, head h, layer l in the exponents of a cache in codes.
+__device__ __forceinline__ size_t exp_off(const CacheParams &c, int l, int pg, int h, int row) {
+  return ((((size_t)l * c.n_pages + pg) * c.Hkv + h) << c.page_shift) + row;
+}
+
+// 2^e of an exponent byte e + 127.
+__device__ __forceinline__ float exp_value(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Two codes (low byte first) as an fp16 pair: exact, NaN stays NaN.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t two) {
+  uint32_t r;
+  asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %1;\n cvt.rn.f16x2.e4m3x2 %0, x;\n}" : "=r"(r) : "r"(two));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes_f16_hi(uint32_t two) {
+  uint32_t r;
+  asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %1;\n cvt.rn.f16x2.e4m3x2 %0, y;\n}" : "=r"(r) : "r"(two));
+  return r;
+}
+
+// The sequence that owns packed row r, or -1: the last one whose rows begin at or before it.
+__device__ __forceinline__ int owner_of(const TreeParams &t, int r) {
+  int lo = 0, hi = t.n_seqs;  // row_off[lo] <= r < row_off[hi], the ends taken for granted
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.row_off[mid] <= r)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
 __device__ __forceinline__ uint64_t row_mask(const TreeParams &t, int row0, int i) {
   return t.mask ? t.mask[row0 + i] : (i >= 63 ? ~0ull : (2ull << i) - 1ull);
 }
@@ -163,6 +226,12 @@ __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 template <bool F16>
@@ -181,6 +250,10 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 
 cudaError_t launch_rope_append(const RopeParams &p, cudaStream_t s);
+cudaError_t launch_norm_rope_append(const RopeParams &p, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheReadParams &p, cudaStream_t s);
+size_t prompt_attn_ws(int D);
+cudaError_t launch_prompt_attn(const PromptParams &p, void *ws, cudaStream_t s, char *why, size_t why_len);
 // Rows per CTA, CTAs per range and ranges of an attention call.
 constexpr int kAttnCtas = 152;  // one per SM of GB300
 struct AttnPlan {
@@ -200,6 +273,18 @@ cudaError_t launch_free(const PagesParams &p, cudaStream_t s);
 
 // status reporting of api.cu (thread-local detail text)
 int api_fail(int status, const char *fmt, ...);
+
+// ---- checks that the entry points share (tree_api.cu)
+inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+inline bool words(const void *p) { return aligned(p, 4); }  // NULL too
+inline bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s <= ((int64_t)1 << 40); }
+int launched(cudaError_t e, const char *where);
+int check_cache(const dfv_kv_cache *c);
+int check_ws(const void *ws, size_t have, size_t need);
+int check_rope(const dfv_kv_cache *cache, int layer, int n_heads, int rot_dim, int interleaved, float scale,
+               const RopeParams &p);
+CacheParams cache_params(const dfv_kv_cache *c);
 
 // Raises a kernel's limit of dynamic shared memory, once per device (the call took
 // 0.5 us of an attention call's 4.4).

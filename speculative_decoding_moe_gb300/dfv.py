@@ -22,13 +22,13 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdfv.so")
 BIND_PATH = os.path.join(HERE, "_dfvbind.so")
 
-F32, BF16, MXFP4, Q8, F16 = 0, 1, 2, 3, 4
+F32, BF16, MXFP4, Q8, F16, E4M3 = 0, 1, 2, 3, 4, 5
 # device error bits (DFV_DEVERR_* in include/dfv.h)
 DEVERR_STAGE_WAIT, DEVERR_SLOT_WAIT, DEVERR_DRAIN_WAIT, DEVERR_GRID_WAIT = 0x1, 0x2, 0x4, 0x8
 DEVERR_SCALE_RANGE, DEVERR_REDUCE_WAIT, DEVERR_ROUTING = 0x10, 0x20, 0x40
 # cache error bits (DFV_KVERR_* in include/dfv.h)
 KVERR_PAGE, KVERR_LEN, KVERR_NO_PAGE, KVERR_PATH, KVERR_SEQ = 0x1, 0x2, 0x4, 0x8, 0x10
-MAX_TREE, MAX_TREE_SEQS = 64, 1024
+MAX_TREE, MAX_TREE_SEQS, MAX_ROWS = 64, 1024, 1 << 24
 _NAMES = {"f32": F32, "bf16": BF16, "mxfp4": MXFP4, "q8": Q8}
 EXPORTS = ("dfv_version", "dfv_status_string", "dfv_last_error_detail", "dfv_profile_set_events",
            "dfv_read_device_error", "dfv_set_path", "dfv_last_layer_path", "dfv_fused_unavailable_reason",
@@ -40,7 +40,8 @@ EXPORTS = ("dfv_version", "dfv_status_string", "dfv_last_error_detail", "dfv_pro
            "dfv_set_stack_launch",
            "dfv_rope_table", "dfv_rope_append", "dfv_tree_attention_workspace_size", "dfv_tree_attention",
            "dfv_logits_workspace_size", "dfv_logits_process", "dfv_accept_tree", "dfv_cache_workspace_size",
-           "dfv_cache_commit", "dfv_cache_copy_pages", "dfv_pages_reserve", "dfv_pages_fork", "dfv_pages_free")
+           "dfv_cache_commit", "dfv_cache_copy_pages", "dfv_pages_reserve", "dfv_pages_fork", "dfv_pages_free",
+           "dfv_norm_rope_append", "dfv_cache_read", "dfv_prompt_attention_workspace_size", "dfv_prompt_attention")
 
 
 class DfvError(RuntimeError):
@@ -67,12 +68,17 @@ class CCache(ctypes.Structure):
                                              "max_seqs", "max_pages")]
                 + [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
                 + [(n, ctypes.c_int64) for n in ("stride_layer", "stride_page", "stride_head", "stride_token")]
-                + [(n, ctypes.c_void_p) for n in ("page_table", "lens", "refs", "err")])
+                + [(n, ctypes.c_void_p) for n in ("page_table", "lens", "refs", "err", "k_exp", "v_exp")])
 
 
 class CTree(ctypes.Structure):
     _fields_ = [("n_seqs", ctypes.c_int), ("n_rows", ctypes.c_int), ("max_nodes", ctypes.c_int),
                 ("seq", ctypes.c_void_p), ("row_off", ctypes.c_void_p), ("mask", ctypes.c_void_p)]
+
+
+class CRows(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int), ("n_rows", ctypes.c_int), ("max_rows", ctypes.c_int),
+                ("seq", ctypes.c_void_p), ("row_off", ctypes.c_void_p)]
 
 
 class CRules(ctypes.Structure):
@@ -89,6 +95,10 @@ class CCacheHandle(ctypes.Structure):
 
 class CTreeHandle(ctypes.Structure):
     _fields_ = [("c", CTree), ("index", ctypes.c_int)]
+
+
+class CRowsHandle(ctypes.Structure):
+    _fields_ = [("c", CRows), ("index", ctypes.c_int)]
 
 
 class CRulesHandle(ctypes.Structure):
@@ -153,6 +163,11 @@ def _load():
         L.dfv_pages_reserve.argtypes = [P, P, P, I, P, S, P]
         L.dfv_pages_fork.argtypes = [P, P, P, I, P, S, P]
         L.dfv_pages_free.argtypes = [P, P, I, P]
+        L.dfv_norm_rope_append.argtypes = [P, I, P, I, P, P, F, I, I, F, P, P, L64, L64, P, L64, L64, P, L64, L64, P, P, L64, L64, P]
+        L.dfv_cache_read.argtypes = [P, I, P, P, L64, L64, P, L64, L64, P]
+        L.dfv_prompt_attention_workspace_size.restype = S
+        L.dfv_prompt_attention_workspace_size.argtypes = [P, I, I, I]
+        L.dfv_prompt_attention.argtypes = [I, P, P, I, I, I, F, P, L64, L64, P, L64, L64, P, L64, L64, P, L64, L64, P, P, P, S, P]
         _lib = L
     return _lib
 
@@ -480,23 +495,32 @@ def _given(t: Optional[torch.Tensor], what: str, dtype, shape, index: int) -> Op
 class KVCache:
     """A paged key/value cache of all layers (include/dfv.h, dfv_kv_cache).
 
-    k, v        [n_layers, n_pages, n_kv_heads, page_size, head_dim] bf16 or fp16, any strides that both share with
-                the last dimension contiguous (permuted views of token-major pages, halves of one allocation)
+    k, v        [n_layers, n_pages, n_kv_heads, page_size, head_dim] bf16, fp16 or float8_e4m3fn, any strides that both
+                share with the last dimension contiguous (permuted views of token-major pages, halves of one allocation)
     page_table  [max_seqs, max_pages] int32, -1 where there is no page
     lens        [max_seqs] int32 committed tokens
     refs        [n_pages] int32 holders of each page, 0 = free (for the page calls)
     err         [1] int32 error bits (KVERR_*), sticky; made here when not given
+    k_exp, v_exp [n_layers, n_pages, n_kv_heads, page_size] uint8, for float8_e4m3fn: a token's values are its codes
+                times 2^(exp - 127); rows in and out of such a cache are bf16
     """
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
-                 refs: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None):
+                 refs: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+                 k_exp: Optional[torch.Tensor] = None, v_exp: Optional[torch.Tensor] = None):
         if k.dim() != 5 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
             raise ValueError("k and v must be alike: [layers, pages, kv heads, page size, head dim]")
-        if k.dtype not in (torch.bfloat16, torch.float16):
-            raise TypeError("the cache must be bf16 or fp16, got %s" % k.dtype)
+        kind = {torch.bfloat16: BF16, torch.float16: F16, torch.float8_e4m3fn: E4M3}.get(k.dtype)
+        if kind is None:
+            raise TypeError("the cache must be bf16, fp16 or float8_e4m3fn, got %s" % k.dtype)
         if k.stride(4) != 1 or v.stride(4) != 1 or any(a != b for a, b, n in zip(k.stride(), v.stride(), k.shape) if n > 1):
             raise ValueError("k and v must have the same strides and a contiguous head dimension")
         at = k.get_device()
+        if kind == E4M3:
+            _need(k_exp, "k_exp", torch.uint8, k.shape[:4], at)
+            _need(v_exp, "v_exp", torch.uint8, k.shape[:4], at)
+        elif k_exp is not None or v_exp is not None:
+            raise ValueError("k_exp and v_exp belong to a float8_e4m3fn cache, this one is %s" % k.dtype)
         if page_table.dim() != 2:
             raise ValueError("page_table must be [max_seqs, max_pages], got %s" % (tuple(page_table.shape),))
         _need(page_table, "page_table", torch.int32, page_table.shape, at)
@@ -507,14 +531,15 @@ class KVCache:
         _need(err, "err", torch.int32, (1,), at)
         self.index = at
         self.k, self.v, self.page_table, self.lens, self.refs, self.err = k, v, page_table, lens, refs, err
+        self.k_exp, self.v_exp = k_exp, v_exp
         self.n_layers, self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self.dtype = k.dtype
         st = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(4)]
         self.c = CCache(self.n_layers, self.n_pages, self.page_size, self.n_kv_heads, self.head_dim,
-                        BF16 if k.dtype == torch.bfloat16 else F16, page_table.shape[0], page_table.shape[1],
+                        kind, page_table.shape[0], page_table.shape[1],
                         k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], k.stride(3) if self.page_size > 1 else self.head_dim,
                         page_table.data_ptr(), lens.data_ptr(), None if refs is None else refs.data_ptr(),
-                        err.data_ptr())
+                        err.data_ptr(), None if k_exp is None else k_exp.data_ptr(), None if v_exp is None else v_exp.data_ptr())
         self._handle = CCacheHandle(self.c, at)
         self.c = self._handle.c
         self.ref = ctypes.byref(self.c)
@@ -525,9 +550,12 @@ class KVCache:
               max_pages: int, dtype=torch.bfloat16, device="cuda") -> "KVCache":
         """An empty cache: every page free, every sequence without tokens."""
         kv = torch.zeros(2, n_layers, n_pages, n_kv_heads, page_size, head_dim, dtype=dtype, device=device)
+        exp = [None, None]
+        if dtype == torch.float8_e4m3fn:
+            exp = torch.full((2, n_layers, n_pages, n_kv_heads, page_size), 127, dtype=torch.uint8, device=device)
         i32 = dict(dtype=torch.int32, device=device)
         return cls(kv[0], kv[1], torch.full((max_seqs, max_pages), -1, **i32), torch.zeros(max_seqs, **i32),
-                   refs=torch.zeros(n_pages, **i32))
+                   refs=torch.zeros(n_pages, **i32), k_exp=exp[0], v_exp=exp[1])
 
     def errors(self) -> int:
         """Error bits so far (waits for the device)."""
@@ -553,6 +581,26 @@ class TreeBatch:
         self.c = CTree(self.n_seqs, self.n_rows, self.max_nodes, None if seq is None else seq.data_ptr(),
                        row_off.data_ptr(), None if mask is None else mask.data_ptr())
         self._handle = CTreeHandle(self.c, at)
+        self.c = self._handle.c
+        self.ref = ctypes.byref(self.c)
+        self.addr = ctypes.addressof(self._handle)
+
+
+class RowBatch:
+    """The rows of one call, any number per sequence (include/dfv.h, dfv_row_batch): sequence b's are rows row_off[b] ..
+    row_off[b + 1] of n_rows, at most max_rows; seq [n_seqs] int32 cache sequences (None: 0, 1, ...)."""
+
+    def __init__(self, row_off: torch.Tensor, n_rows: int, max_rows: int, seq: Optional[torch.Tensor] = None):
+        if row_off.dim() != 1 or row_off.numel() < 2:
+            raise ValueError("row_off needs one entry per sequence and one more")
+        at = row_off.get_device()
+        _need(row_off, "row_off", torch.int32, row_off.shape, at)
+        self.n_seqs, self.n_rows, self.max_rows = row_off.numel() - 1, int(n_rows), int(max_rows)
+        _given(seq, "seq", torch.int32, (self.n_seqs,), at)
+        self.index = at
+        self.row_off, self.seq = row_off, seq
+        self.c = CRows(self.n_seqs, self.n_rows, self.max_rows, None if seq is None else seq.data_ptr(), row_off.data_ptr())
+        self._handle = CRowsHandle(self.c, at)
         self.c = self._handle.c
         self.ref = ctypes.byref(self.c)
         self.addr = ctypes.addressof(self._handle)
@@ -601,6 +649,40 @@ def rope_append(cache: KVCache, layer: int, tree: TreeBatch, rope: Rope, q: torc
     return (_ext or _bind()).rope_append(cache.addr, layer, tree.addr, rope.head_dim, rope.rot_dim, rope.interleaved,
                                          rope.scale, rope.turns_addr, q, k, v, positions, out,
                                          _on(stream, cache.index), rope.index)
+
+
+def norm_rope_append(cache: KVCache, layer: int, rows: RowBatch, rope: Rope, q: torch.Tensor, k: torch.Tensor,
+                     v: torch.Tensor, positions: torch.Tensor, q_gain: Optional[torch.Tensor] = None,
+                     k_gain: Optional[torch.Tensor] = None, eps: float = 1e-6, out: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """Normed and rotated q (out, a new tensor or q itself), and the rows' normed and rotated k and their v stored into
+    the cache behind the committed tokens, for any number of rows.  q_gain, k_gain [dim]: the gains of the norm over each
+    head's elements (None: no norm); q [rows, heads, dim], k and v [rows, kv heads, dim] may be slices of one projection."""
+    return (_ext or _bind()).norm_rope_append(cache.addr, layer, rows.addr, rope.head_dim, rope.rot_dim, rope.interleaved,
+                                              rope.scale, rope.turns_addr, q, k, v, positions, q_gain, k_gain, eps, out,
+                                              _on(stream, cache.index), rope.index)
+
+
+def cache_read(cache: KVCache, layer: int, rows: RowBatch, k: Optional[torch.Tensor] = None,
+               v: Optional[torch.Tensor] = None, stream=None):
+    """(k, v) [rows, kv heads, dim]: row i of a sequence is its token i in the cache, counted from its first one (tokens
+    that were appended but not committed yet too); a float8_e4m3fn cache gives bf16."""
+    return (_ext or _bind()).cache_read(cache.addr, layer, rows.addr, cache.k, k, v, _on(stream, cache.index))
+
+
+def prompt_attention_workspace_size(rows: RowBatch, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(_load().dfv_prompt_attention_workspace_size(rows.ref, int(n_heads), int(n_kv_heads), int(head_dim)))
+
+
+def prompt_attention(rows: RowBatch, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ws: torch.Tensor,
+                     keys: Optional[RowBatch] = None, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal attention of packed prompts: q [rows, heads, dim] over k, v [key rows, kv heads, dim], bf16 or fp16.
+    keys: the key rows of each sequence when they are not its q rows (the q rows are then the last of them); scale:
+    1/sqrt(dim) by default; lse: optional fp32 [rows, heads] that receives ln(sum exp); err: optional int32 [1] that
+    receives KVERR_LEN for offsets out of range."""
+    return (_ext or _bind()).prompt_attention(rows.addr, 0 if keys is None else keys.addr, q, k, v, ws, scale, out, lse, err,
+                                              _on(stream, rows.index))
 
 
 def tree_attention_workspace_size(cache: KVCache, tree: TreeBatch, n_heads: int) -> int:
