@@ -468,17 +468,19 @@ bool encode_kv(CUtensorMap *map, const CacheParams &c, const char *base, int lay
   if (!fn) return false;
   // a dimension of one entry has no stride of its own
   const cuuint64_t one = 16;
-  const cuuint64_t tok[2] = {(cuuint64_t)1 << c.page_shift, (cuuint64_t)c.st * 2};
-  const cuuint64_t head[2] = {(cuuint64_t)c.Hkv, c.Hkv > 1 ? (cuuint64_t)c.sh * 2 : one};
-  const cuuint64_t page[2] = {(cuuint64_t)c.n_pages, c.n_pages > 1 ? (cuuint64_t)c.sp * 2 : one};
+  const cuuint64_t tok[2] = {(cuuint64_t)1 << c.page_shift, (cuuint64_t)c.st << c.esh};
+  const cuuint64_t head[2] = {(cuuint64_t)c.Hkv, c.Hkv > 1 ? (cuuint64_t)c.sh << c.esh : one};
+  const cuuint64_t page[2] = {(cuuint64_t)c.n_pages, c.n_pages > 1 ? (cuuint64_t)c.sp << c.esh : one};
   const cuuint64_t *a = swap ? head : tok, *b = swap ? tok : head;
   const cuuint64_t dims[4] = {(cuuint64_t)c.D, a[0], b[0], page[0]};
   const cuuint64_t strides[3] = {a[1], b[1], page[1]};
-  const cuuint32_t box[4] = {64, swap ? 1u : (cuuint32_t)rows, swap ? (cuuint32_t)rows : 1u, 1};
+  // 64 elements of 16 bits, or the whole head of codes: rows of 128 bytes, or of 64
+  const bool codes = c.esh == 0;
+  const cuuint32_t box[4] = {codes ? (cuuint32_t)c.D : 64u, swap ? 1u : (cuuint32_t)rows, swap ? (cuuint32_t)rows : 1u, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult r = fn(map, c.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                        const_cast<char *>(base + 2 * layer * c.sl), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const CUresult r = fn(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : c.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                        const_cast<char *>(base + (layer * c.sl << c.esh)), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, codes && c.D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     snprintf(why, why_len, "tensor map of the cache refused (%d)", (int)r);
@@ -500,7 +502,7 @@ cudaError_t launch_mma(const AttnLaunch &L, cudaStream_t s) {
 template <bool F16, int D>
 cudaError_t launch_typed(AttnLaunch &L, cudaStream_t s) {
   const int R = L.p.t.max_nodes * L.p.G;
-  cudaError_t e = L.rows >= 128 ? launch_attn_tc(L, s) : launch_mma<F16, D>(L, s);
+  cudaError_t e = L.rows >= 128 ? launch_attn_tc(L, s) : L.p.c.esh == 0 ? launch_attn_codes(L, s) : launch_mma<F16, D>(L, s);
   if (e != cudaSuccess) return e;
   const int blocks = (R + kJoinRows - 1) / kJoinRows;
   // CTAs of eight rows fill the SMs from about 4000 rows on
@@ -535,7 +537,7 @@ cudaError_t launch_tree_attn(const TreeAttnParams &p, const AttnPlan &a, void *w
   L.n_groups = a.n_groups;
   L.inv_g = (65536u + p.G - 1) / p.G;
   attn_sections(&L, a, p.t.n_seqs, p.c.Hkv, p.c.D, ws);
-  const int tile = L.rows >= 128 ? 128 : kKt, page = 1 << p.c.page_shift, rows = page < tile ? page : tile;
+  const int tile = L.rows >= 128 ? 128 : p.c.esh == 0 ? attn_codes_tile(p.c.D) : kKt, page = 1 << p.c.page_shift, rows = page < tile ? page : tile;
   L.swap = p.c.Hkv > 1 && p.c.sh < p.c.st;
   if (!encode_kv(&L.tm_k, p.c, p.c.k, p.layer, rows, L.swap, why, why_len) ||
       !encode_kv(&L.tm_v, p.c, p.c.v, p.layer, rows, L.swap, why, why_len))

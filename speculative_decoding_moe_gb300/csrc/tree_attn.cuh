@@ -22,6 +22,9 @@ struct AttnLaunch {
 };
 
 cudaError_t launch_attn_tc(const AttnLaunch &L, cudaStream_t s);  // tree_attn_tc.cu: rows 128 or 256
+// tree_attn_codes.cu: rows 16 over a cache in codes, and the keys of its tiles
+cudaError_t launch_attn_codes(const AttnLaunch &L, cudaStream_t s);
+int attn_codes_tile(int D);
 
 // Sections of the attention workspace; returns its size.  Places for the states of
 // kAttnCtas CTAs whatever the plan (n_groups * n_rt of them run, a few less where n_rt
@@ -247,8 +250,11 @@ __device__ __noinline__ float unseen(const TreeAttnParams &p, const SeqView &v, 
     const int pos = v.len + j;
     const int pg = checked_page(p.c, p.c.table[(size_t)v.s * p.c.max_pages + (pos >> p.c.page_shift)]);
     const long long off = kv_off(p.c, p.layer, pg, h, pos & ((1 << p.c.page_shift) - 1)) + d;
-    const uint32_t w = reinterpret_cast<const uint16_t *>(p.c.v)[off];
-    const float y = unpack2<F16>(w).x;
+    float y;
+    if (p.c.esh == 0)  // codes: NaN is all that is not finite
+      y = unpack2<true>(codes_f16(reinterpret_cast<const uint8_t *>(p.c.v)[off])).x;
+    else
+      y = unpack2<F16>(reinterpret_cast<const uint16_t *>(p.c.v)[off]).x;
     if (!isfinite(y)) x += y;
   }
   return x;
