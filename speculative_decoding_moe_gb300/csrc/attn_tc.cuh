@@ -106,6 +106,14 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
+__device__ __forceinline__ void less32(float *s, float x) {
+#pragma unroll
+  for (int q = 0; q < 32; q += 2) {
+    const float2 y = add2(make_float2(s[q], s[q + 1]), make_float2(-x, -x));
+    s[q] = y.x;
+    s[q + 1] = y.y;
+  }
+}
 __device__ __forceinline__ float max32(const float *s, float m) {
 #pragma unroll
   for (int q = 0; q < 32; q += 2) m = fmaxf(m, fmaxf(s[q], s[q + 1]));
@@ -122,6 +130,29 @@ __device__ __forceinline__ void exp32(const float *s, float c, float z, uint32_t
     l = add2(l, y);
     x[e] = pack2<F16>(y.x, y.y);
   }
+}
+
+// Scores of a tile whose first key is node j0 (below 0: committed): what the row
+// does not see becomes -inf, in place.  A short loop: it runs once per sequence, and
+// unrolled its instructions took longer to fetch than to execute.
+__device__ __forceinline__ void mask_tile(uint32_t t_s, int j0, uint64_t mask) {
+#pragma unroll 1
+  for (int q = 0; q < 128; q += 16) {
+    const int j = j0 + q;  // node of the first of 16 keys
+    if (j + 16 <= 0) continue;
+    uint32_t sees;
+    if (j >= 0)
+      sees = j < 64 ? (uint32_t)(mask >> j) : 0u;
+    else
+      sees = (uint32_t)(mask << -j) | ((1u << -j) - 1u);
+    float s[16];
+    tmem_ld16(t_s + q, s);
+    uint32_t x[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = sees >> e & 1u ? __float_as_uint(s[e]) : 0xff800000u;
+    tmem_st16(t_s + q, x);
+  }
+  tmem_wait_st();
 }
 
 }  // namespace

@@ -560,7 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
           uint32_t x[32];
           float2 l2;
           for (;;) {
-            const float z = (m == -INFINITY ? 0.f : m * c) - kBias;
+            // (rounded up: the largest p stays within its bound however large the scores are)
+            const float z = (m == -INFINITY ? 0.f : __fmul_ru(m, c)) - kBias;
             float s0[32], s1[32], mx = m;
             l2 = make_float2(0.f, 0.f);
             tmem_ld32(t_s + 64 * hf, s0);
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       tc_fence_after();
       bar_sync_n(1, 256);  // s_bad, and Q's place
       const int bad = s_bad;
-      const float z = (m == -INFINITY ? 0.f : m * c) - kBias;
+      const float z = (m == -INFINITY ? 0.f : __fmul_ru(m, c)) - kBias;
       const bool whole = wk.whole();
       const int slot = wk.slot(blockIdx.x);
       const size_t row = wk.s.row0 + (size_t)i;

@@ -237,8 +237,6 @@ static int check_attn_shape(const dfv_kv_cache *cache, const dfv_tree_batch *tre
   int st = check_cache(cache);
   if (st) return st;
   if ((st = check_tree(tree))) return st;
-  if (cache->dtype == DFV_E4M3 && n_heads / cache->n_kv_heads * tree->max_nodes > 16)
-    return api_fail(DFV_ERR_UNSUPPORTED, "tree attention over a cache in codes: more than 16 rows");
   if (cache->head_dim != 64 && cache->head_dim != 128)
     return api_fail(DFV_ERR_UNSUPPORTED, "attention takes head_dim 64 or 128, not %d", cache->head_dim);
   if (n_heads < 1 || n_heads % cache->n_kv_heads)

@@ -502,7 +502,9 @@ cudaError_t launch_mma(const AttnLaunch &L, cudaStream_t s) {
 template <bool F16, int D>
 cudaError_t launch_typed(AttnLaunch &L, cudaStream_t s) {
   const int R = L.p.t.max_nodes * L.p.G;
-  cudaError_t e = L.rows >= 128 ? launch_attn_tc(L, s) : L.p.c.esh == 0 ? launch_attn_codes(L, s) : launch_mma<F16, D>(L, s);
+  const bool codes = L.p.c.esh == 0;
+  cudaError_t e = L.rows >= 128 ? (codes ? launch_attn_codes_tc(L, s) : launch_attn_tc(L, s))
+                                : (codes ? launch_attn_codes(L, s) : launch_mma<F16, D>(L, s));
   if (e != cudaSuccess) return e;
   const int blocks = (R + kJoinRows - 1) / kJoinRows;
   // CTAs of eight rows fill the SMs from about 4000 rows on

@@ -25,6 +25,7 @@ cudaError_t launch_attn_tc(const AttnLaunch &L, cudaStream_t s);  // tree_attn_t
 // tree_attn_codes.cu: rows 16 over a cache in codes, and the keys of its tiles
 cudaError_t launch_attn_codes(const AttnLaunch &L, cudaStream_t s);
 int attn_codes_tile(int D);
+cudaError_t launch_attn_codes_tc(const AttnLaunch &L, cudaStream_t s);  // tree_attn_codes_tc.cu: rows 128 or 256
 
 // Sections of the attention workspace; returns its size.  Places for the states of
 // kAttnCtas CTAs whatever the plan (n_groups * n_rt of them run, a few less where n_rt

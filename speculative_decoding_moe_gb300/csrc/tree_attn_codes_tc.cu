@@ -1,0 +1,627 @@
+// tree_attn_codes_tc.cu -- tree attention over a cache in e4m3 codes with many rows
+// per kv head, on the fifth-generation tensor cores.
+//
+// The products and the two warpgroups are those of tree_attn_tc.cu (SINGLE: 128
+// rows, even and odd tiles; DUAL: 256 rows, each tile); between the copies and the
+// products, four warps widen the codes of a tile into fp16 in shared memory, a key
+// row a thread.
+//
+// Mathematics.  Key j is K_j 2^a_j, value j is V_j 2^b_j.  With A and B the largest a
+// and b of a tile of 128 keys, the products take K_j 2^(a_j - A) and V_j 2^(b_j - B) in
+// fp16, exact for tokens within 2^15 of the tile's largest power, and absolutely off
+// by 2^-25 of it beyond.  A and B are then constants of the tile: scores are
+// x_j = c 2^A s_j, the weights 2^(x_j + B - M), and the sum takes a tile's weights
+// times 2^-B.  M follows the maximum of x_j + B; it is raised, and O rescaled, when
+// some x_j + B is more than 8 above it.  Precision of q and of the weights as in
+// tree_attn_codes.cu.
+//
+// A tile's scores are taken in halves of 64 keys: the maximum of a half is found from
+// registers before its exponentials, and its product starts while the other half
+// is in them.  Before the second half raises M it waits for the first half's product.
+//
+// What binds: shared memory.  Per tile of 128 keys of 128 elements the codes are
+// written (256 clocks at 128 bytes), read and written as fp16 (768), and read by the
+// products (768 a row tile), beside 512 clocks of products a row tile.
+//
+// Warps 0-3 and 4-7 are the two warpgroups, warp 8 issues the MMAs, warps 9-11 stream
+// codes with TMA, warps 12-15 widen.  Tensor memory: S0 S1 O0 O1 of 128 columns each;
+// P (16-bit pairs) over S.
+#include <cstdio>
+
+#include "attn_tc.cuh"
+#include "tree_attn.cuh"
+
+namespace dfv {
+namespace {
+
+constexpr int kKeys = 128;
+constexpr int kThreads = 512;
+constexpr int kProducers = 3;
+constexpr float kBias = 6.f;
+constexpr int kTells = 16;  // tiles whose powers are kept: more than are between their widening and their scores
+
+template <int D, bool DUAL>
+struct CodeTcShape {
+  static constexpr uint32_t kCodes = kKeys * D;      // a K or V tile in codes
+  static constexpr uint32_t kTile = kKeys * D * 2;   // and in fp16
+  static constexpr int kSlots = D == 64 ? 6 : 3;     // of fp16 tiles
+  static constexpr int kCSlots = D == 64 ? 8 : DUAL ? 4 : 5;  // of codes
+  static constexpr int kOver = DUAL ? 5 : 2;         // tiles' worth of time that a pair costs at least
+  static constexpr uint32_t kQ = (DUAL ? 2 : 1) * 128 * D * 2;
+  static constexpr size_t kSmem = 1024 + kQ + (size_t)kSlots * kTile + (size_t)kCSlots * kCodes;
+};
+
+// Codes of 16 elements (a 16-byte chunk) as fp16 times m
+__device__ __forceinline__ void widen16(const uint4 &x, __half2 m, uint4 &lo, uint4 &hi) {
+  const uint32_t *w = &x.x;
+  uint32_t y[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[2 * i] = codes_f16(w[i]);
+    y[2 * i + 1] = codes_f16_hi(w[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __half2 z = __hmul2(*reinterpret_cast<const __half2 *>(&y[i]), m);
+    y[i] = *reinterpret_cast<const uint32_t *>(&z);
+  }
+  lo = make_uint4(y[0], y[1], y[2], y[3]);
+  hi = make_uint4(y[4], y[5], y[6], y[7]);
+}
+
+// 2^-d in fp16, d >= 0 (0 below its subnormals)
+__device__ __forceinline__ __half2 half_power(int d) {
+  const uint32_t b = d <= 14 ? (uint32_t)(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
+  const uint32_t two = b | b << 16;
+  return *reinterpret_cast<const __half2 *>(&two);
+}
+
+template <int D, bool DUAL>
+__global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const __grid_constant__ AttnLaunch L) {
+  using S = CodeTcShape<D, DUAL>;
+  constexpr int LA = DUAL ? 1 : 2;  // K tiles ahead of the V tile in the rings
+  extern __shared__ __align__(16) unsigned char sm_raw[];
+  unsigned char *sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
+  __shared__ __align__(8) unsigned long long s_full[S::kSlots], s_empty[S::kSlots], s_cfull[S::kCSlots], s_cempty[S::kCSlots],
+      s_sfull[2], s_pready[2][2], s_half[2], s_odone[2], s_qready, s_drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  __shared__ SchedStart s_start;
+  __shared__ long long s_scan[kThreads / 32];
+  __shared__ volatile int s_bad[4];    // of a segment, in turn: NaN was left out
+  __shared__ volatile int2 s_tell[kTells];  // A and B of a tile
+  __shared__ int2 s_most[2][4];        // of the widening warps' keys, in turn
+  __shared__ float s_crow[256];        // c times the power that a row of q was divided by
+  const TreeAttnParams &p = L.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  unsigned char *s_q = sm, *s_ring = sm + S::kQ, *s_codes = s_ring + (size_t)S::kSlots * S::kTile;
+  const uint32_t q_addr = smem_u32(s_q), ring = smem_u32(s_ring), codes = smem_u32(s_codes);
+  if (tid == 0) {
+    s_abort = 0;
+    for (int s = 0; s < 4; ++s) s_bad[s] = 0;
+    for (int s = 0; s < S::kSlots; ++s) {
+      mbar_init(smem_u32(&s_full[s]), 4);
+      mbar_init(smem_u32(&s_empty[s]), 1);
+    }
+    for (int s = 0; s < S::kCSlots; ++s) {
+      mbar_init(smem_u32(&s_cfull[s]), kProducers);
+      mbar_init(smem_u32(&s_cempty[s]), 4);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(smem_u32(&s_sfull[w]), 1);
+      mbar_init(smem_u32(&s_pready[w][0]), 128);
+      mbar_init(smem_u32(&s_pready[w][1]), 128);
+      mbar_init(smem_u32(&s_half[w]), 1);
+      mbar_init(smem_u32(&s_odone[w]), 1);
+    }
+    mbar_init(smem_u32(&s_qready), 256);
+    mbar_init(smem_u32(&s_drain), 1);
+    mbar_init_fence();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(&s_tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  pdl_wait();
+  pdl_trigger();  // the join may now read the call's inputs
+  sched_start<kThreads, kKeys, S::kOver>(L, blockIdx.x, s_scan, &s_start);  // syncs the CTA
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int row0 = (int)(blockIdx.x % L.n_rt) * L.rows;  // first row of this CTA
+  SegWalk<kKeys, S::kOver> wk(L, s_start);
+
+  if (warp >= 9 && warp < 12) {
+    // ---------------------------------------------------------------- producers: every third box of a tile each
+    const int me = warp - 9;
+    int st = 0, ph = 0, issued = 0;
+    bool ok = true;
+    const int shift = p.c.page_shift, boxes = shift >= 7 ? 1 : kKeys >> shift, rows = kKeys / boxes;
+    while (ok && wk.next()) {
+      if (row0 >= wk.v.n * p.G) continue;
+      const int pages = wk.v.s < 0 ? 0 : (wk.total + (1 << shift) - 1) >> shift, n = wk.t1 - wk.t0;
+      const int32_t *table = p.c.table + (size_t)(wk.v.s < 0 ? 0 : wk.v.s) * p.c.max_pages;
+      auto id = [&](int j) {  // this lane's page of the segment's tile j, as it is in the table
+        const int at = (((wk.t0 + j) * kKeys) >> shift) + lane;
+        return j < n && lane < boxes && at < pages ? table[at] : -1;
+      };
+      auto load = [&](const CUtensorMap *map, int j, int pg) {
+        ok = ok && __all_sync(0xffffffffu,
+                              mbar_wait_fast(smem_u32(&s_cempty[st]), ph ^ 1, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
+        if (!ok) return;
+        const uint32_t fb = smem_u32(&s_cfull[st]), dst = codes + (uint32_t)st * S::kCodes;
+        const int nb = min(boxes, pages - (((wk.t0 + j) * kKeys) >> shift)), mine = nb > me ? (nb - me + kProducers - 1) / kProducers : 0;
+        if (lane == 0) {
+          if (mine > 0)
+            mbar_expect_tx(fb, (uint32_t)mine * rows * D);
+          else
+            mbar_arrive(fb);
+        }
+        __syncwarp();
+        const int tok = ((wk.t0 + j) * kKeys) & ((1 << shift) - 1);  // 0 unless a page holds several tiles
+        for (int b = me; b < nb; b += kProducers)
+          tma_kv(dst + (uint32_t)(b * rows * D), map, 0, tok, wk.h, __shfl_sync(0xffffffffu, pg, b), L.swap, fb);
+        ++issued;
+        if (++st == S::kCSlots) { st = 0; ph ^= 1; }
+      };
+      auto checked = [&](int pg, int j) {  // ids were fetched a tile or more before they are looked at
+        const int at = (((wk.t0 + j) * kKeys) >> shift) + lane;
+        return j < n && lane < boxes && at < pages ? checked_page(p.c, pg) : 0;
+      };
+      // pages of tiles j .. j + LA, and one more on its way
+      int pg[LA + 2];
+#pragma unroll
+      for (int k = 0; k < LA + 2; ++k) pg[k] = id(k);
+#pragma unroll
+      for (int k = 0; k < LA; ++k) {
+        pg[k] = checked(pg[k], k);
+        if (k < n) load(&L.tm_k, k, pg[k]);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        load(&L.tm_v, j, pg[0]);
+        pg[LA] = checked(pg[LA], j + LA);
+        if (j + LA < n) load(&L.tm_k, j + LA, pg[LA]);
+#pragma unroll
+        for (int k = 0; k < LA + 1; ++k) pg[k] = pg[k + 1];
+        pg[LA + 1] = id(j + LA + 2);
+      }
+    }
+    // no copy may land after the CTA exits: wait for the last fill of every slot
+    volatile int never = 0;
+    for (int j = issued - S::kCSlots < 0 ? 0 : issued - S::kCSlots; j < issued; ++j)
+      if (!mbar_wait(smem_u32(&s_cfull[j % S::kCSlots]), (j / S::kCSlots) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never)) break;
+  } else if (warp >= 12) {
+    // ---------------------------------------------------------------- widening: a key row a thread
+    const int kt = tid - 384, ww = warp - 12;
+    int st = 0, ph = 0, cst = 0, cph = 0, seg = 0;
+    unsigned tiles = 0;  // of the segments before
+    bool ok = true;
+    const int shift = p.c.page_shift;
+    // (after a wait gives up the loops still run to the end, so the four warps meet at
+    // every barrier)
+    while (wk.next()) {
+      if (row0 >= wk.v.n * p.G) continue;
+      const int n = wk.t1 - wk.t0;
+      const int32_t *table = p.c.table + (size_t)(wk.v.s < 0 ? 0 : wk.v.s) * p.c.max_pages;
+      // the powers of this thread's key: page id two tiles ahead, bytes one ahead
+      auto id = [&](int j) {
+        const int key = (wk.t0 + j) * kKeys + kt;
+        return j < n && key < wk.total ? table[key >> shift] : -1;
+      };
+      auto bytes = [&](int j, int pg) {  // 0 past the end
+        const int key = (wk.t0 + j) * kKeys + kt;
+        if (j >= n || key >= wk.total) return make_int2(0, 0);
+        const size_t at = exp_off(p.c, p.layer, (unsigned)pg < (unsigned)p.c.n_pages ? pg : 0, wk.h, key & ((1 << shift) - 1));
+        return make_int2(p.c.ke[at], p.c.ve[at]);
+      };
+      int pg1 = id(1), b0 = 0;
+      int2 next = bytes(0, id(0));
+      int2 mine = make_int2(0, 0), most = make_int2(0, 0);
+      int db[LA + 1];  // how far this key's b is below its tile's, of the tiles whose V is to come
+#pragma unroll
+      for (int k = 0; k < LA + 1; ++k) db[k] = 0;
+      // one tile of codes to fp16 times m; V: zero past the last node, NaN of a node taken out
+      auto widen = [&](__half2 m, int jn, bool isv) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_cfull[cst]), cph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_empty[st]), ph ^ 1, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
+        if (!ok) return;
+        const unsigned char *from = s_codes + (size_t)cst * S::kCodes + kt * D;
+        unsigned char *to = s_ring + (size_t)st * S::kTile + kt * 128;
+        uint4 x[D / 16];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {  // chunk order turned by the row: no bank conflicts
+          const int at = D == 128 ? i ^ (kt & 7) : i ^ ((kt >> 1) & 3);  // the chunk's place in the tile; the chunk itself is i
+          x[i] = *reinterpret_cast<const uint4 *>(from + 16 * at);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s_cempty[cst]));
+        if (isv && jn >= 0) {
+          bool nan = false;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t *w = &x[i].x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t z = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              nan = nan || z;
+              w[e] = jn < wk.nodes ? w[e] & ~((z >> 7) * 255u) : 0u;
+            }
+          }
+          if (nan && jn < wk.nodes) s_bad[seg & 3] = 1;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint4 lo, hi;
+          widen16(x[i], m, lo, hi);
+          unsigned char *half = to + ((2 * i) >> 3) * 16384;
+          *reinterpret_cast<uint4 *>(half + ((((2 * i) & 7) ^ (kt & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4 *>(half + ((((2 * i + 1) & 7) ^ (kt & 7)) << 4)) = hi;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s_full[st]));
+        if (++st == S::kSlots) { st = 0; ph ^= 1; }
+        if (++cst == S::kCSlots) { cst = 0; cph ^= 1; }
+      };
+      auto keys = [&](int j) {  // K of tile j, and both powers of the tile
+        mine = next;
+        next = bytes(j + 1, pg1);
+        pg1 = id(j + 2);
+        const int a = __reduce_max_sync(0xffffffffu, mine.x), b = __reduce_max_sync(0xffffffffu, mine.y);
+        const unsigned tile = tiles + (unsigned)j;
+        if (lane == 0) s_most[tile & 1][ww] = make_int2(a, b);
+        bar_sync_n(2, 128);
+        most = make_int2(0, 0);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          most.x = max(most.x, s_most[tile & 1][w].x);
+          most.y = max(most.y, s_most[tile & 1][w].y);
+        }
+        if (kt == 0) {
+          s_tell[tile % kTells].x = most.x;
+          s_tell[tile % kTells].y = most.y;
+        }
+        widen(half_power(most.x - mine.x), -1, false);
+        b0 = most.y - mine.y;
+      };
+#pragma unroll
+      for (int k = 0; k < LA; ++k)
+        if (k < n) {
+          keys(k);
+          db[k] = b0;
+        }
+      for (int j = 0; j < n; ++j) {
+        widen(half_power(db[0]), (wk.t0 + j) * kKeys + kt - wk.v.len, true);
+        if (j + LA < n) {
+          keys(j + LA);
+          db[LA] = b0;
+        }
+#pragma unroll
+        for (int k = 0; k < LA; ++k) db[k] = db[k + 1];
+      }
+      tiles += (unsigned)n;
+      ++seg;
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- MMA issue
+    int st = 0, ph = 0, seg = 0;
+    unsigned np[2] = {0u, 0u};  // tiles of each warpgroup whose P was awaited
+    bool ok = true;
+    const uint32_t iq = idesc_16<true>(kKeys, false), iv = idesc_16<true>(D, true);
+    auto full = [&]() {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_full[st]), ph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+      tc_fence_after();
+    };
+    auto done = [&]() {  // the slot is free once the MMAs issued so far have read it
+      tc_commit_elect(smem_u32(&s_empty[st]));
+      if (++st == S::kSlots) { st = 0; ph ^= 1; }
+    };
+    auto qk = [&](int w) {
+      const uint32_t kb = ring + (uint32_t)st * S::kTile, qb = q_addr + (DUAL ? (uint32_t)w * 128u * D * 2u : 0u);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        tc_mma_ss(tmem + (uint32_t)w * 128u, sdesc_k128(qb + (ks >> 2) * 16384) + (uint64_t)(2 * (ks & 3)),
+                  sdesc_k128(kb + (ks >> 2) * 16384) + (uint64_t)(2 * (ks & 3)), iq, ks > 0 ? 1u : 0u);
+      tc_commit_elect(smem_u32(&s_sfull[w]));
+    };
+    auto pv = [&](int w, bool first, bool last) {
+      const uint32_t vb = ring + (uint32_t)st * S::kTile;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_pready[w][hf]), np[w] & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+        if (!ok) return;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)
+          tc_mma_ts(tmem + 256u + (uint32_t)w * 128u, tmem + (uint32_t)w * 128u + (uint32_t)ks * 8u,
+                    sdesc_mn128(vb + (uint32_t)ks * 2048u), iv, (first && ks == 0) ? 0u : 1u);
+        if (hf == 0) tc_commit_elect(smem_u32(&s_half[w]));
+      }
+      ++np[w];
+      if (last) tc_commit_elect(smem_u32(&s_odone[w]));
+    };
+    while (ok && wk.next()) {
+      if (row0 >= wk.v.n * p.G) continue;
+      const int n = wk.t1 - wk.t0;
+      ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_qready), seg & 1, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+      ++seg;
+      tc_fence_after();
+      if (DUAL) {
+        full();
+        if (!ok) break;
+        qk(0);
+        qk(1);
+        done();
+        for (int j = 0; j < n && ok; ++j) {
+          // V_j, then K_j+1; each warpgroup's next scores right after its own product
+          full();
+          if (!ok) break;
+          pv(0, j == 0, j == n - 1);
+          if (!ok) break;
+          if (j + 1 < n) {
+            const int sv = st, pv_ = ph;
+            if (++st == S::kSlots) { st = 0; ph ^= 1; }
+            full();
+            if (!ok) break;
+            qk(0);
+            st = sv; ph = pv_;
+          }
+          pv(1, j == 0, j == n - 1);
+          if (!ok) break;
+          done();  // V_j
+          if (j + 1 < n) {
+            qk(1);
+            done();  // K_j+1
+          }
+        }
+      } else {
+        for (int k = 0; k < LA && k < n && ok; ++k) {
+          full();
+          if (!ok) break;
+          qk(k);
+          done();
+        }
+        for (int j = 0; j < n && ok; ++j) {
+          full();
+          if (!ok) break;
+          pv(j & 1, j < 2, j + 2 >= n);
+          if (!ok) break;
+          done();
+          if (j + LA < n) {
+            full();
+            if (!ok) break;
+            qk(j & 1);
+            done();
+          }
+        }
+      }
+    }
+    // every MMA issued has completed before tensor memory is released
+    tc_commit_elect(smem_u32(&s_drain));
+    volatile int never = 0;
+    mbar_wait(smem_u32(&s_drain), 0u, p.err, DFV_DEVERR_DRAIN_WAIT, &never);
+  } else {
+    // ---------------------------------------------------------------- softmax and output
+    const int w = warp >> 2, wt = tid & 127;  // warpgroup, and its thread = row of the tile
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t t_s = lane_base + (uint32_t)w * 128u, t_o = lane_base + 256u + (uint32_t)w * 128u;
+    unsigned nt = 0;     // tiles this warpgroup has taken
+    unsigned outs = 0;   // segments it has put out
+    unsigned tiles = 0, seg = 0;  // of the segments before
+    bool ok = true;
+    // after a wait gives up the loops still run to the end without touching
+    // tensor memory, so the warpgroups meet at every barrier
+    while (wk.next()) {
+      const int R = wk.v.n * p.G;
+      if (row0 >= R) continue;  // never the CTA that tells of the pair: its rows are the first
+      const int n = wk.t1 - wk.t0;
+      // rows into the swizzled layout as fp16, each divided by a power of two; past R zero
+      {
+        constexpr int kCh = D / 8, kStep = 256 / kCh;  // 16-byte chunks of a row; rows apart
+        constexpr int kIter = (DUAL ? 256 : 128) / kStep, kBatch = kIter < 8 ? kIter : 8;
+        const int ch = tid % kCh;
+        const char *qh = p.q + 2 * (wk.v.row0 * p.q_row + (long long)wk.h * p.G * p.q_head + ch * 8);
+        uint4 x[kBatch];
+#pragma unroll
+        for (int k0 = 0; k0 < kIter; k0 += kBatch) {
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int r = row0 + tid / kCh + (k0 + k) * kStep, i = node_of(L, r);
+            x[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < R) x[k] = *reinterpret_cast<const uint4 *>(qh + 2 * (i * p.q_row + (r - i * p.G) * p.q_head));
+          }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int rr = tid / kCh + (k0 + k) * kStep;
+            uint32_t *v = &x[k].x;
+            float top = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(v[e])), fabsf(bf16_hi(v[e]))));
+#pragma unroll
+            for (int o = 1; o < kCh; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // times 2^(127 - exponent), the ends of the range the same
+            const int f = min(200, max(1, 254 - (int)(__float_as_uint(top) >> 23)));
+            const float up = exp_value((uint32_t)f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = pack2<true>(bf16_lo(v[e]) * up, bf16_hi(v[e]) * up);
+            if (ch == 0) s_crow[rr] = p.scale_log2 * exp_value((uint32_t)(254 - f));
+            *reinterpret_cast<uint4 *>(s_q + (rr >> 7) * (128 * D * 2) + (ch >> 3) * 16384 + (rr & 127) * 128 +
+                                       (((ch & 7) ^ (rr & 7)) << 4)) = x[k];
+          }
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(smem_u32(&s_qready));
+      bar_sync_n(1, 256);  // s_crow
+
+      const int rr = DUAL ? w * 128 + wt : wt, r = row0 + rr;  // this thread's row
+      const float crow = s_crow[rr];
+      uint64_t mask = 0;
+      if (r < R) mask = wk.mask_of(r);
+      float m = -INFINITY, l = 0.f;
+      bool started = false;
+      for (int j = DUAL ? 0 : w; j < n; j += DUAL ? 1 : 2) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_sfull[w]), nt & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+        ++nt;
+        if (!ok) continue;
+        tc_fence_after();
+        const int j0 = (wk.t0 + j) * kKeys - wk.v.len;  // node number of the tile's first key
+        if (j0 + kKeys > 0) mask_tile(t_s, j0, mask);   // tree nodes or keys past the end in the tile
+        const unsigned tell = (tiles + (unsigned)j) % kTells;
+        // in (0, infinity), so that -inf stays what it is
+        const float c = fminf(fmaxf(crow * exp_value((uint32_t)s_tell[tell].x), 0x1p-120f), 0x1p120f);
+        const int eb = min(max(s_tell[tell].y, 1), 253);
+        const float B = (float)(eb - 127), back = exp_value((uint32_t)(254 - eb));
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          float s0[32], s1[32];
+          tmem_ld32(t_s + 64 * hf, s0);
+          tmem_ld32(t_s + 64 * hf + 32, s1);
+          tmem_wait_ld32(s0);
+          tmem_wait_ld32(s1);
+          const float high = max32(s1, max32(s0, -INFINITY)), top = fmaf(high, c, B);
+          if (__any_sync(0xffffffffu, top - 8.f > m)) {
+            // products into O before these scores: those of the tiles before were
+            // complete when the scores were; the first half's own is waited for
+            if (hf == 1) {
+              ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_half[w]), (nt - 1u) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+              tc_fence_after();
+            }
+            const float mx = fmaxf(m, top), f = m == -INFINITY ? 0.f : ex2(m - mx);
+            l *= f;
+            if (ok && (started || hf == 1)) {
+#pragma unroll 1
+              for (int q = 0; q < D; q += 16) {
+                float o[16];
+                tmem_ld16(t_o + q, o);
+                uint32_t y[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(o[e] * f);
+                tmem_st16(t_o + q, y);
+              }
+            }
+            m = mx;
+          }
+          // x + B - M by differences from the half's maximum: whatever the scores' size, the
+          // exponents are 8 at most and right next to it
+          const float from = high == -INFINITY ? 0.f : high, z = (high == -INFINITY ? 0.f : m - top) - kBias;
+          float2 l2 = make_float2(0.f, 0.f);
+          uint32_t x[16];
+          less32(s0, from);
+          exp32<true>(s0, c, z, x, l2);
+          tmem_st16(t_s + 32 * hf, x);
+          less32(s1, from);
+          exp32<true>(s1, c, z, x, l2);
+          tmem_st16(t_s + 32 * hf + 16, x);
+          l = fmaf(l2.x + l2.y, back, l);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(smem_u32(&s_pready[w][hf]));
+        }
+        started = true;
+      }
+      tiles += (unsigned)n;
+      // ---- output: the last product of this warpgroup, then (SINGLE) both states
+      if (DUAL || w < n) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_odone[w]), outs & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+        ++outs;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      float M = m, lsum = l, f0 = 1.f, f1 = 1.f;
+      // all scores are done when either warpgroup's last product is: Q's place is free
+      float2 *ml = reinterpret_cast<float2 *>(s_q);
+      if (!DUAL && started) ml[w * 128 + wt] = make_float2(m, l);
+      // SINGLE: each warpgroup waited for its own products and reads both outputs, so
+      // what it learned about tensor memory goes through the barrier
+      tc_fence_before();
+      bar_sync_n(1, 256);  // the states, and Q's place
+      tc_fence_after();
+      if (!DUAL) {
+        const float2 a = ml[wt];
+        const float2 b = n > 1 ? ml[128 + wt] : make_float2(-INFINITY, 0.f);
+        M = fmaxf(a.x, b.x);
+        // a state without keys adds its zeros (or NaN of a NaN query)
+        f0 = a.x == -INFINITY ? 1.f : ex2(a.x - M);
+        f1 = b.x == -INFINITY ? 1.f : ex2(b.x - M);
+        lsum = a.y * f0 + b.y * f1;
+      }
+      const int bad = s_bad[seg & 3];
+      const float z = (M == -INFINITY ? 0.f : M) - kBias;
+      const int c0 = DUAL ? 0 : w * (D / 2), c1 = DUAL ? D : c0 + D / 2;
+      const bool whole = wk.whole();
+      const int slot = wk.slot(blockIdx.x), i = node_of(L, r), head = wk.h * p.G + r - i * p.G;
+      const size_t row = wk.v.row0 + i;
+      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // NaN stays NaN
+      char *out = p.o + 2 * (row * p.o_row + head * p.o_head);
+      float4 *part = reinterpret_cast<float4 *>(L.part_o) + (size_t)slot * (D / 4) * L.rows + rr;
+#pragma unroll 1
+      for (int q = c0; q < c1 && ok; q += 32) {
+        float o[32];
+        tmem_ld32(lane_base + 256u + (DUAL ? (uint32_t)w * 128u : 0u) + q, o);
+        if (!DUAL && n > 1) {
+          float o1[32];
+          tmem_ld32(lane_base + 384u + q, o1);
+          tmem_wait_ld32(o);
+          tmem_wait_ld32(o1);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
+        } else {
+          tmem_wait_ld32(o);
+        }
+        if (r >= R) continue;
+        if (whole) {
+          uint32_t x[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = pack2<false>(o[2 * e] * inv, o[2 * e + 1] * inv);
+          uint4 *to = reinterpret_cast<uint4 *>(out + 2 * q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        } else {
+          float4 *to = part + (size_t)(q / 4) * L.rows;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) to[(size_t)e * L.rows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+      if (r < R && ok && c0 == 0) {
+        if (whole) {
+          if (p.lse) p.lse[row * p.H + head] = lsum == 0.f ? -INFINITY : (z + log2f(lsum)) * 0.69314718055994531f;
+        } else {
+          L.part_ml[(size_t)slot * L.rows + rr] = make_float2(M == -INFINITY ? -INFINITY : z, lsum);
+        }
+      }
+      if (whole && bad && r < R && ok) add_unseen<false>(p, wk.v, i, wk.h, out, c0, c1);
+      if (tid == 0) {
+        if (!whole) L.part_bad[slot] = bad;
+        wk.tell(s_start, blockIdx.x);
+      }
+      tc_fence_before();
+      bar_sync_n(1, 256);  // O, Q's place and s_bad are read
+      if (tid == 0) s_bad[seg & 3] = 0;
+      ++seg;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool DUAL>
+cudaError_t launch_one(const AttnLaunch &L, cudaStream_t s) {
+  auto kern = tree_attn_codes_tc_kernel<D, DUAL>;
+  const size_t smem = CodeTcShape<D, DUAL>::kSmem;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(kern, smem, done);
+  if (e != cudaSuccess) return e;
+  return launch_chained(kern, dim3(L.n_groups * L.n_rt), dim3(kThreads), smem, s, L);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_codes_tc(const AttnLaunch &L, cudaStream_t s) {
+  const bool dual = L.rows == 256;
+  if (L.p.c.D == 128) return dual ? launch_one<128, true>(L, s) : launch_one<128, false>(L, s);
+  return dual ? launch_one<64, true>(L, s) : launch_one<64, false>(L, s);
+}
+
+}  // namespace dfv

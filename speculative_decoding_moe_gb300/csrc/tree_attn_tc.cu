@@ -49,30 +49,6 @@ struct TcShape {
   static constexpr size_t kSmem = 1024 + kQ + (size_t)kSlots * kTile;
 };
 
-// Scores of a tile whose first key is node j0 (below 0: committed): what the row
-// does not see becomes -inf, in place.  A short loop, as is clean_row: they run
-// once per sequence, and unrolled their instructions took longer to fetch than
-// to execute.
-__device__ __forceinline__ void mask_tile(uint32_t t_s, int j0, uint64_t mask) {
-#pragma unroll 1
-  for (int q = 0; q < kTKeys; q += 16) {
-    const int j = j0 + q;  // node of the first of 16 keys
-    if (j + 16 <= 0) continue;
-    uint32_t sees;
-    if (j >= 0)
-      sees = j < 64 ? (uint32_t)(mask >> j) : 0u;
-    else
-      sees = (uint32_t)(mask << -j) | ((1u << -j) - 1u);
-    float s[16];
-    tmem_ld16(t_s + q, s);
-    uint32_t x[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = sees >> e & 1u ? __float_as_uint(s[e]) : 0xff800000u;
-    tmem_st16(t_s + q, x);
-  }
-  tmem_wait_st();
-}
-
 // Key row `row` of a V tile in shared memory: zeroed past the last node (j >= n);
 // a node's values that are not finite become zero and set *bad.
 template <bool F16, int D>

@@ -143,6 +143,24 @@ def test_few_rows(dfv, lens, nodes, heads, kv, dim, page):
     Case(lens, nodes, heads, kv, dim, page, seed=len(lens) + heads).check(dfv)
 
 
+# rows per kv head from 17 (one row tile) to 64 x 16 (several CTAs a range)
+@pytest.mark.parametrize("heads,kv,dim,page", [(8, 1, 128, 16), (4, 2, 64, 8), (7, 1, 128, 64), (16, 1, 64, 256), (2, 1, 128, 8)])
+@pytest.mark.parametrize("lens,nodes", [([0], [17]), ([100], [16]), ([127, 0, 64], [33, 40, 1]), ([700], [64]), ([3000, 5], [20, 64]), ([129], [18])])
+def test_many_rows(dfv, lens, nodes, heads, kv, dim, page):
+    Case(lens, nodes, heads, kv, dim, page, seed=len(lens) + heads).check(dfv)
+
+
+def test_many_rows_of_many_sequences(dfv):
+    Case([(37 * s) % 300 for s in range(60)], [s % 33 for s in range(60)], 4, 2, 64, 16, seed=7).check(dfv)
+    Case([(37 * s) % 300 for s in range(30)], [s % 65 for s in range(30)], 5, 1, 128, 32, seed=8).check(dfv)
+
+
+@pytest.mark.parametrize("masks", ["chain", "any"])
+@pytest.mark.parametrize("dim,heads,nodes", [(64, 4, 30), (128, 8, 40)])
+def test_masks_of_many_rows(dfv, masks, dim, heads, nodes):
+    Case([0, 70, 200, 13], [nodes, 5, 20, nodes], heads, 1, dim, 16, seed=4, masks=masks).check(dfv)
+
+
 @pytest.mark.parametrize("masks", ["tree", "chain", "any"])
 @pytest.mark.parametrize("dim", [64, 128])
 def test_masks(dfv, masks, dim):
@@ -162,21 +180,23 @@ def test_many_sequences(dfv):
 
 @pytest.mark.parametrize("spread,size,scale", [(3.0, 1.0, None), (8.0, 1.0, 1e-4), (0.5, 30.0, None), (0.5, 1e-20, None), (0.1, 1.0, 1.0)])
 @pytest.mark.parametrize("dim", [64, 128])
-def test_sizes_far_apart(dfv, dim, spread, size, scale):
+@pytest.mark.parametrize("nodes", [2, 16, 40])
+def test_sizes_far_apart(dfv, dim, spread, size, scale, nodes):
     """Tokens whose powers differ by a lot, large and tiny queries: the weights of the product follow p times the power."""
-    c = Case([700], [2], 8, 1, dim, 16, seed=8, spread=spread)
+    c = Case([700], [nodes], 8, 1, dim, 16, seed=8, spread=spread)
     c.q = (c.q.float() * size).to(BF)
     c.check(dfv, scale=scale)
 
 
-def test_a_query_of_zeros_and_one_large_element(dfv):
-    c = Case([300], [2], 4, 1, 128, 16, seed=9)
+@pytest.mark.parametrize("nodes", [2, 9, 50])
+def test_a_query_of_zeros_and_one_large_element(dfv, nodes):
+    c = Case([300], [nodes], 4, 1, 128, 16, seed=9)
     c.q[0] = 0
     c.q[1, :, 5] = 300.0
     c.check(dfv)
 
 
-@pytest.mark.parametrize("heads,nodes", [(8, 2)])
+@pytest.mark.parametrize("heads,nodes", [(8, 2), (8, 9), (8, 40)])
 @pytest.mark.parametrize("dim", [64, 128])
 def test_what_is_masked_does_not_count(dfv, dim, heads, nodes):
     """Codes of NaN and exponent bytes of any value outside the tokens, and NaN in nodes that a row does not see."""
@@ -206,29 +226,32 @@ def test_what_is_masked_does_not_count(dfv, dim, heads, nodes):
     assert bool(bad[:, 3].all()) and int(bad.sum()) == heads
 
 
-def test_nan_in_a_committed_token(dfv):
-    c = Case([200], [2], 4, 2, 64, 16, seed=11)
+@pytest.mark.parametrize("nodes", [2, 12, 64])
+def test_nan_in_a_committed_token(dfv, nodes):
+    c = Case([200], [nodes], 4, 2, 64, 16, seed=11)
     c.raw[1][0, int(c.table[0, 3]), 1, 7, 9] = 0xff
     out, _, err = c.run(dfv)
     bad = torch.isnan(out)
-    assert err == 0 and bool(bad[:, 2:, 9].all()) and int(bad.sum()) == 2 * 2
+    assert err == 0 and bool(bad[:, 2:, 9].all()) and int(bad.sum()) == 2 * nodes
 
 
-def test_missing_pages_and_bad_lengths(dfv):
-    c = Case([100, 50], [2, 2], 4, 2, 64, 16, seed=12)
+@pytest.mark.parametrize("nodes", [2, 20])
+def test_missing_pages_and_bad_lengths(dfv, nodes):
+    c = Case([100, 50], [nodes, 2], 4, 2, 64, 16, seed=12)
     was, _, _ = c.run(dfv)
     cache = c.cache(dfv)
     cache.page_table[0, 2] = -1
     out, _, err = c.run(dfv, cache=cache)
-    assert err == dfv.KVERR_PAGE and torch.equal(out[2:], was[2:])
+    assert err == dfv.KVERR_PAGE and torch.equal(out[nodes:], was[nodes:])
     cache = c.cache(dfv)
     cache.lens[0] = 1 << 20
     out, _, err = c.run(dfv, cache=cache)
-    assert err == dfv.KVERR_LEN and torch.equal(out[2:], was[2:]) and not bool(out[:2].any())
+    assert err == dfv.KVERR_LEN and torch.equal(out[nodes:], was[nodes:]) and not bool(out[:nodes].any())
 
 
-def test_the_same_bits_every_time_and_in_a_graph(dfv):
-    c = Case([3000, 20], [2, 1], 8, 1, 128, 16, seed=13)
+@pytest.mark.parametrize("nodes", [2, 16, 33])
+def test_the_same_bits_every_time_and_in_a_graph(dfv, nodes):
+    c = Case([3000, 20], [nodes, 1], 8, 1, 128, 16, seed=13)
     cache, tree = c.cache(dfv), c.tree(dfv)
     ws = dfv.alloc_workspace(dfv.tree_attention_workspace_size(cache, tree, 8))
     q = c.q.cuda()
@@ -241,14 +264,15 @@ def test_the_same_bits_every_time_and_in_a_graph(dfv):
         out.zero_()
         g.replay()
         assert torch.equal(out, was)
-    cache.lens.copy_(i32([1000, 500]) * 0 + i32([1000, 12]))
+    cache.lens.copy_(i32([1000, 12]))
     g.replay()
     assert torch.equal(out, dfv.tree_attention(cache, 0, tree, q, ws))
 
 
-def test_as_a_bf16_cache_of_the_same_values(dfv):
+@pytest.mark.parametrize("nodes", [2, 30])
+def test_as_a_bf16_cache_of_the_same_values(dfv, nodes):
     """The values of codes fit bf16: both caches give the same attention but for the roundings of p."""
-    c = Case([500, 77], [2, 1], 8, 2, 128, 16, seed=14)
+    c = Case([500, 77], [nodes, 1], 8, 2, 128, 16, seed=14)
     cache = c.cache(dfv)
     k, v = (valued(x.view(E4M3), e).to(BF).cuda() for x, e in zip(c.raw, c.exp))
     other = dfv.KVCache(k, v, c.table.cuda(), i32(c.lens))
