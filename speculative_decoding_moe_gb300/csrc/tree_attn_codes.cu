@@ -111,14 +111,6 @@ __device__ __noinline__ bool clean_codes(uint32_t vb, uint32_t pv, int w0, int j
   return bad;
 }
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-// One of the arrivals that `bar` waits for, once this thread's copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_kernel(const __grid_constant__ AttnLaunch L) {
   using S = CodeShape<D, NT>;

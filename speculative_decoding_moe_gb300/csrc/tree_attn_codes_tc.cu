@@ -45,7 +45,7 @@ struct CodeTcShape {
   static constexpr uint32_t kCodes = kKeys * D;      // a K or V tile in codes
   static constexpr uint32_t kTile = kKeys * D * 2;   // and in fp16
   static constexpr int kSlots = D == 64 ? 6 : 3;     // of fp16 tiles
-  static constexpr int kCSlots = D == 64 ? 8 : DUAL ? 4 : 5;  // of codes
+  static constexpr int kCSlots = D == 64 ? 8 : DUAL ? 3 : 5;  // of codes
   static constexpr int kOver = DUAL ? 5 : 2;         // tiles' worth of time that a pair costs at least
   static constexpr uint32_t kQ = (DUAL ? 2 : 1) * 128 * D * 2;
   static constexpr size_t kSmem = 1024 + kQ + (size_t)kSlots * kTile + (size_t)kCSlots * kCodes;
@@ -69,11 +69,41 @@ __device__ __forceinline__ void widen16(const uint4 &x, __half2 m, uint4 &lo, ui
   hi = make_uint4(y[4], y[5], y[6], y[7]);
 }
 
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4 &v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // 2^-d in fp16, d >= 0 (0 below its subnormals)
 __device__ __forceinline__ __half2 half_power(int d) {
   const uint32_t b = d <= 14 ? (uint32_t)(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
   const uint32_t two = b | b << 16;
   return *reinterpret_cast<const __half2 *>(&two);
+}
+
+// Where a row's chunk of 16 codes is in its swizzled tile.
+template <int D>
+__device__ __forceinline__ uint32_t place(int row, int c) {
+  return (uint32_t)(D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3));
+}
+
+// A key's codes in shared memory: zeroed where it is no node, else its NaN become zero;
+// whether there were any.
+template <int D>
+__device__ __noinline__ bool clean_key(uint32_t row, bool node) {
+  bool nan = false;
+#pragma unroll 1
+  for (int c = 0; c < D / 16; ++c) {
+    uint4 x = lds128(row + 16u * c);
+    uint32_t *w = &x.x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t z = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+      nan = nan || z;
+      w[e] = node ? w[e] & ~((z >> 7) * 255u) : 0u;
+    }
+    sts128(row + 16u * c, x);
+  }
+  return nan && node;
 }
 
 template <int D, bool DUAL>
@@ -90,7 +120,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
   __shared__ long long s_scan[kThreads / 32];
   __shared__ volatile int s_bad[4];    // of a segment, in turn: NaN was left out
   __shared__ volatile int2 s_tell[kTells];  // A and B of a tile
-  __shared__ int2 s_most[2][4];        // of the widening warps' keys, in turn
+  __shared__ uint8_t s_below[4][kKeys];  // how far a key's b is below B, of tiles whose V is to come
+  __shared__ __align__(16) unsigned char s_power[S::kCSlots * 2 * kKeys];  // of K's slots: a and b of the tile's keys
   __shared__ float s_crow[256];        // c times the power that a row of q was divided by
   const TreeAttnParams &p = L.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -104,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
       mbar_init(smem_u32(&s_empty[s]), 1);
     }
     for (int s = 0; s < S::kCSlots; ++s) {
-      mbar_init(smem_u32(&s_cfull[s]), kProducers);
+      mbar_init(smem_u32(&s_cfull[s]), kProducers + 64);  // the codes' boxes, and the powers' lanes
       mbar_init(smem_u32(&s_cempty[s]), 4);
     }
     for (int w = 0; w < 2; ++w) {
@@ -159,6 +190,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
         }
         __syncwarp();
         const int tok = ((wk.t0 + j) * kKeys) & ((1 << shift) - 1);  // 0 unless a page holds several tiles
+        if (me < 2) {  // with K: this lane's four keys' a (the first producer) or b
+          const int my = boxes == 1 ? 0 : (4 * lane) >> shift, page = __shfl_sync(0xffffffffu, pg, my & 31);
+          if (map == &L.tm_k && my < nb)
+            cp_async4(smem_u32(s_power + (st * 2 + me) * kKeys + 4 * lane),
+                      (me == 0 ? p.c.ke : p.c.ve) + exp_off(p.c, p.layer, page, wk.h, ((wk.t0 + j) * kKeys + 4 * lane) & ((1 << shift) - 1)));
+          cp_async_arrive(fb);
+        }
         for (int b = me; b < nb; b += kProducers)
           tma_kv(dst + (uint32_t)(b * rows * D), map, 0, tok, wk.h, __shfl_sync(0xffffffffu, pg, b), L.swap, fb);
         ++issued;
@@ -192,112 +230,86 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
       if (!mbar_wait(smem_u32(&s_cfull[j % S::kCSlots]), (j / S::kCSlots) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never)) break;
   } else if (warp >= 12) {
     // ---------------------------------------------------------------- widening: a key row a thread
-    const int kt = tid - 384, ww = warp - 12;
+    // Items in the order of the rings: LA tiles' K, then V and the next K in turn.  (Short
+    // loops: with the chunks of two items unrolled the warps waited for instructions a third
+    // of their time.)
+    const int kt = tid - 384;
     int st = 0, ph = 0, cst = 0, cph = 0, seg = 0;
     unsigned tiles = 0;  // of the segments before
     bool ok = true;
-    const int shift = p.c.page_shift;
-    // (after a wait gives up the loops still run to the end, so the four warps meet at
-    // every barrier)
-    while (wk.next()) {
+    while (ok && wk.next()) {
       if (row0 >= wk.v.n * p.G) continue;
-      const int n = wk.t1 - wk.t0;
-      const int32_t *table = p.c.table + (size_t)(wk.v.s < 0 ? 0 : wk.v.s) * p.c.max_pages;
-      // the powers of this thread's key: page id two tiles ahead, bytes one ahead
-      auto id = [&](int j) {
-        const int key = (wk.t0 + j) * kKeys + kt;
-        return j < n && key < wk.total ? table[key >> shift] : -1;
-      };
-      auto bytes = [&](int j, int pg) {  // 0 past the end
-        const int key = (wk.t0 + j) * kKeys + kt;
-        if (j >= n || key >= wk.total) return make_int2(0, 0);
-        const size_t at = exp_off(p.c, p.layer, (unsigned)pg < (unsigned)p.c.n_pages ? pg : 0, wk.h, key & ((1 << shift) - 1));
-        return make_int2(p.c.ke[at], p.c.ve[at]);
-      };
-      int pg1 = id(1), b0 = 0;
-      int2 next = bytes(0, id(0));
-      int2 mine = make_int2(0, 0), most = make_int2(0, 0);
-      int db[LA + 1];  // how far this key's b is below its tile's, of the tiles whose V is to come
-#pragma unroll
-      for (int k = 0; k < LA + 1; ++k) db[k] = 0;
-      // one tile of codes to fp16 times m; V: zero past the last node, NaN of a node taken out
-      auto widen = [&](__half2 m, int jn, bool isv) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_cfull[cst]), cph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_empty[st]), ph ^ 1, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
-        if (!ok) return;
-        const unsigned char *from = s_codes + (size_t)cst * S::kCodes + kt * D;
-        unsigned char *to = s_ring + (size_t)st * S::kTile + kt * 128;
-        uint4 x[D / 16];
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {  // chunk order turned by the row: no bank conflicts
-          const int at = D == 128 ? i ^ (kt & 7) : i ^ ((kt >> 1) & 3);  // the chunk's place in the tile; the chunk itself is i
-          x[i] = *reinterpret_cast<const uint4 *>(from + 16 * at);
+      const int n = wk.t1 - wk.t0, ahead = n < LA ? n : LA;
+      // item i: K of tile t (0), or V (1)
+      auto item = [&](int i, int &t) {
+        if (i < ahead) {
+          t = i;
+          return 0;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s_cempty[cst]));
-        if (isv && jn >= 0) {
-          bool nan = false;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            uint32_t *w = &x[i].x;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t z = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-              nan = nan || z;
-              w[e] = jn < wk.nodes ? w[e] & ~((z >> 7) * 255u) : 0u;
-            }
+        i -= ahead;
+        if (i < 2 * (n - ahead)) {
+          t = i & 1 ? (i >> 1) + ahead : i >> 1;
+          return 1 - (i & 1);
+        }
+        t = i - (n - ahead);
+        return 1;
+      };
+#pragma unroll 1
+      for (int i = 0; i < 2 * n && ok; ++i) {
+        int t;
+        const int isv = item(i, t);
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_cfull[cst]), cph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+        if (!ok) break;
+        const uint32_t from = codes + (uint32_t)cst * S::kCodes + (uint32_t)(kt * D);
+        const unsigned tile = tiles + (unsigned)t;
+        int below;
+        if (!isv) {
+          // with K the powers of both tiles: their largest, and how far this key's are below
+          const unsigned char *pw = s_power + cst * 2 * kKeys;
+          const int valid = wk.total - (wk.t0 + t) * kKeys - 4 * lane;  // of this lane's four keys
+          const uint32_t keep = valid >= 4 ? ~0u : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u;
+          uint32_t m = *reinterpret_cast<const uint32_t *>(pw + 4 * lane) & keep, m2 = *reinterpret_cast<const uint32_t *>(pw + kKeys + 4 * lane) & keep;
+          m = __vmaxu4(m, m >> 16);
+          m2 = __vmaxu4(m2, m2 >> 16);
+          const int a = __reduce_max_sync(0xffffffffu, max(m & 255u, m >> 8 & 255u));
+          const int b = __reduce_max_sync(0xffffffffu, max(m2 & 255u, m2 >> 8 & 255u));
+          below = max(0, a - pw[kt]);
+          s_below[tile & 3][kt] = (uint8_t)max(0, b - pw[kKeys + kt]);
+          if (kt == 0) {
+            s_tell[tile % kTells].x = a;
+            s_tell[tile % kTells].y = b;
           }
-          if (nan && jn < wk.nodes) s_bad[seg & 3] = 1;
+        } else {
+          below = s_below[tile & 3][kt];
+          const int jn = (wk.t0 + t) * kKeys + kt - wk.v.len;  // this key's node
+          if (jn >= 0 && clean_key<D>(from, jn < wk.nodes)) s_bad[seg & 3] = 1;
         }
+        const __half2 m = half_power(below);
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_empty[st]), ph ^ 1, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
+        if (!ok) break;
+        const uint32_t to = ring + (uint32_t)st * S::kTile + (uint32_t)(kt * 128);
+#pragma unroll 1
+        for (int c0 = 0; c0 < D / 16; c0 += 4) {
+          uint4 x[4];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          uint4 lo, hi;
-          widen16(x[i], m, lo, hi);
-          unsigned char *half = to + ((2 * i) >> 3) * 16384;
-          *reinterpret_cast<uint4 *>(half + ((((2 * i) & 7) ^ (kt & 7)) << 4)) = lo;
-          *reinterpret_cast<uint4 *>(half + ((((2 * i + 1) & 7) ^ (kt & 7)) << 4)) = hi;
+          for (int c = 0; c < 4; ++c) x[c] = lds128(from + 16u * place<D>(kt, c0 + c));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint4 lo, hi;
+            widen16(x[c], m, lo, hi);
+            const uint32_t half = to + (uint32_t)(c0 >> 2) * 16384u;
+            sts128(half + (((2 * c) ^ (kt & 7)) << 4), lo);
+            sts128(half + (((2 * c + 1) ^ (kt & 7)) << 4), hi);
+          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s_full[st]));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&s_full[st]));
+          mbar_arrive(smem_u32(&s_cempty[cst]));
+        }
         if (++st == S::kSlots) { st = 0; ph ^= 1; }
         if (++cst == S::kCSlots) { cst = 0; cph ^= 1; }
-      };
-      auto keys = [&](int j) {  // K of tile j, and both powers of the tile
-        mine = next;
-        next = bytes(j + 1, pg1);
-        pg1 = id(j + 2);
-        const int a = __reduce_max_sync(0xffffffffu, mine.x), b = __reduce_max_sync(0xffffffffu, mine.y);
-        const unsigned tile = tiles + (unsigned)j;
-        if (lane == 0) s_most[tile & 1][ww] = make_int2(a, b);
-        bar_sync_n(2, 128);
-        most = make_int2(0, 0);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          most.x = max(most.x, s_most[tile & 1][w].x);
-          most.y = max(most.y, s_most[tile & 1][w].y);
-        }
-        if (kt == 0) {
-          s_tell[tile % kTells].x = most.x;
-          s_tell[tile % kTells].y = most.y;
-        }
-        widen(half_power(most.x - mine.x), -1, false);
-        b0 = most.y - mine.y;
-      };
-#pragma unroll
-      for (int k = 0; k < LA; ++k)
-        if (k < n) {
-          keys(k);
-          db[k] = b0;
-        }
-      for (int j = 0; j < n; ++j) {
-        widen(half_power(db[0]), (wk.t0 + j) * kKeys + kt - wk.v.len, true);
-        if (j + LA < n) {
-          keys(j + LA);
-          db[LA] = b0;
-        }
-#pragma unroll
-        for (int k = 0; k < LA; ++k) db[k] = db[k + 1];
       }
       tiles += (unsigned)n;
       ++seg;
@@ -472,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
         const float c = fminf(fmaxf(crow * exp_value((uint32_t)s_tell[tell].x), 0x1p-120f), 0x1p120f);
         const int eb = min(max(s_tell[tell].y, 1), 253);
         const float B = (float)(eb - 127), back = exp_value((uint32_t)(254 - eb));
-#pragma unroll
+#pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
           float s0[32], s1[32];
           tmem_ld32(t_s + 64 * hf, s0);
