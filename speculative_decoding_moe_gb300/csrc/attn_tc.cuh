@@ -90,6 +90,10 @@ __device__ __forceinline__ void tmem_wait_ld32(float *r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4 &v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // (a, b) * (c, c) + (d, d) and sums, two at a time
 __device__ __forceinline__ float2 fma2(float2 a, float c, float d) {
   float2 r;

@@ -139,6 +139,8 @@ int dfv_prompt_attention(int dtype, const dfv_row_batch *rows, const dfv_row_bat
       return api_fail(DFV_ERR_INVALID_ARG, "row and head strides must be non-negative multiples of 8 elements below 2^36");
   if ((keys->n_rows > 1 && (k_row == 0 || v_row == 0)) || (n_kv_heads > 1 && (k_head == 0 || v_head == 0)))
     return api_fail(DFV_ERR_UNSUPPORTED, "k and v with a stride of 0");
+  if ((rows->n_rows > 1 && q_row == 0) || (n_heads > 1 && q_head == 0))
+    return api_fail(DFV_ERR_UNSUPPORTED, "q with a stride of 0");
   if ((st = check_ws(ws, ws_bytes, prompt_attn_ws(head_dim)))) return st;
   PromptParams p = {};
   p.n_seqs = rows->n_seqs;

@@ -5,17 +5,22 @@
 // 2^(c q.k_j - M) for any M, c = scale log2(e); the state (M, l, O) of some keys, and
 // states over disjoint keys join exactly.
 //
-// Rows.  The query heads of a kv head share its keys, so row r of a (sequence, kv
-// head) is position r / G, head r % G of the group, and a tile is 256 rows: 32
-// positions of 8 heads.  The keys that a tile needs end with its last position, so
-// little is computed above the diagonal, and the causal mask is one limit per
-// row.  A CTA streams the tile's keys in blocks of 128: two warpgroups take 128
-// rows each, S = Q K^T goes to tensor memory, a thread turns its row of S into P
-// over S, and O += P V accumulates in tensor memory.  P is given to the products in
-// halves of 64 keys, so that a product starts while the second half is in its
-// exponentials.  M is only raised, and O only rescaled, when a row's maximum grew by
-// more than 2^8; before the second half of a block that waits for the first half's
-// product.
+// Rows.  The query heads of a kv head share its keys.  A tile is P consecutive
+// positions (256 / G, a multiple of 8) of the G heads of a kv head: row g P + i.  The
+// keys that a tile needs end with its last position, so little is computed above the
+// diagonal, and the causal mask is one limit per row.  A CTA streams the tile's keys
+// in blocks of 128: two warpgroups take 128 rows each, S = Q K^T goes to tensor
+// memory, a thread turns its row of S into P over S, and O += P V accumulates in
+// tensor memory.  P is given to the products in halves of 64 keys, so that a product
+// starts while the second half is in its exponentials.  M is only raised, and O only
+// rescaled, when a row's maximum grew by more than 2^8; before the second half of a
+// block that waits for the first half's product.
+//
+// Scores take turns in NB places of 128 columns: two with heads of 128, one a
+// warpgroup; three with heads of 64, where the outputs leave room, so that a warpgroup's
+// next scores are ready while it is still in its exponentials.  The products follow the
+// warpgroups' places in turn, PV_i then QK_(i + NB).  A tile's queries are copied, and
+// its first scores made, while the warpgroups put out the tile before.
 //
 // Work split.  All tiles' blocks form one line, (sequence, kv head, tile) after
 // (sequence, kv head, tile), with some blocks' worth for what a tile costs however
@@ -32,8 +37,8 @@
 //
 // Warps 0-3 and 4-7 are the two warpgroups, warps 8 and 10 stream K and V blocks
 // with TMA into one ring in the order the MMAs use them (half of the head, or half
-// of the keys, each), warp 9 issues the MMAs.
-// Tensor memory: S0 S1 O0 O1 of 128 columns each; P (16-bit pairs) over S.
+// of the keys, each), warp 9 issues the MMAs, warp 11 copies Q and cleans V.
+// Tensor memory: NB places of scores, P (16-bit pairs) over them, then O0 O1.
 #include <cstdio>
 
 #include <cudaTypedefs.h>
@@ -47,24 +52,28 @@ namespace {
 
 constexpr int kKeys = 128;   // of a block
 constexpr int kTile = 256;   // rows of a tile
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 constexpr int kOver = 5;     // blocks' worth of time that a tile costs at least
 constexpr int kWholeKeys = 1024;  // tiles are cut where a sequence may have more keys
 
 template <int D>
 struct PromptShape {
   static constexpr uint32_t kBlock = kKeys * D * 2;  // one K or V block
-  static constexpr int kSlots = D == 64 ? 8 : 5;
+  static constexpr int kK = D == 64 ? 4 : 3, kV = D == 64 ? 4 : 2;  // blocks of K, and of V behind them
+  static constexpr int kSlots = kK + kV;
   static constexpr uint32_t kQ = kTile * D * 2;
+  static constexpr int kNB = D == 64 ? 3 : 2;        // places of scores
+  static constexpr uint32_t kO = 128 * kNB;          // tensor-memory column of O0
   static constexpr size_t kSmem = 1024 + kQ + (size_t)kSlots * kBlock;
 };
 
 struct PromptLaunch {
-  CUtensorMap tm_k, tm_v;  // {head_dim, head, row}, head and row in stride order
+  CUtensorMap tm_q, tm_k, tm_v;  // {head_dim, row, head}
   PromptParams p;
-  int swap_k, swap_v;      // row before head
+  int pos;                 // positions of a tile
+  int run, rise;           // so many tiles further, tiles have so many blocks more
   int whole;               // ranges end at tiles
-  uint32_t inv_g;          // ceil(2^16 / G)
+  uint32_t inv_pos;        // ceil(2^16 / pos)
   int4 *cut;               // [kAttnCtas] sequence, head, tile that begins in the range and goes on, ranges it is in (0: none)
   float2 *part_ml;         // [2 kAttnCtas][kTile] (M, l) of partial states
   float *part_o;           // [2 kAttnCtas][D / 4][kTile][4] their sums of p v
@@ -106,38 +115,37 @@ __device__ __forceinline__ PromptSeq prompt_seq(const PromptParams &p, int b) {
   }
   return s;
 }
-__device__ __forceinline__ int tiles_of(const PromptParams &p, const PromptSeq &s) { return (s.n * p.G + kTile - 1) / kTile; }
+__device__ __forceinline__ int tiles_of(const PromptLaunch &L, const PromptSeq &s) { return (s.n + L.pos - 1) / L.pos; }
 
 // Keys that position i of a sequence sees.
 __device__ __forceinline__ int limit_of(const PromptSeq &s, int i) { return min(s.nk, max(0, s.nk - s.n + i + 1)); }
 
 // Blocks of tile t: at least one (its outputs have to be written).
-__device__ __forceinline__ int blocks_of(const PromptParams &p, const PromptSeq &s, int t) {
-  const int last = min(s.n - 1, (kTile * t + kTile - 1) / p.G);
-  return max(1, (limit_of(s, last) + kKeys - 1) / kKeys);
+__device__ __forceinline__ int blocks_of(const PromptLaunch &L, const PromptSeq &s, int t) {
+  return max(1, (limit_of(s, min(s.n, (t + 1) * L.pos) - 1) + kKeys - 1) / kKeys);
 }
 
-// Blocks of the tiles before tile i <= last tile of the sequence.  Tile t that is
-// not the last ends with position (256 t + 255) / G, so its blocks are
-//   max(1, floor((2 t + B) / G)),  B = floor((255 + G (128 + nk - n)) / 128);
-// the floors are counted in runs of G tiles, over which they grow by 2.
-__device__ __forceinline__ long long blocks_before(const PromptParams &p, const PromptSeq &s, int i) {
-  const int G = p.G, B = (int)((255 + (long long)G * (kKeys + s.nk - s.n)) >> 7);
-  const int i1 = B >= G ? 0 : (G - B + 1) / 2;  // the first tile with a block by the formula
+// Blocks of the tiles before tile i <= last tile of the sequence.  Tile t that is not
+// the last has max(1, floor((P t + C) / 128)) of them, C = P + 127 + nk - n; the
+// floors are counted in runs of 128 / gcd(P, 128) tiles, over which they grow by
+// P / gcd(P, 128).
+__device__ __forceinline__ long long blocks_before(const PromptLaunch &L, const PromptSeq &s, int i) {
+  const int P = L.pos, C = P + kKeys - 1 + s.nk - s.n;
+  const int i1 = C >= kKeys ? 0 : (kKeys - C + P - 1) / P;  // the first tile with a block by the formula
   if (i <= i1) return i;
-  const int c = 2 * i1 + B, w = i - i1, a = w / G, r = w - a * G;
+  const int c = P * i1 + C, w = i - i1, a = w / L.run, r = w - a * L.run;
   int all = 0, part = 0;
-  for (int u = 0; u < G; ++u) {
-    const int f = (2 * u + c) / G;
+  for (int u = 0; u < L.run; ++u) {
+    const int f = (P * u + c) / kKeys;
     all += f;
     if (u < r) part += f;
   }
-  return i1 + (long long)a * all + (long long)G * a * (a - 1) + part + 2ll * a * r;
+  return i1 + (long long)a * all + (long long)L.rise * L.run * ((long long)a * (a - 1) / 2) + part + (long long)L.rise * a * r;
 }
 
-__device__ __forceinline__ long long head_units(const PromptParams &p, const PromptSeq &s) {
-  const int m = tiles_of(p, s);
-  return m == 0 ? 0 : (long long)kOver * m + blocks_before(p, s, m - 1) + blocks_of(p, s, m - 1);
+__device__ __forceinline__ long long head_units(const PromptLaunch &L, const PromptSeq &s) {
+  const int m = tiles_of(L, s);
+  return m == 0 ? 0 : (long long)kOver * m + blocks_before(L, s, m - 1) + blocks_of(L, s, m - 1);
 }
 
 struct PromptStart {
@@ -154,7 +162,7 @@ __device__ __forceinline__ void prompt_start(const PromptLaunch &L, int g, long 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.n_seqs;
   const int per = (n + kThreads - 1) / kThreads, b0 = min(n, tid * per), b1 = min(n, b0 + per);
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += p.Hkv * head_units(p, prompt_seq(p, b));
+  for (int b = b0; b < b1; ++b) sum += p.Hkv * head_units(L, prompt_seq(p, b));
   long long run = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -177,7 +185,7 @@ __device__ __forceinline__ void prompt_start(const PromptLaunch &L, int g, long 
   if (u0 < u1 && at <= u0 && u0 < at + sum) {
     long long base = at;
     for (int b = b0; b < b1; ++b) {
-      const long long c = per == 1 ? sum : p.Hkv * head_units(p, prompt_seq(p, b));
+      const long long c = per == 1 ? sum : p.Hkv * head_units(L, prompt_seq(p, b));
       if (base <= u0 && u0 < base + c) {
         out->u0 = u0;
         out->u1 = u1;
@@ -208,8 +216,8 @@ struct PromptWalk {
   __device__ __forceinline__ PromptWalk(const PromptLaunch &l, const PromptStart &st) : L(l), end(st.u1), u(st.u0), b(st.b), h(0), t(-1), m(0), p0(0), first(true) {
     if (u >= end) return;
     s = prompt_seq(L.p, b);
-    m = tiles_of(L.p, s);
-    const long long per = head_units(L.p, s);
+    m = tiles_of(L, s);
+    const long long per = head_units(L, s);
     long long w = u - st.base;
     h = (int)(w / per);
     w -= h * per;
@@ -217,15 +225,15 @@ struct PromptWalk {
     int lo = 0, hi = m;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if ((long long)kOver * mid + blocks_before(L.p, s, mid) <= w)
+      if ((long long)kOver * mid + blocks_before(L, s, mid) <= w)
         lo = mid;
       else
         hi = mid;
     }
     t = lo;
-    p0 = (int)(w - ((long long)kOver * t + blocks_before(L.p, s, t)));
+    p0 = (int)(w - ((long long)kOver * t + blocks_before(L, s, t)));
     if (L.whole && p0) {  // it belongs to the range before
-      u += kOver + blocks_of(L.p, s, t) - p0;
+      u += kOver + blocks_of(L, s, t) - p0;
       p0 = 0;
       ++t;
     }
@@ -241,10 +249,10 @@ struct PromptWalk {
           h = 0;
           ++b;
           s = prompt_seq(L.p, b);
-          m = tiles_of(L.p, s);
+          m = tiles_of(L, s);
         }
       }
-      T = blocks_of(L.p, s, t);
+      T = blocks_of(L, s, t);
       const int units = kOver + T, p1 = L.whole ? units : (int)min((long long)units, p0 + (end - u));
       last = u - p0 + units - 1;
       t0 = max(0, p0 - kOver);
@@ -262,55 +270,50 @@ struct PromptWalk {
 
 // ---------------------------------------------------------------- pieces
 // A block's box, issued by an elected lane of a warp in step.
-__device__ __forceinline__ void tma_block(uint32_t dst, const CUtensorMap *map, int x, int h, int row, int swap, uint32_t bar) {
+__device__ __forceinline__ void tma_block(uint32_t dst, const CUtensorMap *map, int x, int row, int h, uint32_t bar) {
   asm volatile(
       "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
       " @q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(swap ? row : h), "r"(swap ? h : row), "r"(bar)
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(h), "r"(bar)
       : "memory");
 }
 
-// Scores of a block of which the row sees the first `sees` keys: the others become
-// -inf, in place.
-__device__ __forceinline__ void mask_block(uint32_t t_s, int sees) {
-#pragma unroll 1
-  for (int q = 0; q < kKeys; q += 16) {
-    if (__all_sync(0xffffffffu, q + 16 <= sees)) continue;
-    float s[16];
-    tmem_ld16(t_s + q, s);
-    uint32_t x[16];
+// Of 32 scores the row sees the first `sees`: the others become -inf.
+__device__ __forceinline__ void mask32(float *s, int sees) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = q + e < sees ? __float_as_uint(s[e]) : 0xff800000u;
-    tmem_st16(t_s + q, x);
-  }
-  tmem_wait_st();
+  for (int e = 0; e < 32; ++e) s[e] = e < sees ? s[e] : -INFINITY;
 }
 
-// Key row `row` of a V block in shared memory: zeroed where `past`; else its values
-// that are not finite become zero and set *bad.
+// Rows [from, 128) of a V block in shared memory, by one warp: zeroed from `past` on;
+// values that are not finite before that become zero and are told of.
 template <bool F16, int D>
-__device__ __forceinline__ void clean_key(unsigned char *block, int row, bool past, int *bad) {
+__device__ __forceinline__ bool clean_block(uint32_t block, int from, int past) {
   constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
-#pragma unroll 1
-  for (int c = 0; c < D / 8; ++c) {  // chunk order turned by the row: no bank conflicts
-    uint4 *at = reinterpret_cast<uint4 *>(block + (c >> 3) * 16384 + row * 128 + (((c ^ row) & 7) << 4));
+  constexpr int kCh = D / 8;  // 16-byte chunks of a row
+  bool hit = false;
+#pragma unroll 2
+  for (int u = from * kCh + (threadIdx.x & 31); u < kKeys * kCh; u += 32) {
+    const int row = u / kCh, c = u % kCh;
+    const uint32_t at = block + (uint32_t)((c >> 3) * 16384 + row * 128 + (((c ^ row) & 7) << 4));
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    bool hit = past;
-    if (!hit) {
-      v = *at;
+    bool change = row >= past;
+    if (!change) {
+      v = lds128(at);
       uint32_t *w = &v.x;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if ((w[e] & kExp) == kExp) { w[e] &= 0xffff0000u; hit = true; }
-        if ((w[e] & (kExp << 16)) == (kExp << 16)) { w[e] &= 0x0000ffffu; hit = true; }
+        if ((w[e] & kExp) == kExp) { w[e] &= 0xffff0000u; change = true; }
+        if ((w[e] & (kExp << 16)) == (kExp << 16)) { w[e] &= 0x0000ffffu; change = true; }
       }
-      if (hit) *bad = 1;
+      hit = hit || change;
     }
-    if (hit) *at = v;
+    if (change) sts128(at, v);
   }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  return __any_sync(0xffffffffu, hit);
 }
 
-// What clean_key took out of the values of keys [from, to), added to elements c0 .. c1
+// What clean_block took out of the values of keys [from, to), added to elements c0 .. c1
 // of a stored output (rare: a value next to the diagonal is not finite).
 template <bool F16>
 __device__ __noinline__ void add_taken(const PromptParams &p, const PromptSeq &s, int h, int from, int to, char *out, int c0, int c1) {
@@ -328,42 +331,77 @@ __device__ __noinline__ void add_taken(const PromptParams &p, const PromptSeq &s
   }
 }
 
-// Position within the tile's first row's group and head of row rr of a tile: the
-// quotient of a number below 1024 + 256 by G <= 16.
-__device__ __forceinline__ int over_g(const PromptLaunch &L, int r) { return (int)(((uint32_t)r * L.inv_g) >> 16); }
+// Head of row r < 256 of a tile (its product's error stays below one part in 2^16 / P).
+__device__ __forceinline__ int head_of(const PromptLaunch &L, int r) { return (int)(((uint32_t)r * L.inv_pos) >> 16); }
+
+// A row's 32 elements of a lane become rows' 16-byte quarters among four lanes: lane q of
+// four then stores quarter q of each of the four rows, 64 bytes of a row side by side.
+__device__ __forceinline__ void turn_quads(uint4 (&x)[4]) {
+  const int q = threadIdx.x & 3;
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {  // swap the parts that differ in bit d of (row, quarter)
+    const bool up = q & d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & d) continue;
+      uint4 &lo = x[i], &hi = x[i | d];
+      uint4 give = up ? lo : hi, got;
+      got.x = __shfl_xor_sync(0xffffffffu, give.x, d);
+      got.y = __shfl_xor_sync(0xffffffffu, give.y, d);
+      got.z = __shfl_xor_sync(0xffffffffu, give.z, d);
+      got.w = __shfl_xor_sync(0xffffffffu, give.w, d);
+      if (up)
+        lo = got;
+      else
+        hi = got;
+    }
+  }
+}
 
 template <bool F16, int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_constant__ PromptLaunch L) {
   using S = PromptShape<D>;
+  constexpr int NB = S::kNB, LA = NB - 1;  // K blocks ahead of the V block in the ring
   constexpr float kBias = F16 ? 6.f : 0.f;
   extern __shared__ __align__(16) unsigned char sm_raw[];
   unsigned char *sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) unsigned long long s_full[S::kSlots], s_empty[S::kSlots], s_sfull[2], s_pready[2][2], s_half[2],
-      s_odone[2], s_qready, s_drain;
+  __shared__ __align__(8) unsigned long long s_full[S::kSlots], s_empty[S::kSlots], s_odone[2], s_qfull, s_qfree, s_drain;
+  // By warpgroup and the block's parity: with three places of scores a warpgroup and the
+  // MMA warp can be one block apart, and a wait by parity must not find two phases done.
+  __shared__ __align__(8) unsigned long long s_sfull[2][2], s_pready[2][2][2], s_half[2][2][2];
+  // V to be cleaned is there, and clean.  (The cleaning warp asks the ring's barriers only
+  // about a block that the MMA warp holds: not seeing all their phases, it cannot tell a
+  // phase to come from the one before.)
+  __shared__ __align__(8) unsigned long long s_dirty, s_clean;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ PromptStart s_start;
   __shared__ long long s_scan[kThreads / 32];
-  __shared__ int s_bad;
+  __shared__ volatile int s_bad[4];  // of a segment, in turn: a value that is not finite was left out
   const PromptParams &p = L.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  unsigned char *s_q = sm, *s_ring = sm + S::kQ;
-  const uint32_t q_addr = smem_u32(s_q), ring = smem_u32(s_ring);
+  const uint32_t q_addr = smem_u32(sm), ring = q_addr + S::kQ;
   if (tid == 0) {
     s_abort = 0;
-    s_bad = 0;
+    for (int s = 0; s < 4; ++s) s_bad[s] = 0;
     for (int s = 0; s < S::kSlots; ++s) {
       mbar_init(smem_u32(&s_full[s]), 2);
       mbar_init(smem_u32(&s_empty[s]), 1);
     }
     for (int w = 0; w < 2; ++w) {
-      mbar_init(smem_u32(&s_sfull[w]), 1);
-      mbar_init(smem_u32(&s_pready[w][0]), 128);
-      mbar_init(smem_u32(&s_pready[w][1]), 128);
-      mbar_init(smem_u32(&s_half[w]), 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_u32(&s_sfull[w][b]), 1);
+        for (int hf = 0; hf < 2; ++hf) {
+          mbar_init(smem_u32(&s_pready[w][b][hf]), 128);
+          mbar_init(smem_u32(&s_half[w][b][hf]), 1);
+        }
+      }
       mbar_init(smem_u32(&s_odone[w]), 1);
     }
-    mbar_init(smem_u32(&s_qready), 256);
+    mbar_init(smem_u32(&s_qfull), 1);
+    mbar_init(smem_u32(&s_qfree), 1);
+    mbar_init(smem_u32(&s_dirty), 1);
+    mbar_init(smem_u32(&s_clean), 1);
     mbar_init(smem_u32(&s_drain), 1);
     mbar_init_fence();
   }
@@ -371,6 +409,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     tmem_alloc(smem_u32(&s_tmem), 512);
     tmem_relinquish();
   }
+  // rows of Q that no copy writes
+  for (int u = p.G * L.pos * (D / 8) + tid; u < kTile * (D / 8); u += kThreads)
+    sts128(q_addr + (uint32_t)((u % (D / 8) >> 3) * 32768 + u / (D / 8) * 128 + (u & 7) * 16), make_uint4(0u, 0u, 0u, 0u));
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   tc_fence_before();
   pdl_wait();
   pdl_trigger();  // the join may now read the call's inputs
@@ -382,100 +424,145 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   if (warp == 8 || warp == 10) {
     // ---------------------------------------------------------------- producers
     const int me = (warp - 8) / 2;
-    int st = 0, ph = 0, issued = 0;
+    unsigned nk = 0, nv = 0;  // blocks of K and V so far
     bool ok = true;
+    auto load = [&](const CUtensorMap *map, const PromptWalk &wk, int t, int slot, unsigned phase) {
+      ok = ok && __all_sync(0xffffffffu,
+                            mbar_wait_fast(smem_u32(&s_empty[slot]), (phase & 1u) ^ 1u, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
+      if (!ok) return;
+      // this warp's box: 64 elements of 128 keys (D = 128), or all 64 of half the keys
+      const uint32_t fb = smem_u32(&s_full[slot]), dst = ring + (uint32_t)slot * S::kBlock + (uint32_t)me * (S::kBlock / 2);
+      if (lane == 0) mbar_expect_tx(fb, S::kBlock / 2);
+      __syncwarp();
+      tma_block(dst, map, D == 128 ? 64 * me : 0, wk.s.key0 + t * kKeys + (D == 128 ? 0 : 64 * me), wk.h, fb);
+    };
     while (ok && wk.next()) {
-      auto load = [&](const CUtensorMap *map, int swap, int t) {
-        ok = ok && __all_sync(0xffffffffu,
-                              mbar_wait_fast(smem_u32(&s_empty[st]), ph ^ 1, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
-        if (!ok) return;
-        // this warp's box: 64 elements of 128 keys (D = 128), or all 64 of half the keys
-        const uint32_t fb = smem_u32(&s_full[st]), dst = ring + (uint32_t)st * S::kBlock + (uint32_t)me * (S::kBlock / 2);
-        if (lane == 0) mbar_expect_tx(fb, S::kBlock / 2);
-        __syncwarp();
-        tma_block(dst, map, D == 128 ? 64 * me : 0, wk.h, wk.s.key0 + t * kKeys + (D == 128 ? 0 : 64 * me), swap, fb);
-        ++issued;
-        if (++st == S::kSlots) { st = 0; ph ^= 1; }
-      };
-      load(&L.tm_k, L.swap_k, wk.t0);
-      for (int t = wk.t0; t < wk.t1 && ok; ++t) {
-        load(&L.tm_v, L.swap_v, t);
-        if (t + 1 < wk.t1) load(&L.tm_k, L.swap_k, t + 1);
+      for (int t = wk.t0 - LA; t < wk.t1 && ok; ++t) {  // in the order of their first uses
+        if (t >= wk.t0) {
+          load(&L.tm_v, wk, t, S::kK + (int)(nv % S::kV), nv / S::kV);
+          ++nv;
+        }
+        if (ok && t + LA < wk.t1) {
+          load(&L.tm_k, wk, t + LA, (int)(nk % S::kK), nk / S::kK);
+          ++nk;
+        }
       }
     }
-    // no copy may land after the CTA exits: wait for the last fill of every slot
+    // no copy may land after the CTA exits: wait for the last fill of every slot (after a
+    // wait gave up the last one was not made, and this wait gives up too)
     volatile int never = 0;
-    for (int j = issued - S::kSlots < 0 ? 0 : issued - S::kSlots; j < issued; ++j)
-      if (!mbar_wait(smem_u32(&s_full[j % S::kSlots]), (j / S::kSlots) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never)) break;
+    for (unsigned j = nk > S::kK ? nk - S::kK : 0; j < nk; ++j)
+      if (!mbar_wait(smem_u32(&s_full[j % S::kK]), (j / S::kK) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never)) break;
+    for (unsigned j = nv > S::kV ? nv - S::kV : 0; j < nv; ++j)
+      if (!mbar_wait(smem_u32(&s_full[S::kK + j % S::kV]), (j / S::kV) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never)) break;
+  } else if (warp == 11) {
+    // ---------------------------------------------------------------- Q, and V next to the diagonal
+    unsigned seg = 0, blocks = 0, cleaned = 0;  // segments; blocks of those before; blocks cleaned
+    bool ok = true;
+    while (ok && wk.next()) {
+      const int n = wk.t1 - wk.t0, i0 = wk.t * L.pos, lim0 = limit_of(wk.s, i0);
+      // the scores of the segment before are made: its Q has been read
+      if (seg) ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_qfree), (seg - 1) & 1u, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_expect_tx(smem_u32(&s_qfull), (uint32_t)(p.G * L.pos * D * 2));
+        s_bad[seg & 3] = 0;  // of four segments before: long put out
+      }
+      __syncwarp();
+#pragma unroll
+      for (int hf = 0; hf < D / 64; ++hf)
+        tma_block(q_addr + (uint32_t)hf * (S::kQ / (D / 64)), &L.tm_q, 64 * hf, wk.s.row0 + i0, wk.h * p.G, smem_u32(&s_qfull));
+      // blocks that some row does not see the end of
+      for (int j = max(0, lim0 / kKeys - wk.t0); j < n && ok; ++j) {
+        const unsigned nv = blocks + (unsigned)j, slot = S::kK + nv % S::kV;
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_dirty), cleaned & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_full[slot]), (nv / S::kV) & 1u, p.err,
+                                                          DFV_DEVERR_STAGE_WAIT, &s_abort));
+        if (!ok) break;
+        const int k0 = (wk.t0 + j) * kKeys;
+        if (clean_block<F16, D>(ring + slot * S::kBlock, max(0, lim0 - k0), wk.s.nk - k0)) s_bad[seg & 3] = 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s_clean));
+        ++cleaned;
+      }
+      blocks += (unsigned)n;
+      ++seg;
+    }
+    volatile int never = 0;
+    if (seg) mbar_wait(smem_u32(&s_qfull), (seg - 1) & 1u, p.err, DFV_DEVERR_DRAIN_WAIT, &never);
   } else if (warp == 9) {
     // ---------------------------------------------------------------- MMA issue
-    int st = 0, ph = 0, seg = 0;
-    unsigned np[2] = {0u, 0u};  // blocks of each warpgroup whose P was awaited
+    // (Counters that only ever step on: what the descriptors and addresses come from stays
+    // in uniform registers.  Taken from a segment's lengths they made the issue of an MMA
+    // take longer than the MMA: 1972 us for 1504 with 16381 tokens.)
+    unsigned seg = 0, cleaned = 0;           // segments; blocks cleaned
+    unsigned kst = 0, kph = 0, vst = 0, vph = 0;  // slots of K and V and their phases
+    unsigned kpl = 0, vpl = 0;               // places of scores: of the next QK, of the next PV
+    unsigned kb = 0, vb = 0;                 // blocks of QK and of PV
     bool ok = true;
     const uint32_t iq = idesc_16<F16>(kKeys, false), iv = idesc_16<F16>(D, true);
-    auto full = [&]() {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_full[st]), ph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-      tc_fence_after();
-    };
-    auto done = [&]() {  // the slot is free once the MMAs issued so far have read it
-      tc_commit_elect(smem_u32(&s_empty[st]));
-      if (++st == S::kSlots) { st = 0; ph ^= 1; }
-    };
-    auto qk = [&](int w) {
-      const uint32_t kb = ring + (uint32_t)st * S::kBlock, qb = q_addr + (uint32_t)w * 128u * D * 2u;
+    // scores of the next block of warpgroup w, each block's for both in turn
+    auto qk = [&](int w, bool last) {
+      if (w == 0) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_full[kst]), kph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+        tc_fence_after();
+      }
+      if (!ok) return;
+      const uint32_t kaddr = ring + kst * S::kBlock, qb = q_addr + (uint32_t)w * 16384u, to = tmem + 128u * (NB == 2 ? (uint32_t)w : kpl);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks)
-        tc_mma_ss(tmem + (uint32_t)w * 128u, sdesc_k128(qb + (ks >> 2) * 16384) + (uint64_t)(2 * (ks & 3)),
-                  sdesc_k128(kb + (ks >> 2) * 16384) + (uint64_t)(2 * (ks & 3)), iq, ks > 0 ? 1u : 0u);
-      tc_commit_elect(smem_u32(&s_sfull[w]));
+        tc_mma_ss(to, sdesc_k128(qb + (ks >> 2) * 32768) + (uint64_t)(2 * (ks & 3)),
+                  sdesc_k128(kaddr + (ks >> 2) * 16384) + (uint64_t)(2 * (ks & 3)), iq, ks > 0 ? 1u : 0u);
+      tc_commit_elect(smem_u32(&s_sfull[w][kb & 1]));
+      if (++kpl == NB) kpl = 0;
+      if (w) {  // the slot is free once both have read it, and the segment's Q
+        tc_commit_elect(smem_u32(&s_empty[kst]));
+        if (last) tc_commit_elect(smem_u32(&s_qfree));
+        if (++kst == S::kK) { kst = 0; kph ^= 1; }
+        ++kb;
+      }
     };
-    auto pv = [&](int w, bool first, bool last) {
-      const uint32_t vb = ring + (uint32_t)st * S::kBlock;
+    auto pv = [&](int w, bool first, bool last, bool special) {
+      if (w == 0) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_full[S::kK + vst]), vph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+        if (special) {
+          if (ok && lane == 0) mbar_arrive(smem_u32(&s_dirty));
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_clean), cleaned & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+          ++cleaned;
+        }
+      }
+      const uint32_t vaddr = ring + (S::kK + vst) * S::kBlock, from = tmem + 128u * (NB == 2 ? (uint32_t)w : vpl), to = tmem + S::kO + (uint32_t)(w * D);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_pready[w][hf]), np[w] & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_pready[w][vb & 1][hf]), (vb >> 1) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
         if (!ok) return;
         tc_fence_after();
 #pragma unroll
         for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)
-          tc_mma_ts(tmem + 256u + (uint32_t)w * 128u, tmem + (uint32_t)w * 128u + (uint32_t)ks * 8u,
-                    sdesc_mn128(vb + (uint32_t)ks * 2048u), iv, (first && ks == 0) ? 0u : 1u);
-        if (hf == 0) tc_commit_elect(smem_u32(&s_half[w]));
+          tc_mma_ts(to, from + (uint32_t)(8 * ks), sdesc_mn128(vaddr + (uint32_t)ks * 2048u), iv, (first && ks == 0) ? 0u : 1u);
+        tc_commit_elect(smem_u32(&s_half[w][vb & 1][hf]));
       }
-      ++np[w];
       if (last) tc_commit_elect(smem_u32(&s_odone[w]));
+      if (++vpl == NB) vpl = 0;
+      if (w) {
+        tc_commit_elect(smem_u32(&s_empty[S::kK + vst]));
+        if (++vst == S::kV) { vst = 0; vph ^= 1; }
+        ++vb;
+      }
     };
     while (ok && wk.next()) {
-      const int n = wk.t1 - wk.t0;
-      ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_qready), seg & 1, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+      const int n = wk.t1 - wk.t0, j0 = limit_of(wk.s, wk.t * L.pos) / kKeys - wk.t0;  // blocks from j0 on are cleaned
+      ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_qfull), seg & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
       ++seg;
       tc_fence_after();
-      full();
-      if (!ok) break;
-      qk(0);
-      qk(1);
-      done();
-      for (int j = 0; j < n && ok; ++j) {
-        // V_j, then K_j+1; each warpgroup's next scores right after its own product
-        full();
-        if (!ok) break;
-        pv(0, j == 0, j == n - 1);
-        if (!ok) break;
-        if (j + 1 < n) {
-          const int sv = st, pv_ = ph;
-          if (++st == S::kSlots) { st = 0; ph ^= 1; }
-          full();
-          if (!ok) break;
-          qk(0);
-          st = sv; ph = pv_;
-        }
-        pv(1, j == 0, j == n - 1);
-        if (!ok) break;
-        done();  // V_j
-        if (j + 1 < n) {
-          qk(1);
-          done();  // K_j+1
-        }
+      qk(0, false);
+      if (ok) qk(1, n == 1);
+      if (NB == 3 && ok && n > 1) qk(0, false);
+      for (int j = 0; j < n && ok; ++j) {  // the next scores right after a product freed their place
+        pv(0, j == 0, j == n - 1, j >= j0);
+        if (ok && j + 1 < n) qk(NB == 2 ? 0 : 1, j + 2 == n);
+        if (ok) pv(1, j == 0, j == n - 1, false);
+        if (ok && j + NB - 1 < n) qk(NB == 2 ? 1 : 0, j + 2 == n);
       }
     }
     // every MMA issued has completed before tensor memory is released
@@ -484,99 +571,48 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     mbar_wait(smem_u32(&s_drain), 0u, p.err, DFV_DEVERR_DRAIN_WAIT, &never);
   } else {
     // ---------------------------------------------------------------- softmax and output
-    const int w = warp >> 2, wt = tid & 127;  // warpgroup, and its thread = row of the tile
+    const int w = warp >> 2, rr = tid & 255;  // warpgroup, and the thread's row of the tile
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t t_s = lane_base + (uint32_t)w * 128u, t_o = lane_base + 256u + (uint32_t)w * 128u;
+    const uint32_t t_o = lane_base + S::kO + (uint32_t)(w * D);
     const float c = p.scale_log2;
-    unsigned nt = 0;     // blocks this warpgroup has taken
-    unsigned outs = 0;   // segments it has put out
-    unsigned items = 0;  // ring items of the segments before
+    unsigned nt = 0;              // blocks this warpgroup has taken
+    unsigned seg = 0, turn = (unsigned)w;  // segments it has put out; its place of scores
+    const int g = head_of(L, rr), pi = rr - g * L.pos;
     bool ok = true, told = false;
     // after a wait gives up the loops still run to the end without touching
-    // tensor memory, so the warpgroups meet at every barrier
+    // tensor memory
     while (wk.next()) {
-      const int R = wk.s.n * p.G, n = wk.t1 - wk.t0, r0 = wk.t * kTile;
-      const int i0 = r0 / p.G, rest = r0 - i0 * p.G;  // position and head of the tile's first row
-      // rows into the swizzled layout; past R zero
-      {
-        constexpr int kCh = D / 8, kStep = 256 / kCh;  // 16-byte chunks of a row; rows apart
-        constexpr int kIter = kTile / kStep, kBatch = kIter < 8 ? kIter : 8;
-        const int ch = tid % kCh;
-        const char *qh = p.q + 2 * ((wk.s.row0 + (long long)i0) * p.q_row + (long long)wk.h * p.G * p.q_head + ch * 8);
-        uint4 x[kBatch];
-#pragma unroll
-        for (int k0 = 0; k0 < kIter; k0 += kBatch) {
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int rr = tid / kCh + (k0 + k) * kStep, i = over_g(L, rest + rr), g = rest + rr - i * p.G;
-            x[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (r0 + rr < R) x[k] = *reinterpret_cast<const uint4 *>(qh + 2 * (i * p.q_row + g * p.q_head));
-          }
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int rr = tid / kCh + (k0 + k) * kStep;
-            *reinterpret_cast<uint4 *>(s_q + (rr >> 7) * (128 * D * 2) + (ch >> 3) * 16384 + (rr & 127) * 128 +
-                                       (((ch & 7) ^ (rr & 7)) << 4)) = x[k];
-          }
-        }
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(smem_u32(&s_qready));
-
-      const int rr = w * 128 + wt, r = r0 + rr;  // this thread's row
-      const int pi = over_g(L, rest + rr), i = i0 + pi, head = wk.h * p.G + rest + rr - pi * p.G;
-      const int lim = r < R ? limit_of(wk.s, i) : wk.s.nk, lim0 = limit_of(wk.s, i0);  // keys that this row, and every row, sees
+      const int n = wk.t1 - wk.t0, i0 = wk.t * L.pos, i = i0 + pi, head = wk.h * p.G + g;
+      const bool mine = g < p.G && i < wk.s.n;
+      const int lim = mine ? limit_of(wk.s, i) : wk.s.nk, lim0 = limit_of(wk.s, i0);  // keys that this row, and every row, sees
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_sfull[w]), nt & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-        ++nt;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_sfull[w][nt & 1]), (nt >> 1) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+        const unsigned b = nt++;
+        const uint32_t t_s = lane_base + 128u * turn;
+        turn = (turn + 2u) % NB;
         if (!ok) continue;
         tc_fence_after();
-        const int k0 = (wk.t0 + j) * kKeys;
-        if (k0 + kKeys > lim0) {
-          mask_block(t_s, lim - k0);
-          if (w == 0) {
-            // this block's V before it is multiplied
-            const unsigned it = items + 2u * (unsigned)j + 1u;
-            ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_full[it % S::kSlots]), (it / S::kSlots) & 1u, p.err,
-                                                        DFV_DEVERR_STAGE_WAIT, &s_abort));
-            if (!ok) continue;
-            if (k0 + wt >= lim0) clean_key<F16, D>(s_ring + (size_t)(it % S::kSlots) * S::kBlock, wt, k0 + wt >= wk.s.nk, &s_bad);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          }
-        }
-        if (j == 0) {  // a maximum to begin with
+        const int sees = lim - (wk.t0 + j) * kKeys;  // of this block
+        const bool special = (wk.t0 + j + 1) * kKeys > lim0;
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
           float s0[32], s1[32];
-          tmem_ld32(t_s, s0);
-          tmem_ld32(t_s + 32, s1);
+          tmem_ld32(t_s + 64 * hf, s0);
+          tmem_ld32(t_s + 64 * hf + 32, s1);
           tmem_wait_ld32(s0);
           tmem_wait_ld32(s1);
-          m = max32(s1, max32(s0, m));
-        }
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          // One pass with the M so far: p and the new maximum together.  Only when
-          // some row's maximum grew too far is O rescaled and the pass made again.
-          uint32_t x[32];
-          float2 l2;
-          for (;;) {
-            // (rounded up: the largest p stays within its bound however large the scores are)
-            const float z = (m == -INFINITY ? 0.f : __fmul_ru(m, c)) - kBias;
-            float s0[32], s1[32], mx = m;
-            l2 = make_float2(0.f, 0.f);
-            tmem_ld32(t_s + 64 * hf, s0);
-            tmem_wait_ld32(s0);
-            tmem_ld32(t_s + 64 * hf + 32, s1);
-            mx = max32(s0, mx);
-            exp32<F16>(s0, c, z, x, l2);
-            tmem_wait_ld32(s1);
-            mx = max32(s1, mx);
-            exp32<F16>(s1, c, z, x + 16, l2);
-            if (!__any_sync(0xffffffffu, (mx - m) * c > 8.f)) break;
-            // products into O before these scores: those of the blocks before were
-            // complete when the scores were; the first half's own is waited for
-            if (hf == 1) {
-              ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_half[w]), (nt - 1u) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+          if (special) {
+            mask32(s0, sees - 64 * hf);
+            mask32(s1, sees - 64 * hf - 32);
+          }
+          const float mx = max32(s1, max32(s0, m));
+          if (__any_sync(0xffffffffu, (mx - m) * c > 8.f)) {
+            // the product into O before these scores' own: of this block's first half, or
+            // of the block before
+            if (j > 0 || hf == 1) {
+              const unsigned last = hf ? b : b - 1;
+              ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_half[w][last & 1][hf ^ 1]), (last >> 1) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
               tc_fence_after();
             }
             const float f = m == -INFINITY ? 0.f : ex2((m - mx) * c);
@@ -594,55 +630,71 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
             }
             m = mx;
           }
-          l += l2.x + l2.y;
+          // (rounded up: the largest p stays within its bound however large the scores are)
+          const float z = (m == -INFINITY ? 0.f : __fmul_ru(m, c)) - kBias;
+          float2 l2 = make_float2(0.f, 0.f);
+          uint32_t x[16];
+          exp32<F16>(s0, c, z, x, l2);
           tmem_st16(t_s + 32 * hf, x);
-          tmem_st16(t_s + 32 * hf + 16, x + 16);
+          exp32<F16>(s1, c, z, x, l2);
+          tmem_st16(t_s + 32 * hf + 16, x);
+          l += l2.x + l2.y;
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(smem_u32(&s_pready[w][hf]));
+          mbar_arrive(smem_u32(&s_pready[w][b & 1][hf]));
         }
       }
-      items += 2u * (unsigned)n;
-      // ---- output: the last product of this warpgroup
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_odone[w]), outs & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-      ++outs;
+      // ---- output: after the last product of this warpgroup.  Its next product into O needs
+      // its next P, which comes after these loads.
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_odone[w]), seg & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      bar_sync_n(1, 256);  // s_bad, and Q's place
-      const int bad = s_bad;
+      const int bad = s_bad[seg & 3];
       const float z = (m == -INFINITY ? 0.f : __fmul_ru(m, c)) - kBias;
       const bool whole = wk.whole();
       const int slot = wk.slot(blockIdx.x);
       const size_t row = wk.s.row0 + (size_t)i;
       const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
       char *out = p.o + 2 * ((long long)row * p.o_row + head * p.o_head);
+      char *rows[4];  // of the four lanes
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const unsigned long long r = __shfl_sync(0xffffffffu, mine ? (unsigned long long)out : 0ull, (lane & 28) + e);
+        rows[e] = (char *)r;
+      }
       float4 *part = reinterpret_cast<float4 *>(L.part_o) + (size_t)slot * (D / 4) * kTile + rr;
 #pragma unroll 1
       for (int q = 0; q < D && ok; q += 32) {
         float o[32];
         tmem_ld32(t_o + q, o);
         tmem_wait_ld32(o);
-        if (r >= R) continue;
         if (whole) {
-          uint32_t x[16];
+          uint4 x[4];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = pack2<F16>(o[2 * e] * inv, o[2 * e + 1] * inv);
-          uint4 *to = reinterpret_cast<uint4 *>(out + 2 * q);
+          for (int e = 0; e < 4; ++e)
+            x[e] = make_uint4(pack2<F16>(o[8 * e] * inv, o[8 * e + 1] * inv), pack2<F16>(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                              pack2<F16>(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack2<F16>(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          turn_quads(x);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) to[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-        } else {
+          for (int e = 0; e < 4; ++e)
+            if (rows[e]) *reinterpret_cast<uint4 *>(rows[e] + 2 * q + 16 * (lane & 3)) = x[e];
+        } else if (mine) {
           float4 *to = part + (size_t)(q / 4) * kTile;
 #pragma unroll
           for (int e = 0; e < 8; ++e) to[(size_t)e * kTile] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
-      if (r < R && ok) {
+      tc_fence_before();
+      if (mine && ok) {
         if (whole) {
           if (p.lse) p.lse[row * p.H + head] = l == 0.f ? -INFINITY : (z + log2f(l)) * 0.69314718055994531f;
-          if (bad) add_taken<F16>(p, wk.s, wk.h, lim0, lim, out, 0, D);
         } else {
           L.part_ml[(size_t)slot * kTile + rr] = make_float2(m == -INFINITY ? -INFINITY : z, l);
         }
+      }
+      if (whole && bad && ok) {
+        __syncwarp();  // the row's pieces were stored by four lanes
+        if (mine) add_taken<F16>(p, wk.s, wk.h, lim0, lim, out, 0, D);
       }
       if (tid == 0 && !whole) {
         L.part_bad[slot] = bad;
@@ -651,9 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
           told = true;
         }
       }
-      tc_fence_before();
-      bar_sync_n(1, 256);  // O, Q's place and s_bad are read
-      if (tid == 0) s_bad = 0;
+      ++seg;
     }
     if (tid == 0 && !told) L.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
@@ -678,8 +728,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const __gr
   const int n = cut.w;
   if (n < 2) return;
   const PromptSeq s = prompt_seq(p, cut.x);
-  const int r = cut.z * kTile + rr;
-  if (r >= s.n * p.G) return;
+  const int g = head_of(L, rr), i = cut.z * L.pos + rr - g * L.pos, head = cut.y * p.G + g;
+  if (g >= p.G || i >= s.n) return;
   // state k is range g0 + k's; the tile goes on after the first and began before the others
   auto slot = [&](int k) { return (size_t)(2 * (g0 + k) + (k == 0)); };
   float M = -INFINITY;
@@ -705,36 +755,30 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const __gr
       x[e].w = fmaf(y.w, f, x[e].w);
     }
   }
-  const int i = r / p.G, head = cut.y * p.G + r - i * p.G;
   const size_t row = s.row0 + (size_t)i;
   const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
   char *out = p.o + 2 * ((long long)row * p.o_row + head * p.o_head);
 #pragma unroll
   for (int e = 0; e < kPer; ++e)
     reinterpret_cast<uint2 *>(out)[warp * kPer + e] = make_uint2(pack2<F16>(x[e].x * inv, x[e].y * inv), pack2<F16>(x[e].z * inv, x[e].w * inv));
-  if (bad) add_taken<F16>(p, s, cut.y, limit_of(s, cut.z * kTile / p.G), limit_of(s, i), out, 4 * warp * kPer, 4 * (warp + 1) * kPer);
+  if (bad) add_taken<F16>(p, s, cut.y, limit_of(s, cut.z * L.pos), limit_of(s, i), out, 4 * warp * kPer, 4 * (warp + 1) * kPer);
   if (p.lse && warp == 0) p.lse[row * p.H + head] = l == 0.f ? -INFINITY : (M == -INFINITY ? l : (M + log2f(l)) * 0.69314718055994531f);
 }
 
-bool encode_rows(CUtensorMap *map, const PromptParams &p, const char *base, long long row, long long head, int box_rows,
-                 int *swap, char *why, size_t why_len) {
+bool encode_rows(CUtensorMap *map, const PromptParams &p, const char *base, int n, int heads, long long row, long long head,
+                 int box_rows, int box_heads, char *why, size_t why_len) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn(why, why_len);
   if (!fn) return false;
-  *swap = p.Hkv > 1 && p.n_keys > 1 && row < head;
   // a dimension of one entry has no stride of its own
-  const cuuint64_t one = 16;
-  const cuuint64_t r[2] = {(cuuint64_t)p.n_keys, p.n_keys > 1 ? (cuuint64_t)row * 2 : one};
-  const cuuint64_t h[2] = {(cuuint64_t)p.Hkv, p.Hkv > 1 ? (cuuint64_t)head * 2 : one};
-  const cuuint64_t *a = *swap ? r : h, *b = *swap ? h : r;
-  const cuuint64_t dims[3] = {(cuuint64_t)p.D, a[0], b[0]};
-  const cuuint64_t strides[2] = {a[1], b[1]};
-  const cuuint32_t box[3] = {64, *swap ? (cuuint32_t)box_rows : 1u, *swap ? 1u : (cuuint32_t)box_rows};
+  const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)n, (cuuint64_t)heads};
+  const cuuint64_t strides[2] = {n > 1 ? (cuuint64_t)row * 2 : 16, heads > 1 ? (cuuint64_t)head * 2 : 16};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_heads};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult e = fn(map, p.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                         const_cast<char *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (e != CUDA_SUCCESS) {
-    snprintf(why, why_len, "tensor map of the keys or values refused (%d)", (int)e);
+    snprintf(why, why_len, "tensor map of the queries, keys or values refused (%d)", (int)e);
     return false;
   }
   return true;
@@ -758,12 +802,20 @@ size_t prompt_attn_ws(int D) { return sections(nullptr, D, nullptr); }
 cudaError_t launch_prompt_attn(const PromptParams &p, void *ws, cudaStream_t s, char *why, size_t why_len) {
   static thread_local PromptLaunch L;
   L.p = p;
-  L.inv_g = (65536u + p.G - 1) / p.G;
+  // positions of a tile: a multiple of 8, so that each head's rows begin on a 1024-byte
+  // boundary of the swizzled tile
+  L.pos = kTile / p.G & ~7;
+  int gcd = 8;
+  while (gcd < kKeys && L.pos % (2 * gcd) == 0) gcd *= 2;
+  L.run = kKeys / gcd;
+  L.rise = L.pos / gcd;
+  L.inv_pos = (65536u + L.pos - 1) / L.pos;
   L.whole = p.max_keys <= kWholeKeys;
   sections(&L, p.D, ws);
   const int box = p.D == 128 ? kKeys : kKeys / 2;
-  if (!encode_rows(&L.tm_k, p, p.k, p.k_row, p.k_head, box, &L.swap_k, why, why_len) ||
-      !encode_rows(&L.tm_v, p, p.v, p.v_row, p.v_head, box, &L.swap_v, why, why_len))
+  if (!encode_rows(&L.tm_q, p, p.q, p.n_rows, p.H, p.q_row, p.q_head, L.pos, p.G, why, why_len) ||
+      !encode_rows(&L.tm_k, p, p.k, p.n_keys, p.Hkv, p.k_row, p.k_head, box, 1, why, why_len) ||
+      !encode_rows(&L.tm_v, p, p.v, p.n_keys, p.Hkv, p.v_row, p.v_head, box, 1, why, why_len))
     return cudaErrorInvalidValue;
   if (p.D == 128) return p.f16 ? launch_typed<true, 128>(L, s) : launch_typed<false, 128>(L, s);
   return p.f16 ? launch_typed<true, 64>(L, s) : launch_typed<false, 64>(L, s);

@@ -69,10 +69,6 @@ __device__ __forceinline__ void widen16(const uint4 &x, __half2 m, uint4 &lo, ui
   hi = make_uint4(y[4], y[5], y[6], y[7]);
 }
 
-__device__ __forceinline__ void sts128(uint32_t addr, const uint4 &v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
 // 2^-d in fp16, d >= 0 (0 below its subnormals)
 __device__ __forceinline__ __half2 half_power(int d) {
   const uint32_t b = d <= 14 ? (uint32_t)(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;

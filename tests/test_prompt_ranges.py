@@ -2,6 +2,7 @@
 tile, the cut of the line into ranges, and the partial states that the join reads.  Constants come from the source."""
 from __future__ import annotations
 
+import math
 import os
 import random
 import re
@@ -13,29 +14,36 @@ TEXT = open(os.path.join(CSRC, "prompt_attn.cu")).read()
 KEYS, TILE, OVER, CTAS = 128, 256, int(re.search(r"kOver = (\d+);", TEXT).group(1)), 152
 
 
+def positions(G):
+    return TILE // G & ~7
+
+
 def limit(n, nk, i):
     return min(nk, max(0, nk - n + i + 1))
 
 
 def blocks(n, nk, G, t):
-    return max(1, -(-limit(n, nk, min(n - 1, (TILE * t + TILE - 1) // G)) // KEYS))
+    return max(1, -(-limit(n, nk, min(n, (t + 1) * positions(G)) - 1) // KEYS))
 
 
 def tiles(n, G):
-    return -(-n * G // TILE)
+    return -(-n // positions(G))
 
 
 def blocks_before(n, nk, G, i):
     """The kernel's closed form, statement by statement (C's division: no operand is negative where it divides)."""
-    B = (255 + G * (KEYS + nk - n)) >> 7
-    i1 = 0 if B >= G else (G - B + 1) // 2
+    P = positions(G)
+    C = P + KEYS - 1 + nk - n
+    run, rise = KEYS // math.gcd(P, KEYS), P // math.gcd(P, KEYS)
+    assert run <= 16
+    i1 = 0 if C >= KEYS else (KEYS - C + P - 1) // P
     if i <= i1:
         return i
-    c, w = 2 * i1 + B, i - i1
-    a, r = w // G, w % G
-    f = [(2 * u + c) // G for u in range(G)]
+    c, w = P * i1 + C, i - i1
+    a, r = w // run, w % run
+    f = [(P * u + c) // KEYS for u in range(run)]
     assert c >= 0
-    return i1 + a * sum(f) + G * a * (a - 1) + sum(f[:r]) + 2 * a * r
+    return i1 + a * sum(f) + rise * run * (a * (a - 1) // 2) + sum(f[:r]) + rise * a * r
 
 
 @pytest.mark.parametrize("G", range(1, 17))
@@ -155,9 +163,85 @@ def test_the_join_reads_what_was_left(seqs, G, heads):
     assert not slots
 
 
-def test_the_quotient_by_the_group():
-    """over_g: the product's error stays below one part in 2^16 / G for the numbers that occur (a tile's 256 rows and a
-    remainder below G)."""
+def test_the_head_of_a_row():
+    """head_of: the quotient of a tile's row by its positions."""
     for G in range(1, 17):
-        inv = (65536 + G - 1) // G
-        assert all(r * inv >> 16 == r // G for r in range(256 + G))
+        P = positions(G)
+        assert P % 8 == 0 and P * G <= TILE
+        inv = (65536 + P - 1) // P
+        assert all(r * inv >> 16 == r // P for r in range(TILE))
+
+
+# ---------------------------------------------------------------- the ring and the barriers
+@pytest.mark.parametrize("NB", [2, 3])
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 9])
+def test_the_order_of_the_ring(NB, n):
+    """What the producers load, the products use and the cleaning warp looks for is in the same order, and a block's place
+    is free after its second use."""
+    LA = NB - 1
+    order = [("k", j) for j in range(min(LA, n))]
+    for t in range(n):
+        order.append(("v", t))
+        if t + LA < n:
+            order.append(("k", t + LA))
+    item_k = lambda j: j if j < LA else min(2 * j - LA + 1, n + j)  # noqa: E731
+    item_v = lambda j: j + min(n, j + LA)  # noqa: E731
+    assert len(order) == 2 * n
+    for j in range(n):
+        assert order[item_k(j)] == ("k", j) and order[item_v(j)] == ("v", j)
+    used = []
+    for i in range(-NB, 2 * n):
+        if i >= 0:
+            used.append(item_v(i >> 1))
+        if 0 <= i + NB < 2 * n:
+            used.append(item_k((i + NB) >> 1))
+    first = [used.index(x) for x in range(2 * n)]
+    assert first == sorted(first) and all(used.count(x) == 2 for x in range(2 * n))
+
+
+@pytest.mark.parametrize("NB", [2, 3])
+def test_no_wait_by_parity_meets_two_phases(NB):
+    """Every order of the MMA warp and the two warpgroups that the barriers allow, over two tiles: whoever waits for block b on
+    a barrier finds block b's phase there, not a later one, and nobody waits for ever."""
+    n, tiles_ = 3, 2
+    mma = []
+    for _ in range(tiles_):
+        for i in range(-NB, 2 * n):
+            if i >= 0:
+                mma += [("wait", "p", i & 1, i >> 1, hf) for hf in (0, 1)]
+            if 0 <= i + NB < 2 * n:
+                mma.append(("post", "s", (i + NB) & 1, (i + NB) >> 1, 0))
+        mma.append(("tile",))
+    # the MMA warp's events with blocks counted over both tiles
+    at, m = 0, []
+    for e in mma:
+        if e[0] == "tile":
+            at += n
+        else:
+            m.append((e[0], e[1], e[2], e[3] + at, e[4]))
+    wg = [[e for b in range(n * tiles_) for e in (("wait", "s", w, b, 0), ("post", "p", w, b, 0), ("post", "p", w, b, 1))] for w in (0, 1)]
+    progs = [m] + wg
+    seen, todo = set(), [((0, 0, 0), ())]
+    while todo:
+        pcs, posted = todo.pop()
+        if (pcs, posted) in seen:
+            continue
+        seen.add((pcs, posted))
+        done = dict(posted)  # (kind, warpgroup, parity, half) -> phases done
+        moved = False
+        for k, pc in enumerate(pcs):
+            if pc == len(progs[k]):
+                continue
+            what, kind, w, b, hf = progs[k][pc]
+            key = (kind, w, b & 1, hf)
+            if what == "wait":
+                assert done.get(key, 0) <= (b >> 1) + 1, "a later phase is done"
+                if done.get(key, 0) < (b >> 1) + 1:
+                    continue
+                new = posted
+            else:
+                assert done.get(key, 0) == b >> 1
+                new = tuple(sorted({**done, key: (b >> 1) + 1}.items()))
+            moved = True
+            todo.append((pcs[:k] + (pc + 1,) + pcs[k + 1:], new))
+        assert moved or all(pc == len(q) for pc, q in zip(pcs, progs)), "nobody can go on"
