@@ -53,6 +53,48 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// Scores of a block: D[tmem] = A B^T over D elements, A of 256 rows and B of 128 in blocks
+// of 64 elements.  One elected lane for all of it: an elect.sync an MMA took about
+// as long as the MMA.
+template <int D>
+__device__ __forceinline__ void tc_scores(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc) {
+  if (D == 128)
+    asm volatile(
+      "{\n .reg .pred no, yes, q;\n .reg .b64 a, b;\n setp.ne.b32 no, %3, %3;\n setp.eq.b32 yes, %3, %3;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, no;\n"
+      " add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
+      " add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
+      " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
+      " add.s64 a, %1, 2048;\n add.s64 b, %2, 1024;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
+      " add.s64 a, %1, 2050;\n add.s64 b, %2, 1026;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
+      " add.s64 a, %1, 2052;\n add.s64 b, %2, 1028;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
+      " add.s64 a, %1, 2054;\n add.s64 b, %2, 1030;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
+      "}"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc)
+      : "memory");
+  else
+    asm volatile(
+      "{\n .reg .pred no, yes, q;\n .reg .b64 a, b;\n setp.ne.b32 no, %3, %3;\n setp.eq.b32 yes, %3, %3;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, no;\n"
+      " add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
+      " add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
+      " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
+      "}"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] B over 64 keys: A 8 columns further and B 16 rows of 128 bytes further
+// an MMA
+__device__ __forceinline__ void tc_values(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, yes, q;\n .reg .b64 b;\n .reg .b32 a;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 yes, %3, %3;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " add.s64 b, %2, 128;\n add.u32 a, %1, 8;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
+      " add.s64 b, %2, 256;\n add.u32 a, %1, 16;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
+      " add.s64 b, %2, 384;\n add.u32 a, %1, 24;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 __device__ __forceinline__ void tc_commit_elect(uint32_t bar) {
   asm volatile(
       "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"

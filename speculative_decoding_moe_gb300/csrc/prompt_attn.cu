@@ -278,36 +278,61 @@ __device__ __forceinline__ void tma_block(uint32_t dst, const CUtensorMap *map, 
       : "memory");
 }
 
+// Keys of a block that the products take, 16 at a time: those that the tile's last row
+// sees, of the first block 16 at least (its product writes O).
+__device__ __forceinline__ int steps_of(const PromptLaunch &L, const PromptSeq &s, int t, int j) {
+  const int seen = limit_of(s, min(s.n, (t + 1) * L.pos) - 1) - j * kKeys;
+  return min(kKeys / 16, max(1, (seen + 15) >> 4));
+}
+
 // Of 32 scores the row sees the first `sees`: the others become -inf.
 __device__ __forceinline__ void mask32(float *s, int sees) {
 #pragma unroll
   for (int e = 0; e < 32; ++e) s[e] = e < sees ? s[e] : -INFINITY;
 }
 
-// Rows [from, 128) of a V block in shared memory, by one warp: zeroed from `past` on;
+// Rows [from, to) of a V block in shared memory, by one warp: zeroed from `past` on;
 // values that are not finite before that become zero and are told of.
 template <bool F16, int D>
-__device__ __forceinline__ bool clean_block(uint32_t block, int from, int past) {
-  constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
+__device__ __forceinline__ bool clean_block(uint32_t block, int from, int past, int to) {
+  // a 16-bit half whose exponent is all ones carries into its sign
+  constexpr uint32_t kExp = F16 ? 0x7c007c00u : 0x7f807f80u, kOne = F16 ? 0x04000400u : 0x00800080u;
   constexpr int kCh = D / 8;  // 16-byte chunks of a row
-  bool hit = false;
-#pragma unroll 2
-  for (int u = from * kCh + (threadIdx.x & 31); u < kKeys * kCh; u += 32) {
+  const int lane = threadIdx.x & 31;
+  auto place = [&](int u) {
     const int row = u / kCh, c = u % kCh;
-    const uint32_t at = block + (uint32_t)((c >> 3) * 16384 + row * 128 + (((c ^ row) & 7) << 4));
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    bool change = row >= past;
-    if (!change) {
-      v = lds128(at);
-      uint32_t *w = &v.x;
+    return block + (uint32_t)((c >> 3) * 16384 + row * 128 + (((c ^ row) & 7) << 4));
+  };
+  for (int u = max(from, past) * kCh + lane; u < to * kCh; u += 32) sts128(place(u), make_uint4(0u, 0u, 0u, 0u));
+  bool hit = false;
+  const int end = min(past, to) * kCh;
+  for (int u0 = from * kCh + lane; u0 < end; u0 += 128) {
+    uint4 v[4];
+    uint32_t any = 0u;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if ((w[e] & kExp) == kExp) { w[e] &= 0xffff0000u; change = true; }
-        if ((w[e] & (kExp << 16)) == (kExp << 16)) { w[e] &= 0x0000ffffu; change = true; }
-      }
-      hit = hit || change;
+    for (int i = 0; i < 4; ++i) {
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (u0 + 32 * i < end) v[i] = lds128(place(u0 + 32 * i));
     }
-    if (change) sts128(at, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t *w = &v[i].x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) any |= (w[e] & kExp) + kOne;
+    }
+    if (any & 0x80008000u) {  // rare
+      hit = true;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t *w = &v[i].x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t z = ((w[e] & kExp) + kOne) & 0x80008000u;
+          w[e] &= ~((z >> 15) * 0xffffu);
+        }
+        if (u0 + 32 * i < end) sts128(place(u0 + 32 * i), v[i]);
+      }
+    }
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   return __any_sync(0xffffffffu, hit);
@@ -480,7 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
                                                           DFV_DEVERR_STAGE_WAIT, &s_abort));
         if (!ok) break;
         const int k0 = (wk.t0 + j) * kKeys;
-        if (clean_block<F16, D>(ring + slot * S::kBlock, max(0, lim0 - k0), wk.s.nk - k0)) s_bad[seg & 3] = 1;
+        if (clean_block<F16, D>(ring + slot * S::kBlock, max(0, lim0 - k0), max(0, wk.s.nk - k0), 16 * steps_of(L, wk.s, wk.t, wk.t0 + j)))
+          s_bad[seg & 3] = 1;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s_clean));
         ++cleaned;
@@ -509,10 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       }
       if (!ok) return;
       const uint32_t kaddr = ring + kst * S::kBlock, qb = q_addr + (uint32_t)w * 16384u, to = tmem + 128u * (NB == 2 ? (uint32_t)w : kpl);
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        tc_mma_ss(to, sdesc_k128(qb + (ks >> 2) * 32768) + (uint64_t)(2 * (ks & 3)),
-                  sdesc_k128(kaddr + (ks >> 2) * 16384) + (uint64_t)(2 * (ks & 3)), iq, ks > 0 ? 1u : 0u);
+      tc_scores<D>(to, sdesc_k128(qb), sdesc_k128(kaddr), iq);
       tc_commit_elect(smem_u32(&s_sfull[w][kb & 1]));
       if (++kpl == NB) kpl = 0;
       if (w) {  // the slot is free once both have read it, and the segment's Q
@@ -522,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         ++kb;
       }
     };
-    auto pv = [&](int w, bool first, bool last, bool special) {
+    auto pv = [&](int w, bool first, bool last, bool special, int steps) {
       if (w == 0) {
         ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_full[S::kK + vst]), vph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
         if (special) {
@@ -537,9 +560,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_pready[w][vb & 1][hf]), (vb >> 1) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
         if (!ok) return;
         tc_fence_after();
-#pragma unroll
-        for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)
-          tc_mma_ts(to, from + (uint32_t)(8 * ks), sdesc_mn128(vaddr + (uint32_t)ks * 2048u), iv, (first && ks == 0) ? 0u : 1u);
+        // (keys that no row of the tile sees, 16 at a time, take part in no product)
+        if (steps >= 4 * hf + 4) {
+          tc_values(to, from + 32u * hf, sdesc_mn128(vaddr + 8192u * hf), iv, (first && hf == 0) ? 0u : 1u);
+        } else {
+#pragma unroll 1
+          for (int ks = 4 * hf; ks < steps; ++ks)
+            tc_mma_ts(to, from + (uint32_t)(8 * ks), sdesc_mn128(vaddr + (uint32_t)ks * 2048u), iv, (first && ks == 0) ? 0u : 1u);
+        }
         tc_commit_elect(smem_u32(&s_half[w][vb & 1][hf]));
       }
       if (last) tc_commit_elect(smem_u32(&s_odone[w]));
@@ -559,9 +587,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       if (ok) qk(1, n == 1);
       if (NB == 3 && ok && n > 1) qk(0, false);
       for (int j = 0; j < n && ok; ++j) {  // the next scores right after a product freed their place
-        pv(0, j == 0, j == n - 1, j >= j0);
+        const int steps = j < j0 ? kKeys / 16 : steps_of(L, wk.s, wk.t, wk.t0 + j);
+        pv(0, j == 0, j == n - 1, j >= j0, steps);
         if (ok && j + 1 < n) qk(NB == 2 ? 0 : 1, j + 2 == n);
-        if (ok) pv(1, j == 0, j == n - 1, false);
+        if (ok) pv(1, j == 0, j == n - 1, false, steps);
         if (ok && j + NB - 1 < n) qk(NB == 2 ? 1 : 0, j + 2 == n);
       }
     }
@@ -595,8 +624,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         tc_fence_after();
         const int sees = lim - (wk.t0 + j) * kKeys;  // of this block
         const bool special = (wk.t0 + j + 1) * kKeys > lim0;
+        // keys that no row of the tile sees take part in no product: neither does their half
+        const int halves = special && steps_of(L, wk.s, wk.t, wk.t0 + j) <= 4 ? 1 : 2;
 #pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
+          if (hf == halves) {
+            mbar_arrive(smem_u32(&s_pready[w][b & 1][1]));
+            break;
+          }
           float s0[32], s1[32];
           tmem_ld32(t_s + 64 * hf, s0);
           tmem_ld32(t_s + 64 * hf + 32, s1);
