@@ -83,7 +83,7 @@ __device__ __forceinline__ void tc_scores(uint32_t d_tmem, uint64_t adesc, uint6
       ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc)
       : "memory");
 }
-// D[tmem] (+)= A[tmem] B over 64 keys: A 8 columns further and B 16 rows of 128 bytes further
+// D[tmem] (+)= A[tmem] B over 128 keys: A 8 columns further and B 16 rows of 128 bytes further
 // an MMA
 __device__ __forceinline__ void tc_values(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -91,7 +91,12 @@ __device__ __forceinline__ void tc_values(uint32_t d_tmem, uint32_t a_tmem, uint
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
       " add.s64 b, %2, 128;\n add.u32 a, %1, 8;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
       " add.s64 b, %2, 256;\n add.u32 a, %1, 16;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
-      " add.s64 b, %2, 384;\n add.u32 a, %1, 24;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n}" ::"r"(d_tmem),
+      " add.s64 b, %2, 384;\n add.u32 a, %1, 24;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
+      " add.s64 b, %2, 512;\n add.u32 a, %1, 32;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
+      " add.s64 b, %2, 640;\n add.u32 a, %1, 40;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
+      " add.s64 b, %2, 768;\n add.u32 a, %1, 48;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
+      " add.s64 b, %2, 896;\n add.u32 a, %1, 56;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
+      "}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }

@@ -11,15 +11,17 @@
 // diagonal, and the causal mask is one limit per row.  A CTA streams the tile's keys
 // in blocks of 128: two warpgroups take 128 rows each, S = Q K^T goes to tensor
 // memory, a thread turns its row of S into P over S, and O += P V accumulates in
-// tensor memory.  P is given to the products in halves of 64 keys, so that a product
-// starts while the second half is in its exponentials.  M is only raised, and O only
-// rescaled, when a row's maximum grew by more than 2^8; before the second half of a
-// block that waits for the first half's product.
+// tensor memory.  One pass over the scores computes p with the M so far; M is only
+// raised, and O only rescaled, when a row's maximum grew by more than 2^8, and the
+// pass is then made again.
 //
 // Scores take turns in NB places of 128 columns: two with heads of 128, one a
 // warpgroup; three with heads of 64, where the outputs leave room, so that a warpgroup's
 // next scores are ready while it is still in its exponentials.  The products follow the
-// warpgroups' places in turn, PV_i then QK_(i + NB).  A tile's queries are copied, and
+// warpgroups' places in turn, PV_i then QK_(i + NB) in one step: the tensor core's queue
+// is a few MMAs deep, and each wait of the warp that fills it, ready or not, takes
+// about as long as they do, so a step's waits come first and together (apart, before
+// each product, they took a third of the time).  A tile's queries are copied, and
 // its first scores made, while the warpgroups put out the tile before.
 //
 // Work split.  All tiles' blocks form one line, (sequence, kv head, tile) after
@@ -285,10 +287,20 @@ __device__ __forceinline__ int steps_of(const PromptLaunch &L, const PromptSeq &
   return min(kKeys / 16, max(1, (seen + 15) >> 4));
 }
 
-// Of 32 scores the row sees the first `sees`: the others become -inf.
-__device__ __forceinline__ void mask32(float *s, int sees) {
+// Scores of the first `n` keys of a block of which the row sees the first `sees`: the
+// others become -inf, in place.
+__device__ __forceinline__ void mask_block(uint32_t t_s, int sees, int n) {
+#pragma unroll 1
+  for (int q = 0; q < n; q += 16) {
+    if (__all_sync(0xffffffffu, q + 16 <= sees)) continue;
+    float s[16];
+    tmem_ld16(t_s + q, s);
+    uint32_t x[16];
 #pragma unroll
-  for (int e = 0; e < 32; ++e) s[e] = e < sees ? s[e] : -INFINITY;
+    for (int e = 0; e < 16; ++e) x[e] = q + e < sees ? __float_as_uint(s[e]) : 0xff800000u;
+    tmem_st16(t_s + q, x);
+  }
+  tmem_wait_st();
 }
 
 // Rows [from, to) of a V block in shared memory, by one warp: zeroed from `past` on;
@@ -393,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   __shared__ __align__(8) unsigned long long s_full[S::kSlots], s_empty[S::kSlots], s_odone[2], s_qfull, s_qfree, s_drain;
   // By warpgroup and the block's parity: with three places of scores a warpgroup and the
   // MMA warp can be one block apart, and a wait by parity must not find two phases done.
-  __shared__ __align__(8) unsigned long long s_sfull[2][2], s_pready[2][2][2], s_half[2][2][2];
+  __shared__ __align__(8) unsigned long long s_sfull[2][2], s_pready[2][2];
   // V to be cleaned is there, and clean.  (The cleaning warp asks the ring's barriers only
   // about a block that the MMA warp holds: not seeing all their phases, it cannot tell a
   // phase to come from the one before.)
@@ -416,10 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     for (int w = 0; w < 2; ++w) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(smem_u32(&s_sfull[w][b]), 1);
-        for (int hf = 0; hf < 2; ++hf) {
-          mbar_init(smem_u32(&s_pready[w][b][hf]), 128);
-          mbar_init(smem_u32(&s_half[w][b][hf]), 1);
-        }
+        mbar_init(smem_u32(&s_pready[w][b]), 128);
       }
       mbar_init(smem_u32(&s_odone[w]), 1);
     }
@@ -527,13 +536,23 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     unsigned kb = 0, vb = 0;                 // blocks of QK and of PV
     bool ok = true;
     const uint32_t iq = idesc_16<F16>(kKeys, false), iv = idesc_16<F16>(D, true);
+    auto wait = [&](unsigned long long &bar, unsigned phase) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&bar), phase, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+    };
+    // what PV of warpgroup w waits for, and QK of warpgroup wq (-1: none) behind it
+    auto ready = [&](int w, int wq) {
+      bool r = mbar_try_wait(smem_u32(&s_pready[w][vb & 1]), (vb >> 1) & 1u);
+      if (w == 0) r = mbar_try_wait(smem_u32(&s_full[S::kK + vst]), vph) && r;
+      if (wq == 0) r = mbar_try_wait(smem_u32(&s_full[kst]), kph) && r;
+      if (!__all_sync(0xffffffffu, r)) {
+        if (w == 0) wait(s_full[S::kK + vst], vph);
+        if (wq == 0) wait(s_full[kst], kph);
+        wait(s_pready[w][vb & 1], (vb >> 1) & 1u);
+      }
+      tc_fence_after();
+    };
     // scores of the next block of warpgroup w, each block's for both in turn
     auto qk = [&](int w, bool last) {
-      if (w == 0) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_full[kst]), kph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-        tc_fence_after();
-      }
-      if (!ok) return;
       const uint32_t kaddr = ring + kst * S::kBlock, qb = q_addr + (uint32_t)w * 16384u, to = tmem + 128u * (NB == 2 ? (uint32_t)w : kpl);
       tc_scores<D>(to, sdesc_k128(qb), sdesc_k128(kaddr), iq);
       tc_commit_elect(smem_u32(&s_sfull[w][kb & 1]));
@@ -545,30 +564,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         ++kb;
       }
     };
-    auto pv = [&](int w, bool first, bool last, bool special, int steps) {
-      if (w == 0) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_full[S::kK + vst]), vph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-        if (special) {
-          if (ok && lane == 0) mbar_arrive(smem_u32(&s_dirty));
-          ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_clean), cleaned & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-          ++cleaned;
-        }
-      }
+    auto pv = [&](int w, bool first, bool last, int steps) {
       const uint32_t vaddr = ring + (S::kK + vst) * S::kBlock, from = tmem + 128u * (NB == 2 ? (uint32_t)w : vpl), to = tmem + S::kO + (uint32_t)(w * D);
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_pready[w][vb & 1][hf]), (vb >> 1) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-        if (!ok) return;
-        tc_fence_after();
-        // (keys that no row of the tile sees, 16 at a time, take part in no product)
-        if (steps >= 4 * hf + 4) {
-          tc_values(to, from + 32u * hf, sdesc_mn128(vaddr + 8192u * hf), iv, (first && hf == 0) ? 0u : 1u);
-        } else {
+      if (steps == kKeys / 16) {
+        tc_values(to, from, sdesc_mn128(vaddr), iv, first ? 0u : 1u);
+      } else {  // keys that no row of the tile sees, 16 at a time, take part in no product
 #pragma unroll 1
-          for (int ks = 4 * hf; ks < steps; ++ks)
-            tc_mma_ts(to, from + (uint32_t)(8 * ks), sdesc_mn128(vaddr + (uint32_t)ks * 2048u), iv, (first && ks == 0) ? 0u : 1u);
-        }
-        tc_commit_elect(smem_u32(&s_half[w][vb & 1][hf]));
+        for (int ks = 0; ks < steps; ++ks)
+          tc_mma_ts(to, from + (uint32_t)(8 * ks), sdesc_mn128(vaddr + (uint32_t)ks * 2048u), iv, (first && ks == 0) ? 0u : 1u);
       }
       if (last) tc_commit_elect(smem_u32(&s_odone[w]));
       if (++vpl == NB) vpl = 0;
@@ -580,18 +583,37 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     };
     while (ok && wk.next()) {
       const int n = wk.t1 - wk.t0, j0 = limit_of(wk.s, wk.t * L.pos) / kKeys - wk.t0;  // blocks from j0 on are cleaned
-      ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_qfull), seg & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+      wait(s_qfull, seg & 1u);
       ++seg;
+      wait(s_full[kst], kph);
       tc_fence_after();
+      if (!ok) break;
       qk(0, false);
-      if (ok) qk(1, n == 1);
-      if (NB == 3 && ok && n > 1) qk(0, false);
-      for (int j = 0; j < n && ok; ++j) {  // the next scores right after a product freed their place
-        const int steps = j < j0 ? kKeys / 16 : steps_of(L, wk.s, wk.t, wk.t0 + j);
-        pv(0, j == 0, j == n - 1, j >= j0, steps);
-        if (ok && j + 1 < n) qk(NB == 2 ? 0 : 1, j + 2 == n);
-        if (ok) pv(1, j == 0, j == n - 1, false, steps);
-        if (ok && j + NB - 1 < n) qk(NB == 2 ? 1 : 0, j + 2 == n);
+      qk(1, n == 1);
+      if (NB == 3 && n > 1) {
+        wait(s_full[kst], kph);
+        tc_fence_after();
+        if (!ok) break;
+        qk(0, false);
+      }
+      for (int j = 0; j < n; ++j) {  // the next scores right after a product freed their place
+        const bool more = j + 1 < n, more2 = j + NB - 1 < n;
+        int steps = kKeys / 16;
+        if (j >= j0) {
+          steps = steps_of(L, wk.s, wk.t, wk.t0 + j);
+          wait(s_full[S::kK + vst], vph);
+          if (ok && lane == 0) mbar_arrive(smem_u32(&s_dirty));
+          wait(s_clean, cleaned & 1u);
+          ++cleaned;
+        }
+        ready(0, NB == 2 && more ? 0 : -1);
+        if (!ok) break;
+        pv(0, j == 0, j == n - 1, steps);
+        if (more) qk(NB == 2 ? 0 : 1, j + 2 == n);
+        ready(1, NB == 3 && more2 ? 0 : -1);
+        if (!ok) break;
+        pv(1, j == 0, j == n - 1, steps);
+        if (more2) qk(NB == 2 ? 1 : 0, j + 2 == n);
       }
     }
     // every MMA issued has completed before tensor memory is released
@@ -622,37 +644,59 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         turn = (turn + 2u) % NB;
         if (!ok) continue;
         tc_fence_after();
-        const int sees = lim - (wk.t0 + j) * kKeys;  // of this block
-        const bool special = (wk.t0 + j + 1) * kKeys > lim0;
-        // keys that no row of the tile sees take part in no product: neither does their half
-        const int halves = special && steps_of(L, wk.s, wk.t, wk.t0 + j) <= 4 ? 1 : 2;
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          if (hf == halves) {
-            mbar_arrive(smem_u32(&s_pready[w][b & 1][1]));
-            break;
-          }
+        // keys that no row of the tile sees take part in no product: neither do their 64
+        bool both = true;
+        if ((wk.t0 + j + 1) * kKeys > lim0) {
+          both = steps_of(L, wk.s, wk.t, wk.t0 + j) > 4;
+          mask_block(t_s, lim - (wk.t0 + j) * kKeys, both ? 128 : 64);
+        }
+        if (j == 0) {  // a maximum to begin with
           float s0[32], s1[32];
-          tmem_ld32(t_s + 64 * hf, s0);
-          tmem_ld32(t_s + 64 * hf + 32, s1);
+          tmem_ld32(t_s, s0);
+          tmem_ld32(t_s + 32, s1);
           tmem_wait_ld32(s0);
           tmem_wait_ld32(s1);
-          if (special) {
-            mask32(s0, sees - 64 * hf);
-            mask32(s1, sees - 64 * hf - 32);
+          m = max32(s1, max32(s0, m));
+        }
+        // One pass with the M so far: p and the new maximum together, a quarter of the
+        // scores read while the one before is used.
+        uint32_t x[64];
+        float2 l2;
+        for (;;) {
+          // (rounded up: the largest p stays within its bound however large the scores are)
+          const float z = (m == -INFINITY ? 0.f : __fmul_ru(m, c)) - kBias;
+          float s0[32], s1[32], mx = m;
+          l2 = make_float2(0.f, 0.f);
+          tmem_ld32(t_s, s0);
+          tmem_wait_ld32(s0);
+          tmem_ld32(t_s + 32, s1);
+          mx = max32(s0, mx);
+          exp32<F16>(s0, c, z, x, l2);
+          tmem_wait_ld32(s1);
+          if (both) tmem_ld32(t_s + 64, s0);
+          mx = max32(s1, mx);
+          exp32<F16>(s1, c, z, x + 16, l2);
+          if (both) {
+            tmem_wait_ld32(s0);
+            tmem_ld32(t_s + 96, s1);
+            mx = max32(s0, mx);
+            exp32<F16>(s0, c, z, x + 32, l2);
+            tmem_wait_ld32(s1);
+            mx = max32(s1, mx);
+            exp32<F16>(s1, c, z, x + 48, l2);
           }
-          const float mx = max32(s1, max32(s0, m));
-          if (__any_sync(0xffffffffu, (mx - m) * c > 8.f)) {
-            // the product into O before these scores' own: of this block's first half, or
-            // of the block before
-            if (j > 0 || hf == 1) {
-              const unsigned last = hf ? b : b - 1;
-              ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_half[w][last & 1][hf ^ 1]), (last >> 1) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+          if (!__any_sync(0xffffffffu, (mx - m) * c > 8.f)) break;
+          const float f = m == -INFINITY ? 0.f : ex2((m - mx) * c);
+          l *= f;
+          if (j > 0) {
+            // the product of the block before: with two places it was issued before these
+            // scores; with three its block of V is free once both have it
+            if (NB == 3) {
+              const unsigned last = b - 1;
+              ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_empty[S::kK + last % S::kV]), (last / S::kV) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
               tc_fence_after();
             }
-            const float f = m == -INFINITY ? 0.f : ex2((m - mx) * c);
-            l *= f;
-            if (ok && (j > 0 || hf == 1)) {
+            if (ok) {
 #pragma unroll 1
               for (int q = 0; q < D; q += 16) {
                 float o[16];
@@ -663,21 +707,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
                 tmem_st16(t_o + q, y);
               }
             }
-            m = mx;
           }
-          // (rounded up: the largest p stays within its bound however large the scores are)
-          const float z = (m == -INFINITY ? 0.f : __fmul_ru(m, c)) - kBias;
-          float2 l2 = make_float2(0.f, 0.f);
-          uint32_t x[16];
-          exp32<F16>(s0, c, z, x, l2);
-          tmem_st16(t_s + 32 * hf, x);
-          exp32<F16>(s1, c, z, x, l2);
-          tmem_st16(t_s + 32 * hf + 16, x);
-          l += l2.x + l2.y;
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(smem_u32(&s_pready[w][b & 1][hf]));
+          m = mx;
         }
+        l += l2.x + l2.y;
+        tmem_st16(t_s, x);
+        tmem_st16(t_s + 16, x + 16);
+        if (both) {
+          tmem_st16(t_s + 32, x + 32);
+          tmem_st16(t_s + 48, x + 48);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&s_pready[w][b & 1]));
       }
       // ---- output: after the last product of this warpgroup.  Its next product into O needs
       // its next P, which comes after these loads.
