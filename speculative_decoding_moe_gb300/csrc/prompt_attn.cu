@@ -55,7 +55,7 @@ namespace {
 constexpr int kKeys = 128;   // of a block
 constexpr int kTile = 256;   // rows of a tile
 constexpr int kThreads = 384;
-constexpr int kOver = 5;     // blocks' worth of time that a tile costs at least
+constexpr int kOver = 3;     // blocks' worth of time that a tile costs at least
 constexpr int kWholeKeys = 1024;  // tiles are cut where a sequence may have more keys
 
 template <int D>
