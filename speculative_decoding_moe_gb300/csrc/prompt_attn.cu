@@ -56,7 +56,7 @@ constexpr int kKeys = 128;   // of a block
 constexpr int kTile = 256;   // rows of a tile
 constexpr int kThreads = 384;
 constexpr int kOver = 3;     // blocks' worth of time that a tile costs at least
-constexpr int kWholeKeys = 1024;  // tiles are cut where a sequence may have more keys
+constexpr int kWholeKeys = 1536;  // tiles are cut where a sequence may have more keys
 
 template <int D>
 struct PromptShape {

@@ -78,7 +78,7 @@ def test_lengths(dfv, rows, keys, heads, kv, dim, dtype):
     Case(rows, keys, heads, kv, dim, dtype, seed=len(rows) + heads).check(dfv)
 
 
-@pytest.mark.parametrize("most", [1024, 1025])
+@pytest.mark.parametrize("most", [1536, 1537])
 def test_ranges_that_end_at_tiles_or_cut_them(dfv, most):
     """The same lengths as a call that may have more keys (cut and joined) and as one that may not."""
     for rows in ([200, 3, 900], [1000], [64] * 40):
