@@ -53,10 +53,10 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Scores of a block: D[tmem] = A B^T over D elements, A of 256 rows and B of 128 in blocks
-// of 64 elements.  One elected lane for all of it: an elect.sync an MMA took about
-// as long as the MMA.
-template <int D>
+// Scores of a block: D[tmem] = A B^T over D elements, in blocks of 64: A's AROWS rows, B's
+// 128 rows each.  One elected lane for all of it: an elect.sync an MMA took about as
+// long as the MMA.
+template <int D, int AROWS>
 __device__ __forceinline__ void tc_scores(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc) {
   if (D == 128)
     asm volatile(
@@ -65,12 +65,12 @@ __device__ __forceinline__ void tc_scores(uint32_t d_tmem, uint64_t adesc, uint6
       " add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
       " add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
       " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
-      " add.s64 a, %1, 2048;\n add.s64 b, %2, 1024;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
-      " add.s64 a, %1, 2050;\n add.s64 b, %2, 1026;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
-      " add.s64 a, %1, 2052;\n add.s64 b, %2, 1028;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
-      " add.s64 a, %1, 2054;\n add.s64 b, %2, 1030;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
+      " add.s64 a, %1, %4;\n add.s64 b, %2, 1024;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
+      " add.s64 a, %1, %5;\n add.s64 b, %2, 1026;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
+      " add.s64 a, %1, %6;\n add.s64 b, %2, 1028;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
+      " add.s64 a, %1, %7;\n add.s64 b, %2, 1030;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, yes;\n"
       "}"
-      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc)
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "n"(AROWS * 8), "n"(AROWS * 8 + 2), "n"(AROWS * 8 + 4), "n"(AROWS * 8 + 6)
       : "memory");
   else
     asm volatile(
@@ -120,6 +120,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *r) {
       : DFV_R8(r, 0), DFV_R8(r, 8), DFV_R8(r, 16), DFV_R8(r, 24)
       : "r"(addr));
 }
+// 16 columns, the caller waits
+__device__ __forceinline__ void tmem_ld16_async(uint32_t addr, float *r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : DFV_R8(r, 0), DFV_R8(r, 8)
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), DFV_I8(r, 0) : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
@@ -134,6 +143,9 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
 __device__ __forceinline__ void tmem_wait_ld32(float *r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : DFV_P8(r, 0), DFV_P8(r, 8), DFV_P8(r, 16), DFV_P8(r, 24)::"memory");
+}
+__device__ __forceinline__ void tmem_wait_ld16(float *r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : DFV_P8(r, 0), DFV_P8(r, 8)::"memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -157,18 +169,26 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
-__device__ __forceinline__ void less32(float *s, float x) {
-#pragma unroll
-  for (int q = 0; q < 32; q += 2) {
-    const float2 y = add2(make_float2(s[q], s[q + 1]), make_float2(-x, -x));
-    s[q] = y.x;
-    s[q + 1] = y.y;
-  }
-}
 __device__ __forceinline__ float max32(const float *s, float m) {
 #pragma unroll
   for (int q = 0; q < 32; q += 2) m = fmaxf(m, fmaxf(s[q], s[q + 1]));
   return m;
+}
+__device__ __forceinline__ float max16(const float *s, float m) {
+#pragma unroll
+  for (int q = 0; q < 16; q += 2) m = fmaxf(m, fmaxf(s[q], s[q + 1]));
+  return m;
+}
+// p of 16 scores less `from` as fp16 pairs, and their sum
+__device__ __forceinline__ void exp16(const float *s, float from, float c, float z, uint32_t *x, float2 &l) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float2 y = fma2(add2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(-from, -from)), c, -z);
+    y.x = ex2(y.x);
+    y.y = ex2(y.y);
+    l = add2(l, y);
+    x[e] = pack2<true>(y.x, y.y);
+  }
 }
 // p of 32 scores as 16-bit pairs, and their sum
 template <bool F16>

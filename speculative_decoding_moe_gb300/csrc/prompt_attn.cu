@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     // scores of the next block of warpgroup w, each block's for both in turn
     auto qk = [&](int w, bool last) {
       const uint32_t kaddr = ring + kst * S::kBlock, qb = q_addr + (uint32_t)w * 16384u, to = tmem + 128u * (NB == 2 ? (uint32_t)w : kpl);
-      tc_scores<D>(to, sdesc_k128(qb), sdesc_k128(kaddr), iq);
+      tc_scores<D, kTile>(to, sdesc_k128(qb), sdesc_k128(kaddr), iq);
       tc_commit_elect(smem_u32(&s_sfull[w][kb & 1]));
       if (++kpl == NB) kpl = 0;
       if (w) {  // the slot is free once both have read it, and the segment's Q

@@ -3,8 +3,8 @@
 //
 // The products and the two warpgroups are those of tree_attn_tc.cu (SINGLE: 128
 // rows, even and odd tiles; DUAL: 256 rows, each tile); between the copies and the
-// products, four warps widen the codes of a tile into fp16 in shared memory, a key
-// row a thread.
+// products, eight warps widen the codes of a tile into fp16 in shared memory, half a
+// key row a thread.
 //
 // Mathematics.  Key j is K_j 2^a_j, value j is V_j 2^b_j.  With A and B the largest a
 // and b of a tile of 128 keys, the products take K_j 2^(a_j - A) and V_j 2^(b_j - B) in
@@ -15,16 +15,15 @@
 // some x_j + B is more than 8 above it.  Precision of q and of the weights as in
 // tree_attn_codes.cu.
 //
-// A tile's scores are taken in halves of 64 keys: the maximum of a half is found from
-// registers before its exponentials, and its product starts while the other half
-// is in them.  Before the second half raises M it waits for the first half's product.
+// A tile's maximum is found in one pass over its scores, 16 at a time, and p in another:
+// with 20 warps a thread has 96 registers.
 //
 // What binds: shared memory.  Per tile of 128 keys of 128 elements the codes are
 // written (256 clocks at 128 bytes), read and written as fp16 (768), and read by the
 // products (768 a row tile), beside 512 clocks of products a row tile.
 //
 // Warps 0-3 and 4-7 are the two warpgroups, warp 8 issues the MMAs, warps 9-11 stream
-// codes with TMA, warps 12-15 widen.  Tensor memory: S0 S1 O0 O1 of 128 columns each;
+// codes with TMA, warps 12-19 widen.  Tensor memory: S0 S1 O0 O1 of 128 columns each;
 // P (16-bit pairs) over S.
 #include <cstdio>
 
@@ -35,7 +34,8 @@ namespace dfv {
 namespace {
 
 constexpr int kKeys = 128;
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
+constexpr int kWiden = 8;  // widening warps: two threads a key
 constexpr int kProducers = 3;
 constexpr float kBias = 6.f;
 constexpr int kTells = 16;  // tiles whose powers are kept: more than are between their widening and their scores
@@ -82,14 +82,15 @@ __device__ __forceinline__ uint32_t place(int row, int c) {
   return (uint32_t)(D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3));
 }
 
-// A key's codes in shared memory: zeroed where it is no node, else its NaN become zero;
-// whether there were any.
+// Half a key's codes in shared memory: zeroed where it is no node, else its NaN become
+// zero; whether there were any.
 template <int D>
-__device__ __noinline__ bool clean_key(uint32_t row, bool node) {
+__device__ __noinline__ bool clean_key(uint32_t row, int kt, int part, bool node) {
   bool nan = false;
 #pragma unroll 1
-  for (int c = 0; c < D / 16; ++c) {
-    uint4 x = lds128(row + 16u * c);
+  for (int c = part * (D / 32); c < (part + 1) * (D / 32); ++c) {
+    const uint32_t at = row + 16u * place<D>(kt, c);
+    uint4 x = lds128(at);
     uint32_t *w = &x.x;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -97,7 +98,7 @@ __device__ __noinline__ bool clean_key(uint32_t row, bool node) {
       nan = nan || z;
       w[e] = node ? w[e] & ~((z >> 7) * 255u) : 0u;
     }
-    sts128(row + 16u * c, x);
+    sts128(at, x);
   }
   return nan && node;
 }
@@ -109,14 +110,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
   extern __shared__ __align__(16) unsigned char sm_raw[];
   unsigned char *sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) unsigned long long s_full[S::kSlots], s_empty[S::kSlots], s_cfull[S::kCSlots], s_cempty[S::kCSlots],
-      s_sfull[2], s_pready[2][2], s_half[2], s_odone[2], s_qready, s_drain;
+      s_sfull[2], s_pready[2], s_odone[2], s_qready, s_drain;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ SchedStart s_start;
   __shared__ long long s_scan[kThreads / 32];
   __shared__ volatile int s_bad[4];    // of a segment, in turn: NaN was left out
   __shared__ volatile int2 s_tell[kTells];  // A and B of a tile
-  __shared__ uint8_t s_below[4][kKeys];  // how far a key's b is below B, of tiles whose V is to come
+  __shared__ uint8_t s_below[4][2][kKeys];  // how far a key's b is below B, of tiles whose V is to come
   __shared__ __align__(16) unsigned char s_power[S::kCSlots * 2 * kKeys];  // of K's slots: a and b of the tile's keys
   __shared__ float s_crow[256];        // c times the power that a row of q was divided by
   const TreeAttnParams &p = L.p;
@@ -127,18 +128,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
     s_abort = 0;
     for (int s = 0; s < 4; ++s) s_bad[s] = 0;
     for (int s = 0; s < S::kSlots; ++s) {
-      mbar_init(smem_u32(&s_full[s]), 4);
+      mbar_init(smem_u32(&s_full[s]), kWiden);
       mbar_init(smem_u32(&s_empty[s]), 1);
     }
     for (int s = 0; s < S::kCSlots; ++s) {
       mbar_init(smem_u32(&s_cfull[s]), kProducers + 64);  // the codes' boxes, and the powers' lanes
-      mbar_init(smem_u32(&s_cempty[s]), 4);
+      mbar_init(smem_u32(&s_cempty[s]), kWiden);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(smem_u32(&s_sfull[w]), 1);
-      mbar_init(smem_u32(&s_pready[w][0]), 128);
-      mbar_init(smem_u32(&s_pready[w][1]), 128);
-      mbar_init(smem_u32(&s_half[w]), 1);
+      mbar_init(smem_u32(&s_pready[w]), 128);
       mbar_init(smem_u32(&s_odone[w]), 1);
     }
     mbar_init(smem_u32(&s_qready), 256);
@@ -225,11 +224,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
     for (int j = issued - S::kCSlots < 0 ? 0 : issued - S::kCSlots; j < issued; ++j)
       if (!mbar_wait(smem_u32(&s_cfull[j % S::kCSlots]), (j / S::kCSlots) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never)) break;
   } else if (warp >= 12) {
-    // ---------------------------------------------------------------- widening: a key row a thread
+    // ---------------------------------------------------------------- widening: half a key row a thread
     // Items in the order of the rings: LA tiles' K, then V and the next K in turn.  (Short
     // loops: with the chunks of two items unrolled the warps waited for instructions a third
     // of their time.)
-    const int kt = tid - 384;
+    const int kt = (tid - 384) & 127, part = (tid - 384) >> 7;
     int st = 0, ph = 0, cst = 0, cph = 0, seg = 0;
     unsigned tiles = 0;  // of the segments before
     bool ok = true;
@@ -270,33 +269,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
           const int a = __reduce_max_sync(0xffffffffu, max(m & 255u, m >> 8 & 255u));
           const int b = __reduce_max_sync(0xffffffffu, max(m2 & 255u, m2 >> 8 & 255u));
           below = max(0, a - pw[kt]);
-          s_below[tile & 3][kt] = (uint8_t)max(0, b - pw[kKeys + kt]);
-          if (kt == 0) {
+          s_below[tile & 3][part][kt] = (uint8_t)max(0, b - pw[kKeys + kt]);
+          if (tid == 384) {
             s_tell[tile % kTells].x = a;
             s_tell[tile % kTells].y = b;
           }
         } else {
-          below = s_below[tile & 3][kt];
+          below = s_below[tile & 3][part][kt];
           const int jn = (wk.t0 + t) * kKeys + kt - wk.v.len;  // this key's node
-          if (jn >= 0 && clean_key<D>(from, jn < wk.nodes)) s_bad[seg & 3] = 1;
+          if (jn >= 0 && clean_key<D>(from, kt, part, jn < wk.nodes)) s_bad[seg & 3] = 1;
         }
         const __half2 m = half_power(below);
         ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_empty[st]), ph ^ 1, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
         if (!ok) break;
         const uint32_t to = ring + (uint32_t)st * S::kTile + (uint32_t)(kt * 128);
-#pragma unroll 1
-        for (int c0 = 0; c0 < D / 16; c0 += 4) {
-          uint4 x[4];
+        // this thread's chunks: D / 32 of them, within one block of 64 elements (D = 128)
+        uint4 x[D / 32];
+        const int c0 = part * (D / 32);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) x[c] = lds128(from + 16u * place<D>(kt, c0 + c));
+        for (int c = 0; c < D / 32; ++c) x[c] = lds128(from + 16u * place<D>(kt, c0 + c));
+        const uint32_t half = to + (uint32_t)((2 * c0) >> 3) * 16384u;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint4 lo, hi;
-            widen16(x[c], m, lo, hi);
-            const uint32_t half = to + (uint32_t)(c0 >> 2) * 16384u;
-            sts128(half + (((2 * c) ^ (kt & 7)) << 4), lo);
-            sts128(half + (((2 * c + 1) ^ (kt & 7)) << 4), hi);
-          }
+        for (int c = 0; c < D / 32; ++c) {
+          uint4 lo, hi;
+          widen16(x[c], m, lo, hi);
+          const int ch = 2 * (c0 + c) & 7;
+          sts128(half + ((ch ^ (kt & 7)) << 4), lo);
+          sts128(half + (((ch + 1) ^ (kt & 7)) << 4), hi);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -313,92 +312,98 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA issue
     int st = 0, ph = 0, seg = 0;
-    unsigned np[2] = {0u, 0u};  // tiles of each warpgroup whose P was awaited
+    unsigned np0 = 0u, np1 = 0u;  // phases of the warpgroups' P that were awaited
     bool ok = true;
     const uint32_t iq = idesc_16<true>(kKeys, false), iv = idesc_16<true>(D, true);
-    auto full = [&]() {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_full[st]), ph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+    auto wait = [&](unsigned long long &bar, unsigned phase) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&bar), phase, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+    };
+    // A step's waits come together: P of warpgroup w, this slot (V), and `next` slots further
+    // K (0: none).  Each costs about as long as the tensor core's queue lasts.
+    auto ready = [&](int w, bool v, int next) {
+      int kst = st + next, kph = ph;
+      if (kst >= S::kSlots) { kst -= S::kSlots; kph ^= 1; }
+      const unsigned np = w ? np1 : np0;
+      bool r = mbar_try_wait(smem_u32(&s_pready[w]), np);
+      if (v) r = mbar_try_wait(smem_u32(&s_full[st]), ph) && r;
+      if (next) r = mbar_try_wait(smem_u32(&s_full[kst]), kph) && r;
+      if (!__all_sync(0xffffffffu, r)) {
+        if (v) wait(s_full[st], ph);
+        if (next) wait(s_full[kst], kph);
+        wait(s_pready[w], np);
+      }
       tc_fence_after();
+      if (w)
+        np1 ^= 1u;
+      else
+        np0 ^= 1u;
     };
     auto done = [&]() {  // the slot is free once the MMAs issued so far have read it
       tc_commit_elect(smem_u32(&s_empty[st]));
       if (++st == S::kSlots) { st = 0; ph ^= 1; }
     };
-    auto qk = [&](int w) {
-      const uint32_t kb = ring + (uint32_t)st * S::kTile, qb = q_addr + (DUAL ? (uint32_t)w * 128u * D * 2u : 0u);
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        tc_mma_ss(tmem + (uint32_t)w * 128u, sdesc_k128(qb + (ks >> 2) * 16384) + (uint64_t)(2 * (ks & 3)),
-                  sdesc_k128(kb + (ks >> 2) * 16384) + (uint64_t)(2 * (ks & 3)), iq, ks > 0 ? 1u : 0u);
+    auto qk = [&](int w, int slot) {
+      tc_scores<D, 128>(tmem + (uint32_t)w * 128u, sdesc_k128(q_addr + (DUAL ? (uint32_t)w * 128u * D * 2u : 0u)), sdesc_k128(ring + (uint32_t)slot * S::kTile), iq);
       tc_commit_elect(smem_u32(&s_sfull[w]));
     };
     auto pv = [&](int w, bool first, bool last) {
-      const uint32_t vb = ring + (uint32_t)st * S::kTile;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_pready[w][hf]), np[w] & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-        if (!ok) return;
-        tc_fence_after();
-#pragma unroll
-        for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)
-          tc_mma_ts(tmem + 256u + (uint32_t)w * 128u, tmem + (uint32_t)w * 128u + (uint32_t)ks * 8u,
-                    sdesc_mn128(vb + (uint32_t)ks * 2048u), iv, (first && ks == 0) ? 0u : 1u);
-        if (hf == 0) tc_commit_elect(smem_u32(&s_half[w]));
-      }
-      ++np[w];
+      tc_values(tmem + 256u + (uint32_t)w * 128u, tmem + (uint32_t)w * 128u, sdesc_mn128(ring + (uint32_t)st * S::kTile), iv, first ? 0u : 1u);
       if (last) tc_commit_elect(smem_u32(&s_odone[w]));
     };
     while (ok && wk.next()) {
       if (row0 >= wk.v.n * p.G) continue;
       const int n = wk.t1 - wk.t0;
-      ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_qready), seg & 1, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+      wait(s_qready, seg & 1);
       ++seg;
+      wait(s_full[st], ph);
       tc_fence_after();
+      if (!ok) break;
       if (DUAL) {
-        full();
-        if (!ok) break;
-        qk(0);
-        qk(1);
+        qk(0, st);
+        qk(1, st);
         done();
-        for (int j = 0; j < n && ok; ++j) {
+        for (int j = 0; j < n; ++j) {
           // V_j, then K_j+1; each warpgroup's next scores right after its own product
-          full();
+          const bool more = j + 1 < n;
+          ready(0, true, more ? 1 : 0);
           if (!ok) break;
-          pv(0, j == 0, j == n - 1);
+          pv(0, j == 0, !more);
+          if (more) qk(0, st + 1 == S::kSlots ? 0 : st + 1);
+          ready(1, false, 0);
           if (!ok) break;
-          if (j + 1 < n) {
-            const int sv = st, pv_ = ph;
-            if (++st == S::kSlots) { st = 0; ph ^= 1; }
-            full();
-            if (!ok) break;
-            qk(0);
-            st = sv; ph = pv_;
-          }
-          pv(1, j == 0, j == n - 1);
-          if (!ok) break;
+          pv(1, j == 0, !more);
           done();  // V_j
-          if (j + 1 < n) {
-            qk(1);
+          if (more) {
+            qk(1, st);
             done();  // K_j+1
           }
         }
       } else {
-        for (int k = 0; k < LA && k < n && ok; ++k) {
-          full();
+        qk(0, st);
+        done();
+        if (n > 1) {
+          wait(s_full[st], ph);
+          tc_fence_after();
           if (!ok) break;
-          qk(k);
+          qk(1, st);
           done();
         }
-        for (int j = 0; j < n && ok; ++j) {
-          full();
+        for (int j = 0; j < n; j += 2) {
+          ready(0, true, j + 2 < n ? 1 : 0);
           if (!ok) break;
-          pv(j & 1, j < 2, j + 2 >= n);
-          if (!ok) break;
+          pv(0, j == 0, j + 2 >= n);
           done();
-          if (j + LA < n) {
-            full();
-            if (!ok) break;
-            qk(j & 1);
+          if (j + 2 < n) {
+            qk(0, st);
+            done();
+          }
+          if (j + 1 == n) break;
+          ready(1, true, j + 3 < n ? 1 : 0);
+          if (!ok) break;
+          pv(1, j == 0, j + 3 >= n);
+          done();
+          if (j + 3 < n) {
+            qk(1, st);
             done();
           }
         }
@@ -480,52 +485,64 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
         const float c = fminf(fmaxf(crow * exp_value((uint32_t)s_tell[tell].x), 0x1p-120f), 0x1p120f);
         const int eb = min(max(s_tell[tell].y, 1), 253);
         const float B = (float)(eb - 127), back = exp_value((uint32_t)(254 - eb));
+        float high = -INFINITY;
+        {
+          float s0[16], s1[16];
+          tmem_ld16_async(t_s, s0);
 #pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          float s0[32], s1[32];
-          tmem_ld32(t_s + 64 * hf, s0);
-          tmem_ld32(t_s + 64 * hf + 32, s1);
-          tmem_wait_ld32(s0);
-          tmem_wait_ld32(s1);
-          const float high = max32(s1, max32(s0, -INFINITY)), top = fmaf(high, c, B);
-          if (__any_sync(0xffffffffu, top - 8.f > m)) {
-            // products into O before these scores: those of the tiles before were
-            // complete when the scores were; the first half's own is waited for
-            if (hf == 1) {
-              ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_half[w]), (nt - 1u) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-              tc_fence_after();
-            }
-            const float mx = fmaxf(m, top), f = m == -INFINITY ? 0.f : ex2(m - mx);
-            l *= f;
-            if (ok && (started || hf == 1)) {
-#pragma unroll 1
-              for (int q = 0; q < D; q += 16) {
-                float o[16];
-                tmem_ld16(t_o + q, o);
-                uint32_t y[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(o[e] * f);
-                tmem_st16(t_o + q, y);
-              }
-            }
-            m = mx;
+          for (int q = 0; q < kKeys; q += 32) {
+            tmem_wait_ld16(s0);
+            tmem_ld16_async(t_s + q + 16, s1);
+            high = max16(s0, high);
+            tmem_wait_ld16(s1);
+            tmem_ld16_async(t_s + (q + 32) % kKeys, s0);  // (the last one is the first again)
+            high = max16(s1, high);
           }
-          // x + B - M by differences from the half's maximum: whatever the scores' size, the
+          tmem_wait_ld16(s0);
+        }
+        const float top = fmaf(high, c, B);
+        if (__any_sync(0xffffffffu, top - 8.f > m)) {
+          // the products into O were issued before these scores, and their barrier follows
+          // all that was issued before it
+          const float mx = fmaxf(m, top), f = m == -INFINITY ? 0.f : ex2(m - mx);
+          l *= f;
+          if (started) {
+#pragma unroll 1
+            for (int q = 0; q < D; q += 16) {
+              float o[16];
+              tmem_ld16(t_o + q, o);
+              uint32_t y[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(o[e] * f);
+              tmem_st16(t_o + q, y);
+            }
+          }
+          m = mx;
+        }
+        {
+          // x + B - M by differences from the tile's maximum: whatever the scores' size, the
           // exponents are 8 at most and right next to it
           const float from = high == -INFINITY ? 0.f : high, z = (high == -INFINITY ? 0.f : m - top) - kBias;
           float2 l2 = make_float2(0.f, 0.f);
-          uint32_t x[16];
-          less32(s0, from);
-          exp32<true>(s0, c, z, x, l2);
-          tmem_st16(t_s + 32 * hf, x);
-          less32(s1, from);
-          exp32<true>(s1, c, z, x, l2);
-          tmem_st16(t_s + 32 * hf + 16, x);
+          float s0[16], s1[16];
+          uint32_t x[8];
+          tmem_ld16_async(t_s, s0);
+#pragma unroll 1
+          for (int q = 0; q < kKeys; q += 32) {
+            tmem_wait_ld16(s0);
+            tmem_ld16_async(t_s + q + 16, s1);
+            exp16(s0, from, c, z, x, l2);
+            tmem_wait_ld16(s1);
+            if (q + 32 < kKeys) tmem_ld16_async(t_s + q + 32, s0);
+            tmem_st8(t_s + q / 2, x);  // over scores that have been read
+            exp16(s1, from, c, z, x, l2);
+            tmem_st8(t_s + q / 2 + 8, x);
+          }
           l = fmaf(l2.x + l2.y, back, l);
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(smem_u32(&s_pready[w][hf]));
         }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&s_pready[w]));
         started = true;
       }
       tiles += (unsigned)n;
@@ -564,31 +581,31 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
       char *out = p.o + 2 * (row * p.o_row + head * p.o_head);
       float4 *part = reinterpret_cast<float4 *>(L.part_o) + (size_t)slot * (D / 4) * L.rows + rr;
 #pragma unroll 1
-      for (int q = c0; q < c1 && ok; q += 32) {
-        float o[32];
-        tmem_ld32(lane_base + 256u + (DUAL ? (uint32_t)w * 128u : 0u) + q, o);
+      for (int q = c0; q < c1 && ok; q += 16) {
+        float o[16];
+        tmem_ld16_async(lane_base + 256u + (DUAL ? (uint32_t)w * 128u : 0u) + q, o);
         if (!DUAL && n > 1) {
-          float o1[32];
-          tmem_ld32(lane_base + 384u + q, o1);
-          tmem_wait_ld32(o);
-          tmem_wait_ld32(o1);
+          float o1[16];
+          tmem_ld16_async(lane_base + 384u + q, o1);
+          tmem_wait_ld16(o);
+          tmem_wait_ld16(o1);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
+          for (int e = 0; e < 16; ++e) o[e] = o[e] * f0 + o1[e] * f1;
         } else {
-          tmem_wait_ld32(o);
+          tmem_wait_ld16(o);
         }
         if (r >= R) continue;
         if (whole) {
-          uint32_t x[16];
+          uint32_t x[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = pack2<false>(o[2 * e] * inv, o[2 * e + 1] * inv);
+          for (int e = 0; e < 8; ++e) x[e] = pack2<false>(o[2 * e] * inv, o[2 * e + 1] * inv);
           uint4 *to = reinterpret_cast<uint4 *>(out + 2 * q);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) to[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+          to[0] = make_uint4(x[0], x[1], x[2], x[3]);
+          to[1] = make_uint4(x[4], x[5], x[6], x[7]);
         } else {
           float4 *to = part + (size_t)(q / 4) * L.rows;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) to[(size_t)e * L.rows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int e = 0; e < 4; ++e) to[(size_t)e * L.rows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
       if (r < R && ok && c0 == 0) {
