@@ -83,10 +83,12 @@ __device__ __forceinline__ void tc_scores(uint32_t d_tmem, uint64_t adesc, uint6
       ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc)
       : "memory");
 }
-// D[tmem] (+)= A[tmem] B over 128 keys: A 8 columns further and B 16 rows of 128 bytes further
-// an MMA
+// D[tmem] (+)= A[tmem] B over KEYS = 64 or 128 keys: A 8 columns further and B 16 rows of 128
+// bytes further an MMA
+template <int KEYS>
 __device__ __forceinline__ void tc_values(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
+  if (KEYS == 128)
+    asm volatile(
       "{\n .reg .pred p, yes, q;\n .reg .b64 b;\n .reg .b32 a;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 yes, %3, %3;\n elect.sync _|q, 0xffffffff;\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
       " add.s64 b, %2, 128;\n add.u32 a, %1, 8;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
@@ -96,6 +98,16 @@ __device__ __forceinline__ void tc_values(uint32_t d_tmem, uint32_t a_tmem, uint
       " add.s64 b, %2, 640;\n add.u32 a, %1, 40;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
       " add.s64 b, %2, 768;\n add.u32 a, %1, 48;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
       " add.s64 b, %2, 896;\n add.u32 a, %1, 56;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
+      "}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+  else
+    asm volatile(
+      "{\n .reg .pred p, yes, q;\n .reg .b64 b;\n .reg .b32 a;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 yes, %3, %3;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " add.s64 b, %2, 128;\n add.u32 a, %1, 8;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
+      " add.s64 b, %2, 256;\n add.u32 a, %1, 16;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
+      " add.s64 b, %2, 384;\n add.u32 a, %1, 24;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, yes;\n"
       "}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
@@ -206,9 +218,9 @@ __device__ __forceinline__ void exp32(const float *s, float c, float z, uint32_t
 // Scores of a tile whose first key is node j0 (below 0: committed): what the row
 // does not see becomes -inf, in place.  A short loop: it runs once per sequence, and
 // unrolled its instructions took longer to fetch than to execute.
-__device__ __forceinline__ void mask_tile(uint32_t t_s, int j0, uint64_t mask) {
+__device__ __forceinline__ void mask_tile(uint32_t t_s, int j0, uint64_t mask, int keys = 128) {
 #pragma unroll 1
-  for (int q = 0; q < 128; q += 16) {
+  for (int q = 0; q < keys; q += 16) {
     const int j = j0 + q;  // node of the first of 16 keys
     if (j + 16 <= 0) continue;
     uint32_t sees;

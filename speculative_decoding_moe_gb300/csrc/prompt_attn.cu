@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     auto pv = [&](int w, bool first, bool last, int steps) {
       const uint32_t vaddr = ring + (S::kK + vst) * S::kBlock, from = tmem + 128u * (NB == 2 ? (uint32_t)w : vpl), to = tmem + S::kO + (uint32_t)(w * D);
       if (steps == kKeys / 16) {
-        tc_values(to, from, sdesc_mn128(vaddr), iv, first ? 0u : 1u);
+        tc_values<128>(to, from, sdesc_mn128(vaddr), iv, first ? 0u : 1u);
       } else {  // keys that no row of the tile sees, 16 at a time, take part in no product
 #pragma unroll 1
         for (int ks = 0; ks < steps; ++ks)

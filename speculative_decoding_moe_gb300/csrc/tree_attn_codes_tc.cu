@@ -1,8 +1,13 @@
 // tree_attn_codes_tc.cu -- tree attention over a cache in e4m3 codes with many rows
 // per kv head, on the fifth-generation tensor cores.
 //
-// The products and the two warpgroups are those of tree_attn_tc.cu (SINGLE: 128
-// rows, even and odd tiles; DUAL: 256 rows, each tile); between the copies and the
+// As in tree_attn_tc.cu a CTA takes 128 rows (SINGLE) or 256 rows (DUAL) of one kv
+// head and streams the keys in tiles of 128.  DUAL: a warpgroup takes 128 rows.
+// SINGLE: a warpgroup takes the first or the second 64 keys of every tile, with its own
+// (M, l, O); scores take turns in two places, so that the next tile's are ready while
+// one is in its exponentials; the two states are joined at the end (with even and odd
+// tiles for the warpgroups, each waited for a tile's whole chain: 97 us where this
+// takes XX, 32 x 16 nodes).  Between the copies and the
 // products, eight warps widen the codes of a tile into fp16 in shared memory, half a
 // key row a thread.
 //
@@ -110,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
   extern __shared__ __align__(16) unsigned char sm_raw[];
   unsigned char *sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) unsigned long long s_full[S::kSlots], s_empty[S::kSlots], s_cfull[S::kCSlots], s_cempty[S::kCSlots],
-      s_sfull[2], s_pready[2], s_odone[2], s_qready, s_drain;
+      s_sfull[2], s_pready[2][2], s_pvdone[2], s_odone[2], s_qready, s_drain;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ SchedStart s_start;
@@ -137,7 +142,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(smem_u32(&s_sfull[w]), 1);
-      mbar_init(smem_u32(&s_pready[w]), 128);
+      mbar_init(smem_u32(&s_pready[w][0]), 128);
+      mbar_init(smem_u32(&s_pready[w][1]), 128);
+      mbar_init(smem_u32(&s_pvdone[w]), 1);
       mbar_init(smem_u32(&s_odone[w]), 1);
     }
     mbar_init(smem_u32(&s_qready), 256);
@@ -312,44 +319,38 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA issue
     int st = 0, ph = 0, seg = 0;
-    unsigned np0 = 0u, np1 = 0u;  // phases of the warpgroups' P that were awaited
     bool ok = true;
     const uint32_t iq = idesc_16<true>(kKeys, false), iv = idesc_16<true>(D, true);
     auto wait = [&](unsigned long long &bar, unsigned phase) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&bar), phase, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
     };
-    // A step's waits come together: P of warpgroup w, this slot (V), and `next` slots further
-    // K (0: none).  Each costs about as long as the tensor core's queue lasts.
-    auto ready = [&](int w, bool v, int next) {
-      int kst = st + next, kph = ph;
-      if (kst >= S::kSlots) { kst -= S::kSlots; kph ^= 1; }
-      const unsigned np = w ? np1 : np0;
-      bool r = mbar_try_wait(smem_u32(&s_pready[w]), np);
+    // A step's waits come together: P on `a` (and `b`), this slot (V), and in the next one K.
+    // Each costs about as long as the tensor core's queue lasts.
+    auto ready = [&](unsigned long long &a, unsigned long long *b, unsigned phase, bool v, bool k) {
+      int kst = st + 1, kph = ph;
+      if (kst == S::kSlots) { kst = 0; kph ^= 1; }
+      bool r = mbar_try_wait(smem_u32(&a), phase);
+      if (b) r = mbar_try_wait(smem_u32(b), phase) && r;
       if (v) r = mbar_try_wait(smem_u32(&s_full[st]), ph) && r;
-      if (next) r = mbar_try_wait(smem_u32(&s_full[kst]), kph) && r;
+      if (k) r = mbar_try_wait(smem_u32(&s_full[kst]), kph) && r;
       if (!__all_sync(0xffffffffu, r)) {
         if (v) wait(s_full[st], ph);
-        if (next) wait(s_full[kst], kph);
-        wait(s_pready[w], np);
+        if (k) wait(s_full[kst], kph);
+        wait(a, phase);
+        if (b) wait(*b, phase);
       }
       tc_fence_after();
-      if (w)
-        np1 ^= 1u;
-      else
-        np0 ^= 1u;
     };
     auto done = [&]() {  // the slot is free once the MMAs issued so far have read it
       tc_commit_elect(smem_u32(&s_empty[st]));
       if (++st == S::kSlots) { st = 0; ph ^= 1; }
     };
-    auto qk = [&](int w, int slot) {
-      tc_scores<D, 128>(tmem + (uint32_t)w * 128u, sdesc_k128(q_addr + (DUAL ? (uint32_t)w * 128u * D * 2u : 0u)), sdesc_k128(ring + (uint32_t)slot * S::kTile), iq);
-      tc_commit_elect(smem_u32(&s_sfull[w]));
+    // place of scores `to`, and DUAL warpgroup `to`'s rows
+    auto qk = [&](int to, int slot) {
+      tc_scores<D, 128>(tmem + (uint32_t)to * 128u, sdesc_k128(q_addr + (DUAL ? (uint32_t)to * 128u * D * 2u : 0u)), sdesc_k128(ring + (uint32_t)slot * S::kTile), iq);
+      tc_commit_elect(smem_u32(&s_sfull[to]));
     };
-    auto pv = [&](int w, bool first, bool last) {
-      tc_values(tmem + 256u + (uint32_t)w * 128u, tmem + (uint32_t)w * 128u, sdesc_mn128(ring + (uint32_t)st * S::kTile), iv, first ? 0u : 1u);
-      if (last) tc_commit_elect(smem_u32(&s_odone[w]));
-    };
+    int place = 0, turn = 0;  // SINGLE: of the next product's P, and its barriers' phase; DUAL: the phase
     while (ok && wk.next()) {
       if (row0 >= wk.v.n * p.G) continue;
       const int n = wk.t1 - wk.t0;
@@ -359,17 +360,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
       tc_fence_after();
       if (!ok) break;
       if (DUAL) {
+        auto pv = [&](int w, bool first, bool last) {
+          tc_values<128>(tmem + 256u + (uint32_t)w * 128u, tmem + (uint32_t)w * 128u, sdesc_mn128(ring + (uint32_t)st * S::kTile), iv, first ? 0u : 1u);
+          if (last) tc_commit_elect(smem_u32(&s_odone[w]));
+        };
         qk(0, st);
         qk(1, st);
         done();
         for (int j = 0; j < n; ++j) {
           // V_j, then K_j+1; each warpgroup's next scores right after its own product
           const bool more = j + 1 < n;
-          ready(0, true, more ? 1 : 0);
+          ready(s_pready[0][0], nullptr, turn, true, more);
           if (!ok) break;
           pv(0, j == 0, !more);
           if (more) qk(0, st + 1 == S::kSlots ? 0 : st + 1);
-          ready(1, false, 0);
+          ready(s_pready[1][0], nullptr, turn, false, false);
           if (!ok) break;
           pv(1, j == 0, !more);
           done();  // V_j
@@ -377,35 +382,38 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
             qk(1, st);
             done();  // K_j+1
           }
+          turn ^= 1;
         }
       } else {
-        qk(0, st);
+        qk(place, st);
         done();
         if (n > 1) {
           wait(s_full[st], ph);
           tc_fence_after();
           if (!ok) break;
-          qk(1, st);
+          qk(place ^ 1, st);
           done();
         }
-        for (int j = 0; j < n; j += 2) {
-          ready(0, true, j + 2 < n ? 1 : 0);
+        for (int j = 0; j < n; ++j) {
+          // each warpgroup's 64 keys of V_j into its own O, then the scores of K_j+2
+          ready(s_pready[0][place], &s_pready[1][place], turn, true, j + 2 < n);
           if (!ok) break;
-          pv(0, j == 0, j + 2 >= n);
-          done();
+          const uint32_t from = tmem + (uint32_t)place * 128u;
+          const uint64_t vd = sdesc_mn128(ring + (uint32_t)st * S::kTile);
+          tc_values<64>(tmem + 256u, from, vd, iv, j ? 1u : 0u);
+          tc_values<64>(tmem + 384u, from + 64u, vd + 512u, iv, j ? 1u : 0u);
+          tc_commit_elect(smem_u32(&s_pvdone[place]));
+          if (j + 1 == n) {
+            tc_commit_elect(smem_u32(&s_odone[0]));
+            tc_commit_elect(smem_u32(&s_odone[1]));
+          }
+          done();  // V_j
           if (j + 2 < n) {
-            qk(0, st);
-            done();
+            qk(place, st);
+            done();  // K_j+2
           }
-          if (j + 1 == n) break;
-          ready(1, true, j + 3 < n ? 1 : 0);
-          if (!ok) break;
-          pv(1, j == 0, j + 3 >= n);
-          done();
-          if (j + 3 < n) {
-            qk(1, st);
-            done();
-          }
+          turn ^= place;
+          place ^= 1;
         }
       }
     }
@@ -417,7 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
     // ---------------------------------------------------------------- softmax and output
     const int w = warp >> 2, wt = tid & 127;  // warpgroup, and its thread = row of the tile
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t t_s = lane_base + (uint32_t)w * 128u, t_o = lane_base + 256u + (uint32_t)w * 128u;
+    const uint32_t t_o = lane_base + 256u + (uint32_t)w * 128u;
+    constexpr int kMine = DUAL ? kKeys : kKeys / 2;  // keys of a tile that the warpgroup takes
     unsigned nt = 0;     // tiles this warpgroup has taken
     unsigned outs = 0;   // segments it has put out
     unsigned tiles = 0, seg = 0;  // of the segments before
@@ -473,13 +482,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
       if (r < R) mask = wk.mask_of(r);
       float m = -INFINITY, l = 0.f;
       bool started = false;
-      for (int j = DUAL ? 0 : w; j < n; j += DUAL ? 1 : 2) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_sfull[w]), nt & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-        ++nt;
+      for (int j = 0; j < n; ++j) {
+        const unsigned T = nt++, place = T & 1;
+        const uint32_t t_s = lane_base + (DUAL ? (uint32_t)w * 128u : place * 128u + (uint32_t)w * 64u);
+        if (DUAL)
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_sfull[w]), T & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+        else
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_sfull[place]), (T >> 1) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
         if (!ok) continue;
         tc_fence_after();
-        const int j0 = (wk.t0 + j) * kKeys - wk.v.len;  // node number of the tile's first key
-        if (j0 + kKeys > 0) mask_tile(t_s, j0, mask);   // tree nodes or keys past the end in the tile
+        const int j0 = (wk.t0 + j) * kKeys + (DUAL ? 0 : 64 * w) - wk.v.len;  // node number of the first key
+        if (j0 + kMine > 0) mask_tile(t_s, j0, mask, kMine);  // tree nodes or keys past the end among them
         const unsigned tell = (tiles + (unsigned)j) % kTells;
         // in (0, infinity), so that -inf stays what it is
         const float c = fminf(fmaxf(crow * exp_value((uint32_t)s_tell[tell].x), 0x1p-120f), 0x1p120f);
@@ -490,23 +503,27 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
           float s0[16], s1[16];
           tmem_ld16_async(t_s, s0);
 #pragma unroll 1
-          for (int q = 0; q < kKeys; q += 32) {
+          for (int q = 0; q < kMine; q += 32) {
             tmem_wait_ld16(s0);
             tmem_ld16_async(t_s + q + 16, s1);
             high = max16(s0, high);
             tmem_wait_ld16(s1);
-            tmem_ld16_async(t_s + (q + 32) % kKeys, s0);  // (the last one is the first again)
+            tmem_ld16_async(t_s + (q + 32) % kMine, s0);  // (the last one is the first again)
             high = max16(s1, high);
           }
           tmem_wait_ld16(s0);
         }
         const float top = fmaf(high, c, B);
         if (__any_sync(0xffffffffu, top - 8.f > m)) {
-          // the products into O were issued before these scores, and their barrier follows
-          // all that was issued before it
+          // the product into O before: DUAL's was issued before these scores, and their
+          // barrier follows all that was issued before it
+          if (!DUAL && started) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_pvdone[place ^ 1]), ((T - 1) >> 1) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+            tc_fence_after();
+          }
           const float mx = fmaxf(m, top), f = m == -INFINITY ? 0.f : ex2(m - mx);
           l *= f;
-          if (started) {
+          if (started && ok) {
 #pragma unroll 1
             for (int q = 0; q < D; q += 16) {
               float o[16];
@@ -528,12 +545,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
           uint32_t x[8];
           tmem_ld16_async(t_s, s0);
 #pragma unroll 1
-          for (int q = 0; q < kKeys; q += 32) {
+          for (int q = 0; q < kMine; q += 32) {
             tmem_wait_ld16(s0);
             tmem_ld16_async(t_s + q + 16, s1);
             exp16(s0, from, c, z, x, l2);
             tmem_wait_ld16(s1);
-            if (q + 32 < kKeys) tmem_ld16_async(t_s + q + 32, s0);
+            if (q + 32 < kMine) tmem_ld16_async(t_s + q + 32, s0);
             tmem_st8(t_s + q / 2, x);  // over scores that have been read
             exp16(s1, from, c, z, x, l2);
             tmem_st8(t_s + q / 2 + 8, x);
@@ -542,21 +559,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(smem_u32(&s_pready[w]));
+        mbar_arrive(smem_u32(&s_pready[w][DUAL ? 0 : place]));
         started = true;
       }
       tiles += (unsigned)n;
       // ---- output: the last product of this warpgroup, then (SINGLE) both states
-      if (DUAL || w < n) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_odone[w]), outs & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-        ++outs;
-      }
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_odone[w]), outs & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+      ++outs;
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       float M = m, lsum = l, f0 = 1.f, f1 = 1.f;
       // all scores are done when either warpgroup's last product is: Q's place is free
       float2 *ml = reinterpret_cast<float2 *>(s_q);
-      if (!DUAL && started) ml[w * 128 + wt] = make_float2(m, l);
+      if (!DUAL) ml[w * 128 + wt] = make_float2(m, l);
       // SINGLE: each warpgroup waited for its own products and reads both outputs, so
       // what it learned about tensor memory goes through the barrier
       tc_fence_before();
@@ -564,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
       tc_fence_after();
       if (!DUAL) {
         const float2 a = ml[wt];
-        const float2 b = n > 1 ? ml[128 + wt] : make_float2(-INFINITY, 0.f);
+        const float2 b = ml[128 + wt];
         M = fmaxf(a.x, b.x);
         // a state without keys adds its zeros (or NaN of a NaN query)
         f0 = a.x == -INFINITY ? 1.f : ex2(a.x - M);
@@ -584,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
       for (int q = c0; q < c1 && ok; q += 16) {
         float o[16];
         tmem_ld16_async(lane_base + 256u + (DUAL ? (uint32_t)w * 128u : 0u) + q, o);
-        if (!DUAL && n > 1) {
+        if (!DUAL) {
           float o1[16];
           tmem_ld16_async(lane_base + 384u + q, o1);
           tmem_wait_ld16(o);
