@@ -8,8 +8,9 @@
 // one is in its exponentials; the two states are joined at the end (with even and odd
 // tiles for the warpgroups, each waited for a tile's whole chain: 97 us where this
 // takes XX, 32 x 16 nodes).  Between the copies and the
-// products, eight warps widen the codes of a tile into fp16 in shared memory, half a
-// key row a thread.
+// products, four warps widen the codes of K and four those of V into fp16 in shared
+// memory, a key row a thread, each in rings of their own (eight warps on every tile of
+// either in turn took a third longer: a tile is bound by its latency).
 //
 // Mathematics.  Key j is K_j 2^a_j, value j is V_j 2^b_j.  With A and B the largest a
 // and b of a tile of 128 keys, the products take K_j 2^(a_j - A) and V_j 2^(b_j - B) in
@@ -28,7 +29,7 @@
 // products (768 a row tile), beside 512 clocks of products a row tile.
 //
 // Warps 0-3 and 4-7 are the two warpgroups, warp 8 issues the MMAs, warps 9-11 stream
-// codes with TMA, warps 12-19 widen.  Tensor memory: S0 S1 O0 O1 of 128 columns each;
+// codes with TMA, warps 12-15 widen K and 16-19 V.  Tensor memory: S0 S1 O0 O1 of 128 columns each;
 // P (16-bit pairs) over S.
 #include <cstdio>
 
@@ -40,7 +41,7 @@ namespace {
 
 constexpr int kKeys = 128;
 constexpr int kThreads = 640;
-constexpr int kWiden = 8;  // widening warps: two threads a key
+constexpr int kWiden = 4;  // warps that widen K, and that widen V
 constexpr int kProducers = 3;
 constexpr float kBias = 6.f;
 constexpr int kTells = 16;  // tiles whose powers are kept: more than are between their widening and their scores
@@ -49,8 +50,9 @@ template <int D, bool DUAL>
 struct CodeTcShape {
   static constexpr uint32_t kCodes = kKeys * D;      // a K or V tile in codes
   static constexpr uint32_t kTile = kKeys * D * 2;   // and in fp16
-  static constexpr int kSlots = D == 64 ? 6 : 3;     // of fp16 tiles
-  static constexpr int kCSlots = D == 64 ? 8 : DUAL ? 3 : 5;  // of codes
+  static constexpr int kK = D == 64 ? 2 : 1, kV = D == 64 ? 3 : 2;  // fp16 tiles of K, and of V behind them
+  static constexpr int kCK = D == 64 ? 4 : DUAL ? 1 : 3, kCV = D == 64 ? 4 : 2;  // tiles of codes
+  static constexpr int kSlots = kK + kV, kCSlots = kCK + kCV;
   static constexpr int kOver = DUAL ? 5 : 2;         // tiles' worth of time that a pair costs at least
   static constexpr uint32_t kQ = (DUAL ? 2 : 1) * 128 * D * 2;
   static constexpr size_t kSmem = 1024 + kQ + (size_t)kSlots * kTile + (size_t)kCSlots * kCodes;
@@ -87,15 +89,14 @@ __device__ __forceinline__ uint32_t place(int row, int c) {
   return (uint32_t)(D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3));
 }
 
-// Half a key's codes in shared memory: zeroed where it is no node, else its NaN become
-// zero; whether there were any.
+// A key's codes in shared memory: zeroed where it is no node, else its NaN become zero;
+// whether there were any.
 template <int D>
-__device__ __noinline__ bool clean_key(uint32_t row, int kt, int part, bool node) {
+__device__ __noinline__ bool clean_key(uint32_t row, bool node) {
   bool nan = false;
 #pragma unroll 1
-  for (int c = part * (D / 32); c < (part + 1) * (D / 32); ++c) {
-    const uint32_t at = row + 16u * place<D>(kt, c);
-    uint4 x = lds128(at);
+  for (int c = 0; c < D / 16; ++c) {
+    uint4 x = lds128(row + 16u * c);
     uint32_t *w = &x.x;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -103,7 +104,7 @@ __device__ __noinline__ bool clean_key(uint32_t row, int kt, int part, bool node
       nan = nan || z;
       w[e] = node ? w[e] & ~((z >> 7) * 255u) : 0u;
     }
-    sts128(at, x);
+    sts128(row + 16u * c, x);
   }
   return nan && node;
 }
@@ -122,8 +123,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
   __shared__ long long s_scan[kThreads / 32];
   __shared__ volatile int s_bad[4];    // of a segment, in turn: NaN was left out
   __shared__ volatile int2 s_tell[kTells];  // A and B of a tile
-  __shared__ uint8_t s_below[4][2][kKeys];  // how far a key's b is below B, of tiles whose V is to come
-  __shared__ __align__(16) unsigned char s_power[S::kCSlots * 2 * kKeys];  // of K's slots: a and b of the tile's keys
+  __shared__ uint8_t s_below[8][kKeys];  // how far a key's b is below B, of tiles whose V is to come
+  __shared__ __align__(8) unsigned long long s_told[8];  // (K is widened up to four tiles before V) s_below and s_tell of a tile are there
+  __shared__ __align__(16) unsigned char s_power[S::kCK * 2 * kKeys];  // with K: a and b of the tile's keys
   __shared__ float s_crow[256];        // c times the power that a row of q was divided by
   const TreeAttnParams &p = L.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
       mbar_init(smem_u32(&s_empty[s]), 1);
     }
     for (int s = 0; s < S::kCSlots; ++s) {
-      mbar_init(smem_u32(&s_cfull[s]), kProducers + 64);  // the codes' boxes, and the powers' lanes
+      mbar_init(smem_u32(&s_cfull[s]), s < S::kCK ? kProducers + 64 : kProducers);  // boxes; with K, the powers' lanes
       mbar_init(smem_u32(&s_cempty[s]), kWiden);
     }
     for (int w = 0; w < 2; ++w) {
@@ -147,6 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
       mbar_init(smem_u32(&s_pvdone[w]), 1);
       mbar_init(smem_u32(&s_odone[w]), 1);
     }
+    for (int s = 0; s < 8; ++s) mbar_init(smem_u32(&s_told[s]), kWiden);
     mbar_init(smem_u32(&s_qready), 256);
     mbar_init(smem_u32(&s_drain), 1);
     mbar_init_fence();
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
   if (warp >= 9 && warp < 12) {
     // ---------------------------------------------------------------- producers: every third box of a tile each
     const int me = warp - 9;
-    int st = 0, ph = 0, issued = 0;
+    unsigned nk = 0, nv = 0;  // tiles of K and V so far
     bool ok = true;
     const int shift = p.c.page_shift, boxes = shift >= 7 ? 1 : kKeys >> shift, rows = kKeys / boxes;
     while (ok && wk.next()) {
@@ -178,9 +181,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
         const int at = (((wk.t0 + j) * kKeys) >> shift) + lane;
         return j < n && lane < boxes && at < pages ? table[at] : -1;
       };
-      auto load = [&](const CUtensorMap *map, int j, int pg) {
+      auto load = [&](bool isk, int j, int pg) {
+        const CUtensorMap *map = isk ? &L.tm_k : &L.tm_v;
+        const unsigned at = isk ? nk++ : nv++, st = isk ? at % S::kCK : S::kCK + at % S::kCV, ph = (isk ? at / S::kCK : at / S::kCV) & 1u;
         ok = ok && __all_sync(0xffffffffu,
-                              mbar_wait_fast(smem_u32(&s_cempty[st]), ph ^ 1, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
+                              mbar_wait_fast(smem_u32(&s_cempty[st]), ph ^ 1u, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
         if (!ok) return;
         const uint32_t fb = smem_u32(&s_cfull[st]), dst = codes + (uint32_t)st * S::kCodes;
         const int nb = min(boxes, pages - (((wk.t0 + j) * kKeys) >> shift)), mine = nb > me ? (nb - me + kProducers - 1) / kProducers : 0;
@@ -192,17 +197,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
         }
         __syncwarp();
         const int tok = ((wk.t0 + j) * kKeys) & ((1 << shift) - 1);  // 0 unless a page holds several tiles
-        if (me < 2) {  // with K: this lane's four keys' a (the first producer) or b
+        if (me < 2 && isk) {  // with K: this lane's four keys' a (the first producer) or b
           const int my = boxes == 1 ? 0 : (4 * lane) >> shift, page = __shfl_sync(0xffffffffu, pg, my & 31);
-          if (map == &L.tm_k && my < nb)
+          if (my < nb)
             cp_async4(smem_u32(s_power + (st * 2 + me) * kKeys + 4 * lane),
                       (me == 0 ? p.c.ke : p.c.ve) + exp_off(p.c, p.layer, page, wk.h, ((wk.t0 + j) * kKeys + 4 * lane) & ((1 << shift) - 1)));
           cp_async_arrive(fb);
         }
         for (int b = me; b < nb; b += kProducers)
           tma_kv(dst + (uint32_t)(b * rows * D), map, 0, tok, wk.h, __shfl_sync(0xffffffffu, pg, b), L.swap, fb);
-        ++issued;
-        if (++st == S::kCSlots) { st = 0; ph ^= 1; }
       };
       auto checked = [&](int pg, int j) {  // ids were fetched a tile or more before they are looked at
         const int at = (((wk.t0 + j) * kKeys) >> shift) + lane;
@@ -215,60 +218,45 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
 #pragma unroll
       for (int k = 0; k < LA; ++k) {
         pg[k] = checked(pg[k], k);
-        if (k < n) load(&L.tm_k, k, pg[k]);
+        if (k < n) load(true, k, pg[k]);
       }
       for (int j = 0; j < n && ok; ++j) {
-        load(&L.tm_v, j, pg[0]);
+        load(false, j, pg[0]);
         pg[LA] = checked(pg[LA], j + LA);
-        if (j + LA < n) load(&L.tm_k, j + LA, pg[LA]);
+        if (j + LA < n) load(true, j + LA, pg[LA]);
 #pragma unroll
         for (int k = 0; k < LA + 1; ++k) pg[k] = pg[k + 1];
         pg[LA + 1] = id(j + LA + 2);
       }
     }
-    // no copy may land after the CTA exits: wait for the last fill of every slot
+    // no copy may land after the CTA exits: wait for the last fill of every slot (after a
+    // wait gave up the last one was not made, and this wait gives up too)
     volatile int never = 0;
-    for (int j = issued - S::kCSlots < 0 ? 0 : issued - S::kCSlots; j < issued; ++j)
-      if (!mbar_wait(smem_u32(&s_cfull[j % S::kCSlots]), (j / S::kCSlots) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never)) break;
+    for (unsigned j = nk > S::kCK ? nk - S::kCK : 0; j < nk; ++j)
+      if (!mbar_wait(smem_u32(&s_cfull[j % S::kCK]), (j / S::kCK) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never)) break;
+    for (unsigned j = nv > S::kCV ? nv - S::kCV : 0; j < nv; ++j)
+      if (!mbar_wait(smem_u32(&s_cfull[S::kCK + j % S::kCV]), (j / S::kCV) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never)) break;
   } else if (warp >= 12) {
-    // ---------------------------------------------------------------- widening: half a key row a thread
-    // Items in the order of the rings: LA tiles' K, then V and the next K in turn.  (Short
-    // loops: with the chunks of two items unrolled the warps waited for instructions a third
-    // of their time.)
-    const int kt = (tid - 384) & 127, part = (tid - 384) >> 7;
-    int st = 0, ph = 0, cst = 0, cph = 0, seg = 0;
-    unsigned tiles = 0;  // of the segments before
+    // ---------------------------------------------------------------- widening: a key row a thread
+    // (Short loops: with the chunks of two tiles unrolled the warps waited for instructions
+    // a third of their time.)
+    const bool isv = warp >= 16;
+    const int kt = (tid - 384) & 127, c0 = isv ? S::kCK : 0, cn = isv ? S::kCV : S::kCK, f0 = isv ? S::kK : 0, fn = isv ? S::kV : S::kK;
+    int st = 0, ph = 0, cst = 0, cph = 0;
+    unsigned tile = 0, seg = 0;
     bool ok = true;
     while (ok && wk.next()) {
       if (row0 >= wk.v.n * p.G) continue;
-      const int n = wk.t1 - wk.t0, ahead = n < LA ? n : LA;
-      // item i: K of tile t (0), or V (1)
-      auto item = [&](int i, int &t) {
-        if (i < ahead) {
-          t = i;
-          return 0;
-        }
-        i -= ahead;
-        if (i < 2 * (n - ahead)) {
-          t = i & 1 ? (i >> 1) + ahead : i >> 1;
-          return 1 - (i & 1);
-        }
-        t = i - (n - ahead);
-        return 1;
-      };
 #pragma unroll 1
-      for (int i = 0; i < 2 * n && ok; ++i) {
-        int t;
-        const int isv = item(i, t);
-        ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_cfull[cst]), cph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+      for (int t = wk.t0; t < wk.t1 && ok; ++t, ++tile) {
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_cfull[c0 + cst]), cph, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
         if (!ok) break;
-        const uint32_t from = codes + (uint32_t)cst * S::kCodes + (uint32_t)(kt * D);
-        const unsigned tile = tiles + (unsigned)t;
+        const uint32_t from = codes + (uint32_t)(c0 + cst) * S::kCodes + (uint32_t)(kt * D);
         int below;
         if (!isv) {
-          // with K the powers of both tiles: their largest, and how far this key's are below
+          // the powers of the tile: their largest, and how far this key's are below
           const unsigned char *pw = s_power + cst * 2 * kKeys;
-          const int valid = wk.total - (wk.t0 + t) * kKeys - 4 * lane;  // of this lane's four keys
+          const int valid = wk.total - t * kKeys - 4 * lane;  // of this lane's four keys
           const uint32_t keep = valid >= 4 ? ~0u : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u;
           uint32_t m = *reinterpret_cast<const uint32_t *>(pw + 4 * lane) & keep, m2 = *reinterpret_cast<const uint32_t *>(pw + kKeys + 4 * lane) & keep;
           m = __vmaxu4(m, m >> 16);
@@ -276,78 +264,84 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
           const int a = __reduce_max_sync(0xffffffffu, max(m & 255u, m >> 8 & 255u));
           const int b = __reduce_max_sync(0xffffffffu, max(m2 & 255u, m2 >> 8 & 255u));
           below = max(0, a - pw[kt]);
-          s_below[tile & 3][part][kt] = (uint8_t)max(0, b - pw[kKeys + kt]);
-          if (tid == 384) {
+          s_below[tile & 7][kt] = (uint8_t)max(0, b - pw[kKeys + kt]);
+          if (kt == 0) {
             s_tell[tile % kTells].x = a;
             s_tell[tile % kTells].y = b;
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s_told[tile & 7]));
         } else {
-          below = s_below[tile & 3][part][kt];
-          const int jn = (wk.t0 + t) * kKeys + kt - wk.v.len;  // this key's node
-          if (jn >= 0 && clean_key<D>(from, kt, part, jn < wk.nodes)) s_bad[seg & 3] = 1;
+          const int jn = t * kKeys + kt - wk.v.len;  // this key's node
+          if (jn >= 0 && clean_key<D>(from, jn < wk.nodes)) s_bad[seg & 3] = 1;
+          ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_told[tile & 7]), (tile >> 3) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+          if (!ok) break;
+          below = s_below[tile & 7][kt];
         }
         const __half2 m = half_power(below);
-        ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_empty[st]), ph ^ 1, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_empty[f0 + st]), ph ^ 1, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
         if (!ok) break;
-        const uint32_t to = ring + (uint32_t)st * S::kTile + (uint32_t)(kt * 128);
-        // this thread's chunks: D / 32 of them, within one block of 64 elements (D = 128)
-        uint4 x[D / 32];
-        const int c0 = part * (D / 32);
+        const uint32_t to = ring + (uint32_t)(f0 + st) * S::kTile + (uint32_t)(kt * 128);
+#pragma unroll 1
+        for (int q = 0; q < D / 16; q += 4) {  // 64 elements
+          uint4 x[4];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) x[c] = lds128(from + 16u * place<D>(kt, c0 + c));
-        const uint32_t half = to + (uint32_t)((2 * c0) >> 3) * 16384u;
+          for (int c = 0; c < 4; ++c) x[c] = lds128(from + 16u * place<D>(kt, q + c));
+          const uint32_t half = to + (uint32_t)(q >> 2) * 16384u;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint4 lo, hi;
-          widen16(x[c], m, lo, hi);
-          const int ch = 2 * (c0 + c) & 7;
-          sts128(half + ((ch ^ (kt & 7)) << 4), lo);
-          sts128(half + (((ch + 1) ^ (kt & 7)) << 4), hi);
+          for (int c = 0; c < 4; ++c) {
+            uint4 lo, hi;
+            widen16(x[c], m, lo, hi);
+            sts128(half + (((2 * c) ^ (kt & 7)) << 4), lo);
+            sts128(half + (((2 * c + 1) ^ (kt & 7)) << 4), hi);
+          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&s_full[st]));
-          mbar_arrive(smem_u32(&s_cempty[cst]));
+          mbar_arrive(smem_u32(&s_full[f0 + st]));
+          mbar_arrive(smem_u32(&s_cempty[c0 + cst]));
         }
-        if (++st == S::kSlots) { st = 0; ph ^= 1; }
-        if (++cst == S::kCSlots) { cst = 0; cph ^= 1; }
+        if (++st == fn) { st = 0; ph ^= 1; }
+        if (++cst == cn) { cst = 0; cph ^= 1; }
       }
-      tiles += (unsigned)n;
       ++seg;
     }
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA issue
-    int st = 0, ph = 0, seg = 0;
+    int kst = 0, kph = 0, vst = 0, vph = 0, seg = 0;  // slots of K and V, and their phases
     bool ok = true;
     const uint32_t iq = idesc_16<true>(kKeys, false), iv = idesc_16<true>(D, true);
     auto wait = [&](unsigned long long &bar, unsigned phase) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&bar), phase, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
     };
-    // A step's waits come together: P on `a` (and `b`), this slot (V), and in the next one K.
-    // Each costs about as long as the tensor core's queue lasts.
+    // A step's waits come together: P on `a` (and `b`), V, and the next K.  Each costs about
+    // as long as the tensor core's queue lasts.
     auto ready = [&](unsigned long long &a, unsigned long long *b, unsigned phase, bool v, bool k) {
-      int kst = st + 1, kph = ph;
-      if (kst == S::kSlots) { kst = 0; kph ^= 1; }
       bool r = mbar_try_wait(smem_u32(&a), phase);
       if (b) r = mbar_try_wait(smem_u32(b), phase) && r;
-      if (v) r = mbar_try_wait(smem_u32(&s_full[st]), ph) && r;
+      if (v) r = mbar_try_wait(smem_u32(&s_full[S::kK + vst]), vph) && r;
       if (k) r = mbar_try_wait(smem_u32(&s_full[kst]), kph) && r;
       if (!__all_sync(0xffffffffu, r)) {
-        if (v) wait(s_full[st], ph);
+        if (v) wait(s_full[S::kK + vst], vph);
         if (k) wait(s_full[kst], kph);
         wait(a, phase);
         if (b) wait(*b, phase);
       }
       tc_fence_after();
     };
-    auto done = [&]() {  // the slot is free once the MMAs issued so far have read it
-      tc_commit_elect(smem_u32(&s_empty[st]));
-      if (++st == S::kSlots) { st = 0; ph ^= 1; }
+    // a slot is free once the MMAs issued so far have read it
+    auto done_k = [&]() {
+      tc_commit_elect(smem_u32(&s_empty[kst]));
+      if (++kst == S::kK) { kst = 0; kph ^= 1; }
+    };
+    auto done_v = [&]() {
+      tc_commit_elect(smem_u32(&s_empty[S::kK + vst]));
+      if (++vst == S::kV) { vst = 0; vph ^= 1; }
     };
     // place of scores `to`, and DUAL warpgroup `to`'s rows
-    auto qk = [&](int to, int slot) {
-      tc_scores<D, 128>(tmem + (uint32_t)to * 128u, sdesc_k128(q_addr + (DUAL ? (uint32_t)to * 128u * D * 2u : 0u)), sdesc_k128(ring + (uint32_t)slot * S::kTile), iq);
+    auto qk = [&](int to) {
+      tc_scores<D, 128>(tmem + (uint32_t)to * 128u, sdesc_k128(q_addr + (DUAL ? (uint32_t)to * 128u * D * 2u : 0u)), sdesc_k128(ring + (uint32_t)kst * S::kTile), iq);
       tc_commit_elect(smem_u32(&s_sfull[to]));
     };
     int place = 0, turn = 0;  // SINGLE: of the next product's P, and its barriers' phase; DUAL: the phase
@@ -356,50 +350,50 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
       const int n = wk.t1 - wk.t0;
       wait(s_qready, seg & 1);
       ++seg;
-      wait(s_full[st], ph);
+      wait(s_full[kst], kph);
       tc_fence_after();
       if (!ok) break;
       if (DUAL) {
         auto pv = [&](int w, bool first, bool last) {
-          tc_values<128>(tmem + 256u + (uint32_t)w * 128u, tmem + (uint32_t)w * 128u, sdesc_mn128(ring + (uint32_t)st * S::kTile), iv, first ? 0u : 1u);
+          tc_values<128>(tmem + 256u + (uint32_t)w * 128u, tmem + (uint32_t)w * 128u, sdesc_mn128(ring + (uint32_t)(S::kK + vst) * S::kTile), iv, first ? 0u : 1u);
           if (last) tc_commit_elect(smem_u32(&s_odone[w]));
         };
-        qk(0, st);
-        qk(1, st);
-        done();
+        qk(0);
+        qk(1);
+        done_k();
         for (int j = 0; j < n; ++j) {
-          // V_j, then K_j+1; each warpgroup's next scores right after its own product
+          // each warpgroup's next scores right after its own product
           const bool more = j + 1 < n;
           ready(s_pready[0][0], nullptr, turn, true, more);
           if (!ok) break;
           pv(0, j == 0, !more);
-          if (more) qk(0, st + 1 == S::kSlots ? 0 : st + 1);
+          if (more) qk(0);
           ready(s_pready[1][0], nullptr, turn, false, false);
           if (!ok) break;
           pv(1, j == 0, !more);
-          done();  // V_j
+          done_v();
           if (more) {
-            qk(1, st);
-            done();  // K_j+1
+            qk(1);
+            done_k();
           }
           turn ^= 1;
         }
       } else {
-        qk(place, st);
-        done();
+        qk(place);
+        done_k();
         if (n > 1) {
-          wait(s_full[st], ph);
+          wait(s_full[kst], kph);
           tc_fence_after();
           if (!ok) break;
-          qk(place ^ 1, st);
-          done();
+          qk(place ^ 1);
+          done_k();
         }
         for (int j = 0; j < n; ++j) {
           // each warpgroup's 64 keys of V_j into its own O, then the scores of K_j+2
           ready(s_pready[0][place], &s_pready[1][place], turn, true, j + 2 < n);
           if (!ok) break;
           const uint32_t from = tmem + (uint32_t)place * 128u;
-          const uint64_t vd = sdesc_mn128(ring + (uint32_t)st * S::kTile);
+          const uint64_t vd = sdesc_mn128(ring + (uint32_t)(S::kK + vst) * S::kTile);
           tc_values<64>(tmem + 256u, from, vd, iv, j ? 1u : 0u);
           tc_values<64>(tmem + 384u, from + 64u, vd + 512u, iv, j ? 1u : 0u);
           tc_commit_elect(smem_u32(&s_pvdone[place]));
@@ -407,10 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
             tc_commit_elect(smem_u32(&s_odone[0]));
             tc_commit_elect(smem_u32(&s_odone[1]));
           }
-          done();  // V_j
+          done_v();
           if (j + 2 < n) {
-            qk(place, st);
-            done();  // K_j+2
+            qk(place);
+            done_k();
           }
           turn ^= place;
           place ^= 1;
