@@ -28,8 +28,8 @@
 // written (256 clocks at 128 bytes), read and written as fp16 (768), and read by the
 // products (768 a row tile), beside 512 clocks of products a row tile.
 //
-// Warps 0-3 and 4-7 are the two warpgroups, warp 8 issues the MMAs, warps 9-11 stream
-// codes with TMA, warps 12-15 widen K and 16-19 V.  Tensor memory: S0 S1 O0 O1 of 128 columns each;
+// Warps 0-3 and 4-7 are the two warpgroups, warp 8 issues the MMAs, warps 9 and 10
+// stream codes of K with TMA, warp 11 those of V, warps 12-15 widen K and 16-19 V.  Tensor memory: S0 S1 O0 O1 of 128 columns each;
 // P (16-bit pairs) over S.
 #include <cstdio>
 
@@ -42,7 +42,7 @@ namespace {
 constexpr int kKeys = 128;
 constexpr int kThreads = 640;
 constexpr int kWiden = 4;  // warps that widen K, and that widen V
-constexpr int kProducers = 3;
+
 constexpr float kBias = 6.f;
 constexpr int kTells = 16;  // tiles whose powers are kept: more than are between their widening and their scores
 
@@ -112,7 +112,6 @@ __device__ __noinline__ bool clean_key(uint32_t row, bool node) {
 template <int D, bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const __grid_constant__ AttnLaunch L) {
   using S = CodeTcShape<D, DUAL>;
-  constexpr int LA = DUAL ? 1 : 2;  // K tiles ahead of the V tile in the rings
   extern __shared__ __align__(16) unsigned char sm_raw[];
   unsigned char *sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) unsigned long long s_full[S::kSlots], s_empty[S::kSlots], s_cfull[S::kCSlots], s_cempty[S::kCSlots],
@@ -139,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
       mbar_init(smem_u32(&s_empty[s]), 1);
     }
     for (int s = 0; s < S::kCSlots; ++s) {
-      mbar_init(smem_u32(&s_cfull[s]), s < S::kCK ? kProducers + 64 : kProducers);  // boxes; with K, the powers' lanes
+      mbar_init(smem_u32(&s_cfull[s]), s < S::kCK ? 2 + 64 : 1);  // producers; with K, the powers' lanes
       mbar_init(smem_u32(&s_cempty[s]), kWiden);
     }
     for (int w = 0; w < 2; ++w) {
@@ -168,27 +167,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
   SegWalk<kKeys, S::kOver> wk(L, s_start);
 
   if (warp >= 9 && warp < 12) {
-    // ---------------------------------------------------------------- producers: every third box of a tile each
-    const int me = warp - 9;
-    unsigned nk = 0, nv = 0;  // tiles of K and V so far
+    // ---------------------------------------------------------------- producers: every other box of K each, or V
+    const bool isk = warp < 11;
+    const int me = isk ? warp - 9 : 0, many = isk ? 2 : 1, c0 = isk ? 0 : S::kCK, cn = isk ? S::kCK : S::kCV;
+    const CUtensorMap *map = isk ? &L.tm_k : &L.tm_v;
+    int st = 0, ph = 0, issued = 0;
     bool ok = true;
     const int shift = p.c.page_shift, boxes = shift >= 7 ? 1 : kKeys >> shift, rows = kKeys / boxes;
     while (ok && wk.next()) {
       if (row0 >= wk.v.n * p.G) continue;
-      const int pages = wk.v.s < 0 ? 0 : (wk.total + (1 << shift) - 1) >> shift, n = wk.t1 - wk.t0;
+      const int pages = wk.v.s < 0 ? 0 : (wk.total + (1 << shift) - 1) >> shift;
       const int32_t *table = p.c.table + (size_t)(wk.v.s < 0 ? 0 : wk.v.s) * p.c.max_pages;
-      auto id = [&](int j) {  // this lane's page of the segment's tile j, as it is in the table
-        const int at = (((wk.t0 + j) * kKeys) >> shift) + lane;
-        return j < n && lane < boxes && at < pages ? table[at] : -1;
-      };
-      auto load = [&](bool isk, int j, int pg) {
-        const CUtensorMap *map = isk ? &L.tm_k : &L.tm_v;
-        const unsigned at = isk ? nk++ : nv++, st = isk ? at % S::kCK : S::kCK + at % S::kCV, ph = (isk ? at / S::kCK : at / S::kCV) & 1u;
-        ok = ok && __all_sync(0xffffffffu,
-                              mbar_wait_fast(smem_u32(&s_cempty[st]), ph ^ 1u, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
-        if (!ok) return;
-        const uint32_t fb = smem_u32(&s_cfull[st]), dst = codes + (uint32_t)st * S::kCodes;
-        const int nb = min(boxes, pages - (((wk.t0 + j) * kKeys) >> shift)), mine = nb > me ? (nb - me + kProducers - 1) / kProducers : 0;
+      // page ids a warp's worth at a time, the next ones on their way
+      auto ids = [&](int first) { return first + lane < pages ? table[first + lane] : 0; };
+      int base = ((wk.t0 * kKeys) >> shift) & ~31;
+      int cur = ids(base), ahead = ids(base + 32);
+      if (base + lane < pages) cur = checked_page(p.c, cur);
+      for (int t = wk.t0; t < wk.t1; ++t) {
+        const int first = (t * kKeys) >> shift;  // a tile's pages are within one such lot: their number divides 32
+        if (first >= base + 32) {
+          base += 32;
+          cur = base + lane < pages ? checked_page(p.c, ahead) : 0;
+          ahead = ids(base + 32);
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_cempty[c0 + st]), ph ^ 1, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
+        if (!ok) break;
+        const uint32_t fb = smem_u32(&s_cfull[c0 + st]), dst = codes + (uint32_t)(c0 + st) * S::kCodes;
+        const int nb = min(boxes, pages - first), at = first & 31, mine = nb > me ? (nb - me + many - 1) / many : 0;
         if (lane == 0) {
           if (mine > 0)
             mbar_expect_tx(fb, (uint32_t)mine * rows * D);
@@ -196,46 +201,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
             mbar_arrive(fb);
         }
         __syncwarp();
-        const int tok = ((wk.t0 + j) * kKeys) & ((1 << shift) - 1);  // 0 unless a page holds several tiles
-        if (me < 2 && isk) {  // with K: this lane's four keys' a (the first producer) or b
-          const int my = boxes == 1 ? 0 : (4 * lane) >> shift, page = __shfl_sync(0xffffffffu, pg, my & 31);
+        const int tok = (t * kKeys) & ((1 << shift) - 1);  // 0 unless a page holds several tiles
+        if (isk) {  // with K: this lane's four keys' a (the first producer) or b
+          const int my = boxes == 1 ? 0 : (4 * lane) >> shift, page = __shfl_sync(0xffffffffu, cur, (at + my) & 31);
           if (my < nb)
             cp_async4(smem_u32(s_power + (st * 2 + me) * kKeys + 4 * lane),
-                      (me == 0 ? p.c.ke : p.c.ve) + exp_off(p.c, p.layer, page, wk.h, ((wk.t0 + j) * kKeys + 4 * lane) & ((1 << shift) - 1)));
+                      (me == 0 ? p.c.ke : p.c.ve) + exp_off(p.c, p.layer, page, wk.h, (t * kKeys + 4 * lane) & ((1 << shift) - 1)));
           cp_async_arrive(fb);
         }
-        for (int b = me; b < nb; b += kProducers)
-          tma_kv(dst + (uint32_t)(b * rows * D), map, 0, tok, wk.h, __shfl_sync(0xffffffffu, pg, b), L.swap, fb);
-      };
-      auto checked = [&](int pg, int j) {  // ids were fetched a tile or more before they are looked at
-        const int at = (((wk.t0 + j) * kKeys) >> shift) + lane;
-        return j < n && lane < boxes && at < pages ? checked_page(p.c, pg) : 0;
-      };
-      // pages of tiles j .. j + LA, and one more on its way
-      int pg[LA + 2];
-#pragma unroll
-      for (int k = 0; k < LA + 2; ++k) pg[k] = id(k);
-#pragma unroll
-      for (int k = 0; k < LA; ++k) {
-        pg[k] = checked(pg[k], k);
-        if (k < n) load(true, k, pg[k]);
-      }
-      for (int j = 0; j < n && ok; ++j) {
-        load(false, j, pg[0]);
-        pg[LA] = checked(pg[LA], j + LA);
-        if (j + LA < n) load(true, j + LA, pg[LA]);
-#pragma unroll
-        for (int k = 0; k < LA + 1; ++k) pg[k] = pg[k + 1];
-        pg[LA + 1] = id(j + LA + 2);
+        for (int b = me; b < nb; b += many)
+          tma_kv(dst + (uint32_t)(b * rows * D), map, 0, tok, wk.h, __shfl_sync(0xffffffffu, cur, at + b), L.swap, fb);
+        ++issued;
+        if (++st == cn) { st = 0; ph ^= 1; }
       }
     }
-    // no copy may land after the CTA exits: wait for the last fill of every slot (after a
-    // wait gave up the last one was not made, and this wait gives up too)
+    // no copy may land after the CTA exits: wait for the last fill of every slot
     volatile int never = 0;
-    for (unsigned j = nk > S::kCK ? nk - S::kCK : 0; j < nk; ++j)
-      if (!mbar_wait(smem_u32(&s_cfull[j % S::kCK]), (j / S::kCK) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never)) break;
-    for (unsigned j = nv > S::kCV ? nv - S::kCV : 0; j < nv; ++j)
-      if (!mbar_wait(smem_u32(&s_cfull[S::kCK + j % S::kCV]), (j / S::kCV) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never)) break;
+    for (int j = issued - cn < 0 ? 0 : issued - cn; j < issued; ++j)
+      if (!mbar_wait(smem_u32(&s_cfull[c0 + j % cn]), (j / cn) & 1, p.err, DFV_DEVERR_DRAIN_WAIT, &never)) break;
   } else if (warp >= 12) {
     // ---------------------------------------------------------------- widening: a key row a thread
     // (Short loops: with the chunks of two tiles unrolled the warps waited for instructions
