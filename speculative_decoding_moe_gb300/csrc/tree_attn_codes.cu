@@ -58,7 +58,7 @@ struct CodeShape {
   static constexpr int kStages = 8;                 // of K and V: 128 KB in flight
   static constexpr int kPer = kStages / kGroups;    // stages of a group
   static constexpr int kPitch = D + 4;              // floats of a row of a warp's state
-  static constexpr int kOver = 6;                   // tiles' worth of time that a pair costs at least
+  static constexpr int kOver = 8;                   // tiles' worth of time that a pair costs at least
   static constexpr size_t kState = (size_t)kRows * kPitch * 4;
   static constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * (kTile + kKt) + kCons * kState;
 };

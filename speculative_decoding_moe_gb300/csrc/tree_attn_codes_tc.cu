@@ -5,12 +5,9 @@
 // head and streams the keys in tiles of 128.  DUAL: a warpgroup takes 128 rows.
 // SINGLE: a warpgroup takes the first or the second 64 keys of every tile, with its own
 // (M, l, O); scores take turns in two places, so that the next tile's are ready while
-// one is in its exponentials; the two states are joined at the end (with even and odd
-// tiles for the warpgroups, each waited for a tile's whole chain: 97 us where this
-// takes XX, 32 x 16 nodes).  Between the copies and the
-// products, four warps widen the codes of K and four those of V into fp16 in shared
-// memory, a key row a thread, each in rings of their own (eight warps on every tile of
-// either in turn took a third longer: a tile is bound by its latency).
+// one is in its exponentials; the two states are joined at the end.  Between the copies
+// and the products, four warps widen the codes of K and four those of V into fp16 in
+// shared memory, a key row a thread, each in rings of their own.
 //
 // Mathematics.  Key j is K_j 2^a_j, value j is V_j 2^b_j.  With A and B the largest a
 // and b of a tile of 128 keys, the products take K_j 2^(a_j - A) and V_j 2^(b_j - B) in
@@ -24,13 +21,19 @@
 // A tile's maximum is found in one pass over its scores, 16 at a time, and p in another:
 // with 20 warps a thread has 96 registers.
 //
-// What binds: shared memory.  Per tile of 128 keys of 128 elements the codes are
-// written (256 clocks at 128 bytes), read and written as fp16 (768), and read by the
-// products (768 a row tile), beside 512 clocks of products a row tile.
+// What binds: shared memory, then the chain from a tile's copy to its product.  Per tile
+// of 128 keys of 128 elements the codes are written (256 clocks at 128 bytes), read and
+// written as fp16 (768), and read by the products (768 a row tile), beside 1024 clocks
+// of products a row tile.  Measured: 32 x 16 nodes of 8 heads over up to 8191 keys 84 us
+// (2000 clocks of the 2600 a tile takes are shared memory's), 32 x 32 nodes 134.  Steps
+// on the way, of the first: unrolled widening 157 us (a third of the warps' time went to
+// waiting for instructions), short loops and powers by asynchronous copies 102, the
+// products' waits together and eight widening warps 97, both warpgroups on every tile
+// and rings of K and V apart 93, producers apart 85.
 //
 // Warps 0-3 and 4-7 are the two warpgroups, warp 8 issues the MMAs, warps 9 and 10
-// stream codes of K with TMA, warp 11 those of V, warps 12-15 widen K and 16-19 V.  Tensor memory: S0 S1 O0 O1 of 128 columns each;
-// P (16-bit pairs) over S.
+// stream codes of K with TMA, warp 11 those of V, warps 12-15 widen K and 16-19 V.
+// Tensor memory: S0 S1 O0 O1 of 128 columns each; P (16-bit pairs) over S.
 #include <cstdio>
 
 #include "attn_tc.cuh"
@@ -53,7 +56,7 @@ struct CodeTcShape {
   static constexpr int kK = D == 64 ? 2 : 1, kV = D == 64 ? 3 : 2;  // fp16 tiles of K, and of V behind them
   static constexpr int kCK = D == 64 ? 4 : DUAL ? 1 : 3, kCV = D == 64 ? 4 : 2;  // tiles of codes
   static constexpr int kSlots = kK + kV, kCSlots = kCK + kCV;
-  static constexpr int kOver = DUAL ? 5 : 2;         // tiles' worth of time that a pair costs at least
+  static constexpr int kOver = DUAL ? 5 : 3;         // tiles' worth of time that a pair costs at least
   static constexpr uint32_t kQ = (DUAL ? 2 : 1) * 128 * D * 2;
   static constexpr size_t kSmem = 1024 + kQ + (size_t)kSlots * kTile + (size_t)kCSlots * kCodes;
 };
