@@ -717,8 +717,8 @@ int dfv_pages_free(const dfv_kv_cache *cache, const int32_t *seqs, int n, void *
  * dfv_tree_attention take up to DFV_MAX_TREE).  A prompt, or its next chunk,
  * goes through a layer as
  *   dfv_norm_rope_append    its rows normed, turned and stored at lens[s] + i
- *   dfv_prompt_attention    over its own k and v when nothing was there before;
- *                           else over what dfv_cache_read brought back
+ *   dfv_prompt_attention    over its own turned k and its v when nothing was there
+ *                           before; else over what dfv_cache_read brought back
  * and once all layers are done the caller adds the row counts to lens.
  * ---------------------------------------------------------------------- */
 
@@ -745,8 +745,12 @@ typedef struct dfv_row_batch {
  * fp32 and rounded once.  Arguments as for dfv_rope_append, and
  *   q_gain, k_gain  [head_dim] in the rows' dtype, 16-byte aligned, or NULL
  *   eps             >= 0, finite (read where a gain is given)
+ *   k_out           [n_rows, n_kv_heads, head_dim], strides ko_row, ko_head, or NULL: the
+ *                   normed and turned keys as rows too, for the attention of a prompt
+ *                   of which nothing is cached yet (DFV_E4M3: before they become
+ *                   codes); may be k itself (same strides)
  * Row i of a sequence goes to token lens[s] + i of layer `layer`; rows whose page
- * is missing are not stored (DFV_KVERR_PAGE) while their q is still written.
+ * is missing are not stored (DFV_KVERR_PAGE) while q_out and k_out are written.
  * Rows that row_off gives to no sequence are not touched.  Of a sequence with
  * more than max_rows rows, or whose rows do not fit its table, nothing is stored
  * (DFV_KVERR_LEN).
@@ -755,7 +759,8 @@ int dfv_norm_rope_append(const dfv_kv_cache *cache, int layer, const dfv_row_bat
                          const void *q_gain, const void *k_gain, float eps, int rot_dim, int interleaved, float scale,
                          const uint64_t *turns, const void *q, int64_t q_row, int64_t q_head, const void *k,
                          int64_t k_row, int64_t k_head, const void *v, int64_t v_row, int64_t v_head,
-                         const int32_t *positions, void *q_out, int64_t o_row, int64_t o_head, void *stream);
+                         const int32_t *positions, void *q_out, int64_t o_row, int64_t o_head, void *k_out,
+                         int64_t ko_row, int64_t ko_head, void *stream);
 
 /*
  * Cached tokens as packed rows: row row_off[b] + i receives token i of sequence b

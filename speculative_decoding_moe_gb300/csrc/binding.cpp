@@ -216,7 +216,7 @@ PyObject *rope_append(PyObject *const *a) {
 }
 
 // (cache, layer, rows, plan's head_dim, rot_dim, interleaved, scale, turns, q, k, v, positions, q_gain, k_gain, eps, out,
-// stream, plan's device)
+// stream, plan's device, k_out or None)
 PyObject *norm_rope_append(PyObject *const *a) {
   const Cache &c = handle<Cache>(a[0]);
   const int layer = number(a[1]);
@@ -231,6 +231,8 @@ PyObject *norm_rope_append(PyObject *const *a) {
   const void *qg = given(a[12], "q_gain", dt, {D}, c.index), *kg = given(a[13], "k_gain", dt, {D}, c.index);
   if (number(a[3]) != D) value_error("the rotary plan is for head_dim %d, the cache has %d", number(a[3]), (int)D);
   if (number(a[17]) != c.index) value_error("the rotary plan and the cache are not on one device");
+  Rows3 rko = {nullptr, 0, 0};
+  if (a[18] != Py_None) rko = rows3(tensor(a[18], "k_out"), "k_out", rows, K, D, dt, c.index);
   at::Tensor made;
   if (a[15] == Py_None) made = empty({rows, H, D}, dt, q, stream(a[16]));
   const Rows3 ro = rows3(made.defined() ? made : tensor(a[15], "out"), "out", rows, H, D, dt, c.index);
@@ -238,7 +240,7 @@ PyObject *norm_rope_append(PyObject *const *a) {
   done(dfv_norm_rope_append(&c.c, layer, &r.c, (int)H, qg, kg, (float)real(a[14]), number(a[4]), number(a[5]),
                             (float)real(a[6]), static_cast<const uint64_t *>(stream(a[7])), rq.p, rq.row, rq.head, rk.p,
                             rk.row, rk.head, rv.p, rv.row, rv.head, static_cast<const int32_t *>(pos), ro.p, ro.row,
-                            ro.head, stream(a[16])),
+                            ro.head, rko.p, rko.row, rko.head, stream(a[16])),
        "dfv_norm_rope_append");
   return made.defined() ? THPVariable_Wrap(made) : same(a[15]);
 }
@@ -498,7 +500,7 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyMethodDef kMethods[] = {DFV_ENTRY(rope_append, 15),   DFV_ENTRY(tree_attention, 9), DFV_ENTRY(logits_process, 9),
                           DFV_ENTRY(accept_tree, 6),    DFV_ENTRY(cache_commit, 7),   DFV_ENTRY(cache_copy_pages, 4),
                           DFV_ENTRY(pages_reserve, 5),  DFV_ENTRY(pages_fork, 5),     DFV_ENTRY(pages_free, 3),
-                          DFV_ENTRY(norm_rope_append, 18), DFV_ENTRY(cache_read, 7),   DFV_ENTRY(prompt_attention, 11),
+                          DFV_ENTRY(norm_rope_append, 19), DFV_ENTRY(cache_read, 7),   DFV_ENTRY(prompt_attention, 11),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_dfvbind", "hot calls of the tree-verify and prompt binding", -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

@@ -51,13 +51,20 @@ int dfv_norm_rope_append(const dfv_kv_cache *cache, int layer, const dfv_row_bat
                          const void *q_gain, const void *k_gain, float eps, int rot_dim, int interleaved, float scale,
                          const uint64_t *turns, const void *q, int64_t q_row, int64_t q_head, const void *k,
                          int64_t k_row, int64_t k_head, const void *v, int64_t v_row, int64_t v_head,
-                         const int32_t *positions, void *q_out, int64_t o_row, int64_t o_head, void *stream) {
+                         const int32_t *positions, void *q_out, int64_t o_row, int64_t o_head, void *k_out,
+                         int64_t ko_row, int64_t ko_head, void *stream) {
   int st = check_cache(cache);
   if (st) return st;
   if ((st = check_rows(rows, "rows"))) return st;
   if (!aligned(q_gain, 16) || !aligned(k_gain, 16)) return api_fail(DFV_ERR_INVALID_ARG, "gains not 16-byte aligned");
   if ((q_gain || k_gain) && !(eps >= 0.f && std::isfinite(eps)))
     return api_fail(DFV_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (!aligned(k_out, 16) || (k_out && (!stride_ok(ko_row) || !stride_ok(ko_head))))
+    return api_fail(DFV_ERR_INVALID_ARG, "k_out not 16-byte aligned, or its strides no non-negative multiples of 8 elements");
+  if (k_out && k_out == k && (ko_row != k_row || ko_head != k_head))
+    return api_fail(DFV_ERR_INVALID_ARG, "k_out is k: the strides must be the same");
+  if (k_out && (k_out == q || k_out == v || k_out == q_out))
+    return api_fail(DFV_ERR_INVALID_ARG, "k_out must not be q, v or q_out");
   RopeParams p = {};
   p.c = cache_params(cache);
   p.t = row_params(rows);
@@ -83,6 +90,9 @@ int dfv_norm_rope_append(const dfv_kv_cache *cache, int layer, const dfv_row_bat
   p.q_gain = (const char *)q_gain;
   p.k_gain = (const char *)k_gain;
   p.eps = eps;
+  p.ko = (char *)k_out;
+  p.ko_row = ko_row;
+  p.ko_head = ko_head;
   if ((st = check_rope(cache, layer, n_heads, rot_dim, interleaved, scale, p))) return st;
   return launched(launch_norm_rope_append(p, (cudaStream_t)stream), "norm and rotary append launch");
 }

@@ -266,6 +266,11 @@ __global__ void __launch_bounds__(kRowThreads, 3) append_kernel(const __grid_con
         to[at.y] = narrow<F16>(b);
         continue;
       }
+      if (turned && p.ko) {
+        uint4 *to = reinterpret_cast<uint4 *>(p.ko + 2 * (row * p.ko_row + (h - p.H) * p.ko_head));
+        to[at.x] = narrow<F16>(a);
+        to[at.y] = narrow<F16>(b);
+      }
       if (pg < 0) continue;
       if (CODES) {
         const int kh = turned ? h - p.H : h - HK;

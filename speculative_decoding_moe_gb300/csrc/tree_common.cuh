@@ -43,6 +43,8 @@ struct RopeParams {
   const char *q_gain, *k_gain;  // null: no norm
   float eps;
   int by_seq;  // row_off may be in any order
+  char *ko;    // turned keys as rows, or null
+  long long ko_row, ko_head;
 };
 
 struct CacheReadParams {

@@ -163,7 +163,7 @@ def _load():
         L.dfv_pages_reserve.argtypes = [P, P, P, I, P, S, P]
         L.dfv_pages_fork.argtypes = [P, P, P, I, P, S, P]
         L.dfv_pages_free.argtypes = [P, P, I, P]
-        L.dfv_norm_rope_append.argtypes = [P, I, P, I, P, P, F, I, I, F, P, P, L64, L64, P, L64, L64, P, L64, L64, P, P, L64, L64, P]
+        L.dfv_norm_rope_append.argtypes = [P, I, P, I, P, P, F, I, I, F, P, P, L64, L64, P, L64, L64, P, L64, L64, P, P, L64, L64, P, L64, L64, P]
         L.dfv_cache_read.argtypes = [P, I, P, P, L64, L64, P, L64, L64, P]
         L.dfv_prompt_attention_workspace_size.restype = S
         L.dfv_prompt_attention_workspace_size.argtypes = [P, I, I, I]
@@ -654,13 +654,14 @@ def rope_append(cache: KVCache, layer: int, tree: TreeBatch, rope: Rope, q: torc
 def norm_rope_append(cache: KVCache, layer: int, rows: RowBatch, rope: Rope, q: torch.Tensor, k: torch.Tensor,
                      v: torch.Tensor, positions: torch.Tensor, q_gain: Optional[torch.Tensor] = None,
                      k_gain: Optional[torch.Tensor] = None, eps: float = 1e-6, out: Optional[torch.Tensor] = None,
-                     stream=None) -> torch.Tensor:
+                     k_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Normed and rotated q (out, a new tensor or q itself), and the rows' normed and rotated k and their v stored into
     the cache behind the committed tokens, for any number of rows.  q_gain, k_gain [dim]: the gains of the norm over each
-    head's elements (None: no norm); q [rows, heads, dim], k and v [rows, kv heads, dim] may be slices of one projection."""
+    head's elements (None: no norm); q [rows, heads, dim], k and v [rows, kv heads, dim] may be slices of one projection.
+    k_out: optional rows that receive the normed and rotated k too (k itself is fine), for prompt_attention."""
     return (_ext or _bind()).norm_rope_append(cache.addr, layer, rows.addr, rope.head_dim, rope.rot_dim, rope.interleaved,
                                               rope.scale, rope.turns_addr, q, k, v, positions, q_gain, k_gain, eps, out,
-                                              _on(stream, cache.index), rope.index)
+                                              _on(stream, cache.index), rope.index, k_out)
 
 
 def cache_read(cache: KVCache, layer: int, rows: RowBatch, k: Optional[torch.Tensor] = None,

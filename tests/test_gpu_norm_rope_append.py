@@ -192,6 +192,23 @@ def test_in_place_and_rows_of_nobody(dfv, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("inter", [False, True])
+def test_turned_keys_as_rows(dfv, kind, inter):
+    c = Case([7, 70], [90, 5], 4, 2, 128, 16, kind, seed=16, lead=3, tail=4)
+    cache = c.cache(dfv)
+    ko = torch.full((c.n, 3, 128), 5.0, dtype=c.dt, device="cuda")
+    cache.page_table[0, 2] = -1  # tokens without a page have their rows all the same
+    out, (y, t) = c.run(dfv, cache, inter=inter, k_out=ko[:, :2])
+    got, want, t = ko[3:-4, :2].double().cpu(), y[3:-4, 4:6], t[3:-4, 4:6]
+    assert bool(((got - want).abs() <= t + HALF_STEP[c.dt] * (want.abs() + t) + 2.0 ** -25).all())
+    assert bool((ko[:3] == 5).all()) and bool((ko[-4:] == 5).all()) and bool((ko[:, 2] == 5).all())
+    q, k, v = c.split(c.qkv.cuda())  # into k itself
+    rows, g = dfv.RowBatch(i32(c.off), c.n, 90), [x.cuda() for x in c.gains]
+    dfv.norm_rope_append(cache, 0, rows, dfv.Rope(128, interleaved=inter), q, k, v, c.positions.cuda(), q_gain=g[0], k_gain=g[1], k_out=k)
+    assert torch.equal(k[3:-4], ko[3:-4, :2]) and torch.equal(k[:3].cpu(), c.qkv[:3, 4:6])
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_many_rows_and_sequences(dfv, kind):
     c = Case([(5 * s) % 33 for s in range(400)], [(3 * s) % 7 for s in range(400)], 2, 1, 64, 8, kind, seed=7)
     cache = c.cache(dfv)

@@ -36,11 +36,11 @@ def rows(dfv, **kw):
 
 def append(dfv, c=None, r=None, **kw):
     a = dict(layer=0, heads=32, qg=0x500, kg=0x600, eps=1e-6, rot=128, inter=0, scale=1.0, turns=0x1000, q=0x2000, qr=4096, qh=128,
-             k=0x3000, kr=512, kh=128, v=0x4000, vr=512, vh=128, pos=0x5000, o=0x6000, orow=4096, oh=128)
+             k=0x3000, kr=512, kh=128, v=0x4000, vr=512, vh=128, pos=0x5000, o=0x6000, orow=4096, oh=128, ko=None, kor=512, koh=128)
     a.update(kw)
     return dfv.lib().dfv_norm_rope_append(c or cache(dfv), a["layer"], r or rows(dfv), a["heads"], a["qg"], a["kg"], a["eps"], a["rot"],
                                           a["inter"], a["scale"], a["turns"], a["q"], a["qr"], a["qh"], a["k"], a["kr"], a["kh"],
-                                          a["v"], a["vr"], a["vh"], a["pos"], a["o"], a["orow"], a["oh"], None)
+                                          a["v"], a["vr"], a["vh"], a["pos"], a["o"], a["orow"], a["oh"], a["ko"], a["kor"], a["koh"], None)
 
 
 def read(dfv, c=None, r=None, **kw):
@@ -95,7 +95,9 @@ def test_rows(dfv, kw, status):
     (dict(rot=144), UNSUPPORTED), (dict(inter=2), INVALID), (dict(scale=math.inf), INVALID), (dict(turns=0), INVALID), (dict(turns=0x1004), INVALID),
     (dict(pos=0), INVALID), (dict(pos=0x5002), INVALID), (dict(q=0), INVALID), (dict(k=0x3002), INVALID), (dict(v=0), INVALID), (dict(o=0), INVALID),
     (dict(qr=-8), INVALID), (dict(kh=12), INVALID), (dict(vr=4), INVALID), (dict(orow=1), INVALID), (dict(o=0x2000, orow=8192), INVALID),
-    (dict(qg=0x508), INVALID), (dict(kg=0x602), INVALID), (dict(eps=-1e-6), INVALID), (dict(eps=math.nan), INVALID), (dict(eps=math.inf), INVALID)])
+    (dict(qg=0x508), INVALID), (dict(kg=0x602), INVALID), (dict(eps=-1e-6), INVALID), (dict(eps=math.nan), INVALID), (dict(eps=math.inf), INVALID), (dict(ko=0x7004), INVALID),
+    (dict(ko=0x7000, kor=4), INVALID), (dict(ko=0x7000, koh=-8), INVALID), (dict(ko=0x3000, kor=1024), INVALID), (dict(ko=0x2000), INVALID),
+    (dict(ko=0x4000), INVALID), (dict(ko=0x6000), INVALID)])
 def test_append(dfv, kw, status):
     assert append(dfv, **kw) == status
     assert dfv.lib().dfv_last_error_detail()
@@ -113,7 +115,7 @@ def test_read(dfv, kw, status):
     (dict(kv=2000, heads=2000), INVALID), (dict(heads=68), UNSUPPORTED), (dict(dim=96), UNSUPPORTED), (dict(dim=256), UNSUPPORTED),
     (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=math.nan), INVALID), (dict(q=0), INVALID), (dict(q=0x2004), INVALID),
     (dict(k=0), INVALID), (dict(v=0x4008), INVALID), (dict(o=0), INVALID), (dict(o=0x2000), INVALID), (dict(o=0x3000), INVALID), (dict(o=0x4000), INVALID),
-    (dict(qr=3), INVALID), (dict(oh=-8), INVALID), (dict(kr=1 << 36), INVALID), (dict(kr=0), UNSUPPORTED), (dict(vh=0), UNSUPPORTED),
+    (dict(qr=3), INVALID), (dict(oh=-8), INVALID), (dict(kr=1 << 36), INVALID), (dict(kr=0), UNSUPPORTED), (dict(vh=0), UNSUPPORTED), (dict(qr=0), UNSUPPORTED), (dict(qh=0), UNSUPPORTED),
     (dict(lse=0x7002), INVALID), (dict(err=0x7001), INVALID), (dict(ws=0), WORKSPACE), (dict(ws=0x9010), WORKSPACE), (dict(n=255), WORKSPACE)])
 def test_prompt(dfv, kw, status):
     assert prompt(dfv, **kw) == status
@@ -169,7 +171,9 @@ def test_binding_arguments(dfv):
     for kw in (dict(q_gain=gain[:32]), dict(k_gain=torch.ones(128, dtype=torch.bfloat16)[::2])):
         with pytest.raises(ValueError):
             dfv.norm_rope_append(c, 0, r, rope, q, kv, kv, pos, **kw)
-    for kw in (dict(q_gain=gain.float()), dict(out=q.half())):
+    with pytest.raises(ValueError):
+        dfv.norm_rope_append(c, 0, r, rope, q, kv, kv, pos, k_out=q)
+    for kw in (dict(q_gain=gain.float()), dict(out=q.half()), dict(k_out=kv.half())):
         with pytest.raises(TypeError):
             dfv.norm_rope_append(c, 0, r, rope, q, kv, kv, pos, **kw)
     with pytest.raises(TypeError):  # rows of a cache in codes are bf16
