@@ -1,10 +1,20 @@
 """A verify loop over drafted trees, end to end on the GPU: a small target with attention and MoE layers, a paged cache,
 and a drafter that proposes a tree of tokens for each of several requests.
 
+The prompts go in by chunks of some rows per request, all requests' rows packed:
+  1. pages for the chunk's rows                        pages_reserve
+  2. per layer: norm, one projection to q, k and v     (torch)
+                norms per head, rotary positions,
+                rows into the cache                    norm_rope_append
+                the cached rows (later chunks)         cache_read
+                causal attention of the rows           prompt_attention
+                output projection, MoE block           (as below)
+
 One step, in the order a serving loop runs it:
   1. pages for the trees' nodes                        pages_reserve
   2. per layer: norm, one projection to q, k and v     (torch)
-                rotary positions, rows into the cache  rope_append
+                norms per head, rotary positions,
+                rows into the cache                    norm_rope_append
                 attention of the nodes                 tree_attention
                 output projection, residual            (torch)
                 MoE block                              moe_stack_forward
@@ -15,9 +25,9 @@ Nothing in a step copies to the host: the lengths, page tables, counts and paths
 
 Speculation must not change the text: the committed tokens are those that decoding one token at a time gives.  `main`
 runs both and compares; the drafter here knows the plain decode's text and mixes wrong tokens in, so that paths of every
-length occur.
+length occur.  With --codes the cache holds e4m3 codes with a power of two per token and head, half the bytes.
 
-    python examples/tree_verify.py [--steps 12] [--requests 4] [--nodes 12]
+    python examples/tree_verify.py [--steps 12] [--requests 4] [--nodes 12] [--chunk 24] [--codes]
 """
 from __future__ import annotations
 
@@ -36,7 +46,7 @@ D_MODEL, HEADS, KV_HEADS, HEAD_DIM, LAYERS, VOCAB, PAGE = 512, 8, 2, 64, 2, 2048
 
 
 class Target:
-    """Random weights of a small pre-norm model: attention and MoE blocks in turn."""
+    """Random weights of a small pre-norm model: attention (q and k normed per head) and MoE blocks in turn."""
 
     def __init__(self, seed=0):
         g = torch.Generator(device="cuda").manual_seed(seed)
@@ -48,35 +58,52 @@ class Target:
         self.moe = [dfv.Layer(inputs.make_layer(shape, seed + 1 + i, device="cuda")) for i in range(LAYERS)]
         self.moe_ws = dfv.alloc_workspace(dfv.workspace_size(self.moe[0], 16))
         self.rope = dfv.Rope(HEAD_DIM, theta=1e4)
+        self.gains = [[1 + w(HEAD_DIM) for _ in range(2)] for _ in range(LAYERS)]
 
     @staticmethod
     def norm(x):
         x = x.float()
         return (x * torch.rsqrt(x.pow(2).mean(-1, keepdim=True) + 1e-6)).to(torch.bfloat16)
 
-    def forward(self, cache, tree, tokens, positions, ws):
-        """Logits of every node [rows, VOCAB]; the nodes' keys and values are in the cache afterwards."""
+    def layers(self, cache, rows, tokens, positions, attention):
+        """The residual stream behind the last layer [rows, D_MODEL]; the rows' keys and values are in the cache afterwards.
+        attention(layer, q, k, v): over the rows just stored and what was there before."""
         x = self.embed[tokens.long()]
-        rows = x.shape[0]
+        n = x.shape[0]
         for i in range(LAYERS):
-            qkv = (self.norm(x) @ self.qkv[i]).view(rows, HEADS + 2 * KV_HEADS, HEAD_DIM)
+            qkv = (self.norm(x) @ self.qkv[i]).view(n, HEADS + 2 * KV_HEADS, HEAD_DIM)
             q, k, v = qkv[:, :HEADS], qkv[:, HEADS:HEADS + KV_HEADS], qkv[:, HEADS + KV_HEADS:]
-            q = dfv.rope_append(cache, i, tree, self.rope, q, k, v, positions)
-            o = dfv.tree_attention(cache, i, tree, q, ws)
-            x = (x.float() + (o.view(rows, -1) @ self.proj[i]).float()).to(torch.bfloat16)
-            for r in range(0, rows, 16):  # the residual stack takes blocks of 16 rows
+            q = dfv.norm_rope_append(cache, i, rows, self.rope, q, k, v, positions, q_gain=self.gains[i][0],
+                                     k_gain=self.gains[i][1], k_out=k)
+            o = attention(i, q, k, v)
+            x = (x.float() + (o.view(n, -1) @ self.proj[i]).float()).to(torch.bfloat16)
+            for r in range(0, n, 16):  # the residual stack takes blocks of 16 rows
                 x[r:r + 16] = dfv.moe_stack_forward([self.moe[i]], x[r:r + 16].clone(), self.moe_ws)
+        return x
+
+    def verify(self, cache, tree, tokens, positions, ws):
+        """Logits of every node [rows, VOCAB]."""
+        rows = dfv.RowBatch(tree.row_off, tree.n_rows, tree.max_nodes)
+        x = self.layers(cache, rows, tokens, positions, lambda i, q, k, v: dfv.tree_attention(cache, i, tree, q, ws))
         return (self.norm(x) @ self.embed.t()).float() * 0.05
+
+    def prefill(self, cache, rows, keys, tokens, positions, ws):
+        """A chunk of the prompts; keys: all cached rows with the chunk's, None while nothing was cached before."""
+        def attention(i, q, k, v):
+            if keys is not None:
+                k, v = dfv.cache_read(cache, i, keys)
+            return dfv.prompt_attention(rows, q, k, v, ws, keys=keys)
+        self.layers(cache, rows, tokens, positions, attention)
 
 
 class Server:
     """Requests with their own sequences of one cache."""
 
-    def __init__(self, target, prompts, tokens_per_request, max_nodes):
+    def __init__(self, target, prompts, tokens_per_request, max_nodes, chunk=24, dtype=torch.bfloat16):
         self.t, self.S, self.N = target, len(prompts), max_nodes
         room = max(len(p) for p in prompts) + tokens_per_request + max_nodes
         width = -(-room // PAGE)
-        self.cache = dfv.KVCache.empty(LAYERS, self.S * width + 1, PAGE, KV_HEADS, HEAD_DIM, self.S, width)
+        self.cache = dfv.KVCache.empty(LAYERS, self.S * width + 1, PAGE, KV_HEADS, HEAD_DIM, self.S, width, dtype=dtype)
         self.pages_ws = dfv.alloc_workspace(dfv.cache_workspace_size(self.cache))
         self.all = torch.arange(self.S, dtype=torch.int32, device="cuda")
         self.hist = torch.zeros(self.S, room + 1, dtype=torch.int32, device="cuda")
@@ -86,16 +113,35 @@ class Server:
         self.rules = dfv.LogitRules(hist=self.hist, hist_len=self.hist_len, prompt_len=self.prompt_len, repetition=pen,
                                     frequency=torch.full((self.S,), 0.1, device="cuda"))
         self.logits_ws = dfv.alloc_workspace(dfv.logits_workspace_size(self.S * max(max_nodes, 64)))
-        # prompts but for their last token, which is the first root, as chains of up to max_nodes rows
-        for start in range(0, max(len(p) for p in prompts) - 1, max_nodes):
-            parts = [p[start:min(start + max_nodes, len(p) - 1)] for p in prompts]
-            masks = [[(2 << i) - 1 for i in range(len(p))] for p in parts]
-            tree, toks, pos = self.batch(parts, masks)
-            self.reserve(len(max(parts, key=len)))
-            self.run(tree, toks, pos)
-            path = torch.arange(tree.max_nodes, dtype=torch.int32, device="cuda").repeat(self.S, 1)
-            taken = torch.tensor([len(p) for p in parts], dtype=torch.int32, device="cuda")
-            self.keep(tree, toks, path, taken)
+        # prompts but for their last token, which is the first root
+        done = [0] * self.S
+        for start in range(0, max(len(p) for p in prompts) - 1, chunk):
+            parts = [p[start:min(start + chunk, len(p) - 1)] for p in prompts]
+            self.prefill(parts, done)
+            done = [d + len(p) for d, p in zip(done, parts)]
+
+    @staticmethod
+    def rows(counts):
+        off = [0]
+        for n in counts:
+            off.append(off[-1] + n)
+        return dfv.RowBatch(torch.tensor(off, dtype=torch.int32, device="cuda"), off[-1], max(counts))
+
+    def prefill(self, parts, done):
+        """Rows of prompts behind the first done[s] of each, which are in the cache."""
+        dev = dict(dtype=torch.int32, device="cuda")
+        rows = self.rows([len(p) for p in parts])
+        keys = self.rows([d + len(p) for d, p in zip(done, parts)]) if any(done) else None
+        toks = torch.tensor([x for p in parts for x in p], **dev)
+        pos = torch.tensor([d + i for d, p in zip(done, parts) for i in range(len(p))], **dev)
+        taken = torch.tensor([len(p) for p in parts], **dev)
+        dfv.pages_reserve(self.cache, self.all, taken, self.pages_ws)
+        ws = dfv.alloc_workspace(dfv.prompt_attention_workspace_size(rows, HEADS, KV_HEADS, HEAD_DIM))
+        self.t.prefill(self.cache, rows, keys, toks, pos, ws)
+        self.cache.lens += taken
+        for s, (d, p) in enumerate(zip(done, parts)):
+            self.hist[s, d:d + len(p)] = torch.tensor(p, **dev)
+        self.hist_len += taken
 
     def batch(self, tokens, masks):
         """Tree descriptor, tokens and rotary positions of one call (trees built on the host, as a drafter would)."""
@@ -115,7 +161,7 @@ class Server:
 
     def run(self, tree, tokens, positions):
         ws = dfv.alloc_workspace(dfv.tree_attention_workspace_size(self.cache, tree, HEADS))
-        return self.t.forward(self.cache, tree, tokens, positions, ws)
+        return self.t.verify(self.cache, tree, tokens, positions, ws)
 
     def keep(self, tree, tokens, path, tau):
         """The accepted nodes' rows stay in the cache, their tokens join the history."""
@@ -159,14 +205,17 @@ def main(argv=None):
     ap.add_argument("--steps", type=int, default=12)
     ap.add_argument("--requests", type=int, default=4)
     ap.add_argument("--nodes", type=int, default=12)
+    ap.add_argument("--chunk", type=int, default=24, help="rows of a prompt per call")
+    ap.add_argument("--codes", action="store_true", help="cache in e4m3 codes")
     a = ap.parse_args(argv)
     rng = random.Random(7)
     target = Target()
     prompts = [[rng.randrange(VOCAB) for _ in range(rng.randint(2, 40))] for _ in range(a.requests)]
     total = a.steps * a.nodes
+    how = dict(chunk=a.chunk, dtype=torch.float8_e4m3fn if a.codes else torch.bfloat16)
 
     # one token at a time
-    plain = Server(target, prompts, total, 1)
+    plain = Server(target, prompts, total, 1, **how)
     text = [[] for _ in prompts]
     roots = [p[-1] for p in prompts]
     for _ in range(total):
@@ -176,7 +225,7 @@ def main(argv=None):
             t.append(r)
 
     # trees
-    spec = Server(target, prompts, total, a.nodes)
+    spec = Server(target, prompts, total, a.nodes, **how)
     got = [[] for _ in prompts]
     roots = [p[-1] for p in prompts]
     for _ in range(a.steps):
