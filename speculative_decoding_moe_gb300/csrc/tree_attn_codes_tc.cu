@@ -47,6 +47,7 @@ constexpr int kThreads = 640;
 constexpr int kWiden = 4;  // warps that widen K, and that widen V
 
 constexpr float kBias = 6.f;
+constexpr int kFlags = 8;
 constexpr int kTells = 16;  // tiles whose powers are kept: more than are between their widening and their scores
 
 template <int D, bool DUAL>
@@ -56,6 +57,7 @@ struct CodeTcShape {
   static constexpr int kK = D == 64 ? 2 : 1, kV = D == 64 ? 3 : 2;  // fp16 tiles of K, and of V behind them
   static constexpr int kCK = D == 64 ? 4 : DUAL ? 1 : 3, kCV = D == 64 ? 4 : 2;  // tiles of codes
   static constexpr int kSlots = kK + kV, kCSlots = kCK + kCV;
+  static_assert(kFlags >= kV + 2 && kFlags >= kK + 3, "flags of segments under way");
   static constexpr int kOver = DUAL ? 5 : 3;         // tiles' worth of time that a pair costs at least
   static constexpr uint32_t kQ = (DUAL ? 2 : 1) * 128 * D * 2;
   static constexpr size_t kSmem = 1024 + kQ + (size_t)kSlots * kTile + (size_t)kCSlots * kCodes;
@@ -123,7 +125,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
   __shared__ volatile int s_abort;
   __shared__ SchedStart s_start;
   __shared__ long long s_scan[kThreads / 32];
-  __shared__ volatile int s_bad[4];    // of a segment, in turn: NaN was left out
+  // Of a segment, in turn: NaN was left out.  V is cleaned before its slot is waited for, so with short segments
+  // kV + 1 of them may be cleaned before one is put out and its flag cleared.
+  __shared__ volatile int s_bad[kFlags];
   __shared__ volatile int2 s_tell[kTells];  // A and B of a tile
   __shared__ uint8_t s_below[8][kKeys];  // how far a key's b is below B, of tiles whose V is to come
   __shared__ __align__(8) unsigned long long s_told[8];  // (K is widened up to four tiles before V) s_below and s_tell of a tile are there
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
   const uint32_t q_addr = smem_u32(s_q), ring = smem_u32(s_ring), codes = smem_u32(s_codes);
   if (tid == 0) {
     s_abort = 0;
-    for (int s = 0; s < 4; ++s) s_bad[s] = 0;
+    for (int s = 0; s < kFlags; ++s) s_bad[s] = 0;
     for (int s = 0; s < S::kSlots; ++s) {
       mbar_init(smem_u32(&s_full[s]), kWiden);
       mbar_init(smem_u32(&s_empty[s]), 1);
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
           if (lane == 0) mbar_arrive(smem_u32(&s_told[tile & 7]));
         } else {
           const int jn = t * kKeys + kt - wk.v.len;  // this key's node
-          if (jn >= 0 && clean_key<D>(from, jn < wk.nodes)) s_bad[seg & 3] = 1;
+          if (jn >= 0 && clean_key<D>(from, jn < wk.nodes)) s_bad[seg % kFlags] = 1;
           ok = __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_told[tile & 7]), (tile >> 3) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
           if (!ok) break;
           below = s_below[tile & 7][kt];
@@ -566,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
         f1 = b.x == -INFINITY ? 1.f : ex2(b.x - M);
         lsum = a.y * f0 + b.y * f1;
       }
-      const int bad = s_bad[seg & 3];
+      const int bad = s_bad[seg % kFlags];
       const float z = (M == -INFINITY ? 0.f : M) - kBias;
       const int c0 = DUAL ? 0 : w * (D / 2), c1 = DUAL ? D : c0 + D / 2;
       const bool whole = wk.whole();
@@ -617,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
       }
       tc_fence_before();
       bar_sync_n(1, 256);  // O, Q's place and s_bad are read
-      if (tid == 0) s_bad[seg & 3] = 0;
+      if (tid == 0) s_bad[seg % kFlags] = 0;
       ++seg;
     }
   }
