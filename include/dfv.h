@@ -47,8 +47,8 @@
  *     synchronised): concurrent use races.
  *     Which calls may share one: those of a family, namely (1) dfv_route_topk
  *     and the MoE block and stack calls, (2) dfv_moe_batch_forward, (3)
- *     dfv_accept_greedy, (4) all tree-verify calls (attention, logits, cache
- *     commit and pages).  A workspace that a call of one family has used must be
+ *     dfv_accept_greedy, (4) all tree-verify calls (attention of nodes and of
+ *     prompts, logits, cache commit and pages).  A workspace that a call of one family has used must be
  *     zero-filled again before a call of another takes it: what one leaves
  *     behind lies where another keeps its counters, and nothing detects that.
  *   - Returns DFV_OK (0) or a DFV_ERR_* status; dfv_status_string() names it

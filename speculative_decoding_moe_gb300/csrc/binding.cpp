@@ -1,4 +1,4 @@
-// binding.cpp -- the hot calls of the tree-verify binding as a CPython extension:
+// binding.cpp -- the hot calls of the tree-verify and prompt binding as a CPython extension:
 // argument checks, result allocation and the C ABI call in one step.
 //
 // A decode step makes dozens of these calls, and checking and marshalling one in

@@ -38,9 +38,19 @@
 // see, are taken out and given back to the rows that see them at the end.
 //
 // Warps 0-3 and 4-7 are the two warpgroups, warps 8 and 10 stream K and V blocks
-// with TMA into one ring in the order the MMAs use them (half of the head, or half
+// with TMA into a ring each in the order the MMAs use them (half of the head, or half
 // of the keys, each), warp 9 issues the MMAs, warp 11 copies Q and cleans V.
 // Tensor memory: NB places of scores, P (16-bit pairs) over them, then O0 O1.
+//
+// What binds.  With heads of 128 the tensor core: a block takes 2048 clocks of
+// products and 2700 in all.  With heads of 64 the exponentials (128 x 256 a block at
+// 32 a clock: 1024, as long as its products).  Measured (GB300, device time): 16381
+// tokens of 32 heads of 128 over 4 kv heads 1400 us, 1.57 PFLOP/s of 1.88; 16 prompts
+// of up to 2039 tokens 323 us (0.99 PFLOP/s: a tile's start and output cost it 8000
+// clocks beside 2700 a block); 2 x 1021 tokens behind 30011 with heads of 64 431 us.
+// Not kept: P handed on in halves (1384 -> 1459 us), the maximum in a pass of its own
+// (1504 -> 1527; heads of 64 458 -> 508), ranges that end at tiles with longer prompts
+// too (50 -> 55 us for one prompt of 2039 tokens).
 #include <cstdio>
 
 #include <cudaTypedefs.h>
@@ -150,12 +160,19 @@ __device__ __forceinline__ long long head_units(const PromptLaunch &L, const Pro
   return m == 0 ? 0 : (long long)kOver * m + blocks_before(L, s, m - 1) + blocks_of(L, s, m - 1);
 }
 
+// The start of a kernel is a chain of reads and divisions that nothing overlaps: what it
+// finds out is kept for all warps, and divisions are of 32 bits where the numbers are
+// (one prompt of 137 tokens 12.4 -> 11.0 us).
 struct PromptStart {
   long long u0, u1, base;  // the range, and the first unit of sequence b
   long long U;             // units
+  long long per;           // units of a head of b
   int b, G;                // ranges in use
+  PromptSeq s;             // b
 };
-__device__ __forceinline__ long long range_start(int g, long long U, int G) { return g * U / G; }
+__device__ __forceinline__ long long range_start(int g, long long U, int G) {
+  return U < 1 << 24 ? (uint32_t)g * (uint32_t)U / (uint32_t)G : g * U / G;  // (G <= 152)
+}
 __device__ __forceinline__ int range_of(long long u, long long U, int G) { return (int)(((u + 1) * G - 1) / U); }
 
 // The range of CTA `g` and the sequence it starts in; all threads of the CTA call it.
@@ -163,8 +180,14 @@ __device__ __forceinline__ void prompt_start(const PromptLaunch &L, int g, long 
   const PromptParams &p = L.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.n_seqs;
   const int per = (n + kThreads - 1) / kThreads, b0 = min(n, tid * per), b1 = min(n, b0 + per);
-  long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += p.Hkv * head_units(L, prompt_seq(p, b));
+  long long sum = 0, units = 0;
+  PromptSeq s = {0, 0, 0, 0};
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    s = prompt_seq(p, b);
+    units = head_units(L, s);
+    sum += p.Hkv * units;
+  }
   long long run = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -178,24 +201,31 @@ __device__ __forceinline__ void prompt_start(const PromptLaunch &L, int g, long 
   }
   __syncthreads();
   long long U = 0, at = run - sum;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) at += s_scan[w];
-    U += s_scan[w];
+    const long long x = s_scan[w];
+    if (w < warp) at += x;
+    U += x;
   }
   const int G = U >= kAttnCtas ? kAttnCtas : U > 0 ? (int)U : 1;
   const long long u0 = range_start(g, U, G), u1 = g < G ? range_start(g + 1, U, G) : u0;
   if (u0 < u1 && at <= u0 && u0 < at + sum) {
     long long base = at;
-    for (int b = b0; b < b1; ++b) {
-      const long long c = per == 1 ? sum : p.Hkv * head_units(L, prompt_seq(p, b));
-      if (base <= u0 && u0 < base + c) {
-        out->u0 = u0;
-        out->u1 = u1;
-        out->base = base;
-        out->b = b;
-      }
-      base += c;
+    int b = b0;
+#pragma unroll 1
+    while (per > 1) {  // the one of this thread's that has u0
+      s = prompt_seq(p, b);
+      units = head_units(L, s);
+      if (u0 < base + p.Hkv * units) break;
+      base += p.Hkv * units;
+      ++b;
     }
+    out->u0 = u0;
+    out->u1 = u1;
+    out->base = base;
+    out->per = units;
+    out->b = b;
+    out->s = s;
   }
   if (tid == 0) {
     out->U = U;
@@ -217,23 +247,26 @@ struct PromptWalk {
   PromptSeq s;
   __device__ __forceinline__ PromptWalk(const PromptLaunch &l, const PromptStart &st) : L(l), end(st.u1), u(st.u0), b(st.b), h(0), t(-1), m(0), p0(0), first(true) {
     if (u >= end) return;
-    s = prompt_seq(L.p, b);
+    s = st.s;
     m = tiles_of(L, s);
-    const long long per = head_units(L, s);
     long long w = u - st.base;
-    h = (int)(w / per);
-    w -= h * per;
-    // the last tile that begins at or before unit w of the head
+    h = (w | st.per) >> 31 ? (int)(w / st.per) : (int)((uint32_t)w / (uint32_t)st.per);
+    w -= h * st.per;
+    // the last tile that begins at or before unit w of the head: 32 places at a time, which
+    // a warp's lanes try together (the first one fits)
     int lo = 0, hi = m;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((long long)kOver * mid + blocks_before(L, s, mid) <= w)
-        lo = mid;
-      else
-        hi = mid;
+    long long at = 0;
+#pragma unroll 1
+    while (lo + 1 < hi) {
+      const int gap = (hi - lo + 31) >> 5, i = lo + gap * (int)(threadIdx.x & 31);
+      const long long begins = i < hi ? (long long)kOver * i + blocks_before(L, s, i) : 0;
+      const int last = 31 - __clz(__ballot_sync(0xffffffffu, i < hi && begins <= w));
+      at = __shfl_sync(0xffffffffu, begins, last);
+      lo += gap * last;
+      hi = min(hi, lo + gap);
     }
     t = lo;
-    p0 = (int)(w - ((long long)kOver * t + blocks_before(L, s, t)));
+    p0 = (int)(w - at);
     if (L.whole && p0) {  // it belongs to the range before
       u += kOver + blocks_of(L, s, t) - p0;
       p0 = 0;
@@ -442,6 +475,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   if (warp == 9) {
     tmem_alloc(smem_u32(&s_tmem), 512);
     tmem_relinquish();
+  }
+  if (warp == 11 && lane < 3) {
+    const CUtensorMap *map = lane == 0 ? &L.tm_q : lane == 1 ? &L.tm_k : &L.tm_v;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
   }
   // rows of Q that no copy writes
   for (int u = p.G * L.pos * (D / 8) + tid; u < kTile * (D / 8); u += kThreads)

@@ -34,6 +34,8 @@
 //   above      tcgen05 on 128-row tiles, scores and outputs in tensor memory
 //              (two 16-row tiles of mma.sync took 110 us where it takes 79:
 //              32 x 4 nodes of 8 heads over 8191 keys)
+// Caches in e4m3 codes have kernels of their own for both (tree_attn_codes.cu,
+// tree_attn_codes_tc.cu): the work split and the join are these.
 #include <cstdio>
 #include <cstring>
 

@@ -3,7 +3,7 @@ block-verify path runs in the library's CUDA kernels.  Tensors must be CUDA
 tensors; calls enqueue work on torch's current CUDA stream, or on the one given
 as `stream` (a result that the call makes is then in that stream's memory, as
 under torch.cuda.stream(stream)).  The block-verify
-calls go through ctypes; the tree-verify calls, which a step makes dozens of,
+calls go through ctypes; the tree-verify and prompt calls, which a step makes dozens of,
 through the extension built from csrc/binding.cpp."""
 from __future__ import annotations
 
@@ -176,7 +176,7 @@ _ext = None
 
 
 def _bind():
-    """The extension with the tree-verify calls."""
+    """The extension with the tree-verify and prompt calls."""
     global _ext
     if _ext is None:
         _load()
@@ -257,7 +257,7 @@ def workspace_size(layer: Layer, k_max: int) -> int:
 
 def alloc_workspace(nbytes: int, device="cuda") -> torch.Tensor:
     """Zero-filled workspace (the library requires zeros before first use).  One may serve several calls in stream order
-    if they are of one family: the MoE block and stack calls, the batched ones, accept_greedy, or all tree-verify calls."""
+    if they are of one family: the MoE block and stack calls, the batched ones, accept_greedy, or all tree-verify and prompt calls."""
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
