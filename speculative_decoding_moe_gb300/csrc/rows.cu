@@ -15,14 +15,18 @@
 // Both kernels are bound by memory: a row is read and written once.  A head is 16
 // elements a lane, in two 16-byte pieces of which one lane holds both sides of
 // its pairs (half layout: pieces half a rotation apart), so that the sums and
-// maxima over a head are shuffles within D / 16 lanes.  A CTA takes a few rows,
-// whose sines and cosines it finds once for all heads, while its first pieces are
-// on their way.
+// maxima over a head are shuffles within D / 16 lanes.  Append: a warp takes a row (or
+// a share of one, while there are few), finds the sines and cosines once for all its
+// heads, and walks the heads one at a time in a short loop with the next three on
+// their way by asynchronous copies into places of its lanes' own.
 //
 // Measured (GB300, device time): 8 prompts of up to 2039 rows of 32 + 2 x 4 heads of
-// 128, normed and turned, 59 us, 4.4 TB/s (with 4 CTAs an SM at 64 registers 72; two
-// pieces ahead instead of four 94 to 103); into codes and back, 4 x 1021 rows of 32 + 2
-// x 8 heads of 64 and the 17402 tokens of each, 49 us, 4.9 TB/s; one row 3 us.
+// 128, normed and turned, 47 us, 5.5 TB/s; into codes and back, 4 x 1021 rows of 32 + 2 x
+// 8 heads of 64 and the 17402 tokens of each, 47 us, 5.1 TB/s; one row 3 us.  Steps of
+// the first: four items loaded to registers at once, heads of several rows in turn 59
+// (fewer at once 94 to 103; fetching the unrolled items' instructions took longer than
+// what more loads at once gained); a warp a row, four items at once 62 to 66; by
+// asynchronous copies, four items a turn 58, two 50, one 48.
 #include <cfloat>
 
 #include "tree_common.cuh"
@@ -31,14 +35,14 @@ namespace dfv {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int kMaxRowsCta = 8;    // append: rows of a CTA
-constexpr int kAppendAhead = 4;   // items of a lane that are loaded at once
+constexpr int kMaxRowsCta = 8;  // append: rows of a CTA, a warp each
+constexpr int kAhead = 3, kPlaces = 4;  // append: items of a lane on their way, and places for them
 constexpr int kReadRows = 32;     // read: rows of a CTA
 constexpr int kReadAhead = 4;
 
 struct AppendLaunch {
   RopeParams p;
-  int rows;     // of a CTA
+  int rows;     // log2 of a CTA's
   int by_seq;   // rows are counted as (sequence, row of it) with max_nodes each
   int lanes;    // log2 of the lanes of a head
 };
@@ -103,15 +107,27 @@ __device__ __forceinline__ uint4 narrow(const float2 *x) {
   return make_uint4(pack2<F16>(x[0].x, x[0].y), pack2<F16>(x[1].x, x[1].y), pack2<F16>(x[2].x, x[2].y), pack2<F16>(x[3].x, x[3].y));
 }
 
+__device__ __forceinline__ void copy16(uint32_t to, const char *from, bool have) {  // zeros if not
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(have ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t from) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
+  return v;
+}
+
 // NORM: some gain is given.  INTER: pairs are neighbours.
 template <bool F16, bool CODES, bool NORM, bool INTER>
 __global__ void __launch_bounds__(kRowThreads, 3) append_kernel(const __grid_constant__ AppendLaunch L) {
-  __shared__ __align__(16) float2 s_cos[kMaxRowsCta][64], s_sin[kMaxRowsCta][64];  // of two pairs each
+  __shared__ __align__(16) float s_cos[kMaxRowsCta][128], s_sin[kMaxRowsCta][128];
   __shared__ int s_row[kMaxRowsCta], s_page[kMaxRowsCta], s_tok[kMaxRowsCta];
   const RopeParams &p = L.p;
   const CacheParams &c = p.c;
-  const int tid = threadIdx.x, first = blockIdx.x * L.rows, HK = p.H + c.Hkv, NH = HK + c.Hkv, items = L.rows * NH;
-  const int lid = tid & ((1 << L.lanes) - 1), group = tid >> L.lanes, groups = kRowThreads >> L.lanes;
+  const int tid = threadIdx.x, rows = 1 << L.rows, first = blockIdx.x << L.rows, HK = p.H + c.Hkv, NH = HK + c.Hkv;
+  // The CTA's threads are split among its rows; a row's groups of lanes take its heads in
+  // turn, queries first, then keys, then values.
+  const int lid = tid & ((1 << L.lanes) - 1), group = tid >> L.lanes, share = 8 - L.lanes - L.rows;  // log2 of a row's groups
+  const int j = group >> share, head0 = group & ((1 << share) - 1), step = 1 << share;
   const int n16 = c.D / 16, r16 = p.rot / 16;
   const bool on = lid < n16;
   // pieces of a turned head, and of one that is copied
@@ -119,33 +135,30 @@ __global__ void __launch_bounds__(kRowThreads, 3) append_kernel(const __grid_con
   pdl_trigger();
   pdl_wait();
 
-  // Items: head h of the CTA's row j, queries first, then keys, then values.  A lane's
-  // next item is `groups` further.
-  const int dj = groups / NH, dh = groups - dj * NH;
-  int lj = group / NH, lh = group - lj * NH;  // the next one to load
-  int cj = lj, ch = lh;                       // the next one to work on
-  uint4 x[kAppendAhead][2];
-  auto load = [&]() {
-#pragma unroll
-    for (int u = 0; u < kAppendAhead; ++u) {
-      x[u][0] = x[u][1] = make_uint4(0u, 0u, 0u, 0u);
-      const int row = lj >= L.rows ? -1 : L.by_seq ? s_row[lj] : first + lj;
-      if (on && (unsigned)row < (unsigned)p.t.n_rows) {
-        const char *src = lh < p.H ? p.q + 2 * (row * p.q_row + lh * p.q_head)
-                                   : lh < HK ? p.k + 2 * (row * p.k_row + (lh - p.H) * p.k_head) : p.v + 2 * (row * p.v_row + (lh - HK) * p.v_head);
-        const int2 at = lh < HK ? at_turned : at_plain;
-        x[u][0] = reinterpret_cast<const uint4 *>(src)[at.x];
-        x[u][1] = reinterpret_cast<const uint4 *>(src)[at.y];
-      }
-      lj += dj;
-      lh += dh;
-      if (lh >= NH) { lh -= NH; ++lj; }
+  // Items on their way to this lane, in two pieces each, in places of its own.
+  extern __shared__ __align__(16) unsigned char sm_x[];
+  const uint32_t mine = smem_u32(sm_x) + 16u * tid;
+  auto place = [&](int at, int piece) { return mine + (uint32_t)((2 * at + piece) * 16 * kRowThreads); };
+  auto load = [&](int to, int row, int h) {
+    if (on && h < NH) {
+      const bool have = (unsigned)row < (unsigned)p.t.n_rows;
+      const char *src = h < p.H ? p.q + 2 * (row * p.q_row + h * p.q_head)
+                                : h < HK ? p.k + 2 * (row * p.k_row + (h - p.H) * p.k_head) : p.v + 2 * (row * p.v_row + (h - HK) * p.v_head);
+      const int2 at = h < HK ? at_turned : at_plain;
+      if (!have) src = p.q;
+      copy16(place(to, 0), src + 16 * at.x, have);
+      copy16(place(to, 1), src + 16 * at.y, have);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if (!L.by_seq) load();
+  auto load_first = [&](int row) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(i, row, head0 + i * step);
+  };
+  if (!L.by_seq) load_first(first + j);
 
   // ---- whose rows, and where they go (one warp: a chain of reads)
-  if (tid < L.rows) {
+  if (tid < rows) {
     const int v = first + tid;
     int row = -1, pg = -1, tok = 0, b = -1;
     if (L.by_seq) {
@@ -171,131 +184,153 @@ __global__ void __launch_bounds__(kRowThreads, 3) append_kernel(const __grid_con
   }
   if (L.by_seq) {
     __syncthreads();
-    load();
+    load_first(s_row[j]);
   }
   // ---- sines and cosines, once for all heads (the other warps)
-  for (int u = tid - 32; u < L.rows * (p.rot / 2) && tid >= 32; u += kRowThreads - 32) {
-    const int j = u / (p.rot / 2), i = u - j * (p.rot / 2), row = L.by_seq ? s_row[j] : first + j;
+  for (int u = tid - 32; u < (p.rot / 2) << L.rows && tid >= 32; u += kRowThreads - 32) {
+    const int r = u / (p.rot / 2), i = u - r * (p.rot / 2), row = L.by_seq ? s_row[r] : first + r;
     if ((unsigned)row >= (unsigned)p.t.n_rows) continue;
     const uint64_t turn = (uint64_t)(long long)p.positions[row] * p.turns[i];
     float sn, cs;
     sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn, &cs);
-    reinterpret_cast<float *>(s_cos[j])[i] = cs * p.scale;
-    reinterpret_cast<float *>(s_sin[j])[i] = sn * p.scale;
+    s_cos[r][i] = cs * p.scale;
+    s_sin[r][i] = sn * p.scale;
   }
   __syncthreads();
+  const int row = s_row[j], pg = s_page[j], tok = s_tok[j];
+  // this lane's eight pairs: of its first piece's elements (half layout), or of both pieces
+  float2 cs[4], sn[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int at = INTER ? 2 * ((e < 2 ? at_turned.x : at_turned.y) * 2 + (e & 1)) : 8 * lid + 2 * e;
+    cs[e] = make_float2(1.f, 1.f);
+    sn[e] = make_float2(0.f, 0.f);
+    if (2 * at < p.rot) {
+      cs[e] = *reinterpret_cast<const float2 *>(&s_cos[j][at]);
+      sn[e] = *reinterpret_cast<const float2 *>(&s_sin[j][at]);
+    }
+  }
+  float2 g[8];  // the gain of this lane's elements: queries' first, then keys'
+  auto gains = [&](const char *from) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = make_float2(1.f, 1.f);
+    if (from && on) {
+      widen<F16>(__ldg(reinterpret_cast<const uint4 *>(from) + at_turned.x), g);
+      widen<F16>(__ldg(reinterpret_cast<const uint4 *>(from) + at_turned.y), g + 4);
+    }
+  };
+  bool of_q = head0 < p.H;
+  if (NORM) gains(of_q ? p.q_gain : p.k_gain);
 
-  for (int done = 0; done < items; done += kAppendAhead * groups) {
-    if (done) load();
-#pragma unroll
-    for (int u = 0; u < kAppendAhead; ++u) {
-      if (done + u * groups >= items) break;  // the same for all threads
-      const int j = cj < L.rows ? cj : 0, h = ch;
-      const bool have = cj < L.rows && on;
-      cj += dj;
-      ch += dh;
-      if (ch >= NH) { ch -= NH; ++cj; }
-      const int row = s_row[j], pg = s_page[j];
-      const bool isq = h < p.H, turned = h < HK;
-      const int2 at = turned ? at_turned : at_plain;
-      if (!CODES && !turned) {  // values as they are
-        if (have && pg >= 0) {
-          uint4 *to = reinterpret_cast<uint4 *>(c.v + 2 * kv_off(c, p.layer, pg, h - HK, s_tok[j]));
-          to[at.x] = x[u][0];
-          to[at.y] = x[u][1];
-        }
-        if (!NORM) continue;  // (with norms the warp's other heads sum over shuffles)
+  int at_x = 0;
+#pragma unroll 1
+  for (int h0 = 0; h0 < NH; h0 += step) {  // the same for all threads
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    const int h = h0 + head0;
+    const bool have = h < NH && on && row >= 0, isq = h < p.H, turned = h < HK;
+    const int2 at = turned ? at_turned : at_plain;
+    uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
+    if (on && h < NH) {
+      x0 = lds128(place(at_x, 0));
+      x1 = lds128(place(at_x, 1));
+    }
+    load((at_x + kAhead) % kPlaces, row, h + kAhead * step);  // where the item before was
+    at_x = (at_x + 1) % kPlaces;
+    if (!CODES && !turned) {  // values as they are
+      if (have && pg >= 0) {
+        uint4 *to = reinterpret_cast<uint4 *>(c.v + 2 * kv_off(c, p.layer, pg, h - HK, tok));
+        to[at.x] = x0;
+        to[at.y] = x1;
       }
-      float2 a[4], b[4];
-      widen<F16>(x[u][0], a);
-      widen<F16>(x[u][1], b);
-      if (NORM) {
-        float2 s2 = mul2(a[0], a[0]);
-        s2 = fma2(b[0], b[0], s2);
-#pragma unroll
-        for (int e = 1; e < 4; ++e) s2 = fma2(b[e], b[e], fma2(a[e], a[e], s2));
-        float ss = s2.x + s2.y;
-        for (int o = 1 << L.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const char *gain = isq ? p.q_gain : p.k_gain;
-        if (turned && gain && on) {
-          const float2 inv = both(rsqrtf(ss / (float)c.D + p.eps));
-          float2 g[4];
-          widen<F16>(__ldg(reinterpret_cast<const uint4 *>(gain) + at.x), g);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) a[e] = mul2(mul2(a[e], inv), g[e]);
-          widen<F16>(__ldg(reinterpret_cast<const uint4 *>(gain) + at.y), g);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) b[e] = mul2(mul2(b[e], inv), g[e]);
-        }
+      if (!NORM || h0 >= HK) continue;  // (with norms the warp's other heads sum over shuffles)
+    }
+    float2 a[4], b[4];
+    widen<F16>(x0, a);
+    widen<F16>(x1, b);
+    if (NORM) {
+      if (of_q && !isq) {
+        of_q = false;
+        gains(p.k_gain);
       }
-      if (turned && on) {
-        if (INTER) {
+      float2 s2 = mul2(a[0], a[0]), s3 = mul2(b[0], b[0]);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int piece = q ? at.y : at.x;
-            float2 *y = q ? b : a;
-            if (piece < 2 * r16) {
-              const float4 cs = *reinterpret_cast<const float4 *>(&s_cos[j][2 * piece]), sn = *reinterpret_cast<const float4 *>(&s_sin[j][2 * piece]);
-              const float *cp = &cs.x, *sp = &sn.x;
+      for (int e = 1; e < 4; ++e) {
+        s2 = fma2(a[e], a[e], s2);
+        s3 = fma2(b[e], b[e], s3);
+      }
+      float ss = (s2.x + s2.y) + (s3.x + s3.y);
+      for (int o = 1 << L.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (turned && (isq ? p.q_gain : p.k_gain)) {
+        const float2 inv = both(rsqrtf(ss / (float)c.D + p.eps));
 #pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] = fma2(make_float2(-y[e].y, y[e].x), both(sp[e]), mul2(y[e], both(cp[e])));
-            }
-          }
-        } else if (lid < r16) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 cs = s_cos[j][4 * lid + e], sn = s_sin[j][4 * lid + e], a0 = a[e];
-            a[e] = fma2(make_float2(-b[e].x, -b[e].y), sn, mul2(a0, cs));
-            b[e] = fma2(a0, sn, mul2(b[e], cs));
-          }
+        for (int e = 0; e < 4; ++e) {
+          a[e] = mul2(mul2(a[e], inv), g[e]);
+          b[e] = mul2(mul2(b[e], inv), g[4 + e]);
         }
       }
-      float top = 0.f;
-      if (CODES) {  // of the finite elements; the others become NaN
+    }
+    if (turned) {
+      if (INTER) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float2 *y = q ? b : a;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (!(fabsf(y[e].x) <= FLT_MAX)) y[e].x = NAN;
-            if (!(fabsf(y[e].y) <= FLT_MAX)) y[e].y = NAN;
-            top = fmaxf(top, fmaxf(fabsf(y[e].x), fabsf(y[e].y)));  // fmaxf passes NaN over
-          }
+        for (int e = 0; e < 8; ++e) {
+          float2 &y = e < 4 ? a[e] : b[e - 4];
+          const float2 c2 = cs[e / 2], s2 = sn[e / 2];
+          if ((e < 4 ? at.x : at.y) < 2 * r16) y = fma2(make_float2(-y.y, y.x), both(e & 1 ? s2.y : s2.x), mul2(y, both(e & 1 ? c2.y : c2.x)));
         }
-        for (int o = 1 << L.lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      }
-      if (!have || row < 0) continue;
-      if (isq) {
-        uint4 *to = reinterpret_cast<uint4 *>(p.o + 2 * (row * p.o_row + h * p.o_head));
-        to[at.x] = narrow<F16>(a);
-        to[at.y] = narrow<F16>(b);
-        continue;
-      }
-      if (turned && p.ko) {
-        uint4 *to = reinterpret_cast<uint4 *>(p.ko + 2 * (row * p.ko_row + (h - p.H) * p.ko_head));
-        to[at.x] = narrow<F16>(a);
-        to[at.y] = narrow<F16>(b);
-      }
-      if (pg < 0) continue;
-      if (CODES) {
-        const int kh = turned ? h - p.H : h - HK;
-        const int e = exponent_of(top);
-        const float f = exp_value((uint32_t)(127 - e));
-        uint2 *to = reinterpret_cast<uint2 *>((turned ? c.k : c.v) + kv_off(c, p.layer, pg, kh, s_tok[j]));
+      } else if (lid < r16) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float2 *y = q ? b : a;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], both(f));
-          to[q ? at.y : at.x] = make_uint2(codes_of(y[0].x, y[0].y) | codes_of(y[1].x, y[1].y) << 16,
-                                           codes_of(y[2].x, y[2].y) | codes_of(y[3].x, y[3].y) << 16);
+        for (int e = 0; e < 4; ++e) {
+          const float2 a0 = a[e];
+          a[e] = fma2(make_float2(-b[e].x, -b[e].y), sn[e], mul2(a0, cs[e]));
+          b[e] = fma2(a0, sn[e], mul2(b[e], cs[e]));
         }
-        if (lid == 0) (turned ? c.ke : c.ve)[exp_off(c, p.layer, pg, kh, s_tok[j])] = (uint8_t)(e + 127);
-      } else if (turned) {
-        uint4 *to = reinterpret_cast<uint4 *>(c.k + 2 * kv_off(c, p.layer, pg, h - p.H, s_tok[j]));
-        to[at.x] = narrow<F16>(a);
-        to[at.y] = narrow<F16>(b);
       }
+    }
+    float top = 0.f;
+    if (CODES) {  // of the finite elements; the others become NaN
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float2 *y = q ? b : a;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (!(fabsf(y[e].x) <= FLT_MAX)) y[e].x = NAN;
+          if (!(fabsf(y[e].y) <= FLT_MAX)) y[e].y = NAN;
+          top = fmaxf(top, fmaxf(fabsf(y[e].x), fabsf(y[e].y)));  // fmaxf passes NaN over
+        }
+      }
+      for (int o = 1 << L.lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    if (!have) continue;
+    if (isq) {
+      uint4 *to = reinterpret_cast<uint4 *>(p.o + 2 * (row * p.o_row + h * p.o_head));
+      to[at.x] = narrow<F16>(a);
+      to[at.y] = narrow<F16>(b);
+      continue;
+    }
+    if (turned && p.ko) {
+      uint4 *to = reinterpret_cast<uint4 *>(p.ko + 2 * (row * p.ko_row + (h - p.H) * p.ko_head));
+      to[at.x] = narrow<F16>(a);
+      to[at.y] = narrow<F16>(b);
+    }
+    if (pg < 0) continue;
+    if (CODES) {
+      const int kh = turned ? h - p.H : h - HK;
+      const int e = exponent_of(top);
+      const float f = exp_value((uint32_t)(127 - e));
+      uint2 *to = reinterpret_cast<uint2 *>((turned ? c.k : c.v) + kv_off(c, p.layer, pg, kh, tok));
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float2 *y = q ? b : a;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], both(f));
+        to[q ? at.y : at.x] = make_uint2(codes_of(y[0].x, y[0].y) | codes_of(y[1].x, y[1].y) << 16,
+                                         codes_of(y[2].x, y[2].y) | codes_of(y[3].x, y[3].y) << 16);
+      }
+      if (lid == 0) (turned ? c.ke : c.ve)[exp_off(c, p.layer, pg, kh, tok)] = (uint8_t)(e + 127);
+    } else if (turned) {
+      uint4 *to = reinterpret_cast<uint4 *>(c.k + 2 * kv_off(c, p.layer, pg, h - p.H, tok));
+      to[at.x] = narrow<F16>(a);
+      to[at.y] = narrow<F16>(b);
     }
   }
 }
@@ -399,12 +434,13 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
 template <bool F16, bool CODES>
 cudaError_t append_typed(const AppendLaunch &L, cudaStream_t s) {
   const long long rows = L.by_seq ? (long long)L.p.t.n_seqs * L.p.t.max_nodes : L.p.t.n_rows;
-  const dim3 grid((unsigned)((rows + L.rows - 1) / L.rows)), block(kRowThreads);
+  const dim3 grid((unsigned)((rows + (1 << L.rows) - 1) >> L.rows)), block(kRowThreads);
+  constexpr size_t smem = kPlaces * 2 * 16 * kRowThreads;
   if (L.p.q_gain || L.p.k_gain)
-    return L.p.inter ? launch_chained(append_kernel<F16, CODES, true, true>, grid, block, 0, s, L)
-                     : launch_chained(append_kernel<F16, CODES, true, false>, grid, block, 0, s, L);
-  return L.p.inter ? launch_chained(append_kernel<F16, CODES, false, true>, grid, block, 0, s, L)
-                   : launch_chained(append_kernel<F16, CODES, false, false>, grid, block, 0, s, L);
+    return L.p.inter ? launch_chained(append_kernel<F16, CODES, true, true>, grid, block, smem, s, L)
+                     : launch_chained(append_kernel<F16, CODES, true, false>, grid, block, smem, s, L);
+  return L.p.inter ? launch_chained(append_kernel<F16, CODES, false, true>, grid, block, smem, s, L)
+                   : launch_chained(append_kernel<F16, CODES, false, false>, grid, block, smem, s, L);
 }
 
 }  // namespace
@@ -414,9 +450,10 @@ cudaError_t launch_norm_rope_append(const RopeParams &p, cudaStream_t s) {
   L.p = p;
   L.by_seq = p.by_seq;
   L.lanes = head_lanes(p.c.D);
-  // rows for two rounds of a CTA's loads, one row while there are fewer CTAs than SMs hold
-  const int fit = 2 * kAppendAhead * (kRowThreads >> L.lanes) / (p.H + 2 * p.c.Hkv);
-  L.rows = p.t.n_rows <= 4 * kAttnCtas || fit < 1 ? 1 : fit > kMaxRowsCta ? kMaxRowsCta : fit;
+  // a warp a row, more of them while there would be fewer CTAs than the SMs hold
+  const long long n = L.by_seq ? (long long)p.t.n_seqs * p.t.max_nodes : p.t.n_rows;
+  L.rows = 3;
+  while (L.rows > 0 && n >> L.rows < 2 * kAttnCtas) --L.rows;
   if (p.c.esh == 0) return append_typed<false, true>(L, s);
   return p.c.f16 ? append_typed<true, false>(L, s) : append_typed<false, false>(L, s);
 }
