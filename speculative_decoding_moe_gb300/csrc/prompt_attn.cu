@@ -439,9 +439,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   // By warpgroup and the block's parity: with three places of scores a warpgroup and the
   // MMA warp can be one block apart, and a wait by parity must not find two phases done.
   __shared__ __align__(8) unsigned long long s_sfull[2][2], s_pready[2][2];
-  // V to be cleaned is there, and clean.  (The cleaning warp asks the ring's barriers only
-  // about a block that the MMA warp holds: not seeing all their phases, it cannot tell a
-  // phase to come from the one before.)
+  // V may be cleaned once it is there, and is clean.  (Not seeing all phases of the ring's
+  // barriers, the cleaning warp cannot tell a phase to come from the one before: it asks
+  // about a block only when the MMA warp has had the one before in its slot, which it has
+  // a block ahead.)
   __shared__ __align__(8) unsigned long long s_dirty, s_clean;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
@@ -633,16 +634,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         if (!ok) break;
         qk(0, false);
       }
+      if (j0 <= 0 && lane == 0) mbar_arrive(smem_u32(&s_dirty));
       for (int j = 0; j < n; ++j) {  // the next scores right after a product freed their place
         const bool more = j + 1 < n, more2 = j + NB - 1 < n;
         int steps = kKeys / 16;
         if (j >= j0) {
           steps = steps_of(L, wk.s, wk.t, wk.t0 + j);
-          wait(s_full[S::kK + vst], vph);
-          if (ok && lane == 0) mbar_arrive(smem_u32(&s_dirty));
           wait(s_clean, cleaned & 1u);
           ++cleaned;
         }
+        if (j + 1 >= j0 && more && ok && lane == 0) mbar_arrive(smem_u32(&s_dirty));
         ready(0, NB == 2 && more ? 0 : -1);
         if (!ok) break;
         pv(0, j == 0, j == n - 1, steps);
