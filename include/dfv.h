@@ -728,7 +728,8 @@ int dfv_pages_free(const dfv_kv_cache *cache, const int32_t *seqs, int n, void *
  * The rows of one call: sequence b of the call owns rows row_off[b] ..
  * row_off[b+1] of every [n_rows, ...] argument, at most max_rows and possibly
  * none.  row_off does not decrease.
- *   seq      [n_seqs] int32 cache sequence of each, all different, or NULL: b itself
+ *   seq      [n_seqs] int32 cache sequence of each, all different (dfv_cache_read:
+ *            in any number), or NULL: b itself
  *   row_off  [n_seqs + 1] int32
  * n_seqs <= DFV_MAX_TREE_SEQS, n_rows and max_rows <= DFV_MAX_ROWS.
  */

@@ -603,7 +603,7 @@ class RowBatch:
         self._handle = CRowsHandle(self.c, at)
         self.c = self._handle.c
         self.ref = ctypes.byref(self.c)
-        self.addr = ctypes.addressof(self._handle)
+        self.rows_addr = ctypes.addressof(self._handle)  # (not `addr`: a TreeBatch is another descriptor)
 
 
 class Rope:
@@ -659,7 +659,7 @@ def norm_rope_append(cache: KVCache, layer: int, rows: RowBatch, rope: Rope, q: 
     the cache behind the committed tokens, for any number of rows.  q_gain, k_gain [dim]: the gains of the norm over each
     head's elements (None: no norm); q [rows, heads, dim], k and v [rows, kv heads, dim] may be slices of one projection.
     k_out: optional rows that receive the normed and rotated k too (k itself is fine), for prompt_attention."""
-    return (_ext or _bind()).norm_rope_append(cache.addr, layer, rows.addr, rope.head_dim, rope.rot_dim, rope.interleaved,
+    return (_ext or _bind()).norm_rope_append(cache.addr, layer, rows.rows_addr, rope.head_dim, rope.rot_dim, rope.interleaved,
                                               rope.scale, rope.turns_addr, q, k, v, positions, q_gain, k_gain, eps, out,
                                               _on(stream, cache.index), rope.index, k_out)
 
@@ -668,7 +668,7 @@ def cache_read(cache: KVCache, layer: int, rows: RowBatch, k: Optional[torch.Ten
                v: Optional[torch.Tensor] = None, stream=None):
     """(k, v) [rows, kv heads, dim]: row i of a sequence is its token i in the cache, counted from its first one (tokens
     that were appended but not committed yet too); a float8_e4m3fn cache gives bf16."""
-    return (_ext or _bind()).cache_read(cache.addr, layer, rows.addr, cache.k, k, v, _on(stream, cache.index))
+    return (_ext or _bind()).cache_read(cache.addr, layer, rows.rows_addr, cache.k, k, v, _on(stream, cache.index))
 
 
 def prompt_attention_workspace_size(rows: RowBatch, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -682,7 +682,7 @@ def prompt_attention(rows: RowBatch, q: torch.Tensor, k: torch.Tensor, v: torch.
     keys: the key rows of each sequence when they are not its q rows (the q rows are then the last of them); scale:
     1/sqrt(dim) by default; lse: optional fp32 [rows, heads] that receives ln(sum exp); err: optional int32 [1] that
     receives KVERR_LEN for offsets out of range."""
-    return (_ext or _bind()).prompt_attention(rows.addr, 0 if keys is None else keys.addr, q, k, v, ws, scale, out, lse, err,
+    return (_ext or _bind()).prompt_attention(rows.rows_addr, 0 if keys is None else keys.rows_addr, q, k, v, ws, scale, out, lse, err,
                                               _on(stream, rows.index))
 
 

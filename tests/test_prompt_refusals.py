@@ -176,6 +176,13 @@ def test_binding_arguments(dfv):
     for kw in (dict(q_gain=gain.float()), dict(out=q.half()), dict(k_out=kv.half())):
         with pytest.raises(TypeError):
             dfv.norm_rope_append(c, 0, r, rope, q, kv, kv, pos, **kw)
+    tree = dfv.TreeBatch(off, 5, 3)  # another descriptor
+    for call in (lambda: dfv.norm_rope_append(c, 0, tree, rope, q, kv, kv, pos), lambda: dfv.cache_read(c, 0, tree),
+                 lambda: dfv.prompt_attention(tree, q, kv, kv, ws), lambda: dfv.prompt_attention(r, q, kv, kv, ws, keys=tree),
+                 lambda: dfv.tree_attention(c, 0, r, q, ws), lambda: dfv.rope_append(c, 0, r, rope, q, kv, kv, pos),
+                 lambda: dfv.cache_commit(c, r, pos.view(1, 5), pos[:2], ws)):
+        with pytest.raises(AttributeError):
+            call()
     with pytest.raises(TypeError):  # rows of a cache in codes are bf16
         dfv.norm_rope_append(c, 0, r, rope, q.half(), kv.half(), kv.half(), pos)
     with pytest.raises(ValueError):
