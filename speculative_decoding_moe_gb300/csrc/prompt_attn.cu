@@ -66,7 +66,9 @@ constexpr int kKeys = 128;   // of a block
 constexpr int kTile = 256;   // rows of a tile
 constexpr int kThreads = 384;
 constexpr int kOver = 3;     // blocks' worth of time that a tile costs at least
-constexpr int kWholeKeys = 1536;  // tiles are cut where a sequence may have more keys
+// Tiles are cut where a sequence may have more keys (whole and cut: 16 prompts of 600
+// tokens 66 and 71 us, one of 1200 25 and 31, one of 2039 53 and 50)
+constexpr int kWholeKeys = 1536;
 
 template <int D>
 struct PromptShape {
@@ -829,11 +831,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
 
 // ---------------------------------------------------------------- join
 // A CTA joins 32 rows of the tile that begins in a range and goes on behind it: a
-// lane per row, a warp per D / 8 elements of the head.
-constexpr int kJoinWarps = 8, kJoinRows = 32;
+// lane per row, a warp per D / 8 elements of the head.  One pass in range order, four
+// states' loads at once: with few rows over many keys a tile is in dozens of ranges (3 x 2
+// rows behind 29412 keys 47 us in two passes, 32; sixteen warps and eight states 35, and 5
+// more than these where tiles are in two ranges).
+constexpr int kJoinWarps = 8, kJoinRows = 32, kJoinAhead = 4;
 
 template <bool F16, int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const __grid_constant__ PromptLaunch L) {
+__global__ void __launch_bounds__(32 * kJoinWarps, 2) prompt_join_kernel(const __grid_constant__ PromptLaunch L) {
   constexpr int kPer = D / 4 / kJoinWarps;  // float4 of a thread
   const PromptParams &p = L.p;
   const int g0 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rr = blockIdx.y * kJoinRows + lane;
@@ -847,28 +852,47 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prompt_join_kernel(const __gr
   if (g >= p.G || i >= s.n) return;
   // state k is range g0 + k's; the tile goes on after the first and began before the others
   auto slot = [&](int k) { return (size_t)(2 * (g0 + k) + (k == 0)); };
-  float M = -INFINITY;
-  for (int k = 0; k < n; ++k) M = fmaxf(M, __ldcg(&L.part_ml[slot(k) * kTile + rr]).x);
   float4 x[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
+  float M = -INFINITY, l = 0.f;
   int bad = 0;
-#pragma unroll 2
-  for (int k = 0; k < n; ++k) {
-    const float2 ml = __ldcg(&L.part_ml[slot(k) * kTile + rr]);
-    bad |= __ldcg(&L.part_bad[slot(k)]);
-    const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - M);  // a state without keys holds zeros (or NaN of a NaN query)
-    l = fmaf(ml.y, f, l);
-    const float4 *from = reinterpret_cast<const float4 *>(L.part_o) + (slot(k) * (D / 4) + warp * kPer) * kTile + rr;
+#pragma unroll 1
+  for (int k0 = 0; k0 < n; k0 += kJoinAhead) {
+    float2 ml[kJoinAhead];
+    float4 y[kJoinAhead][kPer];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const float4 y = __ldcg(from + (size_t)e * kTile);
-      x[e].x = fmaf(y.x, f, x[e].x);
-      x[e].y = fmaf(y.y, f, x[e].y);
-      x[e].z = fmaf(y.z, f, x[e].z);
-      x[e].w = fmaf(y.w, f, x[e].w);
+    for (int u = 0; u < kJoinAhead; ++u) {
+      ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) y[u][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 + u < n) {
+        const size_t at = slot(k0 + u);
+        ml[u] = __ldcg(&L.part_ml[at * kTile + rr]);
+        bad |= __ldcg(&L.part_bad[at]);
+        const float4 *from = reinterpret_cast<const float4 *>(L.part_o) + (at * (D / 4) + warp * kPer) * kTile + rr;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) y[u][e] = __ldcg(from + (size_t)e * kTile);
+      }
     }
+    float top = M;
+#pragma unroll
+    for (int u = 0; u < kJoinAhead; ++u) top = fmaxf(top, ml[u].x);
+    // a state without keys holds zeros (or NaN of a NaN query)
+    auto weight = [&](float m) { return m == -INFINITY ? 1.f : ex2(m - top); };
+    auto join = [&](float f, float with, float4 *z, float m) {  // this so far times `with`, and a state times f
+      l = fmaf(m, f, l * with);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        x[e].x = fmaf(z[e].x, f, x[e].x * with);
+        x[e].y = fmaf(z[e].y, f, x[e].y * with);
+        x[e].z = fmaf(z[e].z, f, x[e].z * with);
+        x[e].w = fmaf(z[e].w, f, x[e].w * with);
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < kJoinAhead; ++u) join(weight(ml[u].x), u == 0 ? weight(M) : 1.f, y[u], ml[u].y);
+    M = top;
   }
   const size_t row = s.row0 + (size_t)i;
   const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
