@@ -177,6 +177,61 @@ def test_two_streams_at_once(dfv, kind):
             assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("kind", [BF, E4M3])
+def test_pages_behind_4_gb(dfv, kind):
+    """The same calls over pages whose bytes are more than 2^32 behind the cache's start give the same bits; what nobody wrote is
+    left as it is found there."""
+    total, H, K, D, page, some = [25, 17, 173], 32, 8, 128, 256, 8
+    far = (1 << 32) // (K * page * D * (1 if kind == E4M3 else 2)) + 5
+    qkv = torch.randn(sum(total), H + 2 * K, D, device="cuda", generator=torch.Generator(device="cuda").manual_seed(9)).to(BF)
+    pos = i32([i for n in total for i in range(n)])
+    rows, tree = batch(dfv, total), dfv.TreeBatch(i32([0, 1, 2, 6]), 6, 4)
+    got = []
+    for first in (0, far):
+        k, v = (torch.empty(1, first + some, K, page, D, dtype=kind, device="cuda") for _ in range(2))
+        exp = [torch.full((1, first + some, K, page), 127, dtype=torch.uint8, device="cuda") if kind == E4M3 else None for _ in range(2)]
+        table = i32([[first + 3, -1], [first + 6, -1], [first + 1, -1]])
+        cache = dfv.KVCache(k, v, table, i32([0, 0, 0]), k_exp=exp[0], v_exp=exp[1])
+        q = dfv.norm_rope_append(cache, 0, rows, dfv.Rope(D), qkv[:, :H], qkv[:, H:H + K], qkv[:, H + K:], pos)
+        back = dfv.cache_read(cache, 0, rows)
+        out = [q, *back]
+        for nodes in (tree, dfv.TreeBatch(i32([0, 8, 9, 17]), 17, 8)):  # few and many rows per kv head
+            cache.lens.copy_(i32([n - 8 for n in total]))
+            ws = dfv.alloc_workspace(dfv.tree_attention_workspace_size(cache, nodes, H))
+            out.append(dfv.tree_attention(cache, 0, nodes, q[:nodes.n_rows], ws))
+        assert cache.errors() == 0
+        got.append(out)
+        del k, v, cache
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_rows_behind_4_gb(dfv):
+    """Rows whose stride takes them past 2^32 bytes, as compact ones."""
+    n, H, K, D, pitch = 160, 8, 2, 128, 1 << 24
+    rows, keys = batch(dfv, [60, 100]), batch(dfv, [60, 100])
+    flat = torch.randn(n, H + 2 * K, D, device="cuda", generator=torch.Generator(device="cuda").manual_seed(10)).to(BF)
+    wide = torch.empty(n, pitch, dtype=BF, device="cuda")
+    part = lambda at, m: wide[:, at * D:(at + m) * D].unflatten(1, (m, D))  # noqa: E731
+    q, k, v, o = part(0, H), part(H, K), part(H + K, K), part(H + 2 * K, H)
+    for x, y in ((q, flat[:, :H]), (k, flat[:, H:H + K]), (v, flat[:, H + K:])):
+        x.copy_(y)
+    ws = dfv.alloc_workspace(dfv.prompt_attention_workspace_size(rows, H, K, D))
+    want = dfv.prompt_attention(rows, flat[:, :H], flat[:, H:H + K], flat[:, H + K:], ws)
+    dfv.prompt_attention(rows, q, k, v, ws, keys=keys, out=o)
+    assert torch.equal(o, want)
+    # and through the append and the read, in place
+    cache = dfv.KVCache.empty(1, 24, 16, K, D, 2, 12)
+    cache.page_table.copy_(torch.arange(24, dtype=torch.int32).view(2, 12))
+    pos = i32([*range(60), *range(100)])
+    want = dfv.norm_rope_append(cache, 0, rows, dfv.Rope(D), flat[:, :H], flat[:, H:H + K], flat[:, H + K:], pos)
+    kept = dfv.cache_read(cache, 0, rows)
+    dfv.norm_rope_append(cache, 0, rows, dfv.Rope(D), q, k, v, pos, out=q, k_out=k)
+    assert torch.equal(q, want) and torch.equal(k, kept[0])
+    dfv.cache_read(cache, 0, rows, k=o[:, :K], v=o[:, K:2 * K])
+    assert torch.equal(o[:, :K], kept[0]) and torch.equal(o[:, K:2 * K], kept[1])
+
+
 def test_the_same_sequence_twice(dfv):
     """Two parts of a call that read one sequence; for storing, a sequence may be in a call once."""
     r = Run(dfv, BF, 8, 2, 128, 16)
