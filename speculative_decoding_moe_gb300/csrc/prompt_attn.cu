@@ -45,9 +45,9 @@
 // What binds.  With heads of 128 the tensor core: a block takes 2048 clocks of
 // products and 2700 in all.  With heads of 64 the exponentials (128 x 256 a block at
 // 32 a clock: 1024, as long as its products).  Measured (GB300, device time): 16381
-// tokens of 32 heads of 128 over 4 kv heads 1400 us, 1.57 PFLOP/s of 1.88; 16 prompts
-// of up to 2039 tokens 323 us (0.99 PFLOP/s: a tile's start and output cost it 8000
-// clocks beside 2700 a block); 2 x 1021 tokens behind 30011 with heads of 64 431 us.
+// tokens of 32 heads of 128 over 4 kv heads 1375 us, 1.57 PFLOP/s of 1.88; 16 prompts
+// of up to 2039 tokens 316 us (1.02 PFLOP/s: a tile's start and output cost it 6500
+// clocks beside 2700 a block); 2 x 1021 tokens behind 30011 with heads of 64 430 us.
 // Not kept: P handed on in halves (1384 -> 1459 us), the maximum in a pass of its own
 // (1504 -> 1527; heads of 64 458 -> 508), ranges that end at tiles with longer prompts
 // too (50 -> 55 us for one prompt of 2039 tokens).
