@@ -43,8 +43,9 @@
 // Tensor memory: NB places of scores, P (16-bit pairs) over them, then O0 O1.
 //
 // What binds.  With heads of 128 the tensor core: a block takes 2048 clocks of
-// products and 2700 in all.  With heads of 64 the exponentials (128 x 256 a block at
-// 32 a clock: 1024, as long as its products).  Measured (GB300, device time): 16381
+// products and 2700 in all (16381 tokens without the softmax's arithmetic 1174 us).  With
+// heads of 64 a block takes 2050 clocks, 1600 without that arithmetic: products of 64
+// columns take longer than half of 128 columns' time.  Measured (GB300, device time): 16381
 // tokens of 32 heads of 128 over 4 kv heads 1375 us, 1.57 PFLOP/s of 1.88; 16 prompts
 // of up to 2039 tokens 316 us (1.02 PFLOP/s: a tile's start and output cost it 6500
 // clocks beside 2700 a block); 2 x 1021 tokens behind 30011 with heads of 64 430 us.
