@@ -232,6 +232,27 @@ def test_rows_behind_4_gb(dfv):
     assert torch.equal(o[:, :K], kept[0]) and torch.equal(o[:, K:2 * K], kept[1])
 
 
+@pytest.mark.parametrize("kind", [BF, E4M3])
+def test_a_given_stream(dfv, kind):
+    """Calls on a stream that is not the current one, their results of that stream's memory: as on the current one."""
+    r = Run(dfv, kind, 8, 2, 128, 16)
+    want = [x.clone() for x in r.first()]
+    r.cache.lens.zero_()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    x = r.qkv[0]
+    k = torch.empty_like(want[1])
+    s.wait_stream(torch.cuda.current_stream())
+    q = dfv.norm_rope_append(r.cache, 1, r.rows[0], r.rope, x[:, :8], x[:, 8:10], x[:, 10:], r.pos[0], q_gain=r.gains[0],
+                             k_gain=r.gains[1], k_out=k, stream=s)
+    back = dfv.cache_read(r.cache, 1, r.rows[0], stream=s)
+    o = dfv.prompt_attention(r.rows[0], q, k, x[:, 10:], r.ws, stream=s)
+    s.synchronize()
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(o, want[3])
+    for a, b in zip(back, dfv.cache_read(r.cache, 1, r.rows[0])):
+        assert torch.equal(a, b)
+
+
 def test_the_same_sequence_twice(dfv):
     """Two parts of a call that read one sequence; for storing, a sequence may be in a call once."""
     r = Run(dfv, BF, 8, 2, 128, 16)
