@@ -21,12 +21,12 @@
 // their way by asynchronous copies into places of its lanes' own.
 //
 // Measured (GB300, device time): 8 prompts of up to 2039 rows of 32 + 2 x 4 heads of
-// 128, normed and turned, 47 us, 5.5 TB/s; into codes and back, 4 x 1021 rows of 32 + 2 x
+// 128, normed and turned, 46 us, 5.6 TB/s; into codes and back, 4 x 1021 rows of 32 + 2 x
 // 8 heads of 64 and the 17402 tokens of each, 47 us, 5.1 TB/s; one row 3 us.  Steps of
 // the first: four items loaded to registers at once, heads of several rows in turn 59
 // (fewer at once 94 to 103; fetching the unrolled items' instructions took longer than
 // what more loads at once gained); a warp a row, four items at once 62 to 66; by
-// asynchronous copies, four items a turn 58, two 50, one 48.
+// asynchronous copies, four items a turn 58, two 50, one 48, without a division a head 46.
 #include <cfloat>
 
 #include "tree_common.cuh"
@@ -45,6 +45,7 @@ struct AppendLaunch {
   int rows;     // log2 of a CTA's
   int by_seq;   // rows are counted as (sequence, row of it) with max_nodes each
   int lanes;    // log2 of the lanes of a head
+  float inv_d;  // 1 / head_dim
 };
 struct ReadLaunch {
   CacheReadParams p;
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) append_kernel(const __grid_con
       float ss = (s2.x + s2.y) + (s3.x + s3.y);
       for (int o = 1 << L.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       if (turned && (isq ? p.q_gain : p.k_gain)) {
-        const float2 inv = both(rsqrtf(ss / (float)c.D + p.eps));
+        const float2 inv = both(rsqrtf(fmaf(ss, L.inv_d, p.eps)));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           a[e] = mul2(mul2(a[e], inv), g[e]);
@@ -450,6 +451,7 @@ cudaError_t launch_norm_rope_append(const RopeParams &p, cudaStream_t s) {
   L.p = p;
   L.by_seq = p.by_seq;
   L.lanes = head_lanes(p.c.D);
+  L.inv_d = 1.f / (float)p.c.D;
   // a warp a row; more of them while the CTAs, three an SM, run at once all the same (125
   // rows: eight warps a row 4.3 us, one 8.7; 807 rows: eight in two waves 8.4, four in one
   // 5.9, two 8.0)
