@@ -29,7 +29,7 @@
 // few its keys; the line is cut into one range per SM.  A tile that a range cuts
 // leaves states that a second launch joins in range order (no atomics: the same
 // bits every time).  Where no tile is long the ranges end at tiles instead, and
-// there is no second launch.  How many blocks the tiles before tile i have follows
+// there is no second launch; with no more tiles than SMs each has one.  How many blocks the tiles before tile i have follows
 // from a closed form, since the lengths are only known on the device.
 //
 // Masked places.  Scores beyond a row's limit are selected away.  V rows past the
@@ -47,7 +47,7 @@
 // heads of 64 a block takes 2050 clocks, 1600 without that arithmetic: products of 64
 // columns take longer than half of 128 columns' time.  Measured (GB300, device time): 16381
 // tokens of 32 heads of 128 over 4 kv heads 1375 us, 1.57 PFLOP/s of 1.88; 16 prompts
-// of up to 2039 tokens 316 us (1.02 PFLOP/s: a tile's start and output cost it 6500
+// of up to 2039 tokens 311 us (1.04 PFLOP/s: a tile's start and output cost it 6500
 // clocks beside 2700 a block); 2 x 1021 tokens behind 30011 with heads of 64 430 us.
 // Not kept: P handed on in halves (1384 -> 1459 us), the maximum in a pass of its own
 // (1504 -> 1527; heads of 64 458 -> 508), ranges that end at tiles with longer prompts
@@ -67,9 +67,13 @@ constexpr int kKeys = 128;   // of a block
 constexpr int kTile = 256;   // rows of a tile
 constexpr int kThreads = 384;
 constexpr int kOver = 3;     // blocks' worth of time that a tile costs at least
-// Tiles are cut where a sequence may have more keys (whole and cut: 16 prompts of 600
-// tokens 66 and 71 us, one of 1200 25 and 31, one of 2039 53 and 50)
+// Tiles are whole where no sequence has more keys (without a second launch; whole and cut: 16
+// prompts of 600 tokens 61 and 71 us, one of 1200 22 and 31, one of 2039 53 and 50), and where
+// there are many: each saves about two thirds of a block's time by not being cut, and ranges
+// end up to half the longest tile apart (16 prompts of 2039 311 and 318, 64 of 3000 2290 and
+// 2380; 8 of 4096 568 and 554, 4 of 8192 1330 and 1276).
 constexpr int kWholeKeys = 1536;
+enum PromptMode { kCut, kWhole, kOne };  // ranges cut tiles, end at tiles, are tiles
 
 template <int D>
 struct PromptShape {
@@ -87,7 +91,6 @@ struct PromptLaunch {
   PromptParams p;
   int pos;                 // positions of a tile
   int run, rise;           // so many tiles further, tiles have so many blocks more
-  int whole;               // ranges end at tiles
   uint32_t inv_pos;        // ceil(2^16 / pos)
   int4 *cut;               // [kAttnCtas] sequence, head, tile that begins in the range and goes on, ranges it is in (0: none)
   float2 *part_ml;         // [2 kAttnCtas][kTile] (M, l) of partial states
@@ -172,13 +175,16 @@ struct PromptStart {
   long long per;           // units of a head of b
   int b, G;                // ranges in use
   PromptSeq s;             // b
+  int h, t;                // where a CTA has one tile: its head, and its number
 };
 __device__ __forceinline__ long long range_start(int g, long long U, int G) {
   return U < 1 << 24 ? (uint32_t)g * (uint32_t)U / (uint32_t)G : g * U / G;  // (G <= 152)
 }
 __device__ __forceinline__ int range_of(long long u, long long U, int G) { return (int)(((u + 1) * G - 1) / U); }
 
-// The range of CTA `g` and the sequence it starts in; all threads of the CTA call it.
+// The range of CTA `g` and the sequence it starts in; all threads of the CTA call it.  (Where
+// ranges are tiles no units are counted.)
+template <int MODE>
 __device__ __forceinline__ void prompt_start(const PromptLaunch &L, int g, long long *s_scan, PromptStart *out) {
   const PromptParams &p = L.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.n_seqs;
@@ -188,7 +194,7 @@ __device__ __forceinline__ void prompt_start(const PromptLaunch &L, int g, long 
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     s = prompt_seq(p, b);
-    units = head_units(L, s);
+    units = MODE == kOne ? tiles_of(L, s) : head_units(L, s);
     sum += p.Hkv * units;
   }
   long long run = sum;
@@ -211,14 +217,14 @@ __device__ __forceinline__ void prompt_start(const PromptLaunch &L, int g, long 
     U += x;
   }
   const int G = U >= kAttnCtas ? kAttnCtas : U > 0 ? (int)U : 1;
-  const long long u0 = range_start(g, U, G), u1 = g < G ? range_start(g + 1, U, G) : u0;
+  const long long u0 = MODE == kOne ? g : range_start(g, U, G), u1 = MODE == kOne ? min((long long)g + 1, max(U, (long long)g)) : g < G ? range_start(g + 1, U, G) : u0;
   if (u0 < u1 && at <= u0 && u0 < at + sum) {
     long long base = at;
     int b = b0;
 #pragma unroll 1
     while (per > 1) {  // the one of this thread's that has u0
       s = prompt_seq(p, b);
-      units = head_units(L, s);
+      units = MODE == kOne ? tiles_of(L, s) : head_units(L, s);
       if (u0 < base + p.Hkv * units) break;
       base += p.Hkv * units;
       ++b;
@@ -229,6 +235,11 @@ __device__ __forceinline__ void prompt_start(const PromptLaunch &L, int g, long 
     out->per = units;
     out->b = b;
     out->s = s;
+    if (MODE == kOne) {
+      const int w = (int)(u0 - base);
+      out->h = w / (int)units;
+      out->t = w - out->h * (int)units;
+    }
   }
   if (tid == 0) {
     out->U = U;
@@ -238,6 +249,7 @@ __device__ __forceinline__ void prompt_start(const PromptLaunch &L, int g, long 
 }
 
 // Segments of a range: blocks [t0, t1) of one tile.
+template <int MODE>
 struct PromptWalk {
   const PromptLaunch &L;
   const long long end;
@@ -251,6 +263,11 @@ struct PromptWalk {
   __device__ __forceinline__ PromptWalk(const PromptLaunch &l, const PromptStart &st) : L(l), end(st.u1), u(st.u0), b(st.b), h(0), t(-1), m(0), p0(0), first(true) {
     if (u >= end) return;
     s = st.s;
+    if (MODE == kOne) {
+      h = st.h;
+      t = st.t;
+      return;
+    }
     m = tiles_of(L, s);
     long long w = u - st.base;
     h = (w | st.per) >> 31 ? (int)(w / st.per) : (int)((uint32_t)w / (uint32_t)st.per);
@@ -270,13 +287,21 @@ struct PromptWalk {
     }
     t = lo;
     p0 = (int)(w - at);
-    if (L.whole && p0) {  // it belongs to the range before
+    if (MODE == kWhole && p0) {  // it belongs to the range before
       u += kOver + blocks_of(L, s, t) - p0;
       p0 = 0;
       ++t;
     }
   }
   __device__ __forceinline__ bool next() {
+    if (MODE == kOne) {
+      if (u >= end) return false;
+      ++u;
+      T = blocks_of(L, s, t);
+      t0 = 0;
+      t1 = T;
+      return true;
+    }
     for (;;) {
       if (!first) ++t;
       first = false;
@@ -291,7 +316,7 @@ struct PromptWalk {
         }
       }
       T = blocks_of(L, s, t);
-      const int units = kOver + T, p1 = L.whole ? units : (int)min((long long)units, p0 + (end - u));
+      const int units = kOver + T, p1 = MODE != kCut ? units : (int)min((long long)units, p0 + (end - u));
       last = u - p0 + units - 1;
       t0 = max(0, p0 - kOver);
       t1 = max(0, p1 - kOver);
@@ -300,7 +325,7 @@ struct PromptWalk {
       if (t0 < t1) return true;
     }
   }
-  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == T; }
+  __device__ __forceinline__ bool whole() const { return MODE != kCut || (t0 == 0 && t1 == T); }
   // Partial states of a range: of a tile that began before it, and of one that goes
   // on after it.
   __device__ __forceinline__ int slot(int g) const { return 2 * g + (t0 == 0); }
@@ -431,7 +456,10 @@ __device__ __forceinline__ void turn_quads(uint4 (&x)[4]) {
   }
 }
 
-template <bool F16, int D>
+// (A kernel for each way to end the ranges: without what only cut tiles need, and where
+// there are no more tiles than CTAs without the units, it is smaller and starts sooner.  One
+// prompt of 137 tokens 10.8 -> 8.3 us.)
+template <bool F16, int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_constant__ PromptLaunch L) {
   using S = PromptShape<D>;
   constexpr int NB = S::kNB, LA = NB - 1;  // K blocks ahead of the V block in the ring
@@ -491,17 +519,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   tc_fence_before();
   pdl_wait();
   pdl_trigger();  // the join may now read the call's inputs
-  prompt_start(L, blockIdx.x, s_scan, &s_start);  // syncs the CTA
+  prompt_start<MODE>(L, blockIdx.x, s_scan, &s_start);  // syncs the CTA
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  PromptWalk wk(L, s_start);
+  PromptWalk<MODE> wk(L, s_start);
 
   if (warp == 8 || warp == 10) {
     // ---------------------------------------------------------------- producers
     const int me = (warp - 8) / 2;
     unsigned nk = 0, nv = 0;  // blocks of K and V so far
     bool ok = true;
-    auto load = [&](const CUtensorMap *map, const PromptWalk &wk, int t, int slot, unsigned phase) {
+    auto load = [&](const CUtensorMap *map, const PromptWalk<MODE> &wk, int t, int slot, unsigned phase) {
       ok = ok && __all_sync(0xffffffffu,
                             mbar_wait_fast(smem_u32(&s_empty[slot]), (phase & 1u) ^ 1u, p.err, DFV_DEVERR_SLOT_WAIT, &s_abort));
       if (!ok) return;
@@ -814,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         __syncwarp();  // the row's pieces were stored by four lanes
         if (mine) add_taken<F16>(p, wk.s, wk.h, lim0, lim, out, 0, D);
       }
-      if (tid == 0 && !whole) {
+      if (MODE == kCut && tid == 0 && !whole) {
         L.part_bad[slot] = bad;
         if (wk.t0 == 0) {
           L.cut[blockIdx.x] = make_int4(wk.b, wk.h, wk.t, range_of(wk.last, s_start.U, s_start.G) - (int)blockIdx.x + 1);
@@ -823,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       }
       ++seg;
     }
-    if (tid == 0 && !told) L.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (MODE == kCut && tid == 0 && !told) L.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -924,14 +952,26 @@ bool encode_rows(CUtensorMap *map, const PromptParams &p, const char *base, int 
   return true;
 }
 
+template <bool F16, int D, int MODE>
+cudaError_t launch_kernel(const PromptLaunch &L, int ctas, cudaStream_t s) {
+  auto kern = prompt_attn_kernel<F16, D, MODE>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(kern, PromptShape<D>::kSmem, done);
+  if (e != cudaSuccess) return e;
+  return launch_chained(kern, dim3(ctas), dim3(kThreads), PromptShape<D>::kSmem, s, L);
+}
+
 template <bool F16, int D>
 cudaError_t launch_typed(const PromptLaunch &L, cudaStream_t s) {
-  auto kern = prompt_attn_kernel<F16, D>;
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(kern, PromptShape<D>::kSmem, done);
+  // at most so many tiles (a sequence's last one may be short)
+  const long long tiles = (long long)L.p.Hkv * (L.p.n_rows / L.pos + L.p.n_seqs);
+  const long long longest = kOver + (L.p.max_keys + kKeys - 1) / kKeys;
+  if (L.p.max_keys <= kWholeKeys || 4 * tiles >= 3 * kAttnCtas * longest) {
+    if (tiles <= kAttnCtas) return launch_kernel<F16, D, kOne>(L, (int)tiles, s);
+    return launch_kernel<F16, D, kWhole>(L, kAttnCtas, s);
+  }
+  const cudaError_t e = launch_kernel<F16, D, kCut>(L, kAttnCtas, s);
   if (e != cudaSuccess) return e;
-  e = launch_chained(kern, dim3(kAttnCtas), dim3(kThreads), PromptShape<D>::kSmem, s, L);
-  if (e != cudaSuccess || L.whole) return e;
   return launch_chained(prompt_join_kernel<F16, D>, dim3(kAttnCtas, kTile / kJoinRows), dim3(32 * kJoinWarps), 0, s, L);
 }
 
@@ -950,7 +990,6 @@ cudaError_t launch_prompt_attn(const PromptParams &p, void *ws, cudaStream_t s, 
   L.run = kKeys / gcd;
   L.rise = L.pos / gcd;
   L.inv_pos = (65536u + L.pos - 1) / L.pos;
-  L.whole = p.max_keys <= kWholeKeys;
   sections(&L, p.D, ws);
   const int box = p.D == 128 ? kKeys : kKeys / 2;
   if (!encode_rows(&L.tm_q, p, p.q, p.n_rows, p.H, p.q_row, p.q_head, L.pos, p.G, why, why_len) ||
