@@ -85,6 +85,14 @@ def test_ranges_that_end_at_tiles_or_cut_them(dfv, most):
         Case(rows, rows, 4, 2, 64, BF, seed=5).check(dfv, most=most)
 
 
+@pytest.mark.parametrize("rows,keys,heads,kv,dim", [
+    ([900, 500, 1100], [900, 500, 1100], 16, 8, 64), ([900, 500, 1100], [1000, 1500, 1100], 16, 8, 128),  # whole tiles, several a CTA
+    ([5] * 39 + [20], [5] * 39 + [1601], 64, 64, 64), ([5] * 39 + [20], [7] * 39 + [1601], 64, 64, 128),  # whole, though longer: there are many
+    ([0, 5, 0, 0, 70], [3, 5, 0, 9, 70], 16, 8, 64), ([130] * 9, [130] * 9, 16, 8, 128), ([256] * 4, [400] * 4, 19, 19, 64)])  # a tile a CTA
+def test_every_way_to_end_the_ranges(dfv, rows, keys, heads, kv, dim):
+    Case(rows, keys, heads, kv, dim, BF, seed=6, lead=2, tail=3).check(dfv)
+
+
 def test_many_sequences(dfv):
     rows = [(7 * s) % 19 for s in range(700)]
     Case(rows, rows, 2, 1, 64, HF, seed=3).check(dfv)

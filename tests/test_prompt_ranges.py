@@ -245,3 +245,23 @@ def test_no_wait_by_parity_meets_two_phases(NB):
             moved = True
             todo.append((pcs[:k] + (pc + 1,) + pcs[k + 1:], new))
         assert moved or all(pc == len(q) for pc, q in zip(pcs, progs)), "nobody can go on"
+
+
+def test_a_tile_a_range():
+    """Where ranges are tiles: the host's bound holds all of them, and CTA g's sequence, head and tile are the line's g-th."""
+    rng = random.Random(7)
+    assert "tiles = (long long)L.p.Hkv * (L.p.n_rows / L.pos + L.p.n_seqs)" in TEXT
+    for _ in range(300):
+        G, heads = rng.randint(1, 16), rng.randint(1, 8)
+        rows = [rng.choice((0, 1, rng.randint(1, 40), rng.randint(1, 900))) for _ in range(rng.randint(1, 12))]
+        line = [(b, h, t) for b, n in enumerate(rows) for h in range(heads) for t in range(tiles(n, G))]
+        assert len(line) <= heads * (max(sum(rows), 1) // positions(G) + len(rows))
+        for g, want in enumerate(line):
+            base = 0
+            for b, n in enumerate(rows):
+                m = tiles(n, G)
+                if g < base + heads * m:
+                    w = g - base
+                    assert (b, w // m, w - w // m * m) == want
+                    break
+                base += heads * m
