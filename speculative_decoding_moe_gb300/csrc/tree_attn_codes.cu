@@ -16,8 +16,8 @@
 // round at 2^-25 of it.  The weights are rounded to fp16 (11 bits, times 2^6 so
 // that small ones stay out of its subnormals).  Scores, M, sums and outputs are fp32.
 //
-// What binds is issuing: each code is widened once, in registers, and every
-// instruction per code counts.  So keys and the head's elements are the M side of
+// Next to reading the cache, issuing binds: each code is widened once, in registers,
+// and every instruction per code counts.  So keys and the head's elements are the M side of
 // the products (S^T = K Q^T, O^T = V^T P^T) and the rows are their N side of 8 or 16:
 // a token of a model with up to 8 query heads per kv head takes half the products
 // and half the exponentials that 16 rows on the M side would.  ldmatrix moves pairs
