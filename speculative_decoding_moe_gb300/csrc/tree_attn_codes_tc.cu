@@ -18,6 +18,12 @@
 // some x_j + B is more than 8 above it.  Precision of q and of the weights as in
 // tree_attn_codes.cu.
 //
+// A tile with nodes in it has no such constants: what a row does not see may be of any
+// size and must not touch the row.  Its products take the codes as they are, and a
+// key's powers come in behind the mask, x_j = c 2^a_j s_j and weights 2^(x_j + b_j - M),
+// as in tree_attn_codes.cu.  For the same reason a row's M is raised by what the row sees
+// alone, though the warp's other rows then take part in the rescaling of O.
+//
 // A tile's maximum is found in one pass over its scores, 16 at a time, and p in another:
 // with 20 warps a thread has 96 registers.
 //
@@ -114,6 +120,75 @@ __device__ __noinline__ bool clean_key(uint32_t row, bool node) {
   return nan && node;
 }
 
+// A tile whose keys have factors of their own: x + b of the scores of the keys that the row sees,
+// in place, and their maximum; M and O as they grow; then p and the sum of p 2^-b.  (m, l) before
+// and after; j0: node number of the first key (below 0: committed); bar: the product into O before,
+// 0 where it is done.  Out of line: the other tiles took 2 % longer with it among theirs.
+template <int D, int KEYS>
+__device__ __noinline__ float2 own_tile(uint32_t t_s, uint32_t t_o, bool started, int j0, uint64_t mask, float crow, uint32_t own, uint32_t back, float m, float l,
+                                        uint32_t bar, unsigned phase, unsigned *err, volatile int *abort) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int q = 0; q < KEYS; q += 16) {
+    const int j = j0 + q;  // node of the first of 16 keys (below 0: committed)
+    const uint32_t sees = j >= 0 ? (j < 64 ? (uint32_t)(mask >> j) : 0u) : j > -16 ? (uint32_t)(mask << -j) | ((1u << -j) - 1u) : ~0u;
+    float s[16];
+    uint32_t x[16];
+    tmem_ld16(t_s + q, s);
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const uint4 k = lds128(own + 8u * (q + e));  // 2^a and b of two keys
+      s[e] = sees >> e & 1u ? fmaf(s[e], crow * __uint_as_float(k.x), __uint_as_float(k.y)) : -INFINITY;
+      s[e + 1] = sees >> e & 2u ? fmaf(s[e + 1], crow * __uint_as_float(k.z), __uint_as_float(k.w)) : -INFINITY;
+      x[e] = __float_as_uint(s[e]);
+      x[e + 1] = __float_as_uint(s[e + 1]);
+    }
+    top = max16(s, top);
+    tmem_st16(t_s + q, x);
+  }
+  tmem_wait_st();
+  const float mx = top - 8.f > m ? top : m;  // a row's M follows what the row sees, not its neighbours
+  if (__any_sync(0xffffffffu, mx > m)) {
+    const float f = m == -INFINITY ? 0.f : ex2(m - mx);
+    l *= f;
+    if (bar && started) {  // the product into O before
+      mbar_wait_fast(bar, phase, err, DFV_DEVERR_STAGE_WAIT, abort);
+      __syncwarp();
+      tc_fence_after();
+    }
+#pragma unroll 1
+    for (int q = 0; q < D && started; q += 16) {
+      float o[16];
+      tmem_ld16(t_o + q, o);
+      uint32_t y[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(o[e] * f);
+      tmem_st16(t_o + q, y);
+    }
+    m = mx;
+  }
+  const float from = m == -INFINITY ? 0.f : m;
+  float l0 = 0.f, l1 = 0.f;
+#pragma unroll 1
+  for (int q = 0; q < KEYS; q += 16) {
+    float s[16];
+    uint32_t x[8];
+    tmem_ld16(t_s + q, s);
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      const uint4 k = lds128(back + 4u * (q + e));
+      const float p0 = ex2((s[e] - from) + kBias), p1 = ex2((s[e + 1] - from) + kBias);
+      const float p2 = ex2((s[e + 2] - from) + kBias), p3 = ex2((s[e + 3] - from) + kBias);
+      l0 = fmaf(p2, __uint_as_float(k.z), fmaf(p0, __uint_as_float(k.x), l0));
+      l1 = fmaf(p3, __uint_as_float(k.w), fmaf(p1, __uint_as_float(k.y), l1));
+      x[e / 2] = pack2<true>(p0, p1);
+      x[e / 2 + 1] = pack2<true>(p2, p3);
+    }
+    tmem_st8(t_s + q / 2, x);  // over x + b that have been read
+  }
+  return make_float2(m, l + (l0 + l1));
+}
+
 template <int D, bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const __grid_constant__ AttnLaunch L) {
   using S = CodeTcShape<D, DUAL>;
@@ -128,7 +203,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
   // Of a segment, in turn: NaN was left out.  V is cleaned before its slot is waited for, so with short segments
   // kV + 1 of them may be cleaned before one is put out and its flag cleared.
   __shared__ volatile int s_bad[kFlags];
-  __shared__ volatile int2 s_tell[kTells];  // A and B of a tile
+  __shared__ volatile int2 s_tell[kTells];  // A and B of a tile; A = -1: its keys' own powers are in s_own and s_back
+  __shared__ __align__(16) float2 s_own[8][kKeys];  // 2^a and b
+  __shared__ __align__(16) float s_back[8][kKeys];  // 2^-b
   __shared__ uint8_t s_below[8][kKeys];  // how far a key's b is below B, of tiles whose V is to come
   __shared__ __align__(8) unsigned long long s_told[8];  // (K is widened up to four tiles before V) s_below and s_tell of a tile are there
   __shared__ __align__(16) unsigned char s_power[S::kCK * 2 * kKeys];  // with K: a and b of the tile's keys
@@ -253,10 +330,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
           m2 = __vmaxu4(m2, m2 >> 16);
           const int a = __reduce_max_sync(0xffffffffu, max(m & 255u, m >> 8 & 255u));
           const int b = __reduce_max_sync(0xffffffffu, max(m2 & 255u, m2 >> 8 & 255u));
-          below = max(0, a - pw[kt]);
-          s_below[tile & 7][kt] = (uint8_t)max(0, b - pw[kKeys + kt]);
+          // nodes among them: what a row does not see may be of any size
+          const bool own = (t + 1) * kKeys > wk.v.len, is = t * kKeys + kt < wk.total;
+          below = own ? 0 : max(0, a - pw[kt]);
+          s_below[tile & 7][kt] = (uint8_t)(own ? 0 : max(0, b - pw[kKeys + kt]));
+          if (own) {
+            const int pa = is ? max((int)pw[kt], 1) : 127, pb = is ? min(max((int)pw[kKeys + kt], 1), 253) : 127;
+            s_own[tile & 7][kt] = make_float2(exp_value((uint32_t)pa), (float)(pb - 127));
+            s_back[tile & 7][kt] = exp_value((uint32_t)(254 - pb));
+          }
           if (kt == 0) {
-            s_tell[tile % kTells].x = a;
+            s_tell[tile % kTells].x = own ? -1 : a;
             s_tell[tile % kTells].y = b;
           }
           __syncwarp();
@@ -476,70 +560,80 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
         if (!ok) continue;
         tc_fence_after();
         const int j0 = (wk.t0 + j) * kKeys + (DUAL ? 0 : 64 * w) - wk.v.len;  // node number of the first key
-        if (j0 + kMine > 0) mask_tile(t_s, j0, mask, kMine);  // tree nodes or keys past the end among them
         const unsigned tell = (tiles + (unsigned)j) % kTells;
-        // in (0, infinity), so that -inf stays what it is
-        const float c = fminf(fmaxf(crow * exp_value((uint32_t)s_tell[tell].x), 0x1p-120f), 0x1p120f);
-        const int eb = min(max(s_tell[tell].y, 1), 253);
-        const float B = (float)(eb - 127), back = exp_value((uint32_t)(254 - eb));
-        float high = -INFINITY;
-        {
-          float s0[16], s1[16];
-          tmem_ld16_async(t_s, s0);
+        const int ea = s_tell[tell].x;
+        if (ea < 0) {
+          const int at = DUAL ? 0 : 64 * w;
+          const float2 ml = own_tile<D, kMine>(t_s, t_o, started, j0, mask, crow, smem_u32(&s_own[tell & 7][at]), smem_u32(&s_back[tell & 7][at]), m, l,
+                                               DUAL ? 0u : smem_u32(&s_pvdone[place ^ 1]), ((T - 1) >> 1) & 1u, p.err, &s_abort);
+          m = ml.x;
+          l = ml.y;
+          ok = s_abort == 0;
+        } else {
+          // in (0, infinity)
+          const float c = fminf(fmaxf(crow * exp_value((uint32_t)ea), 0x1p-120f), 0x1p120f);
+          const int eb = min(max(s_tell[tell].y, 1), 253);
+          const float B = (float)(eb - 127), back = exp_value((uint32_t)(254 - eb));
+          float high = -INFINITY;
+          {
+            float s0[16], s1[16];
+            tmem_ld16_async(t_s, s0);
 #pragma unroll 1
-          for (int q = 0; q < kMine; q += 32) {
-            tmem_wait_ld16(s0);
-            tmem_ld16_async(t_s + q + 16, s1);
-            high = max16(s0, high);
-            tmem_wait_ld16(s1);
-            tmem_ld16_async(t_s + (q + 32) % kMine, s0);  // (the last one is the first again)
-            high = max16(s1, high);
-          }
-          tmem_wait_ld16(s0);
-        }
-        const float top = fmaf(high, c, B);
-        if (__any_sync(0xffffffffu, top - 8.f > m)) {
-          // the product into O before: DUAL's was issued before these scores, and their
-          // barrier follows all that was issued before it
-          if (!DUAL && started) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_pvdone[place ^ 1]), ((T - 1) >> 1) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
-            tc_fence_after();
-          }
-          const float mx = fmaxf(m, top), f = m == -INFINITY ? 0.f : ex2(m - mx);
-          l *= f;
-          if (started && ok) {
-#pragma unroll 1
-            for (int q = 0; q < D; q += 16) {
-              float o[16];
-              tmem_ld16(t_o + q, o);
-              uint32_t y[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(o[e] * f);
-              tmem_st16(t_o + q, y);
+            for (int q = 0; q < kMine; q += 32) {
+              tmem_wait_ld16(s0);
+              tmem_ld16_async(t_s + q + 16, s1);
+              high = max16(s0, high);
+              tmem_wait_ld16(s1);
+              tmem_ld16_async(t_s + (q + 32) % kMine, s0);  // (the last one is the first again)
+              high = max16(s1, high);
             }
-          }
-          m = mx;
-        }
-        {
-          // x + B - M by differences from the tile's maximum: whatever the scores' size, the
-          // exponents are 8 at most and right next to it
-          const float from = high == -INFINITY ? 0.f : high, z = (high == -INFINITY ? 0.f : m - top) - kBias;
-          float2 l2 = make_float2(0.f, 0.f);
-          float s0[16], s1[16];
-          uint32_t x[8];
-          tmem_ld16_async(t_s, s0);
-#pragma unroll 1
-          for (int q = 0; q < kMine; q += 32) {
             tmem_wait_ld16(s0);
-            tmem_ld16_async(t_s + q + 16, s1);
-            exp16(s0, from, c, z, x, l2);
-            tmem_wait_ld16(s1);
-            if (q + 32 < kMine) tmem_ld16_async(t_s + q + 32, s0);
-            tmem_st8(t_s + q / 2, x);  // over scores that have been read
-            exp16(s1, from, c, z, x, l2);
-            tmem_st8(t_s + q / 2 + 8, x);
           }
-          l = fmaf(l2.x + l2.y, back, l);
+          const float top = fmaf(high, c, B);
+          if (__any_sync(0xffffffffu, top - 8.f > m)) {
+            // the product into O before: DUAL's was issued before these scores, and their
+            // barrier follows all that was issued before it
+            if (!DUAL && started) {
+              ok = ok && __all_sync(0xffffffffu, mbar_wait_fast(smem_u32(&s_pvdone[place ^ 1]), ((T - 1) >> 1) & 1u, p.err, DFV_DEVERR_STAGE_WAIT, &s_abort));
+              tc_fence_after();
+            }
+            // a row's M follows what the row sees, not its neighbours
+            const float mx = top - 8.f > m ? top : m, f = m == -INFINITY ? 0.f : ex2(m - mx);
+            l *= f;
+            if (started && ok) {
+#pragma unroll 1
+              for (int q = 0; q < D; q += 16) {
+                float o[16];
+                tmem_ld16(t_o + q, o);
+                uint32_t y[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(o[e] * f);
+                tmem_st16(t_o + q, y);
+              }
+            }
+            m = mx;
+          }
+          {
+            // x + B - M by differences from the tile's maximum: whatever the scores' size, the
+            // exponents are 8 at most and right next to it
+            const float from = high == -INFINITY ? 0.f : high, z = (high == -INFINITY ? 0.f : m - top) - kBias;
+            float2 l2 = make_float2(0.f, 0.f);
+            float s0[16], s1[16];
+            uint32_t x[8];
+            tmem_ld16_async(t_s, s0);
+#pragma unroll 1
+            for (int q = 0; q < kMine; q += 32) {
+              tmem_wait_ld16(s0);
+              tmem_ld16_async(t_s + q + 16, s1);
+              exp16(s0, from, c, z, x, l2);
+              tmem_wait_ld16(s1);
+              if (q + 32 < kMine) tmem_ld16_async(t_s + q + 32, s0);
+              tmem_st8(t_s + q / 2, x);  // over scores that have been read
+              exp16(s1, from, c, z, x, l2);
+              tmem_st8(t_s + q / 2 + 8, x);
+            }
+            l = fmaf(l2.x + l2.y, back, l);
+          }
         }
         tmem_wait_st();
         tc_fence_before();

@@ -1,0 +1,63 @@
+"""A key that a row does not attend to leaves the row's bits as they are, however large the key and its value are and
+however much the rows that do attend to it change."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from tests import test_gpu_tree_attention_codes as codes
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dfv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from speculative_decoding_moe_gb300 import build as b
+    b.build()
+    from speculative_decoding_moe_gb300 import dfv as m
+    return m
+
+
+def trees(counts, own=True):
+    """(masks, rows that do not see the hidden nodes): in each tree, the middle node is seen by no other, and by itself if
+    `own`; the others see themselves and those before them."""
+    masks, keep = [], []
+    for n in counts:
+        for i in range(n):
+            hidden = 1 << (n // 2)
+            masks.append(((2 << i) - 1) & ~hidden | (hidden if own and i == n // 2 else 0))
+            keep.append(not (own and i == n // 2))
+    return masks, torch.tensor(keep)
+
+
+def same(a, b, keep):
+    return torch.equal(a[0][keep], b[0][keep]) and torch.equal(a[1][keep], b[1][keep])
+
+
+# trees at the end of a tile, across two, and with nothing before them; so many pairs that a CTA takes several tiles of each
+FEW, MANY = [200, 0, 125], [500 + 17 * s for s in range(24)]
+# 17 to 512 rows per kv head
+CODES = [(heads, dim, nodes, own) for heads, dim in ((8, 128), (2, 64), (16, 64)) for nodes in (2, 3, 7, 16, 17, 40, 64) for own in (True, False)
+         if 16 < heads * nodes <= 512]
+
+
+@pytest.mark.parametrize("lens,kv,heads,dim,nodes,own", [(FEW, 1) + c for c in CODES] + [(MANY, 8, 64, 128, n, True) for n in (16, 25)]
+                         + [(MANY, 8, 16, 64, 40, True)])
+def test_codes(dfv, lens, kv, heads, dim, nodes, own):
+    counts = [nodes] * len(lens)
+    c = codes.Case(lens, counts, heads, kv, dim, 16, seed=nodes + heads)
+    c.masks, keep = trees(counts, own)
+    keep = keep.cuda()
+    was, exps = c.run(dfv), c.exp
+    for sides in ((0,), (1,), (0, 1)):
+        for up in (8, 20, 30, 100, -90) if lens is FEW else (30,):
+            c.exp = [x.clone() for x in exps]
+            for s, n in enumerate(counts):
+                at = lens[s] + n // 2
+                for side in sides:
+                    e = c.exp[side][0, int(c.table[s, at // 16]), :, at % 16]
+                    e.copy_((e.int() + up).clamp(127 - 100, 127 + 120).to(torch.uint8))
+            got = c.run(dfv)
+            assert got[2] == 0 and same(got, was, keep), "sides %s, 2^%d" % (sides, up)
