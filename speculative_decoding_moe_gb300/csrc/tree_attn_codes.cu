@@ -345,9 +345,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_kernel(const __gr
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-              // f = 0 without keys so far: nothing is summed yet
-              const float f = m[n][e] == -INFINITY ? 0.f : ex2(m[n][e] - x);
-              m[n][e] = x;
+              // a row's M follows what the row sees, not its neighbours; f = 0 without keys so
+              // far: nothing is summed yet
+              const bool rise = x - 8.f > m[n][e];
+              const float f = !rise ? 1.f : m[n][e] == -INFINITY ? 0.f : ex2(m[n][e] - x);
+              if (rise) m[n][e] = x;
               l[n][e] *= f;
 #pragma unroll
               for (int c = 0; c < D / 16; ++c) {

@@ -38,13 +38,13 @@ def same(a, b, keep):
 
 # trees at the end of a tile, across two, and with nothing before them; so many pairs that a CTA takes several tiles of each
 FEW, MANY = [200, 0, 125], [500 + 17 * s for s in range(24)]
-# 17 to 512 rows per kv head
+# 1 to 512 rows per kv head
 CODES = [(heads, dim, nodes, own) for heads, dim in ((8, 128), (2, 64), (16, 64)) for nodes in (2, 3, 7, 16, 17, 40, 64) for own in (True, False)
-         if 16 < heads * nodes <= 512]
+         if heads * nodes <= 512] + [(8, 64, 1, False), (8, 128, 1, False)]
 
 
-@pytest.mark.parametrize("lens,kv,heads,dim,nodes,own", [(FEW, 1) + c for c in CODES] + [(MANY, 8, 64, 128, n, True) for n in (16, 25)]
-                         + [(MANY, 8, 16, 64, 40, True)])
+@pytest.mark.parametrize("lens,kv,heads,dim,nodes,own", [(FEW, 1) + c for c in CODES] + [(MANY, 8, 64, 128, n, True) for n in (2, 16, 25)]
+                         + [(MANY, 8, 16, 64, 40, True), (MANY, 8, 64, 64, 2, False)])
 def test_codes(dfv, lens, kv, heads, dim, nodes, own):
     counts = [nodes] * len(lens)
     c = codes.Case(lens, counts, heads, kv, dim, 16, seed=nodes + heads)
