@@ -367,7 +367,9 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
           tmem_wait_ld32(s1);
           mx = max32(s1, mx);
           exp32<F16>(s1, c, z, x + 48, l2);
-          if (!__any_sync(0xffffffffu, (mx - m) * c > 8.f)) break;
+          const bool grew = (mx - m) * c > 8.f;
+          if (!__any_sync(0xffffffffu, grew)) break;
+          if (!grew) mx = m;  // a row's M follows what the row sees, not its neighbours
           if (started) {
             // the last product into O is complete: it was issued before these
             // scores, and their barrier follows all that was issued before it

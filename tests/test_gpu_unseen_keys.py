@@ -5,9 +5,10 @@ from __future__ import annotations
 import pytest
 import torch
 
-from tests import test_gpu_tree_attention_codes as codes
+from tests import _tree_util, test_gpu_tree_attention_codes as codes
 
 pytestmark = pytest.mark.gpu
+BF, HF = torch.bfloat16, torch.float16
 
 
 @pytest.fixture(scope="module")
@@ -61,3 +62,29 @@ def test_codes(dfv, lens, kv, heads, dim, nodes, own):
                     e.copy_((e.int() + up).clamp(127 - 100, 127 + 120).to(torch.uint8))
             got = c.run(dfv)
             assert got[2] == 0 and same(got, was, keep), "sides %s, 2^%d" % (sides, up)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("lens,kv,heads,dim,nodes", [(FEW, 1) + c for c in ((8, 128, 2), (2, 64, 8), (8, 128, 16), (8, 64, 40), (8, 128, 64))]
+                         + [(MANY, 8, 16, 64, 8), (MANY, 8, 64, 128, 2), (MANY, 8, 64, 128, 16), (MANY, 8, 16, 64, 40), (MANY, 8, 64, 64, 25)])
+def test_16_bits(dfv, lens, kv, heads, dim, nodes, dtype):
+    counts = [nodes] * len(lens)
+    c = _tree_util.Case(lens, counts, heads, kv, dim, 16, dtype, seed=nodes + heads)
+    c.masks, keep = trees(counts)
+
+    def run(side=None, factor=1.0):
+        cache, tree = c.gpu(dfv)
+        if side is not None:
+            for s, n in enumerate(counts):
+                at = lens[s] + n // 2
+                (cache.k, cache.v)[side][0, int(c.table[s, at // 16]), :, at % 16] *= factor
+        ws = dfv.alloc_workspace(dfv.tree_attention_workspace_size(cache, tree, heads))
+        lse = torch.zeros(c.rows, heads, device="cuda")
+        out = dfv.tree_attention(cache, 0, tree, c.q.cuda(), ws, lse=lse)
+        assert dfv.read_device_error(ws) == 0 and cache.errors() == 0
+        return out, lse
+
+    was, keep = run(), keep.cuda()
+    for side in (0, 1):
+        for factor in (30.0, -30.0, 1e4, 1e30 if dtype == BF else 1e3) if lens is FEW else (30.0, -30.0):
+            assert same(run(side, factor), was, keep), "%s times %g" % ("kv"[side], factor)
