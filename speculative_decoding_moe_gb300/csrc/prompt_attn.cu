@@ -754,7 +754,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
             mx = max32(s1, mx);
             exp32<F16>(s1, c, z, x + 48, l2);
           }
-          if (!__any_sync(0xffffffffu, (mx - m) * c > 8.f)) break;
+          const bool grew = (mx - m) * c > 8.f;
+          if (!__any_sync(0xffffffffu, grew)) break;
+          if (!grew) mx = m;  // a row's M follows what the row sees, not its neighbours
           const float f = m == -INFINITY ? 0.f : ex2((m - mx) * c);
           l *= f;
           if (j > 0) {

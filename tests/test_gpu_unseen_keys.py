@@ -5,7 +5,7 @@ from __future__ import annotations
 import pytest
 import torch
 
-from tests import _tree_util, test_gpu_tree_attention_codes as codes
+from tests import _tree_util, test_gpu_prompt_attention as prompts, test_gpu_tree_attention_codes as codes
 
 pytestmark = pytest.mark.gpu
 BF, HF = torch.bfloat16, torch.float16
@@ -88,3 +88,21 @@ def test_16_bits(dfv, lens, kv, heads, dim, nodes, dtype):
     for side in (0, 1):
         for factor in (30.0, -30.0, 1e4, 1e30 if dtype == BF else 1e3) if lens is FEW else (30.0, -30.0):
             assert same(run(side, factor), was, keep), "%s times %g" % ("kv"[side], factor)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("heads,dim,rows,keys", [(8, 128, [40], [40]), (1, 64, [200], [200]), (4, 64, [130, 7], [130, 300]), (8, 128, [300], [1700]),
+                                                 (16, 64, [70, 33], [70, 33])])
+def test_prompts(dfv, heads, dim, rows, keys, dtype):
+    """Positions before a key."""
+    c = prompts.Case(rows, keys, heads, 1, dim, dtype, seed=3)
+    was = c.run(dfv)[:2]
+    for i in (1, rows[0] // 2, rows[0] - 1):  # positions of the first prompt
+        at = keys[0] - rows[0] + i
+        keep = torch.ones(c.n, dtype=torch.bool, device="cuda")
+        keep[i:rows[0]] = False
+        for side in (0, 1):
+            for factor in (30.0, -30.0, 1e4, 1e30 if dtype == BF else 1e3):
+                x = [c.k.clone(), c.v.clone()]
+                x[side][at] *= factor
+                assert same(c.run(dfv, k=x[0].cuda(), v=x[1].cuda())[:2], was, keep), "%s of position %d times %g" % ("kv"[side], i, factor)
