@@ -11,17 +11,18 @@
 //
 // Mathematics.  Key j is K_j 2^a_j, value j is V_j 2^b_j.  With A and B the largest a
 // and b of a tile of 128 keys, the products take K_j 2^(a_j - A) and V_j 2^(b_j - B) in
-// fp16, exact for tokens within 2^15 of the tile's largest power, and absolutely off
-// by 2^-25 of it beyond.  A and B are then constants of the tile: scores are
-// x_j = c 2^A s_j, the weights 2^(x_j + B - M), and the sum takes a tile's weights
-// times 2^-B.  M follows the maximum of x_j + B; it is raised, and O rescaled, when
-// some x_j + B is more than 8 above it.  Precision of q and of the weights as in
-// tree_attn_codes.cu.
+// fp16, exact for tokens within 2^15 of the tile's largest power.  A and B are then
+// constants of the tile: scores are x_j = c 2^A s_j, the weights 2^(x_j + B - M), and
+// the sum takes a tile's weights times 2^-B.  M follows the maximum of x_j + B; it is
+// raised, and O rescaled, when some x_j + B is more than 8 above it.  Precision of q and
+// of the weights as in tree_attn_codes.cu.
 //
-// A tile with nodes in it has no such constants: what a row does not see may be of any
-// size and must not touch the row.  Its products take the codes as they are, and a
-// key's powers come in behind the mask, x_j = c 2^a_j s_j and weights 2^(x_j + b_j - M),
-// as in tree_attn_codes.cu.  For the same reason a row's M is raised by what the row sees
+// A tile has no such constants where its powers are further apart (a beyond 2^15, b
+// beyond 2^8: M would follow a value that has no weight, and the weights of others would
+// round among fp16's subnormals), or where there are nodes in it: what a row does not see may
+// be of any size and must not touch the row.  Its products take the codes as they are,
+// and a key's powers come in behind the mask, x_j = c 2^a_j s_j and weights
+// 2^(x_j + b_j - M), as in tree_attn_codes.cu.  A row's M is raised by what the row sees
 // alone, though the warp's other rows then take part in the rescaling of O.
 //
 // A tile's maximum is found in one pass over its scores, 16 at a time, and p in another:
@@ -53,6 +54,7 @@ constexpr int kThreads = 640;
 constexpr int kWiden = 4;  // warps that widen K, and that widen V
 
 constexpr float kBias = 6.f;
+constexpr int kApartK = 15, kApartV = 8;  // how far a tile's powers may be apart for constants of the tile
 constexpr int kFlags = 8;
 constexpr int kTells = 16;  // tiles whose powers are kept: more than are between their widening and their scores
 
@@ -325,13 +327,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
           const unsigned char *pw = s_power + cst * 2 * kKeys;
           const int valid = wk.total - t * kKeys - 4 * lane;  // of this lane's four keys
           const uint32_t keep = valid >= 4 ? ~0u : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u;
-          uint32_t m = *reinterpret_cast<const uint32_t *>(pw + 4 * lane) & keep, m2 = *reinterpret_cast<const uint32_t *>(pw + kKeys + 4 * lane) & keep;
+          const uint32_t w1 = *reinterpret_cast<const uint32_t *>(pw + 4 * lane), w2 = *reinterpret_cast<const uint32_t *>(pw + kKeys + 4 * lane);
+          uint32_t m = w1 & keep, m2 = w2 & keep, n = w1 | ~keep, n2 = w2 | ~keep;
           m = __vmaxu4(m, m >> 16);
           m2 = __vmaxu4(m2, m2 >> 16);
+          n = __vminu4(n, n >> 16);
+          n2 = __vminu4(n2, n2 >> 16);
           const int a = __reduce_max_sync(0xffffffffu, max(m & 255u, m >> 8 & 255u));
           const int b = __reduce_max_sync(0xffffffffu, max(m2 & 255u, m2 >> 8 & 255u));
-          // nodes among them: what a row does not see may be of any size
-          const bool own = (t + 1) * kKeys > wk.v.len, is = t * kKeys + kt < wk.total;
+          const int low = min(n & 255u, n >> 8 & 255u), low2 = min(n2 & 255u, n2 >> 8 & 255u);  // of this lane's
+          // factors of their own: nodes among them, or far apart
+          const bool own = __any_sync(0xffffffffu, (t + 1) * kKeys > wk.v.len || a - low > kApartK || b - low2 > kApartV), is = t * kKeys + kt < wk.total;
           below = own ? 0 : max(0, a - pw[kt]);
           s_below[tile & 7][kt] = (uint8_t)(own ? 0 : max(0, b - pw[kKeys + kt]));
           if (own) {
