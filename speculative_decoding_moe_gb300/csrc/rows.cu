@@ -287,6 +287,15 @@ __global__ void __launch_bounds__(kRowThreads, 3) append_kernel(const __grid_con
         }
       }
     }
+    auto put = [&](char *to_row) {
+      uint4 *to = reinterpret_cast<uint4 *>(to_row);
+      to[at.x] = narrow<F16>(a);
+      to[at.y] = narrow<F16>(b);
+    };
+    if (CODES && have && turned) {  // rows as they are, whatever becomes of them in codes
+      if (isq) put(p.o + 2 * (row * p.o_row + h * p.o_head));
+      if (!isq && p.ko) put(p.ko + 2 * (row * p.ko_row + (h - p.H) * p.ko_head));
+    }
     float top = 0.f;
     if (CODES) {  // of the finite elements; the others become NaN
 #pragma unroll
@@ -303,16 +312,10 @@ __global__ void __launch_bounds__(kRowThreads, 3) append_kernel(const __grid_con
     }
     if (!have) continue;
     if (isq) {
-      uint4 *to = reinterpret_cast<uint4 *>(p.o + 2 * (row * p.o_row + h * p.o_head));
-      to[at.x] = narrow<F16>(a);
-      to[at.y] = narrow<F16>(b);
+      if (!CODES) put(p.o + 2 * (row * p.o_row + h * p.o_head));
       continue;
     }
-    if (turned && p.ko) {
-      uint4 *to = reinterpret_cast<uint4 *>(p.ko + 2 * (row * p.ko_row + (h - p.H) * p.ko_head));
-      to[at.x] = narrow<F16>(a);
-      to[at.y] = narrow<F16>(b);
-    }
+    if (!CODES && turned && p.ko) put(p.ko + 2 * (row * p.ko_row + (h - p.H) * p.ko_head));
     if (pg < 0) continue;
     if (CODES) {
       const int kh = turned ? h - p.H : h - HK;
