@@ -105,6 +105,7 @@ class Server:
         width = -(-room // PAGE)
         self.cache = dfv.KVCache.empty(LAYERS, self.S * width + 1, PAGE, KV_HEADS, HEAD_DIM, self.S, width, dtype=dtype)
         self.pages_ws = dfv.alloc_workspace(dfv.cache_workspace_size(self.cache))
+        self.attn_ws = None
         self.all = torch.arange(self.S, dtype=torch.int32, device="cuda")
         self.hist = torch.zeros(self.S, room + 1, dtype=torch.int32, device="cuda")
         self.hist_len = torch.zeros(self.S, dtype=torch.int32, device="cuda")
@@ -119,6 +120,12 @@ class Server:
             parts = [p[start:min(start + chunk, len(p) - 1)] for p in prompts]
             self.prefill(parts, done)
             done = [d + len(p) for d, p in zip(done, parts)]
+
+    def space(self, nbytes):
+        """One workspace for all attention calls, of chunks and of trees, made again only for a call that needs a larger one."""
+        if self.attn_ws is None or self.attn_ws.numel() < nbytes:
+            self.attn_ws = dfv.alloc_workspace(nbytes)
+        return self.attn_ws
 
     @staticmethod
     def rows(counts):
@@ -136,7 +143,7 @@ class Server:
         pos = torch.tensor([d + i for d, p in zip(done, parts) for i in range(len(p))], **dev)
         taken = torch.tensor([len(p) for p in parts], **dev)
         dfv.pages_reserve(self.cache, self.all, taken, self.pages_ws)
-        ws = dfv.alloc_workspace(dfv.prompt_attention_workspace_size(rows, HEADS, KV_HEADS, HEAD_DIM))
+        ws = self.space(dfv.prompt_attention_workspace_size(rows, HEADS, KV_HEADS, HEAD_DIM))
         self.t.prefill(self.cache, rows, keys, toks, pos, ws)
         self.cache.lens += taken
         for s, (d, p) in enumerate(zip(done, parts)):
@@ -160,7 +167,7 @@ class Server:
         dfv.pages_reserve(self.cache, self.all, torch.full_like(self.all, n), self.pages_ws)
 
     def run(self, tree, tokens, positions):
-        ws = dfv.alloc_workspace(dfv.tree_attention_workspace_size(self.cache, tree, HEADS))
+        ws = self.space(dfv.tree_attention_workspace_size(self.cache, tree, HEADS))
         return self.t.verify(self.cache, tree, tokens, positions, ws)
 
     def keep(self, tree, tokens, path, tau):
