@@ -169,7 +169,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
   // ------------------------------------------------------------------ consumers
   const int cw = (warp - kProd) & 3, group = (warp - kProd) >> 2, gr = lane >> 2, qc = lane & 3;
   const float c = p.scale_log2;
-  constexpr float kBias = F16 ? 6.f : 0.f;
   int st = group * S::kPer, ph = 0, turn = 0;
   bool ok = true;
   SegWalk<kKt, S::kOver> wk(L, s_start);
@@ -255,7 +254,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
         uint32_t a[4];
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const float z = (m[hh] == -INFINITY ? 0.f : m[hh] * c) - kBias;
+          const float z = base_of<F16>(m[hh], c);
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
             const float x = ex2(fmaf(s[nt][2 * hh], c, -z)), y = ex2(fmaf(s[nt][2 * hh + 1], c, -z));
@@ -326,7 +325,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) tree_attn_mma_kernel(const __g
         x[0] = fmaf(a.x, f, x[0]); x[1] = fmaf(a.y, f, x[1]); x[2] = fmaf(a.z, f, x[2]); x[3] = fmaf(a.w, f, x[3]);
         x[4] = fmaf(b.x, f, x[4]); x[5] = fmaf(b.y, f, x[5]); x[6] = fmaf(b.z, f, x[6]); x[7] = fmaf(b.w, f, x[7]);
       }
-      const float z = (M == -INFINITY ? 0.f : M * c) - kBias;
+      const float z = base_of<F16>(M, c);
       if (whole) {
         if (row0 + r < R) store_out<F16>(L, wk.v, row0 + r, wk.h, e, x, z, lsum, isbad);
       } else {

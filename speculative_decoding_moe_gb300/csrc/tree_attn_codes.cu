@@ -45,7 +45,6 @@ namespace dfv {
 namespace {
 
 constexpr int kProd = 4, kCons = 8, kThreads = 32 * (kProd + kCons);
-constexpr float kBias = 6.f;
 
 template <int D, int NT>  // NT blocks of 8 rows
 struct CodeShape {
@@ -361,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_kernel(const __gr
         uint32_t pt[kStep][NT][2];  // P^T of keys 16 u + 8 i + 2 qc, + 1 and row 8 n + gr
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float z0 = (m[n][0] == -INFINITY ? 0.f : m[n][0]) - kBias, z1 = (m[n][1] == -INFINITY ? 0.f : m[n][1]) - kBias;
+          const float z0 = base_of<true>(m[n][0], 1.f), z1 = base_of<true>(m[n][1], 1.f);
 #pragma unroll
           for (int u = 0; u < kStep; ++u)
 #pragma unroll
@@ -437,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_kernel(const __gr
         x[0] = fmaf(a.x, f, x[0]); x[1] = fmaf(a.y, f, x[1]); x[2] = fmaf(a.z, f, x[2]); x[3] = fmaf(a.w, f, x[3]);
         x[4] = fmaf(b.x, f, x[4]); x[5] = fmaf(b.y, f, x[5]); x[6] = fmaf(b.z, f, x[6]); x[7] = fmaf(b.w, f, x[7]);
       }
-      const float z = (M == -INFINITY ? 0.f : M) - kBias;
+      const float z = base_of<true>(M, 1.f);
       if (whole) {
         if (r < R) store_out<false>(L, wk.v, r, wk.h, e, x, z, lsum, isbad);
       } else {

@@ -78,7 +78,6 @@ template <bool F16, int D, bool DUAL>
 __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid_constant__ AttnLaunch L) {
   using S = TcShape<D, DUAL>;
   constexpr int LA = DUAL ? 1 : 2;  // K tiles ahead of the V tile in the ring
-  constexpr float kBias = F16 ? 6.f : 0.f;
   constexpr int kHalves = D / 64;
   extern __shared__ __align__(16) unsigned char sm_raw[];
   unsigned char *sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
@@ -348,7 +347,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
         uint32_t x[64];
         float2 l2;
         for (;;) {
-          const float z = (m == -INFINITY ? 0.f : m * c) - kBias;
+          const float z = base_of<F16>(m, c);
           float s0[32], s1[32], mx = m;
           l2 = make_float2(0.f, 0.f);
           tmem_ld32(t_s, s0);
@@ -423,7 +422,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tree_attn_tc_kernel(const __grid
         lsum = a.y * f0 + b.y * f1;
       }
       const int bad = s_bad;
-      const float z = (M == -INFINITY ? 0.f : M * c) - kBias;
+      const float z = base_of<F16>(M, c);
       const int c0 = DUAL ? 0 : w * (D / 2), c1 = DUAL ? D : c0 + D / 2;
       const bool whole = wk.whole();
       const int slot = wk.slot(blockIdx.x), i = node_of(L, r), head = wk.h * p.G + r - i * p.G;

@@ -236,6 +236,15 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// What p = 2^(x - z) takes for a maximum m of scores whose x is c times as large: c m, for fp16 less
+// 6, rounded up there: scores beyond 2^25 are steps of 4 and more apart, and rounded down z
+// would let p past fp16's largest value.
+template <bool F16>
+__device__ __forceinline__ float base_of(float m, float c) {
+  if (m == -INFINITY) return F16 ? -6.f : 0.f;
+  return F16 ? __fadd_ru(__fmul_ru(m, c), -6.f) : m * c;
+}
+
 template <bool F16>
 __device__ __forceinline__ float2 unpack2(uint32_t v) {
   if (F16) return __half22float2(*reinterpret_cast<const __half2 *>(&v));
