@@ -463,7 +463,6 @@ template <bool F16, int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_constant__ PromptLaunch L) {
   using S = PromptShape<D>;
   constexpr int NB = S::kNB, LA = NB - 1;  // K blocks ahead of the V block in the ring
-  constexpr float kBias = F16 ? 6.f : 0.f;
   extern __shared__ __align__(16) unsigned char sm_raw[];
   unsigned char *sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) unsigned long long s_full[S::kSlots], s_empty[S::kSlots], s_odone[2], s_qfull, s_qfree, s_drain;
@@ -733,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
         float2 l2;
         for (;;) {
           // (rounded up: the largest p stays within its bound however large the scores are)
-          const float z = (m == -INFINITY ? 0.f : __fmul_ru(m, c)) - kBias;
+          const float z = F16 ? base_of<true>(m, c) : m == -INFINITY ? 0.f : __fmul_ru(m, c);
           float s0[32], s1[32], mx = m;
           l2 = make_float2(0.f, 0.f);
           tmem_ld32(t_s, s0);
@@ -798,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       const int bad = s_bad[seg & 3];
-      const float z = (m == -INFINITY ? 0.f : __fmul_ru(m, c)) - kBias;
+      const float z = F16 ? base_of<true>(m, c) : m == -INFINITY ? 0.f : __fmul_ru(m, c);
       const bool whole = wk.whole();
       const int slot = wk.slot(blockIdx.x);
       const size_t row = wk.s.row0 + (size_t)i;

@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from tests import _tree_util, test_gpu_tree_attention_codes as codes
+from tests import _tree_util, test_gpu_prompt_attention as prompts, test_gpu_tree_attention_codes as codes
 from tests._prompt_util import E4M3, coded, valued
 
 pytestmark = pytest.mark.gpu
@@ -62,6 +62,18 @@ def test_trees(dfv, dim, nodes, dtype):
         ws = dfv.alloc_workspace(dfv.tree_attention_workspace_size(cache, tree, 8))
         out = dfv.tree_attention(cache, 0, tree, q.to(dtype).cuda().expand(c.rows, 8, dim).contiguous(), ws, scale=scale)
         assert dfv.read_device_error(ws) == 0
+        inside(out, c.v)
+
+
+@pytest.mark.parametrize("dtype", [HF, BF])
+@pytest.mark.parametrize("dim,rows,keys", [(64, 40, 1500), (128, 300, 1700), (128, 137, 137)])
+def test_prompts(dfv, dim, rows, keys, dtype):
+    c = prompts.Case([rows], [keys], 8, 1, dim, dtype, seed=2)
+    for size, step, (q0, k0) in itertools.product(SIZES, STEPS, FIRST):
+        q, k, scale = rising(keys, dim, size, step, q0, k0)
+        c.q, c.k = q.to(dtype).expand(rows, 8, dim).contiguous(), k.to(dtype)[:, None].contiguous()
+        out, _, err = c.run(dfv, scale=scale)
+        assert err == 0
         inside(out, c.v)
 
 
