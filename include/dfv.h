@@ -719,7 +719,8 @@ int dfv_pages_free(const dfv_kv_cache *cache, const int32_t *seqs, int n, void *
  *   dfv_norm_rope_append    its rows normed, turned and stored at lens[s] + i
  *   dfv_prompt_attention    over its own turned k and its v when nothing was there
  *                           before; else over what dfv_cache_read brought back
- * and once all layers are done the caller adds the row counts to lens.
+ * and once all layers are done the caller adds the row counts to lens.  Rows and
+ * heads of an output may not overlap (a stride below head_dim is refused).
  * ---------------------------------------------------------------------- */
 
 #define DFV_MAX_ROWS (1 << 24) /* rows of one call */

@@ -31,6 +31,11 @@ TreeParams row_params(const dfv_row_batch *r) {
   return p;
 }
 
+// Rows or heads of an output that certainly share elements.
+bool overlap(int rows, int heads, int head_dim, int64_t row, int64_t head) {
+  return (rows > 1 && row < head_dim) || (heads > 1 && head < head_dim) || (rows > 1 && heads > 1 && row == head);
+}
+
 int check_prompt(const dfv_row_batch *rows, int n_heads, int n_kv_heads, int head_dim) {
   const int st = check_rows(rows, "rows");
   if (st) return st;
@@ -94,6 +99,9 @@ int dfv_norm_rope_append(const dfv_kv_cache *cache, int layer, const dfv_row_bat
   p.ko_row = ko_row;
   p.ko_head = ko_head;
   if ((st = check_rope(cache, layer, n_heads, rot_dim, interleaved, scale, p))) return st;
+  if (overlap(rows->n_rows, n_heads, cache->head_dim, o_row, o_head) ||
+      (k_out && overlap(rows->n_rows, cache->n_kv_heads, cache->head_dim, ko_row, ko_head)))
+    return api_fail(DFV_ERR_INVALID_ARG, "rows or heads of q_out or k_out overlap");
   return launched(launch_norm_rope_append(p, (cudaStream_t)stream), "norm and rotary append launch");
 }
 
@@ -108,6 +116,10 @@ int dfv_cache_read(const dfv_kv_cache *cache, int layer, const dfv_row_batch *ro
     return api_fail(DFV_ERR_INVALID_ARG, "neither k_out nor v_out is given, or one is not 16-byte aligned");
   if (!stride_ok(k_row) || !stride_ok(k_head) || !stride_ok(v_row) || !stride_ok(v_head))
     return api_fail(DFV_ERR_INVALID_ARG, "row and head strides must be non-negative multiples of 8 elements");
+  if ((k_out && overlap(rows->n_rows, cache->n_kv_heads, cache->head_dim, k_row, k_head)) ||
+      (v_out && overlap(rows->n_rows, cache->n_kv_heads, cache->head_dim, v_row, v_head)))
+    return api_fail(DFV_ERR_INVALID_ARG, "rows or heads of k_out or v_out overlap");
+  if (k_out == v_out) return api_fail(DFV_ERR_INVALID_ARG, "k_out must not be v_out");
   CacheReadParams p = {};
   p.c = cache_params(cache);
   p.t = row_params(rows);
@@ -151,6 +163,8 @@ int dfv_prompt_attention(int dtype, const dfv_row_batch *rows, const dfv_row_bat
     return api_fail(DFV_ERR_UNSUPPORTED, "k and v with a stride of 0");
   if ((rows->n_rows > 1 && q_row == 0) || (n_heads > 1 && q_head == 0))
     return api_fail(DFV_ERR_UNSUPPORTED, "q with a stride of 0");
+  if (overlap(rows->n_rows, n_heads, head_dim, o_row, o_head))
+    return api_fail(DFV_ERR_INVALID_ARG, "rows or heads of out overlap");
   if ((st = check_ws(ws, ws_bytes, prompt_attn_ws(head_dim)))) return st;
   PromptParams p = {};
   p.n_seqs = rows->n_seqs;
