@@ -297,14 +297,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_kernel(const __gr
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[u][n][e] += s1[u][n][e];
-        // ---- x + b + 127 in their place; 2^-b
+        // ---- x + b in their place; 2^-b
         float back[kStep][2];
 #pragma unroll
         for (int u = 0; u < kStep; ++u)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint32_t at = (uint32_t)(w0 + 16 * u + 8 * e + gr), pb = lds_u8(pv + at);
-            const float a = exp_value(lds_u8(pk + at)), b = __uint_as_float(0x4b000000u | pb) - 8388608.f;
+            const float a = exp_value(lds_u8(pk + at)), b = __uint_as_float(0x4b000000u | pb) - 8388735.f;  // pb - 127
             back[u][e] = exp_value(254u - pb);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_kernel(const __gr
           x += __shfl_xor_sync(0xffffffffu, x, 4);
           x += __shfl_xor_sync(0xffffffffu, x, 8);
           x += __shfl_xor_sync(0xffffffffu, x, 16);
-          if (gr == 0) s_ml[w][r] = make_float2(m[n][e] - 127.f, x);
+          if (gr == 0) s_ml[w][r] = make_float2(m[n][e], x);
 #pragma unroll
           for (int c = 0; c < D / 16; ++c)
             *reinterpret_cast<float2 *>(mine + r * S::kPitch + c * 16 + 2 * gr) = make_float2(o[n][c][e], o[n][c][2 + e]);
