@@ -585,7 +585,9 @@ size_t dfv_tree_attention_workspace_size(const dfv_kv_cache *cache, const dfv_tr
  * Scores, maxima, sums and the output accumulator are fp32; p is rounded to
  * the cache's dtype for the second product, and the output once.  DFV_E4M3: q is
  * taken as fp16 times a power of two per row, codes as fp16 (exact), and p times
- * the value's power of two is rounded to fp16.
+ * the value's power of two is rounded to fp16, next to the row's largest such weight (at
+ * 2^-23 of it where it is smaller than 2^-12 of it).  The sum of p is held relative to it too:
+ * the powers of one head's values may be 2^110 apart.
  * A page-table entry out of range is read as page 0 (DFV_KVERR_PAGE; that
  * sequence's outputs are invalid), a sequence with a length out of range is
  * taken as empty (DFV_KVERR_LEN).  Lengths, tables, masks and row offsets are

@@ -13,7 +13,17 @@
 // memory, a thread turns its row of S into P over S, and O += P V accumulates in
 // tensor memory.  One pass over the scores computes p with the M so far; M is only
 // raised, and O only rescaled, when a row's maximum grew by more than 2^8, and the
-// pass is then made again.
+// pass is then made again; rows of the warp whose maxima did not keep theirs, so that
+// a key that a row does not see leaves the row's bits alone (with scores six times as
+// far apart as products of normal q and k, 4 x 2039 rows took 145 us when they were raised
+// together, and take 153).
+//
+// Precision.  As in tree_attn.cu: scores, M, l and O are fp32, and p alone is rounded
+// to the inputs' type for the second product, since both its operands have one type (p in
+// 32 bits would take tf32 values, at half the rate and twice the bytes, or a second
+// product).  With normal values the outputs' error in the 2-norm is 0.0019 to 0.0023 for
+// bf16, where 32-bit p and the outputs' own rounding make 0.0015 to 0.0017 (fp16:
+// 0.0003 and 0.0002).
 //
 // Scores take turns in NB places of 128 columns: two with heads of 128, one a
 // warpgroup; three with heads of 64, where the outputs leave room, so that a warpgroup's
@@ -44,14 +54,15 @@
 //
 // What binds.  With heads of 128 the tensor core: a block takes 2048 clocks of
 // products and 2700 in all (16381 tokens without the softmax's arithmetic 1174 us).  With
-// heads of 64 a block takes 2050 clocks, 1600 without that arithmetic: products of 64
-// columns take longer than half of 128 columns' time.  Measured (GB300, device time): 16381
-// tokens of 32 heads of 128 over 4 kv heads 1375 us, 1.57 PFLOP/s of 1.88; 16 prompts
-// of up to 2039 tokens 311 us (1.04 PFLOP/s: a tile's start and output cost it 6500
-// clocks beside 2700 a block); 2 x 1021 tokens behind 30011 with heads of 64 430 us.
-// Not kept: P handed on in halves (1384 -> 1459 us), the maximum in a pass of its own
-// (1504 -> 1527; heads of 64 458 -> 508), ranges that end at tiles with longer prompts
-// too (50 -> 55 us for one prompt of 2039 tokens).
+// heads of 64 a block takes 2050 clocks, 1600 without that arithmetic where its products
+// should take 1024: those of 64 columns may take longer than half of 128 columns' time,
+// or wait for shared memory, of which a block reads 96 KB (768 clocks) while TMA writes
+// 32; the two were not told apart.  Measured (GB300, device time): 16381 tokens of 32 heads
+// of 128 over 4 kv heads 1385 us, 1.59 PFLOP/s of 1.88 (ten in a row 1455 each, under the
+// power limit); 16 prompts of 1020 to 2039 tokens 312 us (1.04 PFLOP/s: a tile's start and
+// output cost it 6500 clocks beside 2700 a block); 2 x 1021 tokens behind 30011 with heads
+// of 64 421 to 446 us.  Not kept: P handed on in halves (1384 -> 1459 us), the maximum in a
+// pass of its own (1504 -> 1527; heads of 64 458 -> 508).
 #include <cstdio>
 
 #include <cudaTypedefs.h>
@@ -67,11 +78,11 @@ constexpr int kKeys = 128;   // of a block
 constexpr int kTile = 256;   // rows of a tile
 constexpr int kThreads = 384;
 constexpr int kOver = 3;     // blocks' worth of time that a tile costs at least
-// Tiles are whole where no sequence has more keys (without a second launch; whole and cut: 16
-// prompts of 600 tokens 61 and 71 us, one of 1200 22 and 31, one of 2039 53 and 50), and where
-// there are many: each saves about two thirds of a block's time by not being cut, and ranges
-// end up to half the longest tile apart (16 prompts of 2039 311 and 318, 64 of 3000 2290 and
-// 2380; 8 of 4096 568 and 554, 4 of 8192 1330 and 1276).
+// Tiles are whole where no sequence has more keys (without a second launch; whole and cut, prompts
+// of equal length: 16 of 600 tokens 77 and 90 us, one of 1200 22 and 31, one of 2039 53 and 50),
+// and where there are many: each saves about two thirds of a block's time by not being cut, and
+// ranges end up to half the longest tile apart (16 prompts of 2039 459 and 479, 64 of 3000 3650 and
+// 3690; 8 of 4096 810 and 806, 4 of 8192 1510 and 1453).
 constexpr int kWholeKeys = 1536;
 enum PromptMode { kCut, kWhole, kOne };  // ranges cut tiles, end at tiles, are tiles
 

@@ -7,14 +7,16 @@
 //   o = sum_j 2^(x_j + b_j - M) V_j / sum_j 2^(x_j - M)
 // for any M.  M follows the maximum of x_j + b_j, so that the weights
 // 2^(x_j + b_j - M) of the second product fit fp16 whatever the powers are, and the
-// sum takes them times 2^-b_j.  M is only raised, and O only rescaled, when some
-// x_j + b_j is more than 8 above it.  States of disjoint keys join as in
+// sum takes them times 2^-b_j.  A row's M is only raised, and O only rescaled, when some
+// x_j + b_j of the row is more than 8 above it.  States of disjoint keys join as in
 // tree_attn.cu.
 //
 // Precision.  A row of q becomes fp16 times the power of two that puts its largest
 // element into [1, 2): bf16 elements down to 2^-17 of it stay exact, smaller ones
 // round at 2^-25 of it.  The weights are rounded to fp16 (11 bits, times 2^6 so
-// that small ones stay out of its subnormals).  Scores, M, sums and outputs are fp32.
+// that small ones stay out of its subnormals).  Scores, M, sums and outputs are fp32.  The
+// sum is relative to the largest x + b: where values' powers are 2^110 and more apart, keys
+// of less than 2^-20 of the weight of others can drop out of it.
 //
 // Next to reading the cache, issuing binds: each code is widened once, in registers,
 // and every instruction per code counts.  So keys and the head's elements are the M side of

@@ -31,9 +31,10 @@
 // What binds: shared memory, then the chain from a tile's copy to its product.  Per tile
 // of 128 keys of 128 elements the codes are written (256 clocks at 128 bytes), read and
 // written as fp16 (768), and read by the products (768 a row tile), beside 1024 clocks
-// of products a row tile.  Measured: 32 x 16 nodes of 8 heads over up to 8191 keys 84 us
-// (2000 clocks of the 2600 a tile takes are shared memory's), 32 x 32 nodes 134.  Steps
-// on the way, of the first: unrolled widening 157 us (a third of the warps' time went to
+// of products a row tile.  Measured: 32 x 16 nodes of 8 heads over up to 8191 keys 88.5 us,
+// 32 x 32 nodes 141, and 118 and 203 where every tile's keys take their own powers.  Before
+// nodes did, and rows were raised alone, they were 84 (2000 clocks of the 2600 a tile took
+// were shared memory's) and 134.  Steps on the way there, of the first: unrolled widening 157 us (a third of the warps' time went to
 // waiting for instructions), short loops and powers by asynchronous copies 102, the
 // products' waits together and eight widening warps 97, both warpgroups on every tile
 // and rings of K and V apart 93, producers apart 85.
