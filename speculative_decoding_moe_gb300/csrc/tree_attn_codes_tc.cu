@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
                                                DUAL ? 0u : smem_u32(&s_pvdone[place ^ 1]), ((T - 1) >> 1) & 1u, p.err, &s_abort);
           m = ml.x;
           l = ml.y;
-          ok = s_abort == 0;
+          ok = __all_sync(0xffffffffu, s_abort == 0);
         } else {
           // in (0, infinity)
           const float c = fminf(fmaxf(crow * exp_value((uint32_t)ea), 0x1p-120f), 0x1p120f);
