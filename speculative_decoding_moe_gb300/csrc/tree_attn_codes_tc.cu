@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_codes_tc_kernel(const _
 #pragma unroll
             for (int o = 1; o < kCh; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             // times 2^(127 - exponent), the ends of the range the same
-            const int f = min(200, max(1, 254 - (int)(__float_as_uint(top) >> 23)));
+            const int f = min(253, max(1, 254 - (int)(__float_as_uint(top) >> 23)));
             const float up = exp_value((uint32_t)f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = pack2<true>(bf16_lo(v[e]) * up, bf16_hi(v[e]) * up);
