@@ -218,9 +218,9 @@ __device__ __forceinline__ void exp32(const float *s, float c, float z, uint32_t
 // Scores of a tile whose first key is node j0 (below 0: committed): what the row
 // does not see becomes -inf, in place.  A short loop: it runs once per sequence, and
 // unrolled its instructions took longer to fetch than to execute.
-__device__ __forceinline__ void mask_tile(uint32_t t_s, int j0, uint64_t mask, int keys = 128) {
+__device__ __forceinline__ void mask_tile(uint32_t t_s, int j0, uint64_t mask) {
 #pragma unroll 1
-  for (int q = 0; q < keys; q += 16) {
+  for (int q = 0; q < 128; q += 16) {
     const int j = j0 + q;  // node of the first of 16 keys
     if (j + 16 <= 0) continue;
     uint32_t sees;

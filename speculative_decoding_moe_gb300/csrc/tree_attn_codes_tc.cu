@@ -56,6 +56,7 @@ constexpr int kWiden = 4;  // warps that widen K, and that widen V
 
 constexpr float kBias = 6.f;
 constexpr int kApartK = 15, kApartV = 8;  // how far a tile's powers may be apart for constants of the tile
+static_assert(kApartK <= 15 && kApartV <= 15, "half_power");
 constexpr int kFlags = 8;
 constexpr int kTells = 16;  // tiles whose powers are kept: more than are between their widening and their scores
 
@@ -90,9 +91,9 @@ __device__ __forceinline__ void widen16(const uint4 &x, __half2 m, uint4 &lo, ui
   hi = make_uint4(y[4], y[5], y[6], y[7]);
 }
 
-// 2^-d in fp16, d >= 0 (0 below its subnormals)
+// 2^-d in fp16, d from 0 to 15 (kApartK; the last is a subnormal)
 __device__ __forceinline__ __half2 half_power(int d) {
-  const uint32_t b = d <= 14 ? (uint32_t)(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
+  const uint32_t b = d <= 14 ? (uint32_t)(15 - d) << 10 : 1u << 9;
   const uint32_t two = b | b << 16;
   return *reinterpret_cast<const __half2 *>(&two);
 }

@@ -99,3 +99,26 @@ def test_large_tokens_of_no_weight(dfv, what, up, heads, kv, dim, nodes):
         # the tolerance is that of ordinary values: 2^-8 of the output, and 2^-11 of sum p |v|, which over n <= 3425 keys with
         # values of any sign is sqrt(n) = 59 times the output or less: 0.004 + 1.1 * 59 / 2048 = 0.036
         assert float((to / (o.abs() + 0.01 * o.abs().mean())).median()) < 2.0 ** -4
+
+
+@pytest.mark.parametrize("heads,kv,dim,nodes", [(16, 2, 128, 16), (16, 2, 128, 25), (8, 4, 64, 20)])
+@pytest.mark.parametrize("side,apart", [(0, n) for n in (14, 15, 16)] + [(1, n) for n in (7, 8, 9)])
+def test_where_constants_of_a_tile_end(dfv, side, apart, heads, kv, dim, nodes):
+    """Powers of a tile just as far apart as constants of the tile may be, or one further: tokens of weight at both ends."""
+    lens = [1500 + 100 * s for s in range(20)]
+    c = Case(lens, [nodes] * len(lens), heads, kv, dim, 16, seed=apart, masks="chain", spread=0.0)
+    g = torch.Generator().manual_seed(2)
+    e = c.exp[side]
+    e.fill_(127 - 8 - apart)
+    e[torch.rand(e.shape, generator=g) < 0.2] = 127 - 8
+    if side == 0:
+        c.q *= 0.25  # large keys do not take all weight
+    out, lse, err = c.run(dfv)
+    assert err == 0
+    for s in (0, 7, 12, 19):
+        o, L, to, tl = want(c, s)
+        r = slice(c.off[s], c.off[s + 1])
+        d = (out[r].double().cpu() - o).abs()
+        assert bool((d <= to).all()), "output off by %g of its tolerance" % float((d / to).max())
+        d = (lse[r].double().cpu() - L).abs()
+        assert bool((d <= tl).all()), "lse off by %g of its tolerance" % float((d / tl).max())
