@@ -122,3 +122,28 @@ def test_where_constants_of_a_tile_end(dfv, side, apart, heads, kv, dim, nodes):
         assert bool((d <= to).all()), "output off by %g of its tolerance" % float((d / to).max())
         d = (lse[r].double().cpu() - L).abs()
         assert bool((d <= tl).all()), "lse off by %g of its tolerance" % float((d / tl).max())
+
+
+@pytest.mark.parametrize("heads,kv,dim,nodes", [(16, 2, 128, 16), (16, 2, 128, 25), (8, 4, 64, 3), (16, 2, 128, 2)])
+@pytest.mark.parametrize("low,high", [(-100, -8), (-100, 10), (-60, 50), (-5, 105)])
+def test_values_far_apart_that_all_weigh(dfv, low, high, heads, kv, dim, nodes):
+    """Values of two sizes 2^92 to 2^110 apart (zeros have the lowest power) with weights alike: the sum of the weights has them all."""
+    lens = [1500 + 100 * s for s in range(20)]
+    c = Case(lens, [nodes] * len(lens), heads, kv, dim, 16, seed=nodes, masks="chain", spread=0.0)
+    g = torch.Generator().manual_seed(3)
+    e = c.exp[1]
+    e.fill_(127 + low)
+    if low == -100:
+        c.raw[1].zero_()
+    large = torch.rand(e.shape, generator=g) < 0.3
+    e[large] = 127 + high
+    c.raw[1][large] = torch.randint(0x40, 0x7e, (int(large.sum()), dim), generator=g).to(torch.uint8)
+    out, lse, err = c.run(dfv)
+    assert err == 0
+    for s in (0, 7, 12, 19):
+        o, L, to, tl = want(c, s)
+        r = slice(c.off[s], c.off[s + 1])
+        d = (out[r].double().cpu() - o).abs()
+        assert bool((d <= to).all()), "output off by %g of its tolerance" % float((d / to).max())
+        d = (lse[r].double().cpu() - L).abs()
+        assert bool((d <= tl).all()), "lse off by %g of its tolerance" % float((d / tl).max())
