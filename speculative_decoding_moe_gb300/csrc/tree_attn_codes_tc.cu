@@ -34,10 +34,10 @@
 // of products a row tile.  Measured: 32 x 16 nodes of 8 heads over up to 8191 keys 88.5 us,
 // 32 x 32 nodes 141, and 118 and 203 where every tile's keys take their own powers.  Before
 // nodes did, and rows were raised alone, they were 84 (2000 clocks of the 2600 a tile took
-// were shared memory's) and 134.  Steps on the way there, of the first: unrolled widening 157 us (a third of the warps' time went to
-// waiting for instructions), short loops and powers by asynchronous copies 102, the
-// products' waits together and eight widening warps 97, both warpgroups on every tile
-// and rings of K and V apart 93, producers apart 85.
+// were shared memory's) and 134.  Steps on the way there, of the first: unrolled widening
+// 157 us (a third of the warps' time went to waiting for instructions), short loops and
+// powers by asynchronous copies 102, the products' waits together and eight widening warps
+// 97, both warpgroups on every tile and rings of K and V apart 93, producers apart 85.
 //
 // Warps 0-3 and 4-7 are the two warpgroups, warp 8 issues the MMAs, warps 9 and 10
 // stream codes of K with TMA, warp 11 those of V, warps 12-15 widen K and 16-19 V.
@@ -127,7 +127,7 @@ __device__ __noinline__ bool clean_key(uint32_t row, bool node) {
 // A tile whose keys have factors of their own: x + b of the scores of the keys that the row sees,
 // in place, and their maximum; M and O as they grow; then p and the sum of p 2^-b.  (m, l) before
 // and after; j0: node number of the first key (below 0: committed); bar: the product into O before,
-// 0 where it is done.  Out of line: the other tiles took 2 % longer with it among theirs.
+// 0 where it is done.  Out of line: calls took 1 to 3 % longer with it among the other tiles' code.
 template <int D, int KEYS>
 __device__ __noinline__ float2 own_tile(uint32_t t_s, uint32_t t_o, bool started, int j0, uint64_t mask, float crow, uint32_t own, uint32_t back, float m, float l,
                                         uint32_t bar, unsigned phase, unsigned *err, volatile int *abort) {
